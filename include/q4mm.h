@@ -242,6 +242,177 @@ Q4MM_API int q4_w8_unpack(int8_t *codes, float *scales, const void *W8_packed, i
 Q4MM_API int q4_w8_matmul(const void *W8_packed, const float *X, float *Y, int64_t m, int64_t k, int64_t n,
                           q4mm_stream_t stream);
 
+/* ------------------------------------------- around the linear layers --
+ * What a block of a model has around its quantised linear layers: tokens
+ * coded to int8 and multiplied by int8 weights, the norms before and after a
+ * block, and the sort of tokens by expert that q4_0_matmul_experts expects.
+ *
+ * Conventions of these calls, next to those above:
+ *   - `type` names the element type of every matrix of a call (X, Y, R, ...);
+ *     parameters of the channels and tokens (weights, scales, a channel's or
+ *     token's gate, routing weights) are fp32. Values are computed in fp32
+ *     and rounded once, to nearest even, when they are stored.
+ *   - ld* is the distance between two rows of a matrix in elements, at least
+ *     the row's length. Rows need no alignment beyond their element's; calls
+ *     whose rows all start on 16-byte boundaries move 16 bytes an access,
+ *     others 4 bytes or one element.
+ *   - A matrix that is written may not overlap one that is read, except where
+ *     a call names a pair that may be the same buffer (same pointer and ld).
+ *   - Elements between a row's length and ld are neither read nor written. */
+#define Q4_TYPE_F32 0
+#define Q4_TYPE_F16 1
+#define Q4_TYPE_BF16 2
+#define Q4_TYPE_I8 3   /* int8 codes with one fp32 scale a row */
+
+/* Code m rows of k values to int8: the rule of q4_w8_quantize for a row of
+ * tokens. With amax = max |x| of the row, its scale is amax / 127 and a code
+ * round-half-even(x * (127 / amax)), every step one IEEE fp32 operation. A row
+ * with amax below 2^-110 codes to zeros with scale 0; a row that holds a NaN
+ * or an infinity codes to zeros with a NaN scale (its products are NaN).
+ *   Xq: device int8 [m x k], row r at Xq + r * k (written); sx: device fp32
+ *   [m], 4-byte aligned (written); X: device, row r at X + r * ldx, F32, F16
+ *   or BF16. m >= 0, 1 <= k <= 2^24. */
+Q4MM_API int q4_a8_quantize(int8_t *Xq, float *sx, const void *X, int64_t ldx, int type,
+                            int64_t m, int64_t k, q4mm_stream_t stream);
+
+/* Bytes of scratch the two calls below need (256-byte aligned; it needs no
+ * initialisation): the tokens' codes and scales, and for larger m their tiles
+ * as the tensor cores read them. 0 for invalid sizes or m = 0. */
+Q4MM_API size_t q4_w8a8_workspace_size(int64_t m, int64_t k, int64_t n);
+
+/* The product in 8-bit integers with a scale for each token and each channel:
+ *     Y[t][j] = sx[t] * s_j * sum_c xq[t][c] * code[j][c]
+ * xq and sx are X coded by q4_a8_quantize's rule, code and s_j as
+ * q4_w8_quantize wrote them. Products and, while every partial sum stays below
+ * 2^24, sums are exact (at most k * 127^2; beyond that up to 16 rows still add
+ * in 32-bit integers, more rows in fp32): then fp32, sx * s_j rounded, times
+ * the sum, rounded to ytype.
+ *   W8_packed: as written by q4_w8_quantize for (n, k), 16-byte aligned.
+ *   X: device, row t at X + t * ldx, xtype F32, F16 or BF16. Y: device, row t
+ *   at Y + t * ldy, ytype F32, F16 or BF16, overwritten. Y's rows may be of any
+ *   alignment; 16-byte aligned ones are written 16 bytes an access.
+ *   m >= 0 (0 does nothing), n >= 1, 32 <= k <= 131072, k % 32 == 0.
+ *   workspace: device, 256-byte aligned, q4_w8a8_workspace_size(m, k, n) bytes;
+ *   calls that can run at the same time need one each. */
+Q4MM_API int q4_w8a8_matmul(const void *W8_packed, const void *X, int64_t ldx, int xtype,
+                            void *Y, int64_t ldy, int ytype, int64_t m, int64_t k, int64_t n,
+                            void *workspace, size_t workspace_bytes, q4mm_stream_t stream);
+
+/* The same product of tokens that are codes already (q4_a8_quantize's output,
+ * or a norm's written as Q4_TYPE_I8): Xq int8 [m x k], 16-byte aligned, rows
+ * next to each other, codes of -127 .. 127; sx fp32 [m]. */
+Q4MM_API int q4_w8a8_matmul_codes(const void *W8_packed, const int8_t *Xq, const float *sx,
+                                  void *Y, int64_t ldy, int ytype, int64_t m, int64_t k, int64_t n,
+                                  void *workspace, size_t workspace_bytes, q4mm_stream_t stream);
+
+/* The norm before a block: with N(x) = x / sqrt(mean(x^2) + eps) over a row,
+ *     H[t] = N(X[t]) * (w_offset + w)
+ * as values (htype == type) or, with htype == Q4_TYPE_I8, coded by
+ * q4_a8_quantize's rule from the fp32 values into int8 rows and h_scale[t].
+ *   X: [m x d] of type F32, F16 or BF16; w: fp32 [d], or NULL for weights of 1
+ *   (w_offset then has no effect); h_scale: fp32 [m], only for codes.
+ *   eps > 0, m >= 0, 1 <= d <= 2^24. H may be X when htype == type. */
+Q4MM_API int q4_norm_before(void *H, int64_t ldh, int htype, float *h_scale, const void *X, int64_t ldx, int type,
+                            const float *w, float w_offset, float eps, int64_t m, int64_t d, q4mm_stream_t stream);
+
+/* The norm after a block, with the block's gate, the residual scale and the
+ * residual sum:
+ *     Y[t] = R[t] + scale * g * N(B[t]) * (w_offset + w)
+ * B is the block's output, R the residual stream, Y the stream after it. The
+ * gate g is 1 (Q4_GATE_NONE, gate NULL), fp32 [d] (CHANNEL), fp32 [m] (TOKEN)
+ * or [m x d] of the matrices' type with ldg (FULL; ldg is not read otherwise).
+ * Y may be R. Sizes as for q4_norm_before. */
+#define Q4_GATE_NONE 0
+#define Q4_GATE_CHANNEL 1
+#define Q4_GATE_TOKEN 2
+#define Q4_GATE_FULL 3
+Q4MM_API int q4_norm_after(void *Y, int64_t ldy, const void *R, int64_t ldr, const void *B, int64_t ldb, int type,
+                           const float *w, float w_offset, const void *gate, int64_t ldg, int gate_kind, float scale,
+                           float eps, int64_t m, int64_t d, q4mm_stream_t stream);
+
+/* q4_norm_after and the next block's q4_norm_before in one pass:
+ *     H[t] = N(Y[t]) * (w_offset_next + w_next)
+ * of Y as it is stored, so the results are those of the two calls. */
+Q4MM_API int q4_norm_after_before(void *Y, int64_t ldy, void *H, int64_t ldh, int htype, float *h_scale,
+                                  const void *R, int64_t ldr, const void *B, int64_t ldb, int type, const float *w,
+                                  float w_offset, const void *gate, int64_t ldg, int gate_kind, float scale,
+                                  const float *w_next, float w_offset_next, float eps, int64_t m, int64_t d,
+                                  q4mm_stream_t stream);
+
+/* Bytes of scratch the norms' gradients need for these sizes (16-byte
+ * aligned, no initialisation): partial sums over the tokens. */
+Q4MM_API size_t q4_norm_workspace_size(int64_t m, int64_t d);
+
+/* The gradient of q4_norm_before with the residual stream's added:
+ *     dX = dR + (d H / d X)^T dH         dw = sum over tokens of dH * N(X)
+ * dR [m x d] may be NULL (nothing is added); dw fp32 [d] may be NULL (not
+ * wanted; the workspace then may be too). dX may be dH, dR or X. With m = 0,
+ * dw is zeros. dR and dH are the gradients that reach the block's input past
+ * the block and through it, so this call after q4_norm_after_before's outputs
+ * H and Y gives Y's whole gradient. */
+Q4MM_API int q4_norm_before_backward(void *dX, int64_t lddx, float *dw, const void *dH, int64_t lddh, const void *dR,
+                                     int64_t lddr, const void *X, int64_t ldx, int type, const float *w,
+                                     float w_offset, float eps, int64_t m, int64_t d, void *workspace,
+                                     size_t workspace_bytes, q4mm_stream_t stream);
+
+/* The gradient of q4_norm_after (R's is dY itself):
+ *     dB = (d Y / d B)^T dY,  dw = sum over tokens of scale * g * dY * N(B),
+ *     dgate = scale * dY * N(B) * (w_offset + w), summed over what the gate is
+ *     shared by: fp32 [d] for CHANNEL, fp32 [m] for TOKEN, [m x d] for FULL.
+ * dw and dgate may each be NULL (not wanted). dB may be dY or B. With m = 0, dw
+ * and a channel's dgate are zeros. */
+Q4MM_API int q4_norm_after_backward(void *dB, int64_t lddb, float *dw, void *dgate, int64_t lddgate, const void *dY,
+                                    int64_t lddy, const void *B, int64_t ldb, int type, const float *w, float w_offset,
+                                    const void *gate, int64_t ldg, int gate_kind, float scale, float eps, int64_t m,
+                                    int64_t d, void *workspace, size_t workspace_bytes, q4mm_stream_t stream);
+
+/* Bytes of scratch q4_moe_dispatch needs (16-byte aligned, no
+ * initialisation); 0 for few pairs and for invalid sizes. */
+Q4MM_API size_t q4_moe_workspace_size(int64_t tokens, int64_t top_k, int64_t n_experts);
+
+/* Tokens sorted by expert. Token t has top_k choices, ids[t * top_k + j]; the
+ * pair p = t * top_k + j gets the row that a stable sort of the pairs by
+ * expert gives it, so an expert's rows are next to each other and in the
+ * tokens' order:
+ *   offsets: int64 [n_experts + 1]: expert e has rows offsets[e] ..
+ *     offsets[e + 1] - 1 (copied to the host, what q4_0_matmul_experts takes);
+ *   row_of: int32 [tokens x top_k]: the pair's row;
+ *   pair_of: int32 [tokens * top_k]: the pair at each row (may be NULL);
+ *   Xs: [tokens * top_k x d]: Xs[row_of[p]] = X[t] (X and Xs both NULL: the
+ *     sort alone).
+ * An id outside 0 .. n_experts - 1 (padding, a choice over capacity) is no
+ * expert: its pair sorts after the last expert, row_of is -1 - row, and that
+ * row of Xs is zeros.
+ *   ids: device int32 (id_bytes 4) or int64 (8), naturally aligned; X: [tokens
+ *   x d] of type F32, F16 or BF16. tokens >= 0 (0: offsets are zeros), 1 <=
+ *   top_k <= 1024, tokens * top_k <= 2^24, 1 <= n_experts <= 4096, d >= 1 with
+ *   rows. */
+Q4MM_API int q4_moe_dispatch(void *Xs, int64_t ldxs, int64_t *offsets, int32_t *row_of, int32_t *pair_of,
+                             const void *ids, int id_bytes, const void *X, int64_t ldx, int type, int64_t tokens,
+                             int64_t top_k, int64_t n_experts, int64_t d, void *workspace, size_t workspace_bytes,
+                             q4mm_stream_t stream);
+
+/* The experts' rows back in the tokens' order, weighted and summed in fp32 in
+ * the order of j:
+ *     Y[t] = base[t] + sum over j of weights[t][j] * Ys[row_of[t][j]]
+ * Pairs with a negative row_of are left out, whatever their row and weight
+ * hold. base may be NULL (zeros) and may be Y; weights fp32 [tokens x top_k]
+ * may be NULL (ones: then this is the gradient of q4_moe_dispatch's copy, with
+ * Ys the gradient of Xs). row_of as written by q4_moe_dispatch. */
+Q4MM_API int q4_moe_combine(void *Y, int64_t ldy, const void *base, int64_t ldbase, const void *Ys, int64_t ldys,
+                            int type, const int32_t *row_of, const float *weights, int64_t tokens, int64_t top_k,
+                            int64_t d, q4mm_stream_t stream);
+
+/* The gradient of q4_moe_combine (base's is dY itself):
+ *     dYs[row_of[t][j]] = weights[t][j] * dY[t],  dweights[t][j] = <dY[t], Ys[row_of[t][j]]>
+ * zeros for pairs without an expert (their rows -1 - row_of of dYs included,
+ * so all of dYs is written). dweights fp32 [tokens x top_k] may be NULL; dYs may
+ * be Ys. */
+Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, const void *dY, int64_t lddy,
+                                     const void *Ys, int64_t ldys, int type, const int32_t *row_of,
+                                     const float *weights, int64_t tokens, int64_t top_k, int64_t d,
+                                     q4mm_stream_t stream);
+
 /* Size of the library's fixed scratch array used by q4_0_matmul_static_scratch. */
 #define Q4_STATIC_SCRATCH_BYTES (8u << 20)
 

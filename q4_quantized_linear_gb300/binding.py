@@ -30,6 +30,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _INT = ctypes.c_int
+_F = ctypes.c_float
 
 _SIGS = {
     "q4_0_packed_size": (_SZ, [_I64, _I64]),
@@ -43,6 +44,23 @@ _SIGS = {
     "q4_w8_quantize": (_INT, [_P, _P, _I64, _I64, _P]),
     "q4_w8_unpack": (_INT, [_P, _P, _P, _I64, _I64, _P]),
     "q4_w8_matmul": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P]),
+    "q4_a8_quantize": (_INT, [_P, _P, _P, _I64, _INT, _I64, _I64, _P]),
+    "q4_w8a8_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "q4_w8a8_matmul": (_INT, [_P, _P, _I64, _INT, _P, _I64, _INT, _I64, _I64, _I64, _P, _SZ, _P]),
+    "q4_w8a8_matmul_codes": (_INT, [_P, _P, _P, _P, _I64, _INT, _I64, _I64, _I64, _P, _SZ, _P]),
+    "q4_norm_before": (_INT, [_P, _I64, _INT, _P, _P, _I64, _INT, _P, _F, _F, _I64, _I64, _P]),
+    "q4_norm_after": (_INT, [_P, _I64, _P, _I64, _P, _I64, _INT, _P, _F, _P, _I64, _INT, _F, _F, _I64, _I64, _P]),
+    "q4_norm_after_before": (_INT, [_P, _I64, _P, _I64, _INT, _P, _P, _I64, _P, _I64, _INT, _P, _F, _P, _I64, _INT, _F,
+                                    _P, _F, _F, _I64, _I64, _P]),
+    "q4_norm_workspace_size": (_SZ, [_I64, _I64]),
+    "q4_norm_before_backward": (_INT, [_P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _INT, _P, _F, _F, _I64, _I64, _P,
+                                       _SZ, _P]),
+    "q4_norm_after_backward": (_INT, [_P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _INT, _P, _F, _P, _I64, _INT, _F, _F,
+                                      _I64, _I64, _P, _SZ, _P]),
+    "q4_moe_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "q4_moe_dispatch": (_INT, [_P, _I64, _P, _P, _P, _P, _INT, _P, _I64, _INT, _I64, _I64, _I64, _I64, _P, _SZ, _P]),
+    "q4_moe_combine": (_INT, [_P, _I64, _P, _I64, _P, _I64, _INT, _P, _P, _I64, _I64, _I64, _P]),
+    "q4_moe_combine_backward": (_INT, [_P, _I64, _P, _P, _I64, _P, _I64, _INT, _P, _P, _I64, _I64, _I64, _P]),
     "q4_0_matmul_experts": (_INT, [ctypes.POINTER(_P), _I64, ctypes.POINTER(_I64), _P, _P, _I64, _I64, _P]),
     "q4_0_matmul_static_scratch": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P]),
     "q4_0_matmul_batched_slots": (_INT, [_P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P]),
@@ -193,6 +211,113 @@ def q4_0_matmul_ws(W_packed, X, Y, m: int, k: int, n: int, workspace, workspace_
     rc = _lib.q4_0_matmul_ws(_addr(W_packed), _addr(X), _addr(Y), m, k, n, _addr(workspace),
                              workspace_bytes, _stream(stream))
     return _check(rc, "q4_0_matmul_ws") if check else rc
+
+
+# ---- around the linear layers: element types, the int8 product, norms, experts
+
+Q4_TYPE_F32 = 0
+Q4_TYPE_F16 = 1
+Q4_TYPE_BF16 = 2
+Q4_TYPE_I8 = 3
+Q4_GATE_NONE = 0
+Q4_GATE_CHANNEL = 1
+Q4_GATE_TOKEN = 2
+Q4_GATE_FULL = 3
+
+
+def q4_a8_quantize(Xq, sx, X, ldx: int, type: int, m: int, k: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_a8_quantize(_addr(Xq), _addr(sx), _addr(X), ldx, type, m, k, _stream(stream))
+    return _check(rc, "q4_a8_quantize") if check else rc
+
+
+def q4_w8a8_workspace_size(m: int, k: int, n: int) -> int:
+    return int(_lib.q4_w8a8_workspace_size(m, k, n))
+
+
+def q4_w8a8_matmul(W8_packed, X, ldx: int, xtype: int, Y, ldy: int, ytype: int, m: int, k: int, n: int, workspace,
+                   workspace_bytes: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_w8a8_matmul(_addr(W8_packed), _addr(X), ldx, xtype, _addr(Y), ldy, ytype, m, k, n, _addr(workspace),
+                             workspace_bytes, _stream(stream))
+    return _check(rc, "q4_w8a8_matmul") if check else rc
+
+
+def q4_w8a8_matmul_codes(W8_packed, Xq, sx, Y, ldy: int, ytype: int, m: int, k: int, n: int, workspace,
+                         workspace_bytes: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_w8a8_matmul_codes(_addr(W8_packed), _addr(Xq), _addr(sx), _addr(Y), ldy, ytype, m, k, n,
+                                   _addr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "q4_w8a8_matmul_codes") if check else rc
+
+
+def q4_norm_before(H, ldh: int, htype: int, h_scale, X, ldx: int, type: int, w, w_offset: float, eps: float, m: int,
+                   d: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_norm_before(_addr(H), ldh, htype, _addr(h_scale), _addr(X), ldx, type, _addr(w), w_offset, eps, m, d,
+                             _stream(stream))
+    return _check(rc, "q4_norm_before") if check else rc
+
+
+def q4_norm_after(Y, ldy: int, R, ldr: int, B, ldb: int, type: int, w, w_offset: float, gate, ldg: int,
+                  gate_kind: int, scale: float, eps: float, m: int, d: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_norm_after(_addr(Y), ldy, _addr(R), ldr, _addr(B), ldb, type, _addr(w), w_offset, _addr(gate), ldg,
+                            gate_kind, scale, eps, m, d, _stream(stream))
+    return _check(rc, "q4_norm_after") if check else rc
+
+
+def q4_norm_after_before(Y, ldy: int, H, ldh: int, htype: int, h_scale, R, ldr: int, B, ldb: int, type: int, w,
+                         w_offset: float, gate, ldg: int, gate_kind: int, scale: float, w_next, w_offset_next: float,
+                         eps: float, m: int, d: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_norm_after_before(_addr(Y), ldy, _addr(H), ldh, htype, _addr(h_scale), _addr(R), ldr, _addr(B), ldb,
+                                   type, _addr(w), w_offset, _addr(gate), ldg, gate_kind, scale, _addr(w_next),
+                                   w_offset_next, eps, m, d, _stream(stream))
+    return _check(rc, "q4_norm_after_before") if check else rc
+
+
+def q4_norm_workspace_size(m: int, d: int) -> int:
+    return int(_lib.q4_norm_workspace_size(m, d))
+
+
+def q4_norm_before_backward(dX, lddx: int, dw, dH, lddh: int, dR, lddr: int, X, ldx: int, type: int, w,
+                            w_offset: float, eps: float, m: int, d: int, workspace, workspace_bytes: int, stream=None,
+                            check: bool = True) -> int:
+    rc = _lib.q4_norm_before_backward(_addr(dX), lddx, _addr(dw), _addr(dH), lddh, _addr(dR), lddr, _addr(X), ldx, type,
+                                      _addr(w), w_offset, eps, m, d, _addr(workspace), workspace_bytes,
+                                      _stream(stream))
+    return _check(rc, "q4_norm_before_backward") if check else rc
+
+
+def q4_norm_after_backward(dB, lddb: int, dw, dgate, lddgate: int, dY, lddy: int, B, ldb: int, type: int, w,
+                           w_offset: float, gate, ldg: int, gate_kind: int, scale: float, eps: float, m: int, d: int,
+                           workspace, workspace_bytes: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_norm_after_backward(_addr(dB), lddb, _addr(dw), _addr(dgate), lddgate, _addr(dY), lddy, _addr(B), ldb,
+                                     type, _addr(w), w_offset, _addr(gate), ldg, gate_kind, scale, eps, m, d,
+                                     _addr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "q4_norm_after_backward") if check else rc
+
+
+def q4_moe_workspace_size(tokens: int, top_k: int, n_experts: int) -> int:
+    return int(_lib.q4_moe_workspace_size(tokens, top_k, n_experts))
+
+
+def q4_moe_dispatch(Xs, ldxs: int, offsets, row_of, pair_of, ids, id_bytes: int, X, ldx: int, type: int, tokens: int,
+                    top_k: int, n_experts: int, d: int, workspace, workspace_bytes: int, stream=None,
+                    check: bool = True) -> int:
+    rc = _lib.q4_moe_dispatch(_addr(Xs), ldxs, _addr(offsets), _addr(row_of), _addr(pair_of), _addr(ids), id_bytes,
+                              _addr(X), ldx, type, tokens, top_k, n_experts, d, _addr(workspace), workspace_bytes,
+                              _stream(stream))
+    return _check(rc, "q4_moe_dispatch") if check else rc
+
+
+def q4_moe_combine(Y, ldy: int, base, ldbase: int, Ys, ldys: int, type: int, row_of, weights, tokens: int, top_k: int,
+                   d: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_moe_combine(_addr(Y), ldy, _addr(base), ldbase, _addr(Ys), ldys, type, _addr(row_of), _addr(weights),
+                             tokens, top_k, d, _stream(stream))
+    return _check(rc, "q4_moe_combine") if check else rc
+
+
+def q4_moe_combine_backward(dYs, lddys: int, dweights, dY, lddy: int, Ys, ldys: int, type: int, row_of, weights,
+                            tokens: int, top_k: int, d: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_moe_combine_backward(_addr(dYs), lddys, _addr(dweights), _addr(dY), lddy, _addr(Ys), ldys, type,
+                                      _addr(row_of), _addr(weights), tokens, top_k, d, _stream(stream))
+    return _check(rc, "q4_moe_combine_backward") if check else rc
 
 
 Q4_STATIC_SCRATCH_BYTES = 8 << 20

@@ -32,6 +32,11 @@ struct DeviceInfo {
     int *status = nullptr;   // device address of the status word
 };
 
+// The current device (status code; compute capability 10.3 only), and a CUDA
+// error as a status code.
+int device_info(DeviceInfo *out);
+int cuda_status(cudaError_t e);
+
 // Raise a kernel's dynamic shared-memory limit to the opt-in maximum, once per
 // (device, kernel).
 cudaError_t set_max_smem(const void *func, size_t bytes);

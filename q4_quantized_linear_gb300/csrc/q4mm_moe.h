@@ -1,0 +1,64 @@
+// q4mm_moe.h -- the expert sort's and the combining kernels' arguments and
+// launchers (internal).
+#pragma once
+
+#include "q4mm_internal.h"
+#include "q4mm_rows.h"
+
+namespace q4 {
+
+constexpr int kMoeMaxExperts = 4096;
+constexpr int kMoeMaxTopK = 1024;
+// Most chunks the pairs are cut into for the sort.
+constexpr int kMoeMaxChunks = 128;
+
+struct MoeDispatchArgs {
+    void *Xs;                // nullptr: no rows are copied
+    const void *X;
+    int64_t ldxs, ldx;       // in units of one access
+    int64_t row_units;       // whole accesses of a row
+    int tail_at, tail;       // then `tail` elements of esize bytes from element tail_at
+    int esize;
+    int64_t *offsets;
+    int32_t *row_of, *pair_of;
+    const void *ids;
+    int id_bytes;
+    int64_t tokens, pairs;
+    int top_k, experts;
+    int32_t *hist;           // [chunks][experts + 1]
+    int64_t chunk;           // pairs of a chunk
+    int chunks;
+};
+
+struct MoeCombineArgs {
+    void *Y;
+    const void *base, *Ys;
+    int64_t ldy, ldbase, ldys;
+    const int32_t *row_of;
+    const float *weights;    // nullptr: ones
+    int64_t tokens, pairs;
+    int top_k;
+    int64_t d;
+    int segs;                // CTAs that share a token's columns
+};
+
+struct MoeCombineBwdArgs {
+    void *dYs;
+    float *dweights;         // nullptr: not wanted
+    const void *dY, *Ys;
+    int64_t lddys, lddy, ldys;
+    const int32_t *row_of;
+    const float *weights;
+    int64_t tokens, pairs;
+    int top_k;
+    int64_t d;
+};
+
+// Scratch bytes of the sort (0 where one launch does it all).
+size_t moe_scratch(int64_t pairs, int64_t experts);
+// `unit`: bytes of one access when rows are copied (16, 4 or 2).
+cudaError_t launch_moe_dispatch(MoeDispatchArgs a, int unit, int sm_count, cudaStream_t s);
+cudaError_t launch_moe_combine(MoeCombineArgs a, int type, int vec, int sm_count, cudaStream_t s);
+cudaError_t launch_moe_combine_bwd(const MoeCombineBwdArgs &a, int type, int vec, int sm_count, cudaStream_t s);
+
+} // namespace q4

@@ -1,0 +1,90 @@
+// q4mm_norm.h -- the norm kernels' arguments and launchers (internal).
+#pragma once
+
+#include "q4mm_internal.h"
+#include "q4mm_rows.h"
+
+namespace q4 {
+
+// Most rows of partial column sums of a backward call.
+constexpr int kNormPartials = 608;
+
+// Where a normed row goes: values of the input's type, or int8 codes and a
+// scale per row. H == nullptr: nowhere.
+struct NormOut {
+    void *H;
+    int64_t ldh;
+    int codes;
+    float *h_scale;
+    const float *w;      // nullptr: weights of 1
+    float w_off;
+};
+
+struct NormBeforeArgs {
+    NormOut out;
+    const void *X;
+    int64_t ldx;
+    int plain;           // no norm: h = x (the coding of tokens alone)
+    float eps;
+    int64_t m, d;
+    int G;               // threads of a row
+};
+
+struct NormAfterArgs {
+    NormOut out;         // the next block's norm
+    float out_eps;
+    void *Y;
+    const void *R, *B;
+    int64_t ldy, ldr, ldb;
+    const float *w;
+    float w_off;
+    const void *gate;    // fp32 per channel or token; the matrices' type per value
+    int64_t ldg;
+    int gate_kind;
+    float scale, eps;
+    int64_t m, d;
+    int G;
+};
+
+struct NormBeforeBwdArgs {
+    void *dX;
+    const void *dH, *dR, *X;   // dR may be nullptr
+    int64_t lddx, lddh, lddr, ldx;
+    const float *w;
+    float w_off, eps;
+    float *partials;           // nullptr: no column sums are wanted
+    int64_t m, d;
+    int G;
+};
+
+struct NormAfterBwdArgs {
+    void *dB, *dgate;
+    const void *dY, *B, *gate;
+    int64_t lddb, lddg, lddy, ldb, ldg;
+    const float *w;
+    float w_off;
+    int gate_kind;
+    float scale, eps;
+    float *partials;
+    int64_t m, d;
+    int G;
+};
+
+struct NormColumnArgs {
+    const float *partials;
+    int rows;
+    int64_t d;
+    float scale;
+    float *dw, *dgate;
+    const float *gate, *w;
+    float w_off;
+};
+
+// `vec`: elements of one access; every row of every matrix starts on a
+// multiple of vec elements' bytes.
+cudaError_t launch_norm_before(const NormBeforeArgs &a, int type, int vec, int sm_count, cudaStream_t s);
+cudaError_t launch_norm_after(const NormAfterArgs &a, int type, int vec, int sm_count, cudaStream_t s);
+cudaError_t launch_norm_before_bwd(const NormBeforeBwdArgs &a, float *dw, int type, int vec, int sm_count, cudaStream_t s);
+cudaError_t launch_norm_after_bwd(const NormAfterBwdArgs &a, float *dw, int type, int vec, int sm_count, cudaStream_t s);
+
+} // namespace q4

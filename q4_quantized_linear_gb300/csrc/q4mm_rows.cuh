@@ -1,0 +1,167 @@
+// q4mm_rows.cuh -- what the kernels over rows of activations share: typed
+// vector loads and stores, sums over the threads of a row, the int8 coding of
+// a row, and the choice of vector width and threads a row.
+//
+// A row of d values is held by G threads: a warp (several rows a CTA) or the
+// whole CTA (one row). Vector i of thread t covers the elements
+// (i * G + t) * V .. + V - 1, so every load and store of a warp is contiguous.
+// The first NV vectors of a thread stay in registers; a row longer than
+// G * NV * V is finished by a loop that reads the remaining vectors again
+// where they are needed.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "q4mm_device.cuh"
+
+namespace q4 {
+
+// ------------------------------------------------------- typed elements --
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Rounded once, to nearest even.
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// V elements of type T, moved by one access of V * sizeof(T) bytes.
+template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
+    T e[V];
+};
+
+// Elements c .. c + V - 1 of a row of d, zeros past its end. `p` and the row
+// are aligned to the pack.
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(const T *row, int64_t c, int64_t d)
+{
+    Pack<T, V> r;
+    if (c + V <= d) {
+        r = *reinterpret_cast<const Pack<T, V> *>(row + c);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.e[i] = c + i < d ? row[c + i] : from_f32<T>(0.0f);
+    }
+    return r;
+}
+template <typename T, int V> __device__ __forceinline__ void store_pack(T *row, int64_t c, int64_t d, const Pack<T, V> &v)
+{
+    if (c + V <= d) {
+        *reinterpret_cast<Pack<T, V> *>(row + c) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c + i < d) row[c + i] = v.e[i];
+    }
+}
+
+// V fp32 parameters (weights or gates of the channels) at c, `other` past the
+// end. Their base is aligned to min(16, 4 V) bytes.
+template <int V> __device__ __forceinline__ void load_params(const float *p, int64_t c, int64_t d, float out[V])
+{
+    if (c + V <= d) {
+        if constexpr (V % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4 *>(p + c + i));
+                out[i] = f.x, out[i + 1] = f.y, out[i + 2] = f.z, out[i + 3] = f.w;
+            }
+        } else if constexpr (V == 2) {
+            const float2 f = __ldg(reinterpret_cast<const float2 *>(p + c));
+            out[0] = f.x, out[1] = f.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) out[i] = __ldg(p + c + i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[i] = c + i < d ? __ldg(p + c + i) : 0.0f;
+    }
+}
+
+// ---------------------------------------------------------- row reductions --
+
+// Sums and maxima over the G threads of a row: a shuffle tree in each warp,
+// then, where a row takes the whole CTA, the warps' values through shared
+// memory (every warp adds them in the same order, so all threads hold the same
+// bits). Two buffers in turn: a thread reaches the second use of a buffer only
+// past the barrier of the use between, which follows every read of the first.
+struct RowReducer {
+    float *buf;   // [2][3][32]
+    int warps;    // warps of a row; 1: no shared memory, no barrier
+    int turn = 0;
+
+    template <int N> __device__ __forceinline__ void sum(float (&v)[N])
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+        if (warps == 1) return;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        float *b = buf + turn * 96;
+        turn ^= 1;
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) b[i * 32 + warp] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = lane < warps ? b[i * 32 + lane] : 0.0f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+        }
+    }
+
+    // the largest of unsigned words (the bits of absolute values)
+    __device__ __forceinline__ uint32_t max_bits(uint32_t v)
+    {
+        v = __reduce_max_sync(0xFFFFFFFFu, v);
+        if (warps == 1) return v;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        uint32_t *b = reinterpret_cast<uint32_t *>(buf + turn * 96);
+        turn ^= 1;
+        if (lane == 0) b[warp] = v;
+        __syncthreads();
+        return __reduce_max_sync(0xFFFFFFFFu, lane < warps ? b[lane] : 0u);
+    }
+};
+
+// ------------------------------------------------------------- int8 codes --
+
+// Scale s = amax / 127 and factor 127 / amax of a row whose largest |x| has
+// the bits `amax_bits`, each one IEEE quotient. Below 2^-110 the factor could
+// overflow and s be subnormal: such a row codes to zeros with s = 0. A row
+// holding a NaN or an infinity codes to zeros with s = NaN, so that its
+// outputs are NaN.
+struct CodeScale {
+    float scale, factor;
+};
+__device__ __forceinline__ CodeScale code_scale(uint32_t amax_bits)
+{
+    CodeScale c;
+    if (amax_bits >= 0x7F800000u) {
+        c.scale = __uint_as_float(0x7FC00000u);
+        c.factor = 0.0f;
+    } else if (amax_bits < 0x08800000u) {   // 2^-110
+        c.scale = 0.0f;
+        c.factor = 0.0f;
+    } else {
+        const float amax = __uint_as_float(amax_bits);
+        c.scale = __fdiv_rn(amax, 127.0f);
+        c.factor = __fdiv_rn(127.0f, amax);
+    }
+    return c;
+}
+// round-half-even(x * factor), |code| <= 127; 0 where the row's factor is 0.
+__device__ __forceinline__ int8_t code_of(float x, float factor)
+{
+    return factor == 0.0f ? static_cast<int8_t>(0) : static_cast<int8_t>(__float2int_rn(__fmul_rn(x, factor)));
+}
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+} // namespace q4

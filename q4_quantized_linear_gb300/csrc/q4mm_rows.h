@@ -1,0 +1,33 @@
+// q4mm_rows.h -- host side of the kernels over rows of activations: element
+// types, the vector width that a call's addresses allow, and the threads that
+// hold a row.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/q4mm.h"
+#include "q4mm_internal.h"
+
+namespace q4 {
+
+inline int type_size(int type)
+{
+    return type == Q4_TYPE_F32 ? 4 : type == Q4_TYPE_F16 || type == Q4_TYPE_BF16 ? 2 : type == Q4_TYPE_I8 ? 1 : 0;
+}
+inline bool is_float_type(int type) { return type == Q4_TYPE_F32 || type == Q4_TYPE_F16 || type == Q4_TYPE_BF16; }
+inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Widest access (in bytes, a power of two, at most 16) at which every row of
+// every matrix added so far starts.
+struct RowAlign {
+    uintptr_t bits = 16;
+    void add(const void *p, int64_t ld_bytes)
+    {
+        if (!p) return;
+        bits |= reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld_bytes);
+    }
+    int bytes() const { return static_cast<int>(bits & (~bits + 1)); }
+};
+
+} // namespace q4
