@@ -63,12 +63,34 @@ bool valid_sizes(int64_t m, int64_t k, int64_t n)
     return m >= 0 && m <= (int64_t(1) << 20) && n >= 1 && n <= (int64_t(1) << 31) - 256 && k >= 32 && k % 32 == 0 && k <= kMaxK;
 }
 
-// The workspace: codes [m x k], then scales [m].
+// The workspace: codes [m x k], scales [m], the tokens' tiles.
 size_t codes_bytes(int64_t m, int64_t k) { return static_cast<size_t>(round_up(m * k, 256)); }
+size_t image_at(int64_t m, int64_t k) { return codes_bytes(m, k) + static_cast<size_t>(round_up(4 * m, 256)); }
+
+constexpr int64_t kFewTokens = 16;
 
 int product(const void *W8, const int8_t *Xq, const float *sx, void *Y, int64_t ldy, int ytype, int64_t m, int64_t k,
-            int64_t n, cudaStream_t s)
+            int64_t n, void *workspace, size_t workspace_bytes, const DeviceInfo &dev, cudaStream_t s)
 {
+    if (m > kFewTokens) {
+        W8a8GemmPlan plan;
+        if (!plan_w8a8_gemm(m, k, n, &plan)) return Q4_ERR_INVALID_ARG;
+        if (workspace_bytes < image_at(m, k) + plan.image_bytes) return Q4_ERR_WORKSPACE;
+        W8a8GemmArgs g{};
+        g.W = static_cast<const uint8_t *>(W8);
+        g.np = static_cast<int>(ceil_div(k, kPairK));
+        g.groups = static_cast<int>(ceil_div(n, kW8GroupRows));
+        g.row_scale = reinterpret_cast<const float *>(g.W + static_cast<size_t>(g.groups) * g.np * kW8RecordBytes);
+        g.sx = sx;
+        g.Y = Y;
+        g.ldy = ldy;
+        g.ytype = ytype;
+        g.status = dev.status;
+        wait_settings(&g.wait_ns, &g.prefetch_w);
+        g.m = static_cast<int>(m);
+        g.n = static_cast<int>(n);
+        return cuda_status(launch_w8a8_gemm(plan, g, Xq, k, static_cast<uint8_t *>(workspace) + image_at(m, k), dev.sm_count, s));
+    }
     W8a8Args a{};
     a.W = static_cast<const uint8_t *>(W8);
     a.Xq = Xq;
@@ -95,7 +117,9 @@ extern "C" {
 Q4MM_API size_t q4_w8a8_workspace_size(int64_t m, int64_t k, int64_t n)
 {
     if (m <= 0 || !valid_sizes(m, k, n)) return 0;
-    return codes_bytes(m, k) + static_cast<size_t>(round_up(4 * m, 256));
+    W8a8GemmPlan plan;
+    if (m > kFewTokens && plan_w8a8_gemm(m, k, n, &plan)) return image_at(m, k) + plan.image_bytes;
+    return image_at(m, k);
 }
 
 Q4MM_API int q4_w8a8_matmul(const void *W8_packed, const void *X, int64_t ldx, int xtype, void *Y, int64_t ldy,
@@ -118,7 +142,7 @@ Q4MM_API int q4_w8a8_matmul(const void *W8_packed, const void *X, int64_t ldx, i
     float *sx = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + codes_bytes(m, k));
     rc = quantize_rows(Xq, k, sx, X, ldx, xtype, m, k, dev.sm_count, s);
     if (rc != Q4_OK) return rc;
-    return product(W8_packed, Xq, sx, Y, ldy, ytype, m, k, n, s);
+    return product(W8_packed, Xq, sx, Y, ldy, ytype, m, k, n, workspace, workspace_bytes, dev, s);
 }
 
 Q4MM_API int q4_w8a8_matmul_codes(const void *W8_packed, const int8_t *Xq, const float *sx, void *Y, int64_t ldy,
@@ -135,7 +159,8 @@ Q4MM_API int q4_w8a8_matmul_codes(const void *W8_packed, const int8_t *Xq, const
     DeviceInfo dev;
     const int rc = device_info(&dev);
     if (rc != Q4_OK) return rc;
-    return product(W8_packed, Xq, sx, Y, ldy, ytype, m, k, n, reinterpret_cast<cudaStream_t>(stream));
+    return product(W8_packed, Xq, sx, Y, ldy, ytype, m, k, n, workspace, workspace_bytes, dev,
+                   reinterpret_cast<cudaStream_t>(stream));
 }
 
 } // extern "C"

@@ -21,4 +21,36 @@ struct W8a8Args {
     int m, n, k, np, groups;
 };
 
+// The tensor-core product (many tokens).
+struct W8a8GemmPlan {
+    int N = 0;                // tokens of a tile: a multiple of 32, at most 256
+    int ts = 0;               // token tiles
+    int tiles = 0;            // (256 rows) x (N tokens)
+    int pairs = 0;            // CTA pairs of the grid, each taking tiles in turn
+    int stages = 0, wring = 0;
+    size_t smem = 0;
+    size_t image_bytes = 0;   // the tokens' fp16 tiles
+};
+
+struct W8a8GemmArgs {
+    const uint8_t *W;
+    const float *row_scale;
+    const uint8_t *ximg;
+    const float *sx;
+    void *Y;
+    int64_t ldy;
+    int ytype;
+    int *status;
+    uint64_t wait_ns;
+    int m, n, np, groups;
+    int N, ts, tiles;
+    int stages, wring;
+    int prefetch_w;
+};
+
+bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan);
+// Codes [m x k] to the fp16 tiles, then the product.
+cudaError_t launch_w8a8_gemm(const W8a8GemmPlan &plan, const W8a8GemmArgs &args, const int8_t *Xq, int64_t k,
+                             uint8_t *ximg, int sm_count, cudaStream_t s);
+
 } // namespace q4
