@@ -69,19 +69,30 @@ size_t image_at(int64_t m, int64_t k) { return codes_bytes(m, k) + static_cast<s
 
 constexpr int64_t kFewTokens = 16;
 
-int product(const void *W8, const int8_t *Xq, const float *sx, void *Y, int64_t ldy, int ytype, int64_t m, int64_t k,
-            int64_t n, void *workspace, size_t workspace_bytes, const DeviceInfo &dev, cudaStream_t s)
+// `tok`: codes with their scales, or rows to be coded.
+int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int64_t m, int64_t k, int64_t n,
+            void *workspace, size_t workspace_bytes, q4mm_stream_t stream)
 {
+    DeviceInfo dev;
+    int rc = device_info(&dev);
+    if (rc != Q4_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool coded = tok.Xq != nullptr;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if (!coded) tok.sx = reinterpret_cast<float *>(ws + codes_bytes(m, k));
+    const uint8_t *W = static_cast<const uint8_t *>(W8);
+    const int np = static_cast<int>(ceil_div(k, kPairK)), groups = static_cast<int>(ceil_div(n, kW8GroupRows));
+    const float *row_scale = reinterpret_cast<const float *>(W + static_cast<size_t>(groups) * np * kW8RecordBytes);
     if (m > kFewTokens) {
         W8a8GemmPlan plan;
         if (!plan_w8a8_gemm(m, k, n, &plan)) return Q4_ERR_INVALID_ARG;
         if (workspace_bytes < image_at(m, k) + plan.image_bytes) return Q4_ERR_WORKSPACE;
         W8a8GemmArgs g{};
-        g.W = static_cast<const uint8_t *>(W8);
-        g.np = static_cast<int>(ceil_div(k, kPairK));
-        g.groups = static_cast<int>(ceil_div(n, kW8GroupRows));
-        g.row_scale = reinterpret_cast<const float *>(g.W + static_cast<size_t>(g.groups) * g.np * kW8RecordBytes);
-        g.sx = sx;
+        g.W = W;
+        g.np = np;
+        g.groups = groups;
+        g.row_scale = row_scale;
+        g.sx = tok.sx;
         g.Y = Y;
         g.ldy = ldy;
         g.ytype = ytype;
@@ -89,21 +100,26 @@ int product(const void *W8, const int8_t *Xq, const float *sx, void *Y, int64_t 
         wait_settings(&g.wait_ns, &g.prefetch_w);
         g.m = static_cast<int>(m);
         g.n = static_cast<int>(n);
-        return cuda_status(launch_w8a8_gemm(plan, g, Xq, k, static_cast<uint8_t *>(workspace) + image_at(m, k), dev.sm_count, s));
+        return cuda_status(launch_w8a8_gemm(plan, g, tok, k, ws + image_at(m, k), dev.sm_count, s));
+    }
+    if (!coded) {
+        rc = quantize_rows(reinterpret_cast<int8_t *>(ws), k, tok.sx, tok.X, tok.ldx, tok.xtype, m, k, dev.sm_count, s);
+        if (rc != Q4_OK) return rc;
+        tok.Xq = reinterpret_cast<const int8_t *>(ws);
     }
     W8a8Args a{};
-    a.W = static_cast<const uint8_t *>(W8);
-    a.Xq = Xq;
-    a.sx = sx;
+    a.W = W;
+    a.Xq = tok.Xq;
+    a.sx = tok.sx;
     a.Y = Y;
     a.ldy = ldy;
     a.ytype = ytype;
     a.m = static_cast<int>(m);
     a.n = static_cast<int>(n);
     a.k = static_cast<int>(k);
-    a.np = static_cast<int>(ceil_div(k, kPairK));
-    a.groups = static_cast<int>(ceil_div(n, kW8GroupRows));
-    a.row_scale = reinterpret_cast<const float *>(a.W + static_cast<size_t>(a.groups) * a.np * kW8RecordBytes);
+    a.np = np;
+    a.groups = groups;
+    a.row_scale = row_scale;
     return cuda_status(launch_product(a, s));
 }
 
@@ -134,15 +150,15 @@ Q4MM_API int q4_w8a8_matmul(const void *W8_packed, const void *X, int64_t ldx, i
         return Q4_ERR_ALIGNMENT;
     if (m == 0) return Q4_OK;
     if (!workspace || workspace_bytes < q4_w8a8_workspace_size(m, k, n)) return Q4_ERR_WORKSPACE;
-    DeviceInfo dev;
-    int rc = device_info(&dev);
-    if (rc != Q4_OK) return rc;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int8_t *Xq = static_cast<int8_t *>(workspace);
-    float *sx = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + codes_bytes(m, k));
-    rc = quantize_rows(Xq, k, sx, X, ldx, xtype, m, k, dev.sm_count, s);
-    if (rc != Q4_OK) return rc;
-    return product(W8_packed, Xq, sx, Y, ldy, ytype, m, k, n, workspace, workspace_bytes, dev, s);
+    const int size = type_size(xtype);
+    RowAlign al;
+    al.add(X, ldx * size);
+    W8a8Tokens tok;
+    tok.X = X;
+    tok.ldx = ldx;
+    tok.xtype = xtype;
+    tok.vec = al.bytes() >= 16 ? 16 / size : size == 2 && al.bytes() >= 4 ? 2 : 1;
+    return product(W8_packed, tok, Y, ldy, ytype, m, k, n, workspace, workspace_bytes, stream);
 }
 
 Q4MM_API int q4_w8a8_matmul_codes(const void *W8_packed, const int8_t *Xq, const float *sx, void *Y, int64_t ldy,
@@ -156,11 +172,10 @@ Q4MM_API int q4_w8a8_matmul_codes(const void *W8_packed, const int8_t *Xq, const
         return Q4_ERR_ALIGNMENT;
     if (m == 0) return Q4_OK;
     if (!workspace || workspace_bytes < q4_w8a8_workspace_size(m, k, n)) return Q4_ERR_WORKSPACE;
-    DeviceInfo dev;
-    const int rc = device_info(&dev);
-    if (rc != Q4_OK) return rc;
-    return product(W8_packed, Xq, sx, Y, ldy, ytype, m, k, n, workspace, workspace_bytes, dev,
-                   reinterpret_cast<cudaStream_t>(stream));
+    W8a8Tokens tok;
+    tok.Xq = Xq;
+    tok.sx = const_cast<float *>(sx);   // read only: the codes are there
+    return product(W8_packed, tok, Y, ldy, ytype, m, k, n, workspace, workspace_bytes, stream);
 }
 
 } // extern "C"

@@ -27,7 +27,7 @@ struct W8a8GemmPlan {
     int ts = 0;               // token tiles
     int tiles = 0;            // (256 rows) x (N tokens)
     int pairs = 0;            // CTA pairs of the grid, each taking tiles in turn
-    int stages = 0, wring = 0;
+    int astages = 0, bstages = 0, wring = 0;
     size_t smem = 0;
     size_t image_bytes = 0;   // the tokens' fp16 tiles
 };
@@ -44,13 +44,22 @@ struct W8a8GemmArgs {
     uint64_t wait_ns;
     int m, n, np, groups;
     int N, ts, tiles;
-    int stages, wring;
+    int astages, bstages, wring;
     int prefetch_w;
 };
 
 bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan);
-// Codes [m x k] to the fp16 tiles, then the product.
-cudaError_t launch_w8a8_gemm(const W8a8GemmPlan &plan, const W8a8GemmArgs &args, const int8_t *Xq, int64_t k,
+// The tokens of a call: codes, or rows to be coded (their scales then go to
+// sx; `vec` elements an access).
+struct W8a8Tokens {
+    const int8_t *Xq = nullptr;
+    const void *X = nullptr;
+    int64_t ldx = 0;
+    int xtype = 0, vec = 1;
+    float *sx = nullptr;
+};
+// The tokens' fp16 tiles, then the product.
+cudaError_t launch_w8a8_gemm(const W8a8GemmPlan &plan, const W8a8GemmArgs &args, const W8a8Tokens &tokens, int64_t k,
                              uint8_t *ximg, int sm_count, cudaStream_t s);
 
 } // namespace q4

@@ -49,7 +49,9 @@ constexpr int kErrTimeout = 5;
 constexpr int kDequantWarp0 = 4, kDequantWarps = 8;
 constexpr int kEpilogueWarp0 = 12, kEpilogueWarps = 8;
 constexpr int kThreads = (kEpilogueWarp0 + kEpilogueWarps) * 32;
-constexpr int kMaxStages = 8, kWRing = 8;
+constexpr int kMaxAStages = 8, kMaxBStages = 16, kWRing = 8;
+constexpr int kStageTokens = 16;                                  // token columns an epilogue warp stages at once
+constexpr size_t kStagingBytes = kEpilogueWarps * kStageTokens * 32 * 4;
 
 // Codes to fp16 tiles: [half tile of H = N / 2 tokens][64 columns][H rows of
 // 128 bytes], 16-byte chunk c of row r at c ^ (r & 7). Rows past m and columns
@@ -86,9 +88,74 @@ __global__ void __launch_bounds__(256) tile_kernel(const int8_t *Xq, uint8_t *xi
     }
 }
 
+struct CodeTileArgs {
+    const void *X;
+    int64_t ldx;
+    uint8_t *ximg;
+    float *sx;
+    int m, rows;       // tokens, and with the last tile's padding
+    int64_t k;
+    int np, H;
+};
+
+// Tokens to codes and straight into the tiles: a row per CTA in turn, read
+// once (its first NV vectors a thread stay in registers; what is past them is
+// read again from L2). Rows m .. rows - 1 and columns past k are zeros. The
+// codes and scales are q4_a8_quantize's.
+template <typename T, int V> __global__ void __launch_bounds__(512) code_tile_kernel(const CodeTileArgs a)
+{
+    constexpr int NV = V >= 4 ? 2 : 4;
+    __shared__ float rbuf[2 * 96];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int G = blockDim.x, t = threadIdx.x, k = static_cast<int>(a.k), kp = a.np * kPairK;
+    RowReducer red{rbuf, G / 32};
+    for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T *xr = static_cast<const T *>(a.X) + row * a.ldx;
+        const int kr = row < a.m ? k : 0;
+        Pack<T, V> x[NV];
+        uint32_t mb = 0u;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * G + t) * V;
+            if (c < kr) x[i] = load_pack<T, V>(xr, c, kr);
+            else
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[i].e[j] = from_f32<T>(0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) mb = max(mb, abs_bits(to_f32(x[i].e[j])));
+        for (int c = (NV * G + t) * V; c < kr; c += G * V) {
+            const Pack<T, V> v = load_pack<T, V>(xr, c, kr);
+#pragma unroll
+            for (int j = 0; j < V; ++j) mb = max(mb, abs_bits(to_f32(v.e[j])));
+        }
+        const CodeScale cs = code_scale(red.max_bits(mb));
+        if (t == 0 && row < a.m) a.sx[row] = cs.scale;
+        const int j2 = row / a.H, r = row - j2 * a.H;
+        uint8_t *out = a.ximg + (static_cast<int64_t>(j2) * a.np * a.H + r) * 128;
+        auto put = [&](int c, const Pack<T, V> &v) {
+            Pack<__half, V> o;
+#pragma unroll
+            for (int j = 0; j < V; ++j) o.e[j] = __int2half_rn(code_of(to_f32(v.e[j]), cs.factor));
+            const int p = c / kPairK, e = c - p * kPairK;   // V divides 8: inside one 16-byte chunk
+            *reinterpret_cast<Pack<__half, V> *>(out + static_cast<int64_t>(p) * a.H * 128 + (((e >> 3) ^ (r & 7)) << 4) +
+                                                 (e & 7) * 2) = o;
+        };
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * G + t) * V;
+            if (c < kp) put(c, x[i]);
+        }
+        for (int c = (NV * G + t) * V; c < kp; c += G * V) put(c, load_pack<T, V>(xr, c, kr));
+    }
+}
+
 struct Smem {
-    uint8_t *b, *w;
-    uint64_t *full_b, *full_w, *empty_w, *ready, *empty, *d_full, *d_empty, *done;
+    uint8_t *b, *w, *stage;
+    uint64_t *full_b, *empty_b, *full_w, *empty_w, *ready, *empty_a, *d_full, *d_empty, *done;
     uint32_t *tmem_slot;
     int *abort;
 };
@@ -104,9 +171,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64
 {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, limit_ns)) != 0;
 }
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+// The MMA thread's wait: tests without suspending, since it resumes some 170 ns
+// late from a suspended wait and the tensor cores would run dry (4096 x 14336
+// x 4096: 404 us a call with suspended waits, 364 with tests).
+__device__ __forceinline__ bool spin_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
 {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity, limit_ns)) != 0;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_test_wait(bar, parity)) return true;
+        if ((i & 255u) == 0 && globaltimer_ns() - t0 > limit_ns) return false;
+    }
 }
 
 // A position in a ring of `depth` slots and its phase.
@@ -126,18 +200,20 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
-    const int N = a.N, H = N / 2, S = a.stages, RW = a.wring, np = a.np;
+    const int N = a.N, H = N / 2, SA = a.astages, SB = a.bstages, RW = a.wring, np = a.np;
     const uint32_t bstage = static_cast<uint32_t>(H) * 128u;
     const uint32_t acol0 = static_cast<uint32_t>(N);   // first A column after D (N is a multiple of 32)
 
     Smem sm;
     sm.b = base;
-    sm.w = sm.b + static_cast<size_t>(S) * bstage;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm.w + static_cast<size_t>(RW) * kW8RecordBytes);
+    sm.w = sm.b + static_cast<size_t>(SB) * bstage;
+    sm.stage = sm.w + static_cast<size_t>(RW) * kW8RecordBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm.stage + kStagingBytes);
     sm.full_b = bars;
-    sm.ready = sm.full_b + S;
-    sm.empty = sm.ready + S;
-    sm.full_w = sm.empty + S;
+    sm.empty_b = sm.full_b + SB;
+    sm.ready = sm.empty_b + SB;
+    sm.empty_a = sm.ready + SA;
+    sm.full_w = sm.empty_a + SA;
     sm.empty_w = sm.full_w + RW;
     sm.d_full = sm.empty_w + RW;
     sm.d_empty = sm.d_full + 1;
@@ -145,11 +221,9 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
     sm.tmem_slot = reinterpret_cast<uint32_t *>(sm.done + 1);
     sm.abort = reinterpret_cast<int *>(sm.tmem_slot + 1);
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(&sm.full_b[i], 1);
-            mbar_init(&sm.ready[i], kDequantWarps);     // a set's four warps in each CTA
-            mbar_init(&sm.empty[i], 1);
-        }
+        for (int i = 0; i < SB; ++i) mbar_init(&sm.full_b[i], 1), mbar_init(&sm.empty_b[i], 1);
+        // a step's operands are ready once a set's four warps in each CTA say so
+        for (int i = 0; i < SA; ++i) mbar_init(&sm.ready[i], kDequantWarps), mbar_init(&sm.empty_a[i], 1);
         for (int i = 0; i < RW; ++i) mbar_init(&sm.full_w[i], 1), mbar_init(&sm.empty_w[i], kDequantWarps / 2);
         mbar_init(sm.d_full, 1);
         mbar_init(sm.d_empty, 2 * kEpilogueWarps);
@@ -180,7 +254,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                 const uint8_t *src = a.ximg + (static_cast<size_t>(2 * jt) + rank) * np * bstage;
                 for (int p = 0; p < np; ++p) {
                     if (aborted(sm)) { ok = false; break; }
-                    if (issued >= S && !mbar_wait_cluster(&sm.empty[b.slot], b.phase ^ 1u, a.wait_ns)) {
+                    if (issued >= SB && !mbar_wait(&sm.empty_b[b.slot], b.phase ^ 1u, a.wait_ns)) {
                         fail(sm, a);
                         ok = false;
                         break;
@@ -189,13 +263,13 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                     bulk_g2s(sm.b + static_cast<size_t>(b.slot) * bstage, src + static_cast<size_t>(p) * bstage, bstage,
                              &sm.full_b[b.slot]);
                     ++issued;
-                    b.step(S);
+                    b.step(SB);
                 }
             }
             // after a timeout: what is still landing (all has been read otherwise)
             if (!ok)
-                for (int64_t i = issued > S ? issued - S : 0; i < issued; ++i)
-                    if (!mbar_wait(&sm.full_b[i % S], static_cast<uint32_t>(i / S) & 1u, a.wait_ns)) fail(sm, a);
+                for (int64_t i = issued > SB ? issued - SB : 0; i < issued; ++i)
+                    if (!mbar_wait(&sm.full_b[i % SB], static_cast<uint32_t>(i / SB) & 1u, a.wait_ns)) fail(sm, a);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -235,30 +309,36 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
             const uint32_t idesc = idesc_f16_f32(256, static_cast<uint32_t>(N));
             const uint64_t bdesc0 = smem_desc_sw128(smem_u32(sm.b));
             const uint64_t bstep = static_cast<uint64_t>(bstage >> 4);
-            Ring r;
+            Ring r, b;
             bool ok = true;
             uint32_t seq = 0;
             for (int tile = pair; ok && tile < a.tiles; tile += pairs, ++seq) {
                 // D has been read out of both CTAs' tensor memory
-                if (seq > 0 && !mbar_wait_cluster(sm.d_empty, (seq - 1) & 1u, a.wait_ns)) {
+                if (seq > 0 && !spin_wait(sm.d_empty, (seq - 1) & 1u, a.wait_ns)) {
                     fail(sm, a);
                     break;
                 }
+                bool ready = mbar_test_wait(&sm.ready[r.slot], r.phase);
                 for (int p = 0; p < np; ++p) {
-                    if (!mbar_wait_cluster(&sm.ready[r.slot], r.phase, a.wait_ns)) {
+                    if (!ready && !spin_wait(&sm.ready[r.slot], r.phase, a.wait_ns)) {
                         fail(sm, a);
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint64_t bd = bdesc0 + static_cast<uint64_t>(r.slot) * bstep;
+                    const uint64_t bd = bdesc0 + static_cast<uint64_t>(b.slot) * bstep;
                     const uint32_t at = tmem + acol0 + 32u * static_cast<uint32_t>(r.slot);
+                    const Ring now_a = r, now_b = b;
+                    r.step(SA);
+                    b.step(SB);
+                    // the next step's test overlaps this step's issue
+                    ready = p + 1 < np && mbar_test_wait(&sm.ready[r.slot], r.phase);
+                    tc_fence_after();
                     tc_mma_f16_ts_pair(tmem, at, bd, idesc, p > 0 ? 1u : 0u);
                     tc_mma_f16_ts_pair(tmem, at + 8u, bd + 2u, idesc, 1u);
                     tc_mma_f16_ts_pair(tmem, at + 16u, bd + 4u, idesc, 1u);
                     tc_mma_f16_ts_pair(tmem, at + 24u, bd + 6u, idesc, 1u);
-                    tc_commit_pair(&sm.empty[r.slot], 3);
-                    r.step(S);
+                    tc_commit_pair(&sm.empty_a[now_a.slot], 3);
+                    tc_commit_pair(&sm.empty_b[now_b.slot], 3);
                 }
                 if (ok) tc_commit_pair(sm.d_full, 3);
             }
@@ -270,15 +350,15 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         const int q = warp & 3, set = (warp - kDequantWarp0) >> 2;
         const int row = q * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-        Ring w, r;
+        Ring w, r, b;
         uint32_t step = 0;
         bool ok = true;
         for (int tile = pair; ok && tile < a.tiles; tile += pairs) {
-            for (int p = 0; p < np; ++p, ++step, w.step(RW), r.step(S)) {
-                if (static_cast<int>(step & 1u) != set) continue;   // both rings are even: a slot has one set
+            for (int p = 0; p < np; ++p, ++step, w.step(RW), r.step(SA), b.step(SB)) {
+                if (static_cast<int>(step & 1u) != set) continue;   // W's and A's rings are even: a slot has one set
                 if (__any_sync(0xFFFFFFFFu, aborted(sm))) { ok = false; break; }
                 if (!warp_wait(&sm.full_w[w.slot], w.phase, a.wait_ns) ||
-                    (step >= static_cast<uint32_t>(S) && !warp_wait_cluster(&sm.empty[r.slot], r.phase ^ 1u, a.wait_ns))) {
+                    (step >= static_cast<uint32_t>(SA) && !warp_wait(&sm.empty_a[r.slot], r.phase ^ 1u, a.wait_ns))) {
                     fail(sm, a);
                     ok = false;
                     break;
@@ -318,11 +398,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                 bool landed = true;
                 if (lane == 0) {
                     mbar_arrive(&sm.empty_w[w.slot]);
-                    landed = mbar_wait(&sm.full_b[r.slot], r.phase, a.wait_ns);
-                    if (landed) {
-                        fence_proxy_async_smem();
-                        mbar_arrive_remote(mapa_shared(smem_u32(&sm.ready[r.slot]), 0u));
-                    }
+                    landed = mbar_wait(&sm.full_b[b.slot], b.phase, a.wait_ns);
+                    if (landed) mbar_arrive_remote_async(mapa_shared(smem_u32(&sm.ready[r.slot]), 0u));
                 }
                 if (!__shfl_sync(0xFFFFFFFFu, landed ? 1 : 0, 0)) {
                     fail(sm, a);
@@ -333,36 +410,77 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         }
     } else if (warp >= kEpilogueWarp0) {
         // ------------------------------------------------------- epilogue
+        // A lane holds one weight row; Y's rows are tokens. Sixteen tokens at a
+        // time go through the warp's staging area and out as 16 bytes a lane
+        // (with 2- or 4-byte stores straight from the registers the epilogue of
+        // a 256 x 256 tile took 3.7 us); a Y whose rows are not 16-byte aligned
+        // is written element by element.
         pdl_wait();
         const int q = warp & 3, half = (warp - kEpilogueWarp0) >> 2;
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+        constexpr int kVec = 16 / sizeof(T);            // elements of a store
+        constexpr int kLanesPerToken = 32 / kVec;
+        constexpr int kTokensPerStore = 32 / kLanesPerToken;
+        T *stage = reinterpret_cast<T *>(sm.stage + (warp - kEpilogueWarp0) * (kStageTokens * 32 * 4));
         T *Y = static_cast<T *>(a.Y);
+        const bool wide = (reinterpret_cast<uintptr_t>(Y) & 15u) == 0 && (a.ldy * sizeof(T)) % 16 == 0;
         uint32_t seq = 0;
         for (int tile = pair; tile < a.tiles; tile += pairs, ++seq) {
             const int G = 2 * (tile / a.ts) + static_cast<int>(rank);
-            const int64_t row = static_cast<int64_t>(G) * kW8GroupRows + q * 32 + lane;
-            const bool live = G < a.groups && row < a.n;
-            const float sw = live ? __ldg(a.row_scale + row) : 0.0f;
-            if (!warp_wait_cluster(sm.d_full, seq & 1u, a.wait_ns)) {
+            const int64_t row0 = static_cast<int64_t>(G) * kW8GroupRows + q * 32;
+            const int rows = G < a.groups ? static_cast<int>(max(int64_t(0), min(int64_t(32), a.n - row0))) : 0;
+            const float sw = lane < rows ? __ldg(a.row_scale + row0 + lane) : 0.0f;
+            const int t0 = (tile % a.ts) * N + half * H;        // this warp's tokens: t0 .. t0 + H - 1
+            float sx[4];                                        // of tokens t0 + 32 i + lane
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sx[i] = 32 * i < H && t0 + 32 * i + lane < a.m ? __ldg(a.sx + t0 + 32 * i + lane) : 0.0f;
+            if (!warp_wait(sm.d_full, seq & 1u, a.wait_ns)) {
                 fail(sm, a);
                 break;
             }
             tc_fence_after();
-            const int t0 = (tile % a.ts) * N;
-            for (int c0 = half * H; c0 < half * H + H; c0 += 16) {
+            const uint32_t d0 = tmem + lane_base + static_cast<uint32_t>(half * H);
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+                if (ch * kStageTokens >= H) break;
                 uint32_t v[16];
-                tmem_ld_32x32b_x16(tmem + lane_base + static_cast<uint32_t>(c0), v);
+                tmem_ld_32x32b_x16(d0 + static_cast<uint32_t>(ch * kStageTokens), v);
                 tmem_wait_ld();
-                if (c0 + 16 == half * H + H) {
+                if ((ch + 1) * kStageTokens >= H) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(sm.d_empty), 0u));
+                    if (lane == 0) mbar_arrive_remote_async(mapa_shared(smem_u32(sm.d_empty), 0u));
                 }
+                float y[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = t0 + c0 + i;
-                    if (t < a.m && live)
-                        Y[t * a.ldy + row] = from_f32<T>(__uint_as_float(v[i]) * (__ldg(a.sx + t) * sw));
+                for (int i = 0; i < 16; ++i)
+                    y[i] = __uint_as_float(v[i]) * (__shfl_sync(0xFFFFFFFFu, sx[ch >> 1], (ch & 1) * 16 + i) * sw);
+                const int tc = t0 + ch * kStageTokens;
+                if (wide) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) stage[i * 32 + lane] = from_f32<T>(y[i]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kStageTokens; i += kTokensPerStore) {
+                        const int tk = i + lane / kLanesPerToken, c = (lane % kLanesPerToken) * kVec;
+                        const uint4 o = lds128(stage + tk * 32 + c);
+                        if (tc + tk < a.m) {
+                            T *dst = Y + (tc + tk) * a.ldy + row0 + c;
+                            if (c + kVec <= rows) {
+                                *reinterpret_cast<uint4 *>(dst) = o;
+                            } else {
+                                const T *e = reinterpret_cast<const T *>(&o);
+#pragma unroll
+                                for (int u = 0; u < kVec; ++u)
+                                    if (c + u < rows) dst[u] = e[u];
+                            }
+                        }
+                    }
+                    __syncwarp();
+                } else if (lane < rows) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (tc + i < a.m) Y[(tc + i) * a.ldy + row0 + lane] = from_f32<T>(y[i]);
                 }
             }
         }
@@ -370,7 +488,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
 
     // No MMA of the pair and none of its arrivals is in flight past this.
     __syncthreads();
-    if (tid == 0 && !mbar_wait_cluster(sm.done, 0, a.wait_ns)) fail(sm, a);
+    if (tid == 0 && !mbar_wait(sm.done, 0, a.wait_ns)) fail(sm, a);
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // neither CTA's memory is used by the other past this
@@ -385,10 +503,10 @@ const void *kernel_of(int ytype)
                                   : reinterpret_cast<const void *>(&w8a8_gemm_kernel<__nv_bfloat16>);
 }
 
-size_t smem_bytes(int N, int stages, int wring)
+size_t smem_bytes(int N, int astages, int bstages, int wring)
 {
-    return 1024 + static_cast<size_t>(stages) * (N / 2) * 128 + static_cast<size_t>(wring) * kW8RecordBytes +
-           static_cast<size_t>(3 * stages + 2 * wring + 3) * 8 + 16;
+    return 1024 + static_cast<size_t>(bstages) * (N / 2) * 128 + static_cast<size_t>(wring) * kW8RecordBytes + kStagingBytes +
+           static_cast<size_t>(2 * bstages + 2 * astages + 2 * wring + 3) * 8 + 16;
 }
 
 // CTA pairs that the current device holds at once; 0 when it cannot be asked.
@@ -439,9 +557,11 @@ bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan)
     for (int N = 32; N <= 256; N += 32) {
         W8a8GemmPlan c;
         c.N = N;
-        c.stages = std::min(kMaxStages, (512 - N) / 32) & ~1;
+        c.astages = std::min(kMaxAStages, (512 - N) / 32) & ~1;
         c.wring = kWRing;
-        c.smem = std::max<size_t>(smem_bytes(N, c.stages, c.wring), kSmemPerSM / 2 + 1024);   // one CTA per SM
+        c.bstages = kMaxBStages;
+        while (c.bstages > 2 && smem_bytes(N, c.astages, c.bstages, c.wring) > kSmemOptIn) --c.bstages;
+        c.smem = std::max<size_t>(smem_bytes(N, c.astages, c.bstages, c.wring), kSmemPerSM / 2 + 1024);   // one CTA per SM
         if (c.smem > kSmemOptIn) continue;
         c.ts = static_cast<int>(ceil_div(m, N));
         if (rt * c.ts > (int64_t(1) << 30)) continue;
@@ -462,27 +582,58 @@ bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan)
     return true;
 }
 
-cudaError_t launch_w8a8_gemm(const W8a8GemmPlan &plan, const W8a8GemmArgs &args, const int8_t *Xq, int64_t k,
+namespace {
+template <typename T> cudaError_t launch_code_tiles(CodeTileArgs a, int vec, int sm_count, cudaStream_t s)
+{
+    const void *fn = vec * sizeof(T) == 16 ? reinterpret_cast<const void *>(&code_tile_kernel<T, 16 / sizeof(T)>)
+                     : vec == 2            ? reinterpret_cast<const void *>(&code_tile_kernel<T, 2>)
+                                           : reinterpret_cast<const void *>(&code_tile_kernel<T, 1>);
+    const int64_t vecs = ceil_div(static_cast<int64_t>(a.np) * kPairK, vec);
+    const int threads = static_cast<int>(std::min<int64_t>(512, round_up(ceil_div(vecs, vec >= 4 ? 2 : 4), 32)));
+    const int64_t grid = std::min<int64_t>(a.rows, static_cast<int64_t>(sm_count) * (2048 / std::max(threads, 128)));
+    void *args[] = {&a};
+    return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads)), 0, s, args);
+}
+} // namespace
+
+cudaError_t launch_w8a8_gemm(const W8a8GemmPlan &plan, const W8a8GemmArgs &args, const W8a8Tokens &tok, int64_t k,
                              uint8_t *ximg, int sm_count, cudaStream_t s)
 {
     int m = args.m, np = args.np, H = plan.N / 2, halves = 2 * plan.ts;
-    {
+    cudaError_t e;
+    if (tok.Xq) {
+        const int8_t *Xq = tok.Xq;
         void *kargs[] = {&Xq, &ximg, &m, &k, &np, &H, &halves};
         const int64_t blocks = ceil_div(static_cast<int64_t>(halves) * np * H * 4, 256);
-        const cudaError_t e = launch_pdl(reinterpret_cast<const void *>(&tile_kernel),
-                                         dim3(static_cast<unsigned>(std::min<int64_t>(blocks, 8 * static_cast<int64_t>(sm_count)))),
-                                         dim3(256), 0, s, kargs);
-        if (e != cudaSuccess) return e;
+        e = launch_pdl(reinterpret_cast<const void *>(&tile_kernel),
+                       dim3(static_cast<unsigned>(std::min<int64_t>(blocks, 8 * static_cast<int64_t>(sm_count)))), dim3(256),
+                       0, s, kargs);
+    } else {
+        CodeTileArgs c{};
+        c.X = tok.X;
+        c.ldx = tok.ldx;
+        c.ximg = ximg;
+        c.sx = tok.sx;
+        c.m = m;
+        c.rows = halves * H;
+        c.k = k;
+        c.np = np;
+        c.H = H;
+        e = tok.xtype == Q4_TYPE_F32   ? launch_code_tiles<float>(c, tok.vec, sm_count, s)
+            : tok.xtype == Q4_TYPE_F16 ? launch_code_tiles<__half>(c, tok.vec, sm_count, s)
+                                       : launch_code_tiles<__nv_bfloat16>(c, tok.vec, sm_count, s);
     }
+    if (e != cudaSuccess) return e;
     W8a8GemmArgs a = args;
     a.ximg = ximg;
     a.N = plan.N;
     a.ts = plan.ts;
     a.tiles = plan.tiles;
-    a.stages = plan.stages;
+    a.astages = plan.astages;
+    a.bstages = plan.bstages;
     a.wring = plan.wring;
     const void *fn = kernel_of(a.ytype);
-    const cudaError_t e = set_max_smem(fn, plan.smem);
+    e = set_max_smem(fn, plan.smem);
     if (e != cudaSuccess) return e;
     void *kargs[] = {&a};
     return launch_pdl(fn, dim3(static_cast<unsigned>(2 * plan.pairs)), dim3(kThreads), plan.smem, s, kargs, 2);
