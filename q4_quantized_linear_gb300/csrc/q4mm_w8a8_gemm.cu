@@ -49,7 +49,14 @@ constexpr int kErrTimeout = 5;
 constexpr int kDequantWarp0 = 4, kDequantWarps = 8;
 constexpr int kEpilogueWarp0 = 12, kEpilogueWarps = 8;
 constexpr int kThreads = (kEpilogueWarp0 + kEpilogueWarps) * 32;
-constexpr int kMaxAStages = 8, kMaxBStages = 16, kWRing = 8;
+// A step of the K loop takes two records' columns (128): every barrier is
+// touched half as often as with one, and a step's fixed latencies (two waits,
+// a store to tensor memory, two arrivals, a commit), some 0.35 us, bounded the
+// loop at 0.36 us a record with one.
+constexpr int kStepRecords = 2;
+constexpr uint32_t kSlotBytes = kStepRecords * kW8RecordBytes;
+constexpr int kMaxAStages = 8, kMaxBStages = 10, kWRing = 4;
+constexpr uint32_t kAColumns = kStepRecords * 32;                 // tensor-memory columns of a step's weights
 constexpr int kStageTokens = 16;                                  // token columns an epilogue warp stages at once
 constexpr size_t kStagingBytes = kEpilogueWarps * kStageTokens * 32 * 4;
 
@@ -201,19 +208,22 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
     const uint32_t rank = cluster_ctarank();
     const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
     const int N = a.N, H = N / 2, SA = a.astages, SB = a.bstages, RW = a.wring, np = a.np;
-    const uint32_t bstage = static_cast<uint32_t>(H) * 128u;
+    const uint32_t brec = static_cast<uint32_t>(H) * 128u;    // a record's columns of the half tile
+    const uint32_t bstage = kStepRecords * brec;
+    const int steps = (np + kStepRecords - 1) / kStepRecords;   // of a tile; the last may hold one record
     const uint32_t acol0 = static_cast<uint32_t>(N);   // first A column after D (N is a multiple of 32)
 
     Smem sm;
     sm.b = base;
     sm.w = sm.b + static_cast<size_t>(SB) * bstage;
-    sm.stage = sm.w + static_cast<size_t>(RW) * kW8RecordBytes;
+    sm.stage = sm.w + static_cast<size_t>(RW) * kSlotBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm.stage + kStagingBytes);
     sm.full_b = bars;
-    sm.empty_b = sm.full_b + SB;
-    sm.ready = sm.empty_b + SB;
+    sm.ready = sm.full_b + SB;
     sm.empty_a = sm.ready + SA;
-    sm.full_w = sm.empty_a + SA;
+    // rings of one depth turn together: one commit releases both
+    sm.empty_b = SB == SA ? sm.empty_a : sm.empty_a + SA;
+    sm.full_w = sm.empty_a + SA + (SB == SA ? 0 : SB);
     sm.empty_w = sm.full_w + RW;
     sm.d_full = sm.empty_w + RW;
     sm.d_empty = sm.d_full + 1;
@@ -221,7 +231,9 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
     sm.tmem_slot = reinterpret_cast<uint32_t *>(sm.done + 1);
     sm.abort = reinterpret_cast<int *>(sm.tmem_slot + 1);
     if (tid == 0) {
-        for (int i = 0; i < SB; ++i) mbar_init(&sm.full_b[i], 1), mbar_init(&sm.empty_b[i], 1);
+        for (int i = 0; i < SB; ++i) mbar_init(&sm.full_b[i], 1);
+        if (SB != SA)
+            for (int i = 0; i < SB; ++i) mbar_init(&sm.empty_b[i], 1);
         // a step's operands are ready once a set's four warps in each CTA say so
         for (int i = 0; i < SA; ++i) mbar_init(&sm.ready[i], kDequantWarps), mbar_init(&sm.empty_a[i], 1);
         for (int i = 0; i < RW; ++i) mbar_init(&sm.full_w[i], 1), mbar_init(&sm.empty_w[i], kDequantWarps / 2);
@@ -251,16 +263,17 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
             bool ok = true;
             for (int tile = pair; ok && tile < a.tiles; tile += pairs) {
                 const int jt = tile % a.ts;
-                const uint8_t *src = a.ximg + (static_cast<size_t>(2 * jt) + rank) * np * bstage;
-                for (int p = 0; p < np; ++p) {
+                const uint8_t *src = a.ximg + (static_cast<size_t>(2 * jt) + rank) * np * brec;
+                for (int st = 0; st < steps; ++st) {
                     if (aborted(sm)) { ok = false; break; }
                     if (issued >= SB && !mbar_wait(&sm.empty_b[b.slot], b.phase ^ 1u, a.wait_ns)) {
                         fail(sm, a);
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&sm.full_b[b.slot], bstage);
-                    bulk_g2s(sm.b + static_cast<size_t>(b.slot) * bstage, src + static_cast<size_t>(p) * bstage, bstage,
+                    const uint32_t bytes = static_cast<uint32_t>(min(kStepRecords, np - st * kStepRecords)) * brec;
+                    mbar_arrive_expect_tx(&sm.full_b[b.slot], bytes);
+                    bulk_g2s(sm.b + static_cast<size_t>(b.slot) * bstage, src + static_cast<size_t>(st) * bstage, bytes,
                              &sm.full_b[b.slot]);
                     ++issued;
                     b.step(SB);
@@ -284,16 +297,17 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                 // reads the last group again and writes nothing
                 const int G = min(2 * (tile / a.ts) + static_cast<int>(rank), a.groups - 1);
                 const uint8_t *src = a.W + static_cast<size_t>(G) * np * kW8RecordBytes;
-                for (int p = 0; p < np; ++p) {
+                for (int st = 0; st < steps; ++st) {
                     if (aborted(sm)) { ok = false; break; }
                     if (issued >= RW && !mbar_wait(&sm.empty_w[w.slot], w.phase ^ 1u, a.wait_ns)) {
                         fail(sm, a);
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&sm.full_w[w.slot], kW8RecordBytes);
-                    bulk_g2s(sm.w + static_cast<size_t>(w.slot) * kW8RecordBytes, src + static_cast<size_t>(p) * kW8RecordBytes,
-                             kW8RecordBytes, &sm.full_w[w.slot]);
+                    const uint32_t bytes = static_cast<uint32_t>(min(kStepRecords, np - st * kStepRecords)) * kW8RecordBytes;
+                    mbar_arrive_expect_tx(&sm.full_w[w.slot], bytes);
+                    bulk_g2s(sm.w + static_cast<size_t>(w.slot) * kSlotBytes, src + static_cast<size_t>(st) * kSlotBytes, bytes,
+                             &sm.full_w[w.slot]);
                     ++issued;
                     w.step(RW);
                 }
@@ -308,7 +322,6 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         if (rank == 0 && lane == 0) {
             const uint32_t idesc = idesc_f16_f32(256, static_cast<uint32_t>(N));
             const uint64_t bdesc0 = smem_desc_sw128(smem_u32(sm.b));
-            const uint64_t bstep = static_cast<uint64_t>(bstage >> 4);
             Ring r, b;
             bool ok = true;
             uint32_t seq = 0;
@@ -319,26 +332,30 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                     break;
                 }
                 bool ready = mbar_test_wait(&sm.ready[r.slot], r.phase);
-                for (int p = 0; p < np; ++p) {
+                for (int st = 0; st < steps; ++st) {
                     if (!ready && !spin_wait(&sm.ready[r.slot], r.phase, a.wait_ns)) {
                         fail(sm, a);
                         ok = false;
                         break;
                     }
-                    const uint64_t bd = bdesc0 + static_cast<uint64_t>(b.slot) * bstep;
-                    const uint32_t at = tmem + acol0 + 32u * static_cast<uint32_t>(r.slot);
-                    const Ring now_a = r, now_b = b;
+                    const uint64_t bd = bdesc0 + static_cast<uint64_t>(b.slot) * (bstage >> 4);
+                    const uint32_t at = tmem + acol0 + kAColumns * static_cast<uint32_t>(r.slot);
+                    uint64_t *const done_a = &sm.empty_a[r.slot], *const done_b = &sm.empty_b[b.slot];
                     r.step(SA);
                     b.step(SB);
                     // the next step's test overlaps this step's issue
-                    ready = p + 1 < np && mbar_test_wait(&sm.ready[r.slot], r.phase);
+                    ready = st + 1 < steps && mbar_test_wait(&sm.ready[r.slot], r.phase);
                     tc_fence_after();
-                    tc_mma_f16_ts_pair(tmem, at, bd, idesc, p > 0 ? 1u : 0u);
-                    tc_mma_f16_ts_pair(tmem, at + 8u, bd + 2u, idesc, 1u);
-                    tc_mma_f16_ts_pair(tmem, at + 16u, bd + 4u, idesc, 1u);
-                    tc_mma_f16_ts_pair(tmem, at + 24u, bd + 6u, idesc, 1u);
-                    tc_commit_pair(&sm.empty_a[now_a.slot], 3);
-                    tc_commit_pair(&sm.empty_b[now_b.slot], 3);
+                    tc_mma_f16_ts_pair(tmem, at, bd, idesc, st > 0 ? 1u : 0u);
+#pragma unroll
+                    for (uint32_t i = 1; i < 4; ++i) tc_mma_f16_ts_pair(tmem, at + 8u * i, bd + 2u * i, idesc, 1u);
+                    if ((st + 1) * kStepRecords <= np) {
+                        const uint64_t bd2 = bd + (brec >> 4);
+#pragma unroll
+                        for (uint32_t i = 0; i < 4; ++i) tc_mma_f16_ts_pair(tmem, at + 32u + 8u * i, bd2 + 2u * i, idesc, 1u);
+                    }
+                    tc_commit_pair(done_a, 3);
+                    if (SB != SA) tc_commit_pair(done_b, 3);
                 }
                 if (ok) tc_commit_pair(sm.d_full, 3);
             }
@@ -354,7 +371,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         uint32_t step = 0;
         bool ok = true;
         for (int tile = pair; ok && tile < a.tiles; tile += pairs) {
-            for (int p = 0; p < np; ++p, ++step, w.step(RW), r.step(SA), b.step(SB)) {
+            for (int st = 0; st < steps; ++st, ++step, w.step(RW), r.step(SA), b.step(SB)) {
                 if (static_cast<int>(step & 1u) != set) continue;   // W's and A's rings are even: a slot has one set
                 if (__any_sync(0xFFFFFFFFu, aborted(sm))) { ok = false; break; }
                 if (!warp_wait(&sm.full_w[w.slot], w.phase, a.wait_ns) ||
@@ -363,41 +380,48 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                     ok = false;
                     break;
                 }
-                // A row is four 16-byte chunks, rows 64 bytes apart: lanes reading
-                // the same chunk would share two bank groups, four lanes each. So
-                // lane l starts at chunk (l / 2) % 4, and the chunks are put back in
-                // order by selects (registers take no index).
-                const uint8_t *rec = sm.w + static_cast<size_t>(w.slot) * kW8RecordBytes + row * kPairK;
-                const int rot = (lane >> 1) & 3;
-                uint32_t u[16], out[32];
-                {
-                    uint32_t v[16];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint4 x = lds128(rec + 16 * ((c + rot) & 3));
-                        v[4 * c] = x.x, v[4 * c + 1] = x.y, v[4 * c + 2] = x.z, v[4 * c + 3] = x.w;
-                    }
-                    uint32_t t[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) t[i] = (rot & 1) ? v[(i + 12) & 15] : v[i];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) u[i] = (rot & 2) ? t[(i + 8) & 15] : t[i];
-                }
-                // a byte is 128 + c: as the low mantissa byte of 1024 it is the fp16
-                // 1152 + c, less 1152 exactly c
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    out[2 * i] = hsub2_bits(__byte_perm(u[i], 0x64646464u, 0x4140), 0x64806480u);
-                    out[2 * i + 1] = hsub2_bits(__byte_perm(u[i], 0x64646464u, 0x4342), 0x64806480u);
-                }
                 tc_fence_after();
-                tmem_st_32x32b_x32(tmem + lane_base + acol0 + static_cast<uint32_t>(r.slot) * 32u, out);
+                const uint32_t at = tmem + lane_base + acol0 + static_cast<uint32_t>(r.slot) * kAColumns;
+                const int records = min(kStepRecords, np - st * kStepRecords);
+#pragma unroll
+                for (int rec = 0; rec < kStepRecords; ++rec) {
+                    if (rec >= records) break;
+                    // A row is four 16-byte chunks, rows 64 bytes apart: lanes reading
+                    // the same chunk would share two bank groups, four lanes each. So
+                    // lane l starts at chunk (l / 2) % 4, and the chunks are put back in
+                    // order by selects (registers take no index).
+                    const uint8_t *src = sm.w + static_cast<size_t>(w.slot) * kSlotBytes + rec * kW8RecordBytes + row * kPairK;
+                    const int rot = (lane >> 1) & 3;
+                    uint32_t u[16], out[32];
+                    {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint4 x = lds128(src + 16 * ((c + rot) & 3));
+                            v[4 * c] = x.x, v[4 * c + 1] = x.y, v[4 * c + 2] = x.z, v[4 * c + 3] = x.w;
+                        }
+                        uint32_t t[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) t[i] = (rot & 1) ? v[(i + 12) & 15] : v[i];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) u[i] = (rot & 2) ? t[(i + 8) & 15] : t[i];
+                    }
+                    // a byte is 128 + c: as the low mantissa byte of 1024 it is the fp16
+                    // 1152 + c, less 1152 exactly c
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        out[2 * i] = hsub2_bits(__byte_perm(u[i], 0x64646464u, 0x4140), 0x64806480u);
+                        out[2 * i + 1] = hsub2_bits(__byte_perm(u[i], 0x64646464u, 0x4342), 0x64806480u);
+                    }
+                    tmem_st_32x32b_x32(at + 32u * rec, out);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.empty_w[w.slot]);   // read into registers
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 bool landed = true;
                 if (lane == 0) {
-                    mbar_arrive(&sm.empty_w[w.slot]);
                     landed = mbar_wait(&sm.full_b[b.slot], b.phase, a.wait_ns);
                     if (landed) mbar_arrive_remote_async(mapa_shared(smem_u32(&sm.ready[r.slot]), 0u));
                 }
@@ -440,47 +464,77 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
             }
             tc_fence_after();
             const uint32_t d0 = tmem + lane_base + static_cast<uint32_t>(half * H);
+            // D is read into registers, scaled and rounded, and given back before
+            // the stores: all H columns for 16-bit results, 64 at a time for fp32.
+            constexpr int kHold = sizeof(T) == 2 ? 128 : 64;
 #pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
-                if (ch * kStageTokens >= H) break;
-                uint32_t v[16];
-                tmem_ld_32x32b_x16(d0 + static_cast<uint32_t>(ch * kStageTokens), v);
-                tmem_wait_ld();
-                if ((ch + 1) * kStageTokens >= H) {
+            for (int h0 = 0; h0 < 128; h0 += kHold) {
+                if (h0 >= H) break;
+                uint32_t held[64];
+#pragma unroll
+                for (int ch = 0; ch < kHold / 16; ++ch) {
+                    if (h0 + ch * 16 >= H) break;
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(d0 + static_cast<uint32_t>(h0 + ch * 16), v);
+                    tmem_wait_ld();
+                    float y[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int c = h0 + ch * 16 + i;
+                        y[i] = __uint_as_float(v[i]) * (__shfl_sync(0xFFFFFFFFu, sx[c >> 5], c & 31) * sw);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if constexpr (sizeof(T) == 4) {
+                            held[ch * 16 + i] = __float_as_uint(y[i]);
+                        } else if (i % 2 == 0) {
+                            Pack<T, 2> two;
+                            two.e[0] = from_f32<T>(y[i]), two.e[1] = from_f32<T>(y[i + 1]);
+                            held[ch * 8 + i / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                        }
+                    }
+                }
+                if (h0 + kHold >= H) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_async(mapa_shared(smem_u32(sm.d_empty), 0u));
                 }
-                float y[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    y[i] = __uint_as_float(v[i]) * (__shfl_sync(0xFFFFFFFFu, sx[ch >> 1], (ch & 1) * 16 + i) * sw);
-                const int tc = t0 + ch * kStageTokens;
-                if (wide) {
+                for (int ch = 0; ch < kHold / 16; ++ch) {
+                    if (h0 + ch * 16 >= H) break;
+                    T y[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) stage[i * 32 + lane] = from_f32<T>(y[i]);
-                    __syncwarp();
+                    for (int i = 0; i < 16; ++i) {
+                        if constexpr (sizeof(T) == 4) y[i] = __uint_as_float(held[ch * 16 + i]);
+                        else y[i] = reinterpret_cast<const Pack<T, 2> *>(&held[ch * 8 + i / 2])->e[i % 2];
+                    }
+                    const int tc = t0 + h0 + ch * 16;
+                    if (wide) {
 #pragma unroll
-                    for (int i = 0; i < kStageTokens; i += kTokensPerStore) {
-                        const int tk = i + lane / kLanesPerToken, c = (lane % kLanesPerToken) * kVec;
-                        const uint4 o = lds128(stage + tk * 32 + c);
-                        if (tc + tk < a.m) {
-                            T *dst = Y + (tc + tk) * a.ldy + row0 + c;
-                            if (c + kVec <= rows) {
-                                *reinterpret_cast<uint4 *>(dst) = o;
-                            } else {
-                                const T *e = reinterpret_cast<const T *>(&o);
+                        for (int i = 0; i < 16; ++i) stage[i * 32 + lane] = y[i];
+                        __syncwarp();
 #pragma unroll
-                                for (int u = 0; u < kVec; ++u)
-                                    if (c + u < rows) dst[u] = e[u];
+                        for (int i = 0; i < kStageTokens; i += kTokensPerStore) {
+                            const int tk = i + lane / kLanesPerToken, c = (lane % kLanesPerToken) * kVec;
+                            const uint4 o = lds128(stage + tk * 32 + c);
+                            if (tc + tk < a.m) {
+                                T *dst = Y + (tc + tk) * a.ldy + row0 + c;
+                                if (c + kVec <= rows) {
+                                    *reinterpret_cast<uint4 *>(dst) = o;
+                                } else {
+                                    const T *e = reinterpret_cast<const T *>(&o);
+#pragma unroll
+                                    for (int u = 0; u < kVec; ++u)
+                                        if (c + u < rows) dst[u] = e[u];
+                                }
                             }
                         }
-                    }
-                    __syncwarp();
-                } else if (lane < rows) {
+                        __syncwarp();
+                    } else if (lane < rows) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (tc + i < a.m) Y[(tc + i) * a.ldy + row0 + lane] = from_f32<T>(y[i]);
+                        for (int i = 0; i < 16; ++i)
+                            if (tc + i < a.m) Y[(tc + i) * a.ldy + row0 + lane] = y[i];
+                    }
                 }
             }
         }
@@ -505,7 +559,7 @@ const void *kernel_of(int ytype)
 
 size_t smem_bytes(int N, int astages, int bstages, int wring)
 {
-    return 1024 + static_cast<size_t>(bstages) * (N / 2) * 128 + static_cast<size_t>(wring) * kW8RecordBytes + kStagingBytes +
+    return 1024 + static_cast<size_t>(bstages) * kStepRecords * (N / 2) * 128 + static_cast<size_t>(wring) * kSlotBytes + kStagingBytes +
            static_cast<size_t>(2 * bstages + 2 * astages + 2 * wring + 3) * 8 + 16;
 }
 
@@ -557,10 +611,11 @@ bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan)
     for (int N = 32; N <= 256; N += 32) {
         W8a8GemmPlan c;
         c.N = N;
-        c.astages = std::min(kMaxAStages, (512 - N) / 32) & ~1;
+        c.astages = std::min<int>(kMaxAStages, (512 - N) / kAColumns) & ~1;
         c.wring = kWRing;
         c.bstages = kMaxBStages;
         while (c.bstages > 2 && smem_bytes(N, c.astages, c.bstages, c.wring) > kSmemOptIn) --c.bstages;
+        if (c.bstages <= c.astages + 1) c.bstages = std::min(c.bstages, c.astages);   // one commit a step
         c.smem = std::max<size_t>(smem_bytes(N, c.astages, c.bstages, c.wring), kSmemPerSM / 2 + 1024);   // one CTA per SM
         if (c.smem > kSmemOptIn) continue;
         c.ts = static_cast<int>(ceil_div(m, N));
