@@ -178,15 +178,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64
 {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, limit_ns)) != 0;
 }
-// The MMA thread's wait: tests without suspending, since it resumes some 170 ns
-// late from a suspended wait and the tensor cores would run dry (4096 x 14336
-// x 4096: 404 us a call with suspended waits, 364 with tests).
-__device__ __forceinline__ bool spin_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+// The MMA warp's waits: tests without suspending, since a warp resumes some
+// 170 ns late from a suspended wait and the tensor cores would run dry (4096 x
+// 14336 x 4096: 404 us a call with suspended waits, 364 with tests).
+__device__ __forceinline__ bool warp_test(uint64_t *bar, uint32_t parity)
 {
+    return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)) != 0;
+}
+__device__ __forceinline__ bool warp_spin_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+{
+    for (uint32_t i = 0; i < 64; ++i)
+        if (warp_test(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_test_wait(bar, parity)) return true;
-        if ((i & 255u) == 0 && globaltimer_ns() - t0 > limit_ns) return false;
+    while (true) {
+        for (uint32_t i = 0; i < 64; ++i)
+            if (warp_test(bar, parity)) return true;
+        if (__any_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > limit_ns)) return false;
     }
 }
 
@@ -319,47 +326,54 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        if (rank == 0 && lane == 0) {
+        // The whole warp runs the loop, one elected lane issues.
+        if (rank == 0) {
             const uint32_t idesc = idesc_f16_f32(256, static_cast<uint32_t>(N));
             const uint64_t bdesc0 = smem_desc_sw128(smem_u32(sm.b));
+            const uint32_t d = __shfl_sync(0xFFFFFFFFu, tmem, 0), a0 = d + acol0;
             Ring r, b;
             bool ok = true;
             uint32_t seq = 0;
             for (int tile = pair; ok && tile < a.tiles; tile += pairs, ++seq) {
                 // D has been read out of both CTAs' tensor memory
-                if (seq > 0 && !spin_wait(sm.d_empty, (seq - 1) & 1u, a.wait_ns)) {
-                    fail(sm, a);
+                if (seq > 0 && !warp_spin_wait(sm.d_empty, (seq - 1) & 1u, a.wait_ns)) {
+                    ok = false;
                     break;
                 }
-                bool ready = mbar_test_wait(&sm.ready[r.slot], r.phase);
+                bool ready = warp_test(&sm.ready[r.slot], r.phase);
                 for (int st = 0; st < steps; ++st) {
-                    if (!ready && !spin_wait(&sm.ready[r.slot], r.phase, a.wait_ns)) {
-                        fail(sm, a);
+                    if (!ready && !warp_spin_wait(&sm.ready[r.slot], r.phase, a.wait_ns)) {
                         ok = false;
                         break;
                     }
-                    const uint64_t bd = bdesc0 + static_cast<uint64_t>(b.slot) * (bstage >> 4);
-                    const uint32_t at = tmem + acol0 + kAColumns * static_cast<uint32_t>(r.slot);
+                    const uint64_t bd = bdesc0 + static_cast<uint64_t>(static_cast<uint32_t>(b.slot) * (bstage >> 4));
+                    const uint64_t bd2 = bd + (brec >> 4);
+                    const uint32_t at = a0 + kAColumns * static_cast<uint32_t>(r.slot);
+                    const bool whole = (st + 1) * kStepRecords <= np;
                     uint64_t *const done_a = &sm.empty_a[r.slot], *const done_b = &sm.empty_b[b.slot];
                     r.step(SA);
                     b.step(SB);
-                    // the next step's test overlaps this step's issue
-                    ready = st + 1 < steps && mbar_test_wait(&sm.ready[r.slot], r.phase);
                     tc_fence_after();
-                    tc_mma_f16_ts_pair(tmem, at, bd, idesc, st > 0 ? 1u : 0u);
+                    if (elect_one()) {
+                        tc_mma_f16_ts_pair(d, at, bd, idesc, st > 0 ? 1u : 0u);
 #pragma unroll
-                    for (uint32_t i = 1; i < 4; ++i) tc_mma_f16_ts_pair(tmem, at + 8u * i, bd + 2u * i, idesc, 1u);
-                    if ((st + 1) * kStepRecords <= np) {
-                        const uint64_t bd2 = bd + (brec >> 4);
+                        for (uint32_t i = 1; i < 4; ++i) tc_mma_f16_ts_pair(d, at + 8u * i, bd + 2u * i, idesc, 1u);
+                        if (whole) {
 #pragma unroll
-                        for (uint32_t i = 0; i < 4; ++i) tc_mma_f16_ts_pair(tmem, at + 32u + 8u * i, bd2 + 2u * i, idesc, 1u);
+                            for (uint32_t i = 0; i < 4; ++i) tc_mma_f16_ts_pair(d, at + 32u + 8u * i, bd2 + 2u * i, idesc, 1u);
+                        }
+                        tc_commit_pair(done_a, 3);
+                        if (SB != SA) tc_commit_pair(done_b, 3);
                     }
-                    tc_commit_pair(done_a, 3);
-                    if (SB != SA) tc_commit_pair(done_b, 3);
+                    __syncwarp();
+                    ready = st + 1 < steps && warp_test(&sm.ready[r.slot], r.phase);
                 }
-                if (ok) tc_commit_pair(sm.d_full, 3);
+                if (ok && elect_one()) tc_commit_pair(sm.d_full, 3);
+                __syncwarp();
             }
-            tc_commit_pair(sm.done, 3);   // also after a timeout
+            if (!ok && lane == 0) fail(sm, a);
+            __syncwarp();
+            if (elect_one()) tc_commit_pair(sm.done, 3);   // also after a timeout
         }
         __syncwarp();
     } else if (dequant) {
