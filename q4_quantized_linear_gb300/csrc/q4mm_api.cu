@@ -274,11 +274,7 @@ int matmul_impl(const void *W, const float *X, int64_t ldx, const int32_t *rows,
 
 int device_info(DeviceInfo *out) { return current_device(out); }
 int cuda_status(cudaError_t e) { return map_cuda(e); }
-void wait_settings(uint64_t *wait_ns, int *prefetch_w)
-{
-    *wait_ns = g_wait_ns.load();
-    *prefetch_w = g_prefetch_w.load();
-}
+uint64_t wait_limit() { return g_wait_ns.load(); }
 
 // One launch of the mat-vec over an expert set (each expert at most 16
 // rows). Q4_ERR_INVALID_ARG when no plan fits (the caller then runs the

@@ -204,6 +204,22 @@ __device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t *bar, uint32_t p
     return ok != 0;
 }
 
+// Tests of two barriers in flight together.
+__device__ __forceinline__ bool mbar_test_wait2(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "and.pred p, p, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar0)), "r"(parity0), "r"(smem_u32(bar1)), "r"(parity1)
+        : "memory");
+    return ok != 0;
+}
+
 // Below this limit a wait polls without suspending (try_wait may sleep for
 // longer than the limit inside one call), so that the limit is honoured.
 constexpr uint64_t kShortWaitNs = 100000;

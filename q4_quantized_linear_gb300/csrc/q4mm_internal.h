@@ -36,9 +36,8 @@ struct DeviceInfo {
 // error as a status code.
 int device_info(DeviceInfo *out);
 int cuda_status(cudaError_t e);
-// The limit of device-side waits and whether weights are declared read-only,
-// as set for the calls to come.
-void wait_settings(uint64_t *wait_ns, int *prefetch_w);
+// The limit of device-side waits, as set for the calls to come.
+uint64_t wait_limit();
 
 // Raise a kernel's dynamic shared-memory limit to the opt-in maximum, once per
 // (device, kernel).

@@ -97,7 +97,7 @@ int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int
         g.ldy = ldy;
         g.ytype = ytype;
         g.status = dev.status;
-        wait_settings(&g.wait_ns, &g.prefetch_w);
+        g.wait_ns = wait_limit();
         g.m = static_cast<int>(m);
         g.n = static_cast<int>(n);
         return cuda_status(launch_w8a8_gemm(plan, g, tok, k, ws + image_at(m, k), dev.sm_count, s));

@@ -45,7 +45,6 @@ struct W8a8GemmArgs {
     int m, n, np, groups;
     int N, ts, tiles;
     int astages, bstages, wring;
-    int prefetch_w;
 };
 
 bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan);

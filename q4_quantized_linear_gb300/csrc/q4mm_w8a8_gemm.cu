@@ -22,10 +22,11 @@
 //   0      B producer: bulk copies of its half of the token tile
 //   1      tensor memory; in the even CTA one thread issues the MMAs
 //   2      weight-record producer
-//   4-11   dequantise, two sets of four warps on alternating K steps. A warp
-//          that has stored its rows also waits for the step's B tile, then
-//          arrives on the even CTA's `ready` barrier: one barrier covers both
-//          operands of both CTAs.
+//   3      tells the even CTA when a step's operands are in place here: waits
+//          for the weights in tensor memory and for the B tile, then arrives on
+//          the even CTA's `ready` barrier, one arrival a CTA and step (by the
+//          dequantising warps themselves it took a third of their time)
+//   4-11   dequantise, two sets of four warps on alternating K steps
 //   12-19  epilogue: two warps per 32 rows, half of the token columns each.
 // The MMA's commits release a stage (A and B) in both CTAs. A pair runs
 // through tiles in turn: the rings carry on into the next tile while the
@@ -162,7 +163,7 @@ template <typename T, int V> __global__ void __launch_bounds__(512) code_tile_ke
 
 struct Smem {
     uint8_t *b, *w, *stage;
-    uint64_t *full_b, *empty_b, *full_w, *empty_w, *ready, *empty_a, *d_full, *d_empty, *done;
+    uint64_t *full_b, *empty_b, *full_w, *empty_w, *stored, *ready, *empty_a, *d_full, *d_empty, *done;
     uint32_t *tmem_slot;
     int *abort;
 };
@@ -232,7 +233,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
     sm.empty_b = SB == SA ? sm.empty_a : sm.empty_a + SA;
     sm.full_w = sm.empty_a + SA + (SB == SA ? 0 : SB);
     sm.empty_w = sm.full_w + RW;
-    sm.d_full = sm.empty_w + RW;
+    sm.stored = sm.empty_w + RW;
+    sm.d_full = sm.stored + SA;
     sm.d_empty = sm.d_full + 1;
     sm.done = sm.d_empty + 1;
     sm.tmem_slot = reinterpret_cast<uint32_t *>(sm.done + 1);
@@ -241,8 +243,11 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         for (int i = 0; i < SB; ++i) mbar_init(&sm.full_b[i], 1);
         if (SB != SA)
             for (int i = 0; i < SB; ++i) mbar_init(&sm.empty_b[i], 1);
-        // a step's operands are ready once a set's four warps in each CTA say so
-        for (int i = 0; i < SA; ++i) mbar_init(&sm.ready[i], kDequantWarps), mbar_init(&sm.empty_a[i], 1);
+        for (int i = 0; i < SA; ++i) {
+            mbar_init(&sm.stored[i], kDequantWarps / 2);   // a set's warps
+            mbar_init(&sm.ready[i], 2);                    // both CTAs
+            mbar_init(&sm.empty_a[i], 1);
+        }
         for (int i = 0; i < RW; ++i) mbar_init(&sm.full_w[i], 1), mbar_init(&sm.empty_w[i], kDequantWarps / 2);
         mbar_init(sm.d_full, 1);
         mbar_init(sm.d_empty, 2 * kEpilogueWarps);
@@ -294,7 +299,9 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------ record producer
-        if (!a.prefetch_w) pdl_wait();
+        // No dependency wait: this grid starts once every CTA of the kernel in
+        // front of it, the tokens' tiling, is past its own, and that kernel
+        // writes no weights.
         if (lane == 0) {
             Ring w;
             int64_t issued = 0;
@@ -376,20 +383,40 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
             if (elect_one()) tc_commit_pair(sm.done, 3);   // also after a timeout
         }
         __syncwarp();
+    } else if (warp == 3) {
+        // ------------------------------------------- operands in place here
+        if (lane == 0) {
+            Ring r, b;
+            bool ok = true;
+            const uint32_t ready0 = mapa_shared(smem_u32(sm.ready), 0u);
+            for (int tile = pair; ok && tile < a.tiles; tile += pairs) {
+                for (int st = 0; st < steps; ++st, r.step(SA), b.step(SB)) {
+                    if (!mbar_test_wait2(&sm.full_b[b.slot], b.phase, &sm.stored[r.slot], r.phase) &&
+                        (!mbar_wait(&sm.full_b[b.slot], b.phase, a.wait_ns) || !mbar_wait(&sm.stored[r.slot], r.phase, a.wait_ns))) {
+                        fail(sm, a);
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_remote_async(ready0 + 8u * static_cast<uint32_t>(r.slot));
+                }
+            }
+        }
+        __syncwarp();
     } else if (dequant) {
         // --------------------------------------------------- dequantise W
         const int q = warp & 3, set = (warp - kDequantWarp0) >> 2;
         const int row = q * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-        Ring w, r, b;
+        Ring w, r;
         uint32_t step = 0;
         bool ok = true;
         for (int tile = pair; ok && tile < a.tiles; tile += pairs) {
-            for (int st = 0; st < steps; ++st, ++step, w.step(RW), r.step(SA), b.step(SB)) {
+            for (int st = 0; st < steps; ++st, ++step, w.step(RW), r.step(SA)) {
                 if (static_cast<int>(step & 1u) != set) continue;   // W's and A's rings are even: a slot has one set
-                if (__any_sync(0xFFFFFFFFu, aborted(sm))) { ok = false; break; }
-                if (!warp_wait(&sm.full_w[w.slot], w.phase, a.wait_ns) ||
-                    (step >= static_cast<uint32_t>(SA) && !warp_wait(&sm.empty_a[r.slot], r.phase ^ 1u, a.wait_ns))) {
+                // (a barrier's first phase counts as complete where it has none before)
+                if (!__all_sync(0xFFFFFFFFu, mbar_test_wait2(&sm.full_w[w.slot], w.phase, &sm.empty_a[r.slot], r.phase ^ 1u)) &&
+                    (!warp_wait(&sm.full_w[w.slot], w.phase, a.wait_ns) ||
+                     !warp_wait(&sm.empty_a[r.slot], r.phase ^ 1u, a.wait_ns))) {
                     fail(sm, a);
                     ok = false;
                     break;
@@ -434,16 +461,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                bool landed = true;
-                if (lane == 0) {
-                    landed = mbar_wait(&sm.full_b[b.slot], b.phase, a.wait_ns);
-                    if (landed) mbar_arrive_remote_async(mapa_shared(smem_u32(&sm.ready[r.slot]), 0u));
-                }
-                if (!__shfl_sync(0xFFFFFFFFu, landed ? 1 : 0, 0)) {
-                    fail(sm, a);
-                    ok = false;
-                    break;
-                }
+                if (lane == 0) mbar_arrive(&sm.stored[r.slot]);
             }
         }
     } else if (warp >= kEpilogueWarp0) {
@@ -574,7 +592,7 @@ const void *kernel_of(int ytype)
 size_t smem_bytes(int N, int astages, int bstages, int wring)
 {
     return 1024 + static_cast<size_t>(bstages) * kStepRecords * (N / 2) * 128 + static_cast<size_t>(wring) * kSlotBytes + kStagingBytes +
-           static_cast<size_t>(2 * bstages + 2 * astages + 2 * wring + 3) * 8 + 16;
+           static_cast<size_t>(2 * bstages + 3 * astages + 2 * wring + 3) * 8 + 16;
 }
 
 // CTA pairs that the current device holds at once; 0 when it cannot be asked.
