@@ -26,7 +26,7 @@
 //          for the weights in tensor memory and for the B tile, then arrives on
 //          the even CTA's `ready` barrier, one arrival a CTA and step (by the
 //          dequantising warps themselves it took a third of their time)
-//   4-11   dequantise, two sets of four warps on alternating K steps
+//   4-11   dequantise: four warps take a step's first record, four its second
 //   12-19  epilogue: two warps per 32 rows, half of the token columns each.
 // The MMA's commits release a stage (A and B) in both CTAs. A pair runs
 // through tiles in turn: the rings carry on into the next tile while the
@@ -244,11 +244,11 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         if (SB != SA)
             for (int i = 0; i < SB; ++i) mbar_init(&sm.empty_b[i], 1);
         for (int i = 0; i < SA; ++i) {
-            mbar_init(&sm.stored[i], kDequantWarps / 2);   // a set's warps
+            mbar_init(&sm.stored[i], kDequantWarps);
             mbar_init(&sm.ready[i], 2);                    // both CTAs
             mbar_init(&sm.empty_a[i], 1);
         }
-        for (int i = 0; i < RW; ++i) mbar_init(&sm.full_w[i], 1), mbar_init(&sm.empty_w[i], kDequantWarps / 2);
+        for (int i = 0; i < RW; ++i) mbar_init(&sm.full_w[i], 1), mbar_init(&sm.empty_w[i], kDequantWarps);
         mbar_init(sm.d_full, 1);
         mbar_init(sm.d_empty, 2 * kEpilogueWarps);
         mbar_init(sm.done, 1);
@@ -404,15 +404,19 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         __syncwarp();
     } else if (dequant) {
         // --------------------------------------------------- dequantise W
-        const int q = warp & 3, set = (warp - kDequantWarp0) >> 2;
+        const int q = warp & 3, rec = (warp - kDequantWarp0) >> 2;
         const int row = q * 32 + lane;
-        const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+        const uint32_t at0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + acol0 + 32u * static_cast<uint32_t>(rec);
+        const uint8_t *const src0 = sm.w + rec * kW8RecordBytes + row * kPairK;
+        // A row is four 16-byte chunks, rows 64 bytes apart: lanes reading the same
+        // chunk would share two bank groups, four lanes each. So lane l starts at
+        // chunk (l / 2) % 4, and the chunks are put back in order by selects
+        // (registers take no index).
+        const int rot = (lane >> 1) & 3;
         Ring w, r;
-        uint32_t step = 0;
         bool ok = true;
         for (int tile = pair; ok && tile < a.tiles; tile += pairs) {
-            for (int st = 0; st < steps; ++st, ++step, w.step(RW), r.step(SA)) {
-                if (static_cast<int>(step & 1u) != set) continue;   // W's and A's rings are even: a slot has one set
+            for (int st = 0; st < steps; ++st, w.step(RW), r.step(SA)) {
                 // (a barrier's first phase counts as complete where it has none before)
                 if (!__all_sync(0xFFFFFFFFu, mbar_test_wait2(&sm.full_w[w.slot], w.phase, &sm.empty_a[r.slot], r.phase ^ 1u)) &&
                     (!warp_wait(&sm.full_w[w.slot], w.phase, a.wait_ns) ||
@@ -422,17 +426,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                     break;
                 }
                 tc_fence_after();
-                const uint32_t at = tmem + lane_base + acol0 + static_cast<uint32_t>(r.slot) * kAColumns;
-                const int records = min(kStepRecords, np - st * kStepRecords);
-#pragma unroll
-                for (int rec = 0; rec < kStepRecords; ++rec) {
-                    if (rec >= records) break;
-                    // A row is four 16-byte chunks, rows 64 bytes apart: lanes reading
-                    // the same chunk would share two bank groups, four lanes each. So
-                    // lane l starts at chunk (l / 2) % 4, and the chunks are put back in
-                    // order by selects (registers take no index).
-                    const uint8_t *src = sm.w + static_cast<size_t>(w.slot) * kSlotBytes + rec * kW8RecordBytes + row * kPairK;
-                    const int rot = (lane >> 1) & 3;
+                if (st * kStepRecords + rec < np) {
+                    const uint8_t *src = src0 + static_cast<uint32_t>(w.slot) * kSlotBytes;
                     uint32_t u[16], out[32];
                     {
                         uint32_t v[16];
@@ -454,7 +449,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                         out[2 * i] = hsub2_bits(__byte_perm(u[i], 0x64646464u, 0x4140), 0x64806480u);
                         out[2 * i + 1] = hsub2_bits(__byte_perm(u[i], 0x64646464u, 0x4342), 0x64806480u);
                     }
-                    tmem_st_32x32b_x32(at + 32u * rec, out);
+                    tmem_st_32x32b_x32(at0 + static_cast<uint32_t>(r.slot) * kAColumns, out);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.empty_w[w.slot]);   // read into registers
@@ -643,7 +638,7 @@ bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan)
     for (int N = 32; N <= 256; N += 32) {
         W8a8GemmPlan c;
         c.N = N;
-        c.astages = std::min<int>(kMaxAStages, (512 - N) / kAColumns) & ~1;
+        c.astages = std::min<int>(kMaxAStages, (512 - N) / kAColumns);
         c.wring = kWRing;
         c.bstages = kMaxBStages;
         while (c.bstages > 2 && smem_bytes(N, c.astages, c.bstages, c.wring) > kSmemOptIn) --c.bstages;
