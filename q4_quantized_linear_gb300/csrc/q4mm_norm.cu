@@ -188,6 +188,7 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(1024) nor
 {
     __shared__ float rbuf[2 * 96];
     pdl_wait();
+    pdl_launch_dependents();
     const RowGroup g = row_group(a.G);
     RowReducer red{rbuf, a.G / 32};
     const int d = static_cast<int>(a.d);

@@ -1,5 +1,25 @@
 // q4mm_w8a8.cu -- the product in 8-bit integers with a scale for each token
-// and each channel: Y[t][j] = sx[t] * s_j * sum_c xq[t][c] * code[j][c].
+// and each channel: Y[t][j] = sx[t] * s_j * sum_c xq[t][c] * code[j][c]. Its
+// entry points and the kernel for few tokens; many tokens take the tensor
+// cores' GEMM (q4mm_w8a8_gemm.cu).
+//
+// Few tokens are bound by the weight read, n * k bytes. sm_103a's integer MMA
+// and its four-way integer dot product both run at about 256 products a clock
+// and SM (measured: 0.5 products a picosecond), enough for ten tokens at the
+// rate HBM delivers weights; the fp16 warp MMA does 1024. So codes are turned
+// into fp16 (exact), multiplied by mma.sync m16n8k16 and summed in fp32, which
+// holds the sums exactly for 1024 columns: every 16 records at the latest a
+// warp adds its accumulators to 32-bit integers in shared memory. The integers
+// are the exact sums whatever the split, so nothing depends on it.
+//
+// A warp takes 16 weight rows and a slice of K. A lane's 16-byte load holds 16
+// codes of one row: eight rows of a record are 512 contiguous bytes. K is
+// permuted to suit: lane (g, t) holds columns 16 t .. 16 t + 15 of rows g and
+// g + 8 as the A operands of four MMAs, and the same columns of token g as
+// their B operands, read from the token's codes as they are.
+//   The slices of a unit of 16 rows are warps of one CTA and meet in shared
+// memory. A whole batch of records is loaded before the dependency wait, so
+// the weight stream starts while the tokens are still being coded.
 #include <algorithm>
 #include <cuda_runtime.h>
 
@@ -9,53 +29,149 @@
 namespace q4 {
 namespace {
 
-constexpr int64_t kMaxK = 131072;   // 127 * 127 * k stays below 2^31
-constexpr int kTok = 16;            // tokens of a CTA
-constexpr int kThreads = 256;
+constexpr int64_t kMaxK = 131072;      // 127 * 127 * k stays below 2^31
+constexpr int kUnitRows = 16;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kExactRecords = 16;      // 1024 * 127^2 < 2^24
 
-template <typename T> __global__ void __launch_bounds__(kThreads) product_kernel(const W8a8Args a)
+// Four codes (128 + c a byte) as two fp16x2: as the low mantissa byte of 1024
+// a byte is the fp16 1152 + c.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
-    __shared__ uint32_t w[kW8GroupRows][17];
-    __shared__ uint32_t x[kTok][16];
-    pdl_wait();
-    const int tid = threadIdx.x, r = tid & 127, half = tid >> 7;
-    const int G = blockIdx.x, t0 = blockIdx.y * kTok;
-    int acc[kTok / 2] = {};
-    for (int p = 0; p < a.np; ++p) {
-        const uint32_t *rec = reinterpret_cast<const uint32_t *>(a.W + (static_cast<int64_t>(G) * a.np + p) * kW8RecordBytes);
-        for (int i = tid; i < kW8RecordBytes / 4; i += kThreads) w[i >> 4][i & 15] = rec[i] ^ 0x80808080u;
-        {
-            const int t = tid >> 4, c = tid & 15, col = p * kPairK + 4 * c;
-            x[t][c] = t0 + t < a.m && col < a.k
-                          ? *reinterpret_cast<const uint32_t *>(a.Xq + static_cast<int64_t>(t0 + t) * a.k + col)
-                          : 0u;
+    lo = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u);
+    hi = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u);
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 load_stream(const uint8_t *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// NT: groups of eight tokens; U: records loaded at once.
+template <typename T, int NT, int U> __global__ void __launch_bounds__(kThreads, 2) few_tokens_kernel(const W8a8Args a)
+{
+    __shared__ int32_t sums[kWarps][kUnitRows][8 * NT + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int S = a.slices, slice = warp % S;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kWarps / S) + warp / S;
+    const int per = (a.np + S - 1) / S, p0 = slice * per, p1 = min(a.np, p0 + per);
+    const int64_t row0 = unit * kUnitRows;
+    // units past the last row read the last group's rows and write nothing
+    const int64_t urow = min(row0, static_cast<int64_t>(a.groups) * kW8GroupRows - kUnitRows);
+    const uint8_t *src = a.W + (urow / kW8GroupRows * a.np) * kW8RecordBytes + (urow % kW8GroupRows + g) * kPairK + 16 * t;
+    uint4 w0[U], w1[U];
+    auto load = [&](int p) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            w0[u] = w1[u] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+            if (p + u < p1) {
+                const uint8_t *r = src + static_cast<int64_t>(p + u) * kW8RecordBytes;
+                w0[u] = load_stream(r);
+                w1[u] = load_stream(r + 8 * kPairK);
+            }
         }
-        __syncthreads();
+    };
+    load(p0);
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
+    for (int i = 0; i < kUnitRows * (8 * NT + 1); i += 32)
+        if (i + lane < kUnitRows * (8 * NT + 1)) (&sums[warp][0][0])[i + lane] = 0;
+    __syncwarp();
+    pdl_wait();
+    float acc[NT][4];
 #pragma unroll
-            for (int t = 0; t < kTok / 2; ++t)
-                acc[t] = __dp4a(static_cast<int>(w[r][c]), static_cast<int>(x[half * (kTok / 2) + t][c]), acc[t]);
-        __syncthreads();
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+    const auto flush = [&]() {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sums[warp][g + 8 * (i >> 1)][8 * j + 2 * t + (i & 1)] += __float2int_rn(acc[j][i]);
+                acc[j][i] = 0.0f;
+            }
+    };
+    int held = 0;
+    for (int p = p0; p < p1; p += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (p + u >= p1) break;
+            // the tokens' codes of these columns, biased like the weights'
+            uint4 x[NT];
+            const int col = (p + u) * kPairK + 16 * t;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                x[j] = make_uint4(0u, 0u, 0u, 0u);
+                const int tok = 8 * j + g;
+                if (tok < a.m && col < a.k) x[j] = __ldg(reinterpret_cast<const uint4 *>(a.Xq + static_cast<int64_t>(tok) * a.k + col));
+            }
+            const uint32_t r0[4] = {w0[u].x, w0[u].y, w0[u].z, w0[u].w}, r1[4] = {w1[u].x, w1[u].y, w1[u].z, w1[u].w};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                uint32_t a0, a1, a2, a3;
+                codes_f16(r0[s], a0, a2);
+                codes_f16(r1[s], a1, a3);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint32_t xs = s == 0 ? x[j].x : s == 1 ? x[j].y : s == 2 ? x[j].z : x[j].w;
+                    uint32_t b0, b1;
+                    codes_f16(xs ^ 0x80808080u, b0, b1);
+                    mma_f16(acc[j], a0, a1, a2, a3, b0, b1);
+                }
+            }
+        }
+        held += U;
+        if (held + U > kExactRecords) {
+            flush();
+            held = 0;
+        }
+        if (p + U < p1) load(p + U);
     }
-    const int row = G * kW8GroupRows + r;
-    if (row >= a.n) return;
-    const float sw = a.row_scale[row];
-    for (int t = 0; t < kTok / 2; ++t) {
-        const int tok = t0 + half * (kTok / 2) + t;
-        if (tok < a.m)
-            static_cast<T *>(a.Y)[tok * a.ldy + row] = from_f32<T>(static_cast<float>(acc[t]) * (a.sx[tok] * sw));
+    flush();
+    __syncthreads();
+    // rows next to each other in a thread's neighbours: Y's rows are tokens
+    const int units = kWarps / S, rows = units * kUnitRows;
+    for (int i = threadIdx.x; i < rows * a.m; i += kThreads) {
+        const int r = i % rows, tok = i / rows;
+        const int64_t row = static_cast<int64_t>(blockIdx.x) * rows + r;
+        if (row >= a.n) continue;
+        int32_t s = 0;
+        for (int k = 0; k < S; ++k) s += sums[(r / kUnitRows) * S + k][r % kUnitRows][tok];
+        static_cast<T *>(a.Y)[tok * a.ldy + row] = from_f32<T>(static_cast<float>(s) * (a.sx[tok] * a.row_scale[row]));
     }
 }
 
-cudaError_t launch_product(W8a8Args a, cudaStream_t s)
+template <typename T> const void *few_tokens_of(int m)
 {
-    const void *fn = a.ytype == Q4_TYPE_F32   ? reinterpret_cast<const void *>(&product_kernel<float>)
-                     : a.ytype == Q4_TYPE_F16 ? reinterpret_cast<const void *>(&product_kernel<__half>)
-                                              : reinterpret_cast<const void *>(&product_kernel<__nv_bfloat16>);
+    return m <= 8    ? reinterpret_cast<const void *>(&few_tokens_kernel<T, 1, 8>)
+           : m <= 16 ? reinterpret_cast<const void *>(&few_tokens_kernel<T, 2, 4>)
+                     : reinterpret_cast<const void *>(&few_tokens_kernel<T, 4, 4>);
+}
+
+// Slices of K: the fewest warps that keep the memory busy (24 an SM), but at
+// least two records a warp.
+cudaError_t launch_few_tokens(W8a8Args a, int sm_count, cudaStream_t s)
+{
+    const int64_t units = ceil_div(a.n, kUnitRows);
+    a.slices = 1;
+    while (a.slices < kWarps && units * a.slices < 24 * static_cast<int64_t>(sm_count) && a.np >= 4 * a.slices) a.slices *= 2;
+    const void *fn = a.ytype == Q4_TYPE_F32   ? few_tokens_of<float>(a.m)
+                     : a.ytype == Q4_TYPE_F16 ? few_tokens_of<__half>(a.m)
+                                              : few_tokens_of<__nv_bfloat16>(a.m);
     void *args[] = {&a};
-    return launch_pdl(fn, dim3(static_cast<unsigned>(a.groups), static_cast<unsigned>(ceil_div(a.m, kTok))), dim3(kThreads),
-                      0, s, args);
+    return launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(units, kWarps / a.slices))), dim3(kThreads), 0, s, args);
 }
 
 bool valid_sizes(int64_t m, int64_t k, int64_t n)
@@ -67,7 +183,7 @@ bool valid_sizes(int64_t m, int64_t k, int64_t n)
 size_t codes_bytes(int64_t m, int64_t k) { return static_cast<size_t>(round_up(m * k, 256)); }
 size_t image_at(int64_t m, int64_t k) { return codes_bytes(m, k) + static_cast<size_t>(round_up(4 * m, 256)); }
 
-constexpr int64_t kFewTokens = 16;
+constexpr int64_t kFewTokens = 32;
 
 // `tok`: codes with their scales, or rows to be coded.
 int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int64_t m, int64_t k, int64_t n,
@@ -120,7 +236,7 @@ int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int
     a.np = np;
     a.groups = groups;
     a.row_scale = row_scale;
-    return cuda_status(launch_product(a, s));
+    return cuda_status(launch_few_tokens(a, dev.sm_count, s));
 }
 
 } // namespace

@@ -19,6 +19,7 @@ struct W8a8Args {
     int64_t ldy;
     int ytype;
     int m, n, k, np, groups;
+    int slices;               // of K: warps of a CTA that share 16 rows
 };
 
 // The tensor-core product (many tokens).
