@@ -59,10 +59,51 @@ __device__ __forceinline__ uint4 load_stream(const uint8_t *p)
     return v;
 }
 
-// NT: groups of eight tokens; U: records loaded at once.
-template <typename T, int NT, int U> __global__ void __launch_bounds__(kThreads, 2) few_tokens_kernel(const W8a8Args a)
+// Tokens that each CTA codes for itself: codes in shared memory, rows `stride`
+// bytes apart, and their scales.
+struct OwnCodes {
+    int8_t *codes;
+    float *scale;
+    int stride;
+};
+
+// Codes rows 0 .. m - 1 of X (q4_a8_quantize's rule), a row at a time by the
+// whole CTA; columns k .. np * 64 - 1 are zeros.
+template <typename X, int V> __device__ __forceinline__ void code_rows(const W8a8Args &a, const OwnCodes &o, float *rbuf)
 {
+    RowReducer red{rbuf, kWarps};
+    const int kp = a.np * kPairK;
+    for (int t = 0; t < a.m; ++t) {
+        const X *xr = static_cast<const X *>(a.X) + t * a.ldx;
+        uint32_t mb = 0u;
+        for (int c = static_cast<int>(threadIdx.x) * V; c < a.k; c += kThreads * V) {
+            const Pack<X, V> v = load_pack<X, V>(xr, c, a.k);
+#pragma unroll
+            for (int i = 0; i < V; ++i) mb = max(mb, abs_bits(to_f32(v.e[i])));
+        }
+        const CodeScale cs = code_scale(red.max_bits(mb));
+        if (threadIdx.x == 0) o.scale[t] = cs.scale;
+        for (int c = static_cast<int>(threadIdx.x) * V; c < kp; c += kThreads * V) {
+            const Pack<X, V> v = load_pack<X, V>(xr, c, a.k);   // zeros past k; from the first-level cache
+            Pack<int8_t, V> q;
+#pragma unroll
+            for (int i = 0; i < V; ++i) q.e[i] = code_of(to_f32(v.e[i]), cs.factor);
+            *reinterpret_cast<Pack<int8_t, V> *>(o.codes + t * o.stride + c) = q;
+        }
+    }
+}
+
+// NT: groups of eight tokens; U: records in flight a warp; X: int8_t for coded
+// tokens, else the type of rows that each CTA codes for itself (few enough that
+// this costs less than a launch of its own).
+template <typename T, typename X, int NT, int U, int OCC>
+__global__ void __launch_bounds__(kThreads, OCC) few_tokens_kernel(const W8a8Args a)
+{
+    constexpr bool OWN = sizeof(X) != 1;
+    extern __shared__ __align__(16) uint8_t own_smem[];
     __shared__ int32_t sums[kWarps][kUnitRows][8 * NT + 1];
+    __shared__ float own_scale[8];
+    __shared__ float rbuf[2 * 96];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int S = a.slices, slice = warp % S;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kWarps / S) + warp / S;
@@ -72,23 +113,32 @@ template <typename T, int NT, int U> __global__ void __launch_bounds__(kThreads,
     const int64_t urow = min(row0, static_cast<int64_t>(a.groups) * kW8GroupRows - kUnitRows);
     const uint8_t *src = a.W + (urow / kW8GroupRows * a.np) * kW8RecordBytes + (urow % kW8GroupRows + g) * kPairK + 16 * t;
     uint4 w0[U], w1[U];
-    auto load = [&](int p) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            w0[u] = w1[u] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-            if (p + u < p1) {
-                const uint8_t *r = src + static_cast<int64_t>(p + u) * kW8RecordBytes;
-                w0[u] = load_stream(r);
-                w1[u] = load_stream(r + 8 * kPairK);
-            }
+    auto load = [&](int u, int p) {
+        if (p < p1) {
+            const uint8_t *r = src + static_cast<int64_t>(p) * kW8RecordBytes;
+            w0[u] = load_stream(r);
+            w1[u] = load_stream(r + 8 * kPairK);
         }
     };
-    load(p0);
 #pragma unroll
-    for (int i = 0; i < kUnitRows * (8 * NT + 1); i += 32)
-        if (i + lane < kUnitRows * (8 * NT + 1)) (&sums[warp][0][0])[i + lane] = 0;
-    __syncwarp();
+    for (int u = 0; u < U; ++u) load(u, p0 + u);
+    for (int i = lane; i < kUnitRows * (8 * NT + 1); i += 32) (&sums[warp][0][0])[i] = 0;
     pdl_wait();
+    pdl_launch_dependents();
+    const OwnCodes own{reinterpret_cast<int8_t *>(own_smem), own_scale, a.np * kPairK + (a.np % 2 ? 0 : 64)};
+    if constexpr (OWN) {
+        if (a.vec * sizeof(X) == 16) code_rows<X, 16 / sizeof(X)>(a, own, rbuf);
+        else code_rows<X, 1>(a, own, rbuf);
+        __syncthreads();
+    }
+    const float *const sx = OWN ? own_scale : a.sx;
+    // this lane's columns of its tokens, one pointer per group of eight
+    const int8_t *xq[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int tok = 8 * j + g;
+        xq[j] = tok >= a.m ? nullptr : OWN ? own.codes + tok * own.stride + 16 * t : a.Xq + static_cast<int64_t>(tok) * a.k + 16 * t;
+    }
     float acc[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -108,16 +158,19 @@ template <typename T, int NT, int U> __global__ void __launch_bounds__(kThreads,
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (p + u >= p1) break;
-            // the tokens' codes of these columns, biased like the weights'
             uint4 x[NT];
-            const int col = (p + u) * kPairK + 16 * t;
+            const int col = (p + u) * kPairK;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 x[j] = make_uint4(0u, 0u, 0u, 0u);
-                const int tok = 8 * j + g;
-                if (tok < a.m && col < a.k) x[j] = __ldg(reinterpret_cast<const uint4 *>(a.Xq + static_cast<int64_t>(tok) * a.k + col));
+                if constexpr (OWN) {
+                    if (xq[j]) x[j] = lds128(xq[j] + col);
+                } else if (xq[j] && col + 16 * t < a.k) {
+                    x[j] = __ldg(reinterpret_cast<const uint4 *>(xq[j] + col));
+                }
             }
             const uint32_t r0[4] = {w0[u].x, w0[u].y, w0[u].z, w0[u].w}, r1[4] = {w1[u].x, w1[u].y, w1[u].z, w1[u].w};
+            load(u, p + u + U);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 uint32_t a0, a1, a2, a3;
@@ -127,7 +180,7 @@ template <typename T, int NT, int U> __global__ void __launch_bounds__(kThreads,
                 for (int j = 0; j < NT; ++j) {
                     const uint32_t xs = s == 0 ? x[j].x : s == 1 ? x[j].y : s == 2 ? x[j].z : x[j].w;
                     uint32_t b0, b1;
-                    codes_f16(xs ^ 0x80808080u, b0, b1);
+                    codes_f16(xs ^ 0x80808080u, b0, b1);   // biased like the weights' codes
                     mma_f16(acc[j], a0, a1, a2, a3, b0, b1);
                 }
             }
@@ -137,7 +190,6 @@ template <typename T, int NT, int U> __global__ void __launch_bounds__(kThreads,
             flush();
             held = 0;
         }
-        if (p + U < p1) load(p + U);
     }
     flush();
     __syncthreads();
@@ -149,15 +201,24 @@ template <typename T, int NT, int U> __global__ void __launch_bounds__(kThreads,
         if (row >= a.n) continue;
         int32_t s = 0;
         for (int k = 0; k < S; ++k) s += sums[(r / kUnitRows) * S + k][r % kUnitRows][tok];
-        static_cast<T *>(a.Y)[tok * a.ldy + row] = from_f32<T>(static_cast<float>(s) * (a.sx[tok] * a.row_scale[row]));
+        static_cast<T *>(a.Y)[tok * a.ldy + row] = from_f32<T>(static_cast<float>(s) * (sx[tok] * a.row_scale[row]));
     }
 }
 
-template <typename T> const void *few_tokens_of(int m)
+// Two records in flight a warp and as many warps as that leaves registers for
+// measured best (16 x 14336 x 4096: 17.0 us with 2 records and 3 CTAs an SM, 18.2
+// with 2 and 4, 18.8 with 4 and 3; 1 x 9728 x 2560: 6.7 with 2 and 4, 7.3 with 4
+// and 4, 8.8 with 5 and 3).
+template <typename T> const void *few_tokens_of(const W8a8Args &a)
 {
-    return m <= 8    ? reinterpret_cast<const void *>(&few_tokens_kernel<T, 1, 8>)
-           : m <= 16 ? reinterpret_cast<const void *>(&few_tokens_kernel<T, 2, 4>)
-                     : reinterpret_cast<const void *>(&few_tokens_kernel<T, 4, 4>);
+    if (a.X) {
+        return a.xtype == Q4_TYPE_F32   ? reinterpret_cast<const void *>(&few_tokens_kernel<T, float, 1, 2, 4>)
+               : a.xtype == Q4_TYPE_F16 ? reinterpret_cast<const void *>(&few_tokens_kernel<T, __half, 1, 2, 4>)
+                                        : reinterpret_cast<const void *>(&few_tokens_kernel<T, __nv_bfloat16, 1, 2, 4>);
+    }
+    return a.m <= 8    ? reinterpret_cast<const void *>(&few_tokens_kernel<T, int8_t, 1, 2, 4>)
+           : a.m <= 16 ? reinterpret_cast<const void *>(&few_tokens_kernel<T, int8_t, 2, 2, 3>)
+                       : reinterpret_cast<const void *>(&few_tokens_kernel<T, int8_t, 4, 2, 2>);
 }
 
 // Slices of K: the fewest warps that keep the memory busy (24 an SM), but at
@@ -167,12 +228,18 @@ cudaError_t launch_few_tokens(W8a8Args a, int sm_count, cudaStream_t s)
     const int64_t units = ceil_div(a.n, kUnitRows);
     a.slices = 1;
     while (a.slices < kWarps && units * a.slices < 24 * static_cast<int64_t>(sm_count) && a.np >= 4 * a.slices) a.slices *= 2;
-    const void *fn = a.ytype == Q4_TYPE_F32   ? few_tokens_of<float>(a.m)
-                     : a.ytype == Q4_TYPE_F16 ? few_tokens_of<__half>(a.m)
-                                              : few_tokens_of<__nv_bfloat16>(a.m);
+    const void *fn = a.ytype == Q4_TYPE_F32   ? few_tokens_of<float>(a)
+                     : a.ytype == Q4_TYPE_F16 ? few_tokens_of<__half>(a)
+                                              : few_tokens_of<__nv_bfloat16>(a);
+    const size_t smem = a.X ? static_cast<size_t>(a.m) * (a.np * kPairK + 64) : 0;
     void *args[] = {&a};
-    return launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(units, kWarps / a.slices))), dim3(kThreads), 0, s, args);
+    return launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(units, kWarps / a.slices))), dim3(kThreads), smem, s, args);
 }
+
+// One token of up to so many values is coded by each CTA for itself (1 x 2560 x
+// 9728: 10.2 us, with a launch for the coding 13.4; four tokens of 2560 values
+// take 10.2 this way and 8.0 with the launch).
+constexpr int64_t kOwnValues = 16384;
 
 bool valid_sizes(int64_t m, int64_t k, int64_t n)
 {
@@ -218,7 +285,8 @@ int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int
         g.n = static_cast<int>(n);
         return cuda_status(launch_w8a8_gemm(plan, g, tok, k, ws + image_at(m, k), dev.sm_count, s));
     }
-    if (!coded) {
+    const bool own = !coded && m == 1 && k <= kOwnValues;
+    if (!coded && !own) {
         rc = quantize_rows(reinterpret_cast<int8_t *>(ws), k, tok.sx, tok.X, tok.ldx, tok.xtype, m, k, dev.sm_count, s);
         if (rc != Q4_OK) return rc;
         tok.Xq = reinterpret_cast<const int8_t *>(ws);
@@ -226,6 +294,12 @@ int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int
     W8a8Args a{};
     a.W = W;
     a.Xq = tok.Xq;
+    if (own) {
+        a.X = tok.X;
+        a.ldx = tok.ldx;
+        a.xtype = tok.xtype;
+        a.vec = tok.vec;
+    }
     a.sx = tok.sx;
     a.Y = Y;
     a.ldy = ldy;

@@ -15,6 +15,9 @@ struct W8a8Args {
     const float *row_scale;
     const int8_t *Xq;         // [m x k]
     const float *sx;
+    const void *X;            // else rows that each CTA codes, `vec` elements an access
+    int64_t ldx;
+    int xtype, vec;
     void *Y;
     int64_t ldy;
     int ytype;
