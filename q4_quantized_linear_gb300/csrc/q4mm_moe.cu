@@ -257,7 +257,7 @@ template <typename T, int V> __global__ void __launch_bounds__(256) combine_kern
             if (a.base) {
                 const Pack<T, V> bv = load_pack<T, V>(static_cast<const T *>(a.base) + t * a.ldbase, c, a.d);
 #pragma unroll
-                for (int i = 0; i < V; ++i) y[i] = to_f32(bv.e[i]);
+                for (int i = 0; i < V; ++i) y[i] = elem(bv, i);
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i) y[i] = 0.0f;
@@ -276,13 +276,10 @@ template <typename T, int V> __global__ void __launch_bounds__(256) combine_kern
                     if (!has[j]) continue;
                     const float wj = w ? w[j0 + j] : 1.0f;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) y[i] = fmaf(wj, to_f32(v[j].e[i]), y[i]);
+                    for (int i = 0; i < V; ++i) y[i] = fmaf(wj, elem(v[j], i), y[i]);
                 }
             }
-            Pack<T, V> o;
-#pragma unroll
-            for (int i = 0; i < V; ++i) o.e[i] = from_f32<T>(y[i]);
-            store_pack<T, V>(static_cast<T *>(a.Y) + t * a.ldy, c, a.d, o);
+            store_pack<T, V>(static_cast<T *>(a.Y) + t * a.ldy, c, a.d, pack_of<T, V>(y));
         }
     }
 }
@@ -307,18 +304,17 @@ template <typename T, int V> __global__ void __launch_bounds__(256) combine_bwd_
         float s = 0.0f;
 #pragma unroll 4
         for (int64_t c = lane * V; c < a.d; c += 32 * V) {
-            Pack<T, V> o;
+            Pack<T, V> o = zero_pack<T, V>();
             if (has) {
-                const Pack<T, V> g = load_pack<T, V>(dy, c, a.d), y = load_pack<T, V>(ys, c, a.d);
+                const Pack<T, V> gp = load_pack<T, V>(dy, c, a.d), yp = load_pack<T, V>(ys, c, a.d);
+                float f[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float gi = to_f32(g.e[i]);
-                    s = fmaf(gi, to_f32(y.e[i]), s);
-                    o.e[i] = from_f32<T>(w * gi);
+                    const float gi = elem(gp, i);
+                    s = fmaf(gi, elem(yp, i), s);
+                    f[i] = w * gi;
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) o.e[i] = from_f32<T>(0.0f);
+                o = pack_of<T, V>(f);
             }
             store_pack<T, V>(out, c, a.d, o);
         }

@@ -48,11 +48,9 @@ __device__ __forceinline__ RowGroup row_group(int G)
     return g;
 }
 
-// Rows of the next iteration are loaded before this one's reductions where
-// that doubles no more than 32 bytes a thread and matrix.
-template <typename T, int V, int NV> constexpr bool kAhead = NV * V * sizeof(T) <= 32;
-// The channels' weights stay in registers over the rows where they are few.
-template <int V, int NV> constexpr bool kKeep = NV * V <= 8;
+// The largest CTA of a kernel with NV vectors a thread: its registers allow
+// 1024 threads an SM.
+__host__ __device__ constexpr int max_threads(int NV) { return NV == 1 ? 1024 : 512; }
 
 template <typename T, int V, int NV>
 __device__ __forceinline__ void load_row(Pack<T, V> (&x)[NV], const T *row, int t, int G, int d)
@@ -60,13 +58,11 @@ __device__ __forceinline__ void load_row(Pack<T, V> (&x)[NV], const T *row, int 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * G + t) * V;
-        if (c < d) x[i] = load_pack<T, V>(row, c, d);
-        else
-#pragma unroll
-            for (int j = 0; j < V; ++j) x[i].e[j] = from_f32<T>(0.0f);
+        x[i] = c < d ? load_pack<T, V>(row, c, d) : zero_pack<T, V>();
     }
 }
 
+// (o + w) of V channels.
 template <int V> __device__ __forceinline__ void channel_weights(const float *w, float off, int c, int d, float out[V])
 {
     if (w) {
@@ -79,56 +75,56 @@ template <int V> __device__ __forceinline__ void channel_weights(const float *w,
     }
 }
 
-// h = x * r * w of one vector, for values or for the coding.
-template <typename T, int V>
-__device__ __forceinline__ void normed(const Pack<T, V> &x, float r, const float w[V], float h[V])
+template <typename T, int V> __device__ __forceinline__ float square_sum(const Pack<T, V> &x, float s)
 {
 #pragma unroll
-    for (int j = 0; j < V; ++j) h[j] = to_f32(x.e[j]) * r * w[j];
+    for (int j = 0; j < V; ++j) {
+        const float f = elem(x, j);
+        s = fmaf(f, f, s);
+    }
+    return s;
 }
-
-template <typename T, int V> __device__ __forceinline__ void store_values(T *row, int c, int d, const float h[V])
+// The largest |h| of the vector's elements that the row has.
+template <int V> __device__ __forceinline__ uint32_t largest(const float h[V], int c, int d, uint32_t mb)
 {
-    Pack<T, V> o;
 #pragma unroll
-    for (int j = 0; j < V; ++j) o.e[j] = from_f32<T>(h[j]);
-    store_pack<T, V>(row, c, d, o);
+    for (int j = 0; j < V; ++j) mb = max(mb, c + j < d ? abs_bits(h[j]) : 0u);
+    return mb;
 }
 template <int V> __device__ __forceinline__ void store_codes(int8_t *row, int c, int d, const float h[V], float factor)
 {
-    Pack<int8_t, V> o;
+    int q[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) o.e[j] = code_of(h[j], factor);
-    store_pack<int8_t, V>(row, c, d, o);
+    for (int j = 0; j < V; ++j) q[j] = code_of(h[j], factor);
+    store_pack<int8_t, V>(row, c, d, pack_codes<V>(q));
 }
 
-// The second half of a row that has been summed: h = x * r * (o + w), stored
-// as values or coded. `x(i, c)` gives vector i at element c; vectors past NV
-// are read again by `again(c)`.
+// The second half of a row whose sum is known: h = x * r * (o + w), stored as
+// values or coded. Vector i is x[i]; vectors past NV are `again(c)`.
 template <typename T, int V, int NV, typename Again>
 __device__ __forceinline__ void write_normed(const Pack<T, V> (&x)[NV], Again again, float r, const NormOut &o,
-                                             int64_t row, const RowGroup &g, int d, RowReducer &red,
-                                             const float (&wk)[kKeep<V, NV> ? NV : 1][V])
+                                             int64_t row, const RowGroup &g, int d, RowReducer &red)
 {
-    float w[V], h[V];
+    const auto normed = [&](const Pack<T, V> &v, int c, float (&h)[V]) {
+        float w[V];
+        channel_weights<V>(o.w, o.w_off, c, d, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[j] = elem(v, j) * r * w[j];
+    };
+    const int rest = (NV * g.G + g.t) * V;
+    float h[V];
     if (!o.codes) {
         T *out = static_cast<T *>(o.H) + row * o.ldh;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * g.G + g.t) * V;
             if (c >= d) continue;
-            if constexpr (kKeep<V, NV>) {
-                normed<T, V>(x[i], r, wk[i], h);
-            } else {
-                channel_weights<V>(o.w, o.w_off, c, d, w);
-                normed<T, V>(x[i], r, w, h);
-            }
-            store_values<T, V>(out, c, d, h);
+            normed(x[i], c, h);
+            store_pack<T, V>(out, c, d, pack_of<T, V>(h));
         }
-        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
-            channel_weights<V>(o.w, o.w_off, c, d, w);
-            normed<T, V>(again(c), r, w, h);
-            store_values<T, V>(out, c, d, h);
+        for (int c = rest; c < d; c += g.G * V) {
+            normed(again(c), c, h);
+            store_pack<T, V>(out, c, d, pack_of<T, V>(h));
         }
         return;
     }
@@ -137,20 +133,12 @@ __device__ __forceinline__ void write_normed(const Pack<T, V> (&x)[NV], Again ag
     for (int i = 0; i < NV; ++i) {
         const int c = (i * g.G + g.t) * V;
         if (c >= d) continue;
-        if constexpr (kKeep<V, NV>) {
-            normed<T, V>(x[i], r, wk[i], h);
-        } else {
-            channel_weights<V>(o.w, o.w_off, c, d, w);
-            normed<T, V>(x[i], r, w, h);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) mb = max(mb, c + j < d ? abs_bits(h[j]) : 0u);
+        normed(x[i], c, h);
+        mb = largest<V>(h, c, d, mb);
     }
-    for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
-        channel_weights<V>(o.w, o.w_off, c, d, w);
-        normed<T, V>(again(c), r, w, h);
-#pragma unroll
-        for (int j = 0; j < V; ++j) mb = max(mb, c + j < d ? abs_bits(h[j]) : 0u);
+    for (int c = rest; c < d; c += g.G * V) {
+        normed(again(c), c, h);
+        mb = largest<V>(h, c, d, mb);
     }
     const CodeScale cs = code_scale(red.max_bits(mb));
     if (g.t == 0) o.h_scale[row] = cs.scale;
@@ -159,32 +147,17 @@ __device__ __forceinline__ void write_normed(const Pack<T, V> (&x)[NV], Again ag
     for (int i = 0; i < NV; ++i) {
         const int c = (i * g.G + g.t) * V;
         if (c >= d) continue;
-        if constexpr (kKeep<V, NV>) {
-            normed<T, V>(x[i], r, wk[i], h);
-        } else {
-            channel_weights<V>(o.w, o.w_off, c, d, w);
-            normed<T, V>(x[i], r, w, h);
-        }
+        normed(x[i], c, h);
         store_codes<V>(out, c, d, h, cs.factor);
     }
-    for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
-        channel_weights<V>(o.w, o.w_off, c, d, w);
-        normed<T, V>(again(c), r, w, h);
+    for (int c = rest; c < d; c += g.G * V) {
+        normed(again(c), c, h);
         store_codes<V>(out, c, d, h, cs.factor);
     }
 }
 
-template <int V, int NV>
-__device__ __forceinline__ void keep_weights(float (&wk)[kKeep<V, NV> ? NV : 1][V], const float *w, float off,
-                                             const RowGroup &g, int d)
-{
-    if constexpr (kKeep<V, NV>) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) channel_weights<V>(w, off, (i * g.G + g.t) * V, d, wk[i]);
-    }
-}
-
-template <typename T, int V, int NV> __global__ void __launch_bounds__(1024) norm_before_kernel(const NormBeforeArgs a)
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_before_kernel(const NormBeforeArgs a)
 {
     __shared__ float rbuf[2 * 96];
     pdl_wait();
@@ -192,161 +165,81 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(1024) nor
     const RowGroup g = row_group(a.G);
     RowReducer red{rbuf, a.G / 32};
     const int d = static_cast<int>(a.d);
-    float wk[kKeep<V, NV> ? NV : 1][V];
-    keep_weights<V, NV>(wk, a.out.w, a.out.w_off, g, d);
-    Pack<T, V> next[NV];
-    if (kAhead<T, V, NV> && g.row < a.m) load_row<T, V, NV>(next, static_cast<const T *>(a.X) + g.row * a.ldx, g.t, g.G, d);
     for (int64_t row = g.row; row < a.m; row += g.step) {
         const T *xr = static_cast<const T *>(a.X) + row * a.ldx;
         Pack<T, V> x[NV];
-        if constexpr (kAhead<T, V, NV>) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) x[i] = next[i];
-            if (row + g.step < a.m) load_row<T, V, NV>(next, xr + g.step * a.ldx, g.t, g.G, d);
-        } else {
-            load_row<T, V, NV>(x, xr, g.t, g.G, d);
-        }
+        load_row<T, V, NV>(x, xr, g.t, g.G, d);
         float r = 1.0f;   // x * 1 * 1 is x
         if (!a.plain) {
             float s[1] = {0.0f};
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float f = to_f32(x[i].e[j]);
-                    s[0] = fmaf(f, f, s[0]);
-                }
-            for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
-                const Pack<T, V> v = load_pack<T, V>(xr, c, d);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float f = to_f32(v.e[j]);
-                    s[0] = fmaf(f, f, s[0]);
-                }
-            }
+            for (int i = 0; i < NV; ++i) s[0] = square_sum<T, V>(x[i], s[0]);
+            for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) s[0] = square_sum<T, V>(load_pack<T, V>(xr, c, d), s[0]);
             red.sum(s);
             r = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.eps);
         }
-        write_normed<T, V, NV>(x, [&](int c) { return load_pack<T, V>(xr, c, d); }, r, a.out, row, g, d, red, wk);
+        write_normed<T, V, NV>(x, [&](int c) { return load_pack<T, V>(xr, c, d); }, r, a.out, row, g, d, red);
     }
 }
 
-// y = r + s g N(b) (o + w), one vector; `q` = s / sqrt(mean(b^2) + eps).
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> joined(const Pack<T, V> &rv, const Pack<T, V> &bv, const Pack<T, V> &gv, float q,
-                                             const float wg[V], int gate_kind)
-{
-    Pack<T, V> y;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float f = to_f32(bv.e[j]) * q * wg[j];
-        if (gate_kind == Q4_GATE_FULL) f *= to_f32(gv.e[j]);
-        y.e[j] = from_f32<T>(to_f32(rv.e[j]) + f);
-    }
-    return y;
-}
-// (o + w), times the channel's gate where there is one.
-template <int V> __device__ __forceinline__ void gated_weights(const NormAfterArgs &a, int c, int d, float out[V])
-{
-    channel_weights<V>(a.w, a.w_off, c, d, out);
-    if (a.gate_kind == Q4_GATE_CHANNEL) {
-        float g[V];
-        load_params<V>(static_cast<const float *>(a.gate), c, d, g);
-#pragma unroll
-        for (int j = 0; j < V; ++j) out[j] *= g[j];
-    }
-}
-
-template <typename T, int V, int NV> __global__ void __launch_bounds__(1024) norm_after_kernel(const NormAfterArgs a)
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_after_kernel(const NormAfterArgs a)
 {
     __shared__ float rbuf[2 * 96];
     pdl_wait();
+    pdl_launch_dependents();
     const RowGroup g = row_group(a.G);
     RowReducer red{rbuf, a.G / 32};
-    const int d = static_cast<int>(a.d);
+    const int d = static_cast<int>(a.d), rest = (NV * g.G + g.t) * V;
     const bool full = a.gate_kind == Q4_GATE_FULL;
-    constexpr bool keep = kKeep<V, NV>, ahead = kAhead<T, V, NV>;
-    float wk[keep ? NV : 1][V], wn[keep ? NV : 1][V];
-    if constexpr (keep) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) gated_weights<V>(a, (i * g.G + g.t) * V, d, wk[i]);
-    }
-    if (a.out.H) keep_weights<V, NV>(wn, a.out.w, a.out.w_off, g, d);
-    const T *R = static_cast<const T *>(a.R), *B = static_cast<const T *>(a.B), *Gt = static_cast<const T *>(a.gate);
-    Pack<T, V> bn[NV], rn[NV], gn[NV];
-    if (ahead && g.row < a.m) {
-        load_row<T, V, NV>(bn, B + g.row * a.ldb, g.t, g.G, d);
-        load_row<T, V, NV>(rn, R + g.row * a.ldr, g.t, g.G, d);
-        if (full) load_row<T, V, NV>(gn, Gt + g.row * a.ldg, g.t, g.G, d);
-    }
     for (int64_t row = g.row; row < a.m; row += g.step) {
-        const T *br = B + row * a.ldb, *rr = R + row * a.ldr, *gr = full ? Gt + row * a.ldg : nullptr;
+        const T *br = static_cast<const T *>(a.B) + row * a.ldb, *rr = static_cast<const T *>(a.R) + row * a.ldr;
+        const T *gr = full ? static_cast<const T *>(a.gate) + row * a.ldg : nullptr;
         T *yr = static_cast<T *>(a.Y) + row * a.ldy;
         Pack<T, V> b[NV], r[NV], gt[NV];
-        if constexpr (ahead) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) b[i] = bn[i], r[i] = rn[i], gt[i] = gn[i];
-            if (row + g.step < a.m) {
-                load_row<T, V, NV>(bn, br + g.step * a.ldb, g.t, g.G, d);
-                load_row<T, V, NV>(rn, rr + g.step * a.ldr, g.t, g.G, d);
-                if (full) load_row<T, V, NV>(gn, gr + g.step * a.ldg, g.t, g.G, d);
-            }
-        } else {
-            load_row<T, V, NV>(b, br, g.t, g.G, d);
-            load_row<T, V, NV>(r, rr, g.t, g.G, d);
-            if (full) load_row<T, V, NV>(gt, gr, g.t, g.G, d);
-        }
+        load_row<T, V, NV>(b, br, g.t, g.G, d);
+        load_row<T, V, NV>(r, rr, g.t, g.G, d);
+        if (full) load_row<T, V, NV>(gt, gr, g.t, g.G, d);
         float s[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float f = to_f32(b[i].e[j]);
-                s[0] = fmaf(f, f, s[0]);
-            }
-        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
-            const Pack<T, V> v = load_pack<T, V>(br, c, d);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float f = to_f32(v.e[j]);
-                s[0] = fmaf(f, f, s[0]);
-            }
-        }
+        for (int i = 0; i < NV; ++i) s[0] = square_sum<T, V>(b[i], s[0]);
+        for (int c = rest; c < d; c += g.G * V) s[0] = square_sum<T, V>(load_pack<T, V>(br, c, d), s[0]);
         red.sum(s);
         float q = a.scale / sqrtf(s[0] / static_cast<float>(d) + a.eps);
         if (a.gate_kind == Q4_GATE_TOKEN) q *= static_cast<const float *>(a.gate)[row];
+        // y = r + q g b (o + w), stored; the sum of its squares as stored
         s[0] = 0.0f;
+        const auto join = [&](const Pack<T, V> &rv, const Pack<T, V> &bv, const Pack<T, V> &gv, int c) {
+            float w[V], y[V];
+            channel_weights<V>(a.w, a.w_off, c, d, w);
+            if (a.gate_kind == Q4_GATE_CHANNEL) {
+                float gc[V];
+                load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
+#pragma unroll
+                for (int j = 0; j < V; ++j) w[j] *= gc[j];
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float f = elem(bv, j) * q * w[j];
+                if (full) f *= elem(gv, j);
+                y[j] = c + j < d ? elem(rv, j) + f : 0.0f;
+            }
+            const Pack<T, V> o = pack_of<T, V>(y);
+            store_pack<T, V>(yr, c, d, o);
+            s[0] = square_sum<T, V>(o, s[0]);
+            return o;
+        };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * g.G + g.t) * V;
-            if (c >= d) continue;
-            float w[V];
-            if constexpr (!keep) gated_weights<V>(a, c, d, w);
-            r[i] = joined<T, V>(r[i], b[i], gt[i], q, keep ? wk[keep ? i : 0] : w, a.gate_kind);
-            store_pack<T, V>(yr, c, d, r[i]);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float f = c + j < d ? to_f32(r[i].e[j]) : 0.0f;
-                s[0] = fmaf(f, f, s[0]);
-            }
+            if (c < d) r[i] = join(r[i], b[i], gt[i], c);
         }
-        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
-            float w[V];
-            gated_weights<V>(a, c, d, w);
-            Pack<T, V> gv{};
-            if (full) gv = load_pack<T, V>(gr, c, d);
-            const Pack<T, V> y = joined<T, V>(load_pack<T, V>(rr, c, d), load_pack<T, V>(br, c, d), gv, q, w, a.gate_kind);
-            store_pack<T, V>(yr, c, d, y);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float f = c + j < d ? to_f32(y.e[j]) : 0.0f;
-                s[0] = fmaf(f, f, s[0]);
-            }
-        }
+        for (int c = rest; c < d; c += g.G * V)
+            join(load_pack<T, V>(rr, c, d), load_pack<T, V>(br, c, d), full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>(), c);
         if (a.out.H) {
             red.sum(s);
             const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.out_eps);
-            write_normed<T, V, NV>(r, [&](int c) { return load_pack<T, V>(yr, c, d); }, rho, a.out, row, g, d, red, wn);
+            write_normed<T, V, NV>(r, [&](int c) { return load_pack<T, V>(yr, c, d); }, rho, a.out, row, g, d, red);
         }
     }
 }
@@ -410,46 +303,37 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         load_row<T, V, NV>(dh, hr, g.t, g.G, d);
         if (rr) load_row<T, V, NV>(dr, rr, g.t, g.G, d);
         float s[2] = {0.0f, 0.0f};
+        const auto sums = [&](const Pack<T, V> &xv, const Pack<T, V> &hv, int c) {
+            float w[V];
+            channel_weights<V>(a.w, a.w_off, c, d, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float f = elem(xv, j);
+                s[0] = fmaf(f, f, s[0]);
+                s[1] = fmaf(elem(hv, j) * w[j], f, s[1]);
+            }
+        };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * g.G + g.t) * V;
-            float w[V];
-            if (c >= d) continue;
-            channel_weights<V>(a.w, a.w_off, c, d, w);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float f = to_f32(x[i].e[j]);
-                s[0] = fmaf(f, f, s[0]);
-                s[1] = fmaf(to_f32(dh[i].e[j]) * w[j], f, s[1]);
-            }
+            if (c < d) sums(x[i], dh[i], c);
         }
-        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
-            float w[V];
-            channel_weights<V>(a.w, a.w_off, c, d, w);
-            const Pack<T, V> xv = load_pack<T, V>(xr, c, d), hv = load_pack<T, V>(hr, c, d);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float f = to_f32(xv.e[j]);
-                s[0] = fmaf(f, f, s[0]);
-                s[1] = fmaf(to_f32(hv.e[j]) * w[j], f, s[1]);
-            }
-        }
+        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) sums(load_pack<T, V>(xr, c, d), load_pack<T, V>(hr, c, d), c);
         red.sum(s);
         const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.eps);
         const float mean = rho * s[1] / static_cast<float>(d);
         auto one = [&](int c, const Pack<T, V> &xv, const Pack<T, V> &hv, const Pack<T, V> &rv, float *col) {
             float w[V];
             channel_weights<V>(a.w, a.w_off, c, d, w);
-            Pack<T, V> o;
+            float o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float u = to_f32(xv.e[j]) * rho, h = to_f32(hv.e[j]);
+                const float u = elem(xv, j) * rho, h = elem(hv, j);
                 col[j] = fmaf(h, u, col[j]);
-                float v = rho * (h * w[j] - u * mean);
-                if (rr) v += to_f32(rv.e[j]);
-                o.e[j] = from_f32<T>(v);
+                o[j] = rho * (h * w[j] - u * mean);
+                if (rr) o[j] += elem(rv, j);
             }
-            store_pack<T, V>(out, c, d, o);
+            store_pack<T, V>(out, c, d, pack_of<T, V>(o));
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -460,8 +344,7 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
             float col[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) col[j] = !first && tail && c + j < d ? tail[c + j] : 0.0f;
-            Pack<T, V> rv{};
-            if (rr) rv = load_pack<T, V>(rr, c, d);
+            const Pack<T, V> rv = rr ? load_pack<T, V>(rr, c, d) : zero_pack<T, V>();
             one(c, load_pack<T, V>(xr, c, d), load_pack<T, V>(hr, c, d), rv, col);
             if (tail)
 #pragma unroll
@@ -501,7 +384,8 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         load_row<T, V, NV>(b, br, g.t, g.G, d);
         load_row<T, V, NV>(dy, dyr, g.t, g.G, d);
         if (full) load_row<T, V, NV>(gt, gr, g.t, g.G, d);
-        // sums of b^2, of g w dy b, and (a token's gate) of w dy b
+        // sums of b^2 and of g w dy b (a token's gate is taken out: its gradient is
+        // that sum)
         float s[2] = {0.0f, 0.0f};
         auto sums = [&](int c, const Pack<T, V> &bv, const Pack<T, V> &yv, const Pack<T, V> &gv) {
             float w[V], gc[V];
@@ -509,10 +393,10 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
             if (channel) load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float f = to_f32(bv.e[j]);
-                const float gw = channel ? gc[j] * w[j] : full ? to_f32(gv.e[j]) * w[j] : w[j];
+                const float f = elem(bv, j);
+                const float gw = channel ? gc[j] * w[j] : full ? elem(gv, j) * w[j] : w[j];
                 s[0] = fmaf(f, f, s[0]);
-                s[1] = fmaf(to_f32(yv.e[j]) * gw, f, s[1]);
+                s[1] = fmaf(elem(yv, j) * gw, f, s[1]);
             }
         };
 #pragma unroll
@@ -521,8 +405,7 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
             if (c < d) sums(c, b[i], dy[i], gt[i]);
         }
         for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
-            Pack<T, V> gv{};
-            if (full) gv = load_pack<T, V>(gr, c, d);
+            const Pack<T, V> gv = full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>();
             sums(c, load_pack<T, V>(br, c, d), load_pack<T, V>(dyr, c, d), gv);
         }
         red.sum(s);
@@ -534,18 +417,18 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
             float w[V], gc[V];
             channel_weights<V>(a.w, a.w_off, c, d, w);
             if (channel) load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
-            Pack<T, V> o, og;
+            float o[V], og[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float u = to_f32(bv.e[j]) * rho, y = to_f32(yv.e[j]);
-                const float gv1 = channel ? gc[j] : full ? to_f32(gv.e[j]) : gtok;
+                const float u = elem(bv, j) * rho, y = elem(yv, j);
+                const float gj = channel ? gc[j] : full ? elem(gv, j) : gtok;
                 // the channel's gate, like s, is a factor of the whole column
-                col[j] = fmaf(channel ? y : y * gv1, u, col[j]);
-                o.e[j] = from_f32<T>(q * (y * (gv1 * w[j]) - u * mean));
-                if (full) og.e[j] = from_f32<T>(a.scale * y * u * w[j]);
+                col[j] = fmaf(channel ? y : y * gj, u, col[j]);
+                o[j] = q * (y * (gj * w[j]) - u * mean);
+                og[j] = a.scale * y * u * w[j];
             }
-            store_pack<T, V>(out, c, d, o);
-            if (dgr) store_pack<T, V>(dgr, c, d, og);
+            store_pack<T, V>(out, c, d, pack_of<T, V>(o));
+            if (dgr) store_pack<T, V>(dgr, c, d, pack_of<T, V>(og));
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -556,8 +439,7 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
             float col[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) col[j] = !first && tail && c + j < d ? tail[c + j] : 0.0f;
-            Pack<T, V> gv{};
-            if (full) gv = load_pack<T, V>(gr, c, d);
+            const Pack<T, V> gv = full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>();
             one(c, load_pack<T, V>(br, c, d), load_pack<T, V>(dyr, c, d), gv, col);
             if (tail)
 #pragma unroll
@@ -601,31 +483,31 @@ struct RowPlan {
     int64_t ctas;
 };
 
-// `max_threads`: the kernel's launch bound. A warp holds a row where its
-// registers do; wider rows take a CTA.
-RowPlan plan_rows(int V, bool wide, int64_t m, int64_t d, int max_threads, int64_t max_ctas)
+// Vectors a thread, threads a row and a CTA. `wide`: 16 bytes an access, with 1,
+// 2 or 4 vectors a thread, else 2 or 8. Few rows take many threads each; many
+// take a warp each where that holds them, else CTAs of about 256 threads: their
+// barriers stop fewer others, and several fit on an SM. A row longer than 512
+// threads hold is finished by the kernels' loops.
+RowPlan plan_rows(int V, bool wide, int64_t m, int64_t d, bool backward, int64_t max_ctas)
 {
     RowPlan p;
     p.V = V;
     const int64_t vecs = ceil_div(d, V);
-    const int nvs[2][3] = {{2, 8, 8}, {1, 2, 4}};
-    const int *nv = nvs[wide ? 1 : 0];
-    const int most = nv[2];
-    const bool few = m <= 304;   // fewer rows than CTAs the device holds: threads, not vectors, shorten a row
-    p.NV = most;
+    const int nv[2][3] = {{2, 8, 8}, {1, 2, 4}};
+    const int *n = nv[wide ? 1 : 0];
+    const bool few = m <= 304;
+    p.NV = n[2];
     p.G = 32;
-    if (vecs <= 32 * nv[0]) {
-        p.NV = nv[0];
-    } else if (!few && vecs <= 32 * most) {
-        p.NV = vecs <= 32 * nv[1] ? nv[1] : most;
+    if (vecs <= 32 * n[0]) {
+        p.NV = n[0];
+    } else if (!few && vecs <= 32 * n[2]) {
+        p.NV = vecs <= 32 * n[1] ? n[1] : n[2];
     } else {
-        const int target = few ? max_threads : std::min(512, max_threads);
-        for (int i = 0; i < 3; ++i)
-            if (ceil_div(vecs, nv[i]) <= target || i == 2) {
-                p.NV = nv[i];
-                break;
-            }
-        p.G = static_cast<int>(std::min<int64_t>(max_threads, round_up(ceil_div(vecs, p.NV), 32)));
+        const int limit = few && !backward ? 1024 : few ? 512 : 256;
+        for (int i = 2; i >= 0; --i)
+            if (ceil_div(vecs, n[i]) <= std::min(limit, n[i] == 1 && !backward ? 1024 : 512)) p.NV = n[i];
+        p.G = static_cast<int>(std::min<int64_t>(512, round_up(ceil_div(vecs, p.NV), 32)));
+        if (p.NV == 1 && !backward) p.G = static_cast<int>(round_up(vecs, 32));
     }
     p.threads = p.G == 32 ? (few ? 64 : 256) : p.G;
     p.ctas = std::min<int64_t>(ceil_div(m, p.threads / p.G), max_ctas);
@@ -679,24 +561,24 @@ cudaError_t launch_columns(NormColumnArgs a, cudaStream_t s)
 
 } // namespace
 
-cudaError_t launch_norm_before(const NormBeforeArgs &a, int type, int vec, int sm_count, cudaStream_t s)
+cudaError_t launch_norm_before(const NormBeforeArgs &a, int type, int vec, int, cudaStream_t s)
 {
     const bool wide = vec * type_size(type) == 16;
-    const RowPlan p = plan_rows(vec, wide, a.m, a.d, 1024, 8 * static_cast<int64_t>(sm_count));
+    const RowPlan p = plan_rows(vec, wide, a.m, a.d, false, int64_t(1) << 30);
     return launch_rows<BeforeKernel>(type, p, wide, a, 0, s);
 }
 
-cudaError_t launch_norm_after(const NormAfterArgs &a, int type, int vec, int sm_count, cudaStream_t s)
+cudaError_t launch_norm_after(const NormAfterArgs &a, int type, int vec, int, cudaStream_t s)
 {
     const bool wide = vec * type_size(type) == 16;
-    const RowPlan p = plan_rows(vec, wide, a.m, a.d, 1024, 8 * static_cast<int64_t>(sm_count));
+    const RowPlan p = plan_rows(vec, wide, a.m, a.d, false, int64_t(1) << 30);
     return launch_rows<AfterKernel>(type, p, wide, a, 0, s);
 }
 
 cudaError_t launch_norm_before_bwd(const NormBeforeBwdArgs &a, float *dw, int type, int vec, int sm_count, cudaStream_t s)
 {
     const bool wide = vec * type_size(type) == 16;
-    const RowPlan p = plan_rows(vec, wide, a.m, a.d, 512, std::min<int64_t>(kNormPartials, 2 * static_cast<int64_t>(sm_count)));
+    const RowPlan p = plan_rows(vec, wide, a.m, a.d, true, std::min<int64_t>(kNormPartials, 4 * static_cast<int64_t>(sm_count)));
     cudaError_t e = launch_rows<BeforeBwdKernel>(type, p, wide, a, partial_smem(p), s);
     if (e != cudaSuccess || !dw) return e;
     NormColumnArgs c{};
@@ -711,7 +593,7 @@ cudaError_t launch_norm_before_bwd(const NormBeforeBwdArgs &a, float *dw, int ty
 cudaError_t launch_norm_after_bwd(const NormAfterBwdArgs &a, float *dw, int type, int vec, int sm_count, cudaStream_t s)
 {
     const bool wide = vec * type_size(type) == 16;
-    const RowPlan p = plan_rows(vec, wide, a.m, a.d, 512, std::min<int64_t>(kNormPartials, 2 * static_cast<int64_t>(sm_count)));
+    const RowPlan p = plan_rows(vec, wide, a.m, a.d, true, std::min<int64_t>(kNormPartials, 4 * static_cast<int64_t>(sm_count)));
     cudaError_t e = launch_rows<AfterBwdKernel>(type, p, wide, a, partial_smem(p), s);
     if (e != cudaSuccess || !a.partials) return e;
     NormColumnArgs c{};

@@ -10,6 +10,7 @@
 // where they are needed.
 #pragma once
 
+#include <cstring>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -19,43 +20,134 @@ namespace q4 {
 
 // ------------------------------------------------------- typed elements --
 
-template <typename T> __device__ __forceinline__ float to_f32(T v);
-template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-
 // Rounded once, to nearest even.
 template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// V elements of type T, moved by one access of V * sizeof(T) bytes.
-template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
-    T e[V];
+// V elements of type T, moved by one access of V * sizeof(T) bytes and held as
+// words: an array of 16-bit elements would take a register each.
+template <typename T, int V, int B = static_cast<int>(sizeof(T)) * V> struct Pack {
+    using Word = uint32_t;
+    static constexpr int kWords = B / 4;
+    Word w[kWords];
+};
+template <typename T, int V> struct Pack<T, V, 2> {
+    using Word = uint16_t;
+    static constexpr int kWords = 1;
+    Word w[1];
+};
+template <typename T, int V> struct Pack<T, V, 1> {
+    using Word = uint8_t;
+    static constexpr int kWords = 1;
+    Word w[1];
 };
 
-// Elements c .. c + V - 1 of a row of d, zeros past its end. `p` and the row
-// are aligned to the pack.
-template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(const T *row, int64_t c, int64_t d)
+// Element i (a constant where it matters) in fp32.
+template <typename T, int V> __device__ __forceinline__ float elem(const Pack<T, V> &p, int i)
 {
-    Pack<T, V> r;
-    if (c + V <= d) {
-        r = *reinterpret_cast<const Pack<T, V> *>(row + c);
+    if constexpr (sizeof(T) == 4) {
+        return __uint_as_float(p.w[i]);
+    } else {
+        const uint32_t u = V == 1 ? p.w[0] : p.w[i / 2] >> (16 * (i & 1));
+        if constexpr (__is_same(T, __nv_bfloat16)) return __uint_as_float(V > 1 && (i & 1) ? p.w[i / 2] & 0xFFFF0000u : u << 16);
+        else return __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
+    }
+}
+template <typename T> __device__ __forceinline__ uint32_t bits16(float f)
+{
+    if constexpr (__is_same(T, __nv_bfloat16)) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+    else return __half_as_ushort(__float2half_rn(f));
+}
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> pack_of(const float (&f)[V])
+{
+    Pack<T, V> p;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p.w[i] = __float_as_uint(f[i]);
+    } else if constexpr (V == 1) {
+        p.w[0] = static_cast<uint16_t>(bits16<T>(f[0]));
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) r.e[i] = c + i < d ? row[c + i] : from_f32<T>(0.0f);
+        for (int i = 0; i < V; i += 2) {
+            if constexpr (__is_same(T, __nv_bfloat16)) p.w[i / 2] = pack_bf16x2_rn(f[i], f[i + 1]);
+            else p.w[i / 2] = bits16<T>(f[i]) | bits16<T>(f[i + 1]) << 16;
+        }
     }
-    return r;
+    return p;
 }
-template <typename T, int V> __device__ __forceinline__ void store_pack(T *row, int64_t c, int64_t d, const Pack<T, V> &v)
+// V int8 codes as the bytes of their words.
+template <int V> __device__ __forceinline__ Pack<int8_t, V> pack_codes(const int (&c)[V])
 {
+    Pack<int8_t, V> p;
+    if constexpr (V == 1) {
+        p.w[0] = static_cast<uint8_t>(c[0]);
+    } else if constexpr (V == 2) {
+        p.w[0] = static_cast<uint16_t>((c[0] & 0xFF) | (c[1] & 0xFF) << 8);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            p.w[i / 4] = static_cast<uint32_t>(c[i] & 0xFF) | static_cast<uint32_t>(c[i + 1] & 0xFF) << 8 |
+                         static_cast<uint32_t>(c[i + 2] & 0xFF) << 16 | static_cast<uint32_t>(c[i + 3]) << 24;
+    }
+    return p;
+}
+
+template <int B> struct AccessOf;
+template <> struct AccessOf<16> { using type = uint4; };
+template <> struct AccessOf<8> { using type = uint2; };
+template <> struct AccessOf<4> { using type = uint32_t; };
+template <> struct AccessOf<2> { using type = uint16_t; };
+template <> struct AccessOf<1> { using type = uint8_t; };
+
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> zero_pack()
+{
+    Pack<T, V> p;
+#pragma unroll
+    for (int i = 0; i < Pack<T, V>::kWords; ++i) p.w[i] = 0;
+    return p;
+}
+// Elements c .. c + V - 1 of a row of d, zeros past its end. The row is
+// aligned to the pack and c a multiple of V.
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(const T *row, int64_t c, int64_t d)
+{
+    using A = typename AccessOf<static_cast<int>(sizeof(T)) * V>::type;
+    Pack<T, V> p;
     if (c + V <= d) {
-        *reinterpret_cast<Pack<T, V> *>(row + c) = v;
+        const A v = *reinterpret_cast<const A *>(row + c);
+        memcpy(p.w, &v, sizeof(A));
+    } else {
+        p = zero_pack<T, V>();
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c + i < d) {
+                if constexpr (sizeof(T) == 4) p.w[i] = reinterpret_cast<const uint32_t *>(row)[c + i];
+                else if constexpr (V == 1) p.w[0] = reinterpret_cast<const uint16_t *>(row)[c];
+                else p.w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[c + i]) << (16 * (i & 1));
+            }
+    }
+    return p;
+}
+template <typename T, int V> __device__ __forceinline__ void store_pack(T *row, int64_t c, int64_t d, const Pack<T, V> &p)
+{
+    using A = typename AccessOf<static_cast<int>(sizeof(T)) * V>::type;
+    if (c + V <= d) {
+        A v;
+        memcpy(&v, p.w, sizeof(A));
+        *reinterpret_cast<A *>(row + c) = v;
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (c + i < d) row[c + i] = v.e[i];
+            if (c + i < d) {
+                if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t *>(row)[c + i] = p.w[i];
+                else if constexpr (sizeof(T) == 2)
+                    reinterpret_cast<uint16_t *>(row)[c + i] =
+                        static_cast<uint16_t>(V == 1 ? p.w[0] : p.w[i / 2] >> (16 * (i & 1)));
+                else
+                    reinterpret_cast<uint8_t *>(row)[c + i] =
+                        static_cast<uint8_t>(V <= 2 ? p.w[0] >> (8 * i) : p.w[i / 4] >> (8 * (i & 3)));
+            }
     }
 }
 
@@ -158,9 +250,9 @@ __device__ __forceinline__ CodeScale code_scale(uint32_t amax_bits)
     return c;
 }
 // round-half-even(x * factor), |code| <= 127; 0 where the row's factor is 0.
-__device__ __forceinline__ int8_t code_of(float x, float factor)
+__device__ __forceinline__ int code_of(float x, float factor)
 {
-    return factor == 0.0f ? static_cast<int8_t>(0) : static_cast<int8_t>(__float2int_rn(__fmul_rn(x, factor)));
+    return factor == 0.0f ? 0 : __float2int_rn(__fmul_rn(x, factor));
 }
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 

@@ -79,16 +79,16 @@ template <typename X, int V> __device__ __forceinline__ void code_rows(const W8a
         for (int c = static_cast<int>(threadIdx.x) * V; c < a.k; c += kThreads * V) {
             const Pack<X, V> v = load_pack<X, V>(xr, c, a.k);
 #pragma unroll
-            for (int i = 0; i < V; ++i) mb = max(mb, abs_bits(to_f32(v.e[i])));
+            for (int i = 0; i < V; ++i) mb = max(mb, abs_bits(elem(v, i)));
         }
         const CodeScale cs = code_scale(red.max_bits(mb));
         if (threadIdx.x == 0) o.scale[t] = cs.scale;
         for (int c = static_cast<int>(threadIdx.x) * V; c < kp; c += kThreads * V) {
             const Pack<X, V> v = load_pack<X, V>(xr, c, a.k);   // zeros past k; from the first-level cache
-            Pack<int8_t, V> q;
+            int q[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) q.e[i] = code_of(to_f32(v.e[i]), cs.factor);
-            *reinterpret_cast<Pack<int8_t, V> *>(o.codes + t * o.stride + c) = q;
+            for (int i = 0; i < V; ++i) q[i] = code_of(elem(v, i), cs.factor);
+            store_pack<int8_t, V>(o.codes + t * o.stride, c, kp, pack_codes<V>(q));
         }
     }
 }

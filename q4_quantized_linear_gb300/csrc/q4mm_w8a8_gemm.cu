@@ -126,31 +126,28 @@ template <typename T, int V> __global__ void __launch_bounds__(512) code_tile_ke
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * G + t) * V;
-            if (c < kr) x[i] = load_pack<T, V>(xr, c, kr);
-            else
-#pragma unroll
-                for (int j = 0; j < V; ++j) x[i].e[j] = from_f32<T>(0.0f);
+            x[i] = c < kr ? load_pack<T, V>(xr, c, kr) : zero_pack<T, V>();
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) mb = max(mb, abs_bits(to_f32(x[i].e[j])));
+            for (int j = 0; j < V; ++j) mb = max(mb, abs_bits(elem(x[i], j)));
         for (int c = (NV * G + t) * V; c < kr; c += G * V) {
             const Pack<T, V> v = load_pack<T, V>(xr, c, kr);
 #pragma unroll
-            for (int j = 0; j < V; ++j) mb = max(mb, abs_bits(to_f32(v.e[j])));
+            for (int j = 0; j < V; ++j) mb = max(mb, abs_bits(elem(v, j)));
         }
         const CodeScale cs = code_scale(red.max_bits(mb));
         if (t == 0 && row < a.m) a.sx[row] = cs.scale;
         const int j2 = row / a.H, r = row - j2 * a.H;
         uint8_t *out = a.ximg + (static_cast<int64_t>(j2) * a.np * a.H + r) * 128;
         auto put = [&](int c, const Pack<T, V> &v) {
-            Pack<__half, V> o;
+            float f[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) o.e[j] = __int2half_rn(code_of(to_f32(v.e[j]), cs.factor));
+            for (int j = 0; j < V; ++j) f[j] = static_cast<float>(code_of(elem(v, j), cs.factor));
             const int p = c / kPairK, e = c - p * kPairK;   // V divides 8: inside one 16-byte chunk
-            *reinterpret_cast<Pack<__half, V> *>(out + static_cast<int64_t>(p) * a.H * 128 + (((e >> 3) ^ (r & 7)) << 4) +
-                                                 (e & 7) * 2) = o;
+            store_pack<__half, V>(reinterpret_cast<__half *>(out + static_cast<int64_t>(p) * a.H * 128 +
+                                                             (((e >> 3) ^ (r & 7)) << 4)) + (e & 7), 0, V, pack_of<__half, V>(f));
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -515,9 +512,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                         if constexpr (sizeof(T) == 4) {
                             held[ch * 16 + i] = __float_as_uint(y[i]);
                         } else if (i % 2 == 0) {
-                            Pack<T, 2> two;
-                            two.e[0] = from_f32<T>(y[i]), two.e[1] = from_f32<T>(y[i + 1]);
-                            held[ch * 8 + i / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                            const float two[2] = {y[i], y[i + 1]};
+                            held[ch * 8 + i / 2] = pack_of<T, 2>(two).w[0];
                         }
                     }
                 }
@@ -529,16 +525,18 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
 #pragma unroll
                 for (int ch = 0; ch < kHold / 16; ++ch) {
                     if (h0 + ch * 16 >= H) break;
-                    T y[16];
+                    // elements as bits
+                    using Bits = typename AccessOf<static_cast<int>(sizeof(T))>::type;
+                    Bits y[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        if constexpr (sizeof(T) == 4) y[i] = __uint_as_float(held[ch * 16 + i]);
-                        else y[i] = reinterpret_cast<const Pack<T, 2> *>(&held[ch * 8 + i / 2])->e[i % 2];
+                        if constexpr (sizeof(T) == 4) y[i] = held[ch * 16 + i];
+                        else y[i] = static_cast<Bits>(held[ch * 8 + i / 2] >> (16 * (i & 1)));
                     }
                     const int tc = t0 + h0 + ch * 16;
                     if (wide) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) stage[i * 32 + lane] = y[i];
+                        for (int i = 0; i < 16; ++i) reinterpret_cast<Bits *>(stage)[i * 32 + lane] = y[i];
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < kStageTokens; i += kTokensPerStore) {
@@ -560,7 +558,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                     } else if (lane < rows) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (tc + i < a.m) Y[(tc + i) * a.ldy + row0 + lane] = y[i];
+                            if (tc + i < a.m) reinterpret_cast<Bits *>(Y)[(tc + i) * a.ldy + row0 + lane] = y[i];
                     }
                 }
             }
