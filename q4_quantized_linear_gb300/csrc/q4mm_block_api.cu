@@ -112,6 +112,7 @@ int norm_after_impl(void *Y, int64_t ldy, void *H, int64_t ldh, int htype, float
     a.gate = gate, a.ldg = ldg, a.gate_kind = gate_kind;
     a.scale = scale, a.eps = eps, a.out_eps = eps;
     a.m = m, a.d = d;
+    a.status = dev.status, a.wait_ns = wait_limit();
     if (next) a.out = NormOut{H, ldh, codes ? 1 : 0, h_scale, w_next, w_offset_next};
     return cuda_status(launch_norm_after(a, type, vec_of(al, type, codes ? &ca : nullptr, &pa), dev.sm_count, s));
 }
@@ -243,6 +244,7 @@ Q4MM_API int q4_norm_before_backward(void *dX, int64_t lddx, float *dw, const vo
     a.lddx = lddx, a.lddh = lddh, a.lddr = lddr, a.ldx = ldx;
     a.w = w, a.w_off = w_offset, a.eps = eps;
     a.partials = dw ? static_cast<float *>(workspace) : nullptr;
+    a.status = dev.status, a.wait_ns = wait_limit();
     a.m = m, a.d = d;
     return cuda_status(launch_norm_before_bwd(a, dw, type, vec_of(al, type, nullptr, &pa), dev.sm_count, s));
 }
@@ -294,6 +296,7 @@ Q4MM_API int q4_norm_after_backward(void *dB, int64_t lddb, float *dw, void *dga
     a.w = w, a.w_off = w_offset;
     a.gate_kind = gate_kind, a.scale = scale, a.eps = eps;
     a.partials = columns ? static_cast<float *>(workspace) : nullptr;
+    a.status = dev.status, a.wait_ns = wait_limit();
     a.m = m, a.d = d;
     return cuda_status(launch_norm_after_bwd(a, dw, type, vec_of(al, type, nullptr, &pa), dev.sm_count, s));
 }

@@ -26,135 +26,14 @@
 #include <algorithm>
 #include <cuda_runtime.h>
 
-#include "q4mm_norm.h"
-#include "q4mm_rows.cuh"
+#include "q4mm_norm.cuh"
 
 namespace q4 {
 namespace {
 
-// Which rows this thread works on, and where in them.
-struct RowGroup {
-    int t, G;                 // thread of the row, threads of a row
-    int64_t row, step;        // first row, rows between two of this group's
-};
-__device__ __forceinline__ RowGroup row_group(int G)
-{
-    RowGroup g;
-    const int groups = static_cast<int>(blockDim.x) / G;
-    g.G = G;
-    g.t = static_cast<int>(threadIdx.x) % G;
-    g.row = static_cast<int64_t>(blockIdx.x) * groups + static_cast<int>(threadIdx.x) / G;
-    g.step = static_cast<int64_t>(gridDim.x) * groups;
-    return g;
-}
-
 // The largest CTA of a kernel with NV vectors a thread: its registers allow
 // 1024 threads an SM.
 __host__ __device__ constexpr int max_threads(int NV) { return NV == 1 ? 1024 : 512; }
-
-template <typename T, int V, int NV>
-__device__ __forceinline__ void load_row(Pack<T, V> (&x)[NV], const T *row, int t, int G, int d)
-{
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * G + t) * V;
-        x[i] = c < d ? load_pack<T, V>(row, c, d) : zero_pack<T, V>();
-    }
-}
-
-// (o + w) of V channels.
-template <int V> __device__ __forceinline__ void channel_weights(const float *w, float off, int c, int d, float out[V])
-{
-    if (w) {
-        load_params<V>(w, c, d, out);
-#pragma unroll
-        for (int j = 0; j < V; ++j) out[j] += off;
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) out[j] = 1.0f;
-    }
-}
-
-template <typename T, int V> __device__ __forceinline__ float square_sum(const Pack<T, V> &x, float s)
-{
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const float f = elem(x, j);
-        s = fmaf(f, f, s);
-    }
-    return s;
-}
-// The largest |h| of the vector's elements that the row has.
-template <int V> __device__ __forceinline__ uint32_t largest(const float h[V], int c, int d, uint32_t mb)
-{
-#pragma unroll
-    for (int j = 0; j < V; ++j) mb = max(mb, c + j < d ? abs_bits(h[j]) : 0u);
-    return mb;
-}
-template <int V> __device__ __forceinline__ void store_codes(int8_t *row, int c, int d, const float h[V], float factor)
-{
-    int q[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) q[j] = code_of(h[j], factor);
-    store_pack<int8_t, V>(row, c, d, pack_codes<V>(q));
-}
-
-// The second half of a row whose sum is known: h = x * r * (o + w), stored as
-// values or coded. Vector i is x[i]; vectors past NV are `again(c)`.
-template <typename T, int V, int NV, typename Again>
-__device__ __forceinline__ void write_normed(const Pack<T, V> (&x)[NV], Again again, float r, const NormOut &o,
-                                             int64_t row, const RowGroup &g, int d, RowReducer &red)
-{
-    const auto normed = [&](const Pack<T, V> &v, int c, float (&h)[V]) {
-        float w[V];
-        channel_weights<V>(o.w, o.w_off, c, d, w);
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[j] = elem(v, j) * r * w[j];
-    };
-    const int rest = (NV * g.G + g.t) * V;
-    float h[V];
-    if (!o.codes) {
-        T *out = static_cast<T *>(o.H) + row * o.ldh;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c >= d) continue;
-            normed(x[i], c, h);
-            store_pack<T, V>(out, c, d, pack_of<T, V>(h));
-        }
-        for (int c = rest; c < d; c += g.G * V) {
-            normed(again(c), c, h);
-            store_pack<T, V>(out, c, d, pack_of<T, V>(h));
-        }
-        return;
-    }
-    uint32_t mb = 0u;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * g.G + g.t) * V;
-        if (c >= d) continue;
-        normed(x[i], c, h);
-        mb = largest<V>(h, c, d, mb);
-    }
-    for (int c = rest; c < d; c += g.G * V) {
-        normed(again(c), c, h);
-        mb = largest<V>(h, c, d, mb);
-    }
-    const CodeScale cs = code_scale(red.max_bits(mb));
-    if (g.t == 0) o.h_scale[row] = cs.scale;
-    int8_t *out = static_cast<int8_t *>(o.H) + row * o.ldh;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * g.G + g.t) * V;
-        if (c >= d) continue;
-        normed(x[i], c, h);
-        store_codes<V>(out, c, d, h, cs.factor);
-    }
-    for (int c = rest; c < d; c += g.G * V) {
-        normed(again(c), c, h);
-        store_codes<V>(out, c, d, h, cs.factor);
-    }
-}
 
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_before_kernel(const NormBeforeArgs a)
@@ -165,6 +44,7 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
     const RowGroup g = row_group(a.G);
     RowReducer red{rbuf, a.G / 32};
     const int d = static_cast<int>(a.d);
+    const Channels<V, NV, false> wo;
     for (int64_t row = g.row; row < a.m; row += g.step) {
         const T *xr = static_cast<const T *>(a.X) + row * a.ldx;
         Pack<T, V> x[NV];
@@ -178,7 +58,7 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
             red.sum(s);
             r = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.eps);
         }
-        write_normed<T, V, NV>(x, [&](int c) { return load_pack<T, V>(xr, c, d); }, r, a.out, row, g, d, red);
+        write_normed<T, V, NV, false>(x, [&](int c) { return load_pack<T, V>(xr, c, d); }, r, a.out, wo, row, g, d, red);
     }
 }
 
@@ -192,6 +72,16 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
     RowReducer red{rbuf, a.G / 32};
     const int d = static_cast<int>(a.d), rest = (NV * g.G + g.t) * V;
     const bool full = a.gate_kind == Q4_GATE_FULL;
+    const auto after_at = [&](int c, float (&w)[V]) {
+        channel_weights<V>(a.w, a.w_off, c, d, w);
+        if (a.gate_kind == Q4_GATE_CHANNEL) {
+            float gc[V];
+            load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
+#pragma unroll
+            for (int j = 0; j < V; ++j) w[j] *= gc[j];
+        }
+    };
+    const Channels<V, NV, false> wa, wo;
     for (int64_t row = g.row; row < a.m; row += g.step) {
         const T *br = static_cast<const T *>(a.B) + row * a.ldb, *rr = static_cast<const T *>(a.R) + row * a.ldr;
         const T *gr = full ? static_cast<const T *>(a.gate) + row * a.ldg : nullptr;
@@ -209,15 +99,10 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
         if (a.gate_kind == Q4_GATE_TOKEN) q *= static_cast<const float *>(a.gate)[row];
         // y = r + q g b (o + w), stored; the sum of its squares as stored
         s[0] = 0.0f;
-        const auto join = [&](const Pack<T, V> &rv, const Pack<T, V> &bv, const Pack<T, V> &gv, int c) {
+        const auto join = [&](int i, const Pack<T, V> &rv, const Pack<T, V> &bv, const Pack<T, V> &gv, int c) {
             float w[V], y[V];
-            channel_weights<V>(a.w, a.w_off, c, d, w);
-            if (a.gate_kind == Q4_GATE_CHANNEL) {
-                float gc[V];
-                load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
-#pragma unroll
-                for (int j = 0; j < V; ++j) w[j] *= gc[j];
-            }
+            if (i < 0) after_at(c, w);
+            else wa.get(i, c, after_at, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 float f = elem(bv, j) * q * w[j];
@@ -232,51 +117,19 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * g.G + g.t) * V;
-            if (c < d) r[i] = join(r[i], b[i], gt[i], c);
+            if (c < d) r[i] = join(i, r[i], b[i], gt[i], c);
         }
         for (int c = rest; c < d; c += g.G * V)
-            join(load_pack<T, V>(rr, c, d), load_pack<T, V>(br, c, d), full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>(), c);
+            join(-1, load_pack<T, V>(rr, c, d), load_pack<T, V>(br, c, d), full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>(), c);
         if (a.out.H) {
             red.sum(s);
             const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.out_eps);
-            write_normed<T, V, NV>(r, [&](int c) { return load_pack<T, V>(yr, c, d); }, rho, a.out, row, g, d, red);
+            write_normed<T, V, NV, false>(r, [&](int c) { return load_pack<T, V>(yr, c, d); }, rho, a.out, wo, row, g, d, red);
         }
     }
 }
 
 // ---------------------------------------------------------------- backward --
-
-// Adds the CTA's groups' column sums (one group: its registers as they are)
-// into row blockIdx.x of the partials. The tail past the registers has been
-// added there already.
-template <int V, int NV>
-__device__ __forceinline__ void write_partials(float (&acc)[NV][V], float *partials, const RowGroup &g, int d, float *smem)
-{
-    float *out = partials + static_cast<int64_t>(blockIdx.x) * d;
-    const int groups = static_cast<int>(blockDim.x) / g.G;
-    if (groups == 1) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (c + j < d) out[c + j] = acc[i][j];
-        }
-        return;
-    }
-    const int width = g.G * NV * V;   // >= d
-    const int mine = static_cast<int>(threadIdx.x) / g.G;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) smem[mine * width + (i * g.G + g.t) * V + j] = acc[i][j];
-    __syncthreads();
-    for (int c = threadIdx.x; c < d; c += blockDim.x) {
-        float s = 0.0f;
-        for (int k = 0; k < groups; ++k) s += smem[k * width + c];
-        out[c] = s;
-    }
-}
 
 template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm_before_bwd_kernel(const NormBeforeBwdArgs a)
 {
@@ -295,6 +148,9 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         for (int j = 0; j < V; ++j) acc[i][j] = 0.0f;
     float *tail = a.partials ? a.partials + static_cast<int64_t>(blockIdx.x) * d : nullptr;
     bool first = true;
+    const auto at = [&](int c, float (&w)[V]) { channel_weights<V>(a.w, a.w_off, c, d, w); };
+    Channels<V, NV, true> wc;
+    wc.fill(g, at);
     for (int64_t row = g.row; row < a.m; row += g.step) {
         const T *xr = X + row * a.ldx, *hr = DH + row * a.lddh, *rr = DR ? DR + row * a.lddr : nullptr;
         T *out = static_cast<T *>(a.dX) + row * a.lddx;
@@ -303,9 +159,10 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         load_row<T, V, NV>(dh, hr, g.t, g.G, d);
         if (rr) load_row<T, V, NV>(dr, rr, g.t, g.G, d);
         float s[2] = {0.0f, 0.0f};
-        const auto sums = [&](const Pack<T, V> &xv, const Pack<T, V> &hv, int c) {
+        const auto sums = [&](int i, const Pack<T, V> &xv, const Pack<T, V> &hv, int c) {
             float w[V];
-            channel_weights<V>(a.w, a.w_off, c, d, w);
+            if (i < 0) at(c, w);
+            else wc.get(i, c, at, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float f = elem(xv, j);
@@ -316,15 +173,16 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * g.G + g.t) * V;
-            if (c < d) sums(x[i], dh[i], c);
+            if (c < d) sums(i, x[i], dh[i], c);
         }
-        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) sums(load_pack<T, V>(xr, c, d), load_pack<T, V>(hr, c, d), c);
+        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) sums(-1, load_pack<T, V>(xr, c, d), load_pack<T, V>(hr, c, d), c);
         red.sum(s);
         const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.eps);
         const float mean = rho * s[1] / static_cast<float>(d);
-        auto one = [&](int c, const Pack<T, V> &xv, const Pack<T, V> &hv, const Pack<T, V> &rv, float *col) {
+        const auto one = [&](int i, int c, const Pack<T, V> &xv, const Pack<T, V> &hv, const Pack<T, V> &rv, float (&col)[V]) {
             float w[V];
-            channel_weights<V>(a.w, a.w_off, c, d, w);
+            if (i < 0) at(c, w);
+            else wc.get(i, c, at, w);
             float o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -338,14 +196,14 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * g.G + g.t) * V;
-            if (c < d) one(c, x[i], dh[i], dr[i], acc[i]);
+            if (c < d) one(i, c, x[i], dh[i], dr[i], acc[i]);
         }
         for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
             float col[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) col[j] = !first && tail && c + j < d ? tail[c + j] : 0.0f;
             const Pack<T, V> rv = rr ? load_pack<T, V>(rr, c, d) : zero_pack<T, V>();
-            one(c, load_pack<T, V>(xr, c, d), load_pack<T, V>(hr, c, d), rv, col);
+            one(-1, c, load_pack<T, V>(xr, c, d), load_pack<T, V>(hr, c, d), rv, col);
             if (tail)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
@@ -375,6 +233,18 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         for (int j = 0; j < V; ++j) acc[i][j] = 0.0f;
     float *tail = a.partials ? a.partials + static_cast<int64_t>(blockIdx.x) * d : nullptr;
     bool first = true;
+    // (o + w), times the channel's gate
+    const auto at = [&](int c, float (&w)[V]) {
+        channel_weights<V>(a.w, a.w_off, c, d, w);
+        if (channel) {
+            float gc[V];
+            load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
+#pragma unroll
+            for (int j = 0; j < V; ++j) w[j] *= gc[j];
+        }
+    };
+    Channels<V, NV, true> wc;
+    wc.fill(g, at);
     for (int64_t row = g.row; row < a.m; row += g.step) {
         const T *br = B + row * a.ldb, *dyr = DY + row * a.lddy, *gr = full ? Gt + row * a.ldg : nullptr;
         T *out = static_cast<T *>(a.dB) + row * a.lddb;
@@ -387,44 +257,40 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         // sums of b^2 and of g w dy b (a token's gate is taken out: its gradient is
         // that sum)
         float s[2] = {0.0f, 0.0f};
-        auto sums = [&](int c, const Pack<T, V> &bv, const Pack<T, V> &yv, const Pack<T, V> &gv) {
-            float w[V], gc[V];
-            channel_weights<V>(a.w, a.w_off, c, d, w);
-            if (channel) load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
+        const auto sums = [&](int i, int c, const Pack<T, V> &bv, const Pack<T, V> &yv, const Pack<T, V> &gv) {
+            float w[V];
+            if (i < 0) at(c, w);
+            else wc.get(i, c, at, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float f = elem(bv, j);
-                const float gw = channel ? gc[j] * w[j] : full ? elem(gv, j) * w[j] : w[j];
                 s[0] = fmaf(f, f, s[0]);
-                s[1] = fmaf(elem(yv, j) * gw, f, s[1]);
+                s[1] = fmaf(elem(yv, j) * (full ? elem(gv, j) * w[j] : w[j]), f, s[1]);
             }
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * g.G + g.t) * V;
-            if (c < d) sums(c, b[i], dy[i], gt[i]);
+            if (c < d) sums(i, c, b[i], dy[i], gt[i]);
         }
-        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
-            const Pack<T, V> gv = full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>();
-            sums(c, load_pack<T, V>(br, c, d), load_pack<T, V>(dyr, c, d), gv);
-        }
+        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V)
+            sums(-1, c, load_pack<T, V>(br, c, d), load_pack<T, V>(dyr, c, d), full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>());
         red.sum(s);
         const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.eps);
         if (token && a.dgate && g.t == 0) static_cast<float *>(a.dgate)[row] = a.scale * rho * s[1];
         const float mean = gtok * rho * s[1] / static_cast<float>(d);
         const float q = a.scale * rho;
-        auto one = [&](int c, const Pack<T, V> &bv, const Pack<T, V> &yv, const Pack<T, V> &gv, float *col) {
-            float w[V], gc[V];
-            channel_weights<V>(a.w, a.w_off, c, d, w);
-            if (channel) load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
-            float o[V], og[V];
+        const auto one = [&](int i, int c, const Pack<T, V> &bv, const Pack<T, V> &yv, const Pack<T, V> &gv, float (&col)[V]) {
+            float w[V], o[V], og[V];
+            if (i < 0) at(c, w);
+            else wc.get(i, c, at, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float u = elem(bv, j) * rho, y = elem(yv, j);
-                const float gj = channel ? gc[j] : full ? elem(gv, j) : gtok;
+                const float gy = full ? elem(gv, j) * y : gtok * y;
                 // the channel's gate, like s, is a factor of the whole column
-                col[j] = fmaf(channel ? y : y * gj, u, col[j]);
-                o[j] = q * (y * (gj * w[j]) - u * mean);
+                col[j] = fmaf(gy, u, col[j]);
+                o[j] = q * (gy * w[j] - u * mean);
                 og[j] = a.scale * y * u * w[j];
             }
             store_pack<T, V>(out, c, d, pack_of<T, V>(o));
@@ -433,14 +299,14 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * g.G + g.t) * V;
-            if (c < d) one(c, b[i], dy[i], gt[i], acc[i]);
+            if (c < d) one(i, c, b[i], dy[i], gt[i], acc[i]);
         }
         for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
             float col[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) col[j] = !first && tail && c + j < d ? tail[c + j] : 0.0f;
             const Pack<T, V> gv = full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>();
-            one(c, load_pack<T, V>(br, c, d), load_pack<T, V>(dyr, c, d), gv, col);
+            one(-1, c, load_pack<T, V>(br, c, d), load_pack<T, V>(dyr, c, d), gv, col);
             if (tail)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
@@ -484,17 +350,17 @@ struct RowPlan {
 };
 
 // Vectors a thread, threads a row and a CTA. `wide`: 16 bytes an access, with 1,
-// 2 or 4 vectors a thread, else 2 or 8. Few rows take many threads each; many
+// 2 or 4 vectors a thread, else (4 bytes or an element) 2, 4 or 8. Few rows take many threads each; many
 // take a warp each where that holds them, else CTAs of about 256 threads: their
 // barriers stop fewer others, and several fit on an SM. A row longer than 512
 // threads hold is finished by the kernels' loops.
-RowPlan plan_rows(int V, bool wide, int64_t m, int64_t d, bool backward, int64_t max_ctas)
+RowPlan plan_rows(int V, bool wide, int64_t m, int64_t d, bool backward, int64_t sm_count)
 {
     RowPlan p;
     p.V = V;
     const int64_t vecs = ceil_div(d, V);
-    const int nv[2][3] = {{2, 8, 8}, {1, 2, 4}};
-    const int *n = nv[wide ? 1 : 0];
+    const int nv[3][3] = {{2, 4, 8}, {2, 4, 8}, {1, 2, 4}};
+    const int *n = nv[wide ? 2 : V - 1];
     const bool few = m <= 304;
     p.NV = n[2];
     p.G = 32;
@@ -510,7 +376,11 @@ RowPlan plan_rows(int V, bool wide, int64_t m, int64_t d, bool backward, int64_t
         if (p.NV == 1 && !backward) p.G = static_cast<int>(round_up(vecs, 32));
     }
     p.threads = p.G == 32 ? (few ? 64 : 256) : p.G;
-    p.ctas = std::min<int64_t>(ceil_div(m, p.threads / p.G), max_ctas);
+    // Forward a CTA takes its rows once and leaves: CTAs of other rows fill the
+    // time that its loads take. Backward as many as the device holds at the least
+    // (1024 threads an SM), for the column sums.
+    p.ctas = std::min<int64_t>(ceil_div(m, p.threads / p.G),
+                               backward ? std::min<int64_t>(kNormPartials, sm_count * (1024 / p.threads)) : (int64_t(1) << 30));
     return p;
 }
 
@@ -520,8 +390,8 @@ cudaError_t launch_rows_v(const RowPlan &p, bool wide, Args a, size_t smem, cuda
     constexpr int W = 16 / sizeof(T);
     const void *fn = nullptr;
     if (wide) fn = p.NV == 1 ? K<T, W, 1>::fn() : p.NV == 2 ? K<T, W, 2>::fn() : K<T, W, 4>::fn();
-    else if (sizeof(T) == 2 && p.V == 2) fn = p.NV == 2 ? K<T, 2, 2>::fn() : K<T, 2, 8>::fn();
-    else fn = p.NV == 2 ? K<T, 1, 2>::fn() : K<T, 1, 8>::fn();
+    else if (sizeof(T) == 2 && p.V == 2) fn = p.NV == 2 ? K<T, 2, 2>::fn() : p.NV == 4 ? K<T, 2, 4>::fn() : K<T, 2, 8>::fn();
+    else fn = p.NV == 2 ? K<T, 1, 2>::fn() : p.NV == 4 ? K<T, 1, 4>::fn() : K<T, 1, 8>::fn();
     a.G = p.G;
     void *args[] = {&a};
     return launch_pdl(fn, dim3(static_cast<unsigned>(p.ctas)), dim3(static_cast<unsigned>(p.threads)), smem, s, args);
@@ -561,29 +431,41 @@ cudaError_t launch_columns(NormColumnArgs a, cudaStream_t s)
 
 } // namespace
 
-cudaError_t launch_norm_before(const NormBeforeArgs &a, int type, int vec, int, cudaStream_t s)
+cudaError_t launch_norm_before(const NormBeforeArgs &a, int type, int vec, int sm_count, cudaStream_t s)
 {
     const bool wide = vec * type_size(type) == 16;
-    const RowPlan p = plan_rows(vec, wide, a.m, a.d, false, int64_t(1) << 30);
+    const RowPlan p = plan_rows(vec, wide, a.m, a.d, false, sm_count);
     return launch_rows<BeforeKernel>(type, p, wide, a, 0, s);
 }
 
-cudaError_t launch_norm_after(const NormAfterArgs &a, int type, int vec, int, cudaStream_t s)
+cudaError_t launch_norm_after(const NormAfterArgs &a, int type, int vec, int sm_count, cudaStream_t s)
 {
     const bool wide = vec * type_size(type) == 16;
-    const RowPlan p = plan_rows(vec, wide, a.m, a.d, false, int64_t(1) << 30);
+    NormStreamPlan sp;
+    if (wide && plan_norm_stream(a.m, a.d, type, a.gate_kind == Q4_GATE_FULL ? 3 : 2, sm_count, &sp))
+        return launch_norm_after_stream(sp, a, type, s);
+    const RowPlan p = plan_rows(vec, wide, a.m, a.d, false, sm_count);
     return launch_rows<AfterKernel>(type, p, wide, a, 0, s);
 }
 
 cudaError_t launch_norm_before_bwd(const NormBeforeBwdArgs &a, float *dw, int type, int vec, int sm_count, cudaStream_t s)
 {
     const bool wide = vec * type_size(type) == 16;
-    const RowPlan p = plan_rows(vec, wide, a.m, a.d, true, std::min<int64_t>(kNormPartials, 4 * static_cast<int64_t>(sm_count)));
-    cudaError_t e = launch_rows<BeforeBwdKernel>(type, p, wide, a, partial_smem(p), s);
+    NormStreamPlan sp;
+    cudaError_t e;
+    int64_t ctas;
+    if (wide && plan_norm_stream(a.m, a.d, type, a.dR ? 3 : 2, sm_count, &sp)) {
+        e = launch_norm_before_bwd_stream(sp, a, type, s);
+        ctas = sp.ctas;
+    } else {
+        const RowPlan p = plan_rows(vec, wide, a.m, a.d, true, sm_count);
+        e = launch_rows<BeforeBwdKernel>(type, p, wide, a, partial_smem(p), s);
+        ctas = p.ctas;
+    }
     if (e != cudaSuccess || !dw) return e;
     NormColumnArgs c{};
     c.partials = a.partials;
-    c.rows = static_cast<int>(p.ctas);
+    c.rows = static_cast<int>(ctas);
     c.d = a.d;
     c.scale = 1.0f;
     c.dw = dw;
@@ -593,12 +475,21 @@ cudaError_t launch_norm_before_bwd(const NormBeforeBwdArgs &a, float *dw, int ty
 cudaError_t launch_norm_after_bwd(const NormAfterBwdArgs &a, float *dw, int type, int vec, int sm_count, cudaStream_t s)
 {
     const bool wide = vec * type_size(type) == 16;
-    const RowPlan p = plan_rows(vec, wide, a.m, a.d, true, std::min<int64_t>(kNormPartials, 4 * static_cast<int64_t>(sm_count)));
-    cudaError_t e = launch_rows<AfterBwdKernel>(type, p, wide, a, partial_smem(p), s);
+    NormStreamPlan sp;
+    cudaError_t e;
+    int64_t ctas;
+    if (wide && plan_norm_stream(a.m, a.d, type, a.gate_kind == Q4_GATE_FULL ? 3 : 2, sm_count, &sp)) {
+        e = launch_norm_after_bwd_stream(sp, a, type, s);
+        ctas = sp.ctas;
+    } else {
+        const RowPlan p = plan_rows(vec, wide, a.m, a.d, true, sm_count);
+        e = launch_rows<AfterBwdKernel>(type, p, wide, a, partial_smem(p), s);
+        ctas = p.ctas;
+    }
     if (e != cudaSuccess || !a.partials) return e;
     NormColumnArgs c{};
     c.partials = a.partials;
-    c.rows = static_cast<int>(p.ctas);
+    c.rows = static_cast<int>(ctas);
     c.d = a.d;
     c.scale = a.scale;
     c.dw = dw;

@@ -43,6 +43,8 @@ struct NormAfterArgs {
     int gate_kind;
     float scale, eps;
     int64_t m, d;
+    int *status;
+    uint64_t wait_ns;
     int G;
 };
 
@@ -54,6 +56,8 @@ struct NormBeforeBwdArgs {
     float w_off, eps;
     float *partials;           // nullptr: no column sums are wanted
     int64_t m, d;
+    int *status;
+    uint64_t wait_ns;
     int G;
 };
 
@@ -67,6 +71,8 @@ struct NormAfterBwdArgs {
     float scale, eps;
     float *partials;
     int64_t m, d;
+    int *status;
+    uint64_t wait_ns;
     int G;
 };
 
@@ -79,6 +85,22 @@ struct NormColumnArgs {
     const float *gate, *w;
     float w_off;
 };
+
+// The streaming kernels: a CTA per row in turn, the rows of up to `matrices`
+// inputs copied ahead into a ring in shared memory.
+struct NormStreamPlan {
+    int NV = 0;            // 16-byte vectors a thread
+    int G = 0;             // threads
+    int stages = 0;
+    int64_t ctas = 0;
+    size_t smem = 0;
+};
+// False where they do not apply: rows that are no multiple of 16 bytes, short
+// or very long ones, few rows.
+bool plan_norm_stream(int64_t m, int64_t d, int type, int matrices, int sm_count, NormStreamPlan *plan);
+cudaError_t launch_norm_after_stream(const NormStreamPlan &p, const NormAfterArgs &a, int type, cudaStream_t s);
+cudaError_t launch_norm_before_bwd_stream(const NormStreamPlan &p, const NormBeforeBwdArgs &a, int type, cudaStream_t s);
+cudaError_t launch_norm_after_bwd_stream(const NormStreamPlan &p, const NormAfterBwdArgs &a, int type, cudaStream_t s);
 
 // `vec`: elements of one access; every row of every matrix starts on a
 // multiple of vec elements' bytes.
