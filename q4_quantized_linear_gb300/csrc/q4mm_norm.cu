@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
     const RowGroup g = row_group(a.G);
     RowReducer red{rbuf, a.G / 32};
     const int d = static_cast<int>(a.d);
-    const Channels<V, NV, false> wo;
+    Channels<V, NV, false> wo;
     for (int64_t row = g.row; row < a.m; row += g.step) {
         const T *xr = static_cast<const T *>(a.X) + row * a.ldx;
         Pack<T, V> x[NV];
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
             for (int j = 0; j < V; ++j) w[j] *= gc[j];
         }
     };
-    const Channels<V, NV, false> wa, wo;
+    Channels<V, NV, false> wa, wo;
     for (int64_t row = g.row; row < a.m; row += g.step) {
         const T *br = static_cast<const T *>(a.B) + row * a.ldb, *rr = static_cast<const T *>(a.R) + row * a.ldr;
         const T *gr = full ? static_cast<const T *>(a.gate) + row * a.ldg : nullptr;
