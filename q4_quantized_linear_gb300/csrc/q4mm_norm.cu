@@ -38,12 +38,17 @@ __host__ __device__ constexpr int max_threads(int NV) { return NV == 1 ? 1024 : 
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_before_kernel(const NormBeforeArgs a)
 {
-    __shared__ float rbuf[2 * 96];
+    __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
     const RowGroup g = row_group(a.G);
-    RowReducer red{rbuf, a.G / 32};
+    RowReducer red{rbuf, a.G / 32, false};
+    if (red.warps > 1) {
+        red.clear(static_cast<int>(blockDim.x));
+        __syncthreads();
+    }
     const int d = static_cast<int>(a.d);
+    const float inv_d = 1.0f / static_cast<float>(d);
     Channels<V, NV, false> wo;
     for (int64_t row = g.row; row < a.m; row += g.step) {
         const T *xr = static_cast<const T *>(a.X) + row * a.ldx;
@@ -56,7 +61,7 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
             for (int i = 0; i < NV; ++i) s[0] = square_sum<T, V>(x[i], s[0]);
             for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) s[0] = square_sum<T, V>(load_pack<T, V>(xr, c, d), s[0]);
             red.sum(s);
-            r = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.eps);
+            r = rms_factor(s[0], inv_d, a.eps);
         }
         write_normed<T, V, NV, false>(x, [&](int c) { return load_pack<T, V>(xr, c, d); }, r, a.out, wo, row, g, d, red);
     }
@@ -65,12 +70,17 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_after_kernel(const NormAfterArgs a)
 {
-    __shared__ float rbuf[2 * 96];
+    __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
     const RowGroup g = row_group(a.G);
-    RowReducer red{rbuf, a.G / 32};
+    RowReducer red{rbuf, a.G / 32, false};
+    if (red.warps > 1) {
+        red.clear(static_cast<int>(blockDim.x));
+        __syncthreads();
+    }
     const int d = static_cast<int>(a.d), rest = (NV * g.G + g.t) * V;
+    const float inv_d = 1.0f / static_cast<float>(d);
     const bool full = a.gate_kind == Q4_GATE_FULL;
     const auto after_at = [&](int c, float (&w)[V]) {
         channel_weights<V>(a.w, a.w_off, c, d, w);
@@ -95,7 +105,7 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
         for (int i = 0; i < NV; ++i) s[0] = square_sum<T, V>(b[i], s[0]);
         for (int c = rest; c < d; c += g.G * V) s[0] = square_sum<T, V>(load_pack<T, V>(br, c, d), s[0]);
         red.sum(s);
-        float q = a.scale / sqrtf(s[0] / static_cast<float>(d) + a.eps);
+        float q = a.scale * rms_factor(s[0], inv_d, a.eps);
         if (a.gate_kind == Q4_GATE_TOKEN) q *= static_cast<const float *>(a.gate)[row];
         // y = r + q g b (o + w), stored; the sum of its squares as stored
         s[0] = 0.0f;
@@ -123,7 +133,7 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
             join(-1, load_pack<T, V>(rr, c, d), load_pack<T, V>(br, c, d), full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>(), c);
         if (a.out.H) {
             red.sum(s);
-            const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.out_eps);
+            const float rho = rms_factor(s[0], inv_d, a.out_eps);
             write_normed<T, V, NV, false>(r, [&](int c) { return load_pack<T, V>(yr, c, d); }, rho, a.out, wo, row, g, d, red);
         }
     }
@@ -134,12 +144,17 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
 template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm_before_bwd_kernel(const NormBeforeBwdArgs a)
 {
     extern __shared__ float dsmem[];
-    __shared__ float rbuf[2 * 96];
+    __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
     const RowGroup g = row_group(a.G);
-    RowReducer red{rbuf, a.G / 32};
+    RowReducer red{rbuf, a.G / 32, false};
+    if (red.warps > 1) {
+        red.clear(static_cast<int>(blockDim.x));
+        __syncthreads();
+    }
     const int d = static_cast<int>(a.d);
+    const float inv_d = 1.0f / static_cast<float>(d);
     const T *X = static_cast<const T *>(a.X), *DH = static_cast<const T *>(a.dH), *DR = static_cast<const T *>(a.dR);
     float acc[NV][V];
 #pragma unroll
@@ -177,8 +192,8 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         }
         for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) sums(-1, load_pack<T, V>(xr, c, d), load_pack<T, V>(hr, c, d), c);
         red.sum(s);
-        const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.eps);
-        const float mean = rho * s[1] / static_cast<float>(d);
+        const float rho = rms_factor(s[0], inv_d, a.eps);
+        const float mean = rho * s[1] * inv_d;
         const auto one = [&](int i, int c, const Pack<T, V> &xv, const Pack<T, V> &hv, const Pack<T, V> &rv, float (&col)[V]) {
             float w[V];
             if (i < 0) at(c, w);
@@ -217,12 +232,17 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
 template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm_after_bwd_kernel(const NormAfterBwdArgs a)
 {
     extern __shared__ float dsmem[];
-    __shared__ float rbuf[2 * 96];
+    __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
     const RowGroup g = row_group(a.G);
-    RowReducer red{rbuf, a.G / 32};
+    RowReducer red{rbuf, a.G / 32, false};
+    if (red.warps > 1) {
+        red.clear(static_cast<int>(blockDim.x));
+        __syncthreads();
+    }
     const int d = static_cast<int>(a.d);
+    const float inv_d = 1.0f / static_cast<float>(d);
     const bool full = a.gate_kind == Q4_GATE_FULL, token = a.gate_kind == Q4_GATE_TOKEN;
     const bool channel = a.gate_kind == Q4_GATE_CHANNEL;
     const T *B = static_cast<const T *>(a.B), *DY = static_cast<const T *>(a.dY), *Gt = static_cast<const T *>(a.gate);
@@ -276,9 +296,9 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V)
             sums(-1, c, load_pack<T, V>(br, c, d), load_pack<T, V>(dyr, c, d), full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>());
         red.sum(s);
-        const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.eps);
+        const float rho = rms_factor(s[0], inv_d, a.eps);
         if (token && a.dgate && g.t == 0) static_cast<float *>(a.dgate)[row] = a.scale * rho * s[1];
-        const float mean = gtok * rho * s[1] / static_cast<float>(d);
+        const float mean = gtok * rho * s[1] * inv_d;
         const float q = a.scale * rho;
         const auto one = [&](int i, int c, const Pack<T, V> &bv, const Pack<T, V> &yv, const Pack<T, V> &gv, float (&col)[V]) {
             float w[V], o[V], og[V];
@@ -328,7 +348,13 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const NormColumnArgs a
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float s = 0.0f;
     if (c < a.d)
-        for (int p = warp; p < a.rows; p += 32) s += a.partials[p * a.d + c];
+        for (int p = warp; p < a.rows; p += 32 * 4) {   // four loads in flight
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = p + 32 * i < a.rows ? a.partials[(p + 32 * i) * a.d + c] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s += v[i];
+        }
     part[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || c >= a.d) return;

@@ -1,12 +1,15 @@
 // q4mm_norm_stream.cu -- the norms over many rows of whole 16-byte vectors (the
-// mathematics is in q4mm_norm.cu). A CTA takes rows in turn. Its first thread
+// mathematics is in q4mm_norm.cu). A CTA takes rows in turn. A warp of its own
 // keeps bulk copies of the rows to come in flight, into a ring in shared memory,
 // so the memory is busy while a row's sums meet at a barrier; loads into
 // registers leave it idle then, and there are not enough registers to load far
-// ahead. Both passes over a row, its sums and its results, read it from shared
-// memory; past the barrier of a row's first sum every thread is done with the
-// row before, whose slot is then refilled. The channels' weights, and backward
-// their sums, stay in registers over the rows.
+// ahead. (Issued by one of the row's threads, the copies held up the others at
+// each row's barrier.)
+//   What bounds a CTA then is the way of a row: sums, barrier, root, results.
+// So two rows go that way at once, sharing their barriers and the channels'
+// weights and, backward, their column sums, which stay in registers over the
+// rows. Both passes over a row, its sums and its results, read it from shared
+// memory; then the row's warps release its slot.
 //   Every wait is bounded: after one that ran out the status word says so, the
 // CTA goes through its rows without waiting (its results are void) and leaves
 // when the copies in flight have landed.
@@ -21,10 +24,12 @@ namespace {
 constexpr int kErrTimeout = 5;
 constexpr int kMatrices = 3;
 
-// The rows first, first + step, ... of up to three matrices.
+constexpr int kRows = 1;             // rows that a CTA works on at once
+
+// The rows blockIdx.x, + gridDim.x, ... of up to three matrices.
 struct RowStream {
     uint8_t *buf;
-    uint64_t *full;
+    uint64_t *full, *empty;          // [stages] each
     int stages, used;
     uint32_t bytes;                  // of a row
     const uint8_t *src[kMatrices];
@@ -34,24 +39,35 @@ struct RowStream {
     uint64_t wait_ns;
     bool dead;
 
-    __device__ __forceinline__ void issue(int64_t row, int slot)
-    {
-        mbar_arrive_expect_tx(&full[slot], bytes * used);
-        uint8_t *dst = buf + static_cast<size_t>(slot) * used * bytes;
-        for (int i = 0; i < used; ++i) bulk_g2s(dst + static_cast<size_t>(i) * bytes, src[i] + row * ld[i], bytes, &full[slot]);
-    }
-    __device__ __forceinline__ void start()
+    // the whole CTA, once
+    __device__ __forceinline__ void start(int row_warps)
     {
         if (threadIdx.x == 0) {
-            for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+            for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], row_warps);
             fence_barrier_init();
         }
         __syncthreads();
-        if (threadIdx.x == 0)
-            for (int i = 0; i < stages; ++i) {
-                const int64_t row = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
-                if (row < m) issue(row, i);
+    }
+    // the copying warp's one thread: every row of the CTA; waits for what is in
+    // flight if it has to give up
+    __device__ __forceinline__ void copy_rows()
+    {
+        int slot = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
+            if (issued >= stages && !mbar_wait(&empty[slot], phase ^ 1u, wait_ns)) {
+                record_status(status, kErrTimeout);
+                for (int64_t k = issued - stages; k < issued; ++k)
+                    mbar_wait(&full[k % stages], static_cast<uint32_t>(k / stages) & 1u, wait_ns);
+                return;
             }
+            mbar_arrive_expect_tx(&full[slot], bytes * used);
+            uint8_t *dst = buf + static_cast<size_t>(slot) * used * bytes;
+            for (int i = 0; i < used; ++i) bulk_g2s(dst + static_cast<size_t>(i) * bytes, src[i] + row * ld[i], bytes, &full[slot]);
+            ++issued;
+            if (++slot == stages) slot = 0, phase ^= 1u;
+        }
     }
     __device__ __forceinline__ void wait(int slot, uint32_t phase)
     {
@@ -60,22 +76,11 @@ struct RowStream {
             record_status(status, kErrTimeout);
         }
     }
-    // past the barrier of `row`'s first sum: refill the slot of the row before
-    __device__ __forceinline__ void refill_before(int64_t row, int slot)
+    // a row's warp has read the slot for the last time
+    __device__ __forceinline__ void release(int slot)
     {
-        const int64_t next = row + static_cast<int64_t>(stages - 1) * gridDim.x;
-        if (threadIdx.x == 0 && row >= static_cast<int64_t>(gridDim.x) && next < m && !dead)
-            issue(next, slot == 0 ? stages - 1 : slot - 1);
-    }
-    // after a timeout: what is still landing
-    __device__ __forceinline__ void finish(int slot, uint32_t phase)
-    {
-        if (!__syncthreads_or(dead ? 1 : 0) || threadIdx.x != 0) return;
-        for (int i = 0; i < stages; ++i) {
-            // a slot's last copy completes the phase that its wait would have been for
-            mbar_wait(&full[slot], phase, wait_ns);
-            if (++slot == stages) slot = 0, phase ^= 1u;
-        }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[slot]);
     }
     // the vector at element c
     template <typename T, int V> __device__ __forceinline__ Pack<T, V> get(int slot, int matrix, int c) const
@@ -97,42 +102,77 @@ __device__ __forceinline__ RowStream make_stream(uint8_t *smem, int64_t m, int64
     r.used = used;
     r.buf = smem;
     r.full = reinterpret_cast<uint64_t *>(smem + static_cast<size_t>(stages) * used * r.bytes);
+    r.empty = r.full + stages;
     r.m = m;
     r.status = status;
     r.wait_ns = wait_ns;
     return r;
 }
 
-// Slot and phase of the row being worked on.
+// The weights of vector i as pairs.
+template <int V, int NV, typename F>
+__device__ __forceinline__ void weight_pairs(const Channels<V, NV, true> &ch, int i, int c, F at, F2 (&w)[V / 2])
+{
+    float f[V];
+    ch.get(i, c, at, f);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) w[j] = f2(f[2 * j], f[2 * j + 1]);
+}
+
+// The rows being worked on: their numbers, slots and phases.
 struct Turn {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int stages)
+    int64_t row[kRows];
+    int slot[kRows];
+    uint32_t phase[kRows];
+    int stages;
+    int64_t m;
+    __device__ __forceinline__ Turn(int stages_, int64_t m_) : stages(stages_), m(m_)
     {
-        if (++slot == stages) slot = 0, phase ^= 1u;
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            row[q] = blockIdx.x + static_cast<int64_t>(q) * gridDim.x;
+            slot[q] = q % stages;
+            phase[q] = static_cast<uint32_t>(q / stages) & 1u;
+        }
+    }
+    __device__ __forceinline__ bool has(int q) const { return row[q] < m; }
+    __device__ __forceinline__ void next()
+    {
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            row[q] += static_cast<int64_t>(kRows) * gridDim.x;
+            slot[q] += kRows;
+            while (slot[q] >= stages) slot[q] -= stages, phase[q] ^= 1u;
+        }
     }
 };
 
-// Up to 256 threads three CTAs fit on an SM's registers, else one of 512.
-#define Q4_STREAM_BOUNDS __launch_bounds__(BIG ? 512 : 256, BIG ? 1 : 3)
+// Threads of rows and a warp that copies; two CTAs of up to 256 fit on an SM's
+// registers, or one of 512.
+#define Q4_STREAM_BOUNDS __launch_bounds__((BIG ? 512 : 256) + 32, BIG ? 1 : 2)
 
-template <typename T, int NV, bool BIG>
+template <typename T, int NV, bool BIG, bool full>
 __global__ void Q4_STREAM_BOUNDS norm_after_stream_kernel(const NormAfterArgs a, int stages)
 {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float rbuf[2 * 96];
+    __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
-    const bool full = a.gate_kind == Q4_GATE_FULL;
     const int d = static_cast<int>(a.d);
+    const float inv_d = 1.0f / static_cast<float>(d);
     RowStream rs = make_stream<T>(smem, a.m, a.d, stages, full ? 3 : 2, a.status, a.wait_ns);
     rs.src[0] = static_cast<const uint8_t *>(a.B), rs.ld[0] = a.ldb * sizeof(T);
     rs.src[1] = static_cast<const uint8_t *>(a.R), rs.ld[1] = a.ldr * sizeof(T);
     rs.src[2] = static_cast<const uint8_t *>(a.gate), rs.ld[2] = a.ldg * sizeof(T);
-    rs.start();
-    const RowGroup g = row_group(static_cast<int>(blockDim.x));
-    RowReducer red{rbuf, static_cast<int>(blockDim.x) / 32};
+    RowReducer red{rbuf, a.G / 32, true};
+    red.clear(static_cast<int>(blockDim.x));
+    rs.start(a.G / 32);
+    if (static_cast<int>(threadIdx.x) >= a.G) {
+        if (static_cast<int>(threadIdx.x) == a.G) rs.copy_rows();
+        return;
+    }
+    const RowGroup g{static_cast<int>(threadIdx.x), a.G, blockIdx.x, gridDim.x};
     const auto after_at = [&](int c, float (&w)[V]) {
         channel_weights<V>(a.w, a.w_off, c, d, w);
         if (a.gate_kind == Q4_GATE_CHANNEL) {
@@ -145,49 +185,67 @@ __global__ void Q4_STREAM_BOUNDS norm_after_stream_kernel(const NormAfterArgs a,
     Channels<V, NV, true> wa, wo;
     wa.fill(g, after_at);
     if (a.out.H) wo.fill(g, [&](int c, float (&w)[V]) { channel_weights<V>(a.out.w, a.out.w_off, c, d, w); });
-    Turn turn;
-    for (int64_t row = g.row; row < a.m; row += g.step, turn.next(stages)) {
-        rs.wait(turn.slot, turn.phase);
-        float s[1] = {0.0f};
+    for (Turn turn(stages, a.m); turn.has(0); turn.next()) {
+        float s[kRows];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c < d) s[0] = square_sum<T, V>(rs.get<T, V>(turn.slot, 0, c), s[0]);
+        for (int q = 0; q < kRows; ++q) {
+            s[q] = 0.0f;
+            if (!turn.has(q)) continue;
+            rs.wait(turn.slot[q], turn.phase[q]);
+            F2 sq = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * g.G + g.t) * V;
+                if (c >= d) continue;
+                const Pack<T, V> bv = rs.get<T, V>(turn.slot[q], 0, c);
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) sq = f2_fma(pair(bv, j), pair(bv, j), sq);
+            }
+            s[q] = f2_sum(sq);
         }
         red.sum(s);
-        rs.refill_before(row, turn.slot);
-        float q = a.scale / sqrtf(s[0] / static_cast<float>(d) + a.eps);
-        if (a.gate_kind == Q4_GATE_TOKEN) q *= static_cast<const float *>(a.gate)[row];
-        T *yr = static_cast<T *>(a.Y) + row * a.ldy;
-        s[0] = 0.0f;
-        Pack<T, V> r[NV];
+        Pack<T, V> r[kRows][NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c >= d) continue;
-            const Pack<T, V> bv = rs.get<T, V>(turn.slot, 0, c), rv = rs.get<T, V>(turn.slot, 1, c);
-            float w[V], y[V];
-            wa.get(i, c, after_at, w);
+        for (int q = 0; q < kRows; ++q) {
+            float f = a.scale * rms_factor(s[q], inv_d, a.eps);
+            s[q] = 0.0f;
+            if (!turn.has(q)) continue;
+            if (a.gate_kind == Q4_GATE_TOKEN) f *= static_cast<const float *>(a.gate)[turn.row[q]];
+            T *yr = static_cast<T *>(a.Y) + turn.row[q] * a.ldy;
+            const F2 ff = f2(f, f);
+            F2 sq = 0;
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[j] = elem(bv, j) * q * w[j];
-            if (full) {
-                const Pack<T, V> gv = rs.get<T, V>(turn.slot, 2, c);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * g.G + g.t) * V;
+                if (c >= d) continue;
+                const Pack<T, V> bv = rs.get<T, V>(turn.slot[q], 0, c), rv = rs.get<T, V>(turn.slot[q], 1, c);
+                F2 w[V / 2], y[V / 2];
+                weight_pairs<V, NV>(wa, i, c, after_at, w);
+                if constexpr (full) {
+                    const Pack<T, V> gv = rs.get<T, V>(turn.slot[q], 2, c);
 #pragma unroll
-                for (int j = 0; j < V; ++j) y[j] *= elem(gv, j);
+                    for (int j = 0; j < V / 2; ++j) w[j] = f2_mul(w[j], pair(gv, j));
+                }
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) y[j] = f2_fma(f2_mul(pair(bv, j), ff), w[j], pair(rv, j));
+                r[q][i] = pack_pairs<T, V>(y);
+                store_pack<T, V>(yr, c, d, r[q][i]);
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) sq = f2_fma(pair(r[q][i], j), pair(r[q][i], j), sq);
             }
-#pragma unroll
-            for (int j = 0; j < V; ++j) y[j] += elem(rv, j);
-            r[i] = pack_of<T, V>(y);
-            store_pack<T, V>(yr, c, d, r[i]);
-            s[0] = square_sum<T, V>(r[i], s[0]);
+            s[q] = f2_sum(sq);
+            rs.release(turn.slot[q]);
         }
-        if (a.out.H) {
-            red.sum(s);
-            const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.out_eps);
-            write_normed<T, V, NV, true>(r, [&](int c) { return load_pack<T, V>(yr, c, d); }, rho, a.out, wo, row, g, d, red);
+        if (!a.out.H) continue;
+        red.sum(s);
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            if (!turn.has(q)) continue;
+            const T *yr = static_cast<const T *>(a.Y) + turn.row[q] * a.ldy;
+            write_normed<T, V, NV, true>(r[q], [&](int c) { return load_pack<T, V>(yr, c, d); }, rms_factor(s[q], inv_d, a.out_eps),
+                                         a.out, wo, turn.row[q], g, d, red);
         }
     }
-    rs.finish(turn.slot, turn.phase);
 }
 
 template <typename T, int NV, bool BIG>
@@ -195,87 +253,116 @@ __global__ void Q4_STREAM_BOUNDS norm_before_bwd_stream_kernel(const NormBeforeB
 {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float rbuf[2 * 96];
+    __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
     const bool residual = a.dR != nullptr;
     const int d = static_cast<int>(a.d);
+    const float inv_d = 1.0f / static_cast<float>(d);
     RowStream rs = make_stream<T>(smem, a.m, a.d, stages, residual ? 3 : 2, a.status, a.wait_ns);
     rs.src[0] = static_cast<const uint8_t *>(a.X), rs.ld[0] = a.ldx * sizeof(T);
     rs.src[1] = static_cast<const uint8_t *>(a.dH), rs.ld[1] = a.lddh * sizeof(T);
     rs.src[2] = static_cast<const uint8_t *>(a.dR), rs.ld[2] = a.lddr * sizeof(T);
-    rs.start();
-    const RowGroup g = row_group(static_cast<int>(blockDim.x));
-    RowReducer red{rbuf, static_cast<int>(blockDim.x) / 32};
+    RowReducer red{rbuf, a.G / 32, true};
+    red.clear(static_cast<int>(blockDim.x));
+    rs.start(a.G / 32);
+    if (static_cast<int>(threadIdx.x) >= a.G) {
+        if (static_cast<int>(threadIdx.x) == a.G) rs.copy_rows();
+        return;
+    }
+    const RowGroup g{static_cast<int>(threadIdx.x), a.G, blockIdx.x, gridDim.x};
     const auto at = [&](int c, float (&w)[V]) { channel_weights<V>(a.w, a.w_off, c, d, w); };
     Channels<V, NV, true> wc;
     wc.fill(g, at);
-    float acc[NV][V] = {};
-    Turn turn;
-    for (int64_t row = g.row; row < a.m; row += g.step, turn.next(stages)) {
-        rs.wait(turn.slot, turn.phase);
-        float s[2] = {0.0f, 0.0f};
+    F2 acc[NV][V / 2] = {};
+    for (Turn turn(stages, a.m); turn.has(0); turn.next()) {
+        float s[2 * kRows];   // of x^2 and of dn x, a row each
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c >= d) continue;
-            const Pack<T, V> xv = rs.get<T, V>(turn.slot, 0, c), hv = rs.get<T, V>(turn.slot, 1, c);
-            float w[V];
-            wc.get(i, c, at, w);
+        for (int q = 0; q < kRows; ++q) {
+            s[2 * q] = s[2 * q + 1] = 0.0f;
+            if (!turn.has(q)) continue;
+            rs.wait(turn.slot[q], turn.phase[q]);
+            F2 sq = 0, dot = 0;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float f = elem(xv, j);
-                s[0] = fmaf(f, f, s[0]);
-                s[1] = fmaf(elem(hv, j) * w[j], f, s[1]);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * g.G + g.t) * V;
+                if (c >= d) continue;
+                const Pack<T, V> xv = rs.get<T, V>(turn.slot[q], 0, c), hv = rs.get<T, V>(turn.slot[q], 1, c);
+                F2 w[V / 2];
+                weight_pairs<V, NV>(wc, i, c, at, w);
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    const F2 f = pair(xv, j);
+                    sq = f2_fma(f, f, sq);
+                    dot = f2_fma(f2_mul(pair(hv, j), w[j]), f, dot);
+                }
             }
+            s[2 * q] = f2_sum(sq), s[2 * q + 1] = f2_sum(dot);
         }
         red.sum(s);
-        rs.refill_before(row, turn.slot);
-        const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.eps);
-        const float mean = rho * s[1] / static_cast<float>(d);
-        T *out = static_cast<T *>(a.dX) + row * a.lddx;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c >= d) continue;
-            const Pack<T, V> xv = rs.get<T, V>(turn.slot, 0, c), hv = rs.get<T, V>(turn.slot, 1, c);
-            float w[V], o[V];
-            wc.get(i, c, at, w);
+        for (int q = 0; q < kRows; ++q) {
+            if (!turn.has(q)) continue;
+            // dx = rho dn - x rho^2 mean [+ dr], mean = rho sum(dn x) / d
+            const float rho = rms_factor(s[2 * q], inv_d, a.eps), mean = rho * s[2 * q + 1] * inv_d;
+            const F2 rho2 = f2(rho, rho), back = f2(-rho * mean * rho, -rho * mean * rho);
+            T *out = static_cast<T *>(a.dX) + turn.row[q] * a.lddx;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float u = elem(xv, j) * rho, h = elem(hv, j);
-                acc[i][j] = fmaf(h, u, acc[i][j]);
-                o[j] = rho * (h * w[j] - u * mean);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * g.G + g.t) * V;
+                if (c >= d) continue;
+                const Pack<T, V> xv = rs.get<T, V>(turn.slot[q], 0, c), hv = rs.get<T, V>(turn.slot[q], 1, c);
+                F2 w[V / 2], o[V / 2];
+                weight_pairs<V, NV>(wc, i, c, at, w);
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    const F2 x = pair(xv, j), h = f2_mul(pair(hv, j), rho2);
+                    acc[i][j] = f2_fma(h, x, acc[i][j]);
+                    o[j] = f2_fma(h, w[j], f2_mul(x, back));
+                }
+                if (residual) {
+                    const Pack<T, V> rv = rs.get<T, V>(turn.slot[q], 2, c);
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j) o[j] = f2_fma(o[j], f2(1.0f, 1.0f), pair(rv, j));
+                }
+                store_pack<T, V>(out, c, d, pack_pairs<T, V>(o));
             }
-            if (residual) {
-                const Pack<T, V> rv = rs.get<T, V>(turn.slot, 2, c);
-#pragma unroll
-                for (int j = 0; j < V; ++j) o[j] += elem(rv, j);
-            }
-            store_pack<T, V>(out, c, d, pack_of<T, V>(o));
+            rs.release(turn.slot[q]);
         }
     }
-    rs.finish(turn.slot, turn.phase);
-    if (a.partials) write_partials<V, NV>(acc, a.partials, g, d, nullptr);
+    if (a.partials) {
+        float sums[NV][V];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) f2_split(acc[i][j], sums[i][2 * j], sums[i][2 * j + 1]);
+        write_partials<V, NV>(sums, a.partials, g, d, nullptr);
+    }
 }
 
-template <typename T, int NV, bool BIG>
+template <typename T, int NV, bool BIG, bool full>
 __global__ void Q4_STREAM_BOUNDS norm_after_bwd_stream_kernel(const NormAfterBwdArgs a, int stages)
 {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float rbuf[2 * 96];
+    __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
-    const bool full = a.gate_kind == Q4_GATE_FULL, token = a.gate_kind == Q4_GATE_TOKEN;
+    const bool token = a.gate_kind == Q4_GATE_TOKEN;
     const int d = static_cast<int>(a.d);
+    const float inv_d = 1.0f / static_cast<float>(d);
     RowStream rs = make_stream<T>(smem, a.m, a.d, stages, full ? 3 : 2, a.status, a.wait_ns);
     rs.src[0] = static_cast<const uint8_t *>(a.B), rs.ld[0] = a.ldb * sizeof(T);
     rs.src[1] = static_cast<const uint8_t *>(a.dY), rs.ld[1] = a.lddy * sizeof(T);
     rs.src[2] = static_cast<const uint8_t *>(a.gate), rs.ld[2] = a.ldg * sizeof(T);
-    rs.start();
-    const RowGroup g = row_group(static_cast<int>(blockDim.x));
-    RowReducer red{rbuf, static_cast<int>(blockDim.x) / 32};
+    RowReducer red{rbuf, a.G / 32, true};
+    red.clear(static_cast<int>(blockDim.x));
+    rs.start(a.G / 32);
+    if (static_cast<int>(threadIdx.x) >= a.G) {
+        if (static_cast<int>(threadIdx.x) == a.G) rs.copy_rows();
+        return;
+    }
+    const RowGroup g{static_cast<int>(threadIdx.x), a.G, blockIdx.x, gridDim.x};
     // (o + w), times the channel's gate
     const auto at = [&](int c, float (&w)[V]) {
         channel_weights<V>(a.w, a.w_off, c, d, w);
@@ -288,95 +375,129 @@ __global__ void Q4_STREAM_BOUNDS norm_after_bwd_stream_kernel(const NormAfterBwd
     };
     Channels<V, NV, true> wc;
     wc.fill(g, at);
-    float acc[NV][V] = {};
-    Turn turn;
-    for (int64_t row = g.row; row < a.m; row += g.step, turn.next(stages)) {
-        const float gtok = token ? static_cast<const float *>(a.gate)[row] : 1.0f;
-        rs.wait(turn.slot, turn.phase);
-        // sums of b^2 and of g w dy b (a token's gate is taken out: its gradient is
-        // that sum)
-        float s[2] = {0.0f, 0.0f};
+    F2 acc[NV][V / 2] = {};
+    for (Turn turn(stages, a.m); turn.has(0); turn.next()) {
+        // sums of b^2 and of g w dy b, a row each (a token's gate is taken out: its
+        // gradient is that sum)
+        float s[2 * kRows];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c >= d) continue;
-            const Pack<T, V> bv = rs.get<T, V>(turn.slot, 0, c), yv = rs.get<T, V>(turn.slot, 1, c);
-            float w[V];
-            wc.get(i, c, at, w);
-            if (full) {
-                const Pack<T, V> gv = rs.get<T, V>(turn.slot, 2, c);
+        for (int q = 0; q < kRows; ++q) {
+            s[2 * q] = s[2 * q + 1] = 0.0f;
+            if (!turn.has(q)) continue;
+            rs.wait(turn.slot[q], turn.phase[q]);
+            F2 sq = 0, dot = 0;
 #pragma unroll
-                for (int j = 0; j < V; ++j) w[j] *= elem(gv, j);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * g.G + g.t) * V;
+                if (c >= d) continue;
+                const Pack<T, V> bv = rs.get<T, V>(turn.slot[q], 0, c), yv = rs.get<T, V>(turn.slot[q], 1, c);
+                F2 w[V / 2];
+                weight_pairs<V, NV>(wc, i, c, at, w);
+                if constexpr (full) {
+                    const Pack<T, V> gv = rs.get<T, V>(turn.slot[q], 2, c);
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j) w[j] = f2_mul(w[j], pair(gv, j));
+                }
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    const F2 f = pair(bv, j);
+                    sq = f2_fma(f, f, sq);
+                    dot = f2_fma(f2_mul(pair(yv, j), w[j]), f, dot);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float f = elem(bv, j);
-                s[0] = fmaf(f, f, s[0]);
-                s[1] = fmaf(elem(yv, j) * w[j], f, s[1]);
-            }
+            s[2 * q] = f2_sum(sq), s[2 * q + 1] = f2_sum(dot);
         }
         red.sum(s);
-        rs.refill_before(row, turn.slot);
-        const float rho = 1.0f / sqrtf(s[0] / static_cast<float>(d) + a.eps);
-        if (token && a.dgate && g.t == 0) static_cast<float *>(a.dgate)[row] = a.scale * rho * s[1];
-        const float mean = gtok * rho * s[1] / static_cast<float>(d), q = a.scale * rho;
-        T *out = static_cast<T *>(a.dB) + row * a.lddb;
-        T *dgr = full && a.dgate ? static_cast<T *>(a.dgate) + row * a.lddg : nullptr;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c >= d) continue;
-            const Pack<T, V> bv = rs.get<T, V>(turn.slot, 0, c), yv = rs.get<T, V>(turn.slot, 1, c);
-            float w[V], o[V];
-            wc.get(i, c, at, w);
-            if (dgr) {
+        for (int q = 0; q < kRows; ++q) {
+            if (!turn.has(q)) continue;
+            const int64_t row = turn.row[q];
+            const float gtok = token ? static_cast<const float *>(a.gate)[row] : 1.0f;
+            const float rho = rms_factor(s[2 * q], inv_d, a.eps);
+            if (token && a.dgate && g.t == 0) static_cast<float *>(a.dgate)[row] = a.scale * rho * s[2 * q + 1];
+            // db = scale rho (g dy w - u mean), u = b rho
+            const float mean = gtok * rho * s[2 * q + 1] * inv_d, k = -a.scale * rho * mean * rho;
+            const F2 rho2 = f2(gtok * rho, gtok * rho), back = f2(k, k), scale2 = f2(a.scale, a.scale);
+            T *out = static_cast<T *>(a.dB) + row * a.lddb;
+            T *dgr = full && a.dgate ? static_cast<T *>(a.dgate) + row * a.lddg : nullptr;
 #pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = a.scale * elem(yv, j) * (elem(bv, j) * rho) * w[j];
-                store_pack<T, V>(dgr, c, d, pack_of<T, V>(o));
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * g.G + g.t) * V;
+                if (c >= d) continue;
+                const Pack<T, V> bv = rs.get<T, V>(turn.slot[q], 0, c), yv = rs.get<T, V>(turn.slot[q], 1, c);
+                Pack<T, V> gv;
+                F2 w[V / 2], o[V / 2];
+                weight_pairs<V, NV>(wc, i, c, at, w);
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) w[j] = f2_mul(w[j], scale2);
+                if constexpr (full) {
+                    gv = rs.get<T, V>(turn.slot[q], 2, c);
+                    if (dgr) {
+#pragma unroll
+                        for (int j = 0; j < V / 2; ++j) o[j] = f2_mul(f2_mul(pair(yv, j), rho2), f2_mul(pair(bv, j), w[j]));
+                        store_pack<T, V>(dgr, c, d, pack_pairs<T, V>(o));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    const F2 b = pair(bv, j);
+                    F2 y = f2_mul(pair(yv, j), rho2);
+                    if constexpr (full) y = f2_mul(y, pair(gv, j));
+                    // the channel's gate, like s, is a factor of the whole column
+                    acc[i][j] = f2_fma(y, b, acc[i][j]);
+                    o[j] = f2_fma(y, w[j], f2_mul(b, back));
+                }
+                store_pack<T, V>(out, c, d, pack_pairs<T, V>(o));
             }
-            Pack<T, V> gv = zero_pack<T, V>();
-            if (full) gv = rs.get<T, V>(turn.slot, 2, c);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float u = elem(bv, j) * rho, gy = elem(yv, j) * (full ? elem(gv, j) : gtok);
-                // the channel's gate, like s, is a factor of the whole column
-                acc[i][j] = fmaf(gy, u, acc[i][j]);
-                o[j] = q * (gy * w[j] - u * mean);
-            }
-            store_pack<T, V>(out, c, d, pack_of<T, V>(o));
+            rs.release(turn.slot[q]);
         }
     }
-    rs.finish(turn.slot, turn.phase);
-    if (a.partials) write_partials<V, NV>(acc, a.partials, g, d, nullptr);
+    if (a.partials) {
+        float sums[NV][V];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) f2_split(acc[i][j], sums[i][2 * j], sums[i][2 * j + 1]);
+        write_partials<V, NV>(sums, a.partials, g, d, nullptr);
+    }
 }
 
 template <typename T, int NV, bool BIG> struct AfterStream {
-    static const void *fn() { return reinterpret_cast<const void *>(&norm_after_stream_kernel<T, NV, BIG>); }
+    static const void *fn(const NormAfterArgs &a)
+    {
+        return a.gate_kind == Q4_GATE_FULL ? reinterpret_cast<const void *>(&norm_after_stream_kernel<T, NV, BIG, true>)
+                                           : reinterpret_cast<const void *>(&norm_after_stream_kernel<T, NV, BIG, false>);
+    }
 };
 template <typename T, int NV, bool BIG> struct BeforeBwdStream {
-    static const void *fn() { return reinterpret_cast<const void *>(&norm_before_bwd_stream_kernel<T, NV, BIG>); }
+    static const void *fn(const NormBeforeBwdArgs &) { return reinterpret_cast<const void *>(&norm_before_bwd_stream_kernel<T, NV, BIG>); }
 };
 template <typename T, int NV, bool BIG> struct AfterBwdStream {
-    static const void *fn() { return reinterpret_cast<const void *>(&norm_after_bwd_stream_kernel<T, NV, BIG>); }
+    static const void *fn(const NormAfterBwdArgs &a)
+    {
+        return a.gate_kind == Q4_GATE_FULL ? reinterpret_cast<const void *>(&norm_after_bwd_stream_kernel<T, NV, BIG, true>)
+                                           : reinterpret_cast<const void *>(&norm_after_bwd_stream_kernel<T, NV, BIG, false>);
+    }
 };
 
-template <template <typename, int, bool> class K, typename T> const void *stream_fn(const NormStreamPlan &p)
+template <template <typename, int, bool> class K, typename T, typename Args>
+const void *stream_fn(const NormStreamPlan &p, const Args &a)
 {
-    if (p.G > 256) return p.NV == 2 ? K<T, 2, true>::fn() : K<T, 4, true>::fn();
-    return p.NV == 1 ? K<T, 1, false>::fn() : p.NV == 2 ? K<T, 2, false>::fn() : K<T, 4, false>::fn();
+    if (p.G > 256) return p.NV == 2 ? K<T, 2, true>::fn(a) : K<T, 4, true>::fn(a);
+    return p.NV == 1 ? K<T, 1, false>::fn(a) : p.NV == 2 ? K<T, 2, false>::fn(a) : K<T, 4, false>::fn(a);
 }
 template <template <typename, int, bool> class K, typename Args>
 cudaError_t launch_stream(const NormStreamPlan &p, Args a, int type, cudaStream_t s)
 {
-    const void *fn = type == Q4_TYPE_F32   ? stream_fn<K, float>(p)
-                     : type == Q4_TYPE_F16 ? stream_fn<K, __half>(p)
-                                           : stream_fn<K, __nv_bfloat16>(p);
+    const void *fn = type == Q4_TYPE_F32   ? stream_fn<K, float>(p, a)
+                     : type == Q4_TYPE_F16 ? stream_fn<K, __half>(p, a)
+                                           : stream_fn<K, __nv_bfloat16>(p, a);
     const cudaError_t e = set_max_smem(fn, p.smem);
     if (e != cudaSuccess) return e;
     a.G = p.G;
     int stages = p.stages;
     void *args[] = {&a, &stages};
-    return launch_pdl(fn, dim3(static_cast<unsigned>(p.ctas)), dim3(static_cast<unsigned>(p.G)), p.smem, s, args);
+    return launch_pdl(fn, dim3(static_cast<unsigned>(p.ctas)), dim3(static_cast<unsigned>(p.G + 32)), p.smem, s, args);
 }
 
 } // namespace
@@ -385,16 +506,19 @@ bool plan_norm_stream(int64_t m, int64_t d, int type, int matrices, int sm_count
 {
     const int size = type_size(type), V = 16 / size;
     const int64_t bytes = d * size, vecs = d / V;
-    // a row under 1 KB is a warp's; with fewer rows than CTAs nothing is read ahead
-    if (bytes % 16 != 0 || bytes < 1024 || vecs > 2048 || m <= 2 * sm_count) return false;
+    // shorter rows go faster several to an SM in the general kernels (16384 x 1000
+    // bf16: 41 us there, 46 here); with fewer rows than CTAs nothing is read ahead
+    if (bytes % 16 != 0 || bytes < 2048 || vecs > 2048 || m <= 2 * sm_count) return false;
     NormStreamPlan p;
     const int most = size == 2 ? 2 : 4;   // vectors whose weights stay in registers
     p.NV = vecs <= 256 ? 1 : vecs <= 512 ? 2 : vecs <= 1024 ? most : 4;
     p.G = static_cast<int>(round_up(ceil_div(vecs, p.NV), 32));
-    const size_t stage = static_cast<size_t>(matrices) * bytes + 8;
-    int per_sm = p.G > 256 ? 1 : 3;
+    const size_t stage = static_cast<size_t>(matrices) * bytes + 16;
+    // as many CTAs as the registers of their bound (224 threads' worth at 256, and
+    // so on) leave room for, and three rows ahead
+    int per_sm = p.G > 256 ? 1 : 576 / (p.G + 32);
     for (; per_sm > 0; --per_sm) {
-        p.stages = static_cast<int>(std::min<size_t>(4, (kSmemPerSM / per_sm - 2048) / stage));
+        p.stages = static_cast<int>(std::min<size_t>(6, (kSmemPerSM / per_sm - 3072) / stage));
         if (p.stages >= 3) break;
     }
     if (per_sm == 0) return false;

@@ -77,6 +77,44 @@ template <typename T, int V> __device__ __forceinline__ Pack<T, V> pack_of(const
     }
     return p;
 }
+// Two fp32 values in a register pair, and the packed arithmetic on them (each
+// half rounded once, as by itself): one issue slot for two operations.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float lo, float hi)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_split(F2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(F2 v)
+{
+    float lo, hi;
+    f2_split(v, lo, hi);
+    return lo + hi;
+}
+// Elements 2 i and 2 i + 1.
+template <typename T, int V> __device__ __forceinline__ F2 pair(const Pack<T, V> &p, int i) { return f2(elem(p, 2 * i), elem(p, 2 * i + 1)); }
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> pack_pairs(const F2 (&f)[V / 2])
+{
+    float e[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f2_split(f[i], e[2 * i], e[2 * i + 1]);
+    return pack_of<T, V>(e);
+}
+
 // V int8 codes as the bytes of their words.
 template <int V> __device__ __forceinline__ Pack<int8_t, V> pack_codes(const int (&c)[V])
 {
@@ -179,49 +217,74 @@ template <int V> __device__ __forceinline__ void load_params(const float *p, int
 
 // Sums and maxima over the G threads of a row: a shuffle tree in each warp,
 // then, where a row takes the whole CTA, the warps' values through shared
-// memory (every warp adds them in the same order, so all threads hold the same
-// bits). Two buffers in turn: a thread reaches the second use of a buffer only
-// past the barrier of the use between, which follows every read of the first.
+// memory, which every thread adds in the same order, so all hold the same bits
+// (four warps a vector load: a second shuffle tree would take three times as
+// long, and a row waits for its sums). Two buffers in turn: a
+// thread reaches the second use of a buffer only past the barrier of the use
+// between, which follows every read of the first.
+constexpr int kReduceFloats = 2 * 4 * 32;   // shared floats of a reducer
 struct RowReducer {
-    float *buf;   // [2][3][32]
+    float *buf;   // [2][4][32], 16-byte aligned
     int warps;    // warps of a row; 1: no shared memory, no barrier
+    bool part;    // the CTA has other warps too: the row's meet at a barrier of their own
     int turn = 0;
+
+    // once, by every thread of the CTA or of the row, before a barrier of theirs
+    __device__ __forceinline__ void clear(int threads) const
+    {
+        for (int i = threadIdx.x; i < kReduceFloats; i += threads) buf[i] = 0.0f;
+    }
+    __device__ __forceinline__ void meet() const
+    {
+        if (part) asm volatile("bar.sync 1, %0;" ::"r"(warps * 32) : "memory");
+        else __syncthreads();
+    }
 
     template <int N> __device__ __forceinline__ void sum(float (&v)[N])
     {
+        static_assert(N <= 4, "four sums at most");
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
         if (warps == 1) return;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        float *b = buf + turn * 96;
+        float *b = buf + turn * 128;
         turn ^= 1;
         if (lane == 0)
 #pragma unroll
             for (int i = 0; i < N; ++i) b[i * 32 + warp] = v[i];
-        __syncthreads();
+        meet();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[i] = lane < warps ? b[i * 32 + lane] : 0.0f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+            float t = 0.0f;
+            for (int w = 0; w < warps; w += 4) {   // zeros past the last warp
+                const float4 p = *reinterpret_cast<const float4 *>(b + i * 32 + w);
+                t += p.x, t += p.y, t += p.z, t += p.w;
+            }
+            v[i] = t;
         }
     }
 
     // the largest of unsigned words (the bits of absolute values)
     __device__ __forceinline__ uint32_t max_bits(uint32_t v)
     {
+        // (words past the last warp stay zeros here too)
         v = __reduce_max_sync(0xFFFFFFFFu, v);
         if (warps == 1) return v;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        uint32_t *b = reinterpret_cast<uint32_t *>(buf + turn * 96);
+        uint32_t *b = reinterpret_cast<uint32_t *>(buf + turn * 128);
         turn ^= 1;
         if (lane == 0) b[warp] = v;
-        __syncthreads();
-        return __reduce_max_sync(0xFFFFFFFFu, lane < warps ? b[lane] : 0u);
+        meet();
+        return __reduce_max_sync(0xFFFFFFFFu, b[lane]);
     }
 };
+
+// 1 / sqrt(sum / d + eps); the hardware's reciprocal root is within two units in
+// the last place, an IEEE root and quotient would be a few hundred clocks on
+// every row's way.
+__device__ __forceinline__ float rms_factor(float sum, float inv_d, float eps) { return rsqrtf(fmaf(sum, inv_d, eps)); }
 
 // ------------------------------------------------------------- int8 codes --
 

@@ -71,7 +71,9 @@ struct OwnCodes {
 // whole CTA; columns k .. np * 64 - 1 are zeros.
 template <typename X, int V> __device__ __forceinline__ void code_rows(const W8a8Args &a, const OwnCodes &o, float *rbuf)
 {
-    RowReducer red{rbuf, kWarps};
+    RowReducer red{rbuf, kWarps, false};
+    red.clear(kThreads);
+    __syncthreads();
     const int kp = a.np * kPairK;
     for (int t = 0; t < a.m; ++t) {
         const X *xr = static_cast<const X *>(a.X) + t * a.ldx;
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, OCC) few_tokens_kernel(const W8a8Arg
     extern __shared__ __align__(16) uint8_t own_smem[];
     __shared__ int32_t sums[kWarps][kUnitRows][8 * NT + 1];
     __shared__ float own_scale[8];
-    __shared__ float rbuf[2 * 96];
+    __shared__ __align__(16) float rbuf[kReduceFloats];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int S = a.slices, slice = warp % S;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kWarps / S) + warp / S;

@@ -113,11 +113,13 @@ struct CodeTileArgs {
 template <typename T, int V> __global__ void __launch_bounds__(512) code_tile_kernel(const CodeTileArgs a)
 {
     constexpr int NV = V >= 4 ? 2 : 4;
-    __shared__ float rbuf[2 * 96];
+    __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
     const int G = blockDim.x, t = threadIdx.x, k = static_cast<int>(a.k), kp = a.np * kPairK;
-    RowReducer red{rbuf, G / 32};
+    RowReducer red{rbuf, G / 32, false};
+    red.clear(G);
+    __syncthreads();
     for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *xr = static_cast<const T *>(a.X) + row * a.ldx;
         const int kr = row < a.m ? k : 0;
