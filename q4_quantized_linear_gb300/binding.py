@@ -126,10 +126,26 @@ def _addr(x) -> int | None:
     return x.data_ptr()
 
 
+_raw_stream = None   # torch's (current device's current stream) as an address
+
+
+def _resolve_raw_stream():
+    """The address of the current stream without building a Stream object (3 us
+    of a 10 us call on a Grace core), where torch has the call for it."""
+    global _raw_stream
+    import torch
+    torch.cuda.current_stream()   # initialises CUDA
+    get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if get is not None and device is not None:
+        _raw_stream = lambda: get(device())   # noqa: E731
+    else:
+        _raw_stream = lambda: torch.cuda.current_stream().cuda_stream   # noqa: E731
+    return _raw_stream
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return (_raw_stream or _resolve_raw_stream())()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -345,21 +345,18 @@ Q4MM_API int q4_moe_dispatch(void *Xs, int64_t ldxs, int64_t *offsets, int32_t *
     a.tokens = tokens, a.pairs = tokens * top_k;
     a.top_k = static_cast<int>(top_k), a.experts = static_cast<int>(n_experts);
     a.hist = static_cast<int32_t *>(workspace);
-    int unit = 16;
+    bool whole = true;
     if (X) {
         const int size = type_size(type);
         RowAlign al;
         al.add(X, ldx * size);
         al.add(Xs, ldxs * size);
-        unit = al.bytes() >= 16 ? 16 : al.bytes() >= 4 ? 4 : 2;
         a.X = X, a.Xs = Xs;
-        a.ldx = ldx * size / unit, a.ldxs = ldxs * size / unit;
-        a.esize = size;
-        a.row_units = d * size / unit;
-        a.tail_at = static_cast<int>(a.row_units * unit / size);
-        a.tail = static_cast<int>(d - a.tail_at);
+        a.ldx = ldx * size, a.ldxs = ldxs * size;
+        a.bytes = d * size;
+        whole = al.bytes() == 16 && a.bytes % 16 == 0;
     }
-    return cuda_status(launch_moe_dispatch(a, unit, dev.sm_count, s));
+    return cuda_status(launch_moe_dispatch(a, whole, dev.sm_count, s));
 }
 
 Q4MM_API int q4_moe_combine(void *Y, int64_t ldy, const void *base, int64_t ldbase, const void *Ys, int64_t ldys,
@@ -389,7 +386,7 @@ Q4MM_API int q4_moe_combine(void *Y, int64_t ldy, const void *base, int64_t ldba
     a.row_of = row_of, a.weights = weights;
     a.tokens = tokens, a.pairs = tokens * top_k;
     a.top_k = static_cast<int>(top_k), a.d = d;
-    return cuda_status(launch_moe_combine(a, type, vec_of(al, type), dev.sm_count, as_stream(stream)));
+    return cuda_status(launch_moe_combine(a, type, vec_of(al, type), as_stream(stream)));
 }
 
 Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, const void *dY, int64_t lddy,
@@ -421,7 +418,7 @@ Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, 
     a.row_of = row_of, a.weights = weights;
     a.tokens = tokens, a.pairs = tokens * top_k;
     a.top_k = static_cast<int>(top_k), a.d = d;
-    return cuda_status(launch_moe_combine_bwd(a, type, vec_of(al, type), dev.sm_count, as_stream(stream)));
+    return cuda_status(launch_moe_combine_bwd(a, type, vec_of(al, type), as_stream(stream)));
 }
 
 } // extern "C"

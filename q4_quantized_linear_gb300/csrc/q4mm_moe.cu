@@ -100,38 +100,79 @@ __device__ __forceinline__ void warp_run(int64_t p0, int64_t p1, int w, int64_t 
     *e = min(p1, *b + per);
 }
 
-// Copies token t's row to the rows of its pairs. Row r of a pair: `row_of`'s
-// value, negative for zeros. U: one access; threads `t0` of `threads`.
-template <typename U>
+// Rows of `bytes` bytes on 2-byte boundaries are copied 16 bytes a store,
+// wherever they start: `threads` threads, this one `t0`. A store covers an
+// aligned 16-byte word of the destination; its bytes come from one or two aligned
+// words of the source, each of which holds at least one of them, shifted by what
+// the two rows' starts differ. The bytes before the destination's first whole
+// word and after its last go two by two.
+__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, int by)
+{
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const int r = 8 * (by & 3);
+    uint4 o = a;
+    switch (by >> 2) {   // the same for a whole row
+    case 0: o = make_uint4(__funnelshift_r(w[0], w[1], r), __funnelshift_r(w[1], w[2], r), __funnelshift_r(w[2], w[3], r),
+                           __funnelshift_r(w[3], w[4], r)); break;
+    case 1: o = make_uint4(__funnelshift_r(w[1], w[2], r), __funnelshift_r(w[2], w[3], r), __funnelshift_r(w[3], w[4], r),
+                           __funnelshift_r(w[4], w[5], r)); break;
+    case 2: o = make_uint4(__funnelshift_r(w[2], w[3], r), __funnelshift_r(w[3], w[4], r), __funnelshift_r(w[4], w[5], r),
+                           __funnelshift_r(w[5], w[6], r)); break;
+    default: o = make_uint4(__funnelshift_r(w[3], w[4], r), __funnelshift_r(w[4], w[5], r), __funnelshift_r(w[5], w[6], r),
+                            __funnelshift_r(w[6], w[7], r)); break;
+    }
+    return o;
+}
+__device__ __forceinline__ void copy_bytes(uint8_t *dst, const uint8_t *src, int64_t bytes, bool zero, int t0, int threads)
+{
+    const int64_t head = min(bytes, static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15));
+    const int64_t words = (bytes - head) / 16, tail = head + 16 * words;
+    const uint8_t *from = src + head;
+    const int by = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15);
+    const uint4 *in = reinterpret_cast<const uint4 *>(from - by);
+    uint4 *out = reinterpret_cast<uint4 *>(dst + head);
+    if (zero) {
+        for (int64_t i = t0; i < words; i += threads) out[i] = make_uint4(0u, 0u, 0u, 0u);
+    } else if (by == 0) {
+        for (int64_t i = t0; i < words; i += threads) out[i] = in[i];
+    } else {
+        for (int64_t i = t0; i < words; i += threads) out[i] = shifted(in[i], in[i + 1], by);
+    }
+    const int loose = static_cast<int>((head + bytes - tail) / 2), first = static_cast<int>(head / 2);
+    for (int i = t0; i < loose; i += threads) {
+        const int64_t at = i < first ? 2 * i : tail + 2 * (i - first);
+        *reinterpret_cast<uint16_t *>(dst + at) = zero ? static_cast<uint16_t>(0) : *reinterpret_cast<const uint16_t *>(src + at);
+    }
+}
+
+// Copies token t's row to the rows of its pairs (a negative `rows` entry: zeros
+// to row -1 - it). Threads t0 of `threads`. WHOLE: rows start on 16-byte
+// boundaries and are whole 16-byte words, so each is read once for all its pairs.
+template <bool WHOLE>
 __device__ __forceinline__ void copy_row(const MoeDispatchArgs &a, int64_t t, const int32_t *rows, int t0, int threads)
 {
-    const U *x = static_cast<const U *>(a.X) + t * a.ldx;
-    U *xs = static_cast<U *>(a.Xs);
-    for (int64_t c = t0; c < a.row_units; c += threads) {
-        const U v = x[c];
-        for (int j = 0; j < a.top_k; ++j) {
-            const int32_t r = rows[j];
-            xs[static_cast<int64_t>(r < 0 ? -1 - r : r) * a.ldxs + c] = r < 0 ? U{} : v;
+    const uint8_t *x = static_cast<const uint8_t *>(a.X) + t * a.ldx;
+    uint8_t *xs = static_cast<uint8_t *>(a.Xs);
+    if constexpr (WHOLE) {
+        const int64_t words = a.bytes / 16;
+        for (int64_t c = t0; c < words; c += threads) {
+            const uint4 v = reinterpret_cast<const uint4 *>(x)[c];
+            for (int j = 0; j < a.top_k; ++j) {
+                const int32_t r = rows[j];
+                reinterpret_cast<uint4 *>(xs + static_cast<int64_t>(r < 0 ? -1 - r : r) * a.ldxs)[c] = r < 0 ? make_uint4(0u, 0u, 0u, 0u) : v;
+            }
         }
-    }
-    // the elements past the last whole access
-    for (int i = t0; i < a.tail; i += threads) {
-        const int64_t c = a.tail_at + i;
+    } else {
         for (int j = 0; j < a.top_k; ++j) {
             const int32_t r = rows[j];
-            U *out = xs + static_cast<int64_t>(r < 0 ? -1 - r : r) * a.ldxs;
-            if (a.esize == 4)
-                reinterpret_cast<uint32_t *>(out)[c] = r < 0 ? 0u : reinterpret_cast<const uint32_t *>(x)[c];
-            else
-                reinterpret_cast<uint16_t *>(out)[c] =
-                    r < 0 ? static_cast<uint16_t>(0) : reinterpret_cast<const uint16_t *>(x)[c];
+            copy_bytes(xs + static_cast<int64_t>(r < 0 ? -1 - r : r) * a.ldxs, x, a.bytes, r < 0, t0, threads);
         }
     }
 }
 
 // One launch for few pairs: every CTA sorts them all in shared memory; CTA 0
 // writes the sort's results; the rows are dealt to the CTAs.
-template <typename U> __global__ void __launch_bounds__(kSortThreads) dispatch_small_kernel(const MoeDispatchArgs a, int segs)
+template <bool WHOLE> __global__ void __launch_bounds__(kSortThreads) dispatch_small_kernel(const MoeDispatchArgs a, int segs)
 {
     extern __shared__ int32_t sm[];
     const int E1 = a.experts + 1, tid = threadIdx.x, warp = tid >> 5;
@@ -172,7 +213,7 @@ template <typename U> __global__ void __launch_bounds__(kSortThreads) dispatch_s
     __syncthreads();
     for (int64_t it = blockIdx.x; it < a.tokens * segs; it += gridDim.x) {
         const int64_t t = it / segs;
-        copy_row<U>(a, t, rows + t * a.top_k, static_cast<int>(it % segs) * kSortThreads + tid, segs * kSortThreads);
+        copy_row<WHOLE>(a, t, rows + t * a.top_k, static_cast<int>(it % segs) * kSortThreads + tid, segs * kSortThreads);
     }
 }
 
@@ -233,96 +274,117 @@ __global__ void __launch_bounds__(kSortThreads) rank_kernel(const MoeDispatchArg
     });
 }
 
-template <typename U> __global__ void __launch_bounds__(256) copy_rows_kernel(const MoeDispatchArgs a)
+// A token per CTA.
+template <bool WHOLE> __global__ void __launch_bounds__(256) copy_rows_kernel(const MoeDispatchArgs a)
 {
     pdl_wait();
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x)
-        copy_row<U>(a, t, a.row_of + t * a.top_k, threadIdx.x, blockDim.x);
+    const int64_t t = blockIdx.x;
+    copy_row<WHOLE>(a, t, a.row_of + t * a.top_k, threadIdx.x, blockDim.x);
 }
 
 // ----------------------------------------------------------------- combine --
 
-template <typename T, int V> __global__ void __launch_bounds__(256) combine_kernel(const MoeCombineArgs a)
-{
-    pdl_wait();
-    const T *Ys = static_cast<const T *>(a.Ys);
-    for (int64_t it = blockIdx.x; it < a.tokens * a.segs; it += gridDim.x) {
-        const int64_t t = it / a.segs;
-        const int seg = static_cast<int>(it % a.segs);
-        const int32_t *rows = a.row_of + t * a.top_k;
-        const float *w = a.weights ? a.weights + t * a.top_k : nullptr;
-        for (int64_t c = (static_cast<int64_t>(seg) * blockDim.x + threadIdx.x) * V; c < a.d;
-             c += static_cast<int64_t>(a.segs) * blockDim.x * V) {
-            float y[V];
-            if (a.base) {
-                const Pack<T, V> bv = load_pack<T, V>(static_cast<const T *>(a.base) + t * a.ldbase, c, a.d);
-#pragma unroll
-                for (int i = 0; i < V; ++i) y[i] = elem(bv, i);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) y[i] = 0.0f;
-            }
-            for (int j0 = 0; j0 < a.top_k; j0 += 4) {
-                Pack<T, V> v[4];
-                bool has[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int32_t r = j0 + j < a.top_k ? rows[j0 + j] : -1;
-                    has[j] = r >= 0 && r < a.pairs;
-                    if (has[j]) v[j] = load_pack<T, V>(Ys + static_cast<int64_t>(r) * a.ldys, c, a.d);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (!has[j]) continue;
-                    const float wj = w ? w[j0 + j] : 1.0f;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) y[i] = fmaf(wj, elem(v[j], i), y[i]);
-                }
-            }
-            store_pack<T, V>(static_cast<T *>(a.Y) + t * a.ldy, c, a.d, pack_of<T, V>(y));
-        }
-    }
-}
-
-// A warp per pair: the token's gradient row is read by top_k neighbouring
-// warps at about the same time, from memory once.
-template <typename T, int V> __global__ void __launch_bounds__(256) combine_bwd_kernel(const MoeCombineBwdArgs a)
+// A warp takes 32 U vectors of a token. Its lanes read the token's rows and
+// weights first, J at a time, then all J U vectors are in flight at once.
+template <typename T, int V, int U, int J> __global__ void __launch_bounds__(256) combine_kernel(const MoeCombineArgs a)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-    for (int64_t p = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); p < a.pairs; p += warps) {
-        const int64_t t = p / a.top_k;
-        const int32_t r = a.row_of[p];
-        const bool has = r >= 0;
-        const int64_t row = has ? r : -1 - static_cast<int64_t>(r);
-        if (row >= a.pairs) continue;
-        const float w = !has ? 0.0f : a.weights ? a.weights[p] : 1.0f;
-        const T *dy = static_cast<const T *>(a.dY) + t * a.lddy;
-        const T *ys = static_cast<const T *>(a.Ys) + row * a.ldys;
-        T *out = static_cast<T *>(a.dYs) + row * a.lddys;
-        float s = 0.0f;
-#pragma unroll 4
-        for (int64_t c = lane * V; c < a.d; c += 32 * V) {
-            Pack<T, V> o = zero_pack<T, V>();
-            if (has) {
-                const Pack<T, V> gp = load_pack<T, V>(dy, c, a.d), yp = load_pack<T, V>(ys, c, a.d);
-                float f[V];
+    const int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t t = it / a.segs;
+    if (t >= a.tokens) return;
+    const T *Ys = static_cast<const T *>(a.Ys);
+    const int32_t *rows = a.row_of + t * a.top_k;
+    const float *w = a.weights ? a.weights + t * a.top_k : nullptr;
+    const int64_t c0 = ((it - t * a.segs) * (32 * U) + lane) * V;
+    float y[U][V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float gi = elem(gp, i);
-                    s = fmaf(gi, elem(yp, i), s);
-                    f[i] = w * gi;
-                }
-                o = pack_of<T, V>(f);
-            }
-            store_pack<T, V>(out, c, a.d, o);
-        }
-        if (!a.dweights) continue;
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = c0 + u * 32 * V;
+        const Pack<T, V> b = a.base && c < a.d ? load_pack<T, V>(static_cast<const T *>(a.base) + t * a.ldbase, c, a.d) : zero_pack<T, V>();
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if (lane == 0) a.dweights[p] = s;
+        for (int i = 0; i < V; ++i) y[u][i] = elem(b, i);
     }
+    for (int j0 = 0; j0 < a.top_k; j0 += 32) {
+        const int32_t mine = j0 + lane < a.top_k ? rows[j0 + lane] : -1;
+        const float my_w = j0 + lane < a.top_k && w ? w[j0 + lane] : 1.0f;
+        const int n = min(32, a.top_k - j0);
+        for (int j1 = 0; j1 < n; j1 += J) {
+            Pack<T, V> v[J][U];
+            bool has[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int32_t r = __shfl_sync(0xFFFFFFFFu, mine, (j1 + j) & 31);
+                has[j] = j1 + j < n && r >= 0 && r < a.pairs;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t c = c0 + u * 32 * V;
+                    if (has[j] && c < a.d) v[j][u] = load_pack<T, V>(Ys + static_cast<int64_t>(r) * a.ldys, c, a.d);
+                    else v[j][u] = zero_pack<T, V>();
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float wj = __shfl_sync(0xFFFFFFFFu, my_w, (j1 + j) & 31);
+                if (!has[j]) continue;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) y[u][i] = fmaf(wj, elem(v[j][u], i), y[u][i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = c0 + u * 32 * V;
+        if (c < a.d) store_pack<T, V>(static_cast<T *>(a.Y) + t * a.ldy, c, a.d, pack_of<T, V>(y[u]));
+    }
+}
+
+// A warp per pair: the token's gradient row is read by top_k neighbouring warps
+// at about the same time, from memory once. U vectors of both rows are in flight.
+template <typename T, int V, int U> __global__ void __launch_bounds__(256) combine_bwd_kernel(const MoeCombineBwdArgs a)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t p = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (p >= a.pairs) return;
+    const int64_t t = p / a.top_k;
+    const int32_t r = a.row_of[p];
+    const bool has = r >= 0;
+    const int64_t row = has ? r : -1 - static_cast<int64_t>(r);
+    if (row >= a.pairs) return;
+    const float w = !has ? 0.0f : a.weights ? a.weights[p] : 1.0f;
+    const T *dy = static_cast<const T *>(a.dY) + t * a.lddy;
+    const T *ys = static_cast<const T *>(a.Ys) + row * a.ldys;
+    T *out = static_cast<T *>(a.dYs) + row * a.lddys;
+    const int d = static_cast<int>(a.d);
+    float s = 0.0f;
+    for (int c0 = lane * V; c0 < d; c0 += 32 * U * V) {
+        Pack<T, V> g[U], y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * 32 * V;
+            g[u] = has && c < d ? load_pack<T, V>(dy, c, d) : zero_pack<T, V>();
+            y[u] = has && c < d ? load_pack<T, V>(ys, c, d) : zero_pack<T, V>();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * 32 * V;
+            float f[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float gi = elem(g[u], i);
+                s = fmaf(gi, elem(y[u], i), s);
+                f[i] = has ? w * gi : 0.0f;
+            }
+            if (c < d) store_pack<T, V>(out, c, d, pack_of<T, V>(f));
+        }
+    }
+    if (!a.dweights) return;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0) a.dweights[p] = s;
 }
 
 bool one_launch(int64_t pairs, int64_t experts) { return pairs <= kOneLaunchPairs && experts <= kOneLaunchExperts; }
@@ -334,16 +396,17 @@ void moe_chunks(int64_t pairs, int64_t *chunk, int *chunks)
     *chunks = static_cast<int>(ceil_div(pairs, *chunk));
 }
 
-template <typename U> cudaError_t launch_dispatch(MoeDispatchArgs a, int sm_count, cudaStream_t s)
+template <bool WHOLE> cudaError_t launch_dispatch(MoeDispatchArgs a, int sm_count, cudaStream_t s)
 {
     const int E1 = a.experts + 1;
     const size_t count_smem = sizeof(int32_t) * (static_cast<size_t>(kSortWarps + 1) * E1 + kSortWarps);
+    // one 16-byte word a thread, at most 256 threads
+    const int64_t words = std::max<int64_t>(1, ceil_div(a.bytes, 16));
     if (one_launch(a.pairs, a.experts)) {
-        const int segs = a.Xs ? static_cast<int>(std::max<int64_t>(1, ceil_div(a.row_units, kSortThreads))) : 1;
+        int segs = a.Xs ? static_cast<int>(ceil_div(words, kSortThreads)) : 1;
         const int64_t grid = a.Xs ? std::min<int64_t>(a.tokens * segs, 2 * static_cast<int64_t>(sm_count)) : 1;
-        int sg = segs;
-        void *args[] = {&a, &sg};
-        return launch_pdl(reinterpret_cast<const void *>(&dispatch_small_kernel<U>), dim3(static_cast<unsigned>(grid)),
+        void *args[] = {&a, &segs};
+        return launch_pdl(reinterpret_cast<const void *>(&dispatch_small_kernel<WHOLE>), dim3(static_cast<unsigned>(grid)),
                           dim3(kSortThreads), count_smem + sizeof(int32_t) * a.pairs, s, args);
     }
     void *args[] = {&a};
@@ -357,32 +420,32 @@ template <typename U> cudaError_t launch_dispatch(MoeDispatchArgs a, int sm_coun
     }
     e = launch_pdl(rank, dim3(static_cast<unsigned>(a.chunks)), dim3(kSortThreads), count_smem, s, args);
     if (e != cudaSuccess || !a.Xs) return e;
-    const int64_t grid = std::min<int64_t>(a.tokens, 8 * static_cast<int64_t>(sm_count));
-    return launch_pdl(reinterpret_cast<const void *>(&copy_rows_kernel<U>), dim3(static_cast<unsigned>(grid)), dim3(256),
-                      0, s, args);
+    const int threads = static_cast<int>(std::min<int64_t>(256, round_up(words, 32)));
+    return launch_pdl(reinterpret_cast<const void *>(&copy_rows_kernel<WHOLE>), dim3(static_cast<unsigned>(a.tokens)),
+                      dim3(static_cast<unsigned>(threads)), 0, s, args);
 }
 
-template <typename T> cudaError_t launch_combine(MoeCombineArgs a, int vec, int sm_count, cudaStream_t s)
+template <typename T> cudaError_t launch_combine(MoeCombineArgs a, int vec, cudaStream_t s)
 {
-    const void *fn = vec * sizeof(T) == 16 ? reinterpret_cast<const void *>(&combine_kernel<T, 16 / sizeof(T)>)
-                     : vec == 2            ? reinterpret_cast<const void *>(&combine_kernel<T, 2>)
-                                           : reinterpret_cast<const void *>(&combine_kernel<T, 1>);
-    const int64_t vecs = ceil_div(a.d, vec);
-    const int threads = static_cast<int>(std::min<int64_t>(256, round_up(vecs, 32)));
-    a.segs = static_cast<int>(std::min<int64_t>(ceil_div(vecs, threads), 1024));
-    const int64_t grid = std::min<int64_t>(a.tokens * a.segs, 8 * static_cast<int64_t>(sm_count));
+    constexpr int W = 16 / sizeof(T);
+    const bool wide = vec == W;
+    const int per = 32 * vec * (wide ? 1 : 4);
+    const void *fn = wide       ? reinterpret_cast<const void *>(&combine_kernel<T, W, 1, 8>)
+                     : vec == 2 ? reinterpret_cast<const void *>(&combine_kernel<T, 2, 4, 4>)
+                                : reinterpret_cast<const void *>(&combine_kernel<T, 1, 4, 4>);
+    a.segs = static_cast<int>(ceil_div(a.d, per));
     void *args[] = {&a};
-    return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s, args);
+    return launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(a.tokens * a.segs, 8))), dim3(256), 0, s, args);
 }
 
-template <typename T> cudaError_t launch_combine_bwd(MoeCombineBwdArgs a, int vec, int sm_count, cudaStream_t s)
+template <typename T> cudaError_t launch_combine_bwd(MoeCombineBwdArgs a, int vec, cudaStream_t s)
 {
-    const void *fn = vec * sizeof(T) == 16 ? reinterpret_cast<const void *>(&combine_bwd_kernel<T, 16 / sizeof(T)>)
-                     : vec == 2            ? reinterpret_cast<const void *>(&combine_bwd_kernel<T, 2>)
-                                           : reinterpret_cast<const void *>(&combine_bwd_kernel<T, 1>);
-    const int64_t grid = std::min<int64_t>(ceil_div(a.pairs, 8), 8 * static_cast<int64_t>(sm_count));
+    constexpr int W = 16 / sizeof(T);
+    const void *fn = vec == W   ? reinterpret_cast<const void *>(&combine_bwd_kernel<T, W, 4>)
+                     : vec == 2 ? reinterpret_cast<const void *>(&combine_bwd_kernel<T, 2, 8>)
+                                : reinterpret_cast<const void *>(&combine_bwd_kernel<T, 1, 8>);
     void *args[] = {&a};
-    return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, args);
+    return launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(a.pairs, 8))), dim3(256), 0, s, args);
 }
 
 } // namespace
@@ -396,31 +459,27 @@ size_t moe_scratch(int64_t pairs, int64_t experts)
     return sizeof(int32_t) * static_cast<size_t>(chunks) * static_cast<size_t>(experts + 1);
 }
 
-cudaError_t launch_moe_dispatch(MoeDispatchArgs a, int unit, int sm_count, cudaStream_t s)
+cudaError_t launch_moe_dispatch(MoeDispatchArgs a, bool whole, int sm_count, cudaStream_t s)
 {
     moe_chunks(a.pairs, &a.chunk, &a.chunks);
-    switch (unit) {
-    case 16: return launch_dispatch<uint4>(a, sm_count, s);
-    case 4: return launch_dispatch<uint32_t>(a, sm_count, s);
-    default: return launch_dispatch<uint16_t>(a, sm_count, s);
+    return whole ? launch_dispatch<true>(a, sm_count, s) : launch_dispatch<false>(a, sm_count, s);
+}
+
+cudaError_t launch_moe_combine(const MoeCombineArgs &a, int type, int vec, cudaStream_t s)
+{
+    switch (type) {
+    case Q4_TYPE_F32: return launch_combine<float>(a, vec, s);
+    case Q4_TYPE_F16: return launch_combine<__half>(a, vec, s);
+    default: return launch_combine<__nv_bfloat16>(a, vec, s);
     }
 }
 
-cudaError_t launch_moe_combine(MoeCombineArgs a, int type, int vec, int sm_count, cudaStream_t s)
+cudaError_t launch_moe_combine_bwd(const MoeCombineBwdArgs &a, int type, int vec, cudaStream_t s)
 {
     switch (type) {
-    case Q4_TYPE_F32: return launch_combine<float>(a, vec, sm_count, s);
-    case Q4_TYPE_F16: return launch_combine<__half>(a, vec, sm_count, s);
-    default: return launch_combine<__nv_bfloat16>(a, vec, sm_count, s);
-    }
-}
-
-cudaError_t launch_moe_combine_bwd(const MoeCombineBwdArgs &a, int type, int vec, int sm_count, cudaStream_t s)
-{
-    switch (type) {
-    case Q4_TYPE_F32: return launch_combine_bwd<float>(a, vec, sm_count, s);
-    case Q4_TYPE_F16: return launch_combine_bwd<__half>(a, vec, sm_count, s);
-    default: return launch_combine_bwd<__nv_bfloat16>(a, vec, sm_count, s);
+    case Q4_TYPE_F32: return launch_combine_bwd<float>(a, vec, s);
+    case Q4_TYPE_F16: return launch_combine_bwd<__half>(a, vec, s);
+    default: return launch_combine_bwd<__nv_bfloat16>(a, vec, s);
     }
 }
 

@@ -15,10 +15,8 @@ constexpr int kMoeMaxChunks = 128;
 struct MoeDispatchArgs {
     void *Xs;                // nullptr: no rows are copied
     const void *X;
-    int64_t ldxs, ldx;       // in units of one access
-    int64_t row_units;       // whole accesses of a row
-    int tail_at, tail;       // then `tail` elements of esize bytes from element tail_at
-    int esize;
+    int64_t ldxs, ldx;       // bytes
+    int64_t bytes;           // of a row
     int64_t *offsets;
     int32_t *row_of, *pair_of;
     const void *ids;
@@ -39,7 +37,7 @@ struct MoeCombineArgs {
     int64_t tokens, pairs;
     int top_k;
     int64_t d;
-    int segs;                // CTAs that share a token's columns
+    int segs;                // warps that share a token's columns
 };
 
 struct MoeCombineBwdArgs {
@@ -56,9 +54,9 @@ struct MoeCombineBwdArgs {
 
 // Scratch bytes of the sort (0 where one launch does it all).
 size_t moe_scratch(int64_t pairs, int64_t experts);
-// `unit`: bytes of one access when rows are copied (16, 4 or 2).
-cudaError_t launch_moe_dispatch(MoeDispatchArgs a, int unit, int sm_count, cudaStream_t s);
-cudaError_t launch_moe_combine(MoeCombineArgs a, int type, int vec, int sm_count, cudaStream_t s);
-cudaError_t launch_moe_combine_bwd(const MoeCombineBwdArgs &a, int type, int vec, int sm_count, cudaStream_t s);
+// `whole`: every row starts on a 16-byte boundary and is whole 16-byte words.
+cudaError_t launch_moe_dispatch(MoeDispatchArgs a, bool whole, int sm_count, cudaStream_t s);
+cudaError_t launch_moe_combine(const MoeCombineArgs &a, int type, int vec, cudaStream_t s);
+cudaError_t launch_moe_combine_bwd(const MoeCombineBwdArgs &a, int type, int vec, cudaStream_t s);
 
 } // namespace q4
