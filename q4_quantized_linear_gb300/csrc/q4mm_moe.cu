@@ -43,24 +43,30 @@ __device__ __forceinline__ int key_of(const MoeDispatchArgs &a, int64_t p)
 
 // Ranks a run of pairs [p0, p1) of a warp: calls put(p, key, rank) with the
 // pairs of the same key before p in the run added to cnt[key], which ends as
-// the run's total. All 32 lanes take part.
+// the run's total. All 32 lanes take part. Four steps' keys are loaded at once.
 template <typename Put>
 __device__ __forceinline__ void rank_run(const MoeDispatchArgs &a, int64_t p0, int64_t p1, int32_t *cnt, Put put)
 {
     const int lane = threadIdx.x & 31;
-    for (int64_t b = p0; b < p1; b += 32) {
-        const int64_t p = b + lane;
-        const int key = p < p1 ? key_of(a, p) : -1;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
-        const int before = __popc(same & ((1u << lane) - 1u));
-        int base = 0;
-        if (key >= 0) base = cnt[key];
-        __syncwarp();
-        if (key >= 0) {
-            if (before == 0) cnt[key] = base + __popc(same);
-            put(p, key, base + before);
+    for (int64_t b = p0; b < p1; b += 128) {
+        int keys[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) keys[i] = b + 32 * i + lane < p1 ? key_of(a, b + 32 * i + lane) : -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (b + 32 * i >= p1) break;
+            const int key = keys[i];
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+            const int before = __popc(same & ((1u << lane) - 1u));
+            int base = 0;
+            if (key >= 0) base = cnt[key];
+            __syncwarp();
+            if (key >= 0) {
+                if (before == 0) cnt[key] = base + __popc(same);
+                put(b + 32 * i + lane, key, base + before);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     }
 }
 
@@ -95,7 +101,8 @@ __device__ __forceinline__ void exclusive_scan(int32_t *v, int n, int32_t *tmp)
 // Pairs of warp w of a CTA that holds [p0, p1), a multiple of 32 but the last.
 __device__ __forceinline__ void warp_run(int64_t p0, int64_t p1, int w, int64_t *b, int64_t *e)
 {
-    const int64_t per = ((p1 - p0 + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int warps = static_cast<int>(blockDim.x) >> 5;
+    const int64_t per = ((p1 - p0 + warps - 1) / warps + 31) / 32 * 32;
     *b = min(p1, p0 + w * per);
     *e = min(p1, *b + per);
 }
@@ -106,23 +113,6 @@ __device__ __forceinline__ void warp_run(int64_t p0, int64_t p1, int w, int64_t 
 // words of the source, each of which holds at least one of them, shifted by what
 // the two rows' starts differ. The bytes before the destination's first whole
 // word and after its last go two by two.
-__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, int by)
-{
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const int r = 8 * (by & 3);
-    uint4 o = a;
-    switch (by >> 2) {   // the same for a whole row
-    case 0: o = make_uint4(__funnelshift_r(w[0], w[1], r), __funnelshift_r(w[1], w[2], r), __funnelshift_r(w[2], w[3], r),
-                           __funnelshift_r(w[3], w[4], r)); break;
-    case 1: o = make_uint4(__funnelshift_r(w[1], w[2], r), __funnelshift_r(w[2], w[3], r), __funnelshift_r(w[3], w[4], r),
-                           __funnelshift_r(w[4], w[5], r)); break;
-    case 2: o = make_uint4(__funnelshift_r(w[2], w[3], r), __funnelshift_r(w[3], w[4], r), __funnelshift_r(w[4], w[5], r),
-                           __funnelshift_r(w[5], w[6], r)); break;
-    default: o = make_uint4(__funnelshift_r(w[3], w[4], r), __funnelshift_r(w[4], w[5], r), __funnelshift_r(w[5], w[6], r),
-                            __funnelshift_r(w[6], w[7], r)); break;
-    }
-    return o;
-}
 __device__ __forceinline__ void copy_bytes(uint8_t *dst, const uint8_t *src, int64_t bytes, bool zero, int t0, int threads)
 {
     const int64_t head = min(bytes, static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15));
@@ -229,18 +219,19 @@ __global__ void __launch_bounds__(kSortThreads) histogram_kernel(const MoeDispat
     const int64_t p0 = blockIdx.x * a.chunk, p1 = min(a.pairs, p0 + a.chunk);
     for (int64_t p = p0 + threadIdx.x; p < p1; p += kSortThreads) atomicAdd(&sm[key_of(a, p)], 1);
     __syncthreads();
-    for (int i = threadIdx.x; i < E1; i += kSortThreads) a.hist[static_cast<int64_t>(blockIdx.x) * E1 + i] = sm[i];
+    // an expert's chunks next to each other: the ranks read them as vectors
+    for (int i = threadIdx.x; i < E1; i += kSortThreads) a.hist[static_cast<int64_t>(i) * a.pitch + blockIdx.x] = sm[i];
 }
 
 // The rows of a chunk's pairs, from every chunk's histogram.
-__global__ void __launch_bounds__(kSortThreads) rank_kernel(const MoeDispatchArgs a)
+__global__ void __launch_bounds__(1024) rank_kernel(const MoeDispatchArgs a)
 {
     extern __shared__ int32_t sm[];
-    const int E1 = a.experts + 1, tid = threadIdx.x, warp = tid >> 5;
-    int32_t *cnt = sm;                       // [kSortWarps][E1]
-    int32_t *total = cnt + kSortWarps * E1;  // [E1]
-    int32_t *tmp = total + E1;               // [kSortWarps]
-    for (int i = tid; i < kSortWarps * E1; i += kSortThreads) cnt[i] = 0;
+    const int E1 = a.experts + 1, tid = threadIdx.x, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
+    int32_t *cnt = sm;                  // [warps][E1]
+    int32_t *total = cnt + warps * E1;  // [E1]
+    int32_t *tmp = total + E1;          // [warps]
+    for (int i = tid; i < warps * E1; i += threads) cnt[i] = 0;
     pdl_launch_dependents();
     pdl_wait();
     __syncthreads();
@@ -249,14 +240,26 @@ __global__ void __launch_bounds__(kSortThreads) rank_kernel(const MoeDispatchArg
     warp_run(p0, p1, warp, &b, &e);
     rank_run(a, b, e, cnt + warp * E1, [](int64_t, int, int) {});
     __syncthreads();
-    for (int k = tid; k < E1; k += kSortThreads) {
+    const int me = static_cast<int>(blockIdx.x);
+    for (int k = tid; k < E1; k += threads) {
         int32_t before = 0, all = 0;
-        for (int c = 0; c < a.chunks; ++c) {
-            const int32_t h = a.hist[static_cast<int64_t>(c) * E1 + k];
-            if (c < static_cast<int>(blockIdx.x)) before += h;
-            all += h;
+        const int4 *h = reinterpret_cast<const int4 *>(a.hist + static_cast<int64_t>(k) * a.pitch);
+        for (int c = 0; c < a.chunks; c += 32) {   // eight vectors in flight
+            int4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = c + 4 * i < a.chunks ? h[c / 4 + i] : make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int32_t n[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int32_t x = c + 4 * i + u < a.chunks ? n[u] : 0;   // the pitch's padding is not written
+                    if (c + 4 * i + u < me) before += x;
+                    all += x;
+                }
+            }
         }
-        for (int w = 0; w < kSortWarps; ++w) {
+        for (int w = 0; w < warps; ++w) {
             const int32_t c = cnt[w * E1 + k];
             cnt[w * E1 + k] = before;
             before += c;
@@ -265,8 +268,8 @@ __global__ void __launch_bounds__(kSortThreads) rank_kernel(const MoeDispatchArg
     }
     __syncthreads();
     exclusive_scan(total, E1, tmp);
-    if (blockIdx.x == 0)
-        for (int k = tid; k < E1; k += kSortThreads) a.offsets[k] = total[k];
+    if (me == 0)
+        for (int k = tid; k < E1; k += threads) a.offsets[k] = total[k];
     rank_run(a, b, e, cnt + warp * E1, [&](int64_t p, int key, int rank) {
         const int32_t row = total[key] + rank;
         a.row_of[p] = key == a.experts ? -1 - row : row;
@@ -274,7 +277,8 @@ __global__ void __launch_bounds__(kSortThreads) rank_kernel(const MoeDispatchArg
     });
 }
 
-// A token per CTA.
+// A token per CTA. (A warp per pair took 48 us instead of 31 for 16384 x 8 rows
+// of 1022 bytes: the token's row is read again for each.)
 template <bool WHOLE> __global__ void __launch_bounds__(256) copy_rows_kernel(const MoeDispatchArgs a)
 {
     pdl_wait();
@@ -387,6 +391,130 @@ template <typename T, int V, int U> __global__ void __launch_bounds__(256) combi
     if (lane == 0) a.dweights[p] = s;
 }
 
+// 16-bit rows that start anywhere: the vectors are the aligned 16-byte words of
+// the row that is written, the rows that are read are shifted to it, and the
+// elements before its first whole word and after its last go one by one (with
+// 2-byte accesses all over, 8000 x 2 x 1023 took 40 us; the accesses, not the
+// memory, bounded it).
+struct Words {
+    int first, count, loose, after;   // element of the first whole word, words, elements outside, the one after the words
+};
+template <typename T> __device__ __forceinline__ Words words_of(const T *row, int d)
+{
+    Words w;
+    w.first = min(d, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 2));
+    w.count = (d - w.first) / 8;
+    w.after = w.first + 8 * w.count;
+    w.loose = w.first + d - w.after;
+    return w;
+}
+
+template <typename T> __global__ void __launch_bounds__(256) combine_anywhere_kernel(const MoeCombineArgs a)
+{
+    constexpr int J = 4;
+    pdl_wait();
+    const int lane = threadIdx.x & 31, d = static_cast<int>(a.d);
+    const int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t t = it / a.segs;
+    if (t >= a.tokens) return;
+    const int seg = static_cast<int>(it - t * a.segs);
+    const T *Ys = static_cast<const T *>(a.Ys), *base = a.base ? static_cast<const T *>(a.base) + t * a.ldbase : nullptr;
+    T *out = static_cast<T *>(a.Y) + t * a.ldy;
+    const int32_t *rows = a.row_of + t * a.top_k;
+    const float *w = a.weights ? a.weights + t * a.top_k : nullptr;
+    const Words wd = words_of(out, d);
+    for (int i = seg * 32 + lane; i < wd.count; i += a.segs * 32) {
+        const int c = wd.first + 8 * i;
+        float y[8] = {};
+        if (base) {
+            const Pack<T, 8> b = load_anywhere(base, c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = elem(b, e);
+        }
+        for (int j0 = 0; j0 < a.top_k; j0 += J) {
+            Pack<T, 8> v[J];
+            bool has[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int32_t r = j0 + j < a.top_k ? rows[j0 + j] : -1;
+                has[j] = r >= 0 && r < a.pairs;
+                v[j] = has[j] ? load_anywhere(Ys + static_cast<int64_t>(r) * a.ldys, c) : zero_pack<T, 8>();
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!has[j]) continue;
+                const float wj = w ? w[j0 + j] : 1.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = fmaf(wj, elem(v[j], e), y[e]);
+            }
+        }
+        store_pack<T, 8>(out, c, d, pack_of<T, 8>(y));
+    }
+    for (int i = seg * 32 + lane; i < wd.loose; i += a.segs * 32) {
+        const int c = i < wd.first ? i : wd.after + i - wd.first;
+        float y = base ? elem(load_pack<T, 1>(base, c, d), 0) : 0.0f;
+        for (int j = 0; j < a.top_k; ++j) {
+            const int32_t r = rows[j];
+            if (r >= 0 && r < a.pairs) y = fmaf(w ? w[j] : 1.0f, elem(load_pack<T, 1>(Ys + static_cast<int64_t>(r) * a.ldys, c, d), 0), y);
+        }
+        const float one[1] = {y};
+        store_pack<T, 1>(out, c, d, pack_of<T, 1>(one));
+    }
+}
+
+template <typename T> __global__ void __launch_bounds__(256) combine_bwd_anywhere_kernel(const MoeCombineBwdArgs a)
+{
+    constexpr int U = 2;
+    pdl_wait();
+    const int lane = threadIdx.x & 31, d = static_cast<int>(a.d);
+    const int64_t p = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (p >= a.pairs) return;
+    const int64_t t = p / a.top_k;
+    const int32_t r = a.row_of[p];
+    const bool has = r >= 0;
+    const int64_t row = has ? r : -1 - static_cast<int64_t>(r);
+    if (row >= a.pairs) return;
+    const float w = !has ? 0.0f : a.weights ? a.weights[p] : 1.0f;
+    const T *dy = static_cast<const T *>(a.dY) + t * a.lddy, *ys = static_cast<const T *>(a.Ys) + row * a.ldys;
+    T *out = static_cast<T *>(a.dYs) + row * a.lddys;
+    const Words wd = words_of(out, d);
+    float s = 0.0f;
+    for (int i0 = lane; i0 < wd.count; i0 += 32 * U) {
+        Pack<T, 8> g[U], y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = has && i0 + 32 * u < wd.count;
+            g[u] = in ? load_anywhere(dy, wd.first + 8 * (i0 + 32 * u)) : zero_pack<T, 8>();
+            y[u] = in ? load_anywhere(ys, wd.first + 8 * (i0 + 32 * u)) : zero_pack<T, 8>();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float ge = elem(g[u], e);
+                s = fmaf(ge, elem(y[u], e), s);
+                f[e] = has ? w * ge : 0.0f;
+            }
+            if (i0 + 32 * u < wd.count) store_pack<T, 8>(out, wd.first + 8 * (i0 + 32 * u), d, pack_of<T, 8>(f));
+        }
+    }
+    for (int i = lane; i < wd.loose; i += 32) {
+        const int c = i < wd.first ? i : wd.after + i - wd.first;
+        float f[1] = {0.0f};
+        if (has) {
+            const float ge = elem(load_pack<T, 1>(dy, c, d), 0);
+            s = fmaf(ge, elem(load_pack<T, 1>(ys, c, d), 0), s);
+            f[0] = w * ge;
+        }
+        store_pack<T, 1>(out, c, d, pack_of<T, 1>(f));
+    }
+    if (!a.dweights) return;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0) a.dweights[p] = s;
+}
+
 bool one_launch(int64_t pairs, int64_t experts) { return pairs <= kOneLaunchPairs && experts <= kOneLaunchExperts; }
 
 // At least 2048 pairs a chunk (eight warps of 256), at most kMoeMaxChunks.
@@ -413,12 +541,14 @@ template <bool WHOLE> cudaError_t launch_dispatch(MoeDispatchArgs a, int sm_coun
     cudaError_t e = launch_pdl(reinterpret_cast<const void *>(&histogram_kernel), dim3(static_cast<unsigned>(a.chunks)),
                                dim3(kSortThreads), sizeof(int32_t) * E1, s, args);
     if (e != cudaSuccess) return e;
+    // a warp's counts of every expert are in shared memory: 32 warps up to 1024
+    // experts, else eight
     const void *rank = reinterpret_cast<const void *>(&rank_kernel);
-    if (count_smem > 48 * 1024) {
-        e = set_max_smem(rank, count_smem);
-        if (e != cudaSuccess) return e;
-    }
-    e = launch_pdl(rank, dim3(static_cast<unsigned>(a.chunks)), dim3(kSortThreads), count_smem, s, args);
+    const int warps = a.experts <= 1024 ? 32 : kSortWarps;
+    const size_t rank_smem = sizeof(int32_t) * (static_cast<size_t>(warps + 1) * E1 + warps);
+    e = set_max_smem(rank, rank_smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(rank, dim3(static_cast<unsigned>(a.chunks)), dim3(static_cast<unsigned>(32 * warps)), rank_smem, s, args);
     if (e != cudaSuccess || !a.Xs) return e;
     const int threads = static_cast<int>(std::min<int64_t>(256, round_up(words, 32)));
     return launch_pdl(reinterpret_cast<const void *>(&copy_rows_kernel<WHOLE>), dim3(static_cast<unsigned>(a.tokens)),
@@ -428,11 +558,17 @@ template <bool WHOLE> cudaError_t launch_dispatch(MoeDispatchArgs a, int sm_coun
 template <typename T> cudaError_t launch_combine(MoeCombineArgs a, int vec, cudaStream_t s)
 {
     constexpr int W = 16 / sizeof(T);
-    const bool wide = vec == W;
-    const int per = 32 * vec * (wide ? 1 : 4);
-    const void *fn = wide       ? reinterpret_cast<const void *>(&combine_kernel<T, W, 1, 8>)
-                     : vec == 2 ? reinterpret_cast<const void *>(&combine_kernel<T, 2, 4, 4>)
-                                : reinterpret_cast<const void *>(&combine_kernel<T, 1, 4, 4>);
+    const void *fn;
+    int per;   // elements of a warp
+    if constexpr (sizeof(T) == 4) {
+        fn = vec == W ? reinterpret_cast<const void *>(&combine_kernel<T, W, 2, 4>)
+                      : reinterpret_cast<const void *>(&combine_kernel<T, 1, 4, 4>);
+        per = vec == W ? 64 * W : 128;
+    } else {
+        fn = vec == W ? reinterpret_cast<const void *>(&combine_kernel<T, W, 1, 8>)
+                      : reinterpret_cast<const void *>(&combine_anywhere_kernel<T>);
+        per = 32 * W;
+    }
     a.segs = static_cast<int>(ceil_div(a.d, per));
     void *args[] = {&a};
     return launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(a.tokens * a.segs, 8))), dim3(256), 0, s, args);
@@ -441,9 +577,10 @@ template <typename T> cudaError_t launch_combine(MoeCombineArgs a, int vec, cuda
 template <typename T> cudaError_t launch_combine_bwd(MoeCombineBwdArgs a, int vec, cudaStream_t s)
 {
     constexpr int W = 16 / sizeof(T);
-    const void *fn = vec == W   ? reinterpret_cast<const void *>(&combine_bwd_kernel<T, W, 4>)
-                     : vec == 2 ? reinterpret_cast<const void *>(&combine_bwd_kernel<T, 2, 8>)
-                                : reinterpret_cast<const void *>(&combine_bwd_kernel<T, 1, 8>);
+    const void *fn;
+    if (vec == W) fn = reinterpret_cast<const void *>(&combine_bwd_kernel<T, W, 4>);
+    else if constexpr (sizeof(T) == 4) fn = reinterpret_cast<const void *>(&combine_bwd_kernel<T, 1, 8>);
+    else fn = reinterpret_cast<const void *>(&combine_bwd_anywhere_kernel<T>);
     void *args[] = {&a};
     return launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(a.pairs, 8))), dim3(256), 0, s, args);
 }
@@ -456,12 +593,13 @@ size_t moe_scratch(int64_t pairs, int64_t experts)
     int64_t chunk;
     int chunks;
     moe_chunks(pairs, &chunk, &chunks);
-    return sizeof(int32_t) * static_cast<size_t>(chunks) * static_cast<size_t>(experts + 1);
+    return sizeof(int32_t) * static_cast<size_t>(round_up(chunks, 4)) * static_cast<size_t>(experts + 1);
 }
 
 cudaError_t launch_moe_dispatch(MoeDispatchArgs a, bool whole, int sm_count, cudaStream_t s)
 {
     moe_chunks(a.pairs, &a.chunk, &a.chunks);
+    a.pitch = static_cast<int>(round_up(a.chunks, 4));
     return whole ? launch_dispatch<true>(a, sm_count, s) : launch_dispatch<false>(a, sm_count, s);
 }
 

@@ -23,9 +23,9 @@ struct MoeDispatchArgs {
     int id_bytes;
     int64_t tokens, pairs;
     int top_k, experts;
-    int32_t *hist;           // [chunks][experts + 1]
+    int32_t *hist;           // [experts + 1][pitch]: pairs of each chunk
     int64_t chunk;           // pairs of a chunk
-    int chunks;
+    int chunks, pitch;
 };
 
 struct MoeCombineArgs {

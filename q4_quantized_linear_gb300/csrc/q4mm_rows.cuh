@@ -189,6 +189,38 @@ template <typename T, int V> __device__ __forceinline__ void store_pack(T *row, 
     }
 }
 
+// Sixteen bytes at any 2-byte boundary: bytes by .. by + 15 of two neighbouring
+// aligned words.
+__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, int by)
+{
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const int r = 8 * (by & 3);
+    switch (by >> 2) {   // the same for a whole row
+    case 0: return make_uint4(__funnelshift_r(w[0], w[1], r), __funnelshift_r(w[1], w[2], r), __funnelshift_r(w[2], w[3], r),
+                              __funnelshift_r(w[3], w[4], r));
+    case 1: return make_uint4(__funnelshift_r(w[1], w[2], r), __funnelshift_r(w[2], w[3], r), __funnelshift_r(w[3], w[4], r),
+                              __funnelshift_r(w[4], w[5], r));
+    case 2: return make_uint4(__funnelshift_r(w[2], w[3], r), __funnelshift_r(w[3], w[4], r), __funnelshift_r(w[4], w[5], r),
+                              __funnelshift_r(w[5], w[6], r));
+    default: return make_uint4(__funnelshift_r(w[3], w[4], r), __funnelshift_r(w[4], w[5], r), __funnelshift_r(w[5], w[6], r),
+                               __funnelshift_r(w[6], w[7], r));
+    }
+}
+// Eight 16-bit elements from element c of a row that starts anywhere, all of
+// them the row's. Each aligned word that is read holds one of them, so it lies in
+// the row's allocation.
+template <typename T> __device__ __forceinline__ Pack<T, 8> load_anywhere(const T *row, int64_t c)
+{
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+    const int by = static_cast<int>(at & 15);
+    const uint4 *in = reinterpret_cast<const uint4 *>(at - by);
+    uint4 v = in[0];
+    if (by) v = shifted(v, in[1], by);
+    Pack<T, 8> p;
+    p.w[0] = v.x, p.w[1] = v.y, p.w[2] = v.z, p.w[3] = v.w;
+    return p;
+}
+
 // V fp32 parameters (weights or gates of the channels) at c, `other` past the
 // end. Their base is aligned to min(16, 4 V) bytes.
 template <int V> __device__ __forceinline__ void load_params(const float *p, int64_t c, int64_t d, float out[V])
