@@ -243,8 +243,10 @@ __global__ void __launch_bounds__(1024) rank_kernel(const MoeDispatchArgs a)
     const int me = static_cast<int>(blockIdx.x);
     for (int k = tid; k < E1; k += threads) {
         int32_t before = 0, all = 0;
+        if (a.chunks == 1)
+            for (int w = 0; w < warps; ++w) all += cnt[w * E1 + k];
         const int4 *h = reinterpret_cast<const int4 *>(a.hist + static_cast<int64_t>(k) * a.pitch);
-        for (int c = 0; c < a.chunks; c += 32) {   // eight vectors in flight
+        for (int c = 0; a.chunks > 1 && c < a.chunks; c += 32) {   // eight vectors in flight
             int4 v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = c + 4 * i < a.chunks ? h[c / 4 + i] : make_int4(0, 0, 0, 0);
@@ -517,10 +519,11 @@ template <typename T> __global__ void __launch_bounds__(256) combine_bwd_anywher
 
 bool one_launch(int64_t pairs, int64_t experts) { return pairs <= kOneLaunchPairs && experts <= kOneLaunchExperts; }
 
-// At least 2048 pairs a chunk (eight warps of 256), at most kMoeMaxChunks.
+// Up to 8192 pairs one CTA, which needs no histogram of others; then at least
+// 2048 pairs a chunk, at most kMoeMaxChunks chunks.
 void moe_chunks(int64_t pairs, int64_t *chunk, int *chunks)
 {
-    *chunk = std::max<int64_t>(2048, round_up(ceil_div(pairs, kMoeMaxChunks), 32));
+    *chunk = pairs <= 8192 ? pairs : std::max<int64_t>(2048, round_up(ceil_div(pairs, kMoeMaxChunks), 32));
     *chunks = static_cast<int>(ceil_div(pairs, *chunk));
 }
 
@@ -538,8 +541,10 @@ template <bool WHOLE> cudaError_t launch_dispatch(MoeDispatchArgs a, int sm_coun
                           dim3(kSortThreads), count_smem + sizeof(int32_t) * a.pairs, s, args);
     }
     void *args[] = {&a};
-    cudaError_t e = launch_pdl(reinterpret_cast<const void *>(&histogram_kernel), dim3(static_cast<unsigned>(a.chunks)),
-                               dim3(kSortThreads), sizeof(int32_t) * E1, s, args);
+    cudaError_t e = cudaSuccess;
+    if (a.chunks > 1)
+        e = launch_pdl(reinterpret_cast<const void *>(&histogram_kernel), dim3(static_cast<unsigned>(a.chunks)),
+                       dim3(kSortThreads), sizeof(int32_t) * E1, s, args);
     if (e != cudaSuccess) return e;
     // a warp's counts of every expert are in shared memory: 32 warps up to 1024
     // experts, else eight
@@ -593,6 +598,7 @@ size_t moe_scratch(int64_t pairs, int64_t experts)
     int64_t chunk;
     int chunks;
     moe_chunks(pairs, &chunk, &chunks);
+    if (chunks == 1) return 0;
     return sizeof(int32_t) * static_cast<size_t>(round_up(chunks, 4)) * static_cast<size_t>(experts + 1);
 }
 
