@@ -59,7 +59,8 @@ constexpr uint32_t kSlotBytes = kStepRecords * kW8RecordBytes;
 constexpr int kMaxAStages = 8, kMaxBStages = 10, kWRing = 4;
 constexpr uint32_t kAColumns = kStepRecords * 32;                 // tensor-memory columns of a step's weights
 constexpr int kStageTokens = 16;                                  // token columns an epilogue warp stages at once
-constexpr size_t kStagingBytes = kEpilogueWarps * kStageTokens * 32 * 4;
+constexpr size_t kWarpStaging = kStageTokens * 32 * 4;
+constexpr size_t kStagingBytes = kEpilogueWarps * (kWarpStaging + 128 * 4);   // and its tokens' scales
 
 // Codes to fp16 tiles: [half tile of H = N / 2 tokens][64 columns][H rows of
 // 128 bytes], 16-byte chunk c of row r at c ^ (r & 7). Rows past m and columns
@@ -206,6 +207,30 @@ struct Ring {
         if (++slot == depth) slot = 0, phase ^= 1u;
     }
 };
+
+// A staged [16 tokens][32 rows] out to `tokens` rows of Y, B bytes a store; of the
+// 32 weight rows `rows` exist.
+template <typename T, int B>
+__device__ __forceinline__ void store_staged(T *dst, int64_t ld, const uint8_t *stage, int rows, int tokens, int lane)
+{
+    using A = typename AccessOf<B>::type;
+    constexpr int kVec = B / static_cast<int>(sizeof(T)), kLanes = 32 / kVec, kTokens = 32 / kLanes;
+    const int c = lane % kLanes * kVec;
+#pragma unroll
+    for (int i = 0; i < kStageTokens; i += kTokens) {
+        const int t = i + lane / kLanes;
+        const T *src = reinterpret_cast<const T *>(stage) + t * 32 + c;
+        if (t >= tokens) continue;
+        T *out = dst + t * ld + c;
+        if (c + kVec <= rows) {
+            *reinterpret_cast<A *>(out) = *reinterpret_cast<const A *>(src);
+        } else {
+            using E = typename AccessOf<static_cast<int>(sizeof(T))>::type;
+            for (int u = 0; u < kVec; ++u)
+                if (c + u < rows) reinterpret_cast<E *>(out)[u] = reinterpret_cast<const E *>(src)[u];
+        }
+    }
+}
 
 template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_kernel(const W8a8GemmArgs a)
 {
@@ -461,19 +486,16 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
     } else if (warp >= kEpilogueWarp0) {
         // ------------------------------------------------------- epilogue
         // A lane holds one weight row; Y's rows are tokens. Sixteen tokens at a
-        // time go through the warp's staging area and out as 16 bytes a lane
-        // (with 2- or 4-byte stores straight from the registers the epilogue of
-        // a 256 x 256 tile took 3.7 us); a Y whose rows are not 16-byte aligned
-        // is written element by element.
+        // time go through the warp's staging area and out as 16 bytes a lane, or
+        // 8 or 4 where Y's rows are aligned to no more (with 2- or 4-byte stores
+        // straight from the registers the epilogue of a 256 x 256 tile took 3.7 us).
         pdl_wait();
         const int q = warp & 3, half = (warp - kEpilogueWarp0) >> 2;
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-        constexpr int kVec = 16 / sizeof(T);            // elements of a store
-        constexpr int kLanesPerToken = 32 / kVec;
-        constexpr int kTokensPerStore = 32 / kLanesPerToken;
-        T *stage = reinterpret_cast<T *>(sm.stage + (warp - kEpilogueWarp0) * (kStageTokens * 32 * 4));
+        uint8_t *stage = sm.stage + (warp - kEpilogueWarp0) * (kWarpStaging + 128 * 4);
+        float *const sxs = reinterpret_cast<float *>(stage + kWarpStaging);
         T *Y = static_cast<T *>(a.Y);
-        const bool wide = (reinterpret_cast<uintptr_t>(Y) & 15u) == 0 && (a.ldy * sizeof(T)) % 16 == 0;
+        const uintptr_t ybits = reinterpret_cast<uintptr_t>(Y) | static_cast<uintptr_t>(a.ldy * sizeof(T));
         uint32_t seq = 0;
         for (int tile = pair; tile < a.tiles; tile += pairs, ++seq) {
             const int G = 2 * (tile / a.ts) + static_cast<int>(rank);
@@ -481,88 +503,52 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
             const int rows = G < a.groups ? static_cast<int>(max(int64_t(0), min(int64_t(32), a.n - row0))) : 0;
             const float sw = lane < rows ? __ldg(a.row_scale + row0 + lane) : 0.0f;
             const int t0 = (tile % a.ts) * N + half * H;        // this warp's tokens: t0 .. t0 + H - 1
-            float sx[4];                                        // of tokens t0 + 32 i + lane
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sx[i] = 32 * i < H && t0 + 32 * i + lane < a.m ? __ldg(a.sx + t0 + 32 * i + lane) : 0.0f;
+            for (int i = lane; i < H; i += 32) sxs[i] = t0 + i < a.m ? __ldg(a.sx + t0 + i) : 0.0f;
+            __syncwarp();
+            const F2 sw2 = f2(sw, sw);
             if (!warp_wait(sm.d_full, seq & 1u, a.wait_ns)) {
                 fail(sm, a);
                 break;
             }
             tc_fence_after();
             const uint32_t d0 = tmem + lane_base + static_cast<uint32_t>(half * H);
-            // D is read into registers, scaled and rounded, and given back before
-            // the stores: all H columns for 16-bit results, 64 at a time for fp32.
-            constexpr int kHold = sizeof(T) == 2 ? 128 : 64;
-#pragma unroll
-            for (int h0 = 0; h0 < 128; h0 += kHold) {
-                if (h0 >= H) break;
-                uint32_t held[64];
-#pragma unroll
-                for (int ch = 0; ch < kHold / 16; ++ch) {
-                    if (h0 + ch * 16 >= H) break;
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(d0 + static_cast<uint32_t>(h0 + ch * 16), v);
-                    tmem_wait_ld();
-                    float y[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int c = h0 + ch * 16 + i;
-                        y[i] = __uint_as_float(v[i]) * (__shfl_sync(0xFFFFFFFFu, sx[c >> 5], c & 31) * sw);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if constexpr (sizeof(T) == 4) {
-                            held[ch * 16 + i] = __float_as_uint(y[i]);
-                        } else if (i % 2 == 0) {
-                            const float two[2] = {y[i], y[i + 1]};
-                            held[ch * 8 + i / 2] = pack_of<T, 2>(two).w[0];
-                        }
-                    }
-                }
-                if (h0 + kHold >= H) {
+            // Sixteen columns at a time; D is given back when the last have been read.
+            // (Held in registers, all of them before the first store, D came back
+            // sooner, but the registers spilled: 31.9 us instead of 30.7 at 540 x 9728
+            // x 2560 fp32, 152 instead of 138 at 3332 x 17044 x 1472.)
+#pragma unroll 1
+            for (int ch = 0; ch * 16 < H; ++ch) {
+                uint32_t c[16];
+                tmem_ld_32x32b_x16(d0 + static_cast<uint32_t>(ch * 16), c);
+                tmem_wait_ld();
+                if ((ch + 1) * 16 >= H) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_async(mapa_shared(smem_u32(sm.d_empty), 0u));
                 }
+                using Bits = typename AccessOf<static_cast<int>(sizeof(T))>::type;
+                Bits *const st = reinterpret_cast<Bits *>(stage);
 #pragma unroll
-                for (int ch = 0; ch < kHold / 16; ++ch) {
-                    if (h0 + ch * 16 >= H) break;
-                    // elements as bits
-                    using Bits = typename AccessOf<static_cast<int>(sizeof(T))>::type;
-                    Bits y[16];
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 sx = *reinterpret_cast<const float4 *>(sxs + ch * 16 + i);
+                    const F2 y[2] = {f2_mul(f2(__uint_as_float(c[i]), __uint_as_float(c[i + 1])), f2_mul(f2(sx.x, sx.y), sw2)),
+                                     f2_mul(f2(__uint_as_float(c[i + 2]), __uint_as_float(c[i + 3])), f2_mul(f2(sx.z, sx.w), sw2))};
+                    const Pack<T, 4> o = pack_pairs<T, 4>(y);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if constexpr (sizeof(T) == 4) y[i] = held[ch * 16 + i];
-                        else y[i] = static_cast<Bits>(held[ch * 8 + i / 2] >> (16 * (i & 1)));
-                    }
-                    const int tc = t0 + h0 + ch * 16;
-                    if (wide) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) reinterpret_cast<Bits *>(stage)[i * 32 + lane] = y[i];
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < kStageTokens; i += kTokensPerStore) {
-                            const int tk = i + lane / kLanesPerToken, c = (lane % kLanesPerToken) * kVec;
-                            const uint4 o = lds128(stage + tk * 32 + c);
-                            if (tc + tk < a.m) {
-                                T *dst = Y + (tc + tk) * a.ldy + row0 + c;
-                                if (c + kVec <= rows) {
-                                    *reinterpret_cast<uint4 *>(dst) = o;
-                                } else {
-                                    const T *e = reinterpret_cast<const T *>(&o);
-#pragma unroll
-                                    for (int u = 0; u < kVec; ++u)
-                                        if (c + u < rows) dst[u] = e[u];
-                                }
-                            }
-                        }
-                        __syncwarp();
-                    } else if (lane < rows) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (tc + i < a.m) reinterpret_cast<Bits *>(Y)[(tc + i) * a.ldy + row0 + lane] = y[i];
+                    for (int u = 0; u < 4; ++u) {
+                        if constexpr (sizeof(T) == 4) st[(i + u) * 32 + lane] = o.w[u];
+                        else st[(i + u) * 32 + lane] = static_cast<Bits>(o.w[u / 2] >> (16 * (u & 1)));
                     }
                 }
+                __syncwarp();
+                const int tc = t0 + ch * 16;
+                T *const dst = Y + tc * a.ldy + row0;
+                const int tokens = min(kStageTokens, a.m - tc);
+                if ((ybits & 15u) == 0) store_staged<T, 16>(dst, a.ldy, stage, rows, tokens, lane);
+                else if ((ybits & 7u) == 0) store_staged<T, 8>(dst, a.ldy, stage, rows, tokens, lane);
+                else if ((ybits & 3u) == 0) store_staged<T, 4>(dst, a.ldy, stage, rows, tokens, lane);
+                else store_staged<T, static_cast<int>(sizeof(T))>(dst, a.ldy, stage, rows, tokens, lane);
+                __syncwarp();
             }
         }
     }
