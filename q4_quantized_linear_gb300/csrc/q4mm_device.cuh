@@ -220,6 +220,12 @@ __device__ __forceinline__ bool mbar_test_wait2(uint64_t *bar0, uint32_t parity0
     return ok != 0;
 }
 
+// What is already issued into a CTA's memory is waited for at least so long
+// before the CTA leaves, whatever the caller's limit: it lands in microseconds,
+// and must not land after the CTA is gone.
+constexpr uint64_t kLandNs = 200000000ull;
+__device__ __forceinline__ uint64_t landing_limit(uint64_t limit_ns) { return limit_ns > kLandNs ? limit_ns : kLandNs; }
+
 // Below this limit a wait polls without suspending (try_wait may sleep for
 // longer than the limit inside one call), so that the limit is honoured.
 constexpr uint64_t kShortWaitNs = 100000;

@@ -48,8 +48,7 @@ struct RowStream {
         }
         __syncthreads();
     }
-    // the copying warp's one thread: every row of the CTA; waits for what is in
-    // flight if it has to give up
+    // the copying warp's one thread: every row of the CTA, until all have landed
     __device__ __forceinline__ void copy_rows()
     {
         int slot = 0;
@@ -58,9 +57,7 @@ struct RowStream {
         for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
             if (issued >= stages && !mbar_wait(&empty[slot], phase ^ 1u, wait_ns)) {
                 record_status(status, kErrTimeout);
-                for (int64_t k = issued - stages; k < issued; ++k)
-                    mbar_wait(&full[k % stages], static_cast<uint32_t>(k / stages) & 1u, wait_ns);
-                return;
+                break;
             }
             mbar_arrive_expect_tx(&full[slot], bytes * used);
             uint8_t *dst = buf + static_cast<size_t>(slot) * used * bytes;
@@ -68,6 +65,8 @@ struct RowStream {
             ++issued;
             if (++slot == stages) slot = 0, phase ^= 1u;
         }
+        for (int64_t k = issued > stages ? issued - stages : 0; k < issued; ++k)
+            mbar_wait(&full[k % stages], static_cast<uint32_t>(k / stages) & 1u, landing_limit(wait_ns));
     }
     __device__ __forceinline__ void wait(int slot, uint32_t phase)
     {

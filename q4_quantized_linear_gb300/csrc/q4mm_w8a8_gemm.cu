@@ -315,10 +315,9 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                     b.step(SB);
                 }
             }
-            // after a timeout: what is still landing (all has been read otherwise)
-            if (!ok)
-                for (int64_t i = issued > SB ? issued - SB : 0; i < issued; ++i)
-                    if (!mbar_wait(&sm.full_b[i % SB], static_cast<uint32_t>(i / SB) & 1u, a.wait_ns)) fail(sm, a);
+            // no copy may be landing when the CTA leaves, also if another role gave up
+            for (int64_t i = issued > SB ? issued - SB : 0; i < issued; ++i)
+                if (!mbar_wait(&sm.full_b[i % SB], static_cast<uint32_t>(i / SB) & 1u, landing_limit(a.wait_ns))) fail(sm, a);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -350,9 +349,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                     w.step(RW);
                 }
             }
-            if (!ok)
-                for (int64_t i = issued > RW ? issued - RW : 0; i < issued; ++i)
-                    if (!mbar_wait(&sm.full_w[i % RW], static_cast<uint32_t>(i / RW) & 1u, a.wait_ns)) fail(sm, a);
+            for (int64_t i = issued > RW ? issued - RW : 0; i < issued; ++i)
+                if (!mbar_wait(&sm.full_w[i % RW], static_cast<uint32_t>(i / RW) & 1u, landing_limit(a.wait_ns))) fail(sm, a);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -555,7 +553,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
 
     // No MMA of the pair and none of its arrivals is in flight past this.
     __syncthreads();
-    if (tid == 0 && !mbar_wait(sm.done, 0, a.wait_ns)) fail(sm, a);
+    if (tid == 0 && !mbar_wait(sm.done, 0, landing_limit(a.wait_ns))) fail(sm, a);
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // neither CTA's memory is used by the other past this
