@@ -218,9 +218,8 @@ template <typename T> const void *few_tokens_of(const W8a8Args &a)
                : a.xtype == Q4_TYPE_F16 ? reinterpret_cast<const void *>(&few_tokens_kernel<T, __half, 1, 2, 4>)
                                         : reinterpret_cast<const void *>(&few_tokens_kernel<T, __nv_bfloat16, 1, 2, 4>);
     }
-    return a.m <= 8    ? reinterpret_cast<const void *>(&few_tokens_kernel<T, int8_t, 1, 2, 4>)
-           : a.m <= 16 ? reinterpret_cast<const void *>(&few_tokens_kernel<T, int8_t, 2, 2, 3>)
-                       : reinterpret_cast<const void *>(&few_tokens_kernel<T, int8_t, 4, 2, 2>);
+    return a.m <= 8 ? reinterpret_cast<const void *>(&few_tokens_kernel<T, int8_t, 1, 2, 4>)
+                    : reinterpret_cast<const void *>(&few_tokens_kernel<T, int8_t, 2, 2, 3>);
 }
 
 // Slices of K: the fewest warps that keep the memory busy (24 an SM), but at
@@ -252,7 +251,7 @@ bool valid_sizes(int64_t m, int64_t k, int64_t n)
 size_t codes_bytes(int64_t m, int64_t k) { return static_cast<size_t>(round_up(m * k, 256)); }
 size_t image_at(int64_t m, int64_t k) { return codes_bytes(m, k) + static_cast<size_t>(round_up(4 * m, 256)); }
 
-constexpr int64_t kFewTokens = 32;
+constexpr int64_t kFewTokens = 16;
 
 // `tok`: codes with their scales, or rows to be coded.
 int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int64_t m, int64_t k, int64_t n,
@@ -271,7 +270,7 @@ int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int
     if (m > kFewTokens) {
         W8a8GemmPlan plan;
         if (!plan_w8a8_gemm(m, k, n, &plan)) return Q4_ERR_INVALID_ARG;
-        if (workspace_bytes < image_at(m, k) + plan.image_bytes) return Q4_ERR_WORKSPACE;
+        if (workspace_bytes < image_at(m, k) + plan.image_bytes + plan.partial_bytes) return Q4_ERR_WORKSPACE;
         W8a8GemmArgs g{};
         g.W = W;
         g.np = np;
@@ -326,7 +325,7 @@ Q4MM_API size_t q4_w8a8_workspace_size(int64_t m, int64_t k, int64_t n)
 {
     if (m <= 0 || !valid_sizes(m, k, n)) return 0;
     W8a8GemmPlan plan;
-    if (m > kFewTokens && plan_w8a8_gemm(m, k, n, &plan)) return image_at(m, k) + plan.image_bytes;
+    if (m > kFewTokens && plan_w8a8_gemm(m, k, n, &plan)) return image_at(m, k) + plan.image_bytes + plan.partial_bytes;
     return image_at(m, k);
 }
 

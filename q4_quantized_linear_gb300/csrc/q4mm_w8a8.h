@@ -29,11 +29,13 @@ struct W8a8Args {
 struct W8a8GemmPlan {
     int N = 0;                // tokens of a tile: a multiple of 32, at most 256
     int ts = 0;               // token tiles
-    int tiles = 0;            // (256 rows) x (N tokens)
+    int kslices = 1;          // of K: each slice of a tile is one of `tiles`
+    int tiles = 0;            // (256 rows) x (N tokens) x (K slice)
     int pairs = 0;            // CTA pairs of the grid, each taking tiles in turn
     int astages = 0, bstages = 0, wring = 0;
     size_t smem = 0;
-    size_t image_bytes = 0;   // the tokens' fp16 tiles
+    size_t image_bytes = 0;   // the tokens' fp16 tiles; 256-byte aligned
+    size_t partial_bytes = 0; // the slices' sums, behind them
 };
 
 struct W8a8GemmArgs {
@@ -47,7 +49,8 @@ struct W8a8GemmArgs {
     int *status;
     uint64_t wait_ns;
     int m, n, np, groups;
-    int N, ts, tiles;
+    int N, ts, tiles, kslices;
+    int64_t slice_stride;     // elements from a slice's sums to the next's
     int astages, bstages, wring;
 };
 

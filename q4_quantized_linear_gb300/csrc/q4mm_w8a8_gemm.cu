@@ -31,6 +31,9 @@
 // The MMA's commits release a stage (A and B) in both CTAs. A pair runs
 // through tiles in turn: the rings carry on into the next tile while the
 // epilogue reads D; only D's own read keeps the MMA waiting.
+// Where tiles are too few for the device, K is cut into slices, each a tile of its
+// own that writes its raw sums (whole numbers in fp32) to the workspace; a second
+// kernel adds them in slice order and scales.
 // Every wait is bounded; after a timeout all roles leave their loops, the
 // MMAs and copies in flight are waited for and the CTAs of the pair leave
 // together.
@@ -96,6 +99,15 @@ __global__ void __launch_bounds__(256) tile_kernel(const int8_t *Xq, uint8_t *xi
         *reinterpret_cast<uint4 *>(dst + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
+
+struct SliceSumArgs {
+    const float *partials;     // [slices][m][ld]
+    int64_t ld, stride;
+    int slices;
+    const float *sx, *row_scale;
+    void *Y;
+    int64_t ldy, n;
+};
 
 struct CodeTileArgs {
     const void *X;
@@ -232,7 +244,8 @@ __device__ __forceinline__ void store_staged(T *dst, int64_t ld, const uint8_t *
     }
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_kernel(const W8a8GemmArgs a)
+// SLICED: K slices (T is float: raw sums).
+template <typename T, bool SLICED> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_kernel(const W8a8GemmArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -242,7 +255,12 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
     const int N = a.N, H = N / 2, SA = a.astages, SB = a.bstages, RW = a.wring, np = a.np;
     const uint32_t brec = static_cast<uint32_t>(H) * 128u;    // a record's columns of the half tile
     const uint32_t bstage = kStepRecords * brec;
-    const int steps = (np + kStepRecords - 1) / kStepRecords;   // of a tile; the last may hold one record
+    // Steps of a tile: K slice `tile % KS` has `per` of them, the last slice what is
+    // left; the last step of K may hold one record.
+    const int all_steps = (np + kStepRecords - 1) / kStepRecords, KS = SLICED ? a.kslices : 1;
+    const int per = SLICED ? (all_steps + KS - 1) / KS : all_steps;
+    const auto first_step = [&](int tile) { return tile % KS * per; };
+    const auto end_step = [&](int tile) { return min(all_steps, first_step(tile) + per); };
     const uint32_t acol0 = static_cast<uint32_t>(N);   // first A column after D (N is a multiple of 32)
 
     Smem sm;
@@ -298,9 +316,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
             int64_t issued = 0;
             bool ok = true;
             for (int tile = pair; ok && tile < a.tiles; tile += pairs) {
-                const int jt = tile % a.ts;
+                const int jt = tile / KS % a.ts;
                 const uint8_t *src = a.ximg + (static_cast<size_t>(2 * jt) + rank) * np * brec;
-                for (int st = 0; st < steps; ++st) {
+                const int end = end_step(tile);
+                for (int st = first_step(tile); st < end; ++st) {
                     if (aborted(sm)) { ok = false; break; }
                     if (issued >= SB && !mbar_wait(&sm.empty_b[b.slot], b.phase ^ 1u, a.wait_ns)) {
                         fail(sm, a);
@@ -332,9 +351,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
             for (int tile = pair; ok && tile < a.tiles; tile += pairs) {
                 // the last pair of an odd number of groups: its second CTA
                 // reads the last group again and writes nothing
-                const int G = min(2 * (tile / a.ts) + static_cast<int>(rank), a.groups - 1);
+                const int G = min(2 * (tile / KS / a.ts) + static_cast<int>(rank), a.groups - 1);
                 const uint8_t *src = a.W + static_cast<size_t>(G) * np * kW8RecordBytes;
-                for (int st = 0; st < steps; ++st) {
+                const int end = end_step(tile);
+                for (int st = first_step(tile); st < end; ++st) {
                     if (aborted(sm)) { ok = false; break; }
                     if (issued >= RW && !mbar_wait(&sm.empty_w[w.slot], w.phase ^ 1u, a.wait_ns)) {
                         fail(sm, a);
@@ -370,7 +390,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                     break;
                 }
                 bool ready = warp_test(&sm.ready[r.slot], r.phase);
-                for (int st = 0; st < steps; ++st) {
+                const int begin = first_step(tile), end = end_step(tile);
+                for (int st = begin; st < end; ++st) {
                     if (!ready && !warp_spin_wait(&sm.ready[r.slot], r.phase, a.wait_ns)) {
                         ok = false;
                         break;
@@ -384,7 +405,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                     b.step(SB);
                     tc_fence_after();
                     if (elect_one()) {
-                        tc_mma_f16_ts_pair(d, at, bd, idesc, st > 0 ? 1u : 0u);
+                        tc_mma_f16_ts_pair(d, at, bd, idesc, st > begin ? 1u : 0u);
 #pragma unroll
                         for (uint32_t i = 1; i < 4; ++i) tc_mma_f16_ts_pair(d, at + 8u * i, bd + 2u * i, idesc, 1u);
                         if (whole) {
@@ -395,7 +416,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                         if (SB != SA) tc_commit_pair(done_b, 3);
                     }
                     __syncwarp();
-                    ready = st + 1 < steps && warp_test(&sm.ready[r.slot], r.phase);
+                    ready = st + 1 < end && warp_test(&sm.ready[r.slot], r.phase);
                 }
                 if (ok && elect_one()) tc_commit_pair(sm.d_full, 3);
                 __syncwarp();
@@ -412,7 +433,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
             bool ok = true;
             const uint32_t ready0 = mapa_shared(smem_u32(sm.ready), 0u);
             for (int tile = pair; ok && tile < a.tiles; tile += pairs) {
-                for (int st = 0; st < steps; ++st, r.step(SA), b.step(SB)) {
+                const int end = end_step(tile);
+                for (int st = first_step(tile); st < end; ++st, r.step(SA), b.step(SB)) {
                     if (!mbar_test_wait2(&sm.full_b[b.slot], b.phase, &sm.stored[r.slot], r.phase) &&
                         (!mbar_wait(&sm.full_b[b.slot], b.phase, a.wait_ns) || !mbar_wait(&sm.stored[r.slot], r.phase, a.wait_ns))) {
                         fail(sm, a);
@@ -438,7 +460,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         Ring w, r;
         bool ok = true;
         for (int tile = pair; ok && tile < a.tiles; tile += pairs) {
-            for (int st = 0; st < steps; ++st, w.step(RW), r.step(SA)) {
+            const int end = end_step(tile);
+            for (int st = first_step(tile); st < end; ++st, w.step(RW), r.step(SA)) {
                 // (a barrier's first phase counts as complete where it has none before)
                 if (!__all_sync(0xFFFFFFFFu, mbar_test_wait2(&sm.full_w[w.slot], w.phase, &sm.empty_a[r.slot], r.phase ^ 1u)) &&
                     (!warp_wait(&sm.full_w[w.slot], w.phase, a.wait_ns) ||
@@ -496,12 +519,13 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
         const uintptr_t ybits = reinterpret_cast<uintptr_t>(Y) | static_cast<uintptr_t>(a.ldy * sizeof(T));
         uint32_t seq = 0;
         for (int tile = pair; tile < a.tiles; tile += pairs, ++seq) {
-            const int G = 2 * (tile / a.ts) + static_cast<int>(rank);
+            const int G = 2 * (tile / KS / a.ts) + static_cast<int>(rank);
             const int64_t row0 = static_cast<int64_t>(G) * kW8GroupRows + q * 32;
             const int rows = G < a.groups ? static_cast<int>(max(int64_t(0), min(int64_t(32), a.n - row0))) : 0;
-            const float sw = lane < rows ? __ldg(a.row_scale + row0 + lane) : 0.0f;
-            const int t0 = (tile % a.ts) * N + half * H;        // this warp's tokens: t0 .. t0 + H - 1
-            for (int i = lane; i < H; i += 32) sxs[i] = t0 + i < a.m ? __ldg(a.sx + t0 + i) : 0.0f;
+            const float sw = SLICED ? 1.0f : lane < rows ? __ldg(a.row_scale + row0 + lane) : 0.0f;
+            const int t0 = (tile / KS % a.ts) * N + half * H;   // this warp's tokens: t0 .. t0 + H - 1
+            T *const Yt = SLICED ? Y + tile % KS * a.slice_stride : Y;
+            for (int i = lane; i < H; i += 32) sxs[i] = SLICED ? 1.0f : t0 + i < a.m ? __ldg(a.sx + t0 + i) : 0.0f;
             __syncwarp();
             const F2 sw2 = f2(sw, sw);
             if (!warp_wait(sm.d_full, seq & 1u, a.wait_ns)) {
@@ -540,7 +564,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
                 }
                 __syncwarp();
                 const int tc = t0 + ch * 16;
-                T *const dst = Y + tc * a.ldy + row0;
+                T *const dst = Yt + tc * a.ldy + row0;
                 const int tokens = min(kStageTokens, a.m - tc);
                 if ((ybits & 15u) == 0) store_staged<T, 16>(dst, a.ldy, stage, rows, tokens, lane);
                 else if ((ybits & 7u) == 0) store_staged<T, 8>(dst, a.ldy, stage, rows, tokens, lane);
@@ -561,11 +585,33 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) w8a8_gemm_k
     if (warp == 1) tmem_dealloc_pair(tmem, 512u);
 }
 
-const void *kernel_of(int ytype)
+// Y = sx s_j times the slices' sums, four weight rows a thread where Y's rows
+// allow it.
+template <typename T, int V> __global__ void __launch_bounds__(256) slice_sum_kernel(const SliceSumArgs a)
 {
-    return ytype == Q4_TYPE_F32   ? reinterpret_cast<const void *>(&w8a8_gemm_kernel<float>)
-           : ytype == Q4_TYPE_F16 ? reinterpret_cast<const void *>(&w8a8_gemm_kernel<__half>)
-                                  : reinterpret_cast<const void *>(&w8a8_gemm_kernel<__nv_bfloat16>);
+    pdl_wait();
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
+    const int64_t t = blockIdx.y;
+    if (c >= a.n) return;
+    const float *p = a.partials + t * a.ld + c;   // the partials' rows are whole groups of 128
+    float s[V] = {};
+    for (int k = 0; k < a.slices; ++k) {
+        const Pack<float, V> v = load_pack<float, V>(p + k * a.stride, 0, V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] += elem(v, i);
+    }
+    const float sx = a.sx[t];
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = s[i] * (sx * a.row_scale[c + i]);
+    store_pack<T, V>(static_cast<T *>(a.Y) + t * a.ldy, c, a.n, pack_of<T, V>(s));
+}
+
+const void *kernel_of(int ytype, bool sliced)
+{
+    return sliced                 ? reinterpret_cast<const void *>(&w8a8_gemm_kernel<float, true>)
+           : ytype == Q4_TYPE_F32 ? reinterpret_cast<const void *>(&w8a8_gemm_kernel<float, false>)
+           : ytype == Q4_TYPE_F16 ? reinterpret_cast<const void *>(&w8a8_gemm_kernel<__half, false>)
+                                  : reinterpret_cast<const void *>(&w8a8_gemm_kernel<__nv_bfloat16, false>);
 }
 
 size_t smem_bytes(int N, int astages, int bstages, int wring)
@@ -588,7 +634,7 @@ int max_pairs(size_t smem)
     const auto it = cache.find({dev, smem});
     if (it != cache.end()) return it->second;
     int n = 0;
-    const void *fn = kernel_of(Q4_TYPE_F32);
+    const void *fn = kernel_of(Q4_TYPE_F32, false);
     if (set_max_smem(fn, smem) == cudaSuccess) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(2);
@@ -610,13 +656,14 @@ int max_pairs(size_t smem)
 
 } // namespace
 
-// Tokens a tile: the fewest clocks over the pairs' turns. A K step takes 2 N
-// clocks of MMA (256 x N x 64 at 8192 products a clock and pair), but not
-// under the 300 or so in which a step's operands are prepared; a tile adds
-// its first step's latency and D's read.
+// Tokens a tile and K slices: the fewest clocks over the pairs' turns. A step takes
+// 4 N clocks of MMA (256 x N x 128 at 8192 products a clock and pair), but not
+// under the 700 or so in which its operands are prepared; a tile adds its first
+// step's latency and D's way out; slices add a kernel and their sums' traffic.
 bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan)
 {
-    const int64_t np = ceil_div(k, kPairK), rt = ceil_div(ceil_div(n, kW8GroupRows), 2);
+    const int64_t np = ceil_div(k, kPairK), groups = ceil_div(n, kW8GroupRows), rt = ceil_div(groups, 2);
+    const int64_t steps = ceil_div(np, kStepRecords);
     double best = 1e300;
     W8a8GemmPlan out;
     for (int N = 32; N <= 256; N += 32) {
@@ -630,17 +677,24 @@ bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan)
         c.smem = std::max<size_t>(smem_bytes(N, c.astages, c.bstages, c.wring), kSmemPerSM / 2 + 1024);   // one CTA per SM
         if (c.smem > kSmemOptIn) continue;
         c.ts = static_cast<int>(ceil_div(m, N));
-        if (rt * c.ts > (int64_t(1) << 30)) continue;
-        c.tiles = static_cast<int>(rt * c.ts);
+        if (rt * c.ts > (int64_t(1) << 24)) continue;
         const int held = max_pairs(c.smem);
         if (held < 1) continue;
-        c.pairs = std::min(held, c.tiles);
         c.image_bytes = static_cast<size_t>(2) * c.ts * np * (N / 2) * 128;
-        const double turns = static_cast<double>(ceil_div(c.tiles, c.pairs));
-        const double cost = turns * (static_cast<double>(np) * std::max(2.0 * N, 300.0) + 1000.0 + 4.0 * N);
-        if (cost < best) {
-            best = cost;
-            out = c;
+        for (int ks = 1; ks <= 16; ++ks) {
+            const int64_t per = ceil_div(steps, ks);
+            if (ks > 1 && (per < 3 || ceil_div(steps, per) != ks || m > 65535)) continue;   // every slice has steps
+            c.kslices = ks;
+            c.tiles = static_cast<int>(rt * c.ts * ks);
+            c.pairs = std::min(held, c.tiles);
+            c.partial_bytes = ks > 1 ? static_cast<size_t>(ks) * m * groups * kW8GroupRows * 4 : 0;
+            const double turns = static_cast<double>(ceil_div(c.tiles, c.pairs));
+            const double cost = turns * (static_cast<double>(per) * std::max(4.0 * N, 700.0) + 2500.0 + 8.0 * N) +
+                                (ks > 1 ? 4000.0 + static_cast<double>(c.partial_bytes) / 1500.0 : 0.0);
+            if (cost < best) {
+                best = cost;
+                out = c;
+            }
         }
     }
     if (out.N == 0) return false;
@@ -695,14 +749,46 @@ cudaError_t launch_w8a8_gemm(const W8a8GemmPlan &plan, const W8a8GemmArgs &args,
     a.N = plan.N;
     a.ts = plan.ts;
     a.tiles = plan.tiles;
+    a.kslices = plan.kslices;
     a.astages = plan.astages;
     a.bstages = plan.bstages;
     a.wring = plan.wring;
-    const void *fn = kernel_of(a.ytype);
+    const bool sliced = plan.kslices > 1;
+    const int64_t rows = static_cast<int64_t>(a.groups) * kW8GroupRows;
+    if (sliced) {
+        a.Y = ximg + plan.image_bytes;
+        a.ldy = rows;
+        a.n = static_cast<int>(rows);
+        a.ytype = Q4_TYPE_F32;
+        a.slice_stride = static_cast<int64_t>(m) * rows;
+    }
+    const void *fn = kernel_of(a.ytype, sliced);
     e = set_max_smem(fn, plan.smem);
     if (e != cudaSuccess) return e;
     void *kargs[] = {&a};
-    return launch_pdl(fn, dim3(static_cast<unsigned>(2 * plan.pairs)), dim3(kThreads), plan.smem, s, kargs, 2);
+    e = launch_pdl(fn, dim3(static_cast<unsigned>(2 * plan.pairs)), dim3(kThreads), plan.smem, s, kargs, 2);
+    if (e != cudaSuccess || !sliced) return e;
+    SliceSumArgs r{};
+    r.partials = static_cast<const float *>(a.Y);
+    r.ld = rows;
+    r.stride = a.slice_stride;
+    r.slices = plan.kslices;
+    r.sx = args.sx;
+    r.row_scale = args.row_scale;
+    r.Y = args.Y;
+    r.ldy = args.ldy;
+    r.n = args.n;
+    const int size = type_size(args.ytype);
+    RowAlign al;
+    al.add(args.Y, args.ldy * size);
+    const bool wide = al.bytes() >= 4 * size;
+    fn = args.ytype == Q4_TYPE_F32   ? wide ? reinterpret_cast<const void *>(&slice_sum_kernel<float, 4>) : reinterpret_cast<const void *>(&slice_sum_kernel<float, 1>)
+         : args.ytype == Q4_TYPE_F16 ? wide ? reinterpret_cast<const void *>(&slice_sum_kernel<__half, 4>) : reinterpret_cast<const void *>(&slice_sum_kernel<__half, 1>)
+         : wide                      ? reinterpret_cast<const void *>(&slice_sum_kernel<__nv_bfloat16, 4>)
+                                     : reinterpret_cast<const void *>(&slice_sum_kernel<__nv_bfloat16, 1>);
+    void *rargs[] = {&r};
+    return launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(args.n, 256 * (wide ? 4 : 1))), static_cast<unsigned>(m)), dim3(256), 0,
+                      s, rargs);
 }
 
 } // namespace q4
