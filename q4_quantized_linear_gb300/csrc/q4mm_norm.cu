@@ -348,12 +348,12 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const NormColumnArgs a
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float s = 0.0f;
     if (c < a.d)
-        for (int p = warp; p < a.rows; p += 32 * 4) {   // four loads in flight
-            float v[4];
+        for (int p = warp; p < a.rows; p += 32 * 16) {   // sixteen loads in flight
+            float v[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = p + 32 * i < a.rows ? a.partials[(p + 32 * i) * a.d + c] : 0.0f;
+            for (int i = 0; i < 16; ++i) v[i] = p + 32 * i < a.rows ? a.partials[(p + 32 * i) * a.d + c] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s += v[i];
+            for (int i = 0; i < 16; ++i) s += v[i];
         }
     part[warp][lane] = s;
     __syncthreads();

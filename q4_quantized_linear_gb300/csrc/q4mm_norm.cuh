@@ -170,9 +170,16 @@ __device__ __forceinline__ void write_partials(float (&acc)[NV][V], float *parti
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * g.G + g.t) * V;
+            if (V % 4 == 0 && (d & 3) == 0) {   // a partial row starts on 16 bytes
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (c + j < d) out[c + j] = acc[i][j];
+                for (int j = 0; j < V; j += 4)
+                    if (c + j < d)
+                        *reinterpret_cast<float4 *>(out + c + j) = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (c + j < d) out[c + j] = acc[i][j];
+            }
         }
         return;
     }

@@ -362,9 +362,11 @@ __global__ void Q4_STREAM_BOUNDS norm_after_bwd_stream_kernel(const NormAfterBwd
         return;
     }
     const RowGroup g{static_cast<int>(threadIdx.x), a.G, blockIdx.x, gridDim.x};
-    // (o + w), times the channel's gate
+    // s (o + w), times the channel's gate
     const auto at = [&](int c, float (&w)[V]) {
         channel_weights<V>(a.w, a.w_off, c, d, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[j] *= a.scale;
         if (a.gate_kind == Q4_GATE_CHANNEL) {
             float gc[V];
             load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
@@ -376,7 +378,7 @@ __global__ void Q4_STREAM_BOUNDS norm_after_bwd_stream_kernel(const NormAfterBwd
     wc.fill(g, at);
     F2 acc[NV][V / 2] = {};
     for (Turn turn(stages, a.m); turn.has(0); turn.next()) {
-        // sums of b^2 and of g w dy b, a row each (a token's gate is taken out: its
+        // sums of b^2 and of s g w dy b, a row each (a token's gate is taken out: its
         // gradient is that sum)
         float s[2 * kRows];
 #pragma unroll
@@ -413,10 +415,10 @@ __global__ void Q4_STREAM_BOUNDS norm_after_bwd_stream_kernel(const NormAfterBwd
             const int64_t row = turn.row[q];
             const float gtok = token ? static_cast<const float *>(a.gate)[row] : 1.0f;
             const float rho = rms_factor(s[2 * q], inv_d, a.eps);
-            if (token && a.dgate && g.t == 0) static_cast<float *>(a.dgate)[row] = a.scale * rho * s[2 * q + 1];
-            // db = scale rho (g dy w - u mean), u = b rho
-            const float mean = gtok * rho * s[2 * q + 1] * inv_d, k = -a.scale * rho * mean * rho;
-            const F2 rho2 = f2(gtok * rho, gtok * rho), back = f2(k, k), scale2 = f2(a.scale, a.scale);
+            if (token && a.dgate && g.t == 0) static_cast<float *>(a.dgate)[row] = rho * s[2 * q + 1];
+            // db = rho (s g dy w - u mean), u = b rho
+            const float mean = gtok * rho * s[2 * q + 1] * inv_d, k = -rho * mean * rho;
+            const F2 rho2 = f2(gtok * rho, gtok * rho), back = f2(k, k);
             T *out = static_cast<T *>(a.dB) + row * a.lddb;
             T *dgr = full && a.dgate ? static_cast<T *>(a.dgate) + row * a.lddg : nullptr;
 #pragma unroll
@@ -427,8 +429,6 @@ __global__ void Q4_STREAM_BOUNDS norm_after_bwd_stream_kernel(const NormAfterBwd
                 Pack<T, V> gv;
                 F2 w[V / 2], o[V / 2];
                 weight_pairs<V, NV>(wc, i, c, at, w);
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) w[j] = f2_mul(w[j], scale2);
                 if constexpr (full) {
                     gv = rs.get<T, V>(turn.slot[q], 2, c);
                     if (dgr) {
