@@ -5,11 +5,17 @@
 // registers leave it idle then, and there are not enough registers to load far
 // ahead. (Issued by one of the row's threads, the copies held up the others at
 // each row's barrier.)
-//   What bounds a CTA then is the way of a row: sums, barrier, root, results.
-// So two rows go that way at once, sharing their barriers and the channels'
-// weights and, backward, their column sums, which stay in registers over the
-// rows. Both passes over a row, its sums and its results, read it from shared
-// memory; then the row's warps release its slot.
+//   Both passes over a row, its sums and its results, read it from shared memory;
+// then the row's warps release its slot. The channels' weights, and backward
+// their sums, stay in registers over the rows. What bounds a CTA then is the way
+// of a row (sums, barrier, root, results) and its instructions, two CTAs an SM
+// side by side; packed fp32 arithmetic took a fifth off them. Two rows at once a
+// CTA, three CTAs an SM with the weights in shared memory, and more rows ahead
+// measured no faster.
+//   GB300, us a call (floor at the measured copy rate): join 4096 x 4096 bf16 with
+// a gate for each value 32 (25); gradient before 8192 x 4096 bf16 48 (40), 2049 x
+// 2560 fp32 20 (12); after 8192 x 4096 bf16, channel gate 46 (30), a gate for each
+// value 58 (50).
 //   Every wait is bounded: after one that ran out the status word says so, the
 // CTA goes through its rows without waiting (its results are void) and leaves
 // when the copies in flight have landed.
@@ -23,8 +29,6 @@ namespace {
 
 constexpr int kErrTimeout = 5;
 constexpr int kMatrices = 3;
-
-constexpr int kRows = 1;             // rows that a CTA works on at once
 
 // The rows blockIdx.x, + gridDim.x, ... of up to three matrices.
 struct RowStream {
@@ -118,31 +122,13 @@ __device__ __forceinline__ void weight_pairs(const Channels<V, NV, true> &ch, in
     for (int j = 0; j < V / 2; ++j) w[j] = f2(f[2 * j], f[2 * j + 1]);
 }
 
-// The rows being worked on: their numbers, slots and phases.
+// Slot and phase of the row being worked on.
 struct Turn {
-    int64_t row[kRows];
-    int slot[kRows];
-    uint32_t phase[kRows];
-    int stages;
-    int64_t m;
-    __device__ __forceinline__ Turn(int stages_, int64_t m_) : stages(stages_), m(m_)
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages)
     {
-#pragma unroll
-        for (int q = 0; q < kRows; ++q) {
-            row[q] = blockIdx.x + static_cast<int64_t>(q) * gridDim.x;
-            slot[q] = q % stages;
-            phase[q] = static_cast<uint32_t>(q / stages) & 1u;
-        }
-    }
-    __device__ __forceinline__ bool has(int q) const { return row[q] < m; }
-    __device__ __forceinline__ void next()
-    {
-#pragma unroll
-        for (int q = 0; q < kRows; ++q) {
-            row[q] += static_cast<int64_t>(kRows) * gridDim.x;
-            slot[q] += kRows;
-            while (slot[q] >= stages) slot[q] -= stages, phase[q] ^= 1u;
-        }
+        if (++slot == stages) slot = 0, phase ^= 1u;
     }
 };
 
@@ -184,66 +170,51 @@ __global__ void Q4_STREAM_BOUNDS norm_after_stream_kernel(const NormAfterArgs a,
     Channels<V, NV, true> wa, wo;
     wa.fill(g, after_at);
     if (a.out.H) wo.fill(g, [&](int c, float (&w)[V]) { channel_weights<V>(a.out.w, a.out.w_off, c, d, w); });
-    for (Turn turn(stages, a.m); turn.has(0); turn.next()) {
-        float s[kRows];
+    Turn turn;
+    for (int64_t row = g.row; row < a.m; row += g.step, turn.next(stages)) {
+        rs.wait(turn.slot, turn.phase);
+        F2 sq = 0;
 #pragma unroll
-        for (int q = 0; q < kRows; ++q) {
-            s[q] = 0.0f;
-            if (!turn.has(q)) continue;
-            rs.wait(turn.slot[q], turn.phase[q]);
-            F2 sq = 0;
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * g.G + g.t) * V;
+            if (c >= d) continue;
+            const Pack<T, V> bv = rs.get<T, V>(turn.slot, 0, c);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * g.G + g.t) * V;
-                if (c >= d) continue;
-                const Pack<T, V> bv = rs.get<T, V>(turn.slot[q], 0, c);
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) sq = f2_fma(pair(bv, j), pair(bv, j), sq);
-            }
-            s[q] = f2_sum(sq);
+            for (int j = 0; j < V / 2; ++j) sq = f2_fma(pair(bv, j), pair(bv, j), sq);
         }
+        float s[1] = {f2_sum(sq)};
         red.sum(s);
-        Pack<T, V> r[kRows][NV];
+        Pack<T, V> r[NV];
+        float f = a.scale * rms_factor(s[0], inv_d, a.eps);
+        if (a.gate_kind == Q4_GATE_TOKEN) f *= static_cast<const float *>(a.gate)[row];
+        T *yr = static_cast<T *>(a.Y) + row * a.ldy;
+        const F2 ff = f2(f, f);
+        sq = 0;
 #pragma unroll
-        for (int q = 0; q < kRows; ++q) {
-            float f = a.scale * rms_factor(s[q], inv_d, a.eps);
-            s[q] = 0.0f;
-            if (!turn.has(q)) continue;
-            if (a.gate_kind == Q4_GATE_TOKEN) f *= static_cast<const float *>(a.gate)[turn.row[q]];
-            T *yr = static_cast<T *>(a.Y) + turn.row[q] * a.ldy;
-            const F2 ff = f2(f, f);
-            F2 sq = 0;
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * g.G + g.t) * V;
+            if (c >= d) continue;
+            const Pack<T, V> bv = rs.get<T, V>(turn.slot, 0, c), rv = rs.get<T, V>(turn.slot, 1, c);
+            F2 w[V / 2], y[V / 2];
+            weight_pairs<V, NV>(wa, i, c, after_at, w);
+            if constexpr (full) {
+                const Pack<T, V> gv = rs.get<T, V>(turn.slot, 2, c);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * g.G + g.t) * V;
-                if (c >= d) continue;
-                const Pack<T, V> bv = rs.get<T, V>(turn.slot[q], 0, c), rv = rs.get<T, V>(turn.slot[q], 1, c);
-                F2 w[V / 2], y[V / 2];
-                weight_pairs<V, NV>(wa, i, c, after_at, w);
-                if constexpr (full) {
-                    const Pack<T, V> gv = rs.get<T, V>(turn.slot[q], 2, c);
-#pragma unroll
-                    for (int j = 0; j < V / 2; ++j) w[j] = f2_mul(w[j], pair(gv, j));
-                }
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) y[j] = f2_fma(f2_mul(pair(bv, j), ff), w[j], pair(rv, j));
-                r[q][i] = pack_pairs<T, V>(y);
-                store_pack<T, V>(yr, c, d, r[q][i]);
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) sq = f2_fma(pair(r[q][i], j), pair(r[q][i], j), sq);
+                for (int j = 0; j < V / 2; ++j) w[j] = f2_mul(w[j], pair(gv, j));
             }
-            s[q] = f2_sum(sq);
-            rs.release(turn.slot[q]);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) y[j] = f2_fma(f2_mul(pair(bv, j), ff), w[j], pair(rv, j));
+            r[i] = pack_pairs<T, V>(y);
+            store_pack<T, V>(yr, c, d, r[i]);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) sq = f2_fma(pair(r[i], j), pair(r[i], j), sq);
         }
+        s[0] = f2_sum(sq);
+        rs.release(turn.slot);
         if (!a.out.H) continue;
         red.sum(s);
-#pragma unroll
-        for (int q = 0; q < kRows; ++q) {
-            if (!turn.has(q)) continue;
-            const T *yr = static_cast<const T *>(a.Y) + turn.row[q] * a.ldy;
-            write_normed<T, V, NV, true>(r[q], [&](int c) { return load_pack<T, V>(yr, c, d); }, rms_factor(s[q], inv_d, a.out_eps),
-                                         a.out, wo, turn.row[q], g, d, red);
-        }
+        write_normed<T, V, NV, true>(r, [&](int c) { return load_pack<T, V>(yr, c, d); }, rms_factor(s[0], inv_d, a.out_eps),
+                                     a.out, wo, row, g, d, red);
     }
 }
 
@@ -274,60 +245,52 @@ __global__ void Q4_STREAM_BOUNDS norm_before_bwd_stream_kernel(const NormBeforeB
     Channels<V, NV, true> wc;
     wc.fill(g, at);
     F2 acc[NV][V / 2] = {};
-    for (Turn turn(stages, a.m); turn.has(0); turn.next()) {
-        float s[2 * kRows];   // of x^2 and of dn x, a row each
+    Turn turn;
+    for (int64_t row = g.row; row < a.m; row += g.step, turn.next(stages)) {
+        float s[2];   // of x^2 and of dn x
+        rs.wait(turn.slot, turn.phase);
+        F2 sq = 0, dot = 0;
 #pragma unroll
-        for (int q = 0; q < kRows; ++q) {
-            s[2 * q] = s[2 * q + 1] = 0.0f;
-            if (!turn.has(q)) continue;
-            rs.wait(turn.slot[q], turn.phase[q]);
-            F2 sq = 0, dot = 0;
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * g.G + g.t) * V;
+            if (c >= d) continue;
+            const Pack<T, V> xv = rs.get<T, V>(turn.slot, 0, c), hv = rs.get<T, V>(turn.slot, 1, c);
+            F2 w[V / 2];
+            weight_pairs<V, NV>(wc, i, c, at, w);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * g.G + g.t) * V;
-                if (c >= d) continue;
-                const Pack<T, V> xv = rs.get<T, V>(turn.slot[q], 0, c), hv = rs.get<T, V>(turn.slot[q], 1, c);
-                F2 w[V / 2];
-                weight_pairs<V, NV>(wc, i, c, at, w);
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                    const F2 f = pair(xv, j);
-                    sq = f2_fma(f, f, sq);
-                    dot = f2_fma(f2_mul(pair(hv, j), w[j]), f, dot);
-                }
+            for (int j = 0; j < V / 2; ++j) {
+                const F2 f = pair(xv, j);
+                sq = f2_fma(f, f, sq);
+                dot = f2_fma(f2_mul(pair(hv, j), w[j]), f, dot);
             }
-            s[2 * q] = f2_sum(sq), s[2 * q + 1] = f2_sum(dot);
         }
+        s[0] = f2_sum(sq), s[1] = f2_sum(dot);
         red.sum(s);
+        // dx = rho dn - x rho^2 mean [+ dr], mean = rho sum(dn x) / d
+        const float rho = rms_factor(s[0], inv_d, a.eps), mean = rho * s[1] * inv_d;
+        const F2 rho2 = f2(rho, rho), back = f2(-rho * mean * rho, -rho * mean * rho);
+        T *out = static_cast<T *>(a.dX) + row * a.lddx;
 #pragma unroll
-        for (int q = 0; q < kRows; ++q) {
-            if (!turn.has(q)) continue;
-            // dx = rho dn - x rho^2 mean [+ dr], mean = rho sum(dn x) / d
-            const float rho = rms_factor(s[2 * q], inv_d, a.eps), mean = rho * s[2 * q + 1] * inv_d;
-            const F2 rho2 = f2(rho, rho), back = f2(-rho * mean * rho, -rho * mean * rho);
-            T *out = static_cast<T *>(a.dX) + turn.row[q] * a.lddx;
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * g.G + g.t) * V;
+            if (c >= d) continue;
+            const Pack<T, V> xv = rs.get<T, V>(turn.slot, 0, c), hv = rs.get<T, V>(turn.slot, 1, c);
+            F2 w[V / 2], o[V / 2];
+            weight_pairs<V, NV>(wc, i, c, at, w);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * g.G + g.t) * V;
-                if (c >= d) continue;
-                const Pack<T, V> xv = rs.get<T, V>(turn.slot[q], 0, c), hv = rs.get<T, V>(turn.slot[q], 1, c);
-                F2 w[V / 2], o[V / 2];
-                weight_pairs<V, NV>(wc, i, c, at, w);
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                    const F2 x = pair(xv, j), h = f2_mul(pair(hv, j), rho2);
-                    acc[i][j] = f2_fma(h, x, acc[i][j]);
-                    o[j] = f2_fma(h, w[j], f2_mul(x, back));
-                }
-                if (residual) {
-                    const Pack<T, V> rv = rs.get<T, V>(turn.slot[q], 2, c);
-#pragma unroll
-                    for (int j = 0; j < V / 2; ++j) o[j] = f2_fma(o[j], f2(1.0f, 1.0f), pair(rv, j));
-                }
-                store_pack<T, V>(out, c, d, pack_pairs<T, V>(o));
+            for (int j = 0; j < V / 2; ++j) {
+                const F2 x = pair(xv, j), h = f2_mul(pair(hv, j), rho2);
+                acc[i][j] = f2_fma(h, x, acc[i][j]);
+                o[j] = f2_fma(h, w[j], f2_mul(x, back));
             }
-            rs.release(turn.slot[q]);
+            if (residual) {
+                const Pack<T, V> rv = rs.get<T, V>(turn.slot, 2, c);
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) o[j] = f2_fma(o[j], f2(1.0f, 1.0f), pair(rv, j));
+            }
+            store_pack<T, V>(out, c, d, pack_pairs<T, V>(o));
         }
+        rs.release(turn.slot);
     }
     if (a.partials) {
         float sums[NV][V];
@@ -377,79 +340,70 @@ __global__ void Q4_STREAM_BOUNDS norm_after_bwd_stream_kernel(const NormAfterBwd
     Channels<V, NV, true> wc;
     wc.fill(g, at);
     F2 acc[NV][V / 2] = {};
-    for (Turn turn(stages, a.m); turn.has(0); turn.next()) {
-        // sums of b^2 and of s g w dy b, a row each (a token's gate is taken out: its
+    Turn turn;
+    for (int64_t row = g.row; row < a.m; row += g.step, turn.next(stages)) {
+        // sums of b^2 and of s g w dy b (a token's gate is taken out: its
         // gradient is that sum)
-        float s[2 * kRows];
+        float s[2];
+        rs.wait(turn.slot, turn.phase);
+        F2 sq = 0, dot = 0;
 #pragma unroll
-        for (int q = 0; q < kRows; ++q) {
-            s[2 * q] = s[2 * q + 1] = 0.0f;
-            if (!turn.has(q)) continue;
-            rs.wait(turn.slot[q], turn.phase[q]);
-            F2 sq = 0, dot = 0;
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * g.G + g.t) * V;
+            if (c >= d) continue;
+            const Pack<T, V> bv = rs.get<T, V>(turn.slot, 0, c), yv = rs.get<T, V>(turn.slot, 1, c);
+            F2 w[V / 2];
+            weight_pairs<V, NV>(wc, i, c, at, w);
+            if constexpr (full) {
+                const Pack<T, V> gv = rs.get<T, V>(turn.slot, 2, c);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * g.G + g.t) * V;
-                if (c >= d) continue;
-                const Pack<T, V> bv = rs.get<T, V>(turn.slot[q], 0, c), yv = rs.get<T, V>(turn.slot[q], 1, c);
-                F2 w[V / 2];
-                weight_pairs<V, NV>(wc, i, c, at, w);
-                if constexpr (full) {
-                    const Pack<T, V> gv = rs.get<T, V>(turn.slot[q], 2, c);
-#pragma unroll
-                    for (int j = 0; j < V / 2; ++j) w[j] = f2_mul(w[j], pair(gv, j));
-                }
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                    const F2 f = pair(bv, j);
-                    sq = f2_fma(f, f, sq);
-                    dot = f2_fma(f2_mul(pair(yv, j), w[j]), f, dot);
-                }
+                for (int j = 0; j < V / 2; ++j) w[j] = f2_mul(w[j], pair(gv, j));
             }
-            s[2 * q] = f2_sum(sq), s[2 * q + 1] = f2_sum(dot);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                const F2 f = pair(bv, j);
+                sq = f2_fma(f, f, sq);
+                dot = f2_fma(f2_mul(pair(yv, j), w[j]), f, dot);
+            }
         }
+        s[0] = f2_sum(sq), s[1] = f2_sum(dot);
         red.sum(s);
+        const float gtok = token ? static_cast<const float *>(a.gate)[row] : 1.0f;
+        const float rho = rms_factor(s[0], inv_d, a.eps);
+        if (token && a.dgate && g.t == 0) static_cast<float *>(a.dgate)[row] = rho * s[1];
+        // db = rho (s g dy w - u mean), u = b rho
+        const float mean = gtok * rho * s[1] * inv_d, k = -rho * mean * rho;
+        const F2 rho2 = f2(gtok * rho, gtok * rho), back = f2(k, k);
+        T *out = static_cast<T *>(a.dB) + row * a.lddb;
+        T *dgr = full && a.dgate ? static_cast<T *>(a.dgate) + row * a.lddg : nullptr;
 #pragma unroll
-        for (int q = 0; q < kRows; ++q) {
-            if (!turn.has(q)) continue;
-            const int64_t row = turn.row[q];
-            const float gtok = token ? static_cast<const float *>(a.gate)[row] : 1.0f;
-            const float rho = rms_factor(s[2 * q], inv_d, a.eps);
-            if (token && a.dgate && g.t == 0) static_cast<float *>(a.dgate)[row] = rho * s[2 * q + 1];
-            // db = rho (s g dy w - u mean), u = b rho
-            const float mean = gtok * rho * s[2 * q + 1] * inv_d, k = -rho * mean * rho;
-            const F2 rho2 = f2(gtok * rho, gtok * rho), back = f2(k, k);
-            T *out = static_cast<T *>(a.dB) + row * a.lddb;
-            T *dgr = full && a.dgate ? static_cast<T *>(a.dgate) + row * a.lddg : nullptr;
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * g.G + g.t) * V;
+            if (c >= d) continue;
+            const Pack<T, V> bv = rs.get<T, V>(turn.slot, 0, c), yv = rs.get<T, V>(turn.slot, 1, c);
+            Pack<T, V> gv;
+            F2 w[V / 2], o[V / 2];
+            weight_pairs<V, NV>(wc, i, c, at, w);
+            if constexpr (full) {
+                gv = rs.get<T, V>(turn.slot, 2, c);
+                if (dgr) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * g.G + g.t) * V;
-                if (c >= d) continue;
-                const Pack<T, V> bv = rs.get<T, V>(turn.slot[q], 0, c), yv = rs.get<T, V>(turn.slot[q], 1, c);
-                Pack<T, V> gv;
-                F2 w[V / 2], o[V / 2];
-                weight_pairs<V, NV>(wc, i, c, at, w);
-                if constexpr (full) {
-                    gv = rs.get<T, V>(turn.slot[q], 2, c);
-                    if (dgr) {
-#pragma unroll
-                        for (int j = 0; j < V / 2; ++j) o[j] = f2_mul(f2_mul(pair(yv, j), rho2), f2_mul(pair(bv, j), w[j]));
-                        store_pack<T, V>(dgr, c, d, pack_pairs<T, V>(o));
-                    }
+                    for (int j = 0; j < V / 2; ++j) o[j] = f2_mul(f2_mul(pair(yv, j), rho2), f2_mul(pair(bv, j), w[j]));
+                    store_pack<T, V>(dgr, c, d, pack_pairs<T, V>(o));
                 }
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                    const F2 b = pair(bv, j);
-                    F2 y = f2_mul(pair(yv, j), rho2);
-                    if constexpr (full) y = f2_mul(y, pair(gv, j));
-                    // the channel's gate, like s, is a factor of the whole column
-                    acc[i][j] = f2_fma(y, b, acc[i][j]);
-                    o[j] = f2_fma(y, w[j], f2_mul(b, back));
-                }
-                store_pack<T, V>(out, c, d, pack_pairs<T, V>(o));
             }
-            rs.release(turn.slot[q]);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                const F2 b = pair(bv, j);
+                F2 y = f2_mul(pair(yv, j), rho2);
+                if constexpr (full) y = f2_mul(y, pair(gv, j));
+                // the channel's gate, like s, is a factor of the whole column
+                acc[i][j] = f2_fma(y, b, acc[i][j]);
+                o[j] = f2_fma(y, w[j], f2_mul(b, back));
+            }
+            store_pack<T, V>(out, c, d, pack_pairs<T, V>(o));
         }
+        rs.release(turn.slot);
     }
     if (a.partials) {
         float sums[NV][V];
