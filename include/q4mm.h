@@ -283,17 +283,22 @@ Q4MM_API size_t q4_w8a8_workspace_size(int64_t m, int64_t k, int64_t n);
 /* The product in 8-bit integers with a scale for each token and each channel:
  *     Y[t][j] = sx[t] * s_j * sum_c xq[t][c] * code[j][c]
  * xq and sx are X coded by q4_a8_quantize's rule, code and s_j as
- * q4_w8_quantize wrote them. Products and, while every partial sum stays below
- * 2^24, sums are exact (at most k * 127^2; beyond that up to 16 rows still add
- * in 32-bit integers, more rows in fp32): then fp32, sx * s_j rounded, times
- * the sum, rounded to ytype.
+ * q4_w8_quantize wrote them. Products are exact, and so are sums whose partial
+ * sums stay below 2^24 (up to 16 tokens' sums always are: they add in 32-bit
+ * integers; more tokens' add in fp32). Then fp32: sx * s_j rounded, times the
+ * sum, rounded to ytype.
  *   W8_packed: as written by q4_w8_quantize for (n, k), 16-byte aligned.
  *   X: device, row t at X + t * ldx, xtype F32, F16 or BF16. Y: device, row t
  *   at Y + t * ldy, ytype F32, F16 or BF16, overwritten. Y's rows may be of any
  *   alignment; 16-byte aligned ones are written 16 bytes an access.
- *   m >= 0 (0 does nothing), n >= 1, 32 <= k <= 131072, k % 32 == 0.
+ *   0 <= m <= 2^20 (0 does nothing), n >= 1, 32 <= k <= 131072, k % 32 == 0.
  *   workspace: device, 256-byte aligned, q4_w8a8_workspace_size(m, k, n) bytes;
- *   calls that can run at the same time need one each. */
+ *   calls that can run at the same time need one each.
+ * Up to 16 tokens run a mat-vec on the warp-level MMA, more the tensor cores'
+ * GEMM, with K cut into slices where the tiles are too few for the device. The
+ * weights are read before the tokens are coded, while kernels in front may
+ * still run: what writes W8_packed must not let its dependents start before it
+ * is done (q4_w8_quantize, copies and other ordinary launches do not). */
 Q4MM_API int q4_w8a8_matmul(const void *W8_packed, const void *X, int64_t ldx, int xtype,
                             void *Y, int64_t ldy, int ytype, int64_t m, int64_t k, int64_t n,
                             void *workspace, size_t workspace_bytes, q4mm_stream_t stream);
@@ -482,7 +487,8 @@ Q4MM_API int q4_build_flags(void);
  * A wait that runs out sets Q4_ERR_DEVICE_TIMEOUT in the device status word
  * and the kernel returns without its result. The decode mat-vec (the default
  * path for m <= 16) then still waits, for at least 0.2 s, for the transfers
- * already issued into its own shared memory, so any limit >= 1 is safe there;
+ * already issued into its own shared memory, so any limit >= 1 is safe there,
+ * and so it is for the int8 product of coded tokens and the norms;
  * the other kernels take the limit as given for every wait and need one well
  * above their transfers' latency (>= 1 ms). */
 Q4MM_API int q4_set_wait_limit_ns(uint64_t ns);

@@ -114,7 +114,7 @@ int norm_after_impl(void *Y, int64_t ldy, void *H, int64_t ldh, int htype, float
     a.m = m, a.d = d;
     a.status = dev.status, a.wait_ns = wait_limit();
     if (next) a.out = NormOut{H, ldh, codes ? 1 : 0, h_scale, w_next, w_offset_next};
-    return cuda_status(launch_norm_after(a, type, vec_of(al, type, codes ? &ca : nullptr, &pa), dev.sm_count, s));
+    return guarded([&] { return cuda_status(launch_norm_after(a, type, vec_of(al, type, codes ? &ca : nullptr, &pa), dev.sm_count, s)); });
 }
 
 } // namespace
@@ -130,7 +130,7 @@ int quantize_rows(int8_t *Xq, int64_t ldq, float *sx, const void *X, int64_t ldx
     a.out = NormOut{Xq, ldq, 1, sx, nullptr, 0.0f};
     a.X = X, a.ldx = ldx, a.plain = 1;
     a.m = m, a.d = k;
-    return cuda_status(launch_norm_before(a, type, vec_of(al, type, &ca), sm_count, s));
+    return guarded([&] { return cuda_status(launch_norm_before(a, type, vec_of(al, type, &ca), sm_count, s)); });
 }
 
 } // namespace q4
@@ -182,8 +182,8 @@ Q4MM_API int q4_norm_before(void *H, int64_t ldh, int htype, float *h_scale, con
     a.out = NormOut{H, ldh, codes ? 1 : 0, h_scale, w, w_offset};
     a.X = X, a.ldx = ldx, a.eps = eps;
     a.m = m, a.d = d;
-    return cuda_status(launch_norm_before(a, type, vec_of(al, type, codes ? &ca : nullptr, &pa), dev.sm_count,
-                                          as_stream(stream)));
+    return guarded([&] { return cuda_status(launch_norm_before(a, type, vec_of(al, type, codes ? &ca : nullptr, &pa), dev.sm_count,
+                                          as_stream(stream))); });
 }
 
 Q4MM_API int q4_norm_after(void *Y, int64_t ldy, const void *R, int64_t ldr, const void *B, int64_t ldb, int type,
@@ -246,7 +246,7 @@ Q4MM_API int q4_norm_before_backward(void *dX, int64_t lddx, float *dw, const vo
     a.partials = dw ? static_cast<float *>(workspace) : nullptr;
     a.status = dev.status, a.wait_ns = wait_limit();
     a.m = m, a.d = d;
-    return cuda_status(launch_norm_before_bwd(a, dw, type, vec_of(al, type, nullptr, &pa), dev.sm_count, s));
+    return guarded([&] { return cuda_status(launch_norm_before_bwd(a, dw, type, vec_of(al, type, nullptr, &pa), dev.sm_count, s)); });
 }
 
 Q4MM_API int q4_norm_after_backward(void *dB, int64_t lddb, float *dw, void *dgate, int64_t lddgate, const void *dY,
@@ -298,7 +298,7 @@ Q4MM_API int q4_norm_after_backward(void *dB, int64_t lddb, float *dw, void *dga
     a.partials = columns ? static_cast<float *>(workspace) : nullptr;
     a.status = dev.status, a.wait_ns = wait_limit();
     a.m = m, a.d = d;
-    return cuda_status(launch_norm_after_bwd(a, dw, type, vec_of(al, type, nullptr, &pa), dev.sm_count, s));
+    return guarded([&] { return cuda_status(launch_norm_after_bwd(a, dw, type, vec_of(al, type, nullptr, &pa), dev.sm_count, s)); });
 }
 
 static bool valid_moe(int64_t tokens, int64_t top_k)
@@ -356,7 +356,7 @@ Q4MM_API int q4_moe_dispatch(void *Xs, int64_t ldxs, int64_t *offsets, int32_t *
         a.bytes = d * size;
         whole = al.bytes() == 16 && a.bytes % 16 == 0;
     }
-    return cuda_status(launch_moe_dispatch(a, whole, dev.sm_count, s));
+    return guarded([&] { return cuda_status(launch_moe_dispatch(a, whole, dev.sm_count, s)); });
 }
 
 Q4MM_API int q4_moe_combine(void *Y, int64_t ldy, const void *base, int64_t ldbase, const void *Ys, int64_t ldys,
@@ -386,7 +386,7 @@ Q4MM_API int q4_moe_combine(void *Y, int64_t ldy, const void *base, int64_t ldba
     a.row_of = row_of, a.weights = weights;
     a.tokens = tokens, a.pairs = tokens * top_k;
     a.top_k = static_cast<int>(top_k), a.d = d;
-    return cuda_status(launch_moe_combine(a, type, vec_of(al, type), as_stream(stream)));
+    return guarded([&] { return cuda_status(launch_moe_combine(a, type, vec_of(al, type), as_stream(stream))); });
 }
 
 Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, const void *dY, int64_t lddy,
@@ -418,7 +418,7 @@ Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, 
     a.row_of = row_of, a.weights = weights;
     a.tokens = tokens, a.pairs = tokens * top_k;
     a.top_k = static_cast<int>(top_k), a.d = d;
-    return cuda_status(launch_moe_combine_bwd(a, type, vec_of(al, type), as_stream(stream)));
+    return guarded([&] { return cuda_status(launch_moe_combine_bwd(a, type, vec_of(al, type), as_stream(stream))); });
 }
 
 } // extern "C"

@@ -13,9 +13,9 @@
 // CTA, three CTAs an SM with the weights in shared memory, and more rows ahead
 // measured no faster.
 //   GB300, us a call (floor at the measured copy rate): join 4096 x 4096 bf16 with
-// a gate for each value 32 (25); gradient before 8192 x 4096 bf16 48 (40), 2049 x
-// 2560 fp32 20 (12); after 8192 x 4096 bf16, channel gate 46 (30), a gate for each
-// value 58 (50).
+// a gate for each value 31 (25), fp32 52 (40); gradient before 8192 x 4096 bf16 47
+// (40), 2049 x 2560 fp32 20 (12); after 8192 x 4096 bf16, channel gate 45 (30), a
+// gate for each value 59 (50).
 //   Every wait is bounded: after one that ran out the status word says so, the
 // CTA goes through its rows without waiting (its results are void) and leaves
 // when the copies in flight have landed.

@@ -30,4 +30,15 @@ struct RowAlign {
     int bytes() const { return static_cast<int>(bits & (~bits + 1)); }
 };
 
+// The library's own bookkeeping (maps of plans and kernel limits) may run out of
+// host memory: no exception leaves a C entry point.
+template <typename F> int guarded(F body) noexcept
+{
+    try {
+        return body();
+    } catch (...) {
+        return Q4_ERR_NO_MEMORY;
+    }
+}
+
 } // namespace q4
