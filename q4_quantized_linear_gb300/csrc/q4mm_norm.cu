@@ -24,11 +24,11 @@
 // rows of a CTA, go to the workspace as one row of partial sums per CTA and
 // are added there in CTA order by a second kernel: the same bits every run.
 //
-// The kernels of this file take few rows, narrow ones and those that do not
-// start on 16 bytes. GB300, us a call (floor), join: 1 x 2560 fp32 3.7 (0.01; the
-// launch, a load, two reductions); 16384 x 1000 bf16 41 (19); 4000 x 4097 bf16, rows
-// on odd boundaries, 90 (19; its 2-byte accesses); 2000 x 16384 fp32 124 (77; values
-// past the registers are read twice).
+// The kernels of this file take few rows, narrow ones and very long ones, and those
+// of matrices whose rows start unlike one another. GB300, us a call (floor), join:
+// 1 x 2560 fp32 3.7 (0.01; the launch, a load, two reductions); 16384 x 1000 bf16 41
+// (19); 12000 x 601 bf16, rows on odd boundaries, 28 (9; 600 aligned 23); 2000 x 16384
+// fp32 124 (77; values past the registers are read twice).
 #include <algorithm>
 #include <cuda_runtime.h>
 
@@ -41,13 +41,13 @@ namespace {
 // 1024 threads an SM.
 __host__ __device__ constexpr int max_threads(int NV) { return NV == 1 ? 1024 : 512; }
 
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, bool ANY>
 __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_before_kernel(const NormBeforeArgs a)
 {
     __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
-    const RowGroup g = row_group(a.G);
+    RowGroup g = row_group(a.G);
     RowReducer red{rbuf, a.G / 32, false};
     if (red.warps > 1) {
         red.clear(static_cast<int>(blockDim.x));
@@ -58,41 +58,43 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
     Channels<V, NV, false> wo;
     for (int64_t row = g.row; row < a.m; row += g.step) {
         const T *xr = static_cast<const T *>(a.X) + row * a.ldx;
+        g.begin<ANY>(xr, d);
         Pack<T, V> x[NV];
-        load_row<T, V, NV>(x, xr, g.t, g.G, d);
+        load_row<T, V, NV>(x, xr, g, d);
+        const float alone = g.loose >= 0 ? load_elem(xr, g.loose) : 0.0f;
         float r = 1.0f;   // x * 1 * 1 is x
         if (!a.plain) {
-            float s[1] = {0.0f};
+            float s[1] = {alone * alone};
 #pragma unroll
             for (int i = 0; i < NV; ++i) s[0] = square_sum<T, V>(x[i], s[0]);
-            for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) s[0] = square_sum<T, V>(load_pack<T, V>(xr, c, d), s[0]);
+            for (int c = g.at<V>(NV); c < g.end; c += g.G * V) s[0] = square_sum<T, V>(load_pack<T, V>(xr, c, d), s[0]);
             red.sum(s);
             r = rms_factor(s[0], inv_d, a.eps);
         }
-        write_normed<T, V, NV, false>(x, [&](int c) { return load_pack<T, V>(xr, c, d); }, r, a.out, wo, row, g, d, red);
+        write_normed<T, V, NV, false, ANY>(x, [&](int c) { return load_pack<T, V>(xr, c, d); }, alone, r, a.out, wo, row, g, d, red);
     }
 }
 
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, bool ANY>
 __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_after_kernel(const NormAfterArgs a)
 {
     __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
-    const RowGroup g = row_group(a.G);
+    RowGroup g = row_group(a.G);
     RowReducer red{rbuf, a.G / 32, false};
     if (red.warps > 1) {
         red.clear(static_cast<int>(blockDim.x));
         __syncthreads();
     }
-    const int d = static_cast<int>(a.d), rest = (NV * g.G + g.t) * V;
+    const int d = static_cast<int>(a.d);
     const float inv_d = 1.0f / static_cast<float>(d);
     const bool full = a.gate_kind == Q4_GATE_FULL;
     const auto after_at = [&](int c, float (&w)[V]) {
-        channel_weights<V>(a.w, a.w_off, c, d, w);
+        channel_weights<V, ANY>(a.w, a.w_off, c, d, w);
         if (a.gate_kind == Q4_GATE_CHANNEL) {
             float gc[V];
-            load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
+            load_params<V, ANY>(static_cast<const float *>(a.gate), c, d, gc);
 #pragma unroll
             for (int j = 0; j < V; ++j) w[j] *= gc[j];
         }
@@ -102,14 +104,17 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
         const T *br = static_cast<const T *>(a.B) + row * a.ldb, *rr = static_cast<const T *>(a.R) + row * a.ldr;
         const T *gr = full ? static_cast<const T *>(a.gate) + row * a.ldg : nullptr;
         T *yr = static_cast<T *>(a.Y) + row * a.ldy;
+        g.begin<ANY>(br, d);
+        const int rest = g.at<V>(NV);
         Pack<T, V> b[NV], r[NV], gt[NV];
-        load_row<T, V, NV>(b, br, g.t, g.G, d);
-        load_row<T, V, NV>(r, rr, g.t, g.G, d);
-        if (full) load_row<T, V, NV>(gt, gr, g.t, g.G, d);
-        float s[1] = {0.0f};
+        load_row<T, V, NV>(b, br, g, d);
+        load_row<T, V, NV>(r, rr, g, d);
+        if (full) load_row<T, V, NV>(gt, gr, g, d);
+        float alone = g.loose >= 0 ? load_elem(br, g.loose) : 0.0f;
+        float s[1] = {alone * alone};
 #pragma unroll
         for (int i = 0; i < NV; ++i) s[0] = square_sum<T, V>(b[i], s[0]);
-        for (int c = rest; c < d; c += g.G * V) s[0] = square_sum<T, V>(load_pack<T, V>(br, c, d), s[0]);
+        for (int c = rest; c < g.end; c += g.G * V) s[0] = square_sum<T, V>(load_pack<T, V>(br, c, d), s[0]);
         red.sum(s);
         float q = a.scale * rms_factor(s[0], inv_d, a.eps);
         if (a.gate_kind == Q4_GATE_TOKEN) q *= static_cast<const float *>(a.gate)[row];
@@ -132,28 +137,35 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c < d) r[i] = join(i, r[i], b[i], gt[i], c);
+            const int c = g.at<V>(i);
+            if (c < g.end) r[i] = join(i, r[i], b[i], gt[i], c);
         }
-        for (int c = rest; c < d; c += g.G * V)
+        for (int c = rest; c < g.end; c += g.G * V)
             join(-1, load_pack<T, V>(rr, c, d), load_pack<T, V>(br, c, d), full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>(), c);
+        if (g.loose >= 0) {
+            float w = channel_weight(a.w, a.w_off, g.loose);
+            if (a.gate_kind == Q4_GATE_CHANNEL) w *= static_cast<const float *>(a.gate)[g.loose];
+            if (full) w *= load_elem(gr, g.loose);
+            alone = store_elem(yr, g.loose, load_elem(rr, g.loose) + alone * q * w);
+            s[0] = fmaf(alone, alone, s[0]);
+        }
         if (a.out.H) {
             red.sum(s);
             const float rho = rms_factor(s[0], inv_d, a.out_eps);
-            write_normed<T, V, NV, false>(r, [&](int c) { return load_pack<T, V>(yr, c, d); }, rho, a.out, wo, row, g, d, red);
+            write_normed<T, V, NV, false, ANY>(r, [&](int c) { return load_pack<T, V>(yr, c, d); }, alone, rho, a.out, wo, row, g, d, red);
         }
     }
 }
 
 // ---------------------------------------------------------------- backward --
 
-template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm_before_bwd_kernel(const NormBeforeBwdArgs a)
+template <typename T, int V, int NV, bool ANY> __global__ void __launch_bounds__(512) norm_before_bwd_kernel(const NormBeforeBwdArgs a)
 {
     extern __shared__ float dsmem[];
     __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
-    const RowGroup g = row_group(a.G);
+    RowGroup g = row_group(a.G);
     RowReducer red{rbuf, a.G / 32, false};
     if (red.warps > 1) {
         red.clear(static_cast<int>(blockDim.x));
@@ -167,19 +179,23 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[i][j] = 0.0f;
+    float alone = 0.0f;   // the column sum outside the vectors
     float *tail = a.partials ? a.partials + static_cast<int64_t>(blockIdx.x) * d : nullptr;
     bool first = true;
-    const auto at = [&](int c, float (&w)[V]) { channel_weights<V>(a.w, a.w_off, c, d, w); };
+    const auto at = [&](int c, float (&w)[V]) { channel_weights<V, ANY>(a.w, a.w_off, c, d, w); };
+    g.begin<ANY>(X + g.row * a.ldx, d);   // the same in all of the group's rows
     Channels<V, NV, true> wc;
     wc.fill(g, at);
     for (int64_t row = g.row; row < a.m; row += g.step) {
         const T *xr = X + row * a.ldx, *hr = DH + row * a.lddh, *rr = DR ? DR + row * a.lddr : nullptr;
         T *out = static_cast<T *>(a.dX) + row * a.lddx;
         Pack<T, V> x[NV], dh[NV], dr[NV];
-        load_row<T, V, NV>(x, xr, g.t, g.G, d);
-        load_row<T, V, NV>(dh, hr, g.t, g.G, d);
-        if (rr) load_row<T, V, NV>(dr, rr, g.t, g.G, d);
-        float s[2] = {0.0f, 0.0f};
+        load_row<T, V, NV>(x, xr, g, d);
+        load_row<T, V, NV>(dh, hr, g, d);
+        if (rr) load_row<T, V, NV>(dr, rr, g, d);
+        float xa = 0.0f, ha = 0.0f, wl = 0.0f;   // outside the vectors
+        if (g.loose >= 0) xa = load_elem(xr, g.loose), ha = load_elem(hr, g.loose), wl = channel_weight(a.w, a.w_off, g.loose);
+        float s[2] = {xa * xa, ha * wl * xa};
         const auto sums = [&](int i, const Pack<T, V> &xv, const Pack<T, V> &hv, int c) {
             float w[V];
             if (i < 0) at(c, w);
@@ -193,10 +209,10 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c < d) sums(i, x[i], dh[i], c);
+            const int c = g.at<V>(i);
+            if (c < g.end) sums(i, x[i], dh[i], c);
         }
-        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) sums(-1, load_pack<T, V>(xr, c, d), load_pack<T, V>(hr, c, d), c);
+        for (int c = g.at<V>(NV); c < g.end; c += g.G * V) sums(-1, load_pack<T, V>(xr, c, d), load_pack<T, V>(hr, c, d), c);
         red.sum(s);
         const float rho = rms_factor(s[0], inv_d, a.eps);
         const float mean = rho * s[1] * inv_d;
@@ -216,10 +232,15 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c < d) one(i, c, x[i], dh[i], dr[i], acc[i]);
+            const int c = g.at<V>(i);
+            if (c < g.end) one(i, c, x[i], dh[i], dr[i], acc[i]);
         }
-        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
+        if (g.loose >= 0) {
+            const float u = xa * rho;
+            alone = fmaf(ha, u, alone);
+            store_elem(out, g.loose, rho * (ha * wl - u * mean) + (rr ? load_elem(rr, g.loose) : 0.0f));
+        }
+        for (int c = g.at<V>(NV); c < g.end; c += g.G * V) {
             float col[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) col[j] = !first && tail && c + j < d ? tail[c + j] : 0.0f;
@@ -232,16 +253,16 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         }
         first = false;
     }
-    if (a.partials) write_partials<V, NV>(acc, a.partials, g, d, dsmem);
+    if (a.partials) write_partials<V, NV, ANY>(acc, alone, a.partials, g, d, dsmem);
 }
 
-template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm_after_bwd_kernel(const NormAfterBwdArgs a)
+template <typename T, int V, int NV, bool ANY> __global__ void __launch_bounds__(512) norm_after_bwd_kernel(const NormAfterBwdArgs a)
 {
     extern __shared__ float dsmem[];
     __shared__ __align__(16) float rbuf[kReduceFloats];
     pdl_wait();
     pdl_launch_dependents();
-    const RowGroup g = row_group(a.G);
+    RowGroup g = row_group(a.G);
     RowReducer red{rbuf, a.G / 32, false};
     if (red.warps > 1) {
         red.clear(static_cast<int>(blockDim.x));
@@ -257,18 +278,20 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[i][j] = 0.0f;
+    float alone = 0.0f;   // the column sum outside the vectors
     float *tail = a.partials ? a.partials + static_cast<int64_t>(blockIdx.x) * d : nullptr;
     bool first = true;
     // (o + w), times the channel's gate
     const auto at = [&](int c, float (&w)[V]) {
-        channel_weights<V>(a.w, a.w_off, c, d, w);
+        channel_weights<V, ANY>(a.w, a.w_off, c, d, w);
         if (channel) {
             float gc[V];
-            load_params<V>(static_cast<const float *>(a.gate), c, d, gc);
+            load_params<V, ANY>(static_cast<const float *>(a.gate), c, d, gc);
 #pragma unroll
             for (int j = 0; j < V; ++j) w[j] *= gc[j];
         }
     };
+    g.begin<ANY>(B + g.row * a.ldb, d);   // the same in all of the group's rows
     Channels<V, NV, true> wc;
     wc.fill(g, at);
     for (int64_t row = g.row; row < a.m; row += g.step) {
@@ -277,12 +300,18 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         T *dgr = full && a.dgate ? static_cast<T *>(a.dgate) + row * a.lddg : nullptr;
         const float gtok = token ? static_cast<const float *>(a.gate)[row] : 1.0f;
         Pack<T, V> b[NV], dy[NV], gt[NV];
-        load_row<T, V, NV>(b, br, g.t, g.G, d);
-        load_row<T, V, NV>(dy, dyr, g.t, g.G, d);
-        if (full) load_row<T, V, NV>(gt, gr, g.t, g.G, d);
+        load_row<T, V, NV>(b, br, g, d);
+        load_row<T, V, NV>(dy, dyr, g, d);
+        if (full) load_row<T, V, NV>(gt, gr, g, d);
         // sums of b^2 and of g w dy b (a token's gate is taken out: its gradient is
         // that sum)
-        float s[2] = {0.0f, 0.0f};
+        float ba = 0.0f, ya = 0.0f, ga = 1.0f, wl = 0.0f;   // outside the vectors
+        if (g.loose >= 0) {
+            ba = load_elem(br, g.loose), ya = load_elem(dyr, g.loose), wl = channel_weight(a.w, a.w_off, g.loose);
+            if (channel) wl *= static_cast<const float *>(a.gate)[g.loose];
+            if (full) ga = load_elem(gr, g.loose);
+        }
+        float s[2] = {ba * ba, ya * ga * wl * ba};
         const auto sums = [&](int i, int c, const Pack<T, V> &bv, const Pack<T, V> &yv, const Pack<T, V> &gv) {
             float w[V];
             if (i < 0) at(c, w);
@@ -296,10 +325,10 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c < d) sums(i, c, b[i], dy[i], gt[i]);
+            const int c = g.at<V>(i);
+            if (c < g.end) sums(i, c, b[i], dy[i], gt[i]);
         }
-        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V)
+        for (int c = g.at<V>(NV); c < g.end; c += g.G * V)
             sums(-1, c, load_pack<T, V>(br, c, d), load_pack<T, V>(dyr, c, d), full ? load_pack<T, V>(gr, c, d) : zero_pack<T, V>());
         red.sum(s);
         const float rho = rms_factor(s[0], inv_d, a.eps);
@@ -324,10 +353,16 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c < d) one(i, c, b[i], dy[i], gt[i], acc[i]);
+            const int c = g.at<V>(i);
+            if (c < g.end) one(i, c, b[i], dy[i], gt[i], acc[i]);
         }
-        for (int c = (NV * g.G + g.t) * V; c < d; c += g.G * V) {
+        if (g.loose >= 0) {
+            const float u = ba * rho, gy = full ? ga * ya : gtok * ya;
+            alone = fmaf(gy, u, alone);
+            store_elem(out, g.loose, q * (gy * wl - u * mean));
+            if (dgr) store_elem(dgr, g.loose, a.scale * ya * u * wl);
+        }
+        for (int c = g.at<V>(NV); c < g.end; c += g.G * V) {
             float col[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) col[j] = !first && tail && c + j < d ? tail[c + j] : 0.0f;
@@ -340,7 +375,7 @@ template <typename T, int V, int NV> __global__ void __launch_bounds__(512) norm
         }
         first = false;
     }
-    if (a.partials) write_partials<V, NV>(acc, a.partials, g, d, dsmem);
+    if (a.partials) write_partials<V, NV, ANY>(acc, alone, a.partials, g, d, dsmem);
 }
 
 // Column sums of the partials: 32 columns a CTA, the rows dealt to 32 warps
@@ -381,18 +416,18 @@ struct RowPlan {
     int64_t ctas;
 };
 
-// Vectors a thread, threads a row and a CTA. `wide`: 16 bytes an access, with 1,
-// 2 or 4 vectors a thread, else (4 bytes or an element) 2, 4 or 8. Few rows take many threads each; many
-// take a warp each where that holds them, else CTAs of about 256 threads: their
-// barriers stop fewer others, and several fit on an SM. A row longer than 512
-// threads hold is finished by the kernels' loops.
-RowPlan plan_rows(int V, bool wide, int64_t m, int64_t d, bool backward, int64_t sm_count)
+// Vectors a thread, threads a row and a CTA. With 16-byte vectors 1, 2 or 4 a
+// thread, else 2, 4 or 8 elements. Few rows take many threads each; many take a
+// warp each where that holds them, else CTAs of about 256 threads: their barriers
+// stop fewer others, and several fit on an SM. A row longer than 512 threads hold
+// is finished by the kernels' loops.
+RowPlan plan_rows(const RowAccess &acc, int64_t m, int64_t d, bool backward, int64_t sm_count)
 {
     RowPlan p;
-    p.V = V;
-    const int64_t vecs = ceil_div(d, V);
-    const int nv[3][3] = {{2, 4, 8}, {2, 4, 8}, {1, 2, 4}};
-    const int *n = nv[wide ? 2 : V - 1];
+    p.V = acc.vec;
+    const int64_t vecs = acc.any ? std::max<int64_t>(1, d / acc.vec) : ceil_div(d, acc.vec);   // at most
+    const bool wide = acc.vec > 1;
+    const int n[3] = {wide ? 1 : 2, wide ? 2 : 4, wide ? 4 : 8};
     const bool few = m <= 304;
     p.NV = n[2];
     p.G = 32;
@@ -410,49 +445,51 @@ RowPlan plan_rows(int V, bool wide, int64_t m, int64_t d, bool backward, int64_t
     p.threads = p.G == 32 ? (few ? 64 : 256) : p.G;
     // Forward a CTA takes its rows once and leaves: CTAs of other rows fill the
     // time that its loads take. Backward as many as the device holds at the least
-    // (1024 threads an SM), for the column sums.
+    // (1024 threads an SM), for the column sums; a multiple of kRowStep, so that
+    // a group's rows all start alike.
     p.ctas = std::min<int64_t>(ceil_div(m, p.threads / p.G),
-                               backward ? std::min<int64_t>(kNormPartials, sm_count * (1024 / p.threads)) : (int64_t(1) << 30));
+                               backward ? round_row_step(std::min<int64_t>(kNormPartials, sm_count * (1024 / p.threads)))
+                                        : (int64_t(1) << 30));
     return p;
 }
 
-template <template <typename, int, int> class K, typename T, typename Args>
-cudaError_t launch_rows_v(const RowPlan &p, bool wide, Args a, size_t smem, cudaStream_t s)
+template <template <typename, int, int, bool> class K, typename T, typename Args>
+cudaError_t launch_rows_v(const RowPlan &p, bool any, Args a, size_t smem, cudaStream_t s)
 {
     constexpr int W = 16 / sizeof(T);
     const void *fn = nullptr;
-    if (wide) fn = p.NV == 1 ? K<T, W, 1>::fn() : p.NV == 2 ? K<T, W, 2>::fn() : K<T, W, 4>::fn();
-    else if (sizeof(T) == 2 && p.V == 2) fn = p.NV == 2 ? K<T, 2, 2>::fn() : p.NV == 4 ? K<T, 2, 4>::fn() : K<T, 2, 8>::fn();
-    else fn = p.NV == 2 ? K<T, 1, 2>::fn() : p.NV == 4 ? K<T, 1, 4>::fn() : K<T, 1, 8>::fn();
+    if (any) fn = p.NV == 1 ? K<T, W, 1, true>::fn() : p.NV == 2 ? K<T, W, 2, true>::fn() : K<T, W, 4, true>::fn();
+    else if (p.V == W) fn = p.NV == 1 ? K<T, W, 1, false>::fn() : p.NV == 2 ? K<T, W, 2, false>::fn() : K<T, W, 4, false>::fn();
+    else fn = p.NV == 2 ? K<T, 1, 2, false>::fn() : p.NV == 4 ? K<T, 1, 4, false>::fn() : K<T, 1, 8, false>::fn();
     a.G = p.G;
     void *args[] = {&a};
     return launch_pdl(fn, dim3(static_cast<unsigned>(p.ctas)), dim3(static_cast<unsigned>(p.threads)), smem, s, args);
 }
-template <template <typename, int, int> class K, typename Args>
-cudaError_t launch_rows(int type, const RowPlan &p, bool wide, const Args &a, size_t smem, cudaStream_t s)
+template <template <typename, int, int, bool> class K, typename Args>
+cudaError_t launch_rows(int type, const RowPlan &p, bool any, const Args &a, size_t smem, cudaStream_t s)
 {
     switch (type) {
-    case Q4_TYPE_F32: return launch_rows_v<K, float>(p, wide, a, smem, s);
-    case Q4_TYPE_F16: return launch_rows_v<K, __half>(p, wide, a, smem, s);
-    default: return launch_rows_v<K, __nv_bfloat16>(p, wide, a, smem, s);
+    case Q4_TYPE_F32: return launch_rows_v<K, float>(p, any, a, smem, s);
+    case Q4_TYPE_F16: return launch_rows_v<K, __half>(p, any, a, smem, s);
+    default: return launch_rows_v<K, __nv_bfloat16>(p, any, a, smem, s);
     }
 }
 
-template <typename T, int V, int NV> struct BeforeKernel {
-    static const void *fn() { return reinterpret_cast<const void *>(&norm_before_kernel<T, V, NV>); }
+template <typename T, int V, int NV, bool ANY> struct BeforeKernel {
+    static const void *fn() { return reinterpret_cast<const void *>(&norm_before_kernel<T, V, NV, ANY>); }
 };
-template <typename T, int V, int NV> struct AfterKernel {
-    static const void *fn() { return reinterpret_cast<const void *>(&norm_after_kernel<T, V, NV>); }
+template <typename T, int V, int NV, bool ANY> struct AfterKernel {
+    static const void *fn() { return reinterpret_cast<const void *>(&norm_after_kernel<T, V, NV, ANY>); }
 };
-template <typename T, int V, int NV> struct BeforeBwdKernel {
-    static const void *fn() { return reinterpret_cast<const void *>(&norm_before_bwd_kernel<T, V, NV>); }
+template <typename T, int V, int NV, bool ANY> struct BeforeBwdKernel {
+    static const void *fn() { return reinterpret_cast<const void *>(&norm_before_bwd_kernel<T, V, NV, ANY>); }
 };
-template <typename T, int V, int NV> struct AfterBwdKernel {
-    static const void *fn() { return reinterpret_cast<const void *>(&norm_after_bwd_kernel<T, V, NV>); }
+template <typename T, int V, int NV, bool ANY> struct AfterBwdKernel {
+    static const void *fn() { return reinterpret_cast<const void *>(&norm_after_bwd_kernel<T, V, NV, ANY>); }
 };
 
 // Shared memory in which the groups of a CTA meet (one group: none).
-size_t partial_smem(const RowPlan &p) { return p.threads > p.G ? sizeof(float) * p.threads * p.NV * p.V : 0; }
+size_t partial_smem(const RowPlan &p, int64_t d) { return p.threads > p.G ? sizeof(float) * (p.threads / p.G) * d : 0; }
 
 cudaError_t launch_columns(NormColumnArgs a, cudaStream_t s)
 {
@@ -463,35 +500,32 @@ cudaError_t launch_columns(NormColumnArgs a, cudaStream_t s)
 
 } // namespace
 
-cudaError_t launch_norm_before(const NormBeforeArgs &a, int type, int vec, int sm_count, cudaStream_t s)
+cudaError_t launch_norm_before(const NormBeforeArgs &a, int type, const RowAccess &acc, int sm_count, cudaStream_t s)
 {
-    const bool wide = vec * type_size(type) == 16;
-    const RowPlan p = plan_rows(vec, wide, a.m, a.d, false, sm_count);
-    return launch_rows<BeforeKernel>(type, p, wide, a, 0, s);
+    const RowPlan p = plan_rows(acc, a.m, a.d, false, sm_count);
+    return launch_rows<BeforeKernel>(type, p, acc.any, a, 0, s);
 }
 
-cudaError_t launch_norm_after(const NormAfterArgs &a, int type, int vec, int sm_count, cudaStream_t s)
+cudaError_t launch_norm_after(const NormAfterArgs &a, int type, const RowAccess &acc, int sm_count, cudaStream_t s)
 {
-    const bool wide = vec * type_size(type) == 16;
     NormStreamPlan sp;
-    if (wide && plan_norm_stream(a.m, a.d, type, a.gate_kind == Q4_GATE_FULL ? 3 : 2, sm_count, &sp))
+    if (acc.vec > 1 && plan_norm_stream(a.m, a.d, type, acc.any, a.gate_kind == Q4_GATE_FULL ? 3 : 2, sm_count, &sp))
         return launch_norm_after_stream(sp, a, type, s);
-    const RowPlan p = plan_rows(vec, wide, a.m, a.d, false, sm_count);
-    return launch_rows<AfterKernel>(type, p, wide, a, 0, s);
+    const RowPlan p = plan_rows(acc, a.m, a.d, false, sm_count);
+    return launch_rows<AfterKernel>(type, p, acc.any, a, 0, s);
 }
 
-cudaError_t launch_norm_before_bwd(const NormBeforeBwdArgs &a, float *dw, int type, int vec, int sm_count, cudaStream_t s)
+cudaError_t launch_norm_before_bwd(const NormBeforeBwdArgs &a, float *dw, int type, const RowAccess &acc, int sm_count, cudaStream_t s)
 {
-    const bool wide = vec * type_size(type) == 16;
     NormStreamPlan sp;
     cudaError_t e;
     int64_t ctas;
-    if (wide && plan_norm_stream(a.m, a.d, type, a.dR ? 3 : 2, sm_count, &sp)) {
+    if (acc.vec > 1 && plan_norm_stream(a.m, a.d, type, acc.any, a.dR ? 3 : 2, sm_count, &sp)) {
         e = launch_norm_before_bwd_stream(sp, a, type, s);
         ctas = sp.ctas;
     } else {
-        const RowPlan p = plan_rows(vec, wide, a.m, a.d, true, sm_count);
-        e = launch_rows<BeforeBwdKernel>(type, p, wide, a, partial_smem(p), s);
+        const RowPlan p = plan_rows(acc, a.m, a.d, true, sm_count);
+        e = launch_rows<BeforeBwdKernel>(type, p, acc.any, a, partial_smem(p, a.d), s);
         ctas = p.ctas;
     }
     if (e != cudaSuccess || !dw) return e;
@@ -504,18 +538,17 @@ cudaError_t launch_norm_before_bwd(const NormBeforeBwdArgs &a, float *dw, int ty
     return launch_columns(c, s);
 }
 
-cudaError_t launch_norm_after_bwd(const NormAfterBwdArgs &a, float *dw, int type, int vec, int sm_count, cudaStream_t s)
+cudaError_t launch_norm_after_bwd(const NormAfterBwdArgs &a, float *dw, int type, const RowAccess &acc, int sm_count, cudaStream_t s)
 {
-    const bool wide = vec * type_size(type) == 16;
     NormStreamPlan sp;
     cudaError_t e;
     int64_t ctas;
-    if (wide && plan_norm_stream(a.m, a.d, type, a.gate_kind == Q4_GATE_FULL ? 3 : 2, sm_count, &sp)) {
+    if (acc.vec > 1 && plan_norm_stream(a.m, a.d, type, acc.any, a.gate_kind == Q4_GATE_FULL ? 3 : 2, sm_count, &sp)) {
         e = launch_norm_after_bwd_stream(sp, a, type, s);
         ctas = sp.ctas;
     } else {
-        const RowPlan p = plan_rows(vec, wide, a.m, a.d, true, sm_count);
-        e = launch_rows<AfterBwdKernel>(type, p, wide, a, partial_smem(p), s);
+        const RowPlan p = plan_rows(acc, a.m, a.d, true, sm_count);
+        e = launch_rows<AfterBwdKernel>(type, p, acc.any, a, partial_smem(p, a.d), s);
         ctas = p.ctas;
     }
     if (e != cudaSuccess || !a.partials) return e;

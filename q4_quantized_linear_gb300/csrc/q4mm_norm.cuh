@@ -9,10 +9,28 @@
 namespace q4 {
 namespace {
 
-// Which rows this thread works on, and where in them.
+// Which rows this thread works on, and where in them. Where rows start anywhere
+// (ANY) their vectors are the aligned 16-byte words inside them, the same elements
+// in every matrix of the call; the few elements before and after those are dealt to
+// lanes of the row's last warp, one each. (Edge vectors masked and stored element
+// by element were on every row's way: join 4000 x 3999 bf16 49 us, so 34.)
 struct RowGroup {
     int t, G;                 // thread of the row, threads of a row
     int64_t row, step;        // first row, rows between two of this group's
+    int first = 0, end = 0;   // elements of the vectors
+    int loose = -1;           // this thread's element outside them, or -1
+
+    template <int V> __device__ __forceinline__ int at(int i) const { return first + (i * G + t) * V; }   // vector i
+    template <bool ANY, typename T> __device__ __forceinline__ void begin(const T *r, int d)
+    {
+        end = d;
+        if (!ANY) return;
+        constexpr int V = 16 / sizeof(T);
+        first = min(d, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(r) & 15)) & 15) / static_cast<int>(sizeof(T)));
+        end = first + (d - first) / V * V;
+        const int l = t - (G - 32);
+        loose = l < 0 ? -1 : l < first ? l : end + l - first < d ? end + l - first : -1;
+    }
 };
 __device__ __forceinline__ RowGroup row_group(int G)
 {
@@ -31,12 +49,13 @@ __device__ __forceinline__ RowGroup row_group(int G)
 // more loads than the rows themselves.
 template <int V, int NV, bool KEEP> struct Channels {
     static constexpr bool kKept = KEEP && NV * V <= 16;
-    float kept[kKept ? NV : 1][V];
+    float kept[kKept ? NV : 1][V] = {};
     template <typename F> __device__ __forceinline__ void fill(const RowGroup &g, F at)
     {
         if constexpr (kKept) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) at((i * g.G + g.t) * V, kept[i]);
+            for (int i = 0; i < NV; ++i)
+                if (g.template at<V>(i) < g.end) at(g.template at<V>(i), kept[i]);
         }
     }
     // those of vector i, at element c
@@ -52,20 +71,20 @@ template <int V, int NV, bool KEEP> struct Channels {
 };
 
 template <typename T, int V, int NV>
-__device__ __forceinline__ void load_row(Pack<T, V> (&x)[NV], const T *row, int t, int G, int d)
+__device__ __forceinline__ void load_row(Pack<T, V> (&x)[NV], const T *row, const RowGroup &g, int d)
 {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * G + t) * V;
-        x[i] = c < d ? load_pack<T, V>(row, c, d) : zero_pack<T, V>();
+        const int c = g.at<V>(i);
+        x[i] = c < g.end ? load_pack<T, V>(row, c, d) : zero_pack<T, V>();
     }
 }
 
 // (o + w) of V channels.
-template <int V> __device__ __forceinline__ void channel_weights(const float *w, float off, int c, int d, float out[V])
+template <int V, bool ANY> __device__ __forceinline__ void channel_weights(const float *w, float off, int c, int d, float out[V])
 {
     if (w) {
-        load_params<V>(w, c, d, out);
+        load_params<V, ANY>(w, c, d, out);
 #pragma unroll
         for (int j = 0; j < V; ++j) out[j] += off;
     } else {
@@ -73,6 +92,9 @@ template <int V> __device__ __forceinline__ void channel_weights(const float *w,
         for (int j = 0; j < V; ++j) out[j] = 1.0f;
     }
 }
+
+// (o + w) of one channel.
+__device__ __forceinline__ float channel_weight(const float *w, float off, int c) { return w ? __ldg(w + c) + off : 1.0f; }
 
 template <typename T, int V> __device__ __forceinline__ float square_sum(const Pack<T, V> &x, float s)
 {
@@ -90,22 +112,23 @@ template <int V> __device__ __forceinline__ uint32_t largest(const float h[V], i
     for (int j = 0; j < V; ++j) mb = max(mb, c + j < d ? abs_bits(h[j]) : 0u);
     return mb;
 }
-template <int V> __device__ __forceinline__ void store_codes(int8_t *row, int c, int d, const float h[V], float factor)
+template <int V, bool ANY> __device__ __forceinline__ void store_codes(int8_t *row, int c, int d, const float h[V], float factor)
 {
     int q[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) q[j] = code_of(h[j], factor);
-    store_pack<int8_t, V>(row, c, d, pack_codes<V>(q));
+    store_pack<int8_t, V, ANY>(row, c, d, pack_codes<V>(q));
 }
 
 // The second half of a row whose sum is known: h = x * r * (o + w), stored as
-// values or coded. Vector i is x[i]; vectors past NV are `again(c)`.
-template <typename T, int V, int NV, bool KEEP, typename Again>
-__device__ __forceinline__ void write_normed(const Pack<T, V> (&x)[NV], Again again, float r, const NormOut &o,
+// values or coded. Vector i is x[i]; vectors past NV are `again(c)`; `alone` is the
+// thread's element outside the vectors.
+template <typename T, int V, int NV, bool KEEP, bool ANY, typename Again>
+__device__ __forceinline__ void write_normed(const Pack<T, V> (&x)[NV], Again again, float alone, float r, const NormOut &o,
                                              const Channels<V, NV, KEEP> &ch, int64_t row, const RowGroup &g, int d,
                                              RowReducer &red)
 {
-    const auto at = [&](int c, float (&w)[V]) { channel_weights<V>(o.w, o.w_off, c, d, w); };
+    const auto at = [&](int c, float (&w)[V]) { channel_weights<V, ANY>(o.w, o.w_off, c, d, w); };
     const auto normed = [&](int i, const Pack<T, V> &v, int c, float (&h)[V]) {
         float w[V];
         if (i < 0) at(c, w);
@@ -113,32 +136,34 @@ __device__ __forceinline__ void write_normed(const Pack<T, V> (&x)[NV], Again ag
 #pragma unroll
         for (int j = 0; j < V; ++j) h[j] = elem(v, j) * r * w[j];
     };
-    const int rest = (NV * g.G + g.t) * V;
+    const int rest = g.at<V>(NV);
+    const float ha = g.loose >= 0 ? alone * r * channel_weight(o.w, o.w_off, g.loose) : 0.0f;
     float h[V];
     if (!o.codes) {
         T *out = static_cast<T *>(o.H) + row * o.ldh;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (c >= d) continue;
+            const int c = g.at<V>(i);
+            if (c >= g.end) continue;
             normed(i, x[i], c, h);
             store_pack<T, V>(out, c, d, pack_of<T, V>(h));
         }
-        for (int c = rest; c < d; c += g.G * V) {
+        for (int c = rest; c < g.end; c += g.G * V) {
             normed(-1, again(c), c, h);
             store_pack<T, V>(out, c, d, pack_of<T, V>(h));
         }
+        if (g.loose >= 0) store_elem<T>(out, g.loose, ha);
         return;
     }
-    uint32_t mb = 0u;
+    uint32_t mb = abs_bits(ha);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * g.G + g.t) * V;
-        if (c >= d) continue;
+        const int c = g.at<V>(i);
+        if (c >= g.end) continue;
         normed(i, x[i], c, h);
         mb = largest<V>(h, c, d, mb);
     }
-    for (int c = rest; c < d; c += g.G * V) {
+    for (int c = rest; c < g.end; c += g.G * V) {
         normed(-1, again(c), c, h);
         mb = largest<V>(h, c, d, mb);
     }
@@ -147,30 +172,32 @@ __device__ __forceinline__ void write_normed(const Pack<T, V> (&x)[NV], Again ag
     int8_t *out = static_cast<int8_t *>(o.H) + row * o.ldh;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * g.G + g.t) * V;
-        if (c >= d) continue;
+        const int c = g.at<V>(i);
+        if (c >= g.end) continue;
         normed(i, x[i], c, h);
-        store_codes<V>(out, c, d, h, cs.factor);
+        store_codes<V, ANY>(out, c, d, h, cs.factor);
     }
-    for (int c = rest; c < d; c += g.G * V) {
+    for (int c = rest; c < g.end; c += g.G * V) {
         normed(-1, again(c), c, h);
-        store_codes<V>(out, c, d, h, cs.factor);
+        store_codes<V, ANY>(out, c, d, h, cs.factor);
     }
+    if (g.loose >= 0) out[g.loose] = static_cast<int8_t>(code_of(ha, cs.factor));
 }
 
 // Adds the CTA's groups' column sums (one group: its registers as they are)
 // into row blockIdx.x of the partials. The tail past the registers has been
 // added there already.
-template <int V, int NV>
-__device__ __forceinline__ void write_partials(float (&acc)[NV][V], float *partials, const RowGroup &g, int d, float *smem)
+template <int V, int NV, bool ANY>
+__device__ __forceinline__ void write_partials(float (&acc)[NV][V], float alone, float *partials, const RowGroup &g, int d,
+                                               float *smem)
 {
     float *out = partials + static_cast<int64_t>(blockIdx.x) * d;
     const int groups = static_cast<int>(blockDim.x) / g.G;
     if (groups == 1) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * g.G + g.t) * V;
-            if (V % 4 == 0 && (d & 3) == 0) {   // a partial row starts on 16 bytes
+            const int c = g.at<V>(i);
+            if (!ANY && V % 4 == 0 && (d & 3) == 0) {   // a partial row starts on 16 bytes
 #pragma unroll
                 for (int j = 0; j < V; j += 4)
                     if (c + j < d)
@@ -178,17 +205,22 @@ __device__ __forceinline__ void write_partials(float (&acc)[NV][V], float *parti
             } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    if (c + j < d) out[c + j] = acc[i][j];
+                    if (c + j < g.end) out[c + j] = acc[i][j];
             }
         }
+        if (g.loose >= 0) out[g.loose] = alone;
         return;
     }
-    const int width = g.G * NV * V;   // >= d
+    const int width = d;
     const int mine = static_cast<int>(threadIdx.x) / g.G;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) smem[mine * width + (i * g.G + g.t) * V + j] = acc[i][j];
+        for (int j = 0; j < V; ++j) {
+            const int c = g.at<V>(i) + j;
+            if (c < g.end) smem[mine * width + c] = acc[i][j];
+        }
+    if (g.loose >= 0) smem[mine * width + g.loose] = alone;
     __syncthreads();
     for (int c = threadIdx.x; c < d; c += blockDim.x) {
         float s = 0.0f;

@@ -9,6 +9,11 @@ namespace q4 {
 // Most rows of partial column sums of a backward call.
 constexpr int kNormPartials = 608;
 
+// Rows that are a multiple of this apart start alike within 16 bytes, whatever
+// their stride (elements have 2 bytes or more).
+constexpr int64_t kRowStep = 8;
+inline int64_t round_row_step(int64_t rows) { return rows < kRowStep ? kRowStep : rows / kRowStep * kRowStep; }
+
 // Where a normed row goes: values of the input's type, or int8 codes and a
 // scale per row. H == nullptr: nowhere.
 struct NormOut {
@@ -94,19 +99,20 @@ struct NormStreamPlan {
     int stages = 0;
     int64_t ctas = 0;
     size_t smem = 0;
+    bool any = false;      // rows start anywhere
 };
-// False where they do not apply: rows that are no multiple of 16 bytes, short
-// or very long ones, few rows.
-bool plan_norm_stream(int64_t m, int64_t d, int type, int matrices, int sm_count, NormStreamPlan *plan);
+// False where they do not apply: short or very long rows, few rows.
+bool plan_norm_stream(int64_t m, int64_t d, int type, bool any, int matrices, int sm_count, NormStreamPlan *plan);
 cudaError_t launch_norm_after_stream(const NormStreamPlan &p, const NormAfterArgs &a, int type, cudaStream_t s);
+cudaError_t launch_norm_after_stream_any(const NormStreamPlan &p, const NormAfterArgs &a, int type, cudaStream_t s);
 cudaError_t launch_norm_before_bwd_stream(const NormStreamPlan &p, const NormBeforeBwdArgs &a, int type, cudaStream_t s);
+cudaError_t launch_norm_before_bwd_stream_any(const NormStreamPlan &p, const NormBeforeBwdArgs &a, int type, cudaStream_t s);
 cudaError_t launch_norm_after_bwd_stream(const NormStreamPlan &p, const NormAfterBwdArgs &a, int type, cudaStream_t s);
+cudaError_t launch_norm_after_bwd_stream_any(const NormStreamPlan &p, const NormAfterBwdArgs &a, int type, cudaStream_t s);
 
-// `vec`: elements of one access; every row of every matrix starts on a
-// multiple of vec elements' bytes.
-cudaError_t launch_norm_before(const NormBeforeArgs &a, int type, int vec, int sm_count, cudaStream_t s);
-cudaError_t launch_norm_after(const NormAfterArgs &a, int type, int vec, int sm_count, cudaStream_t s);
-cudaError_t launch_norm_before_bwd(const NormBeforeBwdArgs &a, float *dw, int type, int vec, int sm_count, cudaStream_t s);
-cudaError_t launch_norm_after_bwd(const NormAfterBwdArgs &a, float *dw, int type, int vec, int sm_count, cudaStream_t s);
+cudaError_t launch_norm_before(const NormBeforeArgs &a, int type, const RowAccess &acc, int sm_count, cudaStream_t s);
+cudaError_t launch_norm_after(const NormAfterArgs &a, int type, const RowAccess &acc, int sm_count, cudaStream_t s);
+cudaError_t launch_norm_before_bwd(const NormBeforeBwdArgs &a, float *dw, int type, const RowAccess &acc, int sm_count, cudaStream_t s);
+cudaError_t launch_norm_after_bwd(const NormAfterBwdArgs &a, float *dw, int type, const RowAccess &acc, int sm_count, cudaStream_t s);
 
 } // namespace q4

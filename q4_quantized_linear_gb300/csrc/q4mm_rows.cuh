@@ -146,8 +146,8 @@ template <typename T, int V> __device__ __forceinline__ Pack<T, V> zero_pack()
     for (int i = 0; i < Pack<T, V>::kWords; ++i) p.w[i] = 0;
     return p;
 }
-// Elements c .. c + V - 1 of a row of d, zeros past its end. The row is
-// aligned to the pack and c a multiple of V.
+// Elements c .. c + V - 1 of a row of d, zeros past its end. row + c is aligned to
+// the pack.
 template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(const T *row, int64_t c, int64_t d)
 {
     using A = typename AccessOf<static_cast<int>(sizeof(T)) * V>::type;
@@ -167,10 +167,12 @@ template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(con
     }
     return p;
 }
-template <typename T, int V> __device__ __forceinline__ void store_pack(T *row, int64_t c, int64_t d, const Pack<T, V> &p)
+template <typename T, int V, bool ANY = false>
+__device__ __forceinline__ void store_pack(T *row, int64_t c, int64_t d, const Pack<T, V> &p)
 {
     using A = typename AccessOf<static_cast<int>(sizeof(T)) * V>::type;
-    if (c + V <= d) {
+    // ANY: codes beside values whose vectors are aligned; theirs may not be
+    if (c + V <= d && (!ANY || (reinterpret_cast<uintptr_t>(row + c) & (sizeof(A) - 1)) == 0)) {
         A v;
         memcpy(&v, p.w, sizeof(A));
         *reinterpret_cast<A *>(row + c) = v;
@@ -221,11 +223,43 @@ template <typename T> __device__ __forceinline__ Pack<T, 8> load_anywhere(const 
     return p;
 }
 
-// V fp32 parameters (weights or gates of the channels) at c, `other` past the
-// end. Their base is aligned to min(16, 4 V) bytes.
-template <int V> __device__ __forceinline__ void load_params(const float *p, int64_t c, int64_t d, float out[V])
+// Element c of a row, and its store; the stored value.
+template <typename T> __device__ __forceinline__ float load_elem(const T *row, int c) { return elem(load_pack<T, 1>(row, c, c + 1), 0); }
+template <typename T> __device__ __forceinline__ float store_elem(T *row, int c, float v)
 {
-    if (c + V <= d) {
+    const float f[1] = {v};
+    const Pack<T, 1> p = pack_of<T, 1>(f);
+    store_pack<T, 1>(row, c, c + 1, p);
+    return elem(p, 0);
+}
+
+// V fp32 parameters (weights or gates of the channels) at c, zeros past the end.
+// Their base is aligned to min(16, 4 V) bytes; ANY: it and c are not, all V are in
+// the row, and the aligned words that hold one of them are shifted.
+template <int V, bool ANY = false> __device__ __forceinline__ void load_params(const float *p, int64_t c, int64_t d, float out[V])
+{
+    if constexpr (ANY) {
+        constexpr int W = V / 4 + 1;
+        const int by = static_cast<int>(reinterpret_cast<uintptr_t>(p + c) >> 2 & 3);   // the same for a whole row
+        const float4 *in = reinterpret_cast<const float4 *>(p + c - by);
+        float f[4 * W];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k < W - 1 || by) v = __ldg(in + k);
+            f[4 * k] = v.x, f[4 * k + 1] = v.y, f[4 * k + 2] = v.z, f[4 * k + 3] = v.w;
+        }
+        const auto take = [&](int s) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) out[i] = f[s + i];
+        };
+        switch (by) {
+        case 0: take(0); break;
+        case 1: take(1); break;
+        case 2: take(2); break;
+        default: take(3); break;
+        }
+    } else if (c + V <= d) {
         if constexpr (V % 4 == 0) {
 #pragma unroll
             for (int i = 0; i < V; i += 4) {

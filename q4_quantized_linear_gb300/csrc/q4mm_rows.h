@@ -22,12 +22,28 @@ inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<ui
 // every matrix added so far starts.
 struct RowAlign {
     uintptr_t bits = 16;
+    // of the first matrix; whether a row's start within 16 bytes is the same in all
+    uintptr_t start = 0, stride = 0;
+    bool none = true, alike = true;
     void add(const void *p, int64_t ld_bytes)
     {
         if (!p) return;
-        bits |= reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld_bytes);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p), ld = static_cast<uintptr_t>(ld_bytes);
+        bits |= at | ld;
+        if (none) start = at, stride = ld;
+        alike = alike && ((at ^ start) & 15) == 0 && ((ld ^ stride) & 15) == 0;
+        none = false;
     }
     int bytes() const { return static_cast<int>(bits & (~bits + 1)); }
+};
+
+// How rows are read and written: vectors of `vec` elements, 16 bytes or a single
+// element. any: a row starts anywhere, its vectors are the aligned 16-byte words
+// that hold some of it, and the codes and channels' parameters beside it are
+// aligned to their elements alone.
+struct RowAccess {
+    int vec;
+    bool any;
 };
 
 // The library's own bookkeeping (maps of plans and kernel limits) may run out of

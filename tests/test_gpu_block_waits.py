@@ -47,8 +47,9 @@ def test_int8_product(q4lib, m, n, k):
 @pytest.mark.parametrize("m,d,kind", [(400, 2560, 0), (3000, 4096, 3)])
 def test_norms(q4lib, m, d, kind):
     R, B, dY, gate = (torch.randn(m, d, device="cuda") for _ in range(4))
-    w, dw = torch.randn(d, device="cuda"), torch.empty(d, device="cuda")
-    Y, H, dB, dg = (torch.empty(m, d, device="cuda") for _ in range(4))
+    # zeros: each call writes some of these, and all are compared
+    w, dw = torch.randn(d, device="cuda"), torch.zeros(d, device="cuda")
+    Y, H, dB, dg = (torch.zeros(m, d, device="cuda") for _ in range(4))
     need = q4lib.q4_norm_workspace_size(m, d)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     g, dgate = (gate, dg) if kind else (None, None)
