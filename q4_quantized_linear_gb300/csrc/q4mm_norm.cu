@@ -26,8 +26,8 @@
 //
 // The kernels of this file take few rows, narrow ones and very long ones, and those
 // of matrices whose rows start unlike one another. GB300, us a call (floor), join:
-// 1 x 2560 fp32 3.7 (0.01; the launch, a load, two reductions); 16384 x 1000 bf16 41
-// (19); 12000 x 601 bf16, rows on odd boundaries, 28 (9; 600 aligned 23); 2000 x 16384
+// 1 x 2560 fp32 3.7 (0.01; the launch, a load, two reductions); 16384 x 1000 bf16 39
+// (19); 12000 x 601 bf16, rows on odd boundaries, 27 (9; 600 aligned 22); 2000 x 16384
 // fp32 124 (77; values past the registers are read twice).
 #include <algorithm>
 #include <cuda_runtime.h>
@@ -124,11 +124,23 @@ __global__ void __launch_bounds__(max_threads(NV), 1024 / max_threads(NV)) norm_
             float w[V], y[V];
             if (i < 0) after_at(c, w);
             else wa.get(i, c, after_at, w);
+            if constexpr (kPairs<T, V>) {
+                if (full) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float f = elem(bv, j) * q * w[j];
-                if (full) f *= elem(gv, j);
-                y[j] = c + j < d ? elem(rv, j) + f : 0.0f;
+                    for (int j = 0; j < V; ++j) w[j] *= elem(gv, j);
+                }
+                scaled_sum<T, V>(bv, q, w, rv, y);
+                if (c + V > d) {   // nothing outside enters the sum
+#pragma unroll
+                    for (int j = 0; j < V; ++j) y[j] = c + j < d ? y[j] : 0.0f;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float f = elem(bv, j) * q * w[j];
+                    if (full) f *= elem(gv, j);
+                    y[j] = c + j < d ? elem(rv, j) + f : 0.0f;
+                }
             }
             const Pack<T, V> o = pack_of<T, V>(y);
             store_pack<T, V>(yr, c, d, o);

@@ -14,7 +14,7 @@ bool plan_norm_stream(int64_t m, int64_t d, int type, bool any, int matrices, in
     // of a row's place in shared memory; its vectors at most
     const int64_t bytes = any ? (d * size + 30 - size) / 16 * 16 : d * size, vecs = d * size / 16;
     // shorter rows go faster several to an SM in the general kernels (16384 x 1000
-    // bf16: 41 us there, 46 here); with fewer rows than CTAs nothing is read ahead
+    // bf16: 39 us there, 46 here); with fewer rows than CTAs nothing is read ahead
     if (d * size < 2048 || vecs > 2048 || m <= 2 * sm_count) return false;
     NormStreamPlan p;
     const int most = size == 2 ? 2 : 4;   // vectors whose weights stay in registers
