@@ -253,12 +253,15 @@ Q4MM_API int q4_w8_matmul(const void *W8_packed, const float *X, float *Y, int64
  *     token's gate, routing weights) are fp32. Values are computed in fp32
  *     and rounded once, to nearest even, when they are stored.
  *   - ld* is the distance between two rows of a matrix in elements, at least
- *     the row's length. Rows need no alignment beyond their element's; calls
- *     whose rows all start on 16-byte boundaries move 16 bytes an access,
- *     others 4 bytes or one element.
+ *     the row's length. Rows need no alignment beyond their element's. The
+ *     norms are fastest where the rows of all matrices start on 16-byte
+ *     boundaries or, next to that, all equally far from one (rows of one length
+ *     and stride do); where they start unlike one another they move an element
+ *     an access.
  *   - A matrix that is written may not overlap one that is read, except where
  *     a call names a pair that may be the same buffer (same pointer and ld).
- *   - Elements between a row's length and ld are neither read nor written. */
+ *   - Elements between a row's length and ld are never written. Those within a
+ *     16-byte word of a row's own may be read; they enter nothing. */
 #define Q4_TYPE_F32 0
 #define Q4_TYPE_F16 1
 #define Q4_TYPE_BF16 2

@@ -1,6 +1,6 @@
 // q4mm_norm.cuh -- device code shared by the norms' kernels: the general ones
-// (q4mm_norm.cu) and those that stream aligned rows through shared memory
-// (q4mm_norm_stream.cu).
+// (q4mm_norm.cu) and those that stream rows through shared memory
+// (q4mm_norm_stream.cuh).
 #pragma once
 
 #include "q4mm_norm.h"

@@ -25,7 +25,7 @@ bool plan_norm_stream(int64_t m, int64_t d, int type, bool any, int matrices, in
     // so on) leave room for, and three rows ahead
     int per_sm = p.G > 256 ? 1 : 576 / (p.G + 32);
     for (; per_sm > 0; --per_sm) {
-        p.stages = static_cast<int>(std::min<size_t>(6, (kSmemPerSM / per_sm - 3072) / stage));
+        p.stages = static_cast<int>(std::min<size_t>(6, (kSmemPerSM / per_sm - 3 * 1024) / stage));
         if (p.stages >= 3) break;
     }
     if (per_sm == 0) return false;
