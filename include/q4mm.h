@@ -299,9 +299,8 @@ Q4MM_API size_t q4_w8a8_workspace_size(int64_t m, int64_t k, int64_t n);
  *   calls that can run at the same time need one each.
  * Up to 16 tokens run a mat-vec on the warp-level MMA, more the tensor cores'
  * GEMM, with K cut into slices where the tiles are too few for the device. The
- * weights are read before the tokens are coded, while kernels in front may
- * still run: what writes W8_packed must not let its dependents start before it
- * is done (q4_w8_quantize, copies and other ordinary launches do not). */
+ * weights are read after the kernels in front have completed, or before where
+ * q4_set_weight_prefetch declares them read-only. */
 Q4MM_API int q4_w8a8_matmul(const void *W8_packed, const void *X, int64_t ldx, int xtype,
                             void *Y, int64_t ldy, int ytype, int64_t m, int64_t k, int64_t n,
                             void *workspace, size_t workspace_bytes, q4mm_stream_t stream);
@@ -497,13 +496,14 @@ Q4MM_API int q4_build_flags(void);
 Q4MM_API int q4_set_wait_limit_ns(uint64_t ns);
 
 /* Declare packed weights read-only while matmuls run (default: not declared).
- * When enabled, the matmul kernels (the decode kernel, and the prefill GEMM)
- * start streaming W_packed before the kernels that precede them in the
- * stream have finished, overlapping the two (programmatic dependent launch);
- * X, Y and the workspace are still read only after those kernels complete.
- * Enable it only if no kernel writes a W_packed immediately before a matmul
- * that reads it in the same stream (after q4_0_pack, synchronise or record an
- * event before the first matmul). Applies to launches made after the call. */
+ * When enabled, the matmul kernels (the decode kernel, the prefill GEMM and the
+ * int8 product of coded tokens) start streaming W_packed before the kernels
+ * that precede them in the stream have finished, overlapping the two
+ * (programmatic dependent launch); X, Y and the workspace are still read only
+ * after those kernels complete. Enable it only if no kernel writes a W_packed
+ * immediately before a matmul that reads it in the same stream (after q4_0_pack
+ * or q4_w8_quantize, synchronise or record an event before the first matmul).
+ * Applies to launches made after the call. */
 Q4MM_API int q4_set_weight_prefetch(int enable);
 
 /* Decode kernels (m <= 16). Every one meets the decode tolerance; which one

@@ -275,6 +275,7 @@ int matmul_impl(const void *W, const float *X, int64_t ldx, const int32_t *rows,
 int device_info(DeviceInfo *out) { return current_device(out); }
 int cuda_status(cudaError_t e) { return map_cuda(e); }
 uint64_t wait_limit() { return g_wait_ns.load(); }
+int weight_prefetch() { return g_prefetch_w.load(); }
 
 // One launch of the mat-vec over an expert set (each expert at most 16
 // rows). Q4_ERR_INVALID_ARG when no plan fits (the caller then runs the

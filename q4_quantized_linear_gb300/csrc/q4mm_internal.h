@@ -38,6 +38,8 @@ int device_info(DeviceInfo *out);
 int cuda_status(cudaError_t e);
 // The limit of device-side waits, as set for the calls to come.
 uint64_t wait_limit();
+// Whether the caller has declared packed weights read-only (q4_set_weight_prefetch).
+int weight_prefetch();
 
 // Raise a kernel's dynamic shared-memory limit to the opt-in maximum, once per
 // (device, kernel).

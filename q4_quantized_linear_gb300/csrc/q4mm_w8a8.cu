@@ -18,8 +18,9 @@
 // g + 8 as the A operands of four MMAs, and the same columns of token g as
 // their B operands, read from the token's codes as they are.
 //   The slices of a unit of 16 rows are warps of one CTA and meet in shared
-// memory. A whole batch of records is loaded before the dependency wait, so
-// the weight stream starts while the tokens are still being coded.
+// memory. Where the caller declared the weights read-only, a whole batch of
+// records is loaded before the dependency wait, so the weight stream starts
+// while the tokens are still being coded.
 //   GB300, us a call (floor at the measured copy rate): 1 x 9728 x 2560 6.6 (3.7),
 // 1 x 2560 x 9728 10 (3.7), 1 x 14336 x 4096 14.4 (8.7), 16 x 14336 x 4096 with the
 // norm in front 17.8 (8.8). The loads in flight and their conversion bound it.
@@ -118,6 +119,9 @@ __global__ void __launch_bounds__(kThreads, OCC) few_tokens_kernel(const W8a8Arg
     const int64_t urow = min(row0, static_cast<int64_t>(a.groups) * kW8GroupRows - kUnitRows);
     const uint8_t *src = a.W + (urow / kW8GroupRows * a.np) * kW8RecordBytes + (urow % kW8GroupRows + g) * kPairK + 16 * t;
     uint4 w0[U], w1[U];
+    // What a kernel in front wrote is visible only past the wait: the weights may
+    // be read before it only where the caller declared that none writes them.
+    if (!a.prefetch_w) pdl_wait();
     auto load = [&](int u, int p) {
         if (p < p1) {
             const uint8_t *r = src + static_cast<int64_t>(p) * kW8RecordBytes;
@@ -285,6 +289,7 @@ int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int
         g.ytype = ytype;
         g.status = dev.status;
         g.wait_ns = wait_limit();
+        g.prefetch_w = weight_prefetch();
         g.m = static_cast<int>(m);
         g.n = static_cast<int>(n);
         return cuda_status(launch_w8a8_gemm(plan, g, tok, k, ws + image_at(m, k), dev.sm_count, s));
@@ -314,6 +319,7 @@ int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int
     a.np = np;
     a.groups = groups;
     a.row_scale = row_scale;
+    a.prefetch_w = weight_prefetch();
     return cuda_status(launch_few_tokens(a, dev.sm_count, s));
 }
 

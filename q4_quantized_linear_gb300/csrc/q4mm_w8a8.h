@@ -23,6 +23,7 @@ struct W8a8Args {
     int ytype;
     int m, n, k, np, groups;
     int slices;               // of K: warps of a CTA that share 16 rows
+    int prefetch_w;           // read W before waiting on the preceding kernel
 };
 
 // The tensor-core product (many tokens).
@@ -52,6 +53,7 @@ struct W8a8GemmArgs {
     int N, ts, tiles, kslices;
     int64_t slice_stride;     // elements from a slice's sums to the next's
     int astages, bstages, wring;
+    int prefetch_w;           // read W before waiting on the preceding kernels
 };
 
 bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan);

@@ -346,9 +346,9 @@ template <typename T, bool SLICED> __global__ void __launch_bounds__(kThreads, 1
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------ record producer
-        // No dependency wait: this grid starts once every CTA of the kernel in
-        // front of it, the tokens' tiling, is past its own, and that kernel
-        // writes no weights.
+        // What the kernels in front wrote is visible only past the wait: the
+        // weights stream before it only where the caller declared them read-only.
+        if (!a.prefetch_w) pdl_wait();
         if (lane == 0) {
             Ring w;
             int64_t issued = 0;
