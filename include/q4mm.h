@@ -280,7 +280,9 @@ Q4MM_API int q4_a8_quantize(int8_t *Xq, float *sx, const void *X, int64_t ldx, i
 
 /* Bytes of scratch the two calls below need (256-byte aligned; it needs no
  * initialisation): the tokens' codes and scales, and for larger m their tiles
- * as the tensor cores read them. 0 for invalid sizes or m = 0. */
+ * as the tensor cores read them and room for sums over slices of K. It does not
+ * fall as m grows: a workspace for the largest batch serves every smaller one.
+ * No device is asked. 0 for invalid sizes or m = 0. */
 Q4MM_API size_t q4_w8a8_workspace_size(int64_t m, int64_t k, int64_t n);
 
 /* The product in 8-bit integers with a scale for each token and each channel:

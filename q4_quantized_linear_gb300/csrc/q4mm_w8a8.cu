@@ -262,7 +262,7 @@ constexpr int64_t kFewTokens = 16;
 
 // `tok`: codes with their scales, or rows to be coded.
 int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int64_t m, int64_t k, int64_t n,
-            void *workspace, size_t workspace_bytes, q4mm_stream_t stream)
+            void *workspace, q4mm_stream_t stream)
 {
     DeviceInfo dev;
     int rc = device_info(&dev);
@@ -277,7 +277,6 @@ int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int
     if (m > kFewTokens) {
         W8a8GemmPlan plan;
         if (!plan_w8a8_gemm(m, k, n, &plan)) return Q4_ERR_INVALID_ARG;
-        if (workspace_bytes < image_at(m, k) + plan.image_bytes + plan.partial_bytes) return Q4_ERR_WORKSPACE;
         W8a8GemmArgs g{};
         g.W = W;
         g.np = np;
@@ -333,10 +332,7 @@ extern "C" {
 Q4MM_API size_t q4_w8a8_workspace_size(int64_t m, int64_t k, int64_t n)
 {
     if (m <= 0 || !valid_sizes(m, k, n)) return 0;
-    W8a8GemmPlan plan;
-    bool tiled = false;
-    if (m > kFewTokens) guarded([&] { return (tiled = plan_w8a8_gemm(m, k, n, &plan)) ? Q4_OK : Q4_ERR_CUDA; });
-    return image_at(m, k) + (tiled ? plan.image_bytes + plan.partial_bytes : 0);
+    return image_at(m, k) + (m > kFewTokens ? w8a8_gemm_bytes(m, k, n) : 0);
 }
 
 Q4MM_API int q4_w8a8_matmul(const void *W8_packed, const void *X, int64_t ldx, int xtype, void *Y, int64_t ldy,
@@ -359,7 +355,7 @@ Q4MM_API int q4_w8a8_matmul(const void *W8_packed, const void *X, int64_t ldx, i
     tok.ldx = ldx;
     tok.xtype = xtype;
     tok.vec = al.bytes() >= 16 ? 16 / size : size == 2 && al.bytes() >= 4 ? 2 : 1;
-    return guarded([&] { return product(W8_packed, tok, Y, ldy, ytype, m, k, n, workspace, workspace_bytes, stream); });
+    return guarded([&] { return product(W8_packed, tok, Y, ldy, ytype, m, k, n, workspace, stream); });
 }
 
 Q4MM_API int q4_w8a8_matmul_codes(const void *W8_packed, const int8_t *Xq, const float *sx, void *Y, int64_t ldy,
@@ -376,7 +372,7 @@ Q4MM_API int q4_w8a8_matmul_codes(const void *W8_packed, const int8_t *Xq, const
     W8a8Tokens tok;
     tok.Xq = Xq;
     tok.sx = const_cast<float *>(sx);   // read only: the codes are there
-    return guarded([&] { return product(W8_packed, tok, Y, ldy, ytype, m, k, n, workspace, workspace_bytes, stream); });
+    return guarded([&] { return product(W8_packed, tok, Y, ldy, ytype, m, k, n, workspace, stream); });
 }
 
 } // extern "C"

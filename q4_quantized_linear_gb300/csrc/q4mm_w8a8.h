@@ -35,8 +35,7 @@ struct W8a8GemmPlan {
     int pairs = 0;            // CTA pairs of the grid, each taking tiles in turn
     int astages = 0, bstages = 0, wring = 0;
     size_t smem = 0;
-    size_t image_bytes = 0;   // the tokens' fp16 tiles; 256-byte aligned
-    size_t partial_bytes = 0; // the slices' sums, behind them
+    size_t image_bytes = 0;   // the tokens' fp16 tiles; 256-byte aligned; the slices' sums are behind them
 };
 
 struct W8a8GemmArgs {
@@ -56,6 +55,9 @@ struct W8a8GemmArgs {
     int prefetch_w;           // read W before waiting on the preceding kernels
 };
 
+// Scratch of the tokens' tiles and the slices' sums that every plan for up to m
+// tokens fits into: a workspace for a batch serves the smaller ones too.
+size_t w8a8_gemm_bytes(int64_t m, int64_t k, int64_t n);
 bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan);
 // The tokens of a call: codes, or rows to be coded (their scales then go to
 // sx; `vec` elements an access).

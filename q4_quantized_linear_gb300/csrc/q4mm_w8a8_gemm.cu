@@ -661,6 +661,27 @@ int max_pairs(size_t smem)
 
 } // namespace
 
+// K is cut where a slice has three steps at least, and where the slices' sums stay
+// small: a bound of their own, so that the workspace's size does not follow the
+// plans up and down. (By the costs below slices past these bounds gain 8 % at most,
+// on layers of 30000 columns and more; layers past 131072 rows fill the device.)
+constexpr int64_t kMaxSlices = 16, kMinSliceSteps = 3;
+constexpr int64_t kMaxSlicedRowTiles = 512, kMaxSliceBytes = int64_t(64) << 20;
+constexpr int64_t kMaxSlicedTokens = 65535;   // a grid dimension of the second kernel
+static int64_t slice_bytes(int64_t slices, int64_t m, int64_t n) { return slices * m * round_up(n, kW8GroupRows) * 4; }
+
+size_t w8a8_gemm_bytes(int64_t m, int64_t k, int64_t n)
+{
+    const int64_t np = ceil_div(k, kPairK), steps = ceil_div(np, kStepRecords);
+    // tokens of the tiles: a multiple of 32, less than a tile of at most 256 (or of
+    // the tokens, rounded up) past m
+    const int64_t tokens = std::min(2 * round_up(m, 32), (m + 255) / 32 * 32);
+    const int64_t slices = std::min(kMaxSlices, ceil_div(steps, kMinSliceSteps));
+    const bool sliced = slices > 1 && ceil_div(n, 2 * kW8GroupRows) <= kMaxSlicedRowTiles;
+    const int64_t sums = sliced ? std::min(kMaxSliceBytes, slice_bytes(slices, std::min(m, kMaxSlicedTokens), n)) : 0;
+    return static_cast<size_t>(tokens * np * 128 + sums);
+}
+
 // Tokens a tile and K slices: the fewest clocks over the pairs' turns. A step takes
 // 4 N clocks of MMA (256 x N x 128 at 8192 products a clock and pair), but not
 // under the 700 or so in which its operands are prepared; a tile adds its first
@@ -671,7 +692,8 @@ bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan)
     const int64_t steps = ceil_div(np, kStepRecords);
     double best = 1e300;
     W8a8GemmPlan out;
-    for (int N = 32; N <= 256; N += 32) {
+    const int widest = static_cast<int>(std::min<int64_t>(256, round_up(m, 32)));
+    for (int N = 32; N <= widest; N += 32) {
         W8a8GemmPlan c;
         c.N = N;
         c.astages = std::min<int>(kMaxAStages, (512 - N) / kAColumns);
@@ -686,16 +708,17 @@ bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan)
         const int held = max_pairs(c.smem);
         if (held < 1) continue;
         c.image_bytes = static_cast<size_t>(2) * c.ts * np * (N / 2) * 128;
-        for (int ks = 1; ks <= 16; ++ks) {
-            const int64_t per = ceil_div(steps, ks);
-            if (ks > 1 && (per < 3 || ceil_div(steps, per) != ks || m > 65535)) continue;   // every slice has steps
+        for (int ks = 1; ks <= kMaxSlices; ++ks) {
+            const int64_t per = ceil_div(steps, ks), sums = ks > 1 ? slice_bytes(ks, m, n) : 0;
+            if (ks > 1 && (per < kMinSliceSteps || ceil_div(steps, per) != ks ||   // every slice has steps
+                           m > kMaxSlicedTokens || rt > kMaxSlicedRowTiles || sums > kMaxSliceBytes))
+                continue;
             c.kslices = ks;
             c.tiles = static_cast<int>(rt * c.ts * ks);
             c.pairs = std::min(held, c.tiles);
-            c.partial_bytes = ks > 1 ? static_cast<size_t>(ks) * m * groups * kW8GroupRows * 4 : 0;
             const double turns = static_cast<double>(ceil_div(c.tiles, c.pairs));
             const double cost = turns * (static_cast<double>(per) * std::max(4.0 * N, 700.0) + 2500.0 + 8.0 * N) +
-                                (ks > 1 ? 4000.0 + static_cast<double>(c.partial_bytes) / 1500.0 : 0.0);
+                                (ks > 1 ? 4000.0 + static_cast<double>(sums) / 1500.0 : 0.0);
             if (cost < best) {
                 best = cost;
                 out = c;
