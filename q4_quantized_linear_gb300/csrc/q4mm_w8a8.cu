@@ -276,7 +276,7 @@ int product(const void *W8, W8a8Tokens tok, void *Y, int64_t ldy, int ytype, int
     const float *row_scale = reinterpret_cast<const float *>(W + static_cast<size_t>(groups) * np * kW8RecordBytes);
     if (m > kFewTokens) {
         W8a8GemmPlan plan;
-        if (!plan_w8a8_gemm(m, k, n, &plan)) return Q4_ERR_INVALID_ARG;
+        if (!plan_w8a8_gemm(m, k, n, dev.sm_count, &plan)) return Q4_ERR_INVALID_ARG;
         W8a8GemmArgs g{};
         g.W = W;
         g.np = np;

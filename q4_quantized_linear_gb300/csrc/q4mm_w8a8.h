@@ -58,7 +58,7 @@ struct W8a8GemmArgs {
 // Scratch of the tokens' tiles and the slices' sums that every plan for up to m
 // tokens fits into: a workspace for a batch serves the smaller ones too.
 size_t w8a8_gemm_bytes(int64_t m, int64_t k, int64_t n);
-bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan);
+bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, int sm_count, W8a8GemmPlan *plan);
 // The tokens of a call: codes, or rows to be coded (their scales then go to
 // sx; `vec` elements an access).
 struct W8a8Tokens {

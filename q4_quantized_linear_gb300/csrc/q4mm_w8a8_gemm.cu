@@ -44,9 +44,6 @@
 // together.
 #include <algorithm>
 #include <cuda_runtime.h>
-#include <map>
-#include <mutex>
-#include <utility>
 
 #include "q4mm_rows.cuh"
 #include "q4mm_w8a8.h"
@@ -625,40 +622,6 @@ size_t smem_bytes(int N, int astages, int bstages, int wring)
            static_cast<size_t>(2 * bstages + 3 * astages + 2 * wring + 3) * 8 + 16;
 }
 
-// CTA pairs that the current device holds at once; 0 when it cannot be asked.
-int max_pairs(size_t smem)
-{
-    static std::mutex mu;
-    static std::map<std::pair<int, size_t>, int> cache;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    std::lock_guard<std::mutex> lock(mu);
-    const auto it = cache.find({dev, smem});
-    if (it != cache.end()) return it->second;
-    int n = 0;
-    const void *fn = kernel_of(Q4_TYPE_F32, false);
-    if (set_max_smem(fn, smem) == cudaSuccess) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 2;
-        attr.val.clusterDim.y = 1;
-        attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) n = 0;
-    }
-    cudaGetLastError();
-    cache.emplace(std::make_pair(dev, smem), n);
-    return n;
-}
-
 } // namespace
 
 // K is cut where a slice has three steps at least, and where the slices' sums stay
@@ -686,10 +649,13 @@ size_t w8a8_gemm_bytes(int64_t m, int64_t k, int64_t n)
 // 4 N clocks of MMA (256 x N x 128 at 8192 products a clock and pair), but not
 // under the 700 or so in which its operands are prepared; a tile adds its first
 // step's latency and D's way out; slices add a kernel and their sums' traffic.
-bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan)
+bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, int sm_count, W8a8GemmPlan *plan)
 {
     const int64_t np = ceil_div(k, kPairK), groups = ceil_div(n, kW8GroupRows), rt = ceil_div(groups, 2);
     const int64_t steps = ceil_div(np, kStepRecords);
+    // pairs on the device at once: a CTA takes an SM (where it holds fewer the others
+    // follow: no pair waits on another)
+    const int held = std::max(1, sm_count / 2);
     double best = 1e300;
     W8a8GemmPlan out;
     const int widest = static_cast<int>(std::min<int64_t>(256, round_up(m, 32)));
@@ -705,8 +671,6 @@ bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, W8a8GemmPlan *plan)
         if (c.smem > kSmemOptIn) continue;
         c.ts = static_cast<int>(ceil_div(m, N));
         if (rt * c.ts > (int64_t(1) << 24)) continue;
-        const int held = max_pairs(c.smem);
-        if (held < 1) continue;
         c.image_bytes = static_cast<size_t>(2) * c.ts * np * (N / 2) * 128;
         for (int ks = 1; ks <= kMaxSlices; ++ks) {
             const int64_t per = ceil_div(steps, ks), sums = ks > 1 ? slice_bytes(ks, m, n) : 0;
