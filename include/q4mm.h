@@ -260,6 +260,8 @@ Q4MM_API int q4_w8_matmul(const void *W8_packed, const float *X, float *Y, int64
  *     an access.
  *   - A matrix that is written may not overlap one that is read, except where
  *     a call names a pair that may be the same buffer (same pointer and ld).
+ *   - A call of no rows (m or tokens 0) may have NULL for what holds something
+ *     for each row (an empty tensor has no address).
  *   - Elements between a row's length and ld are never written. Those within a
  *     16-byte word of a row's own may be read; they enter nothing. */
 #define Q4_TYPE_F32 0

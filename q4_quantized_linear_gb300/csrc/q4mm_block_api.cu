@@ -20,9 +20,12 @@ constexpr int64_t kMaxPairs = int64_t(1) << 24;
 cudaStream_t as_stream(q4mm_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // A matrix argument: a pointer, rows at least `cols` apart, on its elements'
-// boundaries. ok() keeps the first fault.
+// boundaries. rc keeps the first fault. Of a call without rows, what holds
+// something for each row may have no address: an empty tensor has none.
 struct Checker {
+    bool rows;
     int rc = Q4_OK;
+    explicit Checker(int64_t m) : rows(m > 0) {}
     void fail(int code)
     {
         if (rc == Q4_OK) rc = code;
@@ -30,7 +33,7 @@ struct Checker {
     void matrix(const void *p, int64_t ld, int64_t cols, int type, bool optional = false)
     {
         if (!p) {
-            if (!optional) fail(Q4_ERR_INVALID_ARG);
+            if (!optional && rows) fail(Q4_ERR_INVALID_ARG);
             return;
         }
         if (ld < cols || ld > (int64_t(1) << 40)) fail(Q4_ERR_INVALID_ARG);
@@ -44,6 +47,8 @@ struct Checker {
             fail(Q4_ERR_ALIGNMENT);
         }
     }
+    // one element or more for each row
+    void per_row(const void *p, uintptr_t align) { vector(p, align, !rows); }
 };
 
 // Elements of one access: 16 bytes, 4 bytes or one element, as the rows allow.
@@ -71,7 +76,8 @@ void check_gate(Checker &c, const void *gate, int64_t ldg, int kind, int64_t d, 
 {
     if (!valid_gate(kind)) c.fail(Q4_ERR_INVALID_ARG);
     else if (kind == Q4_GATE_FULL) c.matrix(gate, ldg, d, type);
-    else if (kind != Q4_GATE_NONE) c.vector(gate, 4);
+    else if (kind == Q4_GATE_TOKEN) c.per_row(gate, 4);
+    else if (kind == Q4_GATE_CHANNEL) c.vector(gate, 4);
 }
 
 int norm_after_impl(void *Y, int64_t ldy, void *H, int64_t ldh, int htype, float *h_scale, bool next, const void *R,
@@ -82,7 +88,7 @@ int norm_after_impl(void *Y, int64_t ldy, void *H, int64_t ldh, int htype, float
     if (!is_float_type(type) || m < 0 || m > kMaxRows || d < 1 || d > kMaxCols || !positive(eps)) return Q4_ERR_INVALID_ARG;
     if (next && htype != type && htype != Q4_TYPE_I8) return Q4_ERR_INVALID_ARG;
     const bool codes = next && htype == Q4_TYPE_I8;
-    Checker c;
+    Checker c(m);
     c.matrix(Y, ldy, d, type);
     c.matrix(R, ldr, d, type);
     c.matrix(B, ldb, d, type);
@@ -91,7 +97,7 @@ int norm_after_impl(void *Y, int64_t ldy, void *H, int64_t ldh, int htype, float
     if (next) {
         c.matrix(H, ldh, d, htype);
         c.vector(w_next, 4, true);
-        if (codes) c.vector(h_scale, 4);
+        if (codes) c.per_row(h_scale, 4);
     }
     if (c.rc != Q4_OK) return c.rc;
     if (m == 0) return Q4_OK;
@@ -147,9 +153,9 @@ Q4MM_API int q4_a8_quantize(int8_t *Xq, float *sx, const void *X, int64_t ldx, i
                             q4mm_stream_t stream)
 {
     if (!is_float_type(type) || m < 0 || m > kMaxRows || k < 1 || k > kMaxCols) return Q4_ERR_INVALID_ARG;
-    Checker c;
-    c.vector(Xq, 1);
-    c.vector(sx, 4);
+    Checker c(m);
+    c.per_row(Xq, 1);
+    c.per_row(sx, 4);
     c.matrix(X, ldx, k, type);
     if (c.rc != Q4_OK) return c.rc;
     if (m == 0) return Q4_OK;
@@ -166,11 +172,11 @@ Q4MM_API int q4_norm_before(void *H, int64_t ldh, int htype, float *h_scale, con
         d > kMaxCols || !positive(eps))
         return Q4_ERR_INVALID_ARG;
     const bool codes = htype == Q4_TYPE_I8;
-    Checker c;
+    Checker c(m);
     c.matrix(H, ldh, d, htype);
     c.matrix(X, ldx, d, type);
     c.vector(w, 4, true);
-    if (codes) c.vector(h_scale, 4);
+    if (codes) c.per_row(h_scale, 4);
     if (c.rc != Q4_OK) return c.rc;
     if (m == 0) return Q4_OK;
     DeviceInfo dev;
@@ -220,7 +226,7 @@ Q4MM_API int q4_norm_before_backward(void *dX, int64_t lddx, float *dw, const vo
                                      size_t workspace_bytes, q4mm_stream_t stream)
 {
     if (!is_float_type(type) || m < 0 || m > kMaxRows || d < 1 || d > kMaxCols || !positive(eps)) return Q4_ERR_INVALID_ARG;
-    Checker c;
+    Checker c(m);
     c.matrix(dX, lddx, d, type);
     c.matrix(dH, lddh, d, type);
     c.matrix(dR, lddr, d, type, true);
@@ -259,7 +265,7 @@ Q4MM_API int q4_norm_after_backward(void *dB, int64_t lddb, float *dw, void *dga
                                     int64_t d, void *workspace, size_t workspace_bytes, q4mm_stream_t stream)
 {
     if (!is_float_type(type) || m < 0 || m > kMaxRows || d < 1 || d > kMaxCols || !positive(eps)) return Q4_ERR_INVALID_ARG;
-    Checker c;
+    Checker c(m);
     c.matrix(dB, lddb, d, type);
     c.matrix(dY, lddy, d, type);
     c.matrix(B, ldb, d, type);
@@ -322,14 +328,14 @@ Q4MM_API int q4_moe_dispatch(void *Xs, int64_t ldxs, int64_t *offsets, int32_t *
                              q4mm_stream_t stream)
 {
     if (!valid_moe(tokens, top_k) || n_experts < 1 || n_experts > kMoeMaxExperts || (id_bytes != 4 && id_bytes != 8) ||
-        (X == nullptr) != (Xs == nullptr))
+        (tokens > 0 && (X == nullptr) != (Xs == nullptr)))
         return Q4_ERR_INVALID_ARG;
-    Checker c;
+    Checker c(tokens);
     c.vector(offsets, 8);
-    c.vector(row_of, 4);
+    c.per_row(row_of, 4);
     c.vector(pair_of, 4, true);
-    c.vector(ids, static_cast<uintptr_t>(id_bytes));
-    if (X) {
+    c.per_row(ids, static_cast<uintptr_t>(id_bytes));
+    if (X || Xs) {
         if (!is_float_type(type) || d < 1 || d > kMaxCols) return Q4_ERR_INVALID_ARG;
         c.matrix(X, ldx, d, type);
         c.matrix(Xs, ldxs, d, type);
@@ -368,11 +374,11 @@ Q4MM_API int q4_moe_combine(void *Y, int64_t ldy, const void *base, int64_t ldba
                             int64_t d, q4mm_stream_t stream)
 {
     if (!is_float_type(type) || !valid_moe(tokens, top_k) || d < 1 || d > kMaxCols) return Q4_ERR_INVALID_ARG;
-    Checker c;
+    Checker c(tokens);
     c.matrix(Y, ldy, d, type);
     c.matrix(base, ldbase, d, type, true);
     c.matrix(Ys, ldys, d, type);
-    c.vector(row_of, 4);
+    c.per_row(row_of, 4);
     c.vector(weights, 4, true);
     if (c.rc != Q4_OK) return c.rc;
     if (tokens == 0) return Q4_OK;
@@ -399,11 +405,11 @@ Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, 
                                      q4mm_stream_t stream)
 {
     if (!is_float_type(type) || !valid_moe(tokens, top_k) || d < 1 || d > kMaxCols) return Q4_ERR_INVALID_ARG;
-    Checker c;
+    Checker c(tokens);
     c.matrix(dYs, lddys, d, type);
     c.matrix(dY, lddy, d, type);
     c.matrix(Ys, ldys, d, type);
-    c.vector(row_of, 4);
+    c.per_row(row_of, 4);
     c.vector(weights, 4, true);
     c.vector(dweights, 4, true);
     if (c.rc != Q4_OK) return c.rc;

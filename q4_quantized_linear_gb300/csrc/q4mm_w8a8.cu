@@ -339,7 +339,7 @@ Q4MM_API int q4_w8a8_matmul(const void *W8_packed, const void *X, int64_t ldx, i
                             int ytype, int64_t m, int64_t k, int64_t n, void *workspace, size_t workspace_bytes,
                             q4mm_stream_t stream)
 {
-    if (!W8_packed || !X || !Y || !is_float_type(xtype) || !is_float_type(ytype) || !valid_sizes(m, k, n) || ldx < k ||
+    if (!W8_packed || (m != 0 && (!X || !Y)) || !is_float_type(xtype) || !is_float_type(ytype) || !valid_sizes(m, k, n) || ldx < k ||
         ldy < n)
         return Q4_ERR_INVALID_ARG;
     if (!aligned_to(W8_packed, 16) || !aligned_to(X, type_size(xtype)) || !aligned_to(Y, type_size(ytype)) ||
@@ -362,7 +362,7 @@ Q4MM_API int q4_w8a8_matmul_codes(const void *W8_packed, const int8_t *Xq, const
                                   int ytype, int64_t m, int64_t k, int64_t n, void *workspace, size_t workspace_bytes,
                                   q4mm_stream_t stream)
 {
-    if (!W8_packed || !Xq || !sx || !Y || !is_float_type(ytype) || !valid_sizes(m, k, n) || ldy < n)
+    if (!W8_packed || (m != 0 && (!Xq || !sx || !Y)) || !is_float_type(ytype) || !valid_sizes(m, k, n) || ldy < n)
         return Q4_ERR_INVALID_ARG;
     if (!aligned_to(W8_packed, 16) || !aligned_to(Xq, 16) || !aligned_to(sx, 4) || !aligned_to(Y, type_size(ytype)) ||
         (workspace && !aligned_to(workspace, 256)))
