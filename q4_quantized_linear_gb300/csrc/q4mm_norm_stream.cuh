@@ -18,9 +18,10 @@
 // (40), 2049 x 2560 fp32 20 (12); after 8192 x 4096 bf16, channel gate 45 (30), a
 // gate for each value 58 (50). On odd boundaries: join 4000 x 4097 bf16 36 (19), fp32
 // 51 (39), gradients before 4000 x 4097 bf16 33 (19), after 3000 x 2561 fp32 24 (14).
-//   Every wait is bounded: after one that ran out the status word says so, the
-// CTA goes through its rows without waiting (its results are void) and leaves
-// when the copies in flight have landed.
+//   Every wait is bounded: after one that ran out the status word says so and the
+// thread goes through its rows without waiting (the call's results are void) and
+// without giving slots back, so the copying warp's own wait runs out too; the CTA
+// leaves when the copies in flight have landed.
 #pragma once
 
 #include "q4mm_norm.cuh"
@@ -81,11 +82,13 @@ struct RowStream {
             record_status(status, kErrTimeout);
         }
     }
-    // a row's warp has read the slot for the last time
+    // A row's warp has read the slot for the last time. Only a lane that saw the
+    // slot's copies land gives it back: a slot given back before that would be armed
+    // for another row while the first is still on its way.
     __device__ __forceinline__ void release(int slot)
     {
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[slot]);
+        if ((threadIdx.x & 31) == 0 && !dead) mbar_arrive(&empty[slot]);
     }
     __device__ __forceinline__ const uint8_t *place(int slot, int matrix) const
     {
