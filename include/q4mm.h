@@ -343,7 +343,9 @@ Q4MM_API int q4_norm_after(void *Y, int64_t ldy, const void *R, int64_t ldr, con
 
 /* q4_norm_after and the next block's q4_norm_before in one pass:
  *     H[t] = N(Y[t]) * (w_offset_next + w_next)
- * of Y as it is stored, so the results are those of the two calls. */
+ * of Y as it is stored. The results are those of the two calls up to the order in
+ * which a row's squares are summed: the last place may differ, and a code whose
+ * value lies halfway between two by one. */
 Q4MM_API int q4_norm_after_before(void *Y, int64_t ldy, void *H, int64_t ldh, int htype, float *h_scale,
                                   const void *R, int64_t ldr, const void *B, int64_t ldb, int type, const float *w,
                                   float w_offset, const void *gate, int64_t ldg, int gate_kind, float scale,
