@@ -291,9 +291,12 @@ Q4MM_API size_t q4_w8a8_workspace_size(int64_t m, int64_t k, int64_t n);
  *     Y[t][j] = sx[t] * s_j * sum_c xq[t][c] * code[j][c]
  * xq and sx are X coded by q4_a8_quantize's rule, code and s_j as
  * q4_w8_quantize wrote them. Products are exact, and so are sums whose partial
- * sums stay below 2^24 (up to 16 tokens' sums always are: they add in 32-bit
- * integers; more tokens' add in fp32). Then fp32: sx * s_j rounded, times the
- * sum, rounded to ytype.
+ * sums stay below 2^24. Past that up to 16 tokens' sums still are (they add in
+ * 32-bit integers), more tokens' add in fp32 and are cut to it every 16 columns:
+ * measured against the sum of the terms' sizes, 8e-6 at k = 14336 and 3e-5 at
+ * 131072 where all codes are large and of one sign, nothing where signs are
+ * mixed. Only there can a token's bits differ between a batch of up to 16 and a
+ * larger one. Then fp32: sx * s_j rounded, times the sum, rounded to ytype.
  *   W8_packed: as written by q4_w8_quantize for (n, k), 16-byte aligned.
  *   X: device, row t at X + t * ldx, xtype F32, F16 or BF16. Y: device, row t
  *   at Y + t * ldy, ytype F32, F16 or BF16, overwritten. Y's rows may be of any
