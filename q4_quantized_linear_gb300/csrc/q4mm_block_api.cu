@@ -51,12 +51,9 @@ struct Checker {
     void per_row(const void *p, uintptr_t align) { vector(p, align, !rows); }
 };
 
-// Elements of one access: 16 bytes, 4 bytes or one element, as the rows allow.
-int vec_of(const RowAlign &a, int type)
-{
-    const int size = type_size(type);
-    return a.bytes() == 16 ? 16 / size : size == 2 && a.bytes() >= 4 ? 2 : 1;
-}
+// Elements of one access of combine and its gradient: 16 bytes where every row
+// starts on them, else one (16-bit rows then go by shifted words).
+int vec_of(const RowAlign &a, int type) { return a.bytes() == 16 ? 16 / type_size(type) : 1; }
 
 // 16 bytes where the rows of every float matrix (a), the codes (one byte an
 // element) and the fp32 parameters beside them start at a vector of theirs, or

@@ -699,9 +699,11 @@ bool plan_w8a8_gemm(int64_t m, int64_t k, int64_t n, int sm_count, W8a8GemmPlan 
 namespace {
 template <typename T> cudaError_t launch_code_tiles(CodeTileArgs a, int vec, int sm_count, cudaStream_t s)
 {
-    const void *fn = vec * sizeof(T) == 16 ? reinterpret_cast<const void *>(&code_tile_kernel<T, 16 / sizeof(T)>)
-                     : vec == 2            ? reinterpret_cast<const void *>(&code_tile_kernel<T, 2>)
-                                           : reinterpret_cast<const void *>(&code_tile_kernel<T, 1>);
+    const void *fn = reinterpret_cast<const void *>(&code_tile_kernel<T, 1>);
+    if (vec * sizeof(T) == 16) fn = reinterpret_cast<const void *>(&code_tile_kernel<T, 16 / sizeof(T)>);
+    else if constexpr (sizeof(T) == 2) {
+        if (vec == 2) fn = reinterpret_cast<const void *>(&code_tile_kernel<T, 2>);
+    }
     const int64_t vecs = ceil_div(static_cast<int64_t>(a.np) * kPairK, vec);
     const int threads = static_cast<int>(std::min<int64_t>(512, round_up(ceil_div(vecs, vec >= 4 ? 2 : 4), 32)));
     const int64_t grid = std::min<int64_t>(a.rows, static_cast<int64_t>(sm_count) * (2048 / std::max(threads, 128)));
