@@ -20,7 +20,7 @@
 // warp matches over consecutive pairs, so no atomic's order enters a result.
 //
 // GB300, us a call (floor at the measured copy rate): dispatch 1 x 8 of 128
-// experts, 2560 fp32, 3.1 (one launch); 8192 x 8 of 128, 4096 bf16, 102 (89), the
+// experts, 2560 fp32, 3.3 (one launch); 8192 x 8 of 128, 4096 bf16, 102 (89), the
 // sort 12 of it; combine 4099 x 4 of 32, 2560 fp32 with a base, 41 (37); its
 // gradient 4096 x 8 of 128, 4096 bf16, 85 (84).
 #include <algorithm>

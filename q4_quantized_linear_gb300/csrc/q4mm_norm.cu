@@ -26,9 +26,9 @@
 //
 // The kernels of this file take few rows, narrow ones and very long ones, and those
 // of matrices whose rows start unlike one another. GB300, us a call (floor), join:
-// 1 x 2560 fp32 3.7 (0.01; the launch, a load, two reductions); 16384 x 1000 bf16 39
+// 1 x 2560 fp32 3.8 (0.01; the launch, a load, two reductions); 16384 x 1000 bf16 39
 // (19); 12000 x 601 bf16, rows on odd boundaries, 27 (9; 600 aligned 22); 2000 x 16384
-// fp32 124 (77; values past the registers are read twice).
+// fp32 125 (77; values past the registers are read twice).
 #include <algorithm>
 #include <cuda_runtime.h>
 

@@ -14,7 +14,7 @@
 // CTA, three CTAs an SM with the weights in shared memory, and more rows ahead
 // measured no faster.
 //   GB300, us a call (floor at the measured copy rate): join 4096 x 4096 bf16 with
-// a gate for each value 31 (25), fp32 52 (40); gradient before 8192 x 4096 bf16 47
+// a gate for each value 30 (25), fp32 52 (40); gradient before 8192 x 4096 bf16 47
 // (40), 2049 x 2560 fp32 20 (12); after 8192 x 4096 bf16, channel gate 45 (30), a
 // gate for each value 58 (50). On odd boundaries: join 4000 x 4097 bf16 36 (19), fp32
 // 51 (39), gradients before 4000 x 4097 bf16 33 (19), after 3000 x 2561 fp32 24 (14).

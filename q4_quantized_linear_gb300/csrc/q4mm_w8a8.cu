@@ -21,9 +21,9 @@
 // memory. Where the caller declared the weights read-only, a whole batch of
 // records is loaded before the dependency wait, so the weight stream starts
 // while the tokens are still being coded.
-//   GB300, us a call (floor at the measured copy rate): 1 x 9728 x 2560 6.6 (3.7),
-// 1 x 2560 x 9728 10 (3.7), 1 x 14336 x 4096 14.4 (8.7), 16 x 14336 x 4096 with the
-// norm in front 17.8 (8.8). The loads in flight and their conversion bound it.
+//   GB300, us a call (floor at the measured copy rate): 1 x 9728 x 2560 6.8 (3.7),
+// 1 x 2560 x 9728 10 (3.7), 1 x 14336 x 4096 14.7 (8.7), 16 x 14336 x 4096 with the
+// norm in front 18.1 (8.8). The loads in flight and their conversion bound it.
 #include <algorithm>
 #include <cuda_runtime.h>
 

@@ -37,10 +37,10 @@
 // own that writes its raw sums (whole numbers in fp32) to the workspace; a second
 // kernel adds them in slice order and scales.
 //   GB300, us a call with the coding (floor at the measured bf16 rate): 4096 x
-// 14336 x 4096 bf16 271 (248); 4096 x 9728 x 2560 fp32 144 (105), its stores; 540 x
-// 9728 x 2560 fp32 30 (14), the dequantising warps (a step of 128 columns takes
+// 14336 x 4096 bf16 274 (248); 4096 x 9728 x 2560 fp32 144 (105), its stores; 540 x
+// 9728 x 2560 fp32 30.5 (14), the dequantising warps (a step of 128 columns takes
 // them 0.4 us whatever the tokens); 540 x 2560 x 9728 bf16 35 (14), 64 x 9728 x
-// 2560 16 (3.7), the latencies of a step and of the launches.
+// 2560 15.4 (3.7), the latencies of a step and of the launches.
 // Every wait is bounded; after a timeout all roles leave their loops, the
 // MMAs and copies in flight are waited for and the CTAs of the pair leave
 // together.
