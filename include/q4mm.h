@@ -431,6 +431,122 @@ Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, 
                                      const float *weights, int64_t tokens, int64_t top_k, int64_t d,
                                      q4mm_stream_t stream);
 
+/* ---------------------------------------------- between the linear layers --
+ * A paged cache of keys and values, the attention of new tokens over it, and
+ * what turns the logit head's rows into tokens. The pages keep a conversation's
+ * state in a slot that its next tokens extend and a rejected draft rewinds
+ * (golem-server, "Several conversations, in one pass"; golem, "Qwen3.8 drafts
+ * its own next token"); their attention runs as three passes, here it is one.
+ *
+ * A batch: n_seq sequences (up to 1024). Their new tokens are rows next to each
+ * other, sequence s's starts[s] .. starts[s + 1] - 1 (starts: device int32
+ * [n_seq + 1], non-decreasing, a sequence may have none); lens[s] (device int32)
+ * is how many tokens the sequence holds in the cache with the new ones, which are
+ * its last. `rows` is at least starts[n_seq] (what the matrices hold); rows past
+ * it are neither read nor written. Nothing of the batch is read by the host, so
+ * a captured call replays with other lengths. A sequence is rewound by calling
+ * with a smaller len.
+ *   table: device int32, row s at table + s * ldt: the pages of sequence s in the
+ *   order of its tokens; token t is in page table[s][t / page_tokens]. Entries
+ *   that no token of a call needs are not read. One page may stand in several rows
+ *   (a shared beginning); a call that writes a place twice leaves either.
+ * A sequence holds at most ldt * page_tokens tokens (and 2^30); a longer len counts
+ * as that. A page that a call needs and that is not 0 .. n_pages - 1 is recorded
+ * as Q4_ERR_DEVICE_CHECK (q4_last_device_status) and nothing is accessed past the
+ * cache; what such a token gives is unspecified.
+ *
+ * pages: n_pages blobs of q4_kv_page_size bytes, 16-byte aligned, in the layout
+ * that the kernels read: for each head K, then V, each as [64 dims][token][64
+ * values] with a row's 16-byte units in an order of their own, dims past d as
+ * zeros; then for a cache of codes K's and V's scales (fp32 a token). A page is
+ * self-contained: it can be copied to the host, to another page or cache of the
+ * same shape. Fresh pages need no initialisation.
+ *   page_tokens: 16, 32, .. 1024; d: 8, 16, .. 256 (memory and time are those of
+ *   the next multiple of 64); ctype: Q4_TYPE_F16, Q4_TYPE_BF16 or Q4_TYPE_I8.
+ * Bytes of a page; 0 for invalid sizes. */
+Q4MM_API size_t q4_kv_page_size(int64_t page_tokens, int64_t kv_heads, int64_t d, int ctype);
+
+/* The new tokens' keys and values into the cache: row r of sequence s, new token
+ * i = r - starts[s], at its place lens[s] - (starts[s + 1] - starts[s]) + i. Values
+ * are rounded once to ctype, or with Q4_TYPE_I8 a head's d values coded by
+ * q4_a8_quantize's rule with a scale of their own. A head's token whose keys or
+ * values are not all finite (in ctype) is held as NaN keys and zero values: the
+ * queries that see it get NaN, others are not touched by it.
+ *   K, V: device, row r at K + r * ldk, kv_heads heads of d values next to each
+ *   other, type F32, F16 or BF16. Rows on 16-byte boundaries are read 16 bytes an
+ *   access. A negative place, or one past the table, is recorded and skipped. */
+Q4MM_API int q4_kv_write(void *pages, int64_t n_pages, int64_t page_tokens, int64_t kv_heads, int64_t d, int ctype,
+                         const int32_t *table, int64_t ldt, const int32_t *lens, const int32_t *starts, int64_t n_seq,
+                         const void *K, int64_t ldk, const void *V, int64_t ldv, int type, int64_t rows,
+                         q4mm_stream_t stream);
+
+/* Keys and values out of the cache: row starts[s] + i of K and V gets token
+ * first[s] + i of sequence s (first: device int32 [n_seq], NULL for zeros), rounded
+ * once to type. A place that the table does not have is recorded and gives zeros;
+ * a place that was never written gives what its memory holds. */
+Q4MM_API int q4_kv_read(void *K, int64_t ldk, void *V, int64_t ldv, int type, const void *pages, int64_t n_pages,
+                        int64_t page_tokens, int64_t kv_heads, int64_t d, int ctype, const int32_t *table, int64_t ldt,
+                        const int32_t *first, const int32_t *starts, int64_t n_seq, int64_t rows, q4mm_stream_t stream);
+
+/* Bytes of scratch q4_attention needs (256-byte aligned, no initialisation). It
+ * does not fall as rows grow. No device is asked; 0 for invalid sizes or no rows. */
+Q4MM_API size_t q4_attention_workspace_size(int64_t rows, int64_t n_seq, int64_t heads, int64_t kv_heads, int64_t d);
+
+/* Attention of the new tokens over the cache, which holds their own keys and
+ * values already (q4_kv_write of the same batch). Query head h uses cached head
+ * h / (heads / kv_heads); the token at place x sees the places y <= x, and with
+ * window > 0 only y > x - window:
+ *     O[r][h] = sum_y p_y V_y / sum_y p_y,   p_y = exp(scale * <Q[r][h], K_y>)
+ * A row that sees nothing (a len below the number of new tokens) gives zeros.
+ *   Q, O: device, heads of d values next to each other, one type: F32, F16 or BF16
+ *   over codes, F32 or F16 over an F16 cache, BF16 over a BF16 one. O may be Q.
+ *   scale > 0; heads a multiple of kv_heads; rows * heads <= 2^30.
+ *   max_new: at least the most new tokens of a sequence (0: rows); it chooses
+ *   the kernel, results hold whatever it is.
+ *   workspace: q4_attention_workspace_size bytes; calls that can run at the same
+ *   time need one each, and so do graphs whose replays can.
+ * Precision: scores and sums in fp32. 16-bit types: products exact, the terms p
+ * rounded once to the operands' type (fp16 over codes). F32: queries and terms
+ * as two fp16 numbers (22 bits), about 1e-6 of the result. */
+Q4MM_API int q4_attention(void *O, int64_t ldo, const void *Q, int64_t ldq, int type, int64_t heads, float scale,
+                          int64_t window, const void *pages, int64_t n_pages, int64_t page_tokens, int64_t kv_heads,
+                          int64_t d, int ctype, const int32_t *table, int64_t ldt, const int32_t *lens,
+                          const int32_t *starts, int64_t n_seq, int64_t rows, int64_t max_new, void *workspace,
+                          size_t workspace_bytes, q4mm_stream_t stream);
+
+/* Probabilities of the logit head's rows at a temperature:
+ *     P[r][i] = exp(x[r][i] / T[r]) / sum_j exp(x[r][j] / T[r])
+ * in fp32. T: device fp32 [rows], NULL for ones; T = 0 gives 1 for the row's
+ * largest logit (the lowest of equal ones; NaN counts for nothing) and 0
+ * elsewhere. A logit of -inf has probability 0, a row of them zeros; a NaN or
+ * +inf makes a row NaN (T > 0). T < 0 gives NaN.
+ *   P: device fp32, row r at P + r * ldp; logits: type F32, F16 or BF16. 1 <= n <=
+ *   2^24. 16-byte aligned rows of both are accessed 16 bytes at a time. */
+Q4MM_API int q4_token_probs(float *P, int64_t ldp, const void *logits, int64_t ldl, int type, const float *temperature,
+                            int64_t rows, int64_t n, q4mm_stream_t stream);
+
+/* Verification of drafted tokens. Slot s drafted counts[s] tokens (device int32,
+ * 0 .. max_draft; NULL: max_draft each), drafted[s * ldd + i], drawn from the
+ * probabilities in row s * max_draft + i of Q (Q NULL: with certainty); row s *
+ * (max_draft + 1) + i of P holds the target's for the same place, and one row more
+ * for the place after them. With x = drafted[s][i] and p, q its rows, the token is
+ * kept while
+ *     accept[s * lda + i] * q[x] < p[x]
+ * and kept[s] counts them. The token after the kept ones is drawn with u =
+ * sample[s]: the lowest index at which the running sum of max(p - q, 0) exceeds u
+ * times its total, p and q those of the first token that was not kept; p alone
+ * after the last one, or where p - q leaves nothing (0 where p is zeros).
+ *   tokens[s * ldt + j], j <= max_draft: the kept tokens, the drawn one, then -1.
+ * accept and sample are uniform in [0, 1). The product is exact, and the draw by
+ * whole numbers of steps of 2^-60: exact for probabilities from 2^-36 on, so that
+ * tokens do not depend on the order of a sum. A probability counts as 0 if it is
+ * negative or NaN, as 1 above; a row's sum must stay below 8. A drafted token
+ * outside 0 .. n - 1 is not kept. 1 <= n <= 2^20, max_draft <= 1024. */
+Q4MM_API int q4_draft_verify(int32_t *tokens, int64_t ldt, int32_t *kept, const float *P, int64_t ldp, const float *Q,
+                             int64_t ldq, const int32_t *drafted, int64_t ldd, const int32_t *counts, const float *accept,
+                             int64_t lda, const float *sample, int64_t n_seq, int64_t max_draft, int64_t n,
+                             q4mm_stream_t stream);
+
 /* Size of the library's fixed scratch array used by q4_0_matmul_static_scratch. */
 #define Q4_STATIC_SCRATCH_BYTES (8u << 20)
 

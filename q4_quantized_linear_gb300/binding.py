@@ -61,6 +61,14 @@ _SIGS = {
     "q4_moe_dispatch": (_INT, [_P, _I64, _P, _P, _P, _P, _INT, _P, _I64, _INT, _I64, _I64, _I64, _I64, _P, _SZ, _P]),
     "q4_moe_combine": (_INT, [_P, _I64, _P, _I64, _P, _I64, _INT, _P, _P, _I64, _I64, _I64, _P]),
     "q4_moe_combine_backward": (_INT, [_P, _I64, _P, _P, _I64, _P, _I64, _INT, _P, _P, _I64, _I64, _I64, _P]),
+    "q4_kv_page_size": (_SZ, [_I64, _I64, _I64, _INT]),
+    "q4_kv_write": (_INT, [_P, _I64, _I64, _I64, _I64, _INT, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _INT, _I64, _P]),
+    "q4_kv_read": (_INT, [_P, _I64, _P, _I64, _INT, _P, _I64, _I64, _I64, _I64, _INT, _P, _I64, _P, _P, _I64, _I64, _P]),
+    "q4_attention_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "q4_attention": (_INT, [_P, _I64, _P, _I64, _INT, _I64, _F, _I64, _P, _I64, _I64, _I64, _I64, _INT, _P, _I64, _P, _P,
+                            _I64, _I64, _I64, _P, _SZ, _P]),
+    "q4_token_probs": (_INT, [_P, _I64, _P, _I64, _INT, _P, _I64, _I64, _P]),
+    "q4_draft_verify": (_INT, [_P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P]),
     "q4_0_matmul_experts": (_INT, [ctypes.POINTER(_P), _I64, ctypes.POINTER(_I64), _P, _P, _I64, _I64, _P]),
     "q4_0_matmul_static_scratch": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P]),
     "q4_0_matmul_batched_slots": (_INT, [_P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P]),
@@ -334,6 +342,52 @@ def q4_moe_combine_backward(dYs, lddys: int, dweights, dY, lddy: int, Ys, ldys: 
     rc = _lib.q4_moe_combine_backward(_addr(dYs), lddys, _addr(dweights), _addr(dY), lddy, _addr(Ys), ldys, type,
                                       _addr(row_of), _addr(weights), tokens, top_k, d, _stream(stream))
     return _check(rc, "q4_moe_combine_backward") if check else rc
+
+
+# ---- between the linear layers: the paged cache, attention, tokens
+
+def q4_kv_page_size(page_tokens: int, kv_heads: int, d: int, ctype: int) -> int:
+    return int(_lib.q4_kv_page_size(page_tokens, kv_heads, d, ctype))
+
+
+def q4_kv_write(pages, n_pages: int, page_tokens: int, kv_heads: int, d: int, ctype: int, table, ldt: int, lens, starts,
+                n_seq: int, K, ldk: int, V, ldv: int, type: int, rows: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_kv_write(_addr(pages), n_pages, page_tokens, kv_heads, d, ctype, _addr(table), ldt, _addr(lens),
+                          _addr(starts), n_seq, _addr(K), ldk, _addr(V), ldv, type, rows, _stream(stream))
+    return _check(rc, "q4_kv_write") if check else rc
+
+
+def q4_kv_read(K, ldk: int, V, ldv: int, type: int, pages, n_pages: int, page_tokens: int, kv_heads: int, d: int,
+               ctype: int, table, ldt: int, first, starts, n_seq: int, rows: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_kv_read(_addr(K), ldk, _addr(V), ldv, type, _addr(pages), n_pages, page_tokens, kv_heads, d, ctype,
+                         _addr(table), ldt, _addr(first), _addr(starts), n_seq, rows, _stream(stream))
+    return _check(rc, "q4_kv_read") if check else rc
+
+
+def q4_attention_workspace_size(rows: int, n_seq: int, heads: int, kv_heads: int, d: int) -> int:
+    return int(_lib.q4_attention_workspace_size(rows, n_seq, heads, kv_heads, d))
+
+
+def q4_attention(O, ldo: int, Q, ldq: int, type: int, heads: int, scale: float, window: int, pages, n_pages: int,
+                 page_tokens: int, kv_heads: int, d: int, ctype: int, table, ldt: int, lens, starts, n_seq: int,
+                 rows: int, max_new: int, workspace, workspace_bytes: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_attention(_addr(O), ldo, _addr(Q), ldq, type, heads, scale, window, _addr(pages), n_pages, page_tokens,
+                           kv_heads, d, ctype, _addr(table), ldt, _addr(lens), _addr(starts), n_seq, rows, max_new,
+                           _addr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "q4_attention") if check else rc
+
+
+def q4_token_probs(P, ldp: int, logits, ldl: int, type: int, temperature, rows: int, n: int, stream=None,
+                   check: bool = True) -> int:
+    rc = _lib.q4_token_probs(_addr(P), ldp, _addr(logits), ldl, type, _addr(temperature), rows, n, _stream(stream))
+    return _check(rc, "q4_token_probs") if check else rc
+
+
+def q4_draft_verify(tokens, ldt: int, kept, P, ldp: int, Q, ldq: int, drafted, ldd: int, counts, accept, lda: int, sample,
+                    n_seq: int, max_draft: int, n: int, stream=None, check: bool = True) -> int:
+    rc = _lib.q4_draft_verify(_addr(tokens), ldt, _addr(kept), _addr(P), ldp, _addr(Q), ldq, _addr(drafted), ldd,
+                              _addr(counts), _addr(accept), lda, _addr(sample), n_seq, max_draft, n, _stream(stream))
+    return _check(rc, "q4_draft_verify") if check else rc
 
 
 Q4_STATIC_SCRATCH_BYTES = 8 << 20

@@ -1,0 +1,121 @@
+// q4mm_attn.cu -- the attention's launches by kind, and the join of what was cut.
+#include <algorithm>
+
+#include "q4mm_attn.cuh"
+
+namespace q4 {
+
+cudaError_t launch_attn_f16(const AttnArgs &a, int sm_count, cudaStream_t s, int *ctas);
+cudaError_t launch_attn_f16x2(const AttnArgs &a, int sm_count, cudaStream_t s, int *ctas);
+cudaError_t launch_attn_bf16(const AttnArgs &a, int sm_count, cudaStream_t s, int *ctas);
+cudaError_t launch_attn_i8(const AttnArgs &a, int sm_count, cudaStream_t s, int *ctas);
+cudaError_t launch_attn_i8x2(const AttnArgs &a, int sm_count, cudaStream_t s, int *ctas);
+
+namespace {
+
+constexpr int kJoinThreads = 256;
+
+// o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over an item's parts i, the
+// CTAs' that follow the one it starts in. A CTA takes a row at a time: the
+// weights first, then W / 4 threads a part, four dims each; the groups of
+// threads take every n-th part, and their sums are added in order.
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a)
+{
+    __shared__ float weight[kAttnMaxCtas + 1];
+    __shared__ float4 sums[kJoinThreads];
+    __shared__ float warp_red[kJoinThreads / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int4 item = a.meta[blockIdx.x];
+    const int parts = item.w;
+    if (parts == 0) return;
+    const Seq q = seq_at(a, item.x);
+    const int W = kChunk * a.c.chunks, lanes = W / 4, groups = kJoinThreads / lanes;
+    const int tid = threadIdx.x, grp = tid / lanes, x = tid - grp * lanes;
+    const int64_t size = attn_part_floats(a.block, a.c.chunks);
+    const int rows = min(a.block, q.rows - item.z * a.block);
+    const auto part_at = [&](int i) { return a.parts + (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0)) * size; };
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        float m = neg_inf();
+        for (int i = tid; i < parts; i += kJoinThreads) m = fmaxf(m, part_at(i)[a.block * W + r]);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        __syncthreads();
+        if (tid % 32 == 0) warp_red[tid / 32] = m;
+        __syncthreads();
+        m = warp_red[0];
+#pragma unroll
+        for (int i = 1; i < kJoinThreads / 32; ++i) m = fmaxf(m, warp_red[i]);
+        float l = 0.0f;
+        for (int i = tid; i < parts; i += kJoinThreads) {
+            const float *p = part_at(i);
+            const float mi = p[a.block * W + r];
+            const float w = mi == neg_inf() ? 1.0f : exp2_fast(mi - m);   // (then its sums are zeros or NaN)
+            weight[i] = w;
+            l += w * p[a.block * W + a.block + r];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        __syncthreads();
+        if (tid % 32 == 0) warp_red[tid / 32] = l;
+        __syncthreads();
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kJoinThreads / 32; ++i) l += warp_red[i];
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (grp < groups) {
+#pragma unroll 4
+            for (int i = grp; i < parts; i += groups) {
+                const float4 v = *reinterpret_cast<const float4 *>(part_at(i) + r * W + 4 * x);
+                const float w = weight[i];
+                s.x += w * v.x, s.y += w * v.y, s.z += w * v.z, s.w += w * v.w;
+            }
+            sums[tid] = s;
+        }
+        __syncthreads();
+        if (grp == 0) {
+            for (int i = 1; i < groups; ++i) {
+                const float4 v = sums[i * lanes + x];
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const int row = item.z * a.block + r, i = row / a.group, head = item.y * a.group + row - i * a.group;
+            const int64_t out = (static_cast<int64_t>(q.start) + i) * a.ldo + static_cast<int64_t>(head) * a.c.d;
+            const float v[4] = {s.x * inv, s.y * inv, s.z * inv, s.w * inv};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int dim = 4 * x + e;
+                if (dim >= a.c.d) continue;
+                if (a.type == Q4_TYPE_F32) static_cast<float *>(a.O)[out + dim] = v[e];
+                else if (a.type == Q4_TYPE_F16) static_cast<__half *>(a.O)[out + dim] = __float2half_rn(v[e]);
+                else static_cast<__nv_bfloat16 *>(a.O)[out + dim] = __float2bfloat16_rn(v[e]);
+            }
+        }
+    }
+}
+
+} // namespace
+
+cudaError_t launch_attn_join(const AttnArgs &args, int ctas, cudaStream_t s)
+{
+    AttnArgs a = args;
+    void *p[] = {&a};
+    const unsigned rows = static_cast<unsigned>(a.block <= 64 ? a.block / 4 : 32);
+    return launch_pdl(reinterpret_cast<const void *>(&attn_join_kernel), dim3(static_cast<unsigned>(ctas), rows), dim3(kJoinThreads), 0, s, p);
+}
+
+cudaError_t launch_attn_warp(AttnArgs a, int sm_count, cudaStream_t s)
+{
+    a.tile = kWarpTile;
+    int ctas = 0;
+    const bool wide = a.type == Q4_TYPE_F32;
+    cudaError_t e;
+    switch (a.c.type) {
+    case Q4_TYPE_F16: e = wide ? launch_attn_f16x2(a, sm_count, s, &ctas) : launch_attn_f16(a, sm_count, s, &ctas); break;
+    case Q4_TYPE_BF16: e = launch_attn_bf16(a, sm_count, s, &ctas); break;
+    default: e = wide ? launch_attn_i8x2(a, sm_count, s, &ctas) : launch_attn_i8(a, sm_count, s, &ctas); break;
+    }
+    return e != cudaSuccess ? e : launch_attn_join(a, ctas, s);
+}
+
+} // namespace q4

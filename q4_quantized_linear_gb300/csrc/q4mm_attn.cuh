@@ -1,0 +1,213 @@
+// q4mm_attn.cuh -- what the attention kernels share: which work a CTA takes,
+// the copies of a tile, and small pieces of arithmetic.
+//
+// An item is a block of query rows of one sequence and one cached head: row r of
+// a sequence stands for new token r / group and query head head * group + r %
+// group, so that all query heads of a cached head share what is read of it. An
+// item's work is its tiles of tokens, from the first that any row sees to the
+// last. The tiles of all items in a row (sequence, head, block, tile) are dealt
+// to the CTAs in equal contiguous shares: no host code needs to know the
+// sequences' lengths, and a long sequence is spread over many CTAs. An item that
+// is cut leaves parts (sums without their denominator, maxima, denominators),
+// which the join adds in the order of the tiles.
+#pragma once
+
+#include "q4mm_cache.h"
+#include "q4mm_rows.cuh"
+
+namespace q4 {
+
+struct Seq {
+    int n, len, start, rows, blocks;   // new tokens, tokens held, first row, query rows, blocks of them
+};
+
+__device__ __forceinline__ Seq seq_at(const AttnArgs &a, int s)
+{
+    const int lo = min(max(a.starts[s], 0), a.rows), hi = min(max(a.starts[s + 1], 0), a.rows);
+    Seq q;
+    q.n = max(hi - lo, 0);
+    q.start = lo;
+    q.len = min(max(a.lens[s], 0), a.c.capacity);
+    q.rows = q.n * a.group;
+    if (q.rows <= a.rows_above || q.rows > a.rows_upto) q.rows = 0;
+    q.blocks = (q.rows + a.block - 1) / a.block;
+    return q;
+}
+// Tokens lo .. hi - 1 that query row r sees.
+__device__ __forceinline__ void row_range(const AttnArgs &a, const Seq &q, int r, int &lo, int &hi)
+{
+    const int pos = q.len - q.n + r / a.group;
+    hi = max(pos + 1, 0);
+    lo = a.window > 0 ? max(hi - a.window, 0) : 0;
+}
+// Tiles of block b: the first, and how many (one at least, so that rows that see
+// nothing are written too); `hi`: tokens past it are seen by none of its rows.
+__device__ __forceinline__ void block_tiles(const AttnArgs &a, const Seq &q, int b, int &first, int &count, int &hi)
+{
+    int lo, x;
+    row_range(a, q, b * a.block, lo, x);
+    row_range(a, q, min((b + 1) * a.block, q.rows) - 1, x, hi);
+    first = lo / a.tile;
+    count = max((hi + a.tile - 1) / a.tile - first, 1);
+}
+
+// The items of a CTA's share, in order. Every thread of the CTA walks alike.
+struct Walk {
+    int s, h, b;              // the item
+    Seq q;
+    int first, count, hi;     // its tiles
+    int from, upto;           // those of them that are this CTA's
+    long long left;           // tiles of the share from this item on
+    long long share;
+
+    __device__ __forceinline__ bool whole() const { return from == 0 && upto == count; }
+    __device__ __forceinline__ void clip()
+    {
+        upto = left < static_cast<long long>(count - from) ? from + static_cast<int>(left) : count;
+    }
+    // `scan`: shared memory of n_seq + 1 numbers, free again after the next barrier.
+    __device__ __forceinline__ void begin(const AttnArgs &a, long long *scan)
+    {
+        for (int i = threadIdx.x; i < a.n_seq; i += blockDim.x) {
+            const Seq x = seq_at(a, i);
+            long long w = 0;
+            for (int j = 0; j < x.blocks; ++j) {
+                int f, n, e;
+                block_tiles(a, x, j, f, n, e);
+                w += n;
+            }
+            scan[i] = w;
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            long long carry = 0;
+            for (int i0 = 0; i0 < a.n_seq; i0 += 32) {
+                const int i = i0 + threadIdx.x;
+                long long v = i < a.n_seq ? scan[i] * a.c.heads : 0;
+                const long long own = v;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                    if (threadIdx.x >= o) v += u;
+                }
+                if (i < a.n_seq) scan[i] = carry + v - own;
+                carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+            }
+            if (threadIdx.x == 0) scan[a.n_seq] = carry;
+        }
+        __syncthreads();
+        const long long total = scan[a.n_seq];
+        share = (total + gridDim.x - 1) / gridDim.x;
+        const long long at = share * blockIdx.x;
+        left = total - at < share ? total - at : share;
+        if (left <= 0) {
+            left = 0;
+            return;
+        }
+        int lo = 0, hi_s = a.n_seq - 1;   // the last sequence whose work starts at or before `at`
+        while (lo < hi_s) {
+            const int mid = (lo + hi_s + 1) >> 1;
+            if (scan[mid] <= at) lo = mid;
+            else hi_s = mid - 1;
+        }
+        s = lo;
+        q = seq_at(a, s);
+        const long long per = (scan[s + 1] - scan[s]) / a.c.heads, x = at - scan[s];
+        h = static_cast<int>(x / per);
+        long long y = x - h * per;
+        for (b = 0;; ++b) {
+            block_tiles(a, q, b, first, count, hi);
+            if (y < count || b + 1 >= q.blocks) break;
+            y -= count;
+        }
+        from = static_cast<int>(y);
+        clip();
+    }
+    __device__ __forceinline__ bool valid() const { return left > 0; }
+    __device__ __forceinline__ void next(const AttnArgs &a)
+    {
+        left -= upto - from;
+        if (left <= 0) return;
+        if (++b >= q.blocks) {
+            b = 0;
+            if (++h >= a.c.heads) {
+                h = 0;
+                do {
+                    if (++s >= a.n_seq) {
+                        left = 0;
+                        return;
+                    }
+                    q = seq_at(a, s);
+                } while (q.blocks == 0);
+            }
+        }
+        block_tiles(a, q, b, first, count, hi);
+        from = 0;
+        clip();
+    }
+    // Parts of an item that starts in this CTA and is not finished in it.
+    __device__ __forceinline__ int parts() const
+    {
+        const long long rest = static_cast<long long>(count) - upto;
+        return 1 + static_cast<int>((rest + share - 1) / share);
+    }
+};
+
+// ----------------------------------------------------------- arithmetic --
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xFF800000); }
+__device__ __forceinline__ uint32_t pack_f16x2_rn(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// Four codes of a word to fp16, exact: the code plus 128 in the low byte of
+// 1024 + (code + 128), less 1152.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t x = w ^ 0x80808080u;
+    lo = hsub2_bits(__byte_perm(x, 0x64646464u, 0x4140), 0x64806480u);
+    hi = hsub2_bits(__byte_perm(x, 0x64646464u, 0x4342), 0x64806480u);
+}
+
+// How far a row's running maximum may be passed before the sums are scaled to
+// the new one: terms stay below 2^kSlack, and most tiles scale nothing.
+constexpr float kSlack = 8.0f;
+// Terms are held 2^kLift times larger (below 2^15), so that small ones keep their
+// bits in fp16: what is lost is below 2^-32 of the largest term.
+constexpr float kLift = 7.0f;
+
+// A row's 8 values from dim c on, as fp32 (zeros past d).
+template <typename T> __device__ __forceinline__ void row8(const T *p, bool vec, float (&f)[8])
+{
+    if (vec) {
+        constexpr int V = 16 / sizeof(T);
+#pragma unroll
+        for (int j = 0; j < 8 / V; ++j) {
+            const Pack<T, V> x = load_pack<T, V>(p, j * V, 8);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[j * V + i] = elem(x, i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = elem(load_pack<T, 1>(p, i, 8), 0);
+    }
+}
+__device__ __forceinline__ void query8(const AttnArgs &a, int64_t at, float (&f)[8])
+{
+    if (a.type == Q4_TYPE_F32) row8(static_cast<const float *>(a.Q) + at, a.vec, f);
+    else if (a.type == Q4_TYPE_F16) row8(static_cast<const __half *>(a.Q) + at, a.vec, f);
+    else row8(static_cast<const __nv_bfloat16 *>(a.Q) + at, a.vec, f);
+}
+
+} // namespace q4

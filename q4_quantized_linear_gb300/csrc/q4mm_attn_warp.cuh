@@ -1,0 +1,663 @@
+// q4mm_attn_warp.cuh -- attention of few query rows over the paged cache, on the
+// warp-level MMA: o = sum_j p_j v_j / sum_j p_j, p_j = 2^(s_j - m), s_j = scale
+// log2(e) <q, k_j>, in one pass over the tokens with a running maximum m.
+//
+// For few rows the bound is the read of the cache. A warp of the CTA copies tiles
+// of 64 tokens (K and V of one head: contiguous rows of 128 bytes, a copy for
+// each page and 64 dims) into a ring; four warps compute. A block of 16 query
+// rows: each warp takes 16 of a tile's tokens, with a running state of its own,
+// joined at the item's end; of 32 rows: two warps by rows, two by tokens; of 64:
+// four by rows. So each value of the cache is turned into an operand once for 16
+// and 32 rows, and by four warps for 64 rows.
+//   Scores and terms stay in registers: the accumulator of S = Q K^T has the
+// layout of the A operand of P V.
+//   Codes of an int8 cache are exact in fp16; a token's key scale multiplies its
+// scores, its value scale its term. Terms times value scales are brought into
+// fp16's range by a power of two of the tokens that the row has seen (E), the sums
+// with them.
+//   TERMS = 2 (fp32 queries and outputs): queries, scaled by a power of two a row,
+// and terms are split into two fp16 numbers (22 bits); the MMA cuts its running
+// sum to fp32, so the sums over a tile start at zero and are added in fp32.
+//   A page's rows past the sequence's end are never copied: what their place in
+// the ring holds is zeros or an earlier tile's, finite as all values of the cache.
+#pragma once
+
+#include "q4mm_attn.cuh"
+
+namespace q4 {
+namespace {
+
+constexpr int kF16 = 0, kBF16 = 1, kI8 = 2;   // operands: fp16 or bf16 as cached, or codes as fp16
+constexpr int kComputeWarps = 4;
+constexpr int kAttnThreads = (kComputeWarps + 1) * 32;
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <bool BF> __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 lds128_at(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+// Value scales up to v: e is raised so that they are below 2^e, and what the sums
+// so far are multiplied by is returned.
+__device__ __forceinline__ float raise(int &e, float v)
+{
+    if (v < pow2(e)) return 1.0f;
+    const int to = min(((__float_as_int(v) >> 23) & 255) - 126, 126);
+    const float down = to - e > 126 ? 0.0f : pow2(e - to);
+    e = to;
+    return down;
+}
+__device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory"); }
+
+// DP: 64 x chunks, or 256 for three and four chunks. WM: 16-row slices of a block.
+template <int KIND, int TERMS, int WM, int DP> struct WarpShape {
+    static constexpr int kBlock = 16 * WM, kWN = kComputeWarps / WM, kTokens = kWarpTile / kWN;
+    static constexpr int kNT = kTokens / 8;                 // score column tiles of a warp
+    static constexpr int kRowBytes = KIND == kI8 ? 64 : 128;   // of a token in a chunk
+    static constexpr int kMaxChunks = DP / kChunk;
+    static constexpr int kQStride = DP * 2 + 16;            // bytes of a query row in shared memory
+    static constexpr int kQBytes = kBlock * kQStride * TERMS;
+    static constexpr int kRedBytes = WM * (kWN - 1) * 16 * DP / 2 * 4;   // sums handed over at an item's end, half the dims at once
+    static constexpr int kFixed = kQBytes + kRedBytes + kBlock * 4 + 4 * 16 * 8 + 144;
+    static constexpr bool kQInRegs = DP <= 128 && TERMS == 1;
+};
+inline int warp_stage_bytes(int chunks, int ctype)
+{
+    return ctype == Q4_TYPE_I8 ? kWarpTile * (2 * chunks * 64 + 8) : kWarpTile * 2 * chunks * 128;
+}
+
+template <int KIND, int TERMS, int WM, int DP>
+__global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_kernel(const AttnArgs a)
+{
+    using S = WarpShape<KIND, TERMS, WM, DP>;
+    constexpr bool BF = KIND == kBF16;
+    constexpr int WN = S::kWN, NT = S::kNT, RB = S::kRowBytes, OT = DP / 8;
+    extern __shared__ __align__(128) uint8_t ring[];        // tiles, then what follows
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int chunks = DP <= 128 ? DP / kChunk : a.c.chunks;
+    const int half = kWarpTile * RB * chunks;               // K, then V
+    const int stage_bytes = 2 * half + (KIND == kI8 ? kWarpTile * 8 : 0);
+    uint8_t *qs = ring + a.stages * stage_bytes;
+    float *red = reinterpret_cast<float *>(qs + S::kQBytes);
+    float *row_factor = red + S::kRedBytes / 4;
+    float2 *red_ml = reinterpret_cast<float2 *>(row_factor + S::kBlock);   // [4 warps][16]
+    uint64_t *full = reinterpret_cast<uint64_t *>(red_ml + 4 * 16), *empty = full + 8;
+    int *abort = reinterpret_cast<int *>(empty + 8);
+    if (tid == 0) {
+        for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], kComputeWarps);
+        *abort = 0;
+        fence_barrier_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    Walk w;
+    w.begin(a, reinterpret_cast<long long *>(ring));
+    __syncthreads();
+    // Values' places in the ring start as zeros: see above.
+    if (KIND != kI8)
+        for (int i = 0; i < a.stages; ++i)
+            for (int x = tid; x < half / 16; x += kAttnThreads)
+                sts128(ring + i * stage_bytes + half + 16 * x, make_uint4(0u, 0u, 0u, 0u));
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+
+    if (warp == kComputeWarps) {
+        // ---------------------------------------------------------- copies
+        int stage = 0;
+        uint32_t phase = 0;
+        long long issued = 0;
+        bool ok = true;
+        const int per_page = 2 * chunks + (KIND == kI8 ? 2 : 0);
+        const int in_page = a.c.page_tokens;
+        for (; ok && w.valid(); w.next(a)) {
+            const int32_t *table = a.c.table + w.s * a.c.ldt;
+            const int64_t head = static_cast<int64_t>(w.h) * a.c.head_bytes;
+            const int end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> a.c.log_page;
+            int held = -32, page = 0;                       // lane l holds page held + l of the sequence
+            for (int t = w.from; t < w.upto; ++t) {
+                const int t0 = (w.first + t) * kWarpTile, tokens = min(max(end - t0, 0), kWarpTile);
+                if (*reinterpret_cast<volatile int *>(abort)) { ok = false; break; }
+                if (issued >= a.stages && !mbar_wait(&empty[stage], phase ^ 1u, a.wait_ns)) {
+                    *reinterpret_cast<volatile int *>(abort) = 1;
+                    record_status(a.status, kErrTimeout);
+                    ok = false;
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok) != 0;
+                if (!ok) break;
+                uint8_t *dst = ring + stage * stage_bytes;
+                const int scale_tokens = KIND == kI8 ? (tokens + 3) & ~3 : 0;
+                if (lane == 0) {
+                    // `pieces` copies add up to this; a tile without tokens has none
+                    mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(tokens * 2 * chunks * RB + 8 * scale_tokens));
+                }
+                __syncwarp();
+                const int p0 = t0 >> a.c.log_page, np = tokens > 0 ? ((t0 + tokens - 1) >> a.c.log_page) - p0 + 1 : 0;
+                if (np > 0 && p0 + np > held + 32) {
+                    held = p0;
+                    page = held + lane < pages ? table[held + lane] : 0;
+                    if (page < 0 || page >= a.c.n_pages) {
+                        record_status(a.status, kErrCheck);
+                        page = min(max(page, 0), a.c.n_pages - 1);
+                    }
+                }
+                const int pieces = np * per_page;
+                for (int x0 = 0; x0 < pieces; x0 += 32) {
+                    const int x = x0 + lane, j = x / per_page, y = x - j * per_page;
+                    const int pg = __shfl_sync(0xFFFFFFFFu, page, min(p0 + j - held, 31));
+                    if (x < pieces) {
+                        const int in = max(t0 - ((p0 + j) << a.c.log_page), 0);          // first token of the page that is in the tile
+                        const int at = ((p0 + j) << a.c.log_page) + in - t0;             // its place in the tile
+                        const int n = min(in_page - in, tokens - at);
+                        const uint8_t *src = a.c.pages + pg * a.c.page_bytes + head;
+                        if (y < 2 * chunks)
+                            bulk_g2s(dst + y * (kWarpTile * RB) + at * RB, src + (y * in_page + in) * RB,
+                                     static_cast<uint32_t>(n * RB), &full[stage]);
+                        else
+                            bulk_g2s(dst + 2 * half + (y - 2 * chunks) * (kWarpTile * 4) + at * 4,
+                                     src + 2 * chunks * in_page * RB + ((y - 2 * chunks) * in_page + in) * 4,
+                                     static_cast<uint32_t>(((n + 3) & ~3) * 4), &full[stage]);
+                    }
+                }
+                ++issued;
+                if (++stage == a.stages) stage = 0, phase ^= 1u;
+            }
+        }
+        // no copy may be landing when the CTA leaves
+        for (long long i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i)
+            if (!mbar_wait(&full[i % a.stages], static_cast<uint32_t>(i / a.stages) & 1u, landing_limit(a.wait_ns)))
+                record_status(a.status, kErrTimeout);
+        return;
+    }
+
+    // ------------------------------------------------------------- compute
+    const int wm = warp / WN, wn = warp % WN;
+    const uint32_t qbase = smem_u32(qs), ring_at = smem_u32(ring);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool alive = true;                                      // a wait ran out: no tile is looked at any more
+    for (; w.valid(); w.next(a)) {
+        // Queries: a warp a row at a time, a lane 8 dims.
+        compute_barrier();                                  // the item before is done with them
+#pragma unroll 2
+        for (int r = warp; r < S::kBlock; r += kComputeWarps) {
+            const int row = w.b * S::kBlock + r;
+            float f[8] = {};
+            if (row < w.q.rows && 8 * lane < a.c.d) {
+                const int i = row / a.group, head = w.h * a.group + row - i * a.group;
+                query8(a, (static_cast<int64_t>(w.q.start) + i) * a.ldq + head * a.c.d + 8 * lane, f);
+            }
+            float factor = a.scale_log2;
+            if (KIND == kI8 || TERMS == 2) {
+                // to fp16's range by a power of two: the largest in 2^12 .. 2^13
+                uint32_t mb = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mb = max(mb, abs_bits(f[i]));
+                mb = __reduce_max_sync(0xFFFFFFFFu, mb);
+                if (mb >= 0x7F800000u) {
+                    factor = __uint_as_float(0x7FC00000u);  // a query that is not finite: NaN
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+                } else if (mb != 0u) {
+                    const int e = min(max(139 - static_cast<int>(mb >> 23), -126), 126);   // 12 - exponent
+                    const float up = pow2(e);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] *= up;
+                    factor *= pow2(-e);
+                }
+            }
+            if (8 * lane < DP) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (BF) {
+                        hi[i] = pack_bf16x2_rn(f[2 * i], f[2 * i + 1]);
+                    } else {
+                        hi[i] = pack_f16x2_rn(f[2 * i], f[2 * i + 1]);
+                        if (TERMS == 2) {
+                            const __half2 h2 = *reinterpret_cast<__half2 *>(&hi[i]);
+                            lo[i] = pack_f16x2_rn(f[2 * i] - __low2float(h2), f[2 * i + 1] - __high2float(h2));
+                        }
+                    }
+                }
+                sts128(qs + r * S::kQStride + 16 * lane, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                if (TERMS == 2)
+                    sts128(qs + S::kBlock * S::kQStride + r * S::kQStride + 16 * lane, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+            }
+            if (lane == 0) row_factor[r] = factor;
+        }
+        compute_barrier();
+        // A operand of 16 dims (k-step ks): for codes the dims in the order in which a
+        // lane's 16 bytes of a token hold them.
+        const auto load_q = [&](int term, int ks, uint32_t (&q)[4]) {
+            const uint32_t at = qbase + term * (S::kBlock * S::kQStride) + (wm * 16 + g) * S::kQStride;
+            if constexpr (KIND == kI8) {
+                const uint32_t dim = (ks / 4) * kChunk + 16 * c + 4 * (ks % 4);
+                const uint2 x = lds64(at + 2 * dim), y = lds64(at + 8 * S::kQStride + 2 * dim);
+                q[0] = x.x, q[1] = y.x, q[2] = x.y, q[3] = y.y;
+            } else {
+                const uint32_t dim = 16 * ks + 2 * c;
+                q[0] = lds32(at + 2 * dim);
+                q[1] = lds32(at + 8 * S::kQStride + 2 * dim);
+                q[2] = lds32(at + 2 * dim + 16);
+                q[3] = lds32(at + 8 * S::kQStride + 2 * dim + 16);
+            }
+        };
+        uint32_t qr[S::kQInRegs ? DP / 16 : 1][4];
+        if constexpr (S::kQInRegs) {
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) load_q(0, ks, qr[ks]);
+        }
+        const float rf0 = row_factor[wm * 16 + g], rf1 = row_factor[wm * 16 + g + 8];
+        int lo0, hi0, lo1, hi1, full_from, full_upto;
+        const int end = min(w.hi, w.q.len);
+        {
+            const int r0 = min(w.b * S::kBlock + wm * 16 + g, w.q.rows - 1), r1 = min(w.b * S::kBlock + wm * 16 + g + 8, w.q.rows - 1);
+            row_range(a, w.q, r0, lo0, hi0);
+            row_range(a, w.q, r1, lo1, hi1);
+            int x;
+            row_range(a, w.q, w.b * S::kBlock, x, full_upto);                                  // the first row's end
+            row_range(a, w.q, min((w.b + 1) * S::kBlock, w.q.rows) - 1, full_from, x);         // the last row's start
+        }
+        float o[OT][4] = {};
+        float m0 = neg_inf(), m1 = neg_inf(), l0 = 0.0f, l1 = 0.0f;
+        int E0 = -118, E1 = -118;                           // value scales that the rows have seen are below 2^E
+        for (int t = w.from; alive && t < w.upto; ++t) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, a.wait_ns))) {
+                if (lane == 0) {
+                    *reinterpret_cast<volatile int *>(abort) = 1;
+                    record_status(a.status, kErrTimeout);
+                }
+                alive = false;                              // (the warps still meet at the items' barriers)
+                break;
+            }
+            const uint32_t kv = ring_at + stage * stage_bytes;
+            const int tok = wn * S::kTokens;                // the warp's tokens of the tile
+            const int t0 = (w.first + t) * kWarpTile + tok;
+            float s[NT][4] = {};
+            float s2[TERMS == 2 ? NT : 1][4] = {};
+#pragma unroll
+            for (int ch = 0; ch < S::kMaxChunks; ++ch) {
+                if (ch < chunks) {
+                    if constexpr (KIND == kI8) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int row = tok + nt * 8 + g;
+                            const uint4 x = lds128_at(kv + ch * (kWarpTile * RB) + row * RB + ((c ^ ((row >> 1) & 3)) << 4));
+                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int k4 = 0; k4 < 4; ++k4) {
+                                uint32_t b0, b1;
+                                codes_f16(xs[k4], b0, b1);
+                                if constexpr (S::kQInRegs) {
+                                    mma16816<BF>(s[nt], qr[ch * 4 + k4], b0, b1);
+                                } else {
+                                    uint32_t q[4];
+                                    load_q(0, ch * 4 + k4, q);
+                                    mma16816<BF>(s[nt], q, b0, b1);
+                                    if constexpr (TERMS == 2) {
+                                        load_q(1, ch * 4 + k4, q);
+                                        mma16816<BF>(s2[nt], q, b0, b1);
+                                    }
+                                }
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {       // 32 dims
+                            uint32_t q[2][4], q2[2][4];
+                            if constexpr (!S::kQInRegs) {
+                                load_q(0, ch * 4 + 2 * p, q[0]), load_q(0, ch * 4 + 2 * p + 1, q[1]);
+                                if constexpr (TERMS == 2) load_q(1, ch * 4 + 2 * p, q2[0]), load_q(1, ch * 4 + 2 * p + 1, q2[1]);
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const int row = tok + nt * 8 + (lane & 7);
+                                uint32_t b[4];
+                                ldsm4(kv + ch * (kWarpTile * RB) + row * RB + (((4 * p + (lane >> 3)) ^ (row & 7)) << 4), b);
+                                if constexpr (S::kQInRegs) {
+                                    mma16816<BF>(s[nt], qr[ch * 4 + 2 * p], b[0], b[1]);
+                                    mma16816<BF>(s[nt], qr[ch * 4 + 2 * p + 1], b[2], b[3]);
+                                } else {
+                                    mma16816<BF>(s[nt], q[0], b[0], b[1]);
+                                    mma16816<BF>(s[nt], q[1], b[2], b[3]);
+                                    if constexpr (TERMS == 2) {
+                                        mma16816<BF>(s2[nt], q2[0], b[0], b[1]);
+                                        mma16816<BF>(s2[nt], q2[1], b[2], b[3]);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            // scores in powers of two
+            float sv[KIND == kI8 ? NT : 1][2];
+            const uint32_t scales = kv + 2 * half;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (TERMS == 2) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[nt][i] += s2[nt][i];
+                }
+                float f0 = rf0, f1 = rf0, f2v = rf1, f3 = rf1;
+                if constexpr (KIND == kI8) {
+                    const uint2 k2 = lds64(scales + 4 * (tok + nt * 8 + 2 * c));
+                    const uint2 v2 = lds64(scales + 4 * (kWarpTile + tok + nt * 8 + 2 * c));
+                    f0 *= __uint_as_float(k2.x), f1 *= __uint_as_float(k2.y);
+                    f2v *= __uint_as_float(k2.x), f3 *= __uint_as_float(k2.y);
+                    sv[nt][0] = __uint_as_float(v2.x), sv[nt][1] = __uint_as_float(v2.y);
+                }
+                s[nt][0] *= f0, s[nt][1] *= f1, s[nt][2] *= f2v, s[nt][3] *= f3;
+            }
+            float v0max = 0.0f, v1max = 0.0f;               // value scales that the rows see
+            if (t0 + S::kTokens > full_upto || t0 < full_from) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int x = t0 + nt * 8 + 2 * c + i;
+                        const bool sees0 = x >= lo0 && x < hi0 && x < end, sees1 = x >= lo1 && x < hi1 && x < end;
+                        if (!sees0) s[nt][i] = neg_inf();
+                        if (!sees1) s[nt][2 + i] = neg_inf();
+                        if constexpr (KIND == kI8) {
+                            if (x >= end) sv[nt][i] = 0.0f;     // a token that was not copied has no scale
+                            if (sees0) v0max = fmaxf(v0max, sv[nt][i]);
+                            if (sees1) v1max = fmaxf(v1max, sv[nt][i]);
+                        }
+                    }
+                }
+            } else if constexpr (KIND == kI8) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) v0max = fmaxf(v0max, fmaxf(sv[nt][0], sv[nt][1]));
+                v1max = v0max;
+            }
+            float x0 = neg_inf(), x1 = neg_inf();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                x0 = fmaxf(x0, fmaxf(s[nt][0], s[nt][1]));
+                x1 = fmaxf(x1, fmaxf(s[nt][2], s[nt][3]));
+            }
+            x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
+            x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 2));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 2));
+            bool wide = false;
+            if constexpr (KIND == kI8) {
+                v0max = fmaxf(v0max, __shfl_xor_sync(0xFFFFFFFFu, v0max, 1));
+                v1max = fmaxf(v1max, __shfl_xor_sync(0xFFFFFFFFu, v1max, 1));
+                v0max = fmaxf(v0max, __shfl_xor_sync(0xFFFFFFFFu, v0max, 2));
+                v1max = fmaxf(v1max, __shfl_xor_sync(0xFFFFFFFFu, v1max, 2));
+                wide = v0max >= pow2(E0) || v1max >= pow2(E1);
+            }
+            if (__any_sync(0xFFFFFFFFu, x0 > m0 + kSlack || x1 > m1 + kSlack || wide)) {
+                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+                float a0 = m0 == neg_inf() ? 0.0f : exp2_fast(m0 - n0), a1 = m1 == neg_inf() ? 0.0f : exp2_fast(m1 - n1);
+                m0 = n0, m1 = n1;
+                l0 *= a0, l1 *= a1;
+                if constexpr (KIND == kI8) {
+                    a0 *= raise(E0, v0max), a1 *= raise(E1, v1max);
+                }
+#pragma unroll
+                for (int j = 0; j < OT; ++j) o[j][0] *= a0, o[j][1] *= a0, o[j][2] *= a1, o[j][3] *= a1;
+            }
+            const float u0 = m0 == neg_inf() ? 0.0f : m0 - kLift, u1 = m1 == neg_inf() ? 0.0f : m1 - kLift;
+            const float down0 = KIND == kI8 ? pow2(-E0) : 1.0f, down1 = KIND == kI8 ? pow2(-E1) : 1.0f;
+            uint32_t p[NT / 2][4], p2[TERMS == 2 ? NT / 2 : 1][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float e[4] = {exp2_fast(s[nt][0] - u0), exp2_fast(s[nt][1] - u0), exp2_fast(s[nt][2] - u1), exp2_fast(s[nt][3] - u1)};
+                l0 += e[0] + e[1], l1 += e[2] + e[3];
+                if constexpr (KIND == kI8) {
+                    // (below 1 where the row sees the token; finite times 0 where not)
+                    e[0] *= fminf(sv[nt][0] * down0, 1.0f), e[1] *= fminf(sv[nt][1] * down0, 1.0f);
+                    e[2] *= fminf(sv[nt][0] * down1, 1.0f), e[3] *= fminf(sv[nt][1] * down1, 1.0f);
+                }
+                const int at = 2 * (nt & 1);
+                if constexpr (BF) {
+                    p[nt / 2][at] = pack_bf16x2_rn(e[0], e[1]), p[nt / 2][at + 1] = pack_bf16x2_rn(e[2], e[3]);
+                } else {
+                    p[nt / 2][at] = pack_f16x2_rn(e[0], e[1]), p[nt / 2][at + 1] = pack_f16x2_rn(e[2], e[3]);
+                    if constexpr (TERMS == 2) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const __half2 h2 = *reinterpret_cast<__half2 *>(&p[nt / 2][at + i]);
+                            p2[nt / 2][at + i] = pack_f16x2_rn(e[2 * i] - __low2float(h2), e[2 * i + 1] - __high2float(h2));
+                        }
+                    }
+                }
+            }
+            // sums of values
+#pragma unroll
+            for (int ch = 0; ch < S::kMaxChunks; ++ch) {
+                if (ch < chunks) {
+                    const uint32_t vb = kv + half + ch * (kWarpTile * RB);
+                    if constexpr (KIND == kI8) {
+                        // eight dims of a lane (8 g ..), as the n of eight column tiles
+                        float fresh[TERMS == 2 ? 8 : 1][4] = {};
+#pragma unroll
+                        for (int k = 0; k < NT / 2; ++k) {
+                            uint2 x[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int row = tok + 16 * k + 2 * c + (i & 1) + 8 * (i >> 1);
+                                x[i] = lds64(vb + row * RB + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g & 1));
+                                x[i].x ^= 0x80808080u, x[i].y ^= 0x80808080u;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint32_t sel = 0x40u + 0x11u * (j & 3);   // byte j of the first token, of the second
+                                const uint32_t t01 = __byte_perm(j < 4 ? x[0].x : x[0].y, j < 4 ? x[1].x : x[1].y, sel);
+                                const uint32_t t23 = __byte_perm(j < 4 ? x[2].x : x[2].y, j < 4 ? x[3].x : x[3].y, sel);
+                                const uint32_t b0 = hsub2_bits(__byte_perm(t01, 0x64646464u, 0x4140), 0x64806480u);
+                                const uint32_t b1 = hsub2_bits(__byte_perm(t23, 0x64646464u, 0x4140), 0x64806480u);
+                                if constexpr (TERMS == 2) {
+                                    mma16816<BF>(fresh[j], p[k], b0, b1);
+                                    mma16816<BF>(fresh[j], p2[k], b0, b1);
+                                } else {
+                                    mma16816<BF>(o[ch * 8 + j], p[k], b0, b1);
+                                }
+                            }
+                        }
+                        if constexpr (TERMS == 2) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[ch * 8 + j][i] += fresh[j][i];
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {       // 16 dims
+                            float fresh[TERMS == 2 ? 2 : 1][4] = {};
+#pragma unroll
+                            for (int k = 0; k < NT / 2; ++k) {
+                                const int row = tok + 16 * k + (lane & 15);
+                                uint32_t b[4];
+                                ldsm4_t(vb + row * RB + (((2 * j + (lane >> 4)) ^ (row & 7)) << 4), b);
+                                if constexpr (TERMS == 2) {
+                                    mma16816<BF>(fresh[0], p[k], b[0], b[1]);
+                                    mma16816<BF>(fresh[1], p[k], b[2], b[3]);
+                                    mma16816<BF>(fresh[0], p2[k], b[0], b[1]);
+                                    mma16816<BF>(fresh[1], p2[k], b[2], b[3]);
+                                } else {
+                                    mma16816<BF>(o[ch * 8 + 2 * j], p[k], b[0], b[1]);
+                                    mma16816<BF>(o[ch * 8 + 2 * j + 1], p[k], b[2], b[3]);
+                                }
+                            }
+                            if constexpr (TERMS == 2) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    o[ch * 8 + 2 * j][i] += fresh[0][i];
+                                    o[ch * 8 + 2 * j + 1][i] += fresh[1][i];
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[stage]);
+            if (++stage == a.stages) stage = 0, phase ^= 1u;
+        }
+        // ------------------------------------------------- the item's end
+        l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 1), l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 1);
+        l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 2), l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 2);
+        // the warps of a row slice come to one maximum, then add up two by two
+        float f0 = KIND == kI8 ? pow2(E0) : 1.0f, f1 = KIND == kI8 ? pow2(E1) : 1.0f;
+        if constexpr (WN > 1) {
+            if (c == 0) {
+                red_ml[warp * 16 + g] = make_float2(m0, l0);
+                red_ml[warp * 16 + g + 8] = make_float2(m1, l1);
+            }
+            compute_barrier();
+            float n0 = neg_inf(), n1 = neg_inf();
+#pragma unroll
+            for (int i = 0; i < WN; ++i) {
+                n0 = fmaxf(n0, red_ml[(wm * WN + i) * 16 + g].x);
+                n1 = fmaxf(n1, red_ml[(wm * WN + i) * 16 + g + 8].x);
+            }
+            l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WN; ++i) {
+                const float2 y0 = red_ml[(wm * WN + i) * 16 + g], y1 = red_ml[(wm * WN + i) * 16 + g + 8];
+                l0 += y0.y * (y0.x == neg_inf() ? 1.0f : exp2_fast(y0.x - n0));
+                l1 += y1.y * (y1.x == neg_inf() ? 1.0f : exp2_fast(y1.x - n1));
+            }
+            f0 *= m0 == neg_inf() ? 1.0f : exp2_fast(m0 - n0);
+            f1 *= m1 == neg_inf() ? 1.0f : exp2_fast(m1 - n1);
+            m0 = n0, m1 = n1;
+        }
+#pragma unroll
+        for (int j = 0; j < OT; ++j) o[j][0] *= f0, o[j][1] *= f0, o[j][2] *= f1, o[j][3] *= f1;
+        if constexpr (WN > 1) {
+            // every warp's sums to the first of its row slice, which adds them in order
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                constexpr int kHalf = OT / 2;
+                float *buf = red + wm * (WN - 1) * (16 * DP / 2);
+                if (wn > 0) {
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j) {
+                        const float(&x)[4] = o[part * kHalf + j];
+                        *reinterpret_cast<float4 *>(buf + (wn - 1) * (16 * DP / 2) + (j * 32 + lane) * 4) = make_float4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+                compute_barrier();
+                if (wn == 0) {
+#pragma unroll
+                    for (int i = 0; i < WN - 1; ++i)
+#pragma unroll
+                        for (int j = 0; j < kHalf; ++j) {
+                            const float4 x = *reinterpret_cast<const float4 *>(buf + i * (16 * DP / 2) + (j * 32 + lane) * 4);
+                            float(&y)[4] = o[part * kHalf + j];
+                            y[0] += x.x, y[1] += x.y, y[2] += x.z, y[3] += x.w;
+                        }
+                }
+                if (part == 0) compute_barrier();
+            }
+        }
+        if (wn == 0) {
+            const bool whole = w.whole();
+            const int slot = 2 * static_cast<int>(blockIdx.x) + (w.from == 0 ? 1 : 0);
+            float *part = a.parts + slot * attn_part_floats(S::kBlock, chunks);
+            const int width = kChunk * chunks;
+#pragma unroll
+            for (int up = 0; up < 2; ++up) {
+                const int r = wm * 16 + g + 8 * up, row = w.b * S::kBlock + r;
+                if (row >= w.q.rows) continue;
+                const float l = up ? l1 : l0;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const int i = row / a.group, head = w.h * a.group + row - i * a.group;
+                const int64_t out = (static_cast<int64_t>(w.q.start) + i) * a.ldo + static_cast<int64_t>(head) * a.c.d;
+#pragma unroll
+                for (int j = 0; j < OT; ++j) {
+                    if (j / 8 >= chunks) continue;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        // column 2 c + x of tile j
+                        const int dim = KIND == kI8 ? (j / 8) * kChunk + 8 * (2 * c + x) + j % 8 : 8 * j + 2 * c + x;
+                        const float v = o[j][2 * up + x];
+                        if (!whole) part[r * width + dim] = v;
+                        else if (dim < a.c.d) {
+                            if (a.type == Q4_TYPE_F32) static_cast<float *>(a.O)[out + dim] = v * inv;
+                            else if (a.type == Q4_TYPE_F16) static_cast<__half *>(a.O)[out + dim] = __float2half_rn(v * inv);
+                            else static_cast<__nv_bfloat16 *>(a.O)[out + dim] = __float2bfloat16_rn(v * inv);
+                        }
+                    }
+                }
+                if (!whole && c == 0) {
+                    part[S::kBlock * width + r] = up ? m1 : m0;
+                    part[S::kBlock * width + S::kBlock + r] = l;
+                }
+            }
+            if (!whole && w.from == 0 && lane == 0 && wm == 0) a.meta[blockIdx.x] = make_int4(w.s, w.h, w.b, w.parts());
+        }
+    }
+}
+
+template <int KIND, int TERMS, int WM, int DP> cudaError_t launch_shape(AttnArgs a, int sm_count, cudaStream_t s, int *ctas)
+{
+    using S = WarpShape<KIND, TERMS, WM, DP>;
+    const int stage = warp_stage_bytes(a.c.chunks, a.c.type);
+    // two CTAs an SM where two rings fit: their waits cover each other
+    const int fixed = S::kFixed;
+    const int two = static_cast<int>(kSmemPerSM / 2) - 1024 - fixed, one = static_cast<int>(kSmemOptIn) - fixed;
+    const int per_sm = DP <= 128 && two / stage >= 2 ? 2 : 1;
+    a.stages = std::min(8, (per_sm == 2 ? two : one) / stage);
+    // the walk's scan lies in the ring at first
+    const size_t smem = fixed + std::max<size_t>(static_cast<size_t>(a.stages) * stage, 8 * (kMaxSeqs + 1));
+    const void *f = reinterpret_cast<const void *>(&attn_warp_kernel<KIND, TERMS, WM, DP>);
+    cudaError_t e = set_max_smem(f, kSmemOptIn);
+    if (e != cudaSuccess) return e;
+    *ctas = std::min(kAttnMaxCtas, per_sm * sm_count);
+    void *args[] = {&a};
+    return launch_pdl(f, dim3(static_cast<unsigned>(*ctas)), dim3(kAttnThreads), smem, s, args);
+}
+template <int KIND, int TERMS> cudaError_t launch_kind(const AttnArgs &a, int sm_count, cudaStream_t s, int *ctas)
+{
+    const int dp = a.c.chunks <= 2 ? a.c.chunks * kChunk : 256;
+#define Q4_SHAPE(wm) (dp == 64 ? launch_shape<KIND, TERMS, wm, 64>(a, sm_count, s, ctas) \
+                      : dp == 128 ? launch_shape<KIND, TERMS, wm, 128>(a, sm_count, s, ctas) : launch_shape<KIND, TERMS, wm, 256>(a, sm_count, s, ctas))
+    return a.block == 16 ? Q4_SHAPE(1) : a.block == 32 ? Q4_SHAPE(2) : Q4_SHAPE(4);
+#undef Q4_SHAPE
+}
+
+} // namespace
+} // namespace q4
