@@ -25,7 +25,7 @@ HEADER = os.path.join(ROOT, "include", "q4mm.h")
 
 SOURCES = ["q4mm_api.cu", "q4mm_pack.cu", "q4mm_decode.cu", "q4mm_gemv.cu", "q4mm_mmv.cu", "q4mm_matvec.cu", "q4mm_w8.cu", "q4mm_prefill.cu",
            "q4mm_static.cu", "q4mm_gguf.cu", "q4mm_experts.cu", "q4mm_norm.cu", "q4mm_norm_stream.cu", "q4mm_norm_stream_any.cu", "q4mm_moe.cu", "q4mm_w8a8.cu", "q4mm_w8a8_gemm.cu",
-           "q4mm_block_api.cu", "q4mm_kv.cu", "q4mm_attn.cu", "q4mm_attn_f16.cu", "q4mm_attn_f16x2.cu", "q4mm_attn_bf16.cu", "q4mm_attn_i8.cu",
+           "q4mm_block_api.cu", "q4mm_kv.cu", "q4mm_attn.cu", "q4mm_attn_tensor.cu", "q4mm_attn_f16.cu", "q4mm_attn_f16x2.cu", "q4mm_attn_bf16.cu", "q4mm_attn_i8.cu",
            "q4mm_attn_i8x2.cu", "q4mm_draft.cu", "q4mm_cache_api.cu"]
 DEPS = ["q4mm_device.cuh", "q4mm_internal.h", "q4mm_rows.cuh", "q4mm_rows.h", "q4mm_norm.h", "q4mm_norm.cuh", "q4mm_norm_stream.cuh", "q4mm_moe.h",
         "q4mm_w8a8.h", "q4mm_cache.h", "q4mm_attn.cuh", "q4mm_attn_warp.cuh"]

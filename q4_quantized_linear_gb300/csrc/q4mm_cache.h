@@ -96,6 +96,7 @@ __host__ __device__ inline int64_t attn_part_floats(int block, int chunks)
     return static_cast<int64_t>(block) * (kChunk * chunks + 2);
 }
 cudaError_t launch_attn_warp(AttnArgs a, int sm_count, cudaStream_t s);
+cudaError_t launch_attn_tensor(AttnArgs a, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnArgs &a, int ctas, cudaStream_t s);
 
 struct ProbsArgs {

@@ -101,6 +101,10 @@ int kv_rows(bool write, const void *K, int64_t ldk, const void *V, int64_t ldv, 
     });
 }
 
+// Whether the tcgen05 kernel has a part in a call with up to so many query rows of
+// a sequence and head: its tensor memory holds the sums of heads of up to 128 dims.
+bool tensor_takes(int64_t rows, int chunks) { return rows > kWarpRows && chunks <= 2; }
+
 int block_of(int64_t rows)
 {
     return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
@@ -142,8 +146,10 @@ Q4MM_API size_t q4_attention_workspace_size(int64_t rows, int64_t n_seq, int64_t
         !valid_batch(n_seq, rows, heads) || rows == 0 || n_seq == 0)
         return 0;
     const int64_t group = heads / kv_heads;
-    const int block = block_of(rows * group);
-    return kMetaBytes + sizeof(float) * 2 * kAttnMaxCtas * static_cast<size_t>(attn_part_floats(block, static_cast<int>(ceil_div(d, kChunk))));
+    const int chunks = static_cast<int>(ceil_div(d, kChunk));
+    int64_t parts = 2 * kAttnMaxCtas * attn_part_floats(block_of(rows * group), chunks);
+    if (tensor_takes(rows * group, chunks)) parts = std::max(parts, kAttnMaxCtas * attn_part_floats(kTensorRows, chunks));
+    return kMetaBytes + sizeof(float) * static_cast<size_t>(parts);
 }
 
 Q4MM_API int q4_attention(void *O, int64_t ldo, const void *Q, int64_t ldq, int type, int64_t heads, float scale,
@@ -186,7 +192,18 @@ Q4MM_API int q4_attention(void *O, int64_t ldo, const void *Q, int64_t ldq, int 
     const int64_t most = (max_new > 0 ? std::min(max_new, rows) : rows) * a.group;   // query rows of a sequence and head
     a.rows_above = 0, a.rows_upto = 0x7FFFFFFF;
     a.block = block_of(most);
-    return guarded([&] { return cuda_status(launch_attn_warp(a, dev.sm_count, as_stream(stream))); });
+    cudaStream_t s = as_stream(stream);
+    return guarded([&] {
+        if (type != Q4_TYPE_F32 && tensor_takes(most, a.c.chunks)) {
+            // sequences with many new tokens; one sequence alone is taken whatever it has
+            AttnArgs many = a;
+            many.rows_above = n_seq == 1 ? 0 : kWarpRows;
+            const cudaError_t e = launch_attn_tensor(many, dev.sm_count, s);
+            if (e != cudaSuccess || n_seq == 1) return cuda_status(e);
+            a.rows_upto = kWarpRows;
+        }
+        return cuda_status(launch_attn_warp(a, dev.sm_count, s));
+    });
 }
 
 Q4MM_API int q4_token_probs(float *P, int64_t ldp, const void *logits, int64_t ldl, int type, const float *temperature,
