@@ -15,10 +15,35 @@ namespace {
 
 constexpr int kJoinThreads = 256;
 
+// Four dims of a row out.
+__device__ __forceinline__ void store4(const AttnArgs &a, int64_t out, int dim, const float (&v)[4])
+{
+    if (dim >= a.c.d) return;                               // (d is a multiple of 8)
+    if (a.type == Q4_TYPE_F32) {
+        float *o = static_cast<float *>(a.O) + out + dim;
+        if (a.vec) *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = v[e];
+        return;
+    }
+    uint16_t *o = static_cast<uint16_t *>(a.O) + out + dim;
+    const bool bf = a.type == Q4_TYPE_BF16;
+    const uint2 u = make_uint2(bf ? pack_bf16x2_rn(v[0], v[1]) : pack_f16x2_rn(v[0], v[1]), bf ? pack_bf16x2_rn(v[2], v[3]) : pack_f16x2_rn(v[2], v[3]));
+    if (a.vec) {
+        *reinterpret_cast<uint2 *>(o) = u;
+    } else {
+        o[0] = static_cast<uint16_t>(u.x), o[1] = static_cast<uint16_t>(u.x >> 16);
+        o[2] = static_cast<uint16_t>(u.y), o[3] = static_cast<uint16_t>(u.y >> 16);
+    }
+}
+
 // o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over an item's parts i, the
-// CTAs' that follow the one it starts in. A CTA takes a row at a time: the
-// weights first, then W / 4 threads a part, four dims each; the groups of
-// threads take every n-th part, and their sums are added in order.
+// CTAs' that follow the one it starts in. Up to 32 parts (blocks of many rows): a
+// warp takes a row, a lane a part's weight and then four dims of all parts in
+// order. More parts (few rows of a long sequence): a CTA takes a row, W / 4 threads
+// a part; the groups of threads take every n-th part, and their sums are added in
+// order.
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a)
 {
     __shared__ float weight[kAttnMaxCtas + 1];
@@ -35,6 +60,45 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     const int64_t size = attn_part_floats(a.block, a.c.chunks);
     const int rows = min(a.block, q.rows - item.z * a.block);
     const auto part_at = [&](int i) { return a.parts + (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0)) * size; };
+    const auto out_at = [&](int r) {
+        const int row = item.z * a.block + r, i = row / a.group, head = item.y * a.group + row - i * a.group;
+        return (static_cast<int64_t>(q.start) + i) * a.ldo + static_cast<int64_t>(head) * a.c.d;
+    };
+    if (parts <= 32) {
+        const int lane = tid % 32;
+        for (int r = blockIdx.y * (kJoinThreads / 32) + tid / 32; r < rows; r += gridDim.y * (kJoinThreads / 32)) {
+            float mi = neg_inf(), l = 0.0f;
+            if (lane < parts) {
+                const float *p = part_at(lane);
+                mi = p[a.block * W + r], l = p[a.block * W + a.block + r];
+            }
+            float m = mi;
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const float w = mi == neg_inf() ? 1.0f : exp2_fast(mi - m);   // (then its sums are zeros or NaN)
+            l *= w;
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const int64_t out = out_at(r);
+            for (int c = 0; c < W; c += 128) {
+                const int dim = c + 4 * lane;
+                float v[4] = {};
+#pragma unroll 4
+                for (int i = 0; i < parts; ++i) {
+                    const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
+                    if (dim < W) {
+                        const float4 u = *reinterpret_cast<const float4 *>(part_at(i) + r * W + dim);
+                        v[0] += wi * u.x, v[1] += wi * u.y, v[2] += wi * u.z, v[3] += wi * u.w;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] *= inv;
+                store4(a, out, dim, v);
+            }
+        }
+        return;
+    }
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
         float m = neg_inf();
         for (int i = tid; i < parts; i += kJoinThreads) m = fmaxf(m, part_at(i)[a.block * W + r]);
@@ -79,17 +143,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
                 s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
             }
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            const int row = item.z * a.block + r, i = row / a.group, head = item.y * a.group + row - i * a.group;
-            const int64_t out = (static_cast<int64_t>(q.start) + i) * a.ldo + static_cast<int64_t>(head) * a.c.d;
             const float v[4] = {s.x * inv, s.y * inv, s.z * inv, s.w * inv};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int dim = 4 * x + e;
-                if (dim >= a.c.d) continue;
-                if (a.type == Q4_TYPE_F32) static_cast<float *>(a.O)[out + dim] = v[e];
-                else if (a.type == Q4_TYPE_F16) static_cast<__half *>(a.O)[out + dim] = __float2half_rn(v[e]);
-                else static_cast<__nv_bfloat16 *>(a.O)[out + dim] = __float2bfloat16_rn(v[e]);
-            }
+            store4(a, out_at(r), 4 * x, v);
         }
     }
 }
@@ -100,7 +155,7 @@ cudaError_t launch_attn_join(const AttnArgs &args, int ctas, cudaStream_t s)
 {
     AttnArgs a = args;
     void *p[] = {&a};
-    const unsigned rows = static_cast<unsigned>(a.block <= 64 ? a.block / 4 : 32);
+    const unsigned rows = static_cast<unsigned>(a.block <= 64 ? a.block / 4 : 16);
     return launch_pdl(reinterpret_cast<const void *>(&attn_join_kernel), dim3(static_cast<unsigned>(ctas), rows), dim3(kJoinThreads), 0, s, p);
 }
 

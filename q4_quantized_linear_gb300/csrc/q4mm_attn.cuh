@@ -68,15 +68,22 @@ struct Walk {
     // `scan`: shared memory of n_seq + 1 numbers, free again after the next barrier.
     __device__ __forceinline__ void begin(const AttnArgs &a, long long *scan)
     {
-        for (int i = threadIdx.x; i < a.n_seq; i += blockDim.x) {
-            const Seq x = seq_at(a, i);
+        // few sequences: a warp's lanes share the blocks of one; many: a thread each
+        // (a prompt of 2000 tokens in four, a thread each: 10 us)
+        const int lanes = a.n_seq * 32 <= static_cast<int>(blockDim.x) ? 32 : a.n_seq * 8 <= static_cast<int>(blockDim.x) ? 8 : 1;
+        for (int i0 = 0; i0 < a.n_seq; i0 += blockDim.x / lanes) {
+            const int i = i0 + threadIdx.x / lanes;
             long long w = 0;
-            for (int j = 0; j < x.blocks; ++j) {
-                int f, n, e;
-                block_tiles(a, x, j, f, n, e);
-                w += n;
+            if (i < a.n_seq) {
+                const Seq x = seq_at(a, i);
+                for (int j = threadIdx.x % lanes; j < x.blocks; j += lanes) {
+                    int f, n, e;
+                    block_tiles(a, x, j, f, n, e);
+                    w += n;
+                }
             }
-            scan[i] = w;
+            for (int o = lanes / 2; o > 0; o /= 2) w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
+            if (i < a.n_seq && threadIdx.x % lanes == 0) scan[i] = w;
         }
         __syncthreads();
         if (threadIdx.x < 32) {
@@ -115,11 +122,28 @@ struct Walk {
         const long long per = (scan[s + 1] - scan[s]) / a.c.heads, x = at - scan[s];
         h = static_cast<int>(x / per);
         long long y = x - h * per;
-        for (b = 0;; ++b) {
-            block_tiles(a, q, b, first, count, hi);
-            if (y < count || b + 1 >= q.blocks) break;
-            y -= count;
+        // the block that tile y is in: a warp looks at 32 at a time
+        const int lane = threadIdx.x & 31;
+        for (b = 0; b + 1 < q.blocks; b += 32) {
+            long long upto_b = 0;
+            if (b + lane < q.blocks) {
+                block_tiles(a, q, b + lane, first, count, hi);
+                upto_b = count;
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const long long u = __shfl_up_sync(0xFFFFFFFFu, upto_b, o);
+                if (lane >= o) upto_b += u;
+            }
+            const unsigned past = __ballot_sync(0xFFFFFFFFu, upto_b > y);
+            const int skip = past ? __ffs(past) - 1 : 32;
+            if (skip > 0) y -= __shfl_sync(0xFFFFFFFFu, upto_b, skip - 1);
+            if (past) {
+                b += skip;
+                break;
+            }
         }
+        block_tiles(a, q, b, first, count, hi);
         from = static_cast<int>(y);
         clip();
     }
@@ -152,6 +176,16 @@ struct Walk {
         return 1 + static_cast<int>((rest + share - 1) / share);
     }
 };
+
+// Page i of a sequence that needs `pages` (0 past them). One that the cache does not
+// have is recorded, and one that it has is read in its place.
+__device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *table, int i, int pages)
+{
+    const int page = i < pages ? table[i] : 0;
+    if (page >= 0 && page < a.c.n_pages) return page;
+    record_status(a.status, kErrCheck);
+    return min(max(page, 0), a.c.n_pages - 1);
+}
 
 // ----------------------------------------------------------- arithmetic --
 

@@ -12,14 +12,15 @@
 // of them. The maximum m is raised, and O scaled, only where a row's scores pass it
 // by 2^8; the softmax threads scale O themselves (S of a tile is committed after
 // the products of the tile before, so O rests).
-//   Warps: 0-3 and 4-7 the halves' softmax (a row a thread: no shuffles), 8 copies,
-// 9 issues the products, 12-15 (codes only) turn codes into fp16 tiles: the scales
-// of keys multiply scores, those of values terms, as in the warp-MMA kernel.
+//   Warps: 0-3 and 4-7 the halves' softmax (a row a thread: no shuffles), the first
+// of each issuing its products; 8 copies, or 8-11 turn codes into fp16 tiles: the
+// scales of keys multiply scores, those of values terms, as in the warp-MMA kernel.
 //   K and V lie in the pages as the tensor cores read them, 64 dims a row of 128
 // bytes, swizzled: K as a K-major operand, V (dims contiguous) as an N-major one.
 //   A page's rows past the sequence's end are never copied: what their place holds
 // is zeros or an earlier tile's values, finite as all values of the cache.
 #include <algorithm>
+#include <type_traits>
 
 #include "q4mm_attn.cuh"
 
@@ -27,28 +28,24 @@ namespace q4 {
 namespace {
 
 constexpr int kHalf = 128, kTile = kTensorTile;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kConvertWarp0 = 12;
+constexpr int kFeedWarp0 = 8;                           // the copies' warp, or the first of four that convert codes
 constexpr uint32_t kAtomRows = kTile * 128;              // bytes of 64 dims of a tile
 
 template <int KIND, int DP> struct TensorShape {
     static constexpr bool kCodes = KIND == 2;
     static constexpr int kChunks = DP / kChunk;
-    static constexpr int kThreads = kCodes ? 512 : 384;
+    static constexpr int kThreads = kCodes ? 384 : 288;
     static constexpr int kTileBytes = kChunks * static_cast<int>(kAtomRows);
-    // 16-bit: rings of K and of V tiles. Codes: one ring of fp16 tiles, K and V in
-    // turn, and one of copied codes with their scales.
-    static constexpr int kK = kCodes ? 3 : DP == 128 ? 2 : 4, kV = kCodes ? 0 : DP == 128 ? 3 : 4;
-    static constexpr int kRaw = kCodes ? 3 : 0, kRawBytes = kTileBytes / 2 + kTile * 4;
-    // registers of a thread: launched with 168 (codes: 128)
-    static constexpr int kSoftmaxRegs = kCodes ? 168 : 208, kOtherRegs = kCodes ? 64 : 80, kConvertRegs = 96;
+    // 16-bit: rings of K and of V tiles. Codes: one ring of fp16 tiles, K and V in turn.
+    static constexpr int kK = 4 - (kCodes || DP == 64 ? 0 : 2), kV = kCodes ? 0 : DP == 128 ? 3 : 4;
     static constexpr int kScaleSlots = 4;                // tiles whose scales are held
-    static constexpr size_t kSmem = 2 * kHalf * DP * 2 + static_cast<size_t>(kK + kV) * kTileBytes + kRaw * kRawBytes +
+    static constexpr size_t kSmem = 2 * kHalf * DP * 2 + static_cast<size_t>(kK + kV) * kTileBytes +
                                     (kCodes ? kScaleSlots * (2 * kTile + 4) * 4 : 0) + 2 * kHalf * 4 + 512 + 1024;
 };
 
 struct Bars {
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], raw_full[4], raw_empty[4], scales_full[4], scales_empty[4];
-    uint64_t q_full[2], s_full[2], p_full[2], done;
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], scales_full[4], scales_empty[4];
+    uint64_t q_full[2], s_full[2], p_full[2], done[2];
     uint32_t tmem;
     int abort;
 };
@@ -94,8 +91,6 @@ __device__ __forceinline__ uint64_t desc_n_major(uint32_t saddr, uint32_t lead)
 }
 constexpr uint32_t kNMajorB = 1u << 16;
 
-template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ F2 f2_add(F2 a, F2 b)
 {
     F2 r;
@@ -114,8 +109,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     uint8_t *const qs = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));                                          // [half][chunk][128 rows][128 bytes]
     uint8_t *const ks = qs + 2 * kHalf * DP * 2;
     uint8_t *const vs = ks + S::kK * S::kTileBytes;
-    uint8_t *const raw = vs + S::kV * S::kTileBytes;
-    float *const scales = reinterpret_cast<float *>(raw + S::kRaw * S::kRawBytes);   // [slot][keys, values][tile], then [slot][4]: the largest
+    float *const scales = reinterpret_cast<float *>(vs + S::kV * S::kTileBytes);   // [slot][keys, values][tile], then [slot][4]: the largest
     float *const row_factor = scales + (CODES ? S::kScaleSlots * (2 * kTile + 4) : 0);
     Bars *const bars = reinterpret_cast<Bars *>(row_factor + 2 * kHalf);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -123,20 +117,17 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars->k_full[i], CODES ? 4 : 1);
-            mbar_init(&bars->k_empty[i], 1);
+            mbar_init(&bars->k_empty[i], 2);                           // both halves
             mbar_init(&bars->v_full[i], 1);
-            mbar_init(&bars->v_empty[i], 1);
-            mbar_init(&bars->raw_full[i], 1);
-            mbar_init(&bars->raw_empty[i], 4);
+            mbar_init(&bars->v_empty[i], 2);
             mbar_init(&bars->scales_full[i], 4);
             mbar_init(&bars->scales_empty[i], 8);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&bars->q_full[i], 4), mbar_init(&bars->s_full[i], 1), mbar_init(&bars->p_full[i], 4);
-        mbar_init(&bars->done, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bars->q_full[i], 4), mbar_init(&bars->s_full[i], 1), mbar_init(&bars->p_full[i], 4), mbar_init(&bars->done[i], 1);
         bars->abort = 0;
         fence_barrier_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == 0) {
         tmem_alloc(&bars->tmem, 512u);
         tmem_relinquish();
     }
@@ -161,20 +152,74 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
 
     if (warp < 8) {
         // ---------------------------------------------------------- softmax
-        reg_inc<S::kSoftmaxRegs>();
         const int half = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + 128u * half, o_at = tmem + lanes + 256u + 128u * half;
-        uint32_t s_phase = 0;
+        uint32_t q_phase = 0, s_phase = 0, p_phase = 0;
         Turn sc;                                                       // the tile's scales
         bool ok = true;
+        // The half's first warp issues its products: the scores of a tile as soon as the
+        // terms of the one before are taken.
+        constexpr uint32_t type = BF ? idesc_bf16_f32(0, 0) : idesc_f16_f32(0, 0);
+        constexpr uint32_t id_s = type | idesc_f16_f32(kHalf, kTile), id_o = type | idesc_f16_f32(kHalf, DP) | kNMajorB;
+        uint64_t *const v_full = CODES ? bars->k_full : bars->v_full, *const v_empty = CODES ? bars->k_empty : bars->v_empty;
+        Turn kt, vt;                                                   // K and V tiles in turn
+        if (CODES) vt.step(S::kK);                                     // ... of one ring
+        const auto next_k = [&] { kt.step(S::kK); if (CODES) kt.step(S::kK); };
+        const auto next_v = [&] { vt.step(CODES ? S::kK : S::kV); if (CODES) vt.step(S::kK); };
+        const auto scores = [&] {
+            const uint32_t d = __shfl_sync(0xFFFFFFFFu, tmem, 0) + 128u * half;
+            const uint64_t kd = smem_desc_sw128(smem_u32(ks)) + static_cast<uint64_t>(kt.slot * (S::kTileBytes >> 4));
+            const uint64_t qd = smem_desc_sw128(smem_u32(qs)) + static_cast<uint64_t>(half * CH * (kAtomRows >> 4));
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tc_mma_f16(d, qd + c * (kAtomRows >> 4) + 2 * i, kd + c * (kAtomRows >> 4) + 2 * i, id_s, c + i > 0 ? 1u : 0u);
+                tc_commit(&bars->s_full[half]);
+                tc_commit(&bars->k_empty[kt.slot]);
+            }
+            __syncwarp();
+            next_k();
+        };
+        const auto sums = [&](bool add, bool last) {
+            const uint32_t d = __shfl_sync(0xFFFFFFFFu, tmem, 0) + 128u * half;
+            const uint64_t vd = desc_n_major(smem_u32(CODES ? ks : vs), kAtomRows) + static_cast<uint64_t>(vt.slot * (S::kTileBytes >> 4));
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < kTile / 16; ++i) tc_mma_f16_ts(d + 256u, d + 8u * i, vd + i * (2048 >> 4), id_o, add || i > 0 ? 1u : 0u);
+                if (last) tc_commit(&bars->s_full[half]);
+                tc_commit(&v_empty[vt.slot]);
+            }
+            __syncwarp();
+            next_v();
+        };
+        const bool issues = (warp & 3) == 0;
         for (; ok && w.valid(); w.next(a)) {
             if (half && !both()) {
-                // (the first half gives the tiles' scales back for both)
-                for (int t = w.from; CODES && t < w.upto; ++t) sc.step(S::kScaleSlots);
+                // the half is not there: it gives its tiles back as they come, so that no
+                // ring runs ahead of it
+                for (int t = w.from; ok && t < w.upto; ++t) {
+                    if constexpr (CODES) {
+                        ok = warp_wait(&bars->scales_full[sc.slot], sc.phase, a.wait_ns);
+                        if (ok && lane == 0) mbar_arrive(&bars->scales_empty[sc.slot]);
+                        sc.step(S::kScaleSlots);
+                    }
+                    if (issues) {
+                        ok = ok && warp_wait(&bars->k_full[kt.slot], kt.phase, a.wait_ns);
+                        if (ok && lane == 0) mbar_arrive(&bars->k_empty[kt.slot]);
+                        ok = ok && warp_wait(&v_full[vt.slot], vt.phase, a.wait_ns);
+                        if (ok && lane == 0) mbar_arrive(&v_empty[vt.slot]);
+                        next_k();
+                        next_v();
+                    }
+                }
+                if (!ok) fail();
                 continue;
             }
-            const bool two = both();
             const int first_row = w.b * kTensorRows + half * kHalf + (warp & 3) * 32;
             // the warp's 32 rows of Q, two or four at a time, into the operand's image
             constexpr int kLanes = DP / 8, kRows = 32 / kLanes;
@@ -216,6 +261,15 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->q_full[half]);
+            if (issues) {
+                if (!warp_wait(&bars->q_full[half], q_phase, a.wait_ns) || !warp_wait(&bars->k_full[kt.slot], kt.phase, a.wait_ns)) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                scores();
+            }
+            q_phase ^= 1u;
             const int my_row = first_row + lane;
             const float rf = CODES ? row_factor[half * kHalf + (warp & 3) * 32 + lane] : a.scale_log2;
             int lo, hi, full_from, full_upto, x;
@@ -236,98 +290,131 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 }
                 s_phase ^= 1u;
                 tc_fence_after();
-                uint32_t r[kTile];
-#pragma unroll
-                for (int i = 0; i < kTile; i += 32) tmem_ld_32x32b_x32(s_at + i, r + i);
-                tmem_wait_ld();
                 const float *sk = scales + sc.slot * (2 * kTile), *sv = sk + kTile;
-                if constexpr (CODES) {
-#pragma unroll
-                    for (int i = 0; i < kTile; i += 4) {
-                        const float4 k4 = *reinterpret_cast<const float4 *>(sk + i);
-                        f2_split(f2_mul(f2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2(k4.x, k4.y)),
-                                 reinterpret_cast<float &>(r[i]), reinterpret_cast<float &>(r[i + 1]));
-                        f2_split(f2_mul(f2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), f2(k4.z, k4.w)),
-                                 reinterpret_cast<float &>(r[i + 2]), reinterpret_cast<float &>(r[i + 3]));
-                    }
-                }
                 float vmax = 0.0f;
-                if (t0 + kTile > full_upto || t0 < full_from) {
-#pragma unroll
-                    for (int i = 0; i < kTile; ++i) {
-                        const bool sees = t0 + i >= lo && t0 + i < hi;
-                        if (!sees) r[i] = 0xFF800000u;
-                        if (CODES && sees) vmax = fmaxf(vmax, sv[i]);
-                    }
-                } else if constexpr (CODES) {
+                if constexpr (CODES) {
                     const float4 x4 = *reinterpret_cast<const float4 *>(scales + S::kScaleSlots * 2 * kTile + sc.slot * 4);
                     vmax = fmaxf(fmaxf(x4.x, x4.y), fmaxf(x4.z, x4.w));
                 }
-                float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll
-                for (int i = 0; i < kTile; i += 8)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], fmaxf(__uint_as_float(r[i + 2 * j]), __uint_as_float(r[i + 2 * j + 1])));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rf;
-                const bool wide = CODES && vmax >= pow2(E);
-                if (__any_sync(0xFFFFFFFFu, top > m + kSlack || wide)) {
-                    const float n = fmaxf(m, top);
-                    float scale = m == neg_inf() ? 0.0f : exp2_fast(m - n);
-                    m = n;
-                    l *= scale;
-                    if (wide) {
-                        const int to = min(((__float_as_int(vmax) >> 23) & 255) - 126, 126);
-                        scale *= to - E > 126 ? 0.0f : pow2(E - to);
-                        E = to;
-                    }
-                    if (t > w.from) {
-#pragma unroll
-                        for (int i = 0; i < DP; i += 16) {
-                            uint32_t o[16];
-                            tmem_ld_32x32b_x16(o_at + i, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale);
-                            tmem_st_32x32b_x16(o_at + i, o);
-                        }
-                    }
-                }
-                const float u = m == neg_inf() ? 0.0f : m - kLift;
-                const F2 rf2 = f2(rf, rf), u2 = f2(-u, -u);
-                const float down = CODES ? pow2(-E) : 1.0f;
-                F2 sum = f2(0.0f, 0.0f), sum2 = sum;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int j = h * 32 + 2 * i;
-                        float e0, e1;
-                        f2_split(f2_fma(f2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), rf2, u2), e0, e1);
-                        e0 = exp2_fast(e0), e1 = exp2_fast(e1);
-                        if (i & 1) sum2 = f2_add(sum2, f2(e0, e1));
-                        else sum = f2_add(sum, f2(e0, e1));
+                const auto tile = [&](auto masked) {
+                    constexpr bool MASK = decltype(masked)::value;
+                    // scores 32 columns at a time, times their keys' scales
+                    const auto scored = [&](int i0, uint32_t (&r)[32]) {
                         if constexpr (CODES) {
-                            // (below 1 where the row sees the token; finite times 0 where not)
-                            const float2 v2 = *reinterpret_cast<const float2 *>(sv + j);
-                            e0 *= fminf(v2.x * down, 1.0f), e1 *= fminf(v2.y * down, 1.0f);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 k4 = *reinterpret_cast<const float4 *>(sk + i0 + i);
+                                float y[4];
+                                f2_split(f2_mul(f2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2(k4.x, k4.y)), y[0], y[1]);
+                                f2_split(f2_mul(f2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), f2(k4.z, k4.w)), y[2], y[3]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) r[i + j] = __float_as_uint(y[j]);
+                            }
                         }
-                        p[i] = BF ? pack_bf16x2_rn(e0, e1) : pack_f16x2_rn(e0, e1);
+                        if constexpr (MASK) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (t0 + i0 + i < lo || t0 + i0 + i >= hi) r[i] = 0xFF800000u;
+                        }
+                    };
+                    if constexpr (MASK && CODES) {
+                        vmax = 0.0f;
+                        for (int i = max(lo - t0, 0); i < min(hi - t0, kTile); ++i) vmax = fmaxf(vmax, sv[i]);
                     }
-                    tmem_st_32x32b_x16(s_at + 16 * h, p);
-                }
-                l += f2_sum(f2_add(sum, sum2));
+                    float mx[2] = {neg_inf(), neg_inf()};
+                    uint32_t r[2][32];
+                    tmem_ld_32x32b_x32(s_at, r[0]);
+#pragma unroll
+                    for (int c = 0; c < kTile / 32; ++c) {
+                        tmem_wait_ld();
+                        // the next columns, and after the last ones the first again for the terms
+                        tmem_ld_32x32b_x32(s_at + (c + 1) % (kTile / 32) * 32, r[(c + 1) & 1]);
+                        scored(32 * c, r[c & 1]);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            mx[0] = fmaxf(mx[0], fmaxf(__uint_as_float(r[c & 1][i]), __uint_as_float(r[c & 1][i + 1])));
+                            mx[1] = fmaxf(mx[1], fmaxf(__uint_as_float(r[c & 1][i + 2]), __uint_as_float(r[c & 1][i + 3])));
+                        }
+                    }
+                    const float top = fmaxf(mx[0], mx[1]) * rf;
+                    const bool wide = CODES && vmax >= pow2(E);
+                    tmem_wait_ld();
+                    if (__any_sync(0xFFFFFFFFu, top > m + kSlack || wide)) {
+                        const float n = fmaxf(m, top);
+                        float scale = m == neg_inf() ? 0.0f : exp2_fast(m - n);
+                        m = n;
+                        l *= scale;
+                        if (wide) {
+                            const int to = min(((__float_as_int(vmax) >> 23) & 255) - 126, 126);
+                            scale *= to - E > 126 ? 0.0f : pow2(E - to);
+                            E = to;
+                        }
+                        if (t > w.from) {
+#pragma unroll 1
+                            for (int i = 0; i < DP; i += 16) {
+                                uint32_t o[16];
+                                tmem_ld_32x32b_x16(o_at + i, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale);
+                                tmem_st_32x32b_x16(o_at + i, o);
+                            }
+                        }
+                    }
+                    const float u = m == neg_inf() ? 0.0f : m - kLift;
+                    const F2 rf2 = f2(rf, rf), u2 = f2(-u, -u);
+                    [[maybe_unused]] const float down = CODES ? pow2(-E) : 1.0f;
+                    F2 sum = f2(0.0f, 0.0f), sum2 = sum;
+#pragma unroll
+                    for (int c = 0; c < kTile / 32; ++c) {
+                        uint32_t(&x)[32] = r[c & 1];
+                        if (c > 0) tmem_wait_ld();
+                        // terms of these columns go where scores have been read already
+                        if (c + 1 < kTile / 32) tmem_ld_32x32b_x32(s_at + 32 * (c + 1), r[(c + 1) & 1]);
+                        scored(32 * c, x);
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float e0, e1;
+                            f2_split(f2_fma(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), rf2, u2), e0, e1);
+                            e0 = exp2_fast(e0), e1 = exp2_fast(e1);
+                            if (i & 1) sum2 = f2_add(sum2, f2(e0, e1));
+                            else sum = f2_add(sum, f2(e0, e1));
+                            if constexpr (CODES) {
+                                // (below 1 where the row sees the token; finite times 0 where not)
+                                const float2 v2 = *reinterpret_cast<const float2 *>(sv + 32 * c + 2 * i);
+                                e0 *= fminf(v2.x * down, 1.0f), e1 *= fminf(v2.y * down, 1.0f);
+                            }
+                            p[i] = BF ? pack_bf16x2_rn(e0, e1) : pack_f16x2_rn(e0, e1);
+                        }
+                        tmem_st_32x32b_x16(s_at + 16 * c, p);
+                    }
+                    l += f2_sum(f2_add(sum, sum2));
+                };
+                if (t0 + kTile > full_upto || t0 < full_from) tile(std::true_type{});
+                else tile(std::false_type{});
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&bars->p_full[half]);
-                    if constexpr (CODES) {
-                        mbar_arrive(&bars->scales_empty[sc.slot]);
-                        if (!two) mbar_arrive(&bars->scales_empty[sc.slot]);
-                    }
+                    if constexpr (CODES) mbar_arrive(&bars->scales_empty[sc.slot]);
                 }
                 sc.step(S::kScaleSlots);
+                if (issues) {
+                    const bool more = t + 1 < w.upto;
+                    if (!warp_wait(&v_full[vt.slot], vt.phase, a.wait_ns) || !warp_wait(&bars->p_full[half], p_phase, a.wait_ns)) ok = false;
+                    if (ok) sums(t > w.from, !more);
+                    if (ok && more) {
+                        ok = warp_wait(&bars->k_full[kt.slot], kt.phase, a.wait_ns);
+                        if (ok) scores();
+                    }
+                    if (!ok) {
+                        fail();
+                        break;
+                    }
+                }
+                p_phase ^= 1u;
             }
             if (!ok) break;
             // ------------------------------------------------ the item's end
@@ -388,230 +475,159 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             if (!whole && w.from == 0 && tid == 0) a.meta[blockIdx.x] = make_int4(w.s, w.h, w.b, w.parts());
             tc_fence_before();
         }
-    } else if (warp < 12) {
-        reg_dec<S::kOtherRegs>();
-        if (warp == kCopyWarp) {
+        if (issues) {
+            // what was issued is done before tensor memory is given back
+            if (elect_one()) tc_commit(&bars->done[half]);
+            __syncwarp();
+            if (!warp_wait(&bars->done[half], 0u, landing_limit(a.wait_ns))) fail();
+        }
+    } else {
+        if constexpr (!CODES) {
             // ------------------------------------------------------- copies
             Turn kt, vt;
-            long long issued_k = 0, issued_v = 0;                      // 16-bit: tiles; codes: both count in issued_k
+            long long issued = 0, landing_k = 0, landing_v = 0;        // tiles; those of keys and of values that copies were issued for
             bool ok = true;
-            constexpr int RB = CODES ? 64 : 128;
             const int in_page = a.c.page_tokens;
             for (; ok && w.valid(); w.next(a)) {
                 const int32_t *table = a.c.table + w.s * a.c.ldt;
                 const int64_t head = static_cast<int64_t>(w.h) * a.c.head_bytes;
                 const int end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> a.c.log_page;
-                int held = -32, page = 0;
-                for (int t = w.from; ok && t < w.upto; ++t) {
+                int held = -32, page = 0;                              // lane l holds page held + l of the sequence
+                for (int t = w.from; ok && t < w.upto; ++t, ++issued) {
                     const int t0 = (w.first + t) * kTile, tokens = min(max(end - t0, 0), kTile);
                     const int p0 = t0 >> a.c.log_page, np = tokens > 0 ? ((t0 + tokens - 1) >> a.c.log_page) - p0 + 1 : 0;
                     if (np > 0 && p0 + np > held + 32) {
                         held = p0;
-                        page = held + lane < pages ? table[held + lane] : 0;
-                        if (page < 0 || page >= a.c.n_pages) {
-                            record_status(a.status, kErrCheck);
-                            page = min(max(page, 0), a.c.n_pages - 1);
-                        }
+                        page = page_of(a, table, held + lane, pages);
                     }
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {                   // keys, then values
-                        Turn &tn = CODES || kv == 0 ? kt : vt;
-                        long long &issued = CODES || kv == 0 ? issued_k : issued_v;
-                        const int depth = CODES ? S::kRaw : kv == 0 ? S::kK : S::kV;
-                        uint64_t *full = CODES ? bars->raw_full : kv == 0 ? bars->k_full : bars->v_full;
-                        uint64_t *empty = CODES ? bars->raw_empty : kv == 0 ? bars->k_empty : bars->v_empty;
-                        uint8_t *dst = CODES ? raw + tn.slot * S::kRawBytes : (kv == 0 ? ks : vs) + tn.slot * S::kTileBytes;
+                        Turn &tn = kv == 0 ? kt : vt;
+                        constexpr int kDepth[2] = {S::kK, S::kV};
+                        uint64_t *full = kv == 0 ? &bars->k_full[tn.slot] : &bars->v_full[tn.slot];
+                        uint64_t *empty = kv == 0 ? &bars->k_empty[tn.slot] : &bars->v_empty[tn.slot];
+                        uint8_t *dst = (kv == 0 ? ks : vs) + tn.slot * S::kTileBytes;
                         bool go = !aborted();
-                        if (go && issued >= depth && !mbar_wait(&empty[tn.slot], tn.phase ^ 1u, a.wait_ns)) {
+                        if (go && issued >= kDepth[kv] && !mbar_wait(empty, tn.phase ^ 1u, a.wait_ns)) {
                             fail();
                             go = false;
                         }
                         ok = __all_sync(0xFFFFFFFFu, go) != 0;
                         if (!ok) break;
-                        const int scale_tokens = CODES ? (tokens + 3) & ~3 : 0;
-                        if (lane == 0) mbar_arrive_expect_tx(&full[tn.slot], static_cast<uint32_t>(tokens * CH * RB + 4 * scale_tokens));
+                        if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(tokens * CH * 128));
                         __syncwarp();
-                        constexpr int per_page = CH + (CODES ? 1 : 0);
-                        const int pieces = np * per_page;
+                        const int pieces = np * CH;
                         for (int x0 = 0; x0 < pieces; x0 += 32) {
-                            const int x = x0 + lane, j = x / per_page, y = x - j * per_page;
+                            const int x = x0 + lane, j = x / CH, y = x % CH;
                             const int pg = __shfl_sync(0xFFFFFFFFu, page, min(p0 + j - held, 31));
                             if (x < pieces) {
                                 const int in = max(t0 - ((p0 + j) << a.c.log_page), 0);
                                 const int at = ((p0 + j) << a.c.log_page) + in - t0;
                                 const int n = min(in_page - in, tokens - at);
-                                const uint8_t *src = a.c.pages + pg * a.c.page_bytes + head;
-                                if (y < CH)
-                                    bulk_g2s(dst + y * (kTile * RB) + at * RB, src + ((kv * CH + y) * in_page + in) * RB, static_cast<uint32_t>(n * RB),
-                                             &full[tn.slot]);
-                                else
-                                    bulk_g2s(dst + CH * kTile * RB + at * 4, src + 2 * CH * in_page * RB + (kv * in_page + in) * 4,
-                                             static_cast<uint32_t>(((n + 3) & ~3) * 4), &full[tn.slot]);
+                                bulk_g2s(dst + y * kAtomRows + at * 128,
+                                         a.c.pages + pg * a.c.page_bytes + head + ((kv * CH + y) * in_page + in) * 128,
+                                         static_cast<uint32_t>(n * 128), full);
                             }
                         }
-                        ++issued;
-                        tn.step(depth);
+                        landing_k = kv == 0 ? issued + 1 : landing_k;
+                        landing_v = kv == 1 ? issued + 1 : landing_v;
+                        tn.step(kDepth[kv]);
                     }
                 }
             }
             // no copy may be landing when the CTA leaves
-            const auto land = [&](uint64_t *full, long long issued, int depth) {
-                for (long long i = issued > depth ? issued - depth : 0; i < issued; ++i)
+            const auto land = [&](uint64_t *full, long long n, int depth) {
+                for (long long i = n > depth ? n - depth : 0; i < n; ++i)
                     if (!mbar_wait(&full[i % depth], static_cast<uint32_t>(i / depth) & 1u, landing_limit(a.wait_ns))) fail();
             };
-            if (CODES) {
-                land(bars->raw_full, issued_k, S::kRaw ? S::kRaw : 1);
-            } else {
-                land(bars->k_full, issued_k, S::kK);
-                land(bars->v_full, issued_v, S::kV ? S::kV : 1);
-            }
-        } else if (warp == kMmaWarp) {
-            // ----------------------------------------------------- products
-            constexpr uint32_t type = BF ? idesc_bf16_f32(0, 0) : idesc_f16_f32(0, 0);
-            constexpr uint32_t id_s = type | idesc_f16_f32(kHalf, kTile), id_o = type | idesc_f16_f32(kHalf, DP) | kNMajorB;
-            const uint32_t d = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-            const uint64_t q0 = smem_desc_sw128(smem_u32(qs)), k0 = smem_desc_sw128(smem_u32(ks));
-            const uint64_t v0 = desc_n_major(smem_u32(CODES ? ks : vs), kAtomRows);
-            uint64_t *const v_full = CODES ? bars->k_full : bars->v_full, *const v_empty = CODES ? bars->k_empty : bars->v_empty;
-            Turn kt, vt;
-            if (CODES) vt.step(S::kK);                                 // K and V tiles in turn in one ring
-            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-            const auto next_k = [&] { kt.step(S::kK); if (CODES) kt.step(S::kK); };
-            const auto next_v = [&] { if (CODES) vt.step(S::kK), vt.step(S::kK); else vt.step(S::kV ? S::kV : 1); };
+            land(bars->k_full, landing_k, S::kK);
+            land(bars->v_full, landing_v, S::kV);
+        } else {
+            // ---------------------------------------------- codes to fp16
+            // Four warps; a thread has a 16-byte unit of eight rows of 64 codes (four at DP =
+            // 64), fetched a tile of keys or values ahead of its conversion.
+            constexpr int kUnits = CH * 4;
+            const int me = tid - kFeedWarp0 * 32, in_page = a.c.page_tokens;
+            const int unit = me & 3;
+            Walk f = w;                                                // where the fetches are
+            int f_t = f.from, f_kv = 0;
+            uint4 codes[kUnits];
+            float scale;
+            // where the next tile's units of rows me / 4 + 32 i are (nullptr: not held), and its scale
+            const uint8_t *src[4];
+            const float *scale_src;
+            const auto aim = [&] {
+                if (!f.valid()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) src[i] = nullptr;
+                    scale_src = nullptr;
+                    return;
+                }
+                const int end = min(f.hi, f.q.len), t0 = (f.first + f_t) * kTile, tokens = min(max(end - t0, 0), kTile);
+                const int p0 = t0 >> a.c.log_page, pages = (end + in_page - 1) >> a.c.log_page;
+                const int page = tokens > 0 ? page_of(a, a.c.table + f.s * a.c.ldt, p0 + (lane & 7), pages) : 0;
+                const uint8_t *head = a.c.pages + static_cast<int64_t>(f.h) * a.c.head_bytes;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = i * 32 + me / 4, x = t0 + tok;
+                    const int pg = __shfl_sync(0xFFFFFFFFu, page, (x >> a.c.log_page) - p0);
+                    src[i] = tok < tokens ? head + pg * a.c.page_bytes + (f_kv * CH * in_page + (x & (in_page - 1))) * 64 + 16 * unit : nullptr;
+                }
+                const int x = t0 + me, pg = __shfl_sync(0xFFFFFFFFu, page, (x >> a.c.log_page) - p0);
+                scale_src = me < tokens ? reinterpret_cast<const float *>(head + pg * a.c.page_bytes + 2 * CH * in_page * 64) + f_kv * in_page + (x & (in_page - 1))
+                                        : nullptr;
+                if (f_kv == 1 && ++f_t >= f.upto) {
+                    f.next(a);
+                    f_t = f.from;
+                }
+                f_kv ^= 1;
+            };
+            const auto load = [&](int j) { return src[j % 4] ? *reinterpret_cast<const uint4 *>(src[j % 4] + j / 4 * (in_page * 64)) : make_uint4(0u, 0u, 0u, 0u); };
+            aim();
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) codes[j] = load(j);
+            scale = scale_src ? *scale_src : 0.0f;
+            Turn kt, sc;
+            long long done = 0;
             bool ok = true;
-            const auto scores = [&](int half) {                        // S of the K tile in turn
-                const uint64_t kd = k0 + static_cast<uint64_t>(kt.slot * (S::kTileBytes >> 4));
-                const uint64_t qd = q0 + static_cast<uint64_t>(half * CH * (kAtomRows >> 4));
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tc_mma_f16(d + 128u * half, qd + c * (kAtomRows >> 4) + 2 * i, kd + c * (kAtomRows >> 4) + 2 * i, id_s, c + i > 0 ? 1u : 0u);
-                    tc_commit(&bars->s_full[half]);
-                }
-                __syncwarp();
-            };
-            const auto sums = [&](int half, bool add, bool last) {     // O of the V tile in turn
-                const uint64_t vd = v0 + static_cast<uint64_t>(vt.slot * (S::kTileBytes >> 4));
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int i = 0; i < kTile / 16; ++i)
-                        tc_mma_f16_ts(d + 256u + 128u * half, d + 128u * half + 8u * i, vd + i * (2048 >> 4), id_o, add || i > 0 ? 1u : 0u);
-                    if (last) tc_commit(&bars->s_full[half]);
-                }
-                __syncwarp();
-            };
-            const auto release = [&](uint64_t *bar) {
-                if (elect_one()) tc_commit(bar);
-                __syncwarp();
-            };
-            const auto wait = [&](uint64_t *bar, uint32_t phase) {
-                if (ok && !warp_wait(bar, phase, a.wait_ns)) {
-                    fail();
-                    ok = false;
-                }
-                return ok;
-            };
             for (; ok && w.valid(); w.next(a)) {
-                const bool two = both();
-                if (!wait(&bars->q_full[0], q_phase[0]) || !wait(&bars->k_full[kt.slot], kt.phase)) break;
-                q_phase[0] ^= 1u;
-                scores(0);
-                if (two) {
-                    if (!wait(&bars->q_full[1], q_phase[1])) break;
-                    q_phase[1] ^= 1u;
-                    scores(1);
-                }
-                release(&bars->k_empty[kt.slot]);
-                next_k();
-                for (int t = w.from; t < w.upto; ++t) {
-                    const bool more = t + 1 < w.upto;
-                    if (!wait(&v_full[vt.slot], vt.phase) || !wait(&bars->p_full[0], p_phase[0])) break;
-                    p_phase[0] ^= 1u;
-                    sums(0, t > w.from, !more);
-                    if (more) {
-                        if (!wait(&bars->k_full[kt.slot], kt.phase)) break;
-                        scores(0);
-                    }
-                    if (two) {
-                        if (!wait(&bars->p_full[1], p_phase[1])) break;
-                        p_phase[1] ^= 1u;
-                        sums(1, t > w.from, !more);
-                    }
-                    release(&v_empty[vt.slot]);
-                    next_v();
-                    if (more) {
-                        if (two) scores(1);
-                        release(&bars->k_empty[kt.slot]);
-                        next_k();
-                    }
-                }
-            }
-            // what was issued is done before tensor memory is given back
-            if (elect_one()) tc_commit(&bars->done);
-            __syncwarp();
-            if (!warp_wait(&bars->done, 0u, landing_limit(a.wait_ns))) fail();
-        }
-    } else if constexpr (CODES) {
-        // ---------------------------------------------------- codes to fp16
-        reg_dec<S::kConvertRegs>();
-        Turn rt, kt, sc;
-        long long done = 0;
-        long long tiles = 0;
-        bool ok = true;
-        const int me = tid - kConvertWarp0 * 32;
-        for (; ok && w.valid(); w.next(a)) {
-            const int end = min(w.hi, w.q.len);
-            for (int t = w.from; ok && t < w.upto; ++t) {
-                const int t0 = (w.first + t) * kTile, tokens = min(max(end - t0, 0), kTile);
-                if (tiles >= S::kScaleSlots && !warp_wait(&bars->scales_empty[sc.slot], sc.phase ^ 1u, a.wait_ns)) ok = false;
-                for (int kv = 0; ok && kv < 2; ++kv) {
-                    if (!warp_wait(&bars->raw_full[rt.slot], rt.phase, a.wait_ns) ||
-                        (done >= S::kK && !warp_wait(&bars->k_empty[kt.slot], kt.phase ^ 1u, a.wait_ns))) {
-                        ok = false;
-                        break;
-                    }
-                    const uint8_t *src = raw + rt.slot * S::kRawBytes;
-                    uint8_t *dst = ks + kt.slot * S::kTileBytes;
-                    // a thread a token, its 16 codes at a time; rows that were not copied: zeros
-                    const bool held = me < tokens;
+                for (int t = w.from; ok && t < w.upto; ++t) {
 #pragma unroll
-                    for (int c = 0; c < CH; ++c)
+                    for (int kv = 0; kv < 2; ++kv) {
+                        aim();
+                        if (kv == 0 && done >= 2 * S::kScaleSlots && !warp_wait(&bars->scales_empty[sc.slot], sc.phase ^ 1u, a.wait_ns)) ok = false;
+                        if (ok && done >= S::kK && !warp_wait(&bars->k_empty[kt.slot], kt.phase ^ 1u, a.wait_ns)) ok = false;
+                        if (!ok) break;
+                        uint8_t *dst = ks + kt.slot * S::kTileBytes;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int unit = i ^ ((me >> 1) & 3);      // what stands at place i
-                            const uint4 v = lds128(src + c * (kTile * 64) + me * 64 + 16 * i);
+                        for (int j = 0; j < kUnits; ++j) {
+                            const uint4 v = codes[j];
+                            codes[j] = load(j);
+                            const int tok = j % 4 * 32 + me / 4, u = unit ^ ((tok >> 1) & 3);   // which of the row's units this is
                             uint32_t o[8];
                             codes_f16(v.x, o[0], o[1]), codes_f16(v.y, o[2], o[3]);
                             codes_f16(v.z, o[4], o[5]), codes_f16(v.w, o[6], o[7]);
-                            if (!held) {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) o[j] = 0u;
-                            }
-                            uint8_t *row = dst + c * kAtomRows + me * 128;
-                            sts128(row + (((2 * unit) ^ (me & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
-                            sts128(row + (((2 * unit + 1) ^ (me & 7)) << 4), make_uint4(o[4], o[5], o[6], o[7]));
+                            uint8_t *row = dst + j / 4 * kAtomRows + tok * 128;
+                            sts128(row + (((2 * u) ^ (tok & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+                            sts128(row + (((2 * u + 1) ^ (tok & 7)) << 4), make_uint4(o[4], o[5], o[6], o[7]));
                         }
-                    const float scale = held ? reinterpret_cast<const float *>(src + CH * kTile * 64)[me] : 0.0f;
-                    scales[sc.slot * (2 * kTile) + kv * kTile + me] = scale;
-                    const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(scale) & 0x7FFFFFFFu);
-                    if (kv == 1 && lane == 0) scales[S::kScaleSlots * 2 * kTile + sc.slot * 4 + warp - kConvertWarp0] = __uint_as_float(largest);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&bars->raw_empty[rt.slot]);
-                        mbar_arrive(&bars->k_full[kt.slot]);
-                        if (kv == 1) mbar_arrive(&bars->scales_full[sc.slot]);
+                        scales[sc.slot * (2 * kTile) + kv * kTile + me] = scale;
+                        if (kv == 1) {
+                            const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(scale) & 0x7FFFFFFFu);
+                            if (lane == 0) scales[S::kScaleSlots * 2 * kTile + sc.slot * 4 + warp - kFeedWarp0] = __uint_as_float(largest);
+                        }
+                        scale = scale_src ? *scale_src : 0.0f;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bars->k_full[kt.slot]);
+                            if (kv == 1) mbar_arrive(&bars->scales_full[sc.slot]);
+                        }
+                        kt.step(S::kK);
+                        ++done;
                     }
-                    rt.step(S::kRaw ? S::kRaw : 1);
-                    kt.step(S::kK);
-                    ++done;
+                    sc.step(S::kScaleSlots);
                 }
-                ++tiles;
-                sc.step(S::kScaleSlots);
             }
             if (!ok) fail();
         }
@@ -619,23 +635,16 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, 512u);
+    if (warp == 0) tmem_dealloc(tmem, 512u);
 }
 
 template <int KIND, int DP> cudaError_t launch(const AttnArgs &args, int sm_count, cudaStream_t s, int *ctas)
 {
-    using S = TensorShape<KIND, DP>;
     AttnArgs a = args;
     const void *f = reinterpret_cast<const void *>(&attn_tensor_kernel<KIND, DP>);
     static_assert(TensorShape<KIND, DP>::kSmem <= kSmemOptIn, "shared memory");
     cudaError_t e = set_max_smem(f, TensorShape<KIND, DP>::kSmem);
     if (e != cudaSuccess) return e;
-    // the warps' shares of registers have to add up to what the launch has
-    static const bool enough = [f] {
-        cudaFuncAttributes fa{};
-        return cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs * S::kThreads >= 128 * (2 * S::kSoftmaxRegs + S::kOtherRegs + (S::kCodes ? S::kConvertRegs : 0));
-    }();
-    if (!enough) return cudaErrorLaunchOutOfResources;
     *ctas = std::min(kAttnMaxCtas / 2, sm_count);
     void *p[] = {&a};
     return launch_pdl(f, dim3(static_cast<unsigned>(*ctas)), dim3(TensorShape<KIND, DP>::kThreads), TensorShape<KIND, DP>::kSmem, s, p);

@@ -172,11 +172,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
                 const int p0 = t0 >> a.c.log_page, np = tokens > 0 ? ((t0 + tokens - 1) >> a.c.log_page) - p0 + 1 : 0;
                 if (np > 0 && p0 + np > held + 32) {
                     held = p0;
-                    page = held + lane < pages ? table[held + lane] : 0;
-                    if (page < 0 || page >= a.c.n_pages) {
-                        record_status(a.status, kErrCheck);
-                        page = min(max(page, 0), a.c.n_pages - 1);
-                    }
+                    page = page_of(a, table, held + lane, pages);
                 }
                 const int pieces = np * per_page;
                 for (int x0 = 0; x0 < pieces; x0 += 32) {

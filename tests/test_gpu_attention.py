@@ -101,6 +101,14 @@ def test_long(q4lib, name, cache, new):
 
 
 @pytest.mark.parametrize("name,cache", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_blocks_of_all_sizes_in_a_row(q4lib, name, cache, d):
+    """Blocks of few and of many rows in turn, over more tiles than any ring has."""
+    counts = [20, 70, 33, 300, 17, 130, 64, 65]
+    run(q4lib, name, cache, 8, 2, d, 32, [n + 1500 for n in counts], counts)
+
+
+@pytest.mark.parametrize("name,cache", KINDS)
 def test_prompt(q4lib, name, cache):
     run(q4lib, name, cache, 4, 2, 128, 64, [515, 700], [515, 300])
 
