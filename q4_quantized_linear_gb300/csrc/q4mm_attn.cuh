@@ -57,13 +57,13 @@ struct Walk {
     Seq q;
     int first, count, hi;     // its tiles
     int from, upto;           // those of them that are this CTA's
-    long long left;           // tiles of the share from this item on
-    long long share;
+    int left;                 // tiles of the share from this item on
+    int share;
 
     __device__ __forceinline__ bool whole() const { return from == 0 && upto == count; }
     __device__ __forceinline__ void clip()
     {
-        upto = left < static_cast<long long>(count - from) ? from + static_cast<int>(left) : count;
+        upto = left < count - from ? from + left : count;
     }
     // `scan`: shared memory of n_seq + 1 numbers, free again after the next barrier.
     __device__ __forceinline__ void begin(const AttnArgs &a, long long *scan)
@@ -104,13 +104,10 @@ struct Walk {
         }
         __syncthreads();
         const long long total = scan[a.n_seq];
-        share = (total + gridDim.x - 1) / gridDim.x;
-        const long long at = share * blockIdx.x;
-        left = total - at < share ? total - at : share;
-        if (left <= 0) {
-            left = 0;
-            return;
-        }
+        share = static_cast<int>((total + gridDim.x - 1) / gridDim.x);
+        const long long at = static_cast<long long>(share) * blockIdx.x;
+        left = static_cast<int>(min(max(total - at, 0ll), static_cast<long long>(share)));
+        if (left == 0) return;
         int lo = 0, hi_s = a.n_seq - 1;   // the last sequence whose work starts at or before `at`
         while (lo < hi_s) {
             const int mid = (lo + hi_s + 1) >> 1;
@@ -172,8 +169,7 @@ struct Walk {
     // Parts of an item that starts in this CTA and is not finished in it.
     __device__ __forceinline__ int parts() const
     {
-        const long long rest = static_cast<long long>(count) - upto;
-        return 1 + static_cast<int>((rest + share - 1) / share);
+        return 1 + (count - upto + share - 1) / share;
     }
 };
 

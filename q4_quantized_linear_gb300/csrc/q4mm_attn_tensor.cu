@@ -12,15 +12,14 @@
 // of them. The maximum m is raised, and O scaled, only where a row's scores pass it
 // by 2^8; the softmax threads scale O themselves (S of a tile is committed after
 // the products of the tile before, so O rests).
-//   Warps: 0-3 and 4-7 the halves' softmax (a row a thread: no shuffles), the first
-// of each issuing its products; 8 copies, or 8-11 turn codes into fp16 tiles: the
+//   Warps: 0-3 and 4-7 the halves' softmax (a row a thread: no shuffles), 8 issues the
+// products, 9 copies; over codes 8-11 turn them into fp16 tiles and 12 issues: the
 // scales of keys multiply scores, those of values terms, as in the warp-MMA kernel.
 //   K and V lie in the pages as the tensor cores read them, 64 dims a row of 128
 // bytes, swizzled: K as a K-major operand, V (dims contiguous) as an N-major one.
 //   A page's rows past the sequence's end are never copied: what their place holds
 // is zeros or an earlier tile's values, finite as all values of the cache.
 #include <algorithm>
-#include <type_traits>
 
 #include "q4mm_attn.cuh"
 
@@ -28,16 +27,22 @@ namespace q4 {
 namespace {
 
 constexpr int kHalf = 128, kTile = kTensorTile;
-constexpr int kFeedWarp0 = 8;                           // the copies' warp, or the first of four that convert codes
+constexpr int kSoftmaxWarps = 8;                        // four a half
+constexpr uint32_t kFirst = 1, kLast = 2, kTwo = 4;     // of a tile: where it stands in its item, and whether the item has a second half
 constexpr uint32_t kAtomRows = kTile * 128;              // bytes of 64 dims of a tile
 
 template <int KIND, int DP> struct TensorShape {
     static constexpr bool kCodes = KIND == 2;
     static constexpr int kChunks = DP / kChunk;
-    static constexpr int kThreads = kCodes ? 384 : 288;
+    // Warps 8 and 9: products and copies; codes: 8-11 convert, 12 products. Warpgroups
+    // share the registers out: a softmax thread holds a row of scores.
+    static constexpr int kThreads = kCodes ? 512 : 384;
+    static constexpr int kConvertWarp0 = 8, kMmaWarp = kCodes ? 12 : 8, kCopyWarp = 9;
+    static constexpr int kSoftmaxRegs = kCodes ? 168 : 208, kConvertRegs = 104, kMmaRegs = kCodes ? 72 : 88;
+    static constexpr int kAllRegs = 128 * (2 * kSoftmaxRegs + kMmaRegs + (kCodes ? kConvertRegs : 0));
     static constexpr int kTileBytes = kChunks * static_cast<int>(kAtomRows);
     // 16-bit: rings of K and of V tiles. Codes: one ring of fp16 tiles, K and V in turn.
-    static constexpr int kK = 4 - (kCodes || DP == 64 ? 0 : 2), kV = kCodes ? 0 : DP == 128 ? 3 : 4;
+    static constexpr int kK = kCodes || DP == 64 ? 4 : 2, kV = kCodes ? 0 : DP == 64 ? 4 : 3;
     static constexpr int kScaleSlots = 4;                // tiles whose scales are held
     static constexpr size_t kSmem = 2 * kHalf * DP * 2 + static_cast<size_t>(kK + kV) * kTileBytes +
                                     (kCodes ? kScaleSlots * (2 * kTile + 4) * 4 : 0) + 2 * kHalf * 4 + 512 + 1024;
@@ -45,27 +50,30 @@ template <int KIND, int DP> struct TensorShape {
 
 struct Bars {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], scales_full[4], scales_empty[4];
-    uint64_t q_full[2], s_full[2], p_full[2], done[2];
+    uint64_t q_full[2], s_full[2], p_full[2][2], done;
+    uint32_t flags[4];                                   // of the K tile in each slot
     uint32_t tmem;
     int abort;
 };
 
-__device__ __forceinline__ bool spin_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+// Waits with one outcome for the warp. A suspended wait (try_wait) resumes some 170
+// ns late, a third of a half's softmax; tests without a pause take shared memory's
+// time from the products' operands. NAP: nanoseconds between two tests.
+template <int NAP> __device__ __forceinline__ bool spin_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
 {
-    // (a suspended wait resumes some 170 ns late, a third of a half's softmax)
-    for (int i = 0; i < 64; ++i)
-        if (mbar_test_wait(bar, parity)) return true;
+    if (mbar_test_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (true) {
-        for (int i = 0; i < 64; ++i)
+        for (int i = 0; i < 16; ++i) {
+            if (NAP > 0) __nanosleep(NAP);
             if (mbar_test_wait(bar, parity)) return true;
+        }
         if (globaltimer_ns() - t0 > limit_ns) return false;
     }
 }
-// One outcome for the warp.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+template <int NAP = 40> __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
 {
-    return __all_sync(0xFFFFFFFFu, spin_wait(bar, parity, limit_ns)) != 0;
+    return __all_sync(0xFFFFFFFFu, spin_wait<NAP>(bar, parity, limit_ns)) != 0;
 }
 
 struct Turn {
@@ -91,6 +99,8 @@ __device__ __forceinline__ uint64_t desc_n_major(uint32_t saddr, uint32_t lead)
 }
 constexpr uint32_t kNMajorB = 1u << 16;
 
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ F2 f2_add(F2 a, F2 b)
 {
     F2 r;
@@ -112,22 +122,29 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     float *const scales = reinterpret_cast<float *>(vs + S::kV * S::kTileBytes);   // [slot][keys, values][tile], then [slot][4]: the largest
     float *const row_factor = scales + (CODES ? S::kScaleSlots * (2 * kTile + 4) : 0);
     Bars *const bars = reinterpret_cast<Bars *>(row_factor + 2 * kHalf);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (a warp's number from one lane: what follows from it stays in uniform registers)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     static_assert(sizeof(Bars) <= 512, "barriers");
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars->k_full[i], CODES ? 4 : 1);
-            mbar_init(&bars->k_empty[i], 2);                           // both halves
+            mbar_init(&bars->k_empty[i], 1);
             mbar_init(&bars->v_full[i], 1);
-            mbar_init(&bars->v_empty[i], 2);
+            mbar_init(&bars->v_empty[i], 1);
             mbar_init(&bars->scales_full[i], 4);
-            mbar_init(&bars->scales_empty[i], 8);
+            mbar_init(&bars->scales_empty[i], kSoftmaxWarps);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&bars->q_full[i], 4), mbar_init(&bars->s_full[i], 1), mbar_init(&bars->p_full[i], 4), mbar_init(&bars->done[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->q_full[i], 4);
+            mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_full[i][0], 4);
+            mbar_init(&bars->p_full[i][1], 4);
+        }
+        mbar_init(&bars->done, 1);
         bars->abort = 0;
         fence_barrier_init();
     }
-    if (warp == 0) {
+    if (warp == S::kMmaWarp) {
         tmem_alloc(&bars->tmem, 512u);
         tmem_relinquish();
     }
@@ -150,72 +167,24 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     };
     const auto both = [&] { return w.q.rows - w.b * kTensorRows > kHalf; };   // whether the item has a second half
 
-    if (warp < 8) {
+    const int tiles = w.left;                                          // of the CTA's share
+    if (warp < kSoftmaxWarps) {
         // ---------------------------------------------------------- softmax
+        reg_inc<S::kSoftmaxRegs>();
         const int half = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + 128u * half, o_at = tmem + lanes + 256u + 128u * half;
-        uint32_t q_phase = 0, s_phase = 0, p_phase = 0;
+        const int r_in = half * kHalf + (warp & 3) * 32 + lane;        // the thread's row in the block
+        uint32_t s_phase = 0;
         Turn sc;                                                       // the tile's scales
         bool ok = true;
-        // The half's first warp issues its products: the scores of a tile as soon as the
-        // terms of the one before are taken.
-        constexpr uint32_t type = BF ? idesc_bf16_f32(0, 0) : idesc_f16_f32(0, 0);
-        constexpr uint32_t id_s = type | idesc_f16_f32(kHalf, kTile), id_o = type | idesc_f16_f32(kHalf, DP) | kNMajorB;
-        uint64_t *const v_full = CODES ? bars->k_full : bars->v_full, *const v_empty = CODES ? bars->k_empty : bars->v_empty;
-        Turn kt, vt;                                                   // K and V tiles in turn
-        if (CODES) vt.step(S::kK);                                     // ... of one ring
-        const auto next_k = [&] { kt.step(S::kK); if (CODES) kt.step(S::kK); };
-        const auto next_v = [&] { vt.step(CODES ? S::kK : S::kV); if (CODES) vt.step(S::kK); };
-        const auto scores = [&] {
-            const uint32_t d = __shfl_sync(0xFFFFFFFFu, tmem, 0) + 128u * half;
-            const uint64_t kd = smem_desc_sw128(smem_u32(ks)) + static_cast<uint64_t>(kt.slot * (S::kTileBytes >> 4));
-            const uint64_t qd = smem_desc_sw128(smem_u32(qs)) + static_cast<uint64_t>(half * CH * (kAtomRows >> 4));
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int c = 0; c < CH; ++c)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tc_mma_f16(d, qd + c * (kAtomRows >> 4) + 2 * i, kd + c * (kAtomRows >> 4) + 2 * i, id_s, c + i > 0 ? 1u : 0u);
-                tc_commit(&bars->s_full[half]);
-                tc_commit(&bars->k_empty[kt.slot]);
-            }
-            __syncwarp();
-            next_k();
-        };
-        const auto sums = [&](bool add, bool last) {
-            const uint32_t d = __shfl_sync(0xFFFFFFFFu, tmem, 0) + 128u * half;
-            const uint64_t vd = desc_n_major(smem_u32(CODES ? ks : vs), kAtomRows) + static_cast<uint64_t>(vt.slot * (S::kTileBytes >> 4));
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int i = 0; i < kTile / 16; ++i) tc_mma_f16_ts(d + 256u, d + 8u * i, vd + i * (2048 >> 4), id_o, add || i > 0 ? 1u : 0u);
-                if (last) tc_commit(&bars->s_full[half]);
-                tc_commit(&v_empty[vt.slot]);
-            }
-            __syncwarp();
-            next_v();
-        };
-        const bool issues = (warp & 3) == 0;
         for (; ok && w.valid(); w.next(a)) {
             if (half && !both()) {
-                // the half is not there: it gives its tiles back as they come, so that no
-                // ring runs ahead of it
-                for (int t = w.from; ok && t < w.upto; ++t) {
-                    if constexpr (CODES) {
-                        ok = warp_wait(&bars->scales_full[sc.slot], sc.phase, a.wait_ns);
-                        if (ok && lane == 0) mbar_arrive(&bars->scales_empty[sc.slot]);
-                        sc.step(S::kScaleSlots);
-                    }
-                    if (issues) {
-                        ok = ok && warp_wait(&bars->k_full[kt.slot], kt.phase, a.wait_ns);
-                        if (ok && lane == 0) mbar_arrive(&bars->k_empty[kt.slot]);
-                        ok = ok && warp_wait(&v_full[vt.slot], vt.phase, a.wait_ns);
-                        if (ok && lane == 0) mbar_arrive(&v_empty[vt.slot]);
-                        next_k();
-                        next_v();
-                    }
+                // the half is not there: it gives the scales back as they come
+                for (int t = w.from; CODES && ok && t < w.upto; ++t) {
+                    ok = warp_wait(&bars->scales_full[sc.slot], sc.phase, a.wait_ns);
+                    if (ok && lane == 0) mbar_arrive(&bars->scales_empty[sc.slot]);
+                    sc.step(S::kScaleSlots);
                 }
                 if (!ok) fail();
                 continue;
@@ -261,15 +230,6 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->q_full[half]);
-            if (issues) {
-                if (!warp_wait(&bars->q_full[half], q_phase, a.wait_ns) || !warp_wait(&bars->k_full[kt.slot], kt.phase, a.wait_ns)) {
-                    fail();
-                    ok = false;
-                    break;
-                }
-                scores();
-            }
-            q_phase ^= 1u;
             const int my_row = first_row + lane;
             const float rf = CODES ? row_factor[half * kHalf + (warp & 3) * 32 + lane] : a.scale_log2;
             int lo, hi, full_from, full_upto, x;
@@ -291,130 +251,102 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 s_phase ^= 1u;
                 tc_fence_after();
                 const float *sk = scales + sc.slot * (2 * kTile), *sv = sk + kTile;
-                float vmax = 0.0f;
+                const bool masked = t0 + kTile > full_upto || t0 < full_from;   // some row does not see all of the tile
+                uint32_t r[kTile];
+#pragma unroll
+                for (int i = 0; i < kTile; i += 32) tmem_ld_32x32b_x32(s_at + i, r + i);
+                tmem_wait_ld();
                 if constexpr (CODES) {
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 4) {
+                        const float4 k4 = *reinterpret_cast<const float4 *>(sk + i);
+                        float y[4];
+                        f2_split(f2_mul(f2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2(k4.x, k4.y)), y[0], y[1]);
+                        f2_split(f2_mul(f2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), f2(k4.z, k4.w)), y[2], y[3]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) r[i + j] = __float_as_uint(y[j]);
+                    }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int i0 = 0; i0 < kTile; i0 += 32) {
+                        // bits of the columns that the row sees
+                        const int from = min(max(lo - t0 - i0, 0), 32), upto = min(max(hi - t0 - i0, 0), 32);
+                        const uint32_t sees = static_cast<uint32_t>(((1ull << upto) - 1ull) & ~((1ull << from) - 1ull));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(sees >> i & 1u)) r[i0 + i] = 0xFF800000u;
+                    }
+                }
+                float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+                for (int i = 0; i < kTile; i += 8)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], fmaxf(__uint_as_float(r[i + 2 * j]), __uint_as_float(r[i + 2 * j + 1])));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rf;
+                float vmax = 0.0f;
+                if (CODES && masked) {
+#pragma unroll 1
+                    for (int i = max(lo - t0, 0); i < min(hi - t0, kTile); ++i) vmax = fmaxf(vmax, sv[i]);
+                } else if constexpr (CODES) {
                     const float4 x4 = *reinterpret_cast<const float4 *>(scales + S::kScaleSlots * 2 * kTile + sc.slot * 4);
                     vmax = fmaxf(fmaxf(x4.x, x4.y), fmaxf(x4.z, x4.w));
                 }
-                const auto tile = [&](auto masked) {
-                    constexpr bool MASK = decltype(masked)::value;
-                    // scores 32 columns at a time, times their keys' scales
-                    const auto scored = [&](int i0, uint32_t (&r)[32]) {
-                        if constexpr (CODES) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 k4 = *reinterpret_cast<const float4 *>(sk + i0 + i);
-                                float y[4];
-                                f2_split(f2_mul(f2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2(k4.x, k4.y)), y[0], y[1]);
-                                f2_split(f2_mul(f2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), f2(k4.z, k4.w)), y[2], y[3]);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) r[i + j] = __float_as_uint(y[j]);
-                            }
-                        }
-                        if constexpr (MASK) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (t0 + i0 + i < lo || t0 + i0 + i >= hi) r[i] = 0xFF800000u;
-                        }
-                    };
-                    if constexpr (MASK && CODES) {
-                        vmax = 0.0f;
-                        for (int i = max(lo - t0, 0); i < min(hi - t0, kTile); ++i) vmax = fmaxf(vmax, sv[i]);
+                const bool wide = CODES && vmax >= pow2(E);
+                if (__any_sync(0xFFFFFFFFu, top > m + kSlack || wide)) {
+                    const float n = fmaxf(m, top);
+                    float scale = m == neg_inf() ? 0.0f : exp2_fast(m - n);
+                    m = n;
+                    l *= scale;
+                    if (wide) {
+                        const int to = min(((__float_as_int(vmax) >> 23) & 255) - 126, 126);
+                        scale *= to - E > 126 ? 0.0f : pow2(E - to);
+                        E = to;
                     }
-                    float mx[2] = {neg_inf(), neg_inf()};
-                    uint32_t r[2][32];
-                    tmem_ld_32x32b_x32(s_at, r[0]);
-#pragma unroll
-                    for (int c = 0; c < kTile / 32; ++c) {
-                        tmem_wait_ld();
-                        // the next columns, and after the last ones the first again for the terms
-                        tmem_ld_32x32b_x32(s_at + (c + 1) % (kTile / 32) * 32, r[(c + 1) & 1]);
-                        scored(32 * c, r[c & 1]);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            mx[0] = fmaxf(mx[0], fmaxf(__uint_as_float(r[c & 1][i]), __uint_as_float(r[c & 1][i + 1])));
-                            mx[1] = fmaxf(mx[1], fmaxf(__uint_as_float(r[c & 1][i + 2]), __uint_as_float(r[c & 1][i + 3])));
-                        }
-                    }
-                    const float top = fmaxf(mx[0], mx[1]) * rf;
-                    const bool wide = CODES && vmax >= pow2(E);
-                    tmem_wait_ld();
-                    if (__any_sync(0xFFFFFFFFu, top > m + kSlack || wide)) {
-                        const float n = fmaxf(m, top);
-                        float scale = m == neg_inf() ? 0.0f : exp2_fast(m - n);
-                        m = n;
-                        l *= scale;
-                        if (wide) {
-                            const int to = min(((__float_as_int(vmax) >> 23) & 255) - 126, 126);
-                            scale *= to - E > 126 ? 0.0f : pow2(E - to);
-                            E = to;
-                        }
-                        if (t > w.from) {
+                    if (t > w.from) {
 #pragma unroll 1
-                            for (int i = 0; i < DP; i += 16) {
-                                uint32_t o[16];
-                                tmem_ld_32x32b_x16(o_at + i, o);
-                                tmem_wait_ld();
+                        for (int i = 0; i < DP; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(o_at + i, o);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale);
-                                tmem_st_32x32b_x16(o_at + i, o);
-                            }
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale);
+                            tmem_st_32x32b_x16(o_at + i, o);
                         }
                     }
-                    const float u = m == neg_inf() ? 0.0f : m - kLift;
-                    const F2 rf2 = f2(rf, rf), u2 = f2(-u, -u);
-                    [[maybe_unused]] const float down = CODES ? pow2(-E) : 1.0f;
-                    F2 sum = f2(0.0f, 0.0f), sum2 = sum;
+                }
+                const float u = m == neg_inf() ? 0.0f : m - kLift;
+                const F2 rf2 = f2(rf, rf), u2 = f2(-u, -u);
+                [[maybe_unused]] const float down = CODES ? pow2(-E) : 1.0f;
+                F2 sum = f2(0.0f, 0.0f), sum2 = sum;
+                // terms in the place of scores, in two parts: products start on the first
 #pragma unroll
-                    for (int c = 0; c < kTile / 32; ++c) {
-                        uint32_t(&x)[32] = r[c & 1];
-                        if (c > 0) tmem_wait_ld();
-                        // terms of these columns go where scores have been read already
-                        if (c + 1 < kTile / 32) tmem_ld_32x32b_x32(s_at + 32 * (c + 1), r[(c + 1) & 1]);
-                        scored(32 * c, x);
-                        uint32_t p[16];
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float e0, e1;
-                            f2_split(f2_fma(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), rf2, u2), e0, e1);
-                            e0 = exp2_fast(e0), e1 = exp2_fast(e1);
-                            if (i & 1) sum2 = f2_add(sum2, f2(e0, e1));
-                            else sum = f2_add(sum, f2(e0, e1));
-                            if constexpr (CODES) {
-                                // (below 1 where the row sees the token; finite times 0 where not)
-                                const float2 v2 = *reinterpret_cast<const float2 *>(sv + 32 * c + 2 * i);
-                                e0 *= fminf(v2.x * down, 1.0f), e1 *= fminf(v2.y * down, 1.0f);
-                            }
-                            p[i] = BF ? pack_bf16x2_rn(e0, e1) : pack_f16x2_rn(e0, e1);
+                    for (int i = 32 * h; i < 32 * h + 32; ++i) {
+                        float e0, e1;
+                        f2_split(f2_fma(f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), rf2, u2), e0, e1);
+                        e0 = exp2_fast(e0), e1 = exp2_fast(e1);
+                        if (i & 1) sum2 = f2_add(sum2, f2(e0, e1));
+                        else sum = f2_add(sum, f2(e0, e1));
+                        if constexpr (CODES) {
+                            // (below 1 where the row sees the token; finite times 0 where not)
+                            const float2 v2 = *reinterpret_cast<const float2 *>(sv + 2 * i);
+                            e0 *= fminf(v2.x * down, 1.0f), e1 *= fminf(v2.y * down, 1.0f);
                         }
-                        tmem_st_32x32b_x16(s_at + 16 * c, p);
+                        r[i] = BF ? pack_bf16x2_rn(e0, e1) : pack_f16x2_rn(e0, e1);
                     }
-                    l += f2_sum(f2_add(sum, sum2));
-                };
-                if (t0 + kTile > full_upto || t0 < full_from) tile(std::true_type{});
-                else tile(std::false_type{});
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bars->p_full[half]);
-                    if constexpr (CODES) mbar_arrive(&bars->scales_empty[sc.slot]);
+                    tmem_st_32x32b_x32(s_at + 32 * h, r + 32 * h);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->p_full[half][h]);
                 }
-                sc.step(S::kScaleSlots);
-                if (issues) {
-                    const bool more = t + 1 < w.upto;
-                    if (!warp_wait(&v_full[vt.slot], vt.phase, a.wait_ns) || !warp_wait(&bars->p_full[half], p_phase, a.wait_ns)) ok = false;
-                    if (ok) sums(t > w.from, !more);
-                    if (ok && more) {
-                        ok = warp_wait(&bars->k_full[kt.slot], kt.phase, a.wait_ns);
-                        if (ok) scores();
-                    }
-                    if (!ok) {
-                        fail();
-                        break;
-                    }
+                l += f2_sum(f2_add(sum, sum2));
+                if constexpr (CODES) {
+                    if (lane == 0) mbar_arrive(&bars->scales_empty[sc.slot]);
+                    sc.step(S::kScaleSlots);
                 }
-                p_phase ^= 1u;
             }
             if (!ok) break;
             // ------------------------------------------------ the item's end
@@ -427,35 +359,34 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             tc_fence_after();
             const bool whole = w.whole();
             const int slot = 2 * static_cast<int>(blockIdx.x) + (w.from == 0 ? 1 : 0);
-            const int r_in = half * kHalf + (warp & 3) * 32 + lane;
             float *part = a.parts + slot * attn_part_floats(kTensorRows, CH);
             const float back = CODES ? pow2(E) : 1.0f;
             const float mul = whole ? (l == 0.0f ? 0.0f : back / l) : back;
             const int i = my_row / a.group, head = w.h * a.group + my_row - i * a.group;
             const int64_t out = (static_cast<int64_t>(w.q.start) + i) * a.ldo + static_cast<int64_t>(head) * a.c.d;
-#pragma unroll
-            for (int c0 = 0; c0 < DP; c0 += 32) {
-                uint32_t o[32];
-                tmem_ld_32x32b_x32(o_at + c0, o);
+#pragma unroll 1
+            for (int c0 = 0; c0 < DP; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(o_at + c0, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * mul);
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * mul);
                 if (my_row >= w.q.rows) {
                     // nothing of this row is kept
                 } else if (!whole) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
+                    for (int j = 0; j < 16; j += 4)
                         *reinterpret_cast<uint4 *>(part + r_in * DP + c0 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
+                    for (int j = 0; j < 16; j += 8) {
                         if (c0 + j >= a.c.d) continue;
                         uint32_t v[4];
                         const bool bf = a.type == Q4_TYPE_BF16;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float x0 = __uint_as_float(o[j + 2 * k]), x1 = __uint_as_float(o[j + 2 * k + 1]);
-                            v[k] = bf ? pack_bf16x2_rn(x0, x1) : pack_f16x2_rn(x0, x1);
+                            const float x0f = __uint_as_float(o[j + 2 * k]), x1f = __uint_as_float(o[j + 2 * k + 1]);
+                            v[k] = bf ? pack_bf16x2_rn(x0f, x1f) : pack_f16x2_rn(x0f, x1f);
                         }
                         uint16_t *dst = static_cast<uint16_t *>(a.O) + out + c0 + j;
                         if (a.vec) {
@@ -475,14 +406,122 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             if (!whole && w.from == 0 && tid == 0) a.meta[blockIdx.x] = make_int4(w.s, w.h, w.b, w.parts());
             tc_fence_before();
         }
-        if (issues) {
+    } else if (warp >= (CODES ? S::kMmaWarp : 8)) {
+        reg_dec<S::kMmaRegs>();
+        if (warp == S::kMmaWarp) {
+            // ----------------------------------------------------- products
+            constexpr uint32_t type = BF ? idesc_bf16_f32(0, 0) : idesc_f16_f32(0, 0);
+            constexpr uint32_t id_s = type | idesc_f16_f32(kHalf, kTile), id_o = type | idesc_f16_f32(kHalf, DP) | kNMajorB;
+            const uint32_t d = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            const uint64_t q0 = smem_desc_sw128(smem_u32(qs)), k0 = smem_desc_sw128(smem_u32(ks));
+            const uint64_t v0 = desc_n_major(smem_u32(CODES ? ks : vs), kAtomRows);
+            uint64_t *const v_full = CODES ? bars->k_full : bars->v_full, *const v_empty = CODES ? bars->k_empty : bars->v_empty;
+            Turn kt, vt;                                               // K and V tiles in turn
+            if (CODES) vt.step(S::kK);                                 // ... of one ring
+            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            bool ok = true;
+            const auto wait = [&](uint64_t *bar, uint32_t phase) {
+                if (ok && !warp_wait<0>(bar, phase, a.wait_ns)) {
+                    fail();
+                    ok = false;
+                }
+                return ok;
+            };
+            // The MMA queue holds some 170 clocks of work, less than a wait and what follows
+            // it take: what the next group waits for is tested in the middle of a group, and
+            // waited for after it only if it was not there.
+            bool there = false;
+            const auto test = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, phase)) != 0; };
+            const auto wait_unless = [&](uint64_t *bar, uint32_t phase) { return there || wait(bar, phase); };
+            const auto scores = [&](int half, bool last_use, auto next) {   // of the K tile in turn
+                const uint64_t kd = k0 + static_cast<uint64_t>(static_cast<uint32_t>(kt.slot) * (S::kTileBytes >> 4));
+                const uint64_t qd = q0 + static_cast<uint64_t>(half * CH * (kAtomRows >> 4));
+                uint64_t *const freed = &bars->k_empty[kt.slot];
+                constexpr int kSteps = CH * 4;
+                tc_fence_after();
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = part * kSteps / 2; i < (part + 1) * kSteps / 2; ++i)
+                            tc_mma_f16(d + 128u * half, qd + i / 4 * (kAtomRows >> 4) + 2 * (i % 4), kd + i / 4 * (kAtomRows >> 4) + 2 * (i % 4), id_s,
+                                       i > 0 ? 1u : 0u);
+                        if (part == 1) {
+                            tc_commit(&bars->s_full[half]);
+                            if (last_use) tc_commit(freed);
+                        }
+                    }
+                    __syncwarp();
+                    if (part == 0) there = next();
+                }
+                if (last_use) {
+                    kt.step(S::kK);
+                    if (CODES) kt.step(S::kK);
+                }
+            };
+            const auto sums = [&](int half, bool add, bool last, bool last_use, auto next) {   // with the V tile in turn
+                const uint64_t vd = v0 + static_cast<uint64_t>(static_cast<uint32_t>(vt.slot) * (S::kTileBytes >> 4));
+                uint64_t *const freed = &v_empty[vt.slot];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 0 ? !wait_unless(&bars->p_full[half][0], p_phase[half]) : !wait(&bars->p_full[half][1], p_phase[half])) return;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 4 * h; i < 4 * h + 4; ++i)
+                            tc_mma_f16_ts(d + 256u + 128u * half, d + 128u * half + 8u * i, vd + i * (2048 >> 4), id_o, add || i > 0 ? 1u : 0u);
+                        if (h == 1) {
+                            if (last) tc_commit(&bars->s_full[half]);
+                            if (last_use) tc_commit(freed);
+                        }
+                    }
+                    __syncwarp();
+                    if (h == 0) there = next();
+                }
+                p_phase[half] ^= 1u;
+                if (last_use) {
+                    vt.step(CODES ? S::kK : S::kV);
+                    if (CODES) vt.step(S::kK);
+                }
+            };
+            const auto terms_there = [&] { return test(&v_full[vt.slot], vt.phase) && test(&bars->p_full[0][0], p_phase[0]); };
+            uint32_t flags = 0;                                        // of the tile
+            bool start = true;
+            for (int t = 0; ok && t < tiles; ++t) {
+                if (start) {
+                    // an item's first scores
+                    if (!wait(&bars->k_full[kt.slot], kt.phase)) break;
+                    flags = bars->flags[kt.slot];
+                    if (!wait(&bars->q_full[0], q_phase[0])) break;
+                    q_phase[0] ^= 1u;
+                    const bool two = (flags & kTwo) != 0;
+                    scores(0, !two, terms_there);
+                    if (two) {
+                        if (!wait(&bars->q_full[1], q_phase[1])) break;
+                        q_phase[1] ^= 1u;
+                        scores(1, true, terms_there);
+                    }
+                }
+                const bool more = (flags & kLast) == 0, two = (flags & kTwo) != 0, add = (flags & kFirst) == 0;
+                if (!there && !wait(&v_full[vt.slot], vt.phase)) break;
+                sums(0, add, !more, !two, [&] { return more ? test(&bars->k_full[kt.slot], kt.phase) : two && test(&bars->p_full[1][0], p_phase[1]); });
+                if (more) {
+                    if (!ok || !wait_unless(&bars->k_full[kt.slot], kt.phase)) break;
+                    flags = bars->flags[kt.slot];
+                    scores(0, !two, [&] { return two ? test(&bars->p_full[1][0], p_phase[1]) : terms_there(); });
+                }
+                if (two) {
+                    if (!ok) break;
+                    sums(1, add, !more, true, [&] { return false; });
+                    if (ok && more) scores(1, true, terms_there);
+                }
+                start = !more;
+            }
             // what was issued is done before tensor memory is given back
-            if (elect_one()) tc_commit(&bars->done[half]);
+            if (elect_one()) tc_commit(&bars->done);
             __syncwarp();
-            if (!warp_wait(&bars->done[half], 0u, landing_limit(a.wait_ns))) fail();
-        }
-    } else {
-        if constexpr (!CODES) {
+            if (!warp_wait(&bars->done, 0u, landing_limit(a.wait_ns))) fail();
+        } else if (!CODES && warp == S::kCopyWarp) {
             // ------------------------------------------------------- copies
             Turn kt, vt;
             long long issued = 0, landing_k = 0, landing_v = 0;        // tiles; those of keys and of values that copies were issued for
@@ -514,7 +553,10 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         }
                         ok = __all_sync(0xFFFFFFFFu, go) != 0;
                         if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(tokens * CH * 128));
+                        if (lane == 0) {
+                            if (kv == 0) bars->flags[tn.slot] = (t == w.from ? kFirst : 0u) | (t + 1 == w.upto ? kLast : 0u) | (both() ? kTwo : 0u);
+                            mbar_arrive_expect_tx(full, static_cast<uint32_t>(tokens * CH * 128));
+                        }
                         __syncwarp();
                         const int pieces = np * CH;
                         for (int x0 = 0; x0 < pieces; x0 += 32) {
@@ -542,12 +584,15 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             };
             land(bars->k_full, landing_k, S::kK);
             land(bars->v_full, landing_v, S::kV);
-        } else {
+        }
+    } else {
+        if constexpr (CODES) {
             // ---------------------------------------------- codes to fp16
+            reg_dec<S::kConvertRegs>();
             // Four warps; a thread has a 16-byte unit of eight rows of 64 codes (four at DP =
             // 64), fetched a tile of keys or values ahead of its conversion.
             constexpr int kUnits = CH * 4;
-            const int me = tid - kFeedWarp0 * 32, in_page = a.c.page_tokens;
+            const int me = tid - S::kConvertWarp0 * 32, in_page = a.c.page_tokens;
             const int unit = me & 3;
             Walk f = w;                                                // where the fetches are
             int f_t = f.from, f_kv = 0;
@@ -614,12 +659,13 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         scales[sc.slot * (2 * kTile) + kv * kTile + me] = scale;
                         if (kv == 1) {
                             const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(scale) & 0x7FFFFFFFu);
-                            if (lane == 0) scales[S::kScaleSlots * 2 * kTile + sc.slot * 4 + warp - kFeedWarp0] = __uint_as_float(largest);
+                            if (lane == 0) scales[S::kScaleSlots * 2 * kTile + sc.slot * 4 + warp - S::kConvertWarp0] = __uint_as_float(largest);
                         }
                         scale = scale_src ? *scale_src : 0.0f;
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
+                            if (kv == 0 && me == 0) bars->flags[kt.slot] = (t == w.from ? kFirst : 0u) | (t + 1 == w.upto ? kLast : 0u) | (both() ? kTwo : 0u);
                             mbar_arrive(&bars->k_full[kt.slot]);
                             if (kv == 1) mbar_arrive(&bars->scales_full[sc.slot]);
                         }
@@ -635,7 +681,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, 512u);
+    if (warp == S::kMmaWarp) tmem_dealloc(tmem, 512u);
 }
 
 template <int KIND, int DP> cudaError_t launch(const AttnArgs &args, int sm_count, cudaStream_t s, int *ctas)
@@ -645,6 +691,13 @@ template <int KIND, int DP> cudaError_t launch(const AttnArgs &args, int sm_coun
     static_assert(TensorShape<KIND, DP>::kSmem <= kSmemOptIn, "shared memory");
     cudaError_t e = set_max_smem(f, TensorShape<KIND, DP>::kSmem);
     if (e != cudaSuccess) return e;
+    // the warpgroups' registers have to add up to what the launch has
+    static const bool enough = [f] {
+        using S = TensorShape<KIND, DP>;
+        cudaFuncAttributes fa{};
+        return cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs * S::kThreads >= S::kAllRegs;
+    }();
+    if (!enough) return cudaErrorLaunchOutOfResources;
     *ctas = std::min(kAttnMaxCtas / 2, sm_count);
     void *p[] = {&a};
     return launch_pdl(f, dim3(static_cast<unsigned>(*ctas)), dim3(TensorShape<KIND, DP>::kThreads), TensorShape<KIND, DP>::kSmem, s, p);
