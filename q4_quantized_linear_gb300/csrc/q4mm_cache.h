@@ -105,6 +105,8 @@ struct ProbsArgs {
     int64_t ldp, ldx;
     const float *temperature;
     int64_t rows, n;
+    int *status;
+    uint64_t wait_ns;
 };
 cudaError_t launch_token_probs(const ProbsArgs &a, int type, int sm_count, cudaStream_t s);
 

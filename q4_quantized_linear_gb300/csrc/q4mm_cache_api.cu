@@ -216,7 +216,7 @@ Q4MM_API int q4_token_probs(float *P, int64_t ldp, const void *logits, int64_t l
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != Q4_OK) return rc;
-    const ProbsArgs a{P, logits, ldp, ldl, temperature, rows, n};
+    const ProbsArgs a{P, logits, ldp, ldl, temperature, rows, n, dev.status, wait_limit()};
     return guarded([&] { return cuda_status(launch_token_probs(a, type, dev.sm_count, as_stream(stream))); });
 }
 

@@ -3,9 +3,7 @@
 //
 // Both read rows as long as the vocabulary, few of them at a time, so a
 // thread-block cluster takes a row: each CTA a contiguous segment, and the CTAs'
-// sums meet in shared memory. The probabilities' values stay in registers between
-// the pass that needs the row's sum and the one that uses it (what a longer row
-// has beyond them is read again): a row is read once and written once.
+// sums meet in shared memory.
 #include <algorithm>
 
 #include "q4mm_cache.h"
@@ -14,8 +12,7 @@
 namespace q4 {
 namespace {
 
-constexpr int kMaxThreads = 1024, kMaxCluster = 8;
-constexpr int kHeldValues = 32;            // of a thread, in registers
+constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -37,6 +34,10 @@ template <bool SUM> __device__ __forceinline__ float block_reduce(float v, float
     for (int i = 1; i < static_cast<int>(blockDim.x) / 32; ++i) v = SUM ? v + buf[i] : fmaxf(v, buf[i]);
     return v;
 }
+// Says that this CTA runs; cluster_wait: that all do, so that their shared memory may
+// be written.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // To the same place in CTA `rank` of the cluster.
 __device__ __forceinline__ void put_far(const unsigned long long *here, uint32_t rank, unsigned long long v)
 {
@@ -67,90 +68,136 @@ struct Segment {
 
 // --------------------------------------------------------- probabilities --
 
-template <typename T, int V> __global__ void __launch_bounds__(kMaxThreads) probs_kernel(const ProbsArgs a, const int cluster)
+constexpr int kProbsThreads = 256;
+constexpr int kProbsBytes = 80 * 1024;     // of a segment, in shared memory at once
+
+// P = 2^((x - max) f) / sum, f = log2(e) / T. A segment comes into shared memory by one
+// bulk copy (of the aligned 16-byte words that hold some of it: a row starts
+// anywhere) and is looked at twice: for a running maximum and sum a thread, and for the
+// results. So a row is read once and written once (a segment past kProbsBytes is
+// copied piece by piece, and again for the results). Several CTAs an SM cover one
+// another's waits: 320 rows of 151936 bf16 by 1024 threads that held values in
+// registers, one CTA an SM, 205 us.
+template <typename T> __global__ void __launch_bounds__(kProbsThreads) probs_kernel(const ProbsArgs a, const int cluster)
 {
-    constexpr int NV = kHeldValues / V;
+    constexpr int V = 16 / sizeof(T);
+    extern __shared__ __align__(128) uint8_t piece[];
     __shared__ float buf[32];
     __shared__ unsigned long long all[kMaxCluster], first[kMaxCluster];
     __shared__ unsigned int lowest;
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_barrier_init();
+    }
     pdl_wait();
     pdl_launch_dependents();
     const uint32_t rank = cluster > 1 ? cluster_ctarank() : 0u;
-    if (cluster > 1) cluster_sync();   // every CTA runs before anything is written into its shared memory
+    if (cluster > 1) cluster_arrive();
+    __syncthreads();
     const int64_t row = blockIdx.x / cluster;
     const T *x = static_cast<const T *>(a.X) + row * a.ldx;
-    float *p = a.P + row * a.ldp;
     const Segment seg(a.n, cluster, rank);
-    const int step = static_cast<int>(blockDim.x) * V;
-    const float temperature = a.temperature ? a.temperature[row] : 1.0f;
+    const int tid = threadIdx.x;
     const float inf = __int_as_float(0x7F800000);
-    float v[NV][V];
-    float m = -inf;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int64_t c = seg.lo + static_cast<int64_t>(i) * step + threadIdx.x * V;
-        if (c < seg.hi) {
-            const Pack<T, V> u = load_pack<T, V>(x, c, seg.hi);
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] = c + j < seg.hi ? elem(u, j) : -inf;
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] = -inf;
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(x + seg.lo), end = reinterpret_cast<uintptr_t>(x + seg.hi);
+    const uintptr_t base = begin & ~uintptr_t(15);
+    const int64_t words = seg.hi > seg.lo ? static_cast<int64_t>((end - base + 15) / 16) : 0;
+    const int64_t e0 = seg.lo - static_cast<int64_t>(begin - base) / static_cast<int64_t>(sizeof(T));   // the element at `base`
+    const int64_t piece_words = kProbsBytes / 16;
+    const int pieces = static_cast<int>((words + piece_words - 1) / piece_words);
+    uint32_t phase = 0;
+    bool ok = true;
+    // f(first word, words) of each piece, in shared memory
+    const auto over = [&](bool again, auto f) {
+        for (int i = 0; i < pieces; ++i) {
+            const int64_t w0 = i * piece_words;
+            const int n = static_cast<int>(min(piece_words, words - w0));
+            if (!again || pieces > 1) {
+                __syncthreads();                             // the piece before has been read
+                if (tid == 0) {
+                    mbar_arrive_expect_tx(&bar, static_cast<uint32_t>(n) * 16u);
+                    bulk_g2s(piece, reinterpret_cast<const void *>(base + w0 * 16), static_cast<uint32_t>(n) * 16u, &bar);
+                }
+                if (!mbar_wait(&bar, phase, landing_limit(a.wait_ns))) {
+                    record_status(a.status, kErrTimeout);
+                    ok = false;
+                }
+                phase ^= 1u;
+            }
+            f(w0, n);
         }
-    }
+    };
+    const auto word = [&](int w) {
+        Pack<T, V> p;
+        const uint4 u = lds128(piece + 16 * w);
+        p.w[0] = u.x, p.w[1] = u.y, p.w[2] = u.z, p.w[3] = u.w;
+        return p;
+    };
+    const float temperature = a.temperature ? a.temperature[row] : 1.0f;
+    const bool greedy = temperature == 0.0f;
+    const float f = temperature > 0.0f ? __fdiv_rn(1.4426950408889634f, temperature) : __int_as_float(0x7FC00000);
+    float m = -inf, s = 0.0f;
+    over(false, [&](int64_t w0, int n) {
+        for (int w = tid; w < n; w += kProbsThreads) {
+            const Pack<T, V> p = word(w);
+            const int64_t e = e0 + (w0 + w) * V;
+            float v[V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+            for (int j = 0; j < V; ++j) v[j] = elem(p, j);
+            if (e < seg.lo || e + V > seg.hi) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) m = fmaxf(m, v[i][j]);
-    const int64_t rest = seg.lo + static_cast<int64_t>(NV) * step + threadIdx.x * V;
-    for (int64_t c = rest; c < seg.hi; c += step) {
-        const Pack<T, V> u = load_pack<T, V>(x, c, seg.hi);
+                for (int j = 0; j < V; ++j)
+                    if (e + j < seg.lo || e + j >= seg.hi) v[j] = -inf;
+            }
+            float top = v[0];
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (c + j < seg.hi) m = fmaxf(m, elem(u, j));
-    }
+            for (int j = 1; j < V; ++j) top = fmaxf(top, v[j]);
+            if (greedy) {
+                m = fmaxf(m, top);
+                continue;
+            }
+            if (top > m) {
+                s *= m == -inf ? 1.0f : exp2_fast((m - top) * f);   // (s: 0 or NaN so far where m is -inf)
+                m = top;
+            }
+            const float from = m == -inf ? 0.0f : m;
+#pragma unroll
+            for (int j = 0; j < V; ++j) s += exp2_fast((v[j] - from) * f);
+        }
+    });
+    const float mine = m;
     m = block_reduce<false>(m, buf);
-    if (temperature == 0.0f) {
+    float *p = a.P + row * a.ldp;
+    if (greedy) {
         // the largest value, the lowest of its places
-        if (threadIdx.x == 0) lowest = 0xFFFFFFFFu;
+        if (tid == 0) lowest = 0xFFFFFFFFu;
         __syncthreads();
         unsigned int at = 0xFFFFFFFFu;
         if (m > -inf)
-            for (int64_t c = seg.lo + threadIdx.x * V; c < seg.hi; c += step) {
-                const Pack<T, V> u = load_pack<T, V>(x, c, seg.hi);
+            over(true, [&](int64_t w0, int n) {
+                for (int w = tid; w < n; w += kProbsThreads) {
+                    const Pack<T, V> u = word(w);
+                    const int64_t e = e0 + (w0 + w) * V;
 #pragma unroll
-                for (int j = V - 1; j >= 0; --j)
-                    if (c + j < seg.hi && elem(u, j) == m) at = min(at, static_cast<unsigned int>(c + j));
-            }
+                    for (int j = V - 1; j >= 0; --j)
+                        if (e + j >= seg.lo && e + j < seg.hi && elem(u, j) == m) at = min(at, static_cast<unsigned int>(e + j));
+                }
+            });
         atomicMin(&lowest, at);
         __syncthreads();
+        if (cluster > 1) cluster_wait();
         exchange(first, static_cast<unsigned long long>(lowest) << 32 | __float_as_uint(m), rank, cluster);
         float best = -inf;
         for (int i = 0; i < cluster; ++i) best = fmaxf(best, __uint_as_float(static_cast<uint32_t>(first[i])));
         at = 0xFFFFFFFFu;
         for (int i = 0; i < cluster; ++i)
             if (__uint_as_float(static_cast<uint32_t>(first[i])) == best) at = min(at, static_cast<unsigned int>(first[i] >> 32));
-        for (int64_t c = seg.lo + threadIdx.x; c < seg.hi; c += blockDim.x) p[c] = c == at ? 1.0f : 0.0f;
+        for (int64_t c = seg.lo + tid; c < seg.hi; c += kProbsThreads) p[c] = c == at ? 1.0f : 0.0f;
         return;
     }
-    // 2^((x - m) f); nothing but -inf: zeros
-    const float f = temperature > 0.0f ? __fdiv_rn(1.4426950408889634f, temperature) : __int_as_float(0x7FC00000);
-    const float base = m == -inf ? 0.0f : m;
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            v[i][j] = exp2_fast((v[i][j] - base) * f);
-            s += v[i][j];
-        }
-    for (int64_t c = rest; c < seg.hi; c += step) {
-        const Pack<T, V> u = load_pack<T, V>(x, c, seg.hi);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (c + j < seg.hi) s += exp2_fast((elem(u, j) - base) * f);
-    }
-    s = block_reduce<true>(s, buf);
+    s = block_reduce<true>(mine == -inf || mine == m ? s : s * exp2_fast((mine - m) * f), buf);
+    if (cluster > 1) cluster_wait();
     exchange(all, static_cast<unsigned long long>(__float_as_uint(s)) << 32 | __float_as_uint(m), rank, cluster);
     float best = -inf, total = 0.0f;
     for (int i = 0; i < cluster; ++i) best = fmaxf(best, __uint_as_float(static_cast<uint32_t>(all[i])));
@@ -158,40 +205,51 @@ template <typename T, int V> __global__ void __launch_bounds__(kMaxThreads) prob
         const float mi = __uint_as_float(static_cast<uint32_t>(all[i]));
         total += __uint_as_float(static_cast<uint32_t>(all[i] >> 32)) * (mi == best || mi == -inf ? 1.0f : exp2_fast((mi - best) * f));
     }
-    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-    const float scale = (m == best || m == -inf ? 1.0f : exp2_fast((m - best) * f)) * inv;
+    if (!ok) total = __int_as_float(0x7FC00000);
+    // nothing but -inf: zeros
+    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total), from = best == -inf ? 0.0f : best;
+    // whole vectors of results where they start on 16 bytes as the words of x do
+    const bool vec = ((reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(e0) * 4) & 15) == 0;
+    over(true, [&](int64_t w0, int n) {
+        if (vec) {
+            for (int w = tid; w < n; w += kProbsThreads) {
+                const Pack<T, V> u = word(w);
+                const int64_t e = e0 + (w0 + w) * V;
+                float v[V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int64_t c = seg.lo + static_cast<int64_t>(i) * step + threadIdx.x * V;
-        if (c >= seg.hi) continue;
-        if constexpr (V == 1) {
-            p[c] = v[i][0] * scale;
+                for (int j = 0; j < V; ++j) v[j] = exp2_fast((elem(u, j) - from) * f) * inv;
+                if (e >= seg.lo && e + V <= seg.hi) {
+#pragma unroll
+                    for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(p + e + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (e + j >= seg.lo && e + j < seg.hi) p[e + j] = v[j];
+                }
+            }
         } else {
-#pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                const float w[4] = {v[i][j] * scale, v[i][j + 1] * scale, v[i][j + 2] * scale, v[i][j + 3] * scale};
-                if (c + j < seg.hi) store_pack<float, 4>(p, c + j, seg.hi, pack_of<float, 4>(w));
+            const T *values = reinterpret_cast<const T *>(piece);
+            const int64_t at = e0 + w0 * V;
+            for (int i = tid; i < n * V; i += kProbsThreads) {
+                const int64_t e = at + i;
+                if (e >= seg.lo && e < seg.hi) p[e] = exp2_fast((elem(load_pack<T, 1>(values, i, n * V), 0) - from) * f) * inv;
             }
         }
-    }
-    for (int64_t c = rest; c < seg.hi; c += step) {
-        const Pack<T, V> u = load_pack<T, V>(x, c, seg.hi);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (c + j < seg.hi) p[c + j] = exp2_fast((elem(u, j) - base) * f) * scale;
-    }
+    });
 }
 
-template <typename T, int V> cudaError_t launch_probs(ProbsArgs a, int sm_count, cudaStream_t s)
+template <typename T> cudaError_t launch_probs(ProbsArgs a, int sm_count, cudaStream_t s)
 {
-    // as many CTAs a row as fill the device, while each has some work
-    int cluster = 1, threads = 128;
-    while (cluster < kMaxCluster && (a.n / cluster > kMaxThreads * kHeldValues || (a.rows * cluster < 2 * sm_count && a.n / cluster > 4096)))
-        cluster *= 2;
-    while (threads < kMaxThreads && a.n / cluster > threads * 16) threads *= 2;
+    // CTAs enough for four an SM while each has some work, and segments that fit
+    int cluster = 1;
+    const auto bytes = [&] { return static_cast<int64_t>(sizeof(T)) * ceil_div(a.n, cluster); };
+    while (cluster < kMaxCluster && (bytes() > kProbsBytes / 2 || (a.rows * cluster < 4 * sm_count && a.n / cluster > 4096))) cluster *= 2;
+    const size_t smem = static_cast<size_t>(std::min<int64_t>(kProbsBytes, round_up(bytes() + 8 * static_cast<int64_t>(sizeof(T)) + 32, 128)));
+    const void *f = reinterpret_cast<const void *>(&probs_kernel<T>);
+    const cudaError_t e = set_max_smem(f, kProbsBytes);
+    if (e != cudaSuccess) return e;
     void *args[] = {&a, &cluster};
-    return launch_pdl(reinterpret_cast<const void *>(&probs_kernel<T, V>), dim3(static_cast<unsigned>(a.rows * cluster)),
-                      dim3(static_cast<unsigned>(threads)), 0, s, args, cluster);
+    return launch_pdl(f, dim3(static_cast<unsigned>(a.rows * cluster)), dim3(kProbsThreads), smem, s, args, cluster);
 }
 
 // ---------------------------------------------------------- verification --
@@ -202,7 +260,13 @@ template <typename T, int V> cudaError_t launch_probs(ProbsArgs a, int sm_count,
 // token, on any number of CTAs.
 __device__ __forceinline__ unsigned long long fixed60(float p)
 {
-    return __float2ull_rn(fminf(fmaxf(p, 0.0f), 1.0f) * 1152921504606846976.0f);   // (NaN: 0)
+    // mantissa 2^(exponent - 150 + 60), the exponent at most 127 (a conversion to 64-bit
+    // integers costs several times as much)
+    const uint32_t bits = __float_as_uint(fminf(fmaxf(p, 0.0f), 1.0f));   // (NaN: 0)
+    const unsigned long long top = static_cast<unsigned long long>((bits & 0x7FFFFFu) | 0x800000u) << 37;
+    unsigned long long v;
+    asm("shr.b64 %0, %1, %2;" : "=l"(v) : "l"(top), "r"(127u - (bits >> 23)));   // (past 63: 0)
+    return v;
 }
 // floor(u r), 0 <= u < 1.
 __device__ __forceinline__ unsigned long long share_of(float u, unsigned long long r)
@@ -217,37 +281,66 @@ __device__ __forceinline__ unsigned long long share_of(float u, unsigned long lo
     return e < 128 ? hi >> (e - 64) : 0ull;
 }
 
-constexpr int kVerifyThreads = 512;
-constexpr int kMaxSpans = 4096;            // spans of a warp's access in a CTA's segment
+constexpr int kVerifyThreads = 1024, kVerifyWarps = kVerifyThreads / 32;   // at most
 
 struct Rest {
     const float *p, *q;
     int64_t known;                         // without q: the token the draft was sure of (-1: none)
     int64_t hi;
-    template <int V> __device__ __forceinline__ void at(int64_t c, unsigned long long (&r)[V]) const
+    template <int V> __device__ __forceinline__ void load(int64_t c, Pack<float, V> &x, Pack<float, V> &y) const
     {
-        const Pack<float, V> x = load_pack<float, V>(p, c, hi);
-        Pack<float, V> y = zero_pack<float, V>();
+        x = zero_pack<float, V>(), y = x;
+        if (c >= hi) return;
+        x = load_pack<float, V>(p, c, hi);
         if (q) y = load_pack<float, V>(q, c, hi);
+    }
+    // what is left of elements c ..
+    template <int V> __device__ __forceinline__ void of(int64_t c, const Pack<float, V> &x, const Pack<float, V> &y, unsigned long long (&r)[V]) const
+    {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const unsigned long long a = fixed60(elem(x, j)), b = fixed60(elem(y, j));
-            r[j] = c + j >= hi || a <= b || c + j == known ? 0ull : a - b;
+            r[j] = a <= b || c + j == known ? 0ull : a - b;
         }
     }
 };
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long s)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    return s;
+}
+// The first of n sums (a lane each) at which the running sum from `run` on passes
+// `target`, and the running sum before it. n - 1 if none does.
+__device__ __forceinline__ int find(unsigned long long own, int n, unsigned long long target, unsigned long long &run)
+{
+    const int lane = threadIdx.x % 32;
+    unsigned long long v = lane < n ? own : 0ull;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
+    }
+    const unsigned past = __ballot_sync(0xFFFFFFFFu, lane < n && run + v > target);
+    const int at = past ? __ffs(past) - 1 : n - 1;
+    const unsigned long long before = __shfl_sync(0xFFFFFFFFu, v, at > 0 ? at - 1 : 0);
+    if (at > 0) run += before;
+    return at;
+}
 
+// A CTA's segment is cut into a contiguous stretch a warp: the sums of stretches need
+// one reduction each. The CTA that holds the drawn place then cuts the warp's stretch
+// among its warps in the same way, until a warp's access holds it.
 template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs a, const int cluster)
 {
-    __shared__ unsigned long long spans[kMaxSpans], sums[2][kMaxCluster];
+    __shared__ unsigned long long spans[kVerifyWarps], sums[2][kMaxCluster];
     __shared__ int kept_shared;
     pdl_wait();
     pdl_launch_dependents();
     const uint32_t rank = cluster > 1 ? cluster_ctarank() : 0u;
-    if (cluster > 1) cluster_sync();   // every CTA runs before anything is written into its shared memory
+    if (cluster > 1) cluster_arrive();
     const int64_t seq = blockIdx.x / cluster;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    constexpr int kWarps = kVerifyThreads / 32;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, warps = blockDim.x / 32;
     const int count = a.counts ? min(max(a.counts[seq], 0), a.max_draft) : a.max_draft;
     if (warp == 0) {
         int kept = count;
@@ -255,11 +348,12 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
             const int i = i0 + lane;
             bool stays = false;
             if (i < count) {
+                const float u = a.accept[seq * a.lda + i];
                 const int64_t x = a.drafted[seq * a.ldd + i];
                 if (x >= 0 && x < a.n) {
                     const double px = a.P[(seq * (a.max_draft + 1) + i) * a.ldp + x];
                     const double qx = a.Q ? static_cast<double>(a.Q[(seq * a.max_draft + i) * a.ldq + x]) : 1.0;
-                    stays = static_cast<double>(a.accept[seq * a.lda + i]) * qx < px;   // the product is exact
+                    stays = static_cast<double>(u) * qx < px;   // the product is exact
                 }
             }
             const unsigned gone = __ballot_sync(0xFFFFFFFFu, i < count && !stays);
@@ -270,6 +364,7 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
         }
         if (lane == 0) kept_shared = kept;
     }
+    const float u = a.sample[seq];
     __syncthreads();
     const int kept = kept_shared;
     const bool refused = kept < count;
@@ -279,85 +374,85 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
     rest.q = refused && a.Q ? a.Q + (seq * a.max_draft + kept) * a.ldq : nullptr;
     rest.known = refused && !a.Q ? a.drafted[seq * a.ldd + kept] : -1;
     rest.hi = seg.hi;
-    const int64_t step = static_cast<int64_t>(kVerifyThreads) * V;
-    unsigned long long total = 0;
-    // once; and once more, of p alone, where the draft leaves nothing of it
-    for (int turn = 0; turn < 2; ++turn) {
-        int i = 0;
-        for (int64_t c0 = seg.lo; c0 < seg.hi; c0 += step, ++i) {
-            unsigned long long r[V], s = 0;
-            const int64_t c = c0 + tid * V;
-            if (c < seg.hi) {
-                rest.at<V>(c, r);
+    // a stretch of `per` elements (whole vectors) from lo on, a warp each; its sum
+    const auto stretch = [&](int64_t lo, int64_t per, int64_t hi) {
+        const int64_t from = lo + warp * per, to = min(from + per, hi);
+        unsigned long long s = 0;
+        constexpr int kAhead = 4;          // accesses in flight
+        for (int64_t c0 = from + lane * V; c0 - lane * V < to; c0 += kAhead * 32 * V) {
+            Pack<float, V> x[kAhead], y[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int64_t c = c0 + i * 32 * V;
+                rest.load<V>(c < to ? c : rest.hi, x[i], y[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                unsigned long long r[V];
+                rest.of<V>(c0 + i * 32 * V, x[i], y[i], r);
 #pragma unroll
                 for (int j = 0; j < V; ++j) s += r[j];
             }
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            if (lane == 0) spans[i * kWarps + warp] = s;
         }
-        const int n_spans = i * kWarps;
+        s = warp_sum(s);
+        if (lane == 0) spans[warp] = s;
+    };
+    const auto share = [&](int64_t n) { return ((n + warps - 1) / warps + 7) / 8 * 8; };
+    unsigned long long total = 0;
+    // once; and once more, of p alone, where the draft leaves nothing of it
+    for (int turn = 0; turn < 2; ++turn) {
+        int64_t lo = seg.lo, hi = seg.hi, per = share(hi - lo);
+        stretch(lo, per, hi);
         __syncthreads();
-        unsigned long long mine = 0;
-        for (int k = lane; k < n_spans; k += 32) mine += spans[k];
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+        const unsigned long long mine = warp_sum(lane < warps ? spans[lane] : 0ull);
+        if (cluster > 1 && turn == 0) cluster_wait();
         exchange(sums[turn], mine, rank, cluster);
         total = 0;
         for (int k = 0; k < cluster; ++k) total += sums[turn][k];
         if (total > 0 || turn == 1 || (!rest.q && rest.known < 0)) {
-            unsigned long long target = share_of(a.sample[seq], total), before = 0;
+            unsigned long long target = share_of(u, total), before = 0;
             for (int k = 0; k < static_cast<int>(rank); ++k) before += sums[turn][k];
             // the one CTA whose segment holds the place, and CTA 0 where there is none
             const bool here = total > 0 ? target >= before && target - before < sums[turn][rank] : rank == 0;
-            if (here && warp == 0) {
-                int64_t token = 0;
-                if (total > 0) {
-                    target -= before;
-                    unsigned long long run = 0;
-                    int k0 = 0;
-                    for (; k0 < n_spans; k0 += 32) {
-                        unsigned long long v = k0 + lane < n_spans ? spans[k0 + lane] : 0ull;
-#pragma unroll
-                        for (int o = 1; o < 32; o *= 2) {
-                            const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-                            if (lane >= o) v += u;
-                        }
-                        const unsigned past = __ballot_sync(0xFFFFFFFFu, run + v > target);
-                        if (past) {
-                            const int at = __ffs(past) - 1;
-                            const unsigned long long upto = __shfl_sync(0xFFFFFFFFu, v, at > 0 ? at - 1 : 0);
-                            if (at > 0) run += upto;
-                            k0 += at;
-                            break;
-                        }
-                        run += __shfl_sync(0xFFFFFFFFu, v, 31);
-                    }
-                    const int64_t c = seg.lo + (static_cast<int64_t>(k0) * 32 + lane) * V;
-                    unsigned long long r[V] = {}, s = 0;
-                    if (c < seg.hi) rest.at<V>(c, r);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) s += r[j];
-                    unsigned long long v = s;
-#pragma unroll
-                    for (int o = 1; o < 32; o *= 2) {
-                        const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-                        if (lane >= o) v += u;
-                    }
-                    run += v - s;                            // before this lane
-                    int found = 0x7FFFFFFF;
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        run += r[j];
-                        if (run > target && found == 0x7FFFFFFF) found = lane * V + j;
-                    }
-                    found = __reduce_min_sync(0xFFFFFFFFu, found);
-                    token = min(seg.lo + static_cast<int64_t>(k0) * 32 * V + found, a.n - 1);
+            if (!here) return;
+            int64_t token = 0;
+            if (total > 0) {
+                target -= before;
+                unsigned long long run = 0;
+                // every warp finds the stretch that holds the place, and takes its part of it
+                while (true) {
+                    const int at = find(lane < warps ? spans[lane] : 0ull, warps, target, run);
+                    lo += at * per, hi = min(lo + per, hi);
+                    if (per <= 32 * V) break;
+                    per = share(hi - lo);
+                    __syncthreads();
+                    stretch(lo, per, hi);
+                    __syncthreads();
                 }
-                for (int j = lane; j <= a.max_draft; j += 32)
-                    a.tokens[seq * a.ldt + j] = j < kept ? a.drafted[seq * a.ldd + j] : j == kept ? static_cast<int32_t>(token) : -1;
-                if (lane == 0) a.kept[seq] = kept;
+                if (warp != 0) return;
+                Pack<float, V> x, y;
+                const int64_t c = lo + lane * V;
+                rest.load<V>(c < hi ? c : rest.hi, x, y);
+                unsigned long long r[V], s = 0;
+                rest.of<V>(c, x, y, r);
+#pragma unroll
+                for (int j = 0; j < V; ++j) s += r[j];
+                const int at = find(s, 32, target, run);
+                int found = 0;
+#pragma unroll
+                for (int j = V - 1; j >= 0; --j) {
+                    unsigned long long upto = run;
+#pragma unroll
+                    for (int k = 0; k <= j; ++k) upto += r[k];
+                    if (upto > target) found = j;
+                }
+                found = __shfl_sync(0xFFFFFFFFu, found, at);
+                token = min(lo + at * V + found, a.n - 1);
             }
+            if (warp != 0) return;
+            for (int j = lane; j <= a.max_draft; j += 32)
+                a.tokens[seq * a.ldt + j] = j < kept ? a.drafted[seq * a.ldd + j] : j == kept ? static_cast<int32_t>(token) : -1;
+            if (lane == 0) a.kept[seq] = kept;
             return;
         }
         rest.q = nullptr;
@@ -366,36 +461,35 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
     }
 }
 
-template <int V> cudaError_t launch_verify(VerifyArgs a, cudaStream_t s)
+template <int V> cudaError_t launch_verify(VerifyArgs a, int sm_count, cudaStream_t s)
 {
     int cluster = kMaxCluster;
     while (cluster > 1 && a.n / cluster < 2048) cluster /= 2;
+    // few CTAs: many threads each, to have a segment in flight at once; many: small ones,
+    // which all fit at once (64 slots: 512 threads 71 us)
+    const unsigned threads = a.n_seq * cluster > sm_count ? 256 : kVerifyThreads;
     void *args[] = {&a, &cluster};
-    return launch_pdl(reinterpret_cast<const void *>(&verify_kernel<V>), dim3(static_cast<unsigned>(a.n_seq * cluster)),
-                      dim3(kVerifyThreads), 0, s, args, cluster);
+    return launch_pdl(reinterpret_cast<const void *>(&verify_kernel<V>), dim3(static_cast<unsigned>(a.n_seq * cluster)), dim3(threads), 0, s,
+                      args, cluster);
 }
 
 } // namespace
 
 cudaError_t launch_token_probs(const ProbsArgs &a, int type, int sm_count, cudaStream_t s)
 {
-    RowAlign al;
-    al.add(a.X, a.ldx * type_size(type));
-    al.add(a.P, a.ldp * 4);
-    const bool vec = al.bytes() == 16;
     switch (type) {
-    case Q4_TYPE_F32: return vec ? launch_probs<float, 4>(a, sm_count, s) : launch_probs<float, 1>(a, sm_count, s);
-    case Q4_TYPE_F16: return vec ? launch_probs<__half, 8>(a, sm_count, s) : launch_probs<__half, 1>(a, sm_count, s);
-    default: return vec ? launch_probs<__nv_bfloat16, 8>(a, sm_count, s) : launch_probs<__nv_bfloat16, 1>(a, sm_count, s);
+    case Q4_TYPE_F32: return launch_probs<float>(a, sm_count, s);
+    case Q4_TYPE_F16: return launch_probs<__half>(a, sm_count, s);
+    default: return launch_probs<__nv_bfloat16>(a, sm_count, s);
     }
 }
 
-cudaError_t launch_draft_verify(const VerifyArgs &a, int, cudaStream_t s)
+cudaError_t launch_draft_verify(const VerifyArgs &a, int sm_count, cudaStream_t s)
 {
     RowAlign al;
     al.add(a.P, a.ldp * 4);
     al.add(a.Q, a.ldq * 4);
-    return al.bytes() == 16 ? launch_verify<4>(a, s) : launch_verify<1>(a, s);
+    return al.bytes() == 16 ? launch_verify<4>(a, sm_count, s) : launch_verify<1>(a, sm_count, s);
 }
 
 } // namespace q4
