@@ -5,6 +5,7 @@
 // thread-block cluster takes a row: each CTA a contiguous segment, and the CTAs'
 // sums meet in shared memory.
 #include <algorithm>
+#include <type_traits>
 
 #include "q4mm_cache.h"
 #include "q4mm_rows.cuh"
@@ -254,20 +255,35 @@ template <typename T> cudaError_t launch_probs(ProbsArgs a, int sm_count, cudaSt
 
 // ---------------------------------------------------------- verification --
 
-// The draw is by whole numbers: probabilities in steps of 2^-60 (exact from
-// 2^-36 on), their sums exact whatever the order, and the place of u times the
-// sum is found without a rounding; so the same numbers always give the same
-// token, on any number of CTAs.
-__device__ __forceinline__ unsigned long long fixed60(float p)
-{
-    // mantissa 2^(exponent - 150 + 60), the exponent at most 127 (a conversion to 64-bit
-    // integers costs several times as much)
-    const uint32_t bits = __float_as_uint(fminf(fmaxf(p, 0.0f), 1.0f));   // (NaN: 0)
-    const unsigned long long top = static_cast<unsigned long long>((bits & 0x7FFFFFu) | 0x800000u) << 37;
-    unsigned long long v;
-    asm("shr.b64 %0, %1, %2;" : "=l"(v) : "l"(top), "r"(127u - (bits >> 23)));   // (past 63: 0)
-    return v;
-}
+// The draw is by whole numbers: probabilities in steps of 2^-60 (exact from 2^-36
+// on), their sums exact whatever the order, and the place of u times the sum is
+// found without a rounding; so the same numbers always give the same token, on any
+// number of CTAs.
+//   A probability x is cut into steps of 2^-22, 2^-45 and 2^-60 by adding 1.5 2^23
+// steps in fp32: the sum is rounded to whole steps, its bits count them, and what is
+// left over is exact. The counts of p - q are differences of those bits: no
+// conversion to 64-bit integers and no shifts by a variable, which bound this kernel
+// (64 slots of 151936: 32 us by shifts, 57 by conversions).
+struct Steps {
+    int a = 0, b = 0, c = 0;               // of 2^-22, 2^-45 and 2^-60
+    __device__ __forceinline__ void add(float p, float q)
+    {
+        constexpr float kA = 3.0f, kB = 3.0f * 1.1920928955078125e-7f, kC = 1.5f * 7.275957614183426e-12f;   // 1.5 2^1, 2^-22, 2^-37
+        p = fminf(fmaxf(p, 0.0f), 1.0f), q = fminf(fmaxf(q, 0.0f), 1.0f);   // (NaN: 0)
+        const float pa = p + kA, qa = q + kA, p1 = p - (pa - kA), q1 = q - (qa - kA);
+        const float pb = p1 + kB, qb = q1 + kB, p2 = p1 - (pb - kB), q2 = q1 - (qb - kB);
+        const float pc = p2 + kC, qc = q2 + kC;
+        if (p > q) {
+            a += __float_as_int(pa) - __float_as_int(qa);
+            b += __float_as_int(pb) - __float_as_int(qb);
+            c += __float_as_int(pc) - __float_as_int(qc);
+        }
+    }
+    __device__ __forceinline__ unsigned long long total() const
+    {
+        return static_cast<unsigned long long>((static_cast<long long>(a) << 38) + (static_cast<long long>(b) << 15) + c);
+    }
+};
 // floor(u r), 0 <= u < 1.
 __device__ __forceinline__ unsigned long long share_of(float u, unsigned long long r)
 {
@@ -294,13 +310,19 @@ struct Rest {
         x = load_pack<float, V>(p, c, hi);
         if (q) y = load_pack<float, V>(q, c, hi);
     }
-    // what is left of elements c ..
+    // what is left of elements c ..: added to s, or one by one
+    template <int V> __device__ __forceinline__ void add(int64_t c, const Pack<float, V> &x, const Pack<float, V> &y, Steps &s) const
+    {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s.add(c + j == known ? 0.0f : elem(x, j), elem(y, j));
+    }
     template <int V> __device__ __forceinline__ void of(int64_t c, const Pack<float, V> &x, const Pack<float, V> &y, unsigned long long (&r)[V]) const
     {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const unsigned long long a = fixed60(elem(x, j)), b = fixed60(elem(y, j));
-            r[j] = a <= b || c + j == known ? 0ull : a - b;
+            Steps s;
+            s.add(c + j == known ? 0.0f : elem(x, j), elem(y, j));
+            r[j] = s.total();
         }
     }
 };
@@ -341,13 +363,14 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
     if (cluster > 1) cluster_arrive();
     const int64_t seq = blockIdx.x / cluster;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, warps = blockDim.x / 32;
-    const int count = a.counts ? min(max(a.counts[seq], 0), a.max_draft) : a.max_draft;
+    int count = a.max_draft;
+    if (a.counts) count = min(max(a.counts[seq], 0), a.max_draft);
     if (warp == 0) {
         int kept = count;
-        for (int i0 = 0; i0 < count; i0 += 32) {
+        for (int i0 = 0; i0 < a.max_draft; i0 += 32) {
             const int i = i0 + lane;
             bool stays = false;
-            if (i < count) {
+            if (i < a.max_draft) {                           // (count may still be on its way)
                 const float u = a.accept[seq * a.lda + i];
                 const int64_t x = a.drafted[seq * a.ldd + i];
                 if (x >= 0 && x < a.n) {
@@ -375,12 +398,13 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
     rest.known = refused && !a.Q ? a.drafted[seq * a.ldd + kept] : -1;
     rest.hi = seg.hi;
     // a stretch of `per` elements (whole vectors) from lo on, a warp each; its sum
-    const auto stretch = [&](int64_t lo, int64_t per, int64_t hi) {
+    const auto stretch = [&](auto ahead, int64_t lo, int64_t per, int64_t hi) {
         const int64_t from = lo + warp * per, to = min(from + per, hi);
         unsigned long long s = 0;
-        constexpr int kAhead = 4;          // accesses in flight
+        constexpr int kAhead = decltype(ahead)::value;   // accesses in flight
         for (int64_t c0 = from + lane * V; c0 - lane * V < to; c0 += kAhead * 32 * V) {
             Pack<float, V> x[kAhead], y[kAhead];
+            Steps st;
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const int64_t c = c0 + i * 32 * V;
@@ -388,11 +412,9 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                unsigned long long r[V];
-                rest.of<V>(c0 + i * 32 * V, x[i], y[i], r);
-#pragma unroll
-                for (int j = 0; j < V; ++j) s += r[j];
+                rest.add<V>(c0 + i * 32 * V, x[i], y[i], st);
             }
+            s += st.total();
         }
         s = warp_sum(s);
         if (lane == 0) spans[warp] = s;
@@ -402,7 +424,7 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
     // once; and once more, of p alone, where the draft leaves nothing of it
     for (int turn = 0; turn < 2; ++turn) {
         int64_t lo = seg.lo, hi = seg.hi, per = share(hi - lo);
-        stretch(lo, per, hi);
+        stretch(std::integral_constant<int, 4>{}, lo, per, hi);
         __syncthreads();
         const unsigned long long mine = warp_sum(lane < warps ? spans[lane] : 0ull);
         if (cluster > 1 && turn == 0) cluster_wait();
@@ -426,7 +448,7 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
                     if (per <= 32 * V) break;
                     per = share(hi - lo);
                     __syncthreads();
-                    stretch(lo, per, hi);
+                    stretch(std::integral_constant<int, 1>{}, lo, per, hi);
                     __syncthreads();
                 }
                 if (warp != 0) return;
