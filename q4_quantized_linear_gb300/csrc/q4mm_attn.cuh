@@ -104,7 +104,8 @@ struct Walk {
         }
         __syncthreads();
         const long long total = scan[a.n_seq];
-        share = static_cast<int>((total + gridDim.x - 1) / gridDim.x);
+        share = total < 0x7FFFFFFF ? static_cast<int>((static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x)
+                                   : static_cast<int>((total + gridDim.x - 1) / gridDim.x);
         const long long at = static_cast<long long>(share) * blockIdx.x;
         left = static_cast<int>(min(max(total - at, 0ll), static_cast<long long>(share)));
         if (left == 0) return;
@@ -116,9 +117,17 @@ struct Walk {
         }
         s = lo;
         q = seq_at(a, s);
-        const long long per = (scan[s + 1] - scan[s]) / a.c.heads, x = at - scan[s];
-        h = static_cast<int>(x / per);
-        long long y = x - h * per;
+        const long long own = scan[s + 1] - scan[s], x = at - scan[s];
+        long long y;
+        if (own < 0x7FFFFFFF) {   // (a 64-bit division takes several times as long)
+            const int per = static_cast<int>(own) / a.c.heads;
+            h = static_cast<int>(x) / per;
+            y = static_cast<int>(x) - h * per;
+        } else {
+            const long long per = own / a.c.heads;
+            h = static_cast<int>(x / per);
+            y = x - h * per;
+        }
         // the block that tile y is in: a warp looks at 32 at a time
         const int lane = threadIdx.x & 31;
         for (b = 0; b + 1 < q.blocks; b += 32) {
@@ -216,6 +225,35 @@ constexpr float kSlack = 8.0f;
 // Terms are held 2^kLift times larger (below 2^15), so that small ones keep their
 // bits in fp16: what is lost is below 2^-32 of the largest term.
 constexpr float kLift = 7.0f;
+
+// Values of O from element `at` on, rounded once; `at` is a multiple of 2 (8) beyond a
+// row's start.
+__device__ __forceinline__ void store2_out(const AttnArgs &a, int64_t at, float v0, float v1)
+{
+    if (a.type == Q4_TYPE_F32) {
+        float *o = static_cast<float *>(a.O) + at;
+        if (a.vec) *reinterpret_cast<float2 *>(o) = make_float2(v0, v1);
+        else o[0] = v0, o[1] = v1;
+    } else {
+        uint16_t *o = static_cast<uint16_t *>(a.O) + at;
+        const uint32_t u = a.type == Q4_TYPE_BF16 ? pack_bf16x2_rn(v0, v1) : pack_f16x2_rn(v0, v1);
+        if (a.vec) *reinterpret_cast<uint32_t *>(o) = u;
+        else o[0] = static_cast<uint16_t>(u), o[1] = static_cast<uint16_t>(u >> 16);
+    }
+}
+__device__ __forceinline__ void store8_out(const AttnArgs &a, int64_t at, const float (&v)[8])
+{
+    if (a.type != Q4_TYPE_F32 && a.vec) {
+        const bool bf = a.type == Q4_TYPE_BF16;
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = bf ? pack_bf16x2_rn(v[2 * i], v[2 * i + 1]) : pack_f16x2_rn(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.O) + at) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) store2_out(a, at + i, v[i], v[i + 1]);
+    }
+}
 
 // A row's 8 values from dim c on, as fp32 (zeros past d).
 template <typename T> __device__ __forceinline__ void row8(const T *p, bool vec, float (&f)[8])

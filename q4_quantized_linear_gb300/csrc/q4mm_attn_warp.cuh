@@ -3,8 +3,9 @@
 // log2(e) <q, k_j>, in one pass over the tokens with a running maximum m.
 //
 // For few rows the bound is the read of the cache. A warp of the CTA copies tiles
-// of 64 tokens (K and V of one head: contiguous rows of 128 bytes, a copy for
-// each page and 64 dims) into a ring; four warps compute. A block of 16 query
+// of 64 tokens into a ring, as the pages have them: a page of a head is one copy (by
+// rows of 64 dims of K and of V, 16 copies of 2 KB a tile of 16-token pages, the copies'
+// issue took 1250 clocks a tile); four warps compute. A block of 16 query
 // rows: each warp takes 16 of a tile's tokens, with a running state of its own,
 // joined at the item's end; of 32 rows: two warps by rows, two by tokens; of 64:
 // four by rows. So each value of the cache is turned into an operand once for 16
@@ -18,6 +19,8 @@
 //   TERMS = 2 (fp32 queries and outputs): queries, scaled by a power of two a row,
 // and terms are split into two fp16 numbers (22 bits); the MMA cuts its running
 // sum to fp32, so the sums over a tile start at zero and are added in fp32.
+//   A running maximum is raised only where a row's scores pass it by 2^8, and what
+// a row's four lanes have seen is brought together only then.
 //   A page's rows past the sequence's end are never copied: what their place in
 // the ring holds is zeros or an earlier tile's, finite as all values of the cache.
 #pragma once
@@ -48,11 +51,11 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4])
 template <bool BF> __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     if constexpr (BF)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -103,17 +106,31 @@ inline int warp_stage_bytes(int chunks, int ctype)
     return ctype == Q4_TYPE_I8 ? kWarpTile * (2 * chunks * 64 + 8) : kWarpTile * 2 * chunks * 128;
 }
 
+// A wait that pauses little: a suspended one resumes some 170 ns late.
+__device__ __forceinline__ bool tile_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+{
+    for (int i = 0; i < 64; ++i) {
+        if (mbar_test_wait(bar, parity)) return true;
+        __nanosleep(20);
+    }
+    return mbar_wait(bar, parity, limit_ns);
+}
+
 template <int KIND, int TERMS, int WM, int DP>
 __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_kernel(const AttnArgs a)
 {
     using S = WarpShape<KIND, TERMS, WM, DP>;
     constexpr bool BF = KIND == kBF16;
-    constexpr int WN = S::kWN, NT = S::kNT, RB = S::kRowBytes, OT = DP / 8;
+    constexpr int WN = S::kWN, NT = S::kNT, NG = NT / 2, RB = S::kRowBytes, OT = DP / 8;
     extern __shared__ __align__(128) uint8_t ring[];        // tiles, then what follows
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int chunks = DP <= 128 ? DP / kChunk : a.c.chunks;
-    const int half = kWarpTile * RB * chunks;               // K, then V
-    const int stage_bytes = 2 * half + (KIND == kI8 ? kWarpTile * 8 : 0);
+    // A tile in the ring: blocks of `together` tokens (a page, or the tile where pages
+    // are longer), each K [chunk][token], V the same, K's scales, V's.
+    const int log_together = min(a.c.log_page, 6), together = 1 << log_together;
+    const int chunk_bytes = together * RB, v_at = chunks * chunk_bytes, scales_at = 2 * v_at;
+    const int block_bytes = scales_at + (KIND == kI8 ? together * 8 : 0);
+    const int stage_bytes = (kWarpTile >> log_together) * block_bytes;
     uint8_t *qs = ring + a.stages * stage_bytes;
     float *red = reinterpret_cast<float *>(qs + S::kQBytes);
     float *row_factor = red + S::kRedBytes / 4;
@@ -125,17 +142,14 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
         *abort = 0;
         fence_barrier_init();
     }
+    if (KIND != kI8)
+        for (int x = tid; x < a.stages * stage_bytes / 16; x += kAttnThreads) sts128(ring + 16 * x, make_uint4(0u, 0u, 0u, 0u));
+    fence_proxy_async_smem();
     pdl_wait();
     pdl_launch_dependents();
     Walk w;
-    w.begin(a, reinterpret_cast<long long *>(ring));
-    __syncthreads();
-    // Values' places in the ring start as zeros: see above.
-    if (KIND != kI8)
-        for (int i = 0; i < a.stages; ++i)
-            for (int x = tid; x < half / 16; x += kAttnThreads)
-                sts128(ring + i * stage_bytes + half + 16 * x, make_uint4(0u, 0u, 0u, 0u));
-    fence_proxy_async_smem();
+    static_assert(S::kQBytes + S::kRedBytes >= 8 * (kMaxSeqs + 1), "room for the walk's scan");
+    w.begin(a, reinterpret_cast<long long *>(qs));
     __syncthreads();
     if (tid == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
 
@@ -145,17 +159,27 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
         uint32_t phase = 0;
         long long issued = 0;
         bool ok = true;
+        const int in_page = a.c.page_tokens, log_page = a.c.log_page;
         const int per_page = 2 * chunks + (KIND == kI8 ? 2 : 0);
-        const int in_page = a.c.page_tokens;
         for (; ok && w.valid(); w.next(a)) {
             const int32_t *table = a.c.table + w.s * a.c.ldt;
-            const int64_t head = static_cast<int64_t>(w.h) * a.c.head_bytes;
-            const int end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> a.c.log_page;
-            int held = -32, page = 0;                       // lane l holds page held + l of the sequence
+            const uint8_t *head = a.c.pages + static_cast<int64_t>(w.h) * a.c.head_bytes;
+            const int end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> log_page;
+            // lane l holds page held + l of the sequence, and the one 32 further on
+            int held = ((w.first + w.from) * kWarpTile) >> log_page;
+            int page = page_of(a, table, held + lane, pages), ahead = page_of(a, table, held + 32 + lane, pages);
             for (int t = w.from; t < w.upto; ++t) {
                 const int t0 = (w.first + t) * kWarpTile, tokens = min(max(end - t0, 0), kWarpTile);
+                const int p0 = t0 >> log_page;
+                // whole pages, and the tokens of one that is not (or is longer than a tile)
+                const int whole = in_page <= kWarpTile ? tokens >> log_page : 0, rest = tokens - (whole << log_page);
+                if (p0 >= held + 32) {                      // (a tile's pages never straddle: 32 is a multiple of their number)
+                    page = ahead;
+                    held += 32;
+                    ahead = page_of(a, table, held + 32 + lane, pages);
+                }
                 if (*reinterpret_cast<volatile int *>(abort)) { ok = false; break; }
-                if (issued >= a.stages && !mbar_wait(&empty[stage], phase ^ 1u, a.wait_ns)) {
+                if (issued >= a.stages && !tile_wait(&empty[stage], phase ^ 1u, a.wait_ns)) {
                     *reinterpret_cast<volatile int *>(abort) = 1;
                     record_status(a.status, kErrTimeout);
                     ok = false;
@@ -163,34 +187,22 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
                 ok = __all_sync(0xFFFFFFFFu, ok) != 0;
                 if (!ok) break;
                 uint8_t *dst = ring + stage * stage_bytes;
-                const int scale_tokens = KIND == kI8 ? (tokens + 3) & ~3 : 0;
-                if (lane == 0) {
-                    // `pieces` copies add up to this; a tile without tokens has none
-                    mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(tokens * 2 * chunks * RB + 8 * scale_tokens));
-                }
+                const int rest_scales = KIND == kI8 ? (rest + 3) & ~3 : 0;
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(whole * block_bytes + rest * 2 * chunks * RB + 8 * rest_scales));
                 __syncwarp();
-                const int p0 = t0 >> a.c.log_page, np = tokens > 0 ? ((t0 + tokens - 1) >> a.c.log_page) - p0 + 1 : 0;
-                if (np > 0 && p0 + np > held + 32) {
-                    held = p0;
-                    page = page_of(a, table, held + lane, pages);
-                }
-                const int pieces = np * per_page;
-                for (int x0 = 0; x0 < pieces; x0 += 32) {
-                    const int x = x0 + lane, j = x / per_page, y = x - j * per_page;
-                    const int pg = __shfl_sync(0xFFFFFFFFu, page, min(p0 + j - held, 31));
-                    if (x < pieces) {
-                        const int in = max(t0 - ((p0 + j) << a.c.log_page), 0);          // first token of the page that is in the tile
-                        const int at = ((p0 + j) << a.c.log_page) + in - t0;             // its place in the tile
-                        const int n = min(in_page - in, tokens - at);
-                        const uint8_t *src = a.c.pages + pg * a.c.page_bytes + head;
-                        if (y < 2 * chunks)
-                            bulk_g2s(dst + y * (kWarpTile * RB) + at * RB, src + (y * in_page + in) * RB,
-                                     static_cast<uint32_t>(n * RB), &full[stage]);
-                        else
-                            bulk_g2s(dst + 2 * half + (y - 2 * chunks) * (kWarpTile * 4) + at * 4,
-                                     src + 2 * chunks * in_page * RB + ((y - 2 * chunks) * in_page + in) * 4,
-                                     static_cast<uint32_t>(((n + 3) & ~3) * 4), &full[stage]);
-                    }
+                const int y = lane - 8;                     // lanes 8 and on: a piece each of the page that is not whole
+                const int pg = __shfl_sync(0xFFFFFFFFu, page, min(p0 - held + min(lane, whole), 31));
+                const uint8_t *src = head + pg * a.c.page_bytes;
+                if (lane < whole) {
+                    bulk_g2s(dst + lane * block_bytes, src, static_cast<uint32_t>(block_bytes), &full[stage]);
+                } else if (y >= 0 && y < per_page && rest > 0) {
+                    const int in = in_page <= kWarpTile ? 0 : t0 & (in_page - 1);
+                    dst += whole * block_bytes;
+                    if (y < 2 * chunks)
+                        bulk_g2s(dst + y * chunk_bytes, src + (y * in_page + in) * RB, static_cast<uint32_t>(rest * RB), &full[stage]);
+                    else
+                        bulk_g2s(dst + scales_at + (y - 2 * chunks) * (together * 4), src + 2 * chunks * in_page * RB + ((y - 2 * chunks) * in_page + in) * 4,
+                                 static_cast<uint32_t>(rest_scales * 4), &full[stage]);
                 }
                 ++issued;
                 if (++stage == a.stages) stage = 0, phase ^= 1u;
@@ -206,58 +218,82 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
     // ------------------------------------------------------------- compute
     const int wm = warp / WN, wn = warp % WN;
     const uint32_t qbase = smem_u32(qs), ring_at = smem_u32(ring);
+    // Where a lane reads: of K (ldmatrix: 8 tokens x 32 dims; codes: 16 bytes of token
+    // g), of V (ldmatrix: 16 tokens x 16 dims; codes: 8 dims of tokens 2 c, 2 c + 1, ..),
+    // and the blocks of the warp's tokens, 16 at a time.
+    const uint32_t k_lane = KIND == kI8 ? g * 64 + ((c ^ ((g >> 1) & 3)) << 4) : (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
+    const uint32_t v_lane = v_at + (KIND == kI8 ? 2 * c * 64 + (((g >> 1) ^ c) << 4) + 8 * (g & 1)
+                                                : (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4));
+    uint32_t off[NG], scale_off[KIND == kI8 ? NG : 1];
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+        const int tok = wn * S::kTokens + 16 * i, block = (tok >> log_together) * block_bytes, in = tok & (together - 1);
+        off[i] = block + in * RB;
+        if constexpr (KIND == kI8) scale_off[i] = block + scales_at + in * 4;
+    }
     int stage = 0;
     uint32_t phase = 0;
     bool alive = true;                                      // a wait ran out: no tile is looked at any more
     for (; w.valid(); w.next(a)) {
-        // Queries: a warp a row at a time, a lane 8 dims.
+        // Queries: DP / 8 threads a row, eight dims each, four rows of a thread in flight.
         compute_barrier();                                  // the item before is done with them
-#pragma unroll 2
-        for (int r = warp; r < S::kBlock; r += kComputeWarps) {
-            const int row = w.b * S::kBlock + r;
-            float f[8] = {};
-            if (row < w.q.rows && 8 * lane < a.c.d) {
-                const int i = row / a.group, head = w.h * a.group + row - i * a.group;
-                query8(a, (static_cast<int64_t>(w.q.start) + i) * a.ldq + head * a.c.d + 8 * lane, f);
-            }
-            float factor = a.scale_log2;
-            if (KIND == kI8 || TERMS == 2) {
-                // to fp16's range by a power of two: the largest in 2^12 .. 2^13
-                uint32_t mb = 0;
+        {
+            constexpr int L = DP / 8, kRows = kComputeWarps * 32 / L, kPasses = S::kBlock / kRows, kBatch = kPasses < 4 ? kPasses : 4;
+            const int x = tid % L;
+            for (int r0 = tid / L; r0 < S::kBlock; r0 += kBatch * kRows) {
+                float f[kBatch][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) mb = max(mb, abs_bits(f[i]));
-                mb = __reduce_max_sync(0xFFFFFFFFu, mb);
-                if (mb >= 0x7F800000u) {
-                    factor = __uint_as_float(0x7FC00000u);  // a query that is not finite: NaN
+                for (int p = 0; p < kBatch; ++p) {
+                    const int row = w.b * S::kBlock + r0 + p * kRows;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-                } else if (mb != 0u) {
-                    const int e = min(max(139 - static_cast<int>(mb >> 23), -126), 126);   // 12 - exponent
-                    const float up = pow2(e);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] *= up;
-                    factor *= pow2(-e);
-                }
-            }
-            if (8 * lane < DP) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (BF) {
-                        hi[i] = pack_bf16x2_rn(f[2 * i], f[2 * i + 1]);
-                    } else {
-                        hi[i] = pack_f16x2_rn(f[2 * i], f[2 * i + 1]);
-                        if (TERMS == 2) {
-                            const __half2 h2 = *reinterpret_cast<__half2 *>(&hi[i]);
-                            lo[i] = pack_f16x2_rn(f[2 * i] - __low2float(h2), f[2 * i + 1] - __high2float(h2));
-                        }
+                    for (int i = 0; i < 8; ++i) f[p][i] = 0.0f;
+                    if (row < w.q.rows && 8 * x < a.c.d) {
+                        const int i = row / a.group, head = w.h * a.group + row - i * a.group;
+                        query8(a, (static_cast<int64_t>(w.q.start) + i) * a.ldq + head * a.c.d + 8 * x, f[p]);
                     }
                 }
-                sts128(qs + r * S::kQStride + 16 * lane, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                if (TERMS == 2)
-                    sts128(qs + S::kBlock * S::kQStride + r * S::kQStride + 16 * lane, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+                for (int p = 0; p < kBatch; ++p) {
+                    const int r = r0 + p * kRows;
+                    float factor = a.scale_log2;
+                    if (KIND == kI8 || TERMS == 2) {
+                        // to fp16's range by a power of two: the largest in 2^12 .. 2^13
+                        uint32_t mb = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) mb = max(mb, abs_bits(f[p][i]));
+#pragma unroll
+                        for (int o = L / 2; o > 0; o /= 2) mb = max(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, o));
+                        if (mb >= 0x7F800000u) {
+                            factor = __uint_as_float(0x7FC00000u);  // a query that is not finite: NaN
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) f[p][i] = 0.0f;
+                        } else if (mb != 0u) {
+                            const int e = min(max(139 - static_cast<int>(mb >> 23), -126), 126);   // 12 - exponent
+                            const float up = pow2(e);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) f[p][i] *= up;
+                            factor *= pow2(-e);
+                        }
+                    }
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (BF) {
+                            hi[i] = pack_bf16x2_rn(f[p][2 * i], f[p][2 * i + 1]);
+                        } else {
+                            hi[i] = pack_f16x2_rn(f[p][2 * i], f[p][2 * i + 1]);
+                            if (TERMS == 2) {
+                                const __half2 h2 = *reinterpret_cast<__half2 *>(&hi[i]);
+                                lo[i] = pack_f16x2_rn(f[p][2 * i] - __low2float(h2), f[p][2 * i + 1] - __high2float(h2));
+                            }
+                        }
+                    }
+                    sts128(qs + r * S::kQStride + 16 * x, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    if (TERMS == 2)
+                        sts128(qs + S::kBlock * S::kQStride + r * S::kQStride + 16 * x, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    if (x == 0) row_factor[r] = factor;
+                }
             }
-            if (lane == 0) row_factor[r] = factor;
         }
         compute_barrier();
         // A operand of 16 dims (k-step ks): for codes the dims in the order in which a
@@ -296,7 +332,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
         float m0 = neg_inf(), m1 = neg_inf(), l0 = 0.0f, l1 = 0.0f;
         int E0 = -118, E1 = -118;                           // value scales that the rows have seen are below 2^E
         for (int t = w.from; alive && t < w.upto; ++t) {
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, a.wait_ns))) {
+            if (!__all_sync(0xFFFFFFFFu, tile_wait(&full[stage], phase, a.wait_ns))) {
                 if (lane == 0) {
                     *reinterpret_cast<volatile int *>(abort) = 1;
                     record_status(a.status, kErrTimeout);
@@ -305,68 +341,53 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
                 break;
             }
             const uint32_t kv = ring_at + stage * stage_bytes;
-            const int tok = wn * S::kTokens;                // the warp's tokens of the tile
-            const int t0 = (w.first + t) * kWarpTile + tok;
+            const int t0 = (w.first + t) * kWarpTile + wn * S::kTokens;
             float s[NT][4] = {};
             float s2[TERMS == 2 ? NT : 1][4] = {};
 #pragma unroll
             for (int ch = 0; ch < S::kMaxChunks; ++ch) {
                 if (ch < chunks) {
+                    const uint32_t kb = kv + ch * chunk_bytes + k_lane;
                     if constexpr (KIND == kI8) {
+                        uint4 x[NT];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const int row = tok + nt * 8 + g;
-                            const uint4 x = lds128_at(kv + ch * (kWarpTile * RB) + row * RB + ((c ^ ((row >> 1) & 3)) << 4));
-                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                        for (int nt = 0; nt < NT; ++nt) x[nt] = lds128_at(kb + off[nt / 2] + (nt & 1) * (8 * RB));
 #pragma unroll
-                            for (int k4 = 0; k4 < 4; ++k4) {
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            uint32_t q[4], q2[4];
+                            if constexpr (!S::kQInRegs) load_q(0, ch * 4 + k4, q);
+                            if constexpr (TERMS == 2) load_q(1, ch * 4 + k4, q2);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
                                 uint32_t b0, b1;
-                                codes_f16(xs[k4], b0, b1);
-                                if constexpr (S::kQInRegs) {
-                                    mma16816<BF>(s[nt], qr[ch * 4 + k4], b0, b1);
-                                } else {
-                                    uint32_t q[4];
-                                    load_q(0, ch * 4 + k4, q);
-                                    mma16816<BF>(s[nt], q, b0, b1);
-                                    if constexpr (TERMS == 2) {
-                                        load_q(1, ch * 4 + k4, q);
-                                        mma16816<BF>(s2[nt], q, b0, b1);
-                                    }
-                                }
+                                codes_f16(k4 == 0 ? x[nt].x : k4 == 1 ? x[nt].y : k4 == 2 ? x[nt].z : x[nt].w, b0, b1);
+                                if constexpr (S::kQInRegs) mma16816<BF>(s[nt], qr[ch * 4 + k4], b0, b1);
+                                else mma16816<BF>(s[nt], q, b0, b1);
+                                if constexpr (TERMS == 2) mma16816<BF>(s2[nt], q2, b0, b1);
                             }
                         }
                     } else {
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {       // 32 dims
-                            uint32_t q[2][4], q2[2][4];
-                            if constexpr (!S::kQInRegs) {
-                                load_q(0, ch * 4 + 2 * p, q[0]), load_q(0, ch * 4 + 2 * p + 1, q[1]);
-                                if constexpr (TERMS == 2) load_q(1, ch * 4 + 2 * p, q2[0]), load_q(1, ch * 4 + 2 * p + 1, q2[1]);
-                            }
+                            uint32_t q[2][4], q2[2][4], b[NT][4];
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const int row = tok + nt * 8 + (lane & 7);
-                                uint32_t b[4];
-                                ldsm4(kv + ch * (kWarpTile * RB) + row * RB + (((4 * p + (lane >> 3)) ^ (row & 7)) << 4), b);
-                                if constexpr (S::kQInRegs) {
-                                    mma16816<BF>(s[nt], qr[ch * 4 + 2 * p], b[0], b[1]);
-                                    mma16816<BF>(s[nt], qr[ch * 4 + 2 * p + 1], b[2], b[3]);
-                                } else {
-                                    mma16816<BF>(s[nt], q[0], b[0], b[1]);
-                                    mma16816<BF>(s[nt], q[1], b[2], b[3]);
-                                    if constexpr (TERMS == 2) {
-                                        mma16816<BF>(s2[nt], q2[0], b[0], b[1]);
-                                        mma16816<BF>(s2[nt], q2[1], b[2], b[3]);
-                                    }
+                            for (int nt = 0; nt < NT; ++nt) ldsm4((kb ^ (64 * p)) + off[nt / 2] + (nt & 1) * (8 * RB), b[nt]);
+                            if constexpr (!S::kQInRegs) load_q(0, ch * 4 + 2 * p, q[0]), load_q(0, ch * 4 + 2 * p + 1, q[1]);
+                            if constexpr (TERMS == 2) load_q(1, ch * 4 + 2 * p, q2[0]), load_q(1, ch * 4 + 2 * p + 1, q2[1]);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    if constexpr (S::kQInRegs) mma16816<BF>(s[nt], qr[ch * 4 + 2 * p + h], b[nt][2 * h], b[nt][2 * h + 1]);
+                                    else mma16816<BF>(s[nt], q[h], b[nt][2 * h], b[nt][2 * h + 1]);
+                                    if constexpr (TERMS == 2) mma16816<BF>(s2[nt], q2[h], b[nt][2 * h], b[nt][2 * h + 1]);
                                 }
-                            }
                         }
                     }
                 }
             }
             // scores in powers of two
             float sv[KIND == kI8 ? NT : 1][2];
-            const uint32_t scales = kv + 2 * half;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 if constexpr (TERMS == 2) {
@@ -375,8 +396,8 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
                 }
                 float f0 = rf0, f1 = rf0, f2v = rf1, f3 = rf1;
                 if constexpr (KIND == kI8) {
-                    const uint2 k2 = lds64(scales + 4 * (tok + nt * 8 + 2 * c));
-                    const uint2 v2 = lds64(scales + 4 * (kWarpTile + tok + nt * 8 + 2 * c));
+                    const uint32_t at = kv + scale_off[nt / 2] + 4 * ((nt & 1) * 8 + 2 * c);
+                    const uint2 k2 = lds64(at), v2 = lds64(at + 4 * together);
                     f0 *= __uint_as_float(k2.x), f1 *= __uint_as_float(k2.y);
                     f2v *= __uint_as_float(k2.x), f3 *= __uint_as_float(k2.y);
                     sv[nt][0] = __uint_as_float(v2.x), sv[nt][1] = __uint_as_float(v2.y);
@@ -411,24 +432,21 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
                 x0 = fmaxf(x0, fmaxf(s[nt][0], s[nt][1]));
                 x1 = fmaxf(x1, fmaxf(s[nt][2], s[nt][3]));
             }
-            x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
-            x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 2));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 2));
-            bool wide = false;
-            if constexpr (KIND == kI8) {
-                v0max = fmaxf(v0max, __shfl_xor_sync(0xFFFFFFFFu, v0max, 1));
-                v1max = fmaxf(v1max, __shfl_xor_sync(0xFFFFFFFFu, v1max, 1));
-                v0max = fmaxf(v0max, __shfl_xor_sync(0xFFFFFFFFu, v0max, 2));
-                v1max = fmaxf(v1max, __shfl_xor_sync(0xFFFFFFFFu, v1max, 2));
-                wide = v0max >= pow2(E0) || v1max >= pow2(E1);
-            }
+            const bool wide = KIND == kI8 && (v0max >= pow2(E0) || v1max >= pow2(E1));
             if (__any_sync(0xFFFFFFFFu, x0 > m0 + kSlack || x1 > m1 + kSlack || wide)) {
+                x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
+                x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 2));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 2));
                 const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
                 float a0 = m0 == neg_inf() ? 0.0f : exp2_fast(m0 - n0), a1 = m1 == neg_inf() ? 0.0f : exp2_fast(m1 - n1);
                 m0 = n0, m1 = n1;
                 l0 *= a0, l1 *= a1;
                 if constexpr (KIND == kI8) {
+                    v0max = fmaxf(v0max, __shfl_xor_sync(0xFFFFFFFFu, v0max, 1));
+                    v1max = fmaxf(v1max, __shfl_xor_sync(0xFFFFFFFFu, v1max, 1));
+                    v0max = fmaxf(v0max, __shfl_xor_sync(0xFFFFFFFFu, v0max, 2));
+                    v1max = fmaxf(v1max, __shfl_xor_sync(0xFFFFFFFFu, v1max, 2));
                     a0 *= raise(E0, v0max), a1 *= raise(E1, v1max);
                 }
 #pragma unroll
@@ -436,7 +454,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
             }
             const float u0 = m0 == neg_inf() ? 0.0f : m0 - kLift, u1 = m1 == neg_inf() ? 0.0f : m1 - kLift;
             const float down0 = KIND == kI8 ? pow2(-E0) : 1.0f, down1 = KIND == kI8 ? pow2(-E1) : 1.0f;
-            uint32_t p[NT / 2][4], p2[TERMS == 2 ? NT / 2 : 1][4];
+            uint32_t p[NG][4], p2[TERMS == 2 ? NG : 1][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float e[4] = {exp2_fast(s[nt][0] - u0), exp2_fast(s[nt][1] - u0), exp2_fast(s[nt][2] - u1), exp2_fast(s[nt][3] - u1)};
@@ -464,19 +482,17 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
 #pragma unroll
             for (int ch = 0; ch < S::kMaxChunks; ++ch) {
                 if (ch < chunks) {
-                    const uint32_t vb = kv + half + ch * (kWarpTile * RB);
+                    const uint32_t vb = kv + ch * chunk_bytes + v_lane;
                     if constexpr (KIND == kI8) {
                         // eight dims of a lane (8 g ..), as the n of eight column tiles
                         float fresh[TERMS == 2 ? 8 : 1][4] = {};
 #pragma unroll
-                        for (int k = 0; k < NT / 2; ++k) {
+                        for (int k = 0; k < NG; ++k) {
                             uint2 x[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int row = tok + 16 * k + 2 * c + (i & 1) + 8 * (i >> 1);
-                                x[i] = lds64(vb + row * RB + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g & 1));
-                                x[i].x ^= 0x80808080u, x[i].y ^= 0x80808080u;
-                            }
+                            for (int i = 0; i < 4; ++i) x[i] = lds64(vb + off[k] + RB * ((i & 1) + 8 * (i >> 1)));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[i].x ^= 0x80808080u, x[i].y ^= 0x80808080u;
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const uint32_t sel = 0x40u + 0x11u * (j & 3);   // byte j of the first token, of the second
@@ -498,31 +514,35 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) o[ch * 8 + j][i] += fresh[j][i];
                         }
-                    } else {
+                    } else if constexpr (TERMS == 2) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {       // 16 dims
-                            float fresh[TERMS == 2 ? 2 : 1][4] = {};
+                            float fresh[2][4] = {};
 #pragma unroll
-                            for (int k = 0; k < NT / 2; ++k) {
-                                const int row = tok + 16 * k + (lane & 15);
+                            for (int k = 0; k < NG; ++k) {
                                 uint32_t b[4];
-                                ldsm4_t(vb + row * RB + (((2 * j + (lane >> 4)) ^ (row & 7)) << 4), b);
-                                if constexpr (TERMS == 2) {
-                                    mma16816<BF>(fresh[0], p[k], b[0], b[1]);
-                                    mma16816<BF>(fresh[1], p[k], b[2], b[3]);
-                                    mma16816<BF>(fresh[0], p2[k], b[0], b[1]);
-                                    mma16816<BF>(fresh[1], p2[k], b[2], b[3]);
-                                } else {
-                                    mma16816<BF>(o[ch * 8 + 2 * j], p[k], b[0], b[1]);
-                                    mma16816<BF>(o[ch * 8 + 2 * j + 1], p[k], b[2], b[3]);
-                                }
+                                ldsm4_t((vb ^ (32 * j)) + off[k], b);
+                                mma16816<BF>(fresh[0], p[k], b[0], b[1]);
+                                mma16816<BF>(fresh[1], p[k], b[2], b[3]);
+                                mma16816<BF>(fresh[0], p2[k], b[0], b[1]);
+                                mma16816<BF>(fresh[1], p2[k], b[2], b[3]);
                             }
-                            if constexpr (TERMS == 2) {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    o[ch * 8 + 2 * j][i] += fresh[0][i];
-                                    o[ch * 8 + 2 * j + 1][i] += fresh[1][i];
-                                }
+                            for (int i = 0; i < 4; ++i) {
+                                o[ch * 8 + 2 * j][i] += fresh[0][i];
+                                o[ch * 8 + 2 * j + 1][i] += fresh[1][i];
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < NG; ++k) {
+                            uint32_t b[4][4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) ldsm4_t((vb ^ (32 * j)) + off[k], b[j]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                mma16816<BF>(o[ch * 8 + 2 * j], p[k], b[j][0], b[j][1]);
+                                mma16816<BF>(o[ch * 8 + 2 * j + 1], p[k], b[j][2], b[j][3]);
                             }
                         }
                     }
@@ -535,7 +555,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
         // ------------------------------------------------- the item's end
         l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 1), l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 1);
         l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 2), l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 2);
-        // the warps of a row slice come to one maximum, then add up two by two
+        // the warps of a row slice come to one maximum, then add up
         float f0 = KIND == kI8 ? pow2(E0) : 1.0f, f1 = KIND == kI8 ? pow2(E1) : 1.0f;
         if constexpr (WN > 1) {
             if (c == 0) {
@@ -544,22 +564,24 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
             }
             compute_barrier();
             float n0 = neg_inf(), n1 = neg_inf();
+            float2 y0[WN], y1[WN];
 #pragma unroll
             for (int i = 0; i < WN; ++i) {
-                n0 = fmaxf(n0, red_ml[(wm * WN + i) * 16 + g].x);
-                n1 = fmaxf(n1, red_ml[(wm * WN + i) * 16 + g + 8].x);
+                y0[i] = red_ml[(wm * WN + i) * 16 + g], y1[i] = red_ml[(wm * WN + i) * 16 + g + 8];
+                n0 = fmaxf(n0, y0[i].x), n1 = fmaxf(n1, y1[i].x);
             }
             l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
             for (int i = 0; i < WN; ++i) {
-                const float2 y0 = red_ml[(wm * WN + i) * 16 + g], y1 = red_ml[(wm * WN + i) * 16 + g + 8];
-                l0 += y0.y * (y0.x == neg_inf() ? 1.0f : exp2_fast(y0.x - n0));
-                l1 += y1.y * (y1.x == neg_inf() ? 1.0f : exp2_fast(y1.x - n1));
+                l0 += y0[i].y * (y0[i].x == neg_inf() ? 1.0f : exp2_fast(y0[i].x - n0));
+                l1 += y1[i].y * (y1[i].x == neg_inf() ? 1.0f : exp2_fast(y1[i].x - n1));
             }
             f0 *= m0 == neg_inf() ? 1.0f : exp2_fast(m0 - n0);
             f1 *= m1 == neg_inf() ? 1.0f : exp2_fast(m1 - n1);
             m0 = n0, m1 = n1;
         }
+        const bool whole = w.whole();
+        if (whole) f0 *= l0 == 0.0f ? 0.0f : 1.0f / l0, f1 *= l1 == 0.0f ? 0.0f : 1.0f / l1;
 #pragma unroll
         for (int j = 0; j < OT; ++j) o[j][0] *= f0, o[j][1] *= f0, o[j][2] *= f1, o[j][3] *= f1;
         if constexpr (WN > 1) {
@@ -590,7 +612,6 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
             }
         }
         if (wn == 0) {
-            const bool whole = w.whole();
             const int slot = 2 * static_cast<int>(blockIdx.x) + (w.from == 0 ? 1 : 0);
             float *part = a.parts + slot * attn_part_floats(S::kBlock, chunks);
             const int width = kChunk * chunks;
@@ -598,29 +619,42 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
             for (int up = 0; up < 2; ++up) {
                 const int r = wm * 16 + g + 8 * up, row = w.b * S::kBlock + r;
                 if (row >= w.q.rows) continue;
-                const float l = up ? l1 : l0;
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 const int i = row / a.group, head = w.h * a.group + row - i * a.group;
                 const int64_t out = (static_cast<int64_t>(w.q.start) + i) * a.ldo + static_cast<int64_t>(head) * a.c.d;
+                if constexpr (KIND == kI8) {
+                    // a lane has dims 8 (2 c + x) .. + 7 of a chunk
 #pragma unroll
-                for (int j = 0; j < OT; ++j) {
-                    if (j / 8 >= chunks) continue;
+                    for (int ch = 0; ch < S::kMaxChunks; ++ch) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        // column 2 c + x of tile j
-                        const int dim = KIND == kI8 ? (j / 8) * kChunk + 8 * (2 * c + x) + j % 8 : 8 * j + 2 * c + x;
-                        const float v = o[j][2 * up + x];
-                        if (!whole) part[r * width + dim] = v;
-                        else if (dim < a.c.d) {
-                            if (a.type == Q4_TYPE_F32) static_cast<float *>(a.O)[out + dim] = v * inv;
-                            else if (a.type == Q4_TYPE_F16) static_cast<__half *>(a.O)[out + dim] = __float2half_rn(v * inv);
-                            else static_cast<__nv_bfloat16 *>(a.O)[out + dim] = __float2bfloat16_rn(v * inv);
+                        for (int x = 0; x < 2; ++x) {
+                            const int dim = ch * kChunk + 8 * (2 * c + x);
+                            float v[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j] = o[ch * 8 + j][2 * up + x];
+                            if (ch < chunks) {
+                                if (!whole) {
+                                    float4 *dst = reinterpret_cast<float4 *>(part + r * width + dim);
+                                    dst[0] = make_float4(v[0], v[1], v[2], v[3]), dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                                } else if (dim < a.c.d) {
+                                    store8_out(a, out + dim, v);
+                                }
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < OT; ++j) {
+                        const int dim = 8 * j + 2 * c;
+                        const float v0 = o[j][2 * up], v1 = o[j][2 * up + 1];
+                        if (j / 8 < chunks) {
+                            if (!whole) *reinterpret_cast<float2 *>(part + r * width + dim) = make_float2(v0, v1);
+                            else if (dim < a.c.d) store2_out(a, out + dim, v0, v1);
                         }
                     }
                 }
                 if (!whole && c == 0) {
                     part[S::kBlock * width + r] = up ? m1 : m0;
-                    part[S::kBlock * width + S::kBlock + r] = l;
+                    part[S::kBlock * width + S::kBlock + r] = up ? l1 : l0;
                 }
             }
             if (!whole && w.from == 0 && lane == 0 && wm == 0) a.meta[blockIdx.x] = make_int4(w.s, w.h, w.b, w.parts());
@@ -637,8 +671,7 @@ template <int KIND, int TERMS, int WM, int DP> cudaError_t launch_shape(AttnArgs
     const int two = static_cast<int>(kSmemPerSM / 2) - 1024 - fixed, one = static_cast<int>(kSmemOptIn) - fixed;
     const int per_sm = DP <= 128 && two / stage >= 2 ? 2 : 1;
     a.stages = std::min(8, (per_sm == 2 ? two : one) / stage);
-    // the walk's scan lies in the ring at first
-    const size_t smem = fixed + std::max<size_t>(static_cast<size_t>(a.stages) * stage, 8 * (kMaxSeqs + 1));
+    const size_t smem = fixed + static_cast<size_t>(a.stages) * stage;
     const void *f = reinterpret_cast<const void *>(&attn_warp_kernel<KIND, TERMS, WM, DP>);
     cudaError_t e = set_max_smem(f, kSmemOptIn);
     if (e != cudaSuccess) return e;
