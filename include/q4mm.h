@@ -443,7 +443,7 @@ Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, 
  * [n_seq + 1], non-decreasing, a sequence may have none); lens[s] (device int32)
  * is how many tokens the sequence holds in the cache with the new ones, which are
  * its last. `rows` is at least starts[n_seq] (what the matrices hold); rows past
- * it are neither read nor written. Nothing of the batch is read by the host, so
+ * it are never written, and what they hold enters nothing. Nothing of the batch is read by the host, so
  * a captured call replays with other lengths. A sequence is rewound by calling
  * with a smaller len.
  *   table: device int32, row s at table + s * ldt: the pages of sequence s in the

@@ -51,18 +51,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     __shared__ float warp_red[kJoinThreads / 32];
     pdl_wait();
     pdl_launch_dependents();
-    const int4 item = a.meta[blockIdx.x];
-    const int parts = item.w;
+    const int4 item = a.meta[2 * blockIdx.x];               // parts, rows, the first of them, head
+    const int start = a.meta[2 * blockIdx.x + 1].x;
+    const int parts = item.x;
     if (parts == 0) return;
-    const Seq q = seq_at(a, item.x);
     const int W = kChunk * a.c.chunks, lanes = W / 4, groups = kJoinThreads / lanes;
     const int tid = threadIdx.x, grp = tid / lanes, x = tid - grp * lanes;
     const int64_t size = attn_part_floats(a.block, a.c.chunks);
-    const int rows = min(a.block, q.rows - item.z * a.block);
+    const int rows = item.y;
     const auto part_at = [&](int i) { return a.parts + (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0)) * size; };
     const auto out_at = [&](int r) {
-        const int row = item.z * a.block + r, i = row / a.group, head = item.y * a.group + row - i * a.group;
-        return (static_cast<int64_t>(q.start) + i) * a.ldo + static_cast<int64_t>(head) * a.c.d;
+        const int row = item.z + r, i = row / a.group, head = item.w * a.group + row - i * a.group;
+        return (static_cast<int64_t>(start) + i) * a.ldo + static_cast<int64_t>(head) * a.c.d;
     };
     if (parts <= 32) {
         const int lane = tid % 32;
@@ -71,6 +71,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
             if (lane < parts) {
                 const float *p = part_at(lane);
                 mi = p[a.block * W + r], l = p[a.block * W + a.block + r];
+            }
+            // the first parts' sums are on their way while the weights are made
+            constexpr int kAhead = 4;
+            float4 u[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                u[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i < parts && 4 * lane < W) u[i] = *reinterpret_cast<const float4 *>(part_at(i) + r * W + 4 * lane);
             }
             float m = mi;
 #pragma unroll
@@ -84,17 +92,21 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
             for (int c = 0; c < W; c += 128) {
                 const int dim = c + 4 * lane;
                 float v[4] = {};
-#pragma unroll 4
-                for (int i = 0; i < parts; ++i) {
-                    const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
-                    if (dim < W) {
-                        const float4 u = *reinterpret_cast<const float4 *>(part_at(i) + r * W + dim);
-                        v[0] += wi * u.x, v[1] += wi * u.y, v[2] += wi * u.z, v[3] += wi * u.w;
+                for (int i0 = 0; i0 < parts; i0 += kAhead) {
+                    if (i0 + c > 0) {
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i)
+                            if (i0 + i < parts && dim < W) u[i] = *reinterpret_cast<const float4 *>(part_at(i0 + i) + r * W + dim);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        const float wi = __shfl_sync(0xFFFFFFFFu, w, min(i0 + i, 31));
+                        if (i0 + i < parts) v[0] += wi * u[i].x, v[1] += wi * u[i].y, v[2] += wi * u[i].z, v[3] += wi * u[i].w;
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] *= inv;
-                store4(a, out, dim, v);
+                if (dim < W) store4(a, out, dim, v);
             }
         }
         return;

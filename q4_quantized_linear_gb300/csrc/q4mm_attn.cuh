@@ -182,6 +182,14 @@ struct Walk {
     }
 };
 
+// What the join needs to know of an item that starts in this CTA and is not finished
+// in it: its parts, rows, first row in the sequence and head; the sequence's first row.
+__device__ __forceinline__ void put_meta(const AttnArgs &a, const Walk &w)
+{
+    a.meta[2 * blockIdx.x] = make_int4(w.parts(), min(a.block, w.q.rows - w.b * a.block), w.b * a.block, w.h);
+    a.meta[2 * blockIdx.x + 1] = make_int4(w.q.start, 0, 0, 0);
+}
+
 // Page i of a sequence that needs `pages` (0 past them). One that the cache does not
 // have is recorded, and one that it has is read in its place.
 __device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *table, int i, int pages)

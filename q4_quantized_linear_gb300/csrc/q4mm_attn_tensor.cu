@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     const uint32_t tmem = bars->tmem;
     const auto aborted = [&] { return *reinterpret_cast<volatile int *>(&bars->abort) != 0; };
     const auto fail = [&] {
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 part[kTensorRows * DP + r_in] = m;
                 part[kTensorRows * DP + kTensorRows + r_in] = l;
             }
-            if (!whole && w.from == 0 && tid == 0) a.meta[blockIdx.x] = make_int4(w.s, w.h, w.b, w.parts());
+            if (!whole && w.from == 0 && tid == 0) put_meta(a, w);
             tc_fence_before();
         }
     } else if (warp >= (CODES ? S::kMmaWarp : 8)) {
@@ -698,7 +698,7 @@ template <int KIND, int DP> cudaError_t launch(const AttnArgs &args, int sm_coun
         return cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs * S::kThreads >= S::kAllRegs;
     }();
     if (!enough) return cudaErrorLaunchOutOfResources;
-    *ctas = std::min(kAttnMaxCtas / 2, sm_count);
+    *ctas = std::min(kTensorMaxCtas, sm_count);
     void *p[] = {&a};
     return launch_pdl(f, dim3(static_cast<unsigned>(*ctas)), dim3(TensorShape<KIND, DP>::kThreads), TensorShape<KIND, DP>::kSmem, s, p);
 }

@@ -25,6 +25,8 @@
 // the ring holds is zeros or an earlier tile's, finite as all values of the cache.
 #pragma once
 
+#include <type_traits>
+
 #include "q4mm_attn.cuh"
 
 namespace q4 {
@@ -77,6 +79,25 @@ __device__ __forceinline__ uint4 lds128_at(uint32_t addr)
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
+// Eight values from element `at` on as words (16-bit values: 4, fp32: 8).
+template <bool VEC, int N> __device__ __forceinline__ void load_raw(const void *src, int64_t at, uint32_t (&w)[N])
+{
+    if constexpr (VEC) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(src) + at * (N / 2));
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 v = p[i];
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (N == 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = static_cast<const uint32_t *>(src)[at + i];
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(src) + at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | static_cast<uint32_t>(p[2 * i + 1]) << 16;
+    }
+}
 // Value scales up to v: e is raised so that they are below 2^e, and what the sums
 // so far are multiplied by is returned.
 __device__ __forceinline__ float raise(int &e, float v)
@@ -99,7 +120,10 @@ template <int KIND, int TERMS, int WM, int DP> struct WarpShape {
     static constexpr int kQBytes = kBlock * kQStride * TERMS;
     static constexpr int kRedBytes = WM * (kWN - 1) * 16 * DP / 2 * 4;   // sums handed over at an item's end, half the dims at once
     static constexpr int kFixed = kQBytes + kRedBytes + kBlock * 4 + 4 * 16 * 8 + 144;
-    static constexpr bool kQInRegs = DP <= 128 && TERMS == 1;
+    // Decode over codes is bound by its instructions' latencies: three CTAs an SM (128
+    // registers, queries from shared memory each time) instead of two.
+    static constexpr int kPerSM = DP > 128 ? 1 : KIND == kI8 && TERMS == 1 && WM == 1 ? 3 : 2;
+    static constexpr bool kQInRegs = DP <= 128 && TERMS == 1 && kPerSM == 2;
 };
 inline int warp_stage_bytes(int chunks, int ctype)
 {
@@ -117,7 +141,7 @@ __device__ __forceinline__ bool tile_wait(uint64_t *bar, uint32_t parity, uint64
 }
 
 template <int KIND, int TERMS, int WM, int DP>
-__global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::kPerSM) attn_warp_kernel(const AttnArgs a)
 {
     using S = WarpShape<KIND, TERMS, WM, DP>;
     constexpr bool BF = KIND == kBF16;
@@ -151,7 +175,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
     static_assert(S::kQBytes + S::kRedBytes >= 8 * (kMaxSeqs + 1), "room for the walk's scan");
     w.begin(a, reinterpret_cast<long long *>(qs));
     __syncthreads();
-    if (tid == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (tid == 0) a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
 
     if (warp == kComputeWarps) {
         // ---------------------------------------------------------- copies
@@ -241,17 +265,37 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
             constexpr int L = DP / 8, kRows = kComputeWarps * 32 / L, kPasses = S::kBlock / kRows, kBatch = kPasses < 4 ? kPasses : 4;
             const int x = tid % L;
             for (int r0 = tid / L; r0 < S::kBlock; r0 += kBatch * kRows) {
+                // (raw values first: all rows' loads are in flight together)
+                using Raw = Pack<float, TERMS == 2 ? 8 : 4, TERMS == 2 ? 32 : 16>;
+                Raw raw[kBatch];
+                const auto fetch = [&](auto whole_vectors) {
+#pragma unroll
+                    for (int p = 0; p < kBatch; ++p) {
+                        const int row = w.b * S::kBlock + r0 + p * kRows;
+#pragma unroll
+                        for (int i = 0; i < Raw::kWords; ++i) raw[p].w[i] = 0u;
+                        if (row < w.q.rows && 8 * x < a.c.d) {
+                            const int i = row / a.group, head = w.h * a.group + row - i * a.group;
+                            const int64_t at = (static_cast<int64_t>(w.q.start) + i) * a.ldq + head * a.c.d + 8 * x;
+                            load_raw<decltype(whole_vectors)::value>(a.Q, at, raw[p].w);
+                        }
+                    }
+                };
+                if (a.vec) fetch(std::true_type{});
+                else fetch(std::false_type{});
                 float f[kBatch][8];
 #pragma unroll
-                for (int p = 0; p < kBatch; ++p) {
-                    const int row = w.b * S::kBlock + r0 + p * kRows;
+                for (int p = 0; p < kBatch; ++p)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[p][i] = 0.0f;
-                    if (row < w.q.rows && 8 * x < a.c.d) {
-                        const int i = row / a.group, head = w.h * a.group + row - i * a.group;
-                        query8(a, (static_cast<int64_t>(w.q.start) + i) * a.ldq + head * a.c.d + 8 * x, f[p]);
+                    for (int i = 0; i < 8; ++i) {
+                        if constexpr (TERMS == 2) {
+                            f[p][i] = __uint_as_float(raw[p].w[i]);
+                        } else {
+                            const uint32_t u = raw[p].w[i / 2] >> (16 * (i & 1));
+                            const float as_half = __half2float(__ushort_as_half(static_cast<unsigned short>(u))), as_bf = __uint_as_float(u << 16);
+                            f[p][i] = KIND == kF16 ? as_half : KIND == kBF16 ? as_bf : a.type == Q4_TYPE_BF16 ? as_bf : as_half;
+                        }
                     }
-                }
 #pragma unroll
                 for (int p = 0; p < kBatch; ++p) {
                     const int r = r0 + p * kRows;
@@ -657,7 +701,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attn_warp_ker
                     part[S::kBlock * width + S::kBlock + r] = up ? l1 : l0;
                 }
             }
-            if (!whole && w.from == 0 && lane == 0 && wm == 0) a.meta[blockIdx.x] = make_int4(w.s, w.h, w.b, w.parts());
+            if (!whole && w.from == 0 && lane == 0 && wm == 0) put_meta(a, w);
         }
     }
 }
@@ -666,12 +710,12 @@ template <int KIND, int TERMS, int WM, int DP> cudaError_t launch_shape(AttnArgs
 {
     using S = WarpShape<KIND, TERMS, WM, DP>;
     const int stage = warp_stage_bytes(a.c.chunks, a.c.type);
-    // two CTAs an SM where two rings fit: their waits cover each other
-    const int fixed = S::kFixed;
-    const int two = static_cast<int>(kSmemPerSM / 2) - 1024 - fixed, one = static_cast<int>(kSmemOptIn) - fixed;
-    const int per_sm = DP <= 128 && two / stage >= 2 ? 2 : 1;
-    a.stages = std::min(8, (per_sm == 2 ? two : one) / stage);
-    const size_t smem = fixed + static_cast<size_t>(a.stages) * stage;
+    // several CTAs an SM where rings of two tiles fit: their waits cover each other
+    int per_sm = S::kPerSM;
+    const auto stages = [&] { return ((per_sm > 1 ? static_cast<int>(kSmemPerSM) / per_sm - 1024 : static_cast<int>(kSmemOptIn)) - S::kFixed) / stage; };
+    while (per_sm > 1 && stages() < 2) --per_sm;
+    a.stages = std::min(8, stages());
+    const size_t smem = S::kFixed + static_cast<size_t>(a.stages) * stage;
     const void *f = reinterpret_cast<const void *>(&attn_warp_kernel<KIND, TERMS, WM, DP>);
     cudaError_t e = set_max_smem(f, kSmemOptIn);
     if (e != cudaSuccess) return e;

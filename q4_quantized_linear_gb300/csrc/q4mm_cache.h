@@ -61,7 +61,7 @@ cudaError_t launch_kv_write(const KvRowsArgs &a, int type, bool vec, int sm_coun
 cudaError_t launch_kv_read(const KvRowsArgs &a, int type, bool vec, int sm_count, cudaStream_t s);
 
 // Most CTAs of the attention's kernels: what the scratch is laid out for.
-constexpr int kAttnMaxCtas = 320;
+constexpr int kAttnMaxCtas = 480, kTensorMaxCtas = 160;
 constexpr int kWarpTile = 64;       // tokens of a tile of the warp-MMA kernel
 constexpr int kTensorRows = 256, kTensorTile = 128;   // query rows and tokens of a tile of the tcgen05 kernel
 // Query rows of a sequence and head (new tokens x query heads that share it)
@@ -85,7 +85,7 @@ struct AttnArgs {
     int tile, block;          // tokens of a tile, query rows of a block
     int stages;
     float *parts;             // [2 * CTAs] of block x (64 * chunks) sums, then [block] maxima and sums
-    int4 *meta;               // [CTAs]: an item whose parts are to be joined
+    int4 *meta;               // [CTAs][2]: an item whose parts are to be joined
     int *status;
     uint64_t wait_ns;
 };

@@ -14,7 +14,7 @@ constexpr int64_t kMaxRows = int64_t(1) << 30;     // rows x heads
 constexpr int64_t kMaxPageTokens = 1024;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;   // of a sequence
 constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxVerifyVocab = int64_t(1) << 20;
-constexpr size_t kMetaBytes = sizeof(int4) * kAttnMaxCtas;
+constexpr size_t kMetaBytes = 2 * sizeof(int4) * kAttnMaxCtas;
 
 cudaStream_t as_stream(q4mm_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
@@ -148,7 +148,7 @@ Q4MM_API size_t q4_attention_workspace_size(int64_t rows, int64_t n_seq, int64_t
     const int64_t group = heads / kv_heads;
     const int chunks = static_cast<int>(ceil_div(d, kChunk));
     int64_t parts = 2 * kAttnMaxCtas * attn_part_floats(block_of(rows * group), chunks);
-    if (tensor_takes(rows * group, chunks)) parts = std::max(parts, kAttnMaxCtas * attn_part_floats(kTensorRows, chunks));
+    if (tensor_takes(rows * group, chunks)) parts = std::max(parts, 2 * kTensorMaxCtas * attn_part_floats(kTensorRows, chunks));
     return kMetaBytes + sizeof(float) * static_cast<size_t>(parts);
 }
 

@@ -54,7 +54,7 @@ template <typename T, bool VEC> __device__ __forceinline__ void store8(T *row, i
 // Which sequence a row belongs to (-1: none) and its place in the cache. The
 // batch's description is read once into shared memory.
 struct Batch {
-    const int32_t *starts, *first;
+    const int32_t *starts, *at;
     int n_seq;
     __device__ __forceinline__ int seq_of(int64_t row) const
     {
@@ -66,18 +66,20 @@ struct Batch {
         }
         return lo < n_seq && starts[lo] <= row && row < starts[lo + 1] ? lo : -1;
     }
+    // the place of the sequence's first row of the batch
+    template <bool WRITE> __device__ __forceinline__ int64_t first(int s) const
+    {
+        return WRITE ? static_cast<int64_t>(at[s]) - (starts[s + 1] - starts[s]) : at[s];
+    }
 };
-template <bool WRITE>
-__device__ __forceinline__ Batch load_batch(const KvRowsArgs &a, int32_t *starts, int32_t *first)
+__device__ __forceinline__ Batch load_batch(const KvRowsArgs &a, int32_t *starts, int32_t *at)
 {
-    for (int i = threadIdx.x; i <= a.n_seq; i += blockDim.x) starts[i] = a.starts[i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.n_seq; i += blockDim.x) {
-        const int at = a.at ? a.at[i] : 0;
-        first[i] = WRITE ? at - max(starts[i + 1] - starts[i], 0) : at;
+    for (int i = threadIdx.x; i <= a.n_seq; i += blockDim.x) {
+        starts[i] = a.starts[i];
+        if (i < a.n_seq) at[i] = a.at ? a.at[i] : 0;
     }
     __syncthreads();
-    return Batch{starts, first, a.n_seq};
+    return Batch{starts, at, a.n_seq};
 }
 // The block of head h in the page of position pos, or nullptr: a position or a
 // page that the cache does not have is recorded and left out.
@@ -108,23 +110,30 @@ template <typename C> __device__ __forceinline__ bool finite8(const Pack<C, 8> &
 // C: the cache's element type (int8_t: codes).
 template <typename T, typename C, int L, bool VEC> __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvRowsArgs a)
 {
-    __shared__ int32_t starts[kMaxSeqs + 1], first[kMaxSeqs];
+    __shared__ int32_t starts[kMaxSeqs + 1], at[kMaxSeqs];
     pdl_wait();
     pdl_launch_dependents();
-    const Batch batch = load_batch<true>(a, starts, first);
     const KvCache &kc = a.c;
     const int l = threadIdx.x % L, c = 8 * l, chunk = c / kChunk, u = l % 8;
     const unsigned lanes = L == 32 ? 0xFFFFFFFFu : ((1u << L) - 1u) << (threadIdx.x % 32 / L * L);
     const int64_t items = a.rows * kc.heads, step = static_cast<int64_t>(gridDim.x) * (kThreads / L);
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / L) + threadIdx.x / L; it < items; it += step) {
+    int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
+    float k[8], v[8];
+    const auto load = [&] {
+        const int64_t row = it / kc.heads;
+        const int h = static_cast<int>(it - row * kc.heads);
+        load8<T, VEC>(static_cast<const T *>(a.K) + row * a.ldk + h * kc.d, c, kc.d, k);
+        load8<T, VEC>(static_cast<const T *>(a.V) + row * a.ldv + h * kc.d, c, kc.d, v);
+    };
+    if (it < items) load();                                 // next to the batch's description
+    const Batch batch = load_batch(a, starts, at);
+    for (bool first = true; it < items; it += step, first = false) {
         const int64_t row = it / kc.heads;
         const int h = static_cast<int>(it - row * kc.heads);
         const int seq = batch.seq_of(row);
         if (seq < 0) continue;
-        float k[8], v[8];
-        load8<T, VEC>(static_cast<const T *>(a.K) + row * a.ldk + h * kc.d, c, kc.d, k);
-        load8<T, VEC>(static_cast<const T *>(a.V) + row * a.ldv + h * kc.d, c, kc.d, v);
-        const int64_t pos = first[seq] + (row - starts[seq]);
+        if (!first) load();
+        const int64_t pos = batch.first<true>(seq) + (row - starts[seq]);
         uint8_t *block = block_of(a, seq, pos, h);
         const int t = static_cast<int>(pos) & (kc.page_tokens - 1);
         if constexpr (sizeof(C) == 1) {
@@ -143,10 +152,10 @@ template <typename T, typename C, int L, bool VEC> __global__ void __launch_boun
             int ck[8], cv[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) ck[i] = code_of(k[i], sk.factor), cv[i] = code_of(v[i], sv.factor);
-            const int at = (chunk * kc.page_tokens + t) * kChunk + (((u >> 1) ^ ((t >> 1) & 3)) << 4) + 8 * (u & 1);
+            const int place = (chunk * kc.page_tokens + t) * kChunk + (((u >> 1) ^ ((t >> 1) & 3)) << 4) + 8 * (u & 1);
             const int half = kc.chunks * kc.page_tokens * kChunk;
-            store_pack<int8_t, 8>(reinterpret_cast<int8_t *>(block + at), 0, 8, pack_codes<8>(ck));
-            store_pack<int8_t, 8>(reinterpret_cast<int8_t *>(block + half + at), 0, 8, pack_codes<8>(cv));
+            store_pack<int8_t, 8>(reinterpret_cast<int8_t *>(block + place), 0, 8, pack_codes<8>(ck));
+            store_pack<int8_t, 8>(reinterpret_cast<int8_t *>(block + half + place), 0, 8, pack_codes<8>(cv));
             if (l == 0) {
                 float *scales = reinterpret_cast<float *>(block + 2 * half);
                 scales[t] = sk.scale;
@@ -160,19 +169,19 @@ template <typename T, typename C, int L, bool VEC> __global__ void __launch_boun
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pk.w[i] = 0x7FFF7FFFu, pv.w[i] = 0u;
             }
-            const int at = (chunk * kc.page_tokens + t) * 128 + ((u ^ (t & 7)) << 4);
-            store_pack<C, 8>(reinterpret_cast<C *>(block + at), 0, 8, pk);
-            store_pack<C, 8>(reinterpret_cast<C *>(block + kc.chunks * kc.page_tokens * 128 + at), 0, 8, pv);
+            const int place = (chunk * kc.page_tokens + t) * 128 + ((u ^ (t & 7)) << 4);
+            store_pack<C, 8>(reinterpret_cast<C *>(block + place), 0, 8, pk);
+            store_pack<C, 8>(reinterpret_cast<C *>(block + kc.chunks * kc.page_tokens * 128 + place), 0, 8, pv);
         }
     }
 }
 
 template <typename T, typename C, int L, bool VEC> __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvRowsArgs a)
 {
-    __shared__ int32_t starts[kMaxSeqs + 1], first[kMaxSeqs];
+    __shared__ int32_t starts[kMaxSeqs + 1], at[kMaxSeqs];
     pdl_wait();
     pdl_launch_dependents();
-    const Batch batch = load_batch<false>(a, starts, first);
+    const Batch batch = load_batch(a, starts, at);
     const KvCache &kc = a.c;
     const int l = threadIdx.x % L, c = 8 * l, chunk = c / kChunk, u = l % 8;
     const int64_t items = a.rows * kc.heads, step = static_cast<int64_t>(gridDim.x) * (kThreads / L);
@@ -181,15 +190,15 @@ template <typename T, typename C, int L, bool VEC> __global__ void __launch_boun
         const int h = static_cast<int>(it - row * kc.heads);
         const int seq = batch.seq_of(row);
         if (seq < 0 || c >= kc.d) continue;
-        const int64_t pos = first[seq] + (row - starts[seq]);
+        const int64_t pos = batch.first<false>(seq) + (row - starts[seq]);
         const uint8_t *block = block_of(a, seq, pos, h);
         const int t = static_cast<int>(pos) & (kc.page_tokens - 1);
         float k[8] = {}, v[8] = {};
         if (block) {
             if constexpr (sizeof(C) == 1) {
-                const int at = (chunk * kc.page_tokens + t) * kChunk + (((u >> 1) ^ ((t >> 1) & 3)) << 4) + 8 * (u & 1);
+                const int place = (chunk * kc.page_tokens + t) * kChunk + (((u >> 1) ^ ((t >> 1) & 3)) << 4) + 8 * (u & 1);
                 const int half = kc.chunks * kc.page_tokens * kChunk;
-                const uint2 wk = *reinterpret_cast<const uint2 *>(block + at), wv = *reinterpret_cast<const uint2 *>(block + half + at);
+                const uint2 wk = *reinterpret_cast<const uint2 *>(block + place), wv = *reinterpret_cast<const uint2 *>(block + half + place);
                 const float *scales = reinterpret_cast<const float *>(block + 2 * half);
                 const float sk = scales[t], sv = scales[kc.page_tokens + t];
 #pragma unroll
@@ -199,9 +208,9 @@ template <typename T, typename C, int L, bool VEC> __global__ void __launch_boun
                     v[i] = sv * static_cast<float>(static_cast<int8_t>(b4 >> (8 * (i & 3))));
                 }
             } else {
-                const int at = (chunk * kc.page_tokens + t) * 128 + ((u ^ (t & 7)) << 4);
-                const Pack<C, 8> pk = load_pack<C, 8>(reinterpret_cast<const C *>(block + at), 0, 8);
-                const Pack<C, 8> pv = load_pack<C, 8>(reinterpret_cast<const C *>(block + kc.chunks * kc.page_tokens * 128 + at), 0, 8);
+                const int place = (chunk * kc.page_tokens + t) * 128 + ((u ^ (t & 7)) << 4);
+                const Pack<C, 8> pk = load_pack<C, 8>(reinterpret_cast<const C *>(block + place), 0, 8);
+                const Pack<C, 8> pv = load_pack<C, 8>(reinterpret_cast<const C *>(block + kc.chunks * kc.page_tokens * 128 + place), 0, 8);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) k[i] = elem(pk, i), v[i] = elem(pv, i);
             }
