@@ -107,123 +107,184 @@ template <typename C> __device__ __forceinline__ bool finite8(const Pack<C, 8> &
     return ok;
 }
 
+// code_of() of eight values: the product, rounded, plus 1.5 2^23 has the nearest
+// integer (halves to even) in its low bits. (By conversions the kernel was bound by
+// them: 4 prompts of 2048 fp32 into int8, 67 MB.)
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float factor)
+{
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(__fadd_rn(__fmul_rn(x[i], factor), 12582912.0f));
+    uint2 w;
+    w.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    w.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    if (factor == 0.0f) w = make_uint2(0u, 0u);
+    return w;
+}
+
+// Heads' rows that a thread has in flight: its loads' latency, not the rate, bounds one
+// (4 prompts of 2048 fp32 into int8: 17 us with one, 67 MB).
+constexpr int kWriteAhead = 1, kReadAhead = 4, kBlocksPerSM = 8;
+
 // C: the cache's element type (int8_t: codes).
 template <typename T, typename C, int L, bool VEC> __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvRowsArgs a)
 {
     __shared__ int32_t starts[kMaxSeqs + 1], at[kMaxSeqs];
+    constexpr int U = kWriteAhead, G = kThreads / L;
     pdl_wait();
     pdl_launch_dependents();
     const KvCache &kc = a.c;
     const int l = threadIdx.x % L, c = 8 * l, chunk = c / kChunk, u = l % 8;
-    const unsigned lanes = L == 32 ? 0xFFFFFFFFu : ((1u << L) - 1u) << (threadIdx.x % 32 / L * L);
-    const int64_t items = a.rows * kc.heads, step = static_cast<int64_t>(gridDim.x) * (kThreads / L);
-    int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-    float k[8], v[8];
-    const auto load = [&] {
-        const int64_t row = it / kc.heads;
-        const int h = static_cast<int>(it - row * kc.heads);
-        load8<T, VEC>(static_cast<const T *>(a.K) + row * a.ldk + h * kc.d, c, kc.d, k);
-        load8<T, VEC>(static_cast<const T *>(a.V) + row * a.ldv + h * kc.d, c, kc.d, v);
-    };
-    if (it < items) load();                                 // next to the batch's description
-    const Batch batch = load_batch(a, starts, at);
-    for (bool first = true; it < items; it += step, first = false) {
-        const int64_t row = it / kc.heads;
-        const int h = static_cast<int>(it - row * kc.heads);
-        const int seq = batch.seq_of(row);
-        if (seq < 0) continue;
-        if (!first) load();
-        const int64_t pos = batch.first<true>(seq) + (row - starts[seq]);
-        uint8_t *block = block_of(a, seq, pos, h);
-        const int t = static_cast<int>(pos) & (kc.page_tokens - 1);
-        if constexpr (sizeof(C) == 1) {
-            uint32_t mk = 0, mv = 0;
+    const int items = static_cast<int>(a.rows) * kc.heads;
+    float k[U][8], v[U][8];
+    int row[U], h[U];
+    const auto load = [&](int base) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mk = max(mk, abs_bits(k[i])), mv = max(mv, abs_bits(v[i]));
-#pragma unroll
-            for (int o = L / 2; o > 0; o /= 2) {
-                mk = max(mk, __shfl_xor_sync(lanes, mk, o));
-                mv = max(mv, __shfl_xor_sync(lanes, mv, o));
-            }
-            if (!block || chunk >= kc.chunks) continue;
-            // a token whose keys or values are not all finite: NaN keys, no values
-            const uint32_t bad = max(mk, mv) >= 0x7F800000u ? 0x7F800000u : 0u;
-            const CodeScale sk = code_scale(max(mk, bad)), sv = code_scale(bad ? 0u : mv);
-            int ck[8], cv[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ck[i] = code_of(k[i], sk.factor), cv[i] = code_of(v[i], sv.factor);
-            const int place = (chunk * kc.page_tokens + t) * kChunk + (((u >> 1) ^ ((t >> 1) & 3)) << 4) + 8 * (u & 1);
-            const int half = kc.chunks * kc.page_tokens * kChunk;
-            store_pack<int8_t, 8>(reinterpret_cast<int8_t *>(block + place), 0, 8, pack_codes<8>(ck));
-            store_pack<int8_t, 8>(reinterpret_cast<int8_t *>(block + half + place), 0, 8, pack_codes<8>(cv));
-            if (l == 0) {
-                float *scales = reinterpret_cast<float *>(block + 2 * half);
-                scales[t] = sk.scale;
-                scales[kc.page_tokens + t] = sv.scale;
-            }
-        } else {
-            Pack<C, 8> pk = pack_of<C, 8>(k), pv = pack_of<C, 8>(v);
-            const bool fine = __all_sync(lanes, finite8(pk) && finite8(pv)) != 0;
-            if (!block || chunk >= kc.chunks) continue;
-            if (!fine) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) pk.w[i] = 0x7FFF7FFFu, pv.w[i] = 0u;
-            }
-            const int place = (chunk * kc.page_tokens + t) * 128 + ((u ^ (t & 7)) << 4);
-            store_pack<C, 8>(reinterpret_cast<C *>(block + place), 0, 8, pk);
-            store_pack<C, 8>(reinterpret_cast<C *>(block + kc.chunks * kc.page_tokens * 128 + place), 0, 8, pv);
+        for (int i = 0; i < U; ++i) {
+            const int it = base + i * G + threadIdx.x / L;
+            row[i] = it / kc.heads, h[i] = it - row[i] * kc.heads;
+            const bool there = it < items;
+            if (!there) row[i] = -1;
+            load8<T, VEC>(static_cast<const T *>(a.K) + row[i] * a.ldk + h[i] * kc.d, there ? c : kc.d, kc.d, k[i]);
+            load8<T, VEC>(static_cast<const T *>(a.V) + row[i] * a.ldv + h[i] * kc.d, there ? c : kc.d, kc.d, v[i]);
         }
+    };
+    int base = static_cast<int>(blockIdx.x) * (U * G);
+    load(base);                                             // next to the batch's description
+    const Batch batch = load_batch(a, starts, at);
+    while (true) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int seq = row[i] < 0 ? -1 : batch.seq_of(row[i]);
+            const int64_t pos = seq < 0 ? 0 : batch.first<true>(seq) + (row[i] - starts[seq]);
+            uint8_t *block = seq < 0 ? nullptr : block_of(a, seq, pos, h[i]);
+            const bool store = block && chunk < kc.chunks;
+            const int t = static_cast<int>(pos) & (kc.page_tokens - 1);
+            if constexpr (sizeof(C) == 1) {
+                uint32_t mk = 0, mv = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mk = max(mk, abs_bits(k[i][j])), mv = max(mv, abs_bits(v[i][j]));
+#pragma unroll
+                for (int o = L / 2; o > 0; o /= 2) {
+                    mk = max(mk, __shfl_xor_sync(0xFFFFFFFFu, mk, o));
+                    mv = max(mv, __shfl_xor_sync(0xFFFFFFFFu, mv, o));
+                }
+                // a token whose keys or values are not all finite: NaN keys, no values
+                const uint32_t bad = max(mk, mv) >= 0x7F800000u ? 0x7F800000u : 0u;
+                const CodeScale sk = code_scale(max(mk, bad)), sv = code_scale(bad ? 0u : mv);
+                const uint2 ck = codes8(k[i], sk.factor), cv = codes8(v[i], sv.factor);
+                const int place = (chunk * kc.page_tokens + t) * kChunk + (((u >> 1) ^ ((t >> 1) & 3)) << 4) + 8 * (u & 1);
+                const int half = kc.chunks * kc.page_tokens * kChunk;
+                if (store) {
+                    *reinterpret_cast<uint2 *>(block + place) = ck;
+                    *reinterpret_cast<uint2 *>(block + half + place) = cv;
+                    if (l == 0) {
+                        float *scales = reinterpret_cast<float *>(block + 2 * half);
+                        scales[t] = sk.scale;
+                        scales[kc.page_tokens + t] = sv.scale;
+                    }
+                }
+            } else {
+                Pack<C, 8> pk = pack_of<C, 8>(k[i]), pv = pack_of<C, 8>(v[i]);
+                uint32_t bad = finite8(pk) && finite8(pv) ? 0u : 1u;
+#pragma unroll
+                for (int o = L / 2; o > 0; o /= 2) bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, o);
+                if (bad) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) pk.w[j] = 0x7FFF7FFFu, pv.w[j] = 0u;
+                }
+                const int place = (chunk * kc.page_tokens + t) * 128 + ((u ^ (t & 7)) << 4);
+                if (store) {
+                    store_pack<C, 8>(reinterpret_cast<C *>(block + place), 0, 8, pk);
+                    store_pack<C, 8>(reinterpret_cast<C *>(block + kc.chunks * kc.page_tokens * 128 + place), 0, 8, pv);
+                }
+            }
+        }
+        const int64_t next = static_cast<int64_t>(base) + static_cast<int64_t>(gridDim.x) * (U * G);
+        if (next >= items) break;
+        base = static_cast<int>(next);
+        load(base);
     }
 }
 
 template <typename T, typename C, int L, bool VEC> __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvRowsArgs a)
 {
     __shared__ int32_t starts[kMaxSeqs + 1], at[kMaxSeqs];
+    constexpr int U = kReadAhead, G = kThreads / L;
     pdl_wait();
     pdl_launch_dependents();
     const Batch batch = load_batch(a, starts, at);
     const KvCache &kc = a.c;
     const int l = threadIdx.x % L, c = 8 * l, chunk = c / kChunk, u = l % 8;
-    const int64_t items = a.rows * kc.heads, step = static_cast<int64_t>(gridDim.x) * (kThreads / L);
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / L) + threadIdx.x / L; it < items; it += step) {
-        const int64_t row = it / kc.heads;
-        const int h = static_cast<int>(it - row * kc.heads);
-        const int seq = batch.seq_of(row);
-        if (seq < 0 || c >= kc.d) continue;
-        const int64_t pos = batch.first<false>(seq) + (row - starts[seq]);
-        const uint8_t *block = block_of(a, seq, pos, h);
-        const int t = static_cast<int>(pos) & (kc.page_tokens - 1);
-        float k[8] = {}, v[8] = {};
-        if (block) {
-            if constexpr (sizeof(C) == 1) {
-                const int place = (chunk * kc.page_tokens + t) * kChunk + (((u >> 1) ^ ((t >> 1) & 3)) << 4) + 8 * (u & 1);
+    const int items = static_cast<int>(a.rows) * kc.heads;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * (U * G); base < items; base += static_cast<int64_t>(gridDim.x) * (U * G)) {
+        const uint8_t *block[U];
+        int row[U], h[U], t[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int it = static_cast<int>(base) + i * G + threadIdx.x / L;
+            row[i] = it / kc.heads, h[i] = it - row[i] * kc.heads;
+            const int seq = it < items && c < kc.d ? batch.seq_of(row[i]) : -1;
+            if (seq < 0) row[i] = -1;
+            const int64_t pos = seq < 0 ? 0 : batch.first<false>(seq) + (row[i] - starts[seq]);
+            block[i] = seq < 0 ? nullptr : block_of(a, seq, pos, h[i]);
+            t[i] = static_cast<int>(pos) & (kc.page_tokens - 1);
+        }
+        if constexpr (sizeof(C) == 1) {
+            uint2 wk[U], wv[U];
+            float sk[U], sv[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int place = (chunk * kc.page_tokens + t[i]) * kChunk + (((u >> 1) ^ ((t[i] >> 1) & 3)) << 4) + 8 * (u & 1);
                 const int half = kc.chunks * kc.page_tokens * kChunk;
-                const uint2 wk = *reinterpret_cast<const uint2 *>(block + place), wv = *reinterpret_cast<const uint2 *>(block + half + place);
-                const float *scales = reinterpret_cast<const float *>(block + 2 * half);
-                const float sk = scales[t], sv = scales[kc.page_tokens + t];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t a4 = i < 4 ? wk.x : wk.y, b4 = i < 4 ? wv.x : wv.y;
-                    k[i] = sk * static_cast<float>(static_cast<int8_t>(a4 >> (8 * (i & 3))));
-                    v[i] = sv * static_cast<float>(static_cast<int8_t>(b4 >> (8 * (i & 3))));
+                wk[i] = make_uint2(0u, 0u), wv[i] = wk[i], sk[i] = 0.0f, sv[i] = 0.0f;
+                if (block[i]) {
+                    wk[i] = *reinterpret_cast<const uint2 *>(block[i] + place), wv[i] = *reinterpret_cast<const uint2 *>(block[i] + half + place);
+                    const float *scales = reinterpret_cast<const float *>(block[i] + 2 * half);
+                    sk[i] = scales[t[i]], sv[i] = scales[kc.page_tokens + t[i]];
                 }
-            } else {
-                const int place = (chunk * kc.page_tokens + t) * 128 + ((u ^ (t & 7)) << 4);
-                const Pack<C, 8> pk = load_pack<C, 8>(reinterpret_cast<const C *>(block + place), 0, 8);
-                const Pack<C, 8> pv = load_pack<C, 8>(reinterpret_cast<const C *>(block + kc.chunks * kc.page_tokens * 128 + place), 0, 8);
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) k[i] = elem(pk, i), v[i] = elem(pv, i);
+            for (int i = 0; i < U; ++i) {
+                if (row[i] < 0) continue;
+                float k[8], v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t a4 = j < 4 ? wk[i].x : wk[i].y, b4 = j < 4 ? wv[i].x : wv[i].y;
+                    k[j] = sk[i] * static_cast<float>(static_cast<int8_t>(a4 >> (8 * (j & 3))));
+                    v[j] = sv[i] * static_cast<float>(static_cast<int8_t>(b4 >> (8 * (j & 3))));
+                }
+                store8<T, VEC>(static_cast<T *>(a.K) + row[i] * a.ldk + h[i] * kc.d, c, kc.d, k);
+                store8<T, VEC>(static_cast<T *>(a.V) + row[i] * a.ldv + h[i] * kc.d, c, kc.d, v);
+            }
+        } else {
+            Pack<C, 8> pk[U], pv[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int place = (chunk * kc.page_tokens + t[i]) * 128 + ((u ^ (t[i] & 7)) << 4);
+                pk[i] = zero_pack<C, 8>(), pv[i] = pk[i];
+                if (block[i]) {
+                    pk[i] = load_pack<C, 8>(reinterpret_cast<const C *>(block[i] + place), 0, 8);
+                    pv[i] = load_pack<C, 8>(reinterpret_cast<const C *>(block[i] + kc.chunks * kc.page_tokens * 128 + place), 0, 8);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (row[i] < 0) continue;
+                float k[8], v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) k[j] = elem(pk[i], j), v[j] = elem(pv[i], j);
+                store8<T, VEC>(static_cast<T *>(a.K) + row[i] * a.ldk + h[i] * kc.d, c, kc.d, k);
+                store8<T, VEC>(static_cast<T *>(a.V) + row[i] * a.ldv + h[i] * kc.d, c, kc.d, v);
             }
         }
-        store8<T, VEC>(static_cast<T *>(a.K) + row * a.ldk + h * kc.d, c, kc.d, k);
-        store8<T, VEC>(static_cast<T *>(a.V) + row * a.ldv + h * kc.d, c, kc.d, v);
     }
 }
 
 template <typename T, typename C, int L, bool VEC, bool WRITE> cudaError_t launch(KvRowsArgs a, int sm_count, cudaStream_t s)
 {
-    const int64_t items = a.rows * a.c.heads;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(ceil_div(items, kThreads / L), int64_t(sm_count) * 16));
+    const int64_t items = a.rows * a.c.heads, block = (WRITE ? kWriteAhead : kReadAhead) * (kThreads / L);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(ceil_div(items, block), int64_t(sm_count) * kBlocksPerSM));
     void *args[] = {&a};
     const void *f = WRITE ? reinterpret_cast<const void *>(&kv_write_kernel<T, C, L, VEC>)
                           : reinterpret_cast<const void *>(&kv_read_kernel<T, C, L, VEC>);
