@@ -263,27 +263,24 @@ __device__ __forceinline__ void store8_out(const AttnArgs &a, int64_t at, const 
     }
 }
 
-// A row's 8 values from dim c on, as fp32 (zeros past d).
-template <typename T> __device__ __forceinline__ void row8(const T *p, bool vec, float (&f)[8])
+// Eight values from element `at` on as words (16-bit values: 4, fp32: 8).
+template <bool VEC, int N> __device__ __forceinline__ void load_raw(const void *src, int64_t at, uint32_t (&w)[N])
 {
-    if (vec) {
-        constexpr int V = 16 / sizeof(T);
+    if constexpr (VEC) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(src) + at * (N / 2));
 #pragma unroll
-        for (int j = 0; j < 8 / V; ++j) {
-            const Pack<T, V> x = load_pack<T, V>(p, j * V, 8);
-#pragma unroll
-            for (int i = 0; i < V; ++i) f[j * V + i] = elem(x, i);
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 v = p[i];
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
         }
-    } else {
+    } else if constexpr (N == 8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = elem(load_pack<T, 1>(p, i, 8), 0);
+        for (int i = 0; i < 8; ++i) w[i] = static_cast<const uint32_t *>(src)[at + i];
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(src) + at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | static_cast<uint32_t>(p[2 * i + 1]) << 16;
     }
-}
-__device__ __forceinline__ void query8(const AttnArgs &a, int64_t at, float (&f)[8])
-{
-    if (a.type == Q4_TYPE_F32) row8(static_cast<const float *>(a.Q) + at, a.vec, f);
-    else if (a.type == Q4_TYPE_F16) row8(static_cast<const __half *>(a.Q) + at, a.vec, f);
-    else row8(static_cast<const __nv_bfloat16 *>(a.Q) + at, a.vec, f);
 }
 
 } // namespace q4

@@ -20,6 +20,7 @@
 //   A page's rows past the sequence's end are never copied: what their place holds
 // is zeros or an earlier tile's values, finite as all values of the cache.
 #include <algorithm>
+#include <type_traits>
 
 #include "q4mm_attn.cuh"
 
@@ -190,52 +191,66 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 continue;
             }
             const int first_row = w.b * kTensorRows + half * kHalf + (warp & 3) * 32;
-            // the warp's 32 rows of Q, two or four at a time, into the operand's image
-            constexpr int kLanes = DP / 8, kRows = 32 / kLanes;
-#pragma unroll 4
-            for (int r0 = 0; r0 < 32; r0 += kRows) {
-                const int r = r0 + lane / kLanes, x = lane % kLanes, row = first_row + r;
-                float f[8] = {};
-                if (row < w.q.rows && 8 * x < a.c.d) {
-                    const int i = row / a.group, head = w.h * a.group + row - i * a.group;
-                    query8(a, (static_cast<int64_t>(w.q.start) + i) * a.ldq + head * a.c.d + 8 * x, f);
-                }
-                if constexpr (CODES) {
-                    // to fp16's range by a power of two: the largest in 2^12 .. 2^13
-                    uint32_t mb = 0;
+            // the warp's 32 rows of Q, two or four an access, eight accesses in flight, into
+            // the operand's image
+            constexpr int kLanes = DP / 8, kRows = 32 / kLanes, kBatch = 8;
+            const int x = lane % kLanes;
+#pragma unroll 1
+            for (int r0 = lane / kLanes; r0 < 32; r0 += kBatch * kRows) {
+                uint32_t raw[kBatch][4];
+                const auto fetch = [&](auto vec) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) mb = max(mb, abs_bits(f[i]));
+                    for (int p = 0; p < kBatch; ++p) {
+                        const int row = first_row + r0 + p * kRows;
 #pragma unroll
-                    for (int o = kLanes / 2; o > 0; o /= 2) mb = max(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, o));
-                    float factor = a.scale_log2;
-                    if (mb >= 0x7F800000u) {
-                        factor = __uint_as_float(0x7FC00000u);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-                    } else if (mb != 0u) {
-                        const int e = min(max(139 - static_cast<int>(mb >> 23), -126), 126);
-                        const float up = pow2(e);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] *= up;
-                        factor *= pow2(-e);
+                        for (int i = 0; i < 4; ++i) raw[p][i] = 0u;
+                        if (row < w.q.rows && 8 * x < a.c.d) {
+                            const int i = row / a.group, head = w.h * a.group + row - i * a.group;
+                            load_raw<decltype(vec)::value>(a.Q, (static_cast<int64_t>(w.q.start) + i) * a.ldq + head * a.c.d + 8 * x, raw[p]);
+                        }
                     }
-                    if (x == 0) row_factor[half * kHalf + (warp & 3) * 32 + r] = factor;
-                }
-                uint32_t u[4];
+                };
+                if (a.vec) fetch(std::true_type{});
+                else fetch(std::false_type{});
 #pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] = BF ? pack_bf16x2_rn(f[2 * i], f[2 * i + 1]) : pack_f16x2_rn(f[2 * i], f[2 * i + 1]);
-                const int rr = (warp & 3) * 32 + r;
-                sts128(qs + (half * CH + x / 8) * kAtomRows + rr * 128 + (((x & 7) ^ (rr & 7)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
+                for (int p = 0; p < kBatch; ++p) {
+                    const int r = (warp & 3) * 32 + r0 + p * kRows;
+                    if constexpr (CODES) {
+                        // to fp16's range by a power of two: the largest in 2^12 .. 2^13
+                        float f[8];
+                        uint32_t mb = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t u = raw[p][i / 2] >> (16 * (i & 1));
+                            f[i] = a.type == Q4_TYPE_BF16 ? __uint_as_float(u << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
+                            mb = max(mb, abs_bits(f[i]));
+                        }
+#pragma unroll
+                        for (int o = kLanes / 2; o > 0; o /= 2) mb = max(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, o));
+                        float factor = a.scale_log2, up = 1.0f;
+                        if (mb >= 0x7F800000u) {
+                            factor = __uint_as_float(0x7FC00000u);
+                        } else if (mb != 0u) {
+                            const int e = min(max(139 - static_cast<int>(mb >> 23), -126), 126);
+                            up = pow2(e);
+                            factor *= pow2(-e);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) raw[p][i] = mb >= 0x7F800000u ? 0u : pack_f16x2_rn(f[2 * i] * up, f[2 * i + 1] * up);
+                        if (x == 0) row_factor[half * kHalf + r] = factor;
+                    }
+                    sts128(qs + (half * CH + x / 8) * kAtomRows + r * 128 + (((x & 7) ^ (r & 7)) << 4), make_uint4(raw[p][0], raw[p][1], raw[p][2], raw[p][3]));
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->q_full[half]);
             const int my_row = first_row + lane;
             const float rf = CODES ? row_factor[half * kHalf + (warp & 3) * 32 + lane] : a.scale_log2;
-            int lo, hi, full_from, full_upto, x;
+            int lo, hi, full_from, full_upto, other;
             row_range(a, w.q, min(my_row, w.q.rows - 1), lo, hi);
-            row_range(a, w.q, min(first_row, w.q.rows - 1), x, full_upto);
-            row_range(a, w.q, min(first_row + 31, w.q.rows - 1), full_from, x);
+            row_range(a, w.q, min(first_row, w.q.rows - 1), other, full_upto);
+            row_range(a, w.q, min(first_row + 31, w.q.rows - 1), full_from, other);
             const int end = min(w.hi, w.q.len);
             hi = min(hi, end);
             float m = neg_inf(), l = 0.0f;
@@ -364,36 +379,61 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             const float mul = whole ? (l == 0.0f ? 0.0f : back / l) : back;
             const int i = my_row / a.group, head = w.h * a.group + my_row - i * a.group;
             const int64_t out = (static_cast<int64_t>(w.q.start) + i) * a.ldo + static_cast<int64_t>(head) * a.c.d;
+            if (whole && !a.vec) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < DP; c0 += 16) {
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(o_at + c0, o);
-                tmem_wait_ld();
+                for (int c0 = 0; c0 < DP; c0 += 16) {
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(o_at + c0, o);
+                    tmem_wait_ld();
+                    if (my_row < w.q.rows) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * mul);
-                if (my_row >= w.q.rows) {
-                    // nothing of this row is kept
-                } else if (!whole) {
+                        for (int j = 0; j < 16; j += 2)
+                            if (c0 + j < a.c.d) store2_out(a, out + c0 + j, __uint_as_float(o[j]) * mul, __uint_as_float(o[j + 1]) * mul);
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // 128 bytes of each of the warp's rows at a time, through the place of its
+                // rows of Q, so that a row's bytes leave together (a thread's 16 bytes by
+                // themselves made an item's end 16 us)
+                uint8_t *const stage = qs + half * CH * kAtomRows + (warp & 3) * 4096;
+                const bool bf = a.type == Q4_TYPE_BF16;
+                const int left = w.q.rows - first_row;                 // rows of the warp that exist
+#pragma unroll 1
+                for (int c0 = 0; c0 < DP; c0 += whole ? 64 : 32) {
+                    uint32_t u[32];
+                    if (whole) {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        *reinterpret_cast<uint4 *>(part + r_in * DP + c0 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                } else {
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(o_at + c0 + 32 * i, o);
+                            tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; j += 8) {
-                        if (c0 + j >= a.c.d) continue;
-                        uint32_t v[4];
-                        const bool bf = a.type == Q4_TYPE_BF16;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float x0f = __uint_as_float(o[j + 2 * k]), x1f = __uint_as_float(o[j + 2 * k + 1]);
-                            v[k] = bf ? pack_bf16x2_rn(x0f, x1f) : pack_f16x2_rn(x0f, x1f);
+                            for (int j = 0; j < 16; ++j) {
+                                const float y0 = __uint_as_float(o[2 * j]) * mul, y1 = __uint_as_float(o[2 * j + 1]) * mul;
+                                u[16 * i + j] = bf ? pack_bf16x2_rn(y0, y1) : pack_f16x2_rn(y0, y1);
+                            }
                         }
-                        uint16_t *dst = static_cast<uint16_t *>(a.O) + out + c0 + j;
-                        if (a.vec) {
-                            *reinterpret_cast<uint4 *>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
-                        } else {
+                    } else {
+                        tmem_ld_32x32b_x32(o_at + c0, u);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) dst[k] = static_cast<uint16_t>(v[k / 2] >> (16 * (k & 1)));
+                        for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * mul);
+                    }
+                    __syncwarp();                                      // what was staged before is out
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sts128(stage + lane * 128 + ((i ^ (lane & 7)) << 4), make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]));
+                    __syncwarp();
+                    const int unit = lane & 7;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = 4 * i + (lane >> 3);
+                        const uint4 v = lds128(stage + row * 128 + ((unit ^ (row & 7)) << 4));
+                        const long long to = __shfl_sync(0xFFFFFFFFu, static_cast<long long>(out), row);
+                        if (row < left) {
+                            if (!whole) *reinterpret_cast<uint4 *>(part + (half * kHalf + (warp & 3) * 32 + row) * DP + c0 + 4 * unit) = v;
+                            else if (c0 + 8 * unit < a.c.d) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.O) + to + c0 + 8 * unit) = v;
                         }
                     }
                 }

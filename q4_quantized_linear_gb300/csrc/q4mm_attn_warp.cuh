@@ -79,25 +79,6 @@ __device__ __forceinline__ uint4 lds128_at(uint32_t addr)
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
-// Eight values from element `at` on as words (16-bit values: 4, fp32: 8).
-template <bool VEC, int N> __device__ __forceinline__ void load_raw(const void *src, int64_t at, uint32_t (&w)[N])
-{
-    if constexpr (VEC) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(src) + at * (N / 2));
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const uint4 v = p[i];
-            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-        }
-    } else if constexpr (N == 8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = static_cast<const uint32_t *>(src)[at + i];
-    } else {
-        const uint16_t *p = static_cast<const uint16_t *>(src) + at;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | static_cast<uint32_t>(p[2 * i + 1]) << 16;
-    }
-}
 // Value scales up to v: e is raised so that they are below 2^e, and what the sums
 // so far are multiplied by is returned.
 __device__ __forceinline__ float raise(int &e, float v)
