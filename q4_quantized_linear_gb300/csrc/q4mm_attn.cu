@@ -174,6 +174,7 @@ cudaError_t launch_attn_join(const AttnArgs &args, int ctas, cudaStream_t s)
 cudaError_t launch_attn_warp(AttnArgs a, int sm_count, cudaStream_t s)
 {
     a.tile = kWarpTile;
+    a.item_cost = 2;
     int ctas = 0;
     const bool wide = a.type == Q4_TYPE_F32;
     cudaError_t e;

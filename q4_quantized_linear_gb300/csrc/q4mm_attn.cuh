@@ -4,12 +4,14 @@
 // An item is a block of query rows of one sequence and one cached head: row r of
 // a sequence stands for new token r / group and query head head * group + r %
 // group, so that all query heads of a cached head share what is read of it. An
-// item's work is its tiles of tokens, from the first that any row sees to the
-// last. The tiles of all items in a row (sequence, head, block, tile) are dealt
-// to the CTAs in equal contiguous shares: no host code needs to know the
-// sequences' lengths, and a long sequence is spread over many CTAs. An item that
-// is cut leaves parts (sums without their denominator, maxima, denominators),
-// which the join adds in the order of the tiles.
+// item's work is its tiles of tokens, from the first that any row sees to the last,
+// and a.item_cost tiles more for what an item costs beside them (windowed prompts,
+// whose first blocks have a tile or two: without, the CTA with the most items took
+// twice the average). The work of all items in a row (sequence, head, block, tile) is
+// dealt to the CTAs in equal contiguous shares: no host code needs to know the
+// sequences' lengths, and a long sequence is spread over many CTAs. An item that is
+// cut leaves parts (sums without their denominator, maxima, denominators), which the
+// join adds in the order of the tiles.
 #pragma once
 
 #include "q4mm_cache.h"
@@ -57,13 +59,17 @@ struct Walk {
     Seq q;
     int first, count, hi;     // its tiles
     int from, upto;           // those of them that are this CTA's
-    int left;                 // tiles of the share from this item on
+    int left;                 // work of the share from this item on
+    int used;                 // of it in this item
     int share;
 
     __device__ __forceinline__ bool whole() const { return from == 0 && upto == count; }
-    __device__ __forceinline__ void clip()
+    // The share starts at `y` of the item's work: first its cost, then a tile each.
+    __device__ __forceinline__ void clip(const AttnArgs &a, int y)
     {
-        upto = left < count - from ? from + left : count;
+        used = min(left, count + a.item_cost - y);
+        from = max(y - a.item_cost, 0);
+        upto = max(y + used - a.item_cost, 0);
     }
     // `scan`: shared memory of n_seq + 1 numbers, free again after the next barrier.
     __device__ __forceinline__ void begin(const AttnArgs &a, long long *scan)
@@ -79,7 +85,7 @@ struct Walk {
                 for (int j = threadIdx.x % lanes; j < x.blocks; j += lanes) {
                     int f, n, e;
                     block_tiles(a, x, j, f, n, e);
-                    w += n;
+                    w += n + a.item_cost;
                 }
             }
             for (int o = lanes / 2; o > 0; o /= 2) w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
@@ -134,7 +140,7 @@ struct Walk {
             long long upto_b = 0;
             if (b + lane < q.blocks) {
                 block_tiles(a, q, b + lane, first, count, hi);
-                upto_b = count;
+                upto_b = count + a.item_cost;
             }
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -150,30 +156,32 @@ struct Walk {
             }
         }
         block_tiles(a, q, b, first, count, hi);
-        from = static_cast<int>(y);
-        clip();
+        clip(a, static_cast<int>(y));
+        if (from >= upto) next(a);
     }
     __device__ __forceinline__ bool valid() const { return left > 0; }
+    // The next item that the share has tiles of.
     __device__ __forceinline__ void next(const AttnArgs &a)
     {
-        left -= upto - from;
-        if (left <= 0) return;
-        if (++b >= q.blocks) {
-            b = 0;
-            if (++h >= a.c.heads) {
-                h = 0;
-                do {
-                    if (++s >= a.n_seq) {
-                        left = 0;
-                        return;
-                    }
-                    q = seq_at(a, s);
-                } while (q.blocks == 0);
+        do {
+            left -= used;
+            if (left <= 0) return;
+            if (++b >= q.blocks) {
+                b = 0;
+                if (++h >= a.c.heads) {
+                    h = 0;
+                    do {
+                        if (++s >= a.n_seq) {
+                            left = 0;
+                            return;
+                        }
+                        q = seq_at(a, s);
+                    } while (q.blocks == 0);
+                }
             }
-        }
-        block_tiles(a, q, b, first, count, hi);
-        from = 0;
-        clip();
+            block_tiles(a, q, b, first, count, hi);
+            clip(a, 0);
+        } while (from >= upto);
     }
     // Parts of an item that starts in this CTA and is not finished in it.
     __device__ __forceinline__ int parts() const

@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kHalf = 128, kTile = kTensorTile;
 constexpr int kSoftmaxWarps = 8;                        // four a half
-constexpr uint32_t kFirst = 1, kLast = 2, kTwo = 4;     // of a tile: where it stands in its item, and whether the item has a second half
+constexpr uint32_t kFirst = 1, kLast = 2, kTwo = 4, kEnd = 8;   // of a tile: where it stands in its item, whether that has a second half, and no tile comes after it
 constexpr uint32_t kAtomRows = kTile * 128;              // bytes of 64 dims of a tile
 
 template <int KIND, int DP> struct TensorShape {
@@ -85,6 +85,12 @@ struct Turn {
         if (++slot == depth) slot = 0, phase ^= 1u;
     }
 };
+
+// A tile's flags: its item's, and what it is in it.
+__device__ __forceinline__ uint32_t flags_of(uint32_t mark, bool first, bool last)
+{
+    return (mark & 0xFFu) | (first ? kFirst : 0u) | (last ? kLast | mark >> 8 : 0u);
+}
 
 // Descriptor of an N-major operand of 64-element rows of 128 bytes, swizzled: the
 // next 64 of N `lead` bytes on, the next 8 of K 1024.
@@ -168,7 +174,6 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     };
     const auto both = [&] { return w.q.rows - w.b * kTensorRows > kHalf; };   // whether the item has a second half
 
-    const int tiles = w.left;                                          // of the CTA's share
     if (warp < kSoftmaxWarps) {
         // ---------------------------------------------------------- softmax
         reg_inc<S::kSoftmaxRegs>();
@@ -527,7 +532,8 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             const auto terms_there = [&] { return test(&v_full[vt.slot], vt.phase) && test(&bars->p_full[0][0], p_phase[0]); };
             uint32_t flags = 0;                                        // of the tile
             bool start = true;
-            for (int t = 0; ok && t < tiles; ++t) {
+            bool work = w.valid();
+            while (ok && work) {
                 if (start) {
                     // an item's first scores
                     if (!wait(&bars->k_full[kt.slot], kt.phase)) break;
@@ -543,6 +549,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                     }
                 }
                 const bool more = (flags & kLast) == 0, two = (flags & kTwo) != 0, add = (flags & kFirst) == 0;
+                work = (flags & kEnd) == 0;
                 if (!there && !wait(&v_full[vt.slot], vt.phase)) break;
                 sums(0, add, !more, !two, [&] { return more ? test(&bars->k_full[kt.slot], kt.phase) : two && test(&bars->p_full[1][0], p_phase[1]); });
                 if (more) {
@@ -567,7 +574,10 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             long long issued = 0, landing_k = 0, landing_v = 0;        // tiles; those of keys and of values that copies were issued for
             bool ok = true;
             const int in_page = a.c.page_tokens;
-            for (; ok && w.valid(); w.next(a)) {
+            for (Walk after; ok && w.valid(); w = after) {
+                after = w;
+                after.next(a);
+                const uint32_t mark = (both() ? kTwo : 0u) | (after.valid() ? 0u : kEnd << 8);   // (kEnd at the last tile)
                 const int32_t *table = a.c.table + w.s * a.c.ldt;
                 const int64_t head = static_cast<int64_t>(w.h) * a.c.head_bytes;
                 const int end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> a.c.log_page;
@@ -594,7 +604,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         ok = __all_sync(0xFFFFFFFFu, go) != 0;
                         if (!ok) break;
                         if (lane == 0) {
-                            if (kv == 0) bars->flags[tn.slot] = (t == w.from ? kFirst : 0u) | (t + 1 == w.upto ? kLast : 0u) | (both() ? kTwo : 0u);
+                            if (kv == 0) bars->flags[tn.slot] = flags_of(mark, t == w.from, t + 1 == w.upto);
                             mbar_arrive_expect_tx(full, static_cast<uint32_t>(tokens * CH * 128));
                         }
                         __syncwarp();
@@ -675,7 +685,10 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             Turn kt, sc;
             long long done = 0;
             bool ok = true;
-            for (; ok && w.valid(); w.next(a)) {
+            for (Walk after; ok && w.valid(); w = after) {
+                after = w;
+                after.next(a);
+                const uint32_t mark = (both() ? kTwo : 0u) | (after.valid() ? 0u : kEnd << 8);   // (kEnd at the last tile)
                 for (int t = w.from; ok && t < w.upto; ++t) {
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
@@ -705,7 +718,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            if (kv == 0 && me == 0) bars->flags[kt.slot] = (t == w.from ? kFirst : 0u) | (t + 1 == w.upto ? kLast : 0u) | (both() ? kTwo : 0u);
+                            if (kv == 0 && me == 0) bars->flags[kt.slot] = flags_of(mark, t == w.from, t + 1 == w.upto);
                             mbar_arrive(&bars->k_full[kt.slot]);
                             if (kv == 1) mbar_arrive(&bars->scales_full[sc.slot]);
                         }
@@ -748,6 +761,7 @@ template <int KIND, int DP> cudaError_t launch(const AttnArgs &args, int sm_coun
 cudaError_t launch_attn_tensor(AttnArgs a, int sm_count, cudaStream_t s)
 {
     a.tile = kTensorTile, a.block = kTensorRows;
+    a.item_cost = 2;
     int ctas = 0;
     const bool small = a.c.chunks == 1;
     cudaError_t e;

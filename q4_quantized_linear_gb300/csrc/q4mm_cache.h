@@ -83,6 +83,7 @@ struct AttnArgs {
     int rows;
     int rows_above, rows_upto;   // the sequences this launch takes: query rows in (above, upto]
     int tile, block;          // tokens of a tile, query rows of a block
+    int item_cost;            // tiles' worth of work that an item costs beside its tiles
     int stages;
     float *parts;             // [2 * CTAs] of block x (64 * chunks) sums, then [block] maxima and sums
     int4 *meta;               // [CTAs][2]: an item whose parts are to be joined
