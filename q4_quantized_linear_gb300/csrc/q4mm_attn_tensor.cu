@@ -36,17 +36,18 @@ template <int KIND, int DP> struct TensorShape {
     static constexpr bool kCodes = KIND == 2;
     static constexpr int kChunks = DP / kChunk;
     // Warps 8 and 9: products and copies; codes: 8-11 convert, 12 products. Warpgroups
-    // share the registers out: a softmax thread holds a row of scores.
+    // share the registers out: a softmax thread holds a row of scores (codes: half a row).
     static constexpr int kThreads = kCodes ? 512 : 384;
     static constexpr int kConvertWarp0 = 8, kMmaWarp = kCodes ? 12 : 8, kCopyWarp = 9;
-    static constexpr int kSoftmaxRegs = kCodes ? 168 : 208, kConvertRegs = 104, kMmaRegs = kCodes ? 72 : 88;
+    static constexpr int kSoftmaxRegs = kCodes ? 136 : 208, kConvertRegs = 136, kMmaRegs = kCodes ? 104 : 88;
+    static constexpr int kLaunchRegs = kCodes ? 128 : 168;
     static constexpr int kAllRegs = 128 * (2 * kSoftmaxRegs + kMmaRegs + (kCodes ? kConvertRegs : 0));
     static constexpr int kTileBytes = kChunks * static_cast<int>(kAtomRows);
     // 16-bit: rings of K and of V tiles. Codes: one ring of fp16 tiles, K and V in turn.
     static constexpr int kK = kCodes || DP == 64 ? 4 : 2, kV = kCodes ? 0 : DP == 64 ? 4 : 3;
     static constexpr int kScaleSlots = 4;                // tiles whose scales are held
     static constexpr size_t kSmem = 2 * kHalf * DP * 2 + static_cast<size_t>(kK + kV) * kTileBytes +
-                                    (kCodes ? kScaleSlots * (2 * kTile + 4) * 4 : 0) + 2 * kHalf * 4 + 512 + 1024;
+                                    (kCodes ? kScaleSlots * (2 * kTile + 4) * 4 + 4 * kTile * 4 : 0) + 2 * kHalf * 4 + 512 + 1024;
 };
 
 struct Bars {
@@ -86,12 +87,22 @@ struct Turn {
     }
 };
 
-// A tile's flags: its item's, and what it is in it.
-__device__ __forceinline__ uint32_t flags_of(uint32_t mark, bool first, bool last)
-{
-    return (mark & 0xFFu) | (first ? kFirst : 0u) | (last ? kLast | mark >> 8 : 0u);
-}
-
+// Over codes: whether a tile's scales are applied by columns, to scores and terms,
+// exactly. They are for fp16 queries, and where some row of the block does not see
+// all of the tile. For bf16 outputs the operands of other tiles carry them, rounded to
+// fp16 (2^-12, far below the output's 2^-9) next to a power of two a tile: reading 256
+// scales a row and tile from shared memory, which the products' operands keep busy,
+// took the softmax 7000 clocks of a tile's 2048 (540 tokens over 8100: 205 us).
+struct Bounds {
+    int from, upto;
+    __device__ __forceinline__ Bounds(const AttnArgs &a, const Walk &w)
+    {
+        int x;
+        row_range(a, w.q, w.b * a.block, x, upto);
+        row_range(a, w.q, min((w.b + 1) * a.block, w.q.rows) - 1, from, x);
+    }
+    __device__ __forceinline__ bool exact(const AttnArgs &a, int t0) const { return a.type != Q4_TYPE_BF16 || t0 + kTile > upto || t0 < from; }
+};
 // Descriptor of an N-major operand of 64-element rows of 128 bytes, swizzled: the
 // next 64 of N `lead` bytes on, the next 8 of K 1024.
 __device__ __forceinline__ uint64_t desc_n_major(uint32_t saddr, uint32_t lead)
@@ -106,8 +117,12 @@ __device__ __forceinline__ uint64_t desc_n_major(uint32_t saddr, uint32_t lead)
 }
 constexpr uint32_t kNMajorB = 1u << 16;
 
-template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// A warpgroup's registers a thread from FROM, the launch's, to TO.
+template <int FROM, int TO> __device__ __forceinline__ void set_regs()
+{
+    if constexpr (TO > FROM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TO));
+    else if constexpr (TO < FROM) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TO));
+}
 __device__ __forceinline__ F2 f2_add(F2 a, F2 b)
 {
     F2 r;
@@ -126,8 +141,9 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     uint8_t *const qs = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));                                          // [half][chunk][128 rows][128 bytes]
     uint8_t *const ks = qs + 2 * kHalf * DP * 2;
     uint8_t *const vs = ks + S::kK * S::kTileBytes;
-    float *const scales = reinterpret_cast<float *>(vs + S::kV * S::kTileBytes);   // [slot][keys, values][tile], then [slot][4]: the largest
-    float *const row_factor = scales + (CODES ? S::kScaleSlots * (2 * kTile + 4) : 0);
+    float *const scales = reinterpret_cast<float *>(vs + S::kV * S::kTileBytes);   // [slot][keys, values][tile], then [slot][4]: the largest value scale, the exponents
+    uint32_t *const factors = reinterpret_cast<uint32_t *>(scales + (CODES ? S::kScaleSlots * (2 * kTile + 4) : 0));   // [converting warp][token]
+    float *const row_factor = reinterpret_cast<float *>(factors + (CODES ? 4 * kTile : 0));
     Bars *const bars = reinterpret_cast<Bars *>(row_factor + 2 * kHalf);
     // (a warp's number from one lane: what follows from it stays in uniform registers)
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
@@ -176,7 +192,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
 
     if (warp < kSoftmaxWarps) {
         // ---------------------------------------------------------- softmax
-        reg_inc<S::kSoftmaxRegs>();
+        set_regs<S::kLaunchRegs, S::kSoftmaxRegs>();
         const int half = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + 128u * half, o_at = tmem + lanes + 256u + 128u * half;
@@ -259,7 +275,8 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             const int end = min(w.hi, w.q.len);
             hi = min(hi, end);
             float m = neg_inf(), l = 0.0f;
-            int E = -118;
+            int E = -118;                                              // of the sums' unit, over codes
+            const Bounds bounds(a, w);
             for (int t = w.from; t < w.upto; ++t) {
                 const int t0 = (w.first + t) * kTile;
                 if (!warp_wait(&bars->s_full[half], s_phase, a.wait_ns) ||
@@ -272,45 +289,67 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 tc_fence_after();
                 const float *sk = scales + sc.slot * (2 * kTile), *sv = sk + kTile;
                 const bool masked = t0 + kTile > full_upto || t0 < full_from;   // some row does not see all of the tile
-                uint32_t r[kTile];
+                // Scales by columns; or in the operands already, but for two powers of two.
+                const bool exact = CODES && bounds.exact(a, t0);
+                const float4 tail = CODES ? *reinterpret_cast<const float4 *>(scales + S::kScaleSlots * 2 * kTile + sc.slot * 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const float rft = CODES && !exact ? rf * pow2(__float_as_int(tail.y)) : rf;
+                // 32 columns of scores: their keys' scales, and what the row does not see
+                const auto scored = [&](int i0, uint32_t *r) {
+                    if (CODES && exact) {
 #pragma unroll
-                for (int i = 0; i < kTile; i += 32) tmem_ld_32x32b_x32(s_at + i, r + i);
-                tmem_wait_ld();
-                if constexpr (CODES) {
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 k4 = *reinterpret_cast<const float4 *>(sk + i0 + i);
+                            const float s4[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-                    for (int i = 0; i < kTile; i += 4) {
-                        const float4 k4 = *reinterpret_cast<const float4 *>(sk + i);
-                        float y[4];
-                        f2_split(f2_mul(f2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2(k4.x, k4.y)), y[0], y[1]);
-                        f2_split(f2_mul(f2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), f2(k4.z, k4.w)), y[2], y[3]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) r[i + j] = __float_as_uint(y[j]);
+                            for (int j = 0; j < 4; ++j) r[i + j] = __float_as_uint(__uint_as_float(r[i + j]) * s4[j]);
+                        }
                     }
-                }
-                if (masked) {
-#pragma unroll
-                    for (int i0 = 0; i0 < kTile; i0 += 32) {
+                    if (masked) {
                         // bits of the columns that the row sees
                         const int from = min(max(lo - t0 - i0, 0), 32), upto = min(max(hi - t0 - i0, 0), 32);
                         const uint32_t sees = static_cast<uint32_t>(((1ull << upto) - 1ull) & ~((1ull << from) - 1ull));
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (!(sees >> i & 1u)) r[i0 + i] = 0xFF800000u;
+                            if (!(sees >> i & 1u)) r[i] = 0xFF800000u;
                     }
-                }
+                };
                 float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+                const auto largest = [&](const uint32_t *r) {
 #pragma unroll
-                for (int i = 0; i < kTile; i += 8)
+                    for (int i = 0; i < 32; i += 8)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], fmaxf(__uint_as_float(r[i + 2 * j]), __uint_as_float(r[i + 2 * j + 1])));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rf;
-                float vmax = 0.0f;
+                        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], fmaxf(__uint_as_float(r[i + 2 * j]), __uint_as_float(r[i + 2 * j + 1])));
+                };
+                // A row's scores stay in registers; over codes, where the converting warps need
+                // some of them, they are read twice, 32 columns at a time.
+                constexpr int kHeld = CODES ? 64 : kTile;
+                uint32_t r[kHeld];
+                if constexpr (CODES) {
+                    tmem_ld_32x32b_x32(s_at, r);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
+                        // the next columns, and after the last ones the first again
+                        tmem_ld_32x32b_x32(s_at + (c + 1) % 4 * 32, r + (c + 1) % 2 * 32);
+                        scored(32 * c, r + c % 2 * 32);
+                        largest(r + c % 2 * 32);
+                    }
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 32) tmem_ld_32x32b_x32(s_at + i, r + i);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 32) scored(i, r + i);
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 32) largest(r + i);
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rft;
+                float vmax = tail.x;                                   // value scales that the row sees are at most this
                 if (CODES && masked) {
+                    vmax = 0.0f;
 #pragma unroll 1
                     for (int i = max(lo - t0, 0); i < min(hi - t0, kTile); ++i) vmax = fmaxf(vmax, sv[i]);
-                } else if constexpr (CODES) {
-                    const float4 x4 = *reinterpret_cast<const float4 *>(scales + S::kScaleSlots * 2 * kTile + sc.slot * 4);
-                    vmax = fmaxf(fmaxf(x4.x, x4.y), fmaxf(x4.z, x4.w));
                 }
                 const bool wide = CODES && vmax >= pow2(E);
                 if (__any_sync(0xFFFFFFFFu, top > m + kSlack || wide)) {
@@ -335,34 +374,60 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         }
                     }
                 }
-                const float u = m == neg_inf() ? 0.0f : m - kLift;
-                const F2 rf2 = f2(rf, rf), u2 = f2(-u, -u);
+                // terms in the sums' unit: of a tile whose values carry their scales 2^shift times p
+                const int shift = CODES && !exact ? max(__float_as_int(tail.z) - E, -120) : 0;
+                const float u = (m == neg_inf() ? 0.0f : m - kLift) - static_cast<float>(shift);
+                const F2 rf2 = f2(rft, rft), u2 = f2(-u, -u);
                 [[maybe_unused]] const float down = CODES ? pow2(-E) : 1.0f;
                 F2 sum = f2(0.0f, 0.0f), sum2 = sum;
-                // terms in the place of scores, in two parts: products start on the first
+                // 32 columns' terms into the 16 words at p, which may be r's own
+                const auto terms = [&](auto by_column, int i0, const uint32_t *r, uint32_t *p) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int i = 32 * h; i < 32 * h + 32; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         float e0, e1;
                         f2_split(f2_fma(f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), rf2, u2), e0, e1);
                         e0 = exp2_fast(e0), e1 = exp2_fast(e1);
                         if (i & 1) sum2 = f2_add(sum2, f2(e0, e1));
                         else sum = f2_add(sum, f2(e0, e1));
-                        if constexpr (CODES) {
+                        if constexpr (decltype(by_column)::value) {
                             // (below 1 where the row sees the token; finite times 0 where not)
-                            const float2 v2 = *reinterpret_cast<const float2 *>(sv + 2 * i);
+                            const float2 v2 = *reinterpret_cast<const float2 *>(sv + i0 + 2 * i);
                             e0 *= fminf(v2.x * down, 1.0f), e1 *= fminf(v2.y * down, 1.0f);
                         }
-                        r[i] = BF ? pack_bf16x2_rn(e0, e1) : pack_f16x2_rn(e0, e1);
+                        p[i] = BF ? pack_bf16x2_rn(e0, e1) : pack_f16x2_rn(e0, e1);
                     }
-                    tmem_st_32x32b_x32(s_at + 32 * h, r + 32 * h);
+                };
+                // they go in the place of scores, in two parts: products start on the first
+                const auto part_done = [&](int h) {
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->p_full[half][h]);
+                };
+                if constexpr (CODES) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t *const now = r + c % 2 * 32;
+                        if (c > 0) tmem_wait_ld();
+                        // (terms of these columns take places that have been read)
+                        if (c + 1 < 4) tmem_ld_32x32b_x32(s_at + 32 * (c + 1), r + (c + 1) % 2 * 32);
+                        scored(32 * c, now);
+                        uint32_t p[16];
+                        if (exact) terms(std::true_type{}, 32 * c, now, p);
+                        else terms(std::false_type{}, 32 * c, now, p);
+                        tmem_st_32x32b_x16(s_at + 16 * c, p);
+                        if (c & 1) part_done(c / 2);
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        terms(std::false_type{}, 0, r + 64 * h, r + 32 * h);
+                        terms(std::false_type{}, 0, r + 64 * h + 32, r + 32 * h + 16);
+                        tmem_st_32x32b_x32(s_at + 32 * h, r + 32 * h);
+                        part_done(h);
+                    }
                 }
-                l += f2_sum(f2_add(sum, sum2));
+                l += f2_sum(f2_add(sum, sum2)) * (CODES ? pow2(-shift) : 1.0f);
                 if constexpr (CODES) {
                     if (lane == 0) mbar_arrive(&bars->scales_empty[sc.slot]);
                     sc.step(S::kScaleSlots);
@@ -452,7 +517,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             tc_fence_before();
         }
     } else if (warp >= (CODES ? S::kMmaWarp : 8)) {
-        reg_dec<S::kMmaRegs>();
+        set_regs<S::kLaunchRegs, S::kMmaRegs>();
         if (warp == S::kMmaWarp) {
             // ----------------------------------------------------- products
             constexpr uint32_t type = BF ? idesc_bf16_f32(0, 0) : idesc_f16_f32(0, 0);
@@ -574,10 +639,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             long long issued = 0, landing_k = 0, landing_v = 0;        // tiles; those of keys and of values that copies were issued for
             bool ok = true;
             const int in_page = a.c.page_tokens;
-            for (Walk after; ok && w.valid(); w = after) {
-                after = w;
-                after.next(a);
-                const uint32_t mark = (both() ? kTwo : 0u) | (after.valid() ? 0u : kEnd << 8);   // (kEnd at the last tile)
+            for (; ok && w.valid(); w.next(a)) {
                 const int32_t *table = a.c.table + w.s * a.c.ldt;
                 const int64_t head = static_cast<int64_t>(w.h) * a.c.head_bytes;
                 const int end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> a.c.log_page;
@@ -604,7 +666,15 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         ok = __all_sync(0xFFFFFFFFu, go) != 0;
                         if (!ok) break;
                         if (lane == 0) {
-                            if (kv == 0) bars->flags[tn.slot] = flags_of(mark, t == w.from, t + 1 == w.upto);
+                            if (kv == 0) {
+                                uint32_t flags = (both() ? kTwo : 0u) | (t == w.from ? kFirst : 0u);
+                                if (t + 1 == w.upto) {
+                                    Walk after = w;
+                                    after.next(a);
+                                    flags |= kLast | (after.valid() ? 0u : kEnd);
+                                }
+                                bars->flags[tn.slot] = flags;
+                            }
                             mbar_arrive_expect_tx(full, static_cast<uint32_t>(tokens * CH * 128));
                         }
                         __syncwarp();
@@ -638,61 +708,112 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     } else {
         if constexpr (CODES) {
             // ---------------------------------------------- codes to fp16
-            reg_dec<S::kConvertRegs>();
-            // Four warps; a thread has a 16-byte unit of eight rows of 64 codes (four at DP =
-            // 64), fetched a tile of keys or values ahead of its conversion.
+            set_regs<S::kLaunchRegs, S::kConvertRegs>();
+            // Four warps; a thread has a 16-byte unit of four tokens' rows in each 64 dims,
+            // fetched a tile of keys or values ahead of its conversion: tokens me / 4 + 32 i.
+            // A lane has the scales of tokens 4 lane .. + 3.
             constexpr int kUnits = CH * 4;
-            const int me = tid - S::kConvertWarp0 * 32, in_page = a.c.page_tokens;
+            const int me = tid - S::kConvertWarp0 * 32, in_page = a.c.page_tokens, log_page = a.c.log_page;
             const int unit = me & 3;
-            Walk f = w;                                                // where the fetches are
-            int f_t = f.from, f_kv = 0;
+            const int to_values = CH * in_page * 64;                   // from a key's unit to its value's
+            // The walk is where the fetches are, a tile ahead: `fresh` says that it has come to
+            // another item. Of the tile that was fetched:
+            int at = w.from, held = 0, page = 0, ahead = 0;            // lane l holds page held + l, and the one 32 further on
+            bool fresh = true;
+            uint32_t mark = 0;
+            bool exact = false;
             uint4 codes[kUnits];
-            float scale;
-            // where the next tile's units of rows me / 4 + 32 i are (nullptr: not held), and its scale
+            float4 scale;
+            // where the fetched tile's keys are (nullptr: not held) and their scales
             const uint8_t *src[4];
-            const float *scale_src;
+            const float4 *scale_src;
+            int scale_tokens;
             const auto aim = [&] {
-                if (!f.valid()) {
+                if (!w.valid()) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) src[i] = nullptr;
-                    scale_src = nullptr;
+                    scale_src = nullptr, scale_tokens = 0;
                     return;
                 }
-                const int end = min(f.hi, f.q.len), t0 = (f.first + f_t) * kTile, tokens = min(max(end - t0, 0), kTile);
-                const int p0 = t0 >> a.c.log_page, pages = (end + in_page - 1) >> a.c.log_page;
-                const int page = tokens > 0 ? page_of(a, a.c.table + f.s * a.c.ldt, p0 + (lane & 7), pages) : 0;
-                const uint8_t *head = a.c.pages + static_cast<int64_t>(f.h) * a.c.head_bytes;
+                const int end = min(w.hi, w.q.len), t0 = (w.first + at) * kTile, tokens = min(max(end - t0, 0), kTile);
+                const int32_t *table = a.c.table + w.s * a.c.ldt;
+                const int p0 = t0 >> log_page, pages = (end + in_page - 1) >> log_page;
+                if (fresh) {
+                    held = p0;
+                    page = page_of(a, table, held + lane, pages);
+                    ahead = page_of(a, table, held + 32 + lane, pages);
+                } else if (p0 >= held + 32) {                          // (a tile's pages never straddle: 32 is a multiple of their number)
+                    held += 32;
+                    page = ahead;
+                    ahead = page_of(a, table, held + 32 + lane, pages);
+                }
+                const uint8_t *head = a.c.pages + static_cast<int64_t>(w.h) * a.c.head_bytes;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int tok = i * 32 + me / 4, x = t0 + tok;
-                    const int pg = __shfl_sync(0xFFFFFFFFu, page, (x >> a.c.log_page) - p0);
-                    src[i] = tok < tokens ? head + pg * a.c.page_bytes + (f_kv * CH * in_page + (x & (in_page - 1))) * 64 + 16 * unit : nullptr;
+                    const int pg = __shfl_sync(0xFFFFFFFFu, page, (x >> log_page) - held);
+                    src[i] = tok < tokens ? head + pg * a.c.page_bytes + (x & (in_page - 1)) * 64 + 16 * unit : nullptr;
                 }
-                const int x = t0 + me, pg = __shfl_sync(0xFFFFFFFFu, page, (x >> a.c.log_page) - p0);
-                scale_src = me < tokens ? reinterpret_cast<const float *>(head + pg * a.c.page_bytes + 2 * CH * in_page * 64) + f_kv * in_page + (x & (in_page - 1))
-                                        : nullptr;
-                if (f_kv == 1 && ++f_t >= f.upto) {
-                    f.next(a);
-                    f_t = f.from;
+                const int x = t0 + 4 * lane, pg = __shfl_sync(0xFFFFFFFFu, page, (x >> log_page) - held);
+                scale_tokens = tokens - 4 * lane;
+                scale_src = scale_tokens > 0 ? reinterpret_cast<const float4 *>(head + pg * a.c.page_bytes + 2 * to_values + (x & (in_page - 1)) * 4) : nullptr;
+                exact = Bounds(a, w).exact(a, t0);
+                mark = (both() ? kTwo : 0u) | (fresh ? kFirst : 0u);
+                fresh = false;
+                if (++at >= w.upto) {
+                    w.next(a);
+                    at = w.from;
+                    fresh = true;
+                    mark |= kLast | (w.valid() ? 0u : kEnd);
                 }
-                f_kv ^= 1;
             };
-            const auto load = [&](int j) { return src[j % 4] ? *reinterpret_cast<const uint4 *>(src[j % 4] + j / 4 * (in_page * 64)) : make_uint4(0u, 0u, 0u, 0u); };
+            const auto load = [&](int j, int kv) {
+                return src[j % 4] ? *reinterpret_cast<const uint4 *>(src[j % 4] + kv * to_values + j / 4 * (in_page * 64)) : make_uint4(0u, 0u, 0u, 0u);
+            };
+            const auto load_scales = [&](int kv) {
+                float4 s = scale_src ? scale_src[kv * (in_page / 4)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (scale_tokens < 4) s.w = 0.0f;
+                if (scale_tokens < 3) s.z = 0.0f;
+                if (scale_tokens < 2) s.y = 0.0f;
+                return s;
+            };
             aim();
 #pragma unroll
-            for (int j = 0; j < kUnits; ++j) codes[j] = load(j);
-            scale = scale_src ? *scale_src : 0.0f;
+            for (int j = 0; j < kUnits; ++j) codes[j] = load(j, 0);
+            scale = load_scales(0);
+            uint32_t *const mine = factors + (warp - S::kConvertWarp0) * kTile;
             Turn kt, sc;
             long long done = 0;
             bool ok = true;
-            for (Walk after; ok && w.valid(); w = after) {
-                after = w;
-                after.next(a);
-                const uint32_t mark = (both() ? kTwo : 0u) | (after.valid() ? 0u : kEnd << 8);   // (kEnd at the last tile)
-                for (int t = w.from; ok && t < w.upto; ++t) {
+            bool work = mark != 0u;                                    // (a tile is kFirst, or there is none)
+            {
+                while (ok && work) {
+                    const uint32_t flags = mark;                       // of this tile
+                    const bool by_column = exact;
+                    work = (flags & kEnd) == 0;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
-                        aim();
+                        const float4 was = scale;
+                        const float s[4] = {was.x, was.y, was.z, was.w};
+                        if (kv == 1) aim();                            // keys of the next tile come next
+                        scale = load_scales(kv ^ 1);
+                        uint32_t top = 0;                              // the largest that is a number
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top = max(top, abs_bits(s[i]) < 0x7F800000u ? abs_bits(s[i]) : 0u);
+                        top = __reduce_max_sync(0xFFFFFFFFu, top);
+                        const int e = max(static_cast<int>(top >> 23) - 126, -118);   // scales are below 2^e
+                        const float down = pow2(-e);
+                        uint32_t factor[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float y = by_column ? 1.0f : s[i] * down;
+                            factor[i] = pack_f16x2_rn(y, y);
+                        }
+                        __syncwarp();                                  // the factors before have been read
+                        sts128(mine + 4 * lane, make_uint4(factor[0], factor[1], factor[2], factor[3]));
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) factor[i] = mine[i * 32 + me / 4];
                         if (kv == 0 && done >= 2 * S::kScaleSlots && !warp_wait(&bars->scales_empty[sc.slot], sc.phase ^ 1u, a.wait_ns)) ok = false;
                         if (ok && done >= S::kK && !warp_wait(&bars->k_empty[kt.slot], kt.phase ^ 1u, a.wait_ns)) ok = false;
                         if (!ok) break;
@@ -700,25 +821,29 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
 #pragma unroll
                         for (int j = 0; j < kUnits; ++j) {
                             const uint4 v = codes[j];
-                            codes[j] = load(j);
+                            codes[j] = load(j, kv ^ 1);
                             const int tok = j % 4 * 32 + me / 4, u = unit ^ ((tok >> 1) & 3);   // which of the row's units this is
                             uint32_t o[8];
                             codes_f16(v.x, o[0], o[1]), codes_f16(v.y, o[2], o[3]);
                             codes_f16(v.z, o[4], o[5]), codes_f16(v.w, o[6], o[7]);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = hmul2_bits(o[i], factor[j % 4]);
                             uint8_t *row = dst + j / 4 * kAtomRows + tok * 128;
                             sts128(row + (((2 * u) ^ (tok & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
                             sts128(row + (((2 * u + 1) ^ (tok & 7)) << 4), make_uint4(o[4], o[5], o[6], o[7]));
                         }
-                        scales[sc.slot * (2 * kTile) + kv * kTile + me] = scale;
-                        if (kv == 1) {
-                            const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(scale) & 0x7FFFFFFFu);
-                            if (lane == 0) scales[S::kScaleSlots * 2 * kTile + sc.slot * 4 + warp - S::kConvertWarp0] = __uint_as_float(largest);
+                        if (warp == S::kConvertWarp0) {
+                            *reinterpret_cast<float4 *>(scales + sc.slot * (2 * kTile) + kv * kTile + 4 * lane) = was;
+                            if (lane == 0) {
+                                float *tail = scales + S::kScaleSlots * 2 * kTile + sc.slot * 4;
+                                tail[1 + kv] = __int_as_float(e);
+                                if (kv == 1) tail[0] = __uint_as_float(top);
+                            }
                         }
-                        scale = scale_src ? *scale_src : 0.0f;
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            if (kv == 0 && me == 0) bars->flags[kt.slot] = flags_of(mark, t == w.from, t + 1 == w.upto);
+                            if (kv == 0 && me == 0) bars->flags[kt.slot] = flags;
                             mbar_arrive(&bars->k_full[kt.slot]);
                             if (kv == 1) mbar_arrive(&bars->scales_full[sc.slot]);
                         }
@@ -748,7 +873,7 @@ template <int KIND, int DP> cudaError_t launch(const AttnArgs &args, int sm_coun
     static const bool enough = [f] {
         using S = TensorShape<KIND, DP>;
         cudaFuncAttributes fa{};
-        return cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs * S::kThreads >= S::kAllRegs;
+        return cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs == S::kLaunchRegs && S::kLaunchRegs * S::kThreads >= S::kAllRegs;
     }();
     if (!enough) return cudaErrorLaunchOutOfResources;
     *ctas = std::min(kTensorMaxCtas, sm_count);

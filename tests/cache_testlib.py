@@ -73,7 +73,7 @@ class Cache:
         return ws
 
 
-def attend64(q, k, v, heads, kv_heads, d, scale, window, lens, counts, round_p, terms):
+def attend64(q, k, v, heads, kv_heads, d, scale, window, lens, counts, round_p, terms, folded=False):
     """The attention in 64 bits and what an output may be off by beyond its own
     rounding. q [rows, heads d], k and v [tokens of all sequences, kv_heads, d] in
     64 bits, as the cache holds them. For a row with scores s_y, B_y = scale sum_i
@@ -91,6 +91,13 @@ def attend64(q, k, v, heads, kv_heads, d, scale, window, lens, counts, round_p, 
         codes twice that: a term of the denominator is 1, so a row's sum is off by at
         most n 2^-31 max |v| over what it sees;
       - the sums add n terms in fp32, 16 at a time: (n / 16 + 8) 2^-23.
+      - `folded` (bf16 queries over codes): a key or value may be code x factor, the
+        factor (its scale over the power of two above the largest that stands near it)
+        and the product each rounded to fp16, 2^-11: 2^-10 relative. A factor below
+        2^-14 is in steps of 2^-24, so off by 2^-25 of that power of two, which is at
+        most twice the largest scale seen: 127 codes of it 2^-24 of the largest key or
+        value seen. For the scores 2^-10 B and 2^-24 scale |q|_1 max |k|, for the values
+        2^-10 A and 2^-24 max |v|.
     A relative error e of every term moves numerator and denominator: 2 e A."""
     group = heads // kv_heads
     out = torch.zeros((sum(counts), heads * d), dtype=torch.float64, device=q.device)
@@ -117,9 +124,12 @@ def attend64(q, k, v, heads, kv_heads, d, scale, window, lens, counts, round_p, 
             b = torch.where(sees, (qq.abs() @ kk.abs().t()) * scale, torch.zeros_like(s))
             worst = b.amax(dim=1, keepdim=True) if n else torch.zeros_like(top)
             eps = ((d / 16 + 6) * 2.0 ** -23 + (2.0 ** -21 if terms == 2 else 0.0)) * worst + 2.0 ** -22 + round_p + (n / 16 + 8) * 2.0 ** -23
+            eps = eps + (2.0 ** -10 * worst + 2.0 ** -24 * scale * qq.abs().sum(dim=1, keepdim=True) * (kk.abs().max() if n else 0.0) if folded else 0.0)
             step = 0.0 if round_p == 2.0 ** -8 else n * 2.0 ** -31
             largest = (torch.where(sees, clean.abs().amax(dim=1)[None, :], torch.zeros_like(s)).amax(dim=1, keepdim=True)
                        if n else torch.zeros_like(top))
             tol[row:row + m, h * d:(h + 1) * d] = 2 * eps * (p @ clean.abs()) + step * largest
+            if folded:
+                tol[row:row + m, h * d:(h + 1) * d] += 2.0 ** -10 * (p @ clean.abs()) + 2.0 ** -24 * largest
         row, at = row + m, at + n
     return out, tol

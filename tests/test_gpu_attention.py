@@ -17,6 +17,7 @@ KINDS = [("f16", "f16"), ("f32", "f16"), ("bf16", "bf16"), ("bf16", "i8"), ("f16
 # The terms' rounding: the operands' type, or two fp16 numbers.
 ROUND_P = {("f16", "f16"): 2.0 ** -11, ("f32", "f16"): 2.0 ** -21, ("bf16", "bf16"): 2.0 ** -8, ("bf16", "i8"): 2.0 ** -11,
            ("f16", "i8"): 2.0 ** -11, ("f32", "i8"): 2.0 ** -21}
+FOLDED = ("bf16", "i8")   # operands may carry their scales, rounded to fp16
 
 
 def run(q4, name, cache, heads, kv_heads, d, page, lens, counts, window=0, pad=0, shift=0, max_new=None, more_rows=0, sharp=1.0,
@@ -37,7 +38,7 @@ def run(q4, name, cache, heads, kv_heads, d, page, lens, counts, window=0, pad=0
     torch.cuda.synchronize()
     assert q4.q4_last_device_status(clear=True) == 0
     ref, tol = attend64(q[:n], held(k, cache), held(v, cache), heads, kv_heads, d, scale, window, lens, counts, ROUND_P[name, cache],
-                        2 if name == "f32" else 1)
+                        2 if name == "f32" else 1, (name, cache) == FOLDED)
     close(o[:n], f64(ref), f64(tol) + ROUND[name] * np.abs(f64(ref)) * 1.01 + TINY[name], f"{name} {cache}")
     assert gaps_kept(o)
     if more_rows:
@@ -222,7 +223,7 @@ def test_scales_of_all_sizes(q4lib, name, cache):
         o = blank(length, heads * d, name)
         c.attend(o, q, name, heads, 0.125, 0, [length], [length])
         ref, tol = attend64(q, held(k, cache), held(vv, cache), heads, kv_heads, d, 0.125, 0, [length], [length], ROUND_P[name, cache],
-                            2 if name == "f32" else 1)
+                            2 if name == "f32" else 1, (name, cache) == FOLDED)
         close(o, f64(ref), f64(tol) + ROUND[name] * np.abs(f64(ref)) * 1.01 + TINY[name])
 
 
