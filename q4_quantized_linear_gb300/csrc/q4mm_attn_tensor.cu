@@ -39,7 +39,7 @@ template <int KIND, int DP> struct TensorShape {
     // share the registers out: a softmax thread holds a row of scores (codes: half a row).
     static constexpr int kThreads = kCodes ? 512 : 384;
     static constexpr int kConvertWarp0 = 8, kMmaWarp = kCodes ? 12 : 8, kCopyWarp = 9;
-    static constexpr int kSoftmaxRegs = kCodes ? 136 : 208, kConvertRegs = 136, kMmaRegs = kCodes ? 104 : 88;
+    static constexpr int kSoftmaxRegs = kCodes ? 144 : 208, kConvertRegs = 128, kMmaRegs = kCodes ? 96 : 88;
     static constexpr int kLaunchRegs = kCodes ? 128 : 168;
     static constexpr int kAllRegs = 128 * (2 * kSoftmaxRegs + kMmaRegs + (kCodes ? kConvertRegs : 0));
     static constexpr int kTileBytes = kChunks * static_cast<int>(kAtomRows);
@@ -289,13 +289,17 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 tc_fence_after();
                 const float *sk = scales + sc.slot * (2 * kTile), *sv = sk + kTile;
                 const bool masked = t0 + kTile > full_upto || t0 < full_from;   // some row does not see all of the tile
-                // Scales by columns; or in the operands already, but for two powers of two.
-                const bool exact = CODES && bounds.exact(a, t0);
+                // Scales by columns; or in the operands already, but for two powers of two. (The
+                // two are apart, and loops over codes are not unrolled: the warps' code together
+                // has to stay in the instruction caches.)
+                const auto tile = [&](auto by_column) {
+                constexpr bool exact = decltype(by_column)::value;     // (only such a tile is not seen whole)
+                const bool hidden = (!CODES || exact) && masked;
                 const float4 tail = CODES ? *reinterpret_cast<const float4 *>(scales + S::kScaleSlots * 2 * kTile + sc.slot * 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 const float rft = CODES && !exact ? rf * pow2(__float_as_int(tail.y)) : rf;
                 // 32 columns of scores: their keys' scales, and what the row does not see
                 const auto scored = [&](int i0, uint32_t *r) {
-                    if (CODES && exact) {
+                    if constexpr (exact) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             const float4 k4 = *reinterpret_cast<const float4 *>(sk + i0 + i);
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                             for (int j = 0; j < 4; ++j) r[i + j] = __float_as_uint(__uint_as_float(r[i + j]) * s4[j]);
                         }
                     }
-                    if (masked) {
+                    if (hidden) {
                         // bits of the columns that the row sees
                         const int from = min(max(lo - t0 - i0, 0), 32), upto = min(max(hi - t0 - i0, 0), 32);
                         const uint32_t sees = static_cast<uint32_t>(((1ull << upto) - 1ull) & ~((1ull << from) - 1ull));
@@ -326,13 +330,17 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 uint32_t r[kHeld];
                 if constexpr (CODES) {
                     tmem_ld_32x32b_x32(s_at, r);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+                        tmem_wait_ld();
+                        tmem_ld_32x32b_x32(s_at + 32 * c + 32, r + 32);
+                        scored(32 * c, r);
+                        largest(r);
                         tmem_wait_ld();
                         // the next columns, and after the last ones the first again
-                        tmem_ld_32x32b_x32(s_at + (c + 1) % 4 * 32, r + (c + 1) % 2 * 32);
-                        scored(32 * c, r + c % 2 * 32);
-                        largest(r + c % 2 * 32);
+                        tmem_ld_32x32b_x32(s_at + (32 * c + 64) % kTile, r);
+                        scored(32 * c + 32, r + 32);
+                        largest(r + 32);
                     }
                     tmem_wait_ld();
                 } else {
@@ -346,7 +354,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rft;
                 float vmax = tail.x;                                   // value scales that the row sees are at most this
-                if (CODES && masked) {
+                if (CODES && hidden) {
                     vmax = 0.0f;
 #pragma unroll 1
                     for (int i = max(lo - t0, 0); i < min(hi - t0, kTile); ++i) vmax = fmaxf(vmax, sv[i]);
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 [[maybe_unused]] const float down = CODES ? pow2(-E) : 1.0f;
                 F2 sum = f2(0.0f, 0.0f), sum2 = sum;
                 // 32 columns' terms into the 16 words at p, which may be r's own
-                const auto terms = [&](auto by_column, int i0, const uint32_t *r, uint32_t *p) {
+                const auto terms = [&](auto columns, int i0, const uint32_t *r, uint32_t *p) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float e0, e1;
@@ -389,7 +397,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         e0 = exp2_fast(e0), e1 = exp2_fast(e1);
                         if (i & 1) sum2 = f2_add(sum2, f2(e0, e1));
                         else sum = f2_add(sum, f2(e0, e1));
-                        if constexpr (decltype(by_column)::value) {
+                        if constexpr (decltype(columns)::value) {
                             // (below 1 where the row sees the token; finite times 0 where not)
                             const float2 v2 = *reinterpret_cast<const float2 *>(sv + i0 + 2 * i);
                             e0 *= fminf(v2.x * down, 1.0f), e1 *= fminf(v2.y * down, 1.0f);
@@ -405,18 +413,21 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                     if (lane == 0) mbar_arrive(&bars->p_full[half][h]);
                 };
                 if constexpr (CODES) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t *const now = r + c % 2 * 32;
-                        if (c > 0) tmem_wait_ld();
-                        // (terms of these columns take places that have been read)
-                        if (c + 1 < 4) tmem_ld_32x32b_x32(s_at + 32 * (c + 1), r + (c + 1) % 2 * 32);
-                        scored(32 * c, now);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
                         uint32_t p[16];
-                        if (exact) terms(std::true_type{}, 32 * c, now, p);
-                        else terms(std::false_type{}, 32 * c, now, p);
+                        // (terms of some columns take places that have been read)
+                        tmem_ld_32x32b_x32(s_at + 32 * c + 32, r + 32);
+                        scored(32 * c, r);
+                        terms(by_column, 32 * c, r, p);
                         tmem_st_32x32b_x16(s_at + 16 * c, p);
-                        if (c & 1) part_done(c / 2);
+                        tmem_wait_ld();
+                        if (c == 0) tmem_ld_32x32b_x32(s_at + 64, r);
+                        scored(32 * c + 32, r + 32);
+                        terms(by_column, 32 * c + 32, r + 32, p);
+                        tmem_st_32x32b_x16(s_at + 16 * c + 16, p);
+                        if (c == 0) tmem_wait_ld();
+                        part_done(c / 2);
                     }
                 } else {
 #pragma unroll
@@ -428,6 +439,13 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                     }
                 }
                 l += f2_sum(f2_add(sum, sum2)) * (CODES ? pow2(-shift) : 1.0f);
+                };
+                if constexpr (CODES) {
+                    if (bounds.exact(a, t0)) tile(std::true_type{});
+                    else tile(std::false_type{});
+                } else {
+                    tile(std::false_type{});
+                }
                 if constexpr (CODES) {
                     if (lane == 0) mbar_arrive(&bars->scales_empty[sc.slot]);
                     sc.step(S::kScaleSlots);
@@ -768,10 +786,11 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 }
             };
             const auto load = [&](int j, int kv) {
-                return src[j % 4] ? *reinterpret_cast<const uint4 *>(src[j % 4] + kv * to_values + j / 4 * (in_page * 64)) : make_uint4(0u, 0u, 0u, 0u);
+                // (past L1: the little of it that is left beside shared memory holds the threads' own)
+                return src[j % 4] ? __ldcg(reinterpret_cast<const uint4 *>(src[j % 4] + kv * to_values + j / 4 * (in_page * 64))) : make_uint4(0u, 0u, 0u, 0u);
             };
             const auto load_scales = [&](int kv) {
-                float4 s = scale_src ? scale_src[kv * (in_page / 4)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float4 s = scale_src ? __ldcg(scale_src + kv * (in_page / 4)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (scale_tokens < 4) s.w = 0.0f;
                 if (scale_tokens < 3) s.z = 0.0f;
                 if (scale_tokens < 2) s.y = 0.0f;
@@ -791,7 +810,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                     const uint32_t flags = mark;                       // of this tile
                     const bool by_column = exact;
                     work = (flags & kEnd) == 0;
-#pragma unroll
+#pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
                         const float4 was = scale;
                         const float s[4] = {was.x, was.y, was.z, was.w};
@@ -873,6 +892,7 @@ template <int KIND, int DP> cudaError_t launch(const AttnArgs &args, int sm_coun
     static const bool enough = [f] {
         using S = TensorShape<KIND, DP>;
         cudaFuncAttributes fa{};
+        if (S::kSoftmaxRegs == S::kLaunchRegs) return true;   // they stay as they are
         return cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs == S::kLaunchRegs && S::kLaunchRegs * S::kThreads >= S::kAllRegs;
     }();
     if (!enough) return cudaErrorLaunchOutOfResources;
