@@ -35,13 +35,11 @@ constexpr uint32_t kAtomRows = kTile * 128;              // bytes of 64 dims of 
 template <int KIND, int DP> struct TensorShape {
     static constexpr bool kCodes = KIND == 2;
     static constexpr int kChunks = DP / kChunk;
-    // Warps 8 and 9: products and copies; codes: 8-11 convert, 12 products. Warpgroups
-    // share the registers out: a softmax thread holds a row of scores (codes: half a row).
-    static constexpr int kThreads = kCodes ? 512 : 384;
+    // Warps 8 and 9: products and copies; codes: 8-11 convert, 12 products, and the
+    // warpgroups share the registers out.
+    static constexpr int kThreads = kCodes ? 512 : 320;
     static constexpr int kConvertWarp0 = 8, kMmaWarp = kCodes ? 12 : 8, kCopyWarp = 9;
-    static constexpr int kSoftmaxRegs = kCodes ? 144 : 208, kConvertRegs = 128, kMmaRegs = kCodes ? 96 : 88;
-    static constexpr int kLaunchRegs = kCodes ? 128 : 168;
-    static constexpr int kAllRegs = 128 * (2 * kSoftmaxRegs + kMmaRegs + (kCodes ? kConvertRegs : 0));
+    static constexpr int kLaunchRegs = 128, kSoftmaxRegs = 144, kConvertRegs = 128, kMmaRegs = 96;   // codes
     static constexpr int kTileBytes = kChunks * static_cast<int>(kAtomRows);
     // 16-bit: rings of K and of V tiles. Codes: one ring of fp16 tiles, K and V in turn.
     static constexpr int kK = kCodes || DP == 64 ? 4 : 2, kV = kCodes ? 0 : DP == 64 ? 4 : 3;
@@ -94,7 +92,8 @@ struct Turn {
 // scales a row and tile from shared memory, which the products' operands keep busy,
 // took the softmax 7000 clocks of a tile's 2048 (540 tokens over 8100: 205 us).
 struct Bounds {
-    int from, upto;
+    int from = 0, upto = 0;
+    __device__ __forceinline__ Bounds() {}
     __device__ __forceinline__ Bounds(const AttnArgs &a, const Walk &w)
     {
         int x;
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
 
     if (warp < kSoftmaxWarps) {
         // ---------------------------------------------------------- softmax
-        set_regs<S::kLaunchRegs, S::kSoftmaxRegs>();
+        if constexpr (CODES) set_regs<S::kLaunchRegs, S::kSoftmaxRegs>();
         const int half = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + 128u * half, o_at = tmem + lanes + 256u + 128u * half;
@@ -324,34 +323,23 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
 #pragma unroll
                         for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], fmaxf(__uint_as_float(r[i + 2 * j]), __uint_as_float(r[i + 2 * j + 1])));
                 };
-                // A row's scores stay in registers; over codes, where the converting warps need
-                // some of them, they are read twice, 32 columns at a time.
-                constexpr int kHeld = CODES ? 64 : kTile;
-                uint32_t r[kHeld];
-                if constexpr (CODES) {
-                    tmem_ld_32x32b_x32(s_at, r);
+                // The scores are read twice, 32 columns at a time: held in registers (208 a softmax
+                // thread, of the other warps') they took longer, by what the others then spilled.
+                uint32_t r[64];
+                tmem_ld_32x32b_x32(s_at, r);
 #pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        tmem_wait_ld();
-                        tmem_ld_32x32b_x32(s_at + 32 * c + 32, r + 32);
-                        scored(32 * c, r);
-                        largest(r);
-                        tmem_wait_ld();
-                        // the next columns, and after the last ones the first again
-                        tmem_ld_32x32b_x32(s_at + (32 * c + 64) % kTile, r);
-                        scored(32 * c + 32, r + 32);
-                        largest(r + 32);
-                    }
+                for (int c = 0; c < 4; c += 2) {
                     tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kTile; i += 32) tmem_ld_32x32b_x32(s_at + i, r + i);
+                    tmem_ld_32x32b_x32(s_at + 32 * c + 32, r + 32);
+                    scored(32 * c, r);
+                    largest(r);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < kTile; i += 32) scored(i, r + i);
-#pragma unroll
-                    for (int i = 0; i < kTile; i += 32) largest(r + i);
+                    // the next columns, and after the last ones the first again
+                    tmem_ld_32x32b_x32(s_at + (32 * c + 64) % kTile, r);
+                    scored(32 * c + 32, r + 32);
+                    largest(r + 32);
                 }
+                tmem_wait_ld();
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rft;
                 float vmax = tail.x;                                   // value scales that the row sees are at most this
                 if (CODES && hidden) {
@@ -412,31 +400,21 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->p_full[half][h]);
                 };
-                if constexpr (CODES) {
 #pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        uint32_t p[16];
-                        // (terms of some columns take places that have been read)
-                        tmem_ld_32x32b_x32(s_at + 32 * c + 32, r + 32);
-                        scored(32 * c, r);
-                        terms(by_column, 32 * c, r, p);
-                        tmem_st_32x32b_x16(s_at + 16 * c, p);
-                        tmem_wait_ld();
-                        if (c == 0) tmem_ld_32x32b_x32(s_at + 64, r);
-                        scored(32 * c + 32, r + 32);
-                        terms(by_column, 32 * c + 32, r + 32, p);
-                        tmem_st_32x32b_x16(s_at + 16 * c + 16, p);
-                        if (c == 0) tmem_wait_ld();
-                        part_done(c / 2);
-                    }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        terms(std::false_type{}, 0, r + 64 * h, r + 32 * h);
-                        terms(std::false_type{}, 0, r + 64 * h + 32, r + 32 * h + 16);
-                        tmem_st_32x32b_x32(s_at + 32 * h, r + 32 * h);
-                        part_done(h);
-                    }
+                for (int c = 0; c < 4; c += 2) {
+                    uint32_t p[16];
+                    // (terms of some columns take places that have been read)
+                    tmem_ld_32x32b_x32(s_at + 32 * c + 32, r + 32);
+                    scored(32 * c, r);
+                    terms(by_column, 32 * c, r, p);
+                    tmem_st_32x32b_x16(s_at + 16 * c, p);
+                    tmem_wait_ld();
+                    if (c == 0) tmem_ld_32x32b_x32(s_at + 64, r);
+                    scored(32 * c + 32, r + 32);
+                    terms(by_column, 32 * c + 32, r + 32, p);
+                    tmem_st_32x32b_x16(s_at + 16 * c + 16, p);
+                    if (c == 0) tmem_wait_ld();
+                    part_done(c / 2);
                 }
                 l += f2_sum(f2_add(sum, sum2)) * (CODES ? pow2(-shift) : 1.0f);
                 };
@@ -535,7 +513,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             tc_fence_before();
         }
     } else if (warp >= (CODES ? S::kMmaWarp : 8)) {
-        set_regs<S::kLaunchRegs, S::kMmaRegs>();
+        if constexpr (CODES) set_regs<S::kLaunchRegs, S::kMmaRegs>();
         if (warp == S::kMmaWarp) {
             // ----------------------------------------------------- products
             constexpr uint32_t type = BF ? idesc_bf16_f32(0, 0) : idesc_f16_f32(0, 0);
@@ -740,6 +718,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             bool fresh = true;
             uint32_t mark = 0;
             bool exact = false;
+            Bounds bounds;
             uint4 codes[kUnits];
             float4 scale;
             // where the fetched tile's keys are (nullptr: not held) and their scales
@@ -775,7 +754,8 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 const int x = t0 + 4 * lane, pg = __shfl_sync(0xFFFFFFFFu, page, (x >> log_page) - held);
                 scale_tokens = tokens - 4 * lane;
                 scale_src = scale_tokens > 0 ? reinterpret_cast<const float4 *>(head + pg * a.c.page_bytes + 2 * to_values + (x & (in_page - 1)) * 4) : nullptr;
-                exact = Bounds(a, w).exact(a, t0);
+                if (fresh) bounds = Bounds(a, w);
+                exact = bounds.exact(a, t0);
                 mark = (both() ? kTwo : 0u) | (fresh ? kFirst : 0u);
                 fresh = false;
                 if (++at >= w.upto) {
@@ -812,6 +792,10 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                     work = (flags & kEnd) == 0;
 #pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
+                        // (tested here, looked at after the factors are made)
+                        uint64_t *const room = &bars->k_empty[kt.slot], *const scales_room = &bars->scales_empty[sc.slot];
+                        const bool need_room = done >= S::kK, need_scales = kv == 0 && done >= 2 * S::kScaleSlots;
+                        const bool there = mbar_test_wait2(room, kt.phase ^ 1u, need_scales ? scales_room : room, need_scales ? sc.phase ^ 1u : kt.phase ^ 1u);
                         const float4 was = scale;
                         const float s[4] = {was.x, was.y, was.z, was.w};
                         if (kv == 1) aim();                            // keys of the next tile come next
@@ -833,8 +817,10 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) factor[i] = mine[i * 32 + me / 4];
-                        if (kv == 0 && done >= 2 * S::kScaleSlots && !warp_wait(&bars->scales_empty[sc.slot], sc.phase ^ 1u, a.wait_ns)) ok = false;
-                        if (ok && done >= S::kK && !warp_wait(&bars->k_empty[kt.slot], kt.phase ^ 1u, a.wait_ns)) ok = false;
+                        if (!__all_sync(0xFFFFFFFFu, there)) {
+                            if (need_scales && !warp_wait(scales_room, sc.phase ^ 1u, a.wait_ns)) ok = false;
+                            if (ok && need_room && !warp_wait(room, kt.phase ^ 1u, a.wait_ns)) ok = false;
+                        }
                         if (!ok) break;
                         uint8_t *dst = ks + kt.slot * S::kTileBytes;
 #pragma unroll
@@ -888,14 +874,16 @@ template <int KIND, int DP> cudaError_t launch(const AttnArgs &args, int sm_coun
     static_assert(TensorShape<KIND, DP>::kSmem <= kSmemOptIn, "shared memory");
     cudaError_t e = set_max_smem(f, TensorShape<KIND, DP>::kSmem);
     if (e != cudaSuccess) return e;
-    // the warpgroups' registers have to add up to what the launch has
-    static const bool enough = [f] {
-        using S = TensorShape<KIND, DP>;
-        cudaFuncAttributes fa{};
-        if (S::kSoftmaxRegs == S::kLaunchRegs) return true;   // they stay as they are
-        return cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs == S::kLaunchRegs && S::kLaunchRegs * S::kThreads >= S::kAllRegs;
-    }();
-    if (!enough) return cudaErrorLaunchOutOfResources;
+    if constexpr (TensorShape<KIND, DP>::kCodes) {
+        // the warpgroups' registers have to add up to what the launch has
+        static const bool enough = [f] {
+            using S = TensorShape<KIND, DP>;
+            cudaFuncAttributes fa{};
+            return cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs == S::kLaunchRegs &&
+                   4 * S::kLaunchRegs >= 2 * S::kSoftmaxRegs + S::kConvertRegs + S::kMmaRegs;
+        }();
+        if (!enough) return cudaErrorLaunchOutOfResources;
+    }
     *ctas = std::min(kTensorMaxCtas, sm_count);
     void *p[] = {&a};
     return launch_pdl(f, dim3(static_cast<unsigned>(*ctas)), dim3(TensorShape<KIND, DP>::kThreads), TensorShape<KIND, DP>::kSmem, s, p);
