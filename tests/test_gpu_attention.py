@@ -260,16 +260,23 @@ def test_rewound(q4lib):
     assert torch.equal(a, b)
 
 
-def test_bad_page_is_recorded(q4lib):
-    c = Cache(q4lib, [100], 1, 64, 16, "f16", fill=0)
-    q, o = rows(torch.ones(1, 64), "f16"), blank(1, 64, "f16")
+@pytest.mark.parametrize("name,cache", KINDS)
+@pytest.mark.parametrize("new", [1, 80])
+def test_bad_page_is_recorded(q4lib, name, cache, new):
+    c = Cache(q4lib, [100], 1, 64, 16, cache, fill=0)
+    q, o = rows(torch.ones(new, 64), name), blank(new, 64, name)
+    good = int(c.table[0, 3])
     for bad in (-1, c.n_pages, 1 << 30):
         c.table[0, 3] = bad
-        c.attend(o, q, "f16", 1, 0.1, 0, [100], [1])
+        c.attend(o, q, name, 1, 0.1, 0, [100], [new])
         torch.cuda.synchronize()
         assert q4lib.q4_last_device_status(clear=True) == q4lib.Q4_ERR_DEVICE_CHECK
     # not needed: not looked at
-    c.attend(o, q, "f16", 1, 0.1, 0, [48], [1])
-    c.attend(o, q, "f16", 1, 0.1, 36, [100], [1])
+    c.attend(o, q, name, 1, 0.1, 0, [48], [min(new, 48)])
+    c.attend(o, q, name, 1, 0.1, 36, [100], [1])
+    torch.cuda.synchronize()
+    assert q4lib.q4_last_device_status(clear=True) == 0
+    c.table[0, 3] = good
+    c.attend(o, q, name, 1, 0.1, 0, [100], [new])
     torch.cuda.synchronize()
     assert q4lib.q4_last_device_status(clear=True) == 0
