@@ -21,6 +21,7 @@ namespace q4 {
 
 constexpr int kMaxSeqs = 1024;      // sequences of a call
 constexpr int kMaxHeadDim = 256;
+constexpr int64_t kMaxVerifyVocab = int64_t(1) << 20;
 constexpr int kChunk = 64;          // dims of a chunk
 constexpr int kErrTimeout = 5, kErrCheck = 10;   // Q4_ERR_DEVICE_TIMEOUT, Q4_ERR_DEVICE_CHECK
 

@@ -13,7 +13,7 @@ namespace {
 constexpr int64_t kMaxRows = int64_t(1) << 30;     // rows x heads
 constexpr int64_t kMaxPageTokens = 1024;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;   // of a sequence
-constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxVerifyVocab = int64_t(1) << 20;
+constexpr int64_t kMaxVocab = int64_t(1) << 24;
 constexpr size_t kMetaBytes = 2 * sizeof(int4) * kAttnMaxCtas;
 
 cudaStream_t as_stream(q4mm_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }

@@ -5,7 +5,6 @@
 // thread-block cluster takes a row: each CTA a contiguous segment, and the CTAs'
 // sums meet in shared memory.
 #include <algorithm>
-#include <type_traits>
 
 #include "q4mm_cache.h"
 #include "q4mm_rows.cuh"
@@ -69,7 +68,7 @@ struct Segment {
 
 // --------------------------------------------------------- probabilities --
 
-constexpr int kProbsThreads = 256;
+constexpr int kProbsMaxThreads = 512;
 constexpr int kProbsBytes = 80 * 1024;     // of a segment, in shared memory at once
 
 // P = 2^((x - max) f) / sum, f = log2(e) / T. A segment comes into shared memory by one
@@ -79,7 +78,7 @@ constexpr int kProbsBytes = 80 * 1024;     // of a segment, in shared memory at 
 // copied piece by piece, and again for the results). Several CTAs an SM cover one
 // another's waits: 320 rows of 151936 bf16 by 1024 threads that held values in
 // registers, one CTA an SM, 205 us.
-template <typename T> __global__ void __launch_bounds__(kProbsThreads) probs_kernel(const ProbsArgs a, const int cluster)
+template <typename T> __global__ void __launch_bounds__(kProbsMaxThreads) probs_kernel(const ProbsArgs a, const int cluster)
 {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(128) uint8_t piece[];
@@ -99,7 +98,7 @@ template <typename T> __global__ void __launch_bounds__(kProbsThreads) probs_ker
     const int64_t row = blockIdx.x / cluster;
     const T *x = static_cast<const T *>(a.X) + row * a.ldx;
     const Segment seg(a.n, cluster, rank);
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, step = blockDim.x;
     const float inf = __int_as_float(0x7F800000);
     const uintptr_t begin = reinterpret_cast<uintptr_t>(x + seg.lo), end = reinterpret_cast<uintptr_t>(x + seg.hi);
     const uintptr_t base = begin & ~uintptr_t(15);
@@ -140,7 +139,7 @@ template <typename T> __global__ void __launch_bounds__(kProbsThreads) probs_ker
     const float f = temperature > 0.0f ? __fdiv_rn(1.4426950408889634f, temperature) : __int_as_float(0x7FC00000);
     float m = -inf, s = 0.0f;
     over(false, [&](int64_t w0, int n) {
-        for (int w = tid; w < n; w += kProbsThreads) {
+        for (int w = tid; w < n; w += step) {
             const Pack<T, V> p = word(w);
             const int64_t e = e0 + (w0 + w) * V;
             float v[V];
@@ -177,7 +176,7 @@ template <typename T> __global__ void __launch_bounds__(kProbsThreads) probs_ker
         unsigned int at = 0xFFFFFFFFu;
         if (m > -inf)
             over(true, [&](int64_t w0, int n) {
-                for (int w = tid; w < n; w += kProbsThreads) {
+                for (int w = tid; w < n; w += step) {
                     const Pack<T, V> u = word(w);
                     const int64_t e = e0 + (w0 + w) * V;
 #pragma unroll
@@ -194,7 +193,7 @@ template <typename T> __global__ void __launch_bounds__(kProbsThreads) probs_ker
         at = 0xFFFFFFFFu;
         for (int i = 0; i < cluster; ++i)
             if (__uint_as_float(static_cast<uint32_t>(first[i])) == best) at = min(at, static_cast<unsigned int>(first[i] >> 32));
-        for (int64_t c = seg.lo + tid; c < seg.hi; c += kProbsThreads) p[c] = c == at ? 1.0f : 0.0f;
+        for (int64_t c = seg.lo + tid; c < seg.hi; c += step) p[c] = c == at ? 1.0f : 0.0f;
         return;
     }
     s = block_reduce<true>(mine == -inf || mine == m ? s : s * exp2_fast((mine - m) * f), buf);
@@ -213,7 +212,7 @@ template <typename T> __global__ void __launch_bounds__(kProbsThreads) probs_ker
     const bool vec = ((reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(e0) * 4) & 15) == 0;
     over(true, [&](int64_t w0, int n) {
         if (vec) {
-            for (int w = tid; w < n; w += kProbsThreads) {
+            for (int w = tid; w < n; w += step) {
                 const Pack<T, V> u = word(w);
                 const int64_t e = e0 + (w0 + w) * V;
                 float v[V];
@@ -231,7 +230,7 @@ template <typename T> __global__ void __launch_bounds__(kProbsThreads) probs_ker
         } else {
             const T *values = reinterpret_cast<const T *>(piece);
             const int64_t at = e0 + w0 * V;
-            for (int i = tid; i < n * V; i += kProbsThreads) {
+            for (int i = tid; i < n * V; i += step) {
                 const int64_t e = at + i;
                 if (e >= seg.lo && e < seg.hi) p[e] = exp2_fast((elem(load_pack<T, 1>(values, i, n * V), 0) - from) * f) * inv;
             }
@@ -249,8 +248,10 @@ template <typename T> cudaError_t launch_probs(ProbsArgs a, int sm_count, cudaSt
     const void *f = reinterpret_cast<const void *>(&probs_kernel<T>);
     const cudaError_t e = set_max_smem(f, kProbsBytes);
     if (e != cudaSuccess) return e;
+    // (4 rows of 151936: 512 threads 6.7 us, 256 7.3; 320 rows: 78 and 68)
+    const unsigned threads = a.rows * cluster > sm_count ? 256 : kProbsMaxThreads;
     void *args[] = {&a, &cluster};
-    return launch_pdl(f, dim3(static_cast<unsigned>(a.rows * cluster)), dim3(kProbsThreads), smem, s, args, cluster);
+    return launch_pdl(f, dim3(static_cast<unsigned>(a.rows * cluster)), dim3(threads), smem, s, args, cluster);
 }
 
 // ---------------------------------------------------------- verification --
@@ -350,12 +351,15 @@ __device__ __forceinline__ int find(unsigned long long own, int n, unsigned long
     return at;
 }
 
-// A CTA's segment is cut into a contiguous stretch a warp: the sums of stretches need
-// one reduction each. The CTA that holds the drawn place then cuts the warp's stretch
-// among its warps in the same way, until a warp's access holds it.
+// A CTA's segment is cut into a contiguous stretch a warp, and that into batches of
+// kAhead accesses, whose sums are kept: they give the total, and the batch that holds
+// the drawn place, which one warp reads once more.
+constexpr int kAhead = 4, kMaxBatches = 1024;
+static_assert(kMaxVerifyVocab / kMaxCluster <= kMaxBatches * kAhead * 32, "a segment's batches, of one element an access");
+
 template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs a, const int cluster)
 {
-    __shared__ unsigned long long spans[kVerifyWarps], sums[2][kMaxCluster];
+    __shared__ unsigned long long spans[kMaxBatches], sums[2][kMaxCluster];
     __shared__ int kept_shared;
     pdl_wait();
     pdl_launch_dependents();
@@ -397,36 +401,35 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
     rest.q = refused && a.Q ? a.Q + (seq * a.max_draft + kept) * a.ldq : nullptr;
     rest.known = refused && !a.Q ? a.drafted[seq * a.ldd + kept] : -1;
     rest.hi = seg.hi;
-    // a stretch of `per` elements (whole vectors) from lo on, a warp each; its sum
-    const auto stretch = [&](auto ahead, int64_t lo, int64_t per, int64_t hi) {
-        const int64_t from = lo + warp * per, to = min(from + per, hi);
-        unsigned long long s = 0;
-        constexpr int kAhead = decltype(ahead)::value;   // accesses in flight
-        for (int64_t c0 = from + lane * V; c0 - lane * V < to; c0 += kAhead * 32 * V) {
-            Pack<float, V> x[kAhead], y[kAhead];
-            Steps st;
+    constexpr int kBatch = kAhead * 32 * V;
+    const int64_t per = ((seg.hi - seg.lo + warps - 1) / warps + 7) / 8 * 8;      // a warp's stretch, whole vectors
+    const int batches = static_cast<int>((per + kBatch - 1) / kBatch);
+    // a batch's accesses, in flight together
+    const auto fetch = [&](int64_t from, int64_t to, Pack<float, V> (&x)[kAhead], Pack<float, V> (&y)[kAhead]) {
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int64_t c = c0 + i * 32 * V;
-                rest.load<V>(c < to ? c : rest.hi, x[i], y[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                rest.add<V>(c0 + i * 32 * V, x[i], y[i], st);
-            }
-            s += st.total();
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t c = from + (i * 32 + lane) * V;
+            rest.load<V>(c < to ? c : rest.hi, x[i], y[i]);
         }
-        s = warp_sum(s);
-        if (lane == 0) spans[warp] = s;
     };
-    const auto share = [&](int64_t n) { return ((n + warps - 1) / warps + 7) / 8 * 8; };
     unsigned long long total = 0;
     // once; and once more, of p alone, where the draft leaves nothing of it
     for (int turn = 0; turn < 2; ++turn) {
-        int64_t lo = seg.lo, hi = seg.hi, per = share(hi - lo);
-        stretch(std::integral_constant<int, 4>{}, lo, per, hi);
+        const int64_t lo = seg.lo + warp * per, hi = min(lo + per, seg.hi);
+        for (int b = 0; b < batches; ++b) {
+            Pack<float, V> x[kAhead], y[kAhead];
+            fetch(lo + b * kBatch, hi, x, y);
+            Steps st;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) rest.add<V>(lo + b * kBatch + (i * 32 + lane) * V, x[i], y[i], st);
+            const unsigned long long s = warp_sum(st.total());
+            if (lane == 0) spans[warp * batches + b] = s;
+        }
         __syncthreads();
-        const unsigned long long mine = warp_sum(lane < warps ? spans[lane] : 0ull);
+        const int n_spans = warps * batches;
+        unsigned long long mine = 0;
+        for (int k = lane; k < n_spans; k += 32) mine += spans[k];
+        mine = warp_sum(mine);
         if (cluster > 1 && turn == 0) cluster_wait();
         exchange(sums[turn], mine, rank, cluster);
         total = 0;
@@ -437,41 +440,47 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
             // the one CTA whose segment holds the place, and CTA 0 where there is none
             const bool here = total > 0 ? target >= before && target - before < sums[turn][rank] : rank == 0;
             if (!here) return;
+            if (warp != 0) return;
             int64_t token = 0;
             if (total > 0) {
                 target -= before;
                 unsigned long long run = 0;
-                // every warp finds the stretch that holds the place, and takes its part of it
-                while (true) {
-                    const int at = find(lane < warps ? spans[lane] : 0ull, warps, target, run);
-                    lo += at * per, hi = min(lo + per, hi);
-                    if (per <= 32 * V) break;
-                    per = share(hi - lo);
-                    __syncthreads();
-                    stretch(std::integral_constant<int, 1>{}, lo, per, hi);
-                    __syncthreads();
+                int k0 = 0;
+                for (; k0 + 32 < n_spans; k0 += 32) {
+                    const unsigned long long s = warp_sum(spans[k0 + lane]);
+                    if (run + s > target) break;
+                    run += s;
                 }
-                if (warp != 0) return;
-                Pack<float, V> x, y;
-                const int64_t c = lo + lane * V;
-                rest.load<V>(c < hi ? c : rest.hi, x, y);
-                unsigned long long r[V], s = 0;
-                rest.of<V>(c, x, y, r);
+                const int k = k0 + find(k0 + lane < n_spans ? spans[k0 + lane] : 0ull, min(32, n_spans - k0), target, run);
+                const int64_t from = seg.lo + k / batches * per, c0 = from + k % batches * kBatch;
+                Pack<float, V> x[kAhead], y[kAhead];
+                fetch(c0, min(from + per, seg.hi), x, y);
+                bool found = false;
 #pragma unroll
-                for (int j = 0; j < V; ++j) s += r[j];
-                const int at = find(s, 32, target, run);
-                int found = 0;
+                for (int i = 0; i < kAhead; ++i) {
+                    unsigned long long r[V], s = 0;
+                    rest.of<V>(c0 + (i * 32 + lane) * V, x[i], y[i], r);
 #pragma unroll
-                for (int j = V - 1; j >= 0; --j) {
-                    unsigned long long upto = run;
+                    for (int j = 0; j < V; ++j) s += r[j];
+                    const unsigned long long all = warp_sum(s);
+                    if (found || run + all <= target) {
+                        run += all;
+                        continue;
+                    }
+                    found = true;
+                    const int at = find(s, 32, target, run);
+                    int which = 0;
 #pragma unroll
-                    for (int k = 0; k <= j; ++k) upto += r[k];
-                    if (upto > target) found = j;
+                    for (int j = V - 1; j >= 0; --j) {
+                        unsigned long long upto = run;
+#pragma unroll
+                        for (int e = 0; e <= j; ++e) upto += r[e];
+                        if (upto > target) which = j;
+                    }
+                    which = __shfl_sync(0xFFFFFFFFu, which, at);
+                    token = min(c0 + (i * 32 + at) * V + which, a.n - 1);
                 }
-                found = __shfl_sync(0xFFFFFFFFu, found, at);
-                token = min(lo + at * V + found, a.n - 1);
             }
-            if (warp != 0) return;
             for (int j = lane; j <= a.max_draft; j += 32)
                 a.tokens[seq * a.ldt + j] = j < kept ? a.drafted[seq * a.ldd + j] : j == kept ? static_cast<int32_t>(token) : -1;
             if (lane == 0) a.kept[seq] = kept;

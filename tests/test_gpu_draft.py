@@ -177,6 +177,19 @@ def test_edges_of_the_draw(q4lib, n):
         assert np.array_equal(got[0], want[0]) and not got[1].any()
 
 
+@pytest.mark.parametrize("slots", [1, 40])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_largest_vocabulary(q4lib, slots, pad):
+    """Equal probabilities of 2^-20 each: the token is the whole part of u 2^20, exactly."""
+    n = 1 << 20
+    p = torch.full((slots, n + pad), 2.0 ** -20, device="cuda")[:, :n]
+    sample = (torch.arange(slots, device="cuda", dtype=torch.float32) + 1 + 2.0 ** -10) / (slots + 1)
+    sample[-1] = 0.99999994
+    none, acc = torch.zeros((slots, 0), dtype=torch.int32, device="cuda"), torch.zeros((slots, 0), device="cuda")
+    got, _ = verify(q4lib, p, None, none, None, acc, sample, n)
+    assert np.array_equal(got[:, 0], np.floor(f64(sample) * n).astype(np.int32))
+
+
 def test_nothing_left(q4lib):
     """p = q with a token refused all the same, and rows of zeros."""
     n = 5000
