@@ -68,8 +68,9 @@ typedef struct CUstream_st *q4mm_stream_t;
 #define Q4_ERR_NO_MEMORY 7          /* the library could not allocate its own workspace */
 #define Q4_ERR_IO 8                 /* a file could not be opened or read */
 #define Q4_ERR_FORMAT 9             /* a file breaks the GGUF layout (q4_gguf_open) */
-#define Q4_ERR_DEVICE_CHECK 10      /* checked build: a kernel found an index or offset out of range and
-                                       skipped the access (read by q4_last_device_status) */
+#define Q4_ERR_DEVICE_CHECK 10      /* a kernel found an index or offset out of range and skipped the access: in any
+                                       build a page or place of the cache, in the checked build also those of
+                                       q4_build_flags() (read by q4_last_device_status) */
 
 /*
  * Packed weight layout (what q4_0_pack writes). Repacking the blocks at load
@@ -442,10 +443,10 @@ Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, 
  * other, sequence s's starts[s] .. starts[s + 1] - 1 (starts: device int32
  * [n_seq + 1], non-decreasing, a sequence may have none); lens[s] (device int32)
  * is how many tokens the sequence holds in the cache with the new ones, which are
- * its last. `rows` is at least starts[n_seq] (what the matrices hold); rows past
- * it are never written, and what they hold enters nothing. Nothing of the batch is read by the host, so
- * a captured call replays with other lengths. A sequence is rewound by calling
- * with a smaller len.
+ * its last. `rows` is at least starts[n_seq] (what the matrices hold); rows of the
+ * matrices from starts[n_seq] on are never written, and what they hold enters
+ * nothing. Nothing of the batch is read by the host, so a captured call replays with
+ * other lengths. A sequence is rewound by calling with a smaller len.
  *   table: device int32, row s at table + s * ldt: the pages of sequence s in the
  *   order of its tokens; token t is in page table[s][t / page_tokens]. Entries
  *   that no token of a call needs are not read. One page may stand in several rows
@@ -507,7 +508,10 @@ Q4MM_API size_t q4_attention_workspace_size(int64_t rows, int64_t n_seq, int64_t
  *   time need one each, and so do graphs whose replays can.
  * Precision: scores and sums in fp32. 16-bit types: products exact, the terms p
  * rounded once to the operands' type (fp16 over codes). F32: queries and terms
- * as two fp16 numbers (22 bits), about 1e-6 of the result. */
+ * as two fp16 numbers (22 bits), about 1e-6 of the result. BF16 over codes, d <=
+ * 128, in calls with max_new * heads / kv_heads above 64: tokens that a whole block
+ * of 256 query rows sees may have their keys and values (code times scale) rounded
+ * to fp16, next to the largest scale of 128 tokens: about 2^-10 of them. */
 Q4MM_API int q4_attention(void *O, int64_t ldo, const void *Q, int64_t ldq, int type, int64_t heads, float scale,
                           int64_t window, const void *pages, int64_t n_pages, int64_t page_tokens, int64_t kv_heads,
                           int64_t d, int ctype, const int32_t *table, int64_t ldt, const int32_t *lens,
@@ -597,8 +601,9 @@ Q4MM_API int q4_0_matmul_batched_slots_ws(const void *W_packed, const float *X_s
 Q4MM_API const char *q4_status_string(int status);
 
 /* Device status word of the current device: Q4_OK, Q4_ERR_DEVICE_TIMEOUT if
- * a kernel's bounded wait ran out, or Q4_ERR_DEVICE_CHECK (checked build
- * only) if a kernel's range check failed, since the word was last cleared
+ * a kernel's bounded wait ran out, or Q4_ERR_DEVICE_CHECK if a kernel's
+ * range check failed (a page or place of the cache in every build, the
+ * others in the checked build only), since the word was last cleared
  * (the first such event is kept). Synchronises the device. clear != 0 resets
  * the word to Q4_OK. */
 Q4MM_API int q4_last_device_status(int clear);
@@ -617,7 +622,8 @@ Q4MM_API int q4_build_flags(void);
  * and the kernel returns without its result. The decode mat-vec (the default
  * path for m <= 16) then still waits, for at least 0.2 s, for the transfers
  * already issued into its own shared memory, so any limit >= 1 is safe there,
- * and so it is for the int8 product of coded tokens and the norms;
+ * and so it is for the int8 product of coded tokens, the norms, q4_attention
+ * and q4_token_probs;
  * the other kernels take the limit as given for every wait and need one well
  * above their transfers' latency (>= 1 ms). */
 Q4MM_API int q4_set_wait_limit_ns(uint64_t ns);

@@ -13,8 +13,17 @@
 // by 2^8; the softmax threads scale O themselves (S of a tile is committed after
 // the products of the tile before, so O rests).
 //   Warps: 0-3 and 4-7 the halves' softmax (a row a thread: no shuffles), 8 issues the
-// products, 9 copies; over codes 8-11 turn them into fp16 tiles and 12 issues: the
-// scales of keys multiply scores, those of values terms, as in the warp-MMA kernel.
+// products, 9 copies. Over codes 8-11 turn them into fp16 tiles and 12 issues; where the
+// scales go, Bounds says.
+//   What bounds it (clocks of a tile of 128 tokens, both halves): the products' 2048 and
+// what the waits between them add. A test of a barrier that is already there answers
+// after some 190 while products read shared memory, and the queue of products holds
+// about three of 64: a loop takes 3300. 2048 new tokens over 16384, 32 heads on 8 of
+// 128: 412 us, 1250 TFLOP/s (65 % of the measured bf16 rate); over codes the converting
+// warps' 3000 a tile of K or V bound it (540 over 8100: 153 us); short items (windowed
+// prompts of 2000, 540 wide: 67 us) their start and end, 8000 to 10000 an item. Tried and
+// slower: two issuing warps (the halves fall into step), 16 softmax warps with half a
+// row each, scores held in registers between the maximum and the terms (spills).
 //   K and V lie in the pages as the tensor cores read them, 64 dims a row of 128
 // bytes, swizzled: K as a K-major operand, V (dims contiguous) as an N-major one.
 //   A page's rows past the sequence's end are never copied: what their place holds

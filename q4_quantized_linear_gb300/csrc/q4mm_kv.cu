@@ -108,8 +108,7 @@ template <typename C> __device__ __forceinline__ bool finite8(const Pack<C, 8> &
 }
 
 // code_of() of eight values: the product, rounded, plus 1.5 2^23 has the nearest
-// integer (halves to even) in its low bits. (By conversions the kernel was bound by
-// them: 4 prompts of 2048 fp32 into int8, 67 MB.)
+// integer (halves to even) in its low bits, without a conversion a value.
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float factor)
 {
     uint32_t b[8];
@@ -122,9 +121,12 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float factor)
     return w;
 }
 
-// Heads' rows that a thread has in flight: its loads' latency, not the rate, bounds one
-// (4 prompts of 2048 fp32 into int8: 17 us with one, 67 MB).
-constexpr int kWriteAhead = 1, kReadAhead = 4, kBlocksPerSM = 8;
+// Heads' rows that a thread has in flight, and CTAs an SM at most. 4 prompts of up to 2048
+// fp32 into int8 take 33 us (135 MB, 4.1 TB/s), 3 x up to 8000 int8 into bf16 21.5 (97 MB,
+// 4.5 TB/s), bf16 into bf16 22.6 (128 MB, 5.7 TB/s). Within a microsecond of that: two and
+// four rows, 8 and 64 CTAs, the next row's loads before a row is stored, a CTA's rows
+// along a head instead of a token; slower: 32-byte loads, 16 codes a lane (29).
+constexpr int kWriteAhead = 1, kReadAhead = 2, kBlocksPerSM = 16;
 
 // C: the cache's element type (int8_t: codes).
 template <typename T, typename C, int L, bool VEC> __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvRowsArgs a)
