@@ -23,7 +23,9 @@
 // warps' 3000 a tile of K or V bound it (540 over 8100: 153 us); short items (windowed
 // prompts of 2000, 540 wide: 67 us) their start and end, 8000 to 10000 an item. Tried and
 // slower: two issuing warps (the halves fall into step), 16 softmax warps with half a
-// row each, scores held in registers between the maximum and the terms (spills).
+// row each, scores held in registers between the maximum and the terms (spills), eight
+// converting warps, four for keys and four for values (150 to 188 us by the registers'
+// split: what the ninth to sixteenth warp gain, spills lose).
 //   K and V lie in the pages as the tensor cores read them, 64 dims a row of 128
 // bytes, swizzled: K as a K-major operand, V (dims contiguous) as an N-major one.
 //   A page's rows past the sequence's end are never copied: what their place holds
