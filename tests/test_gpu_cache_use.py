@@ -2,6 +2,9 @@
 uses them: one behind the other, in captured graphs whose batches change between
 replays, on other streams, from two threads, and with waits that run out."""
 
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -276,3 +279,55 @@ def test_waits_that_run_out(q4lib, name, cache, new):
             assert q4lib.q4_last_device_status(clear=True) == 0 and torch.equal(o, good)
     finally:
         q4lib.q4_set_wait_limit_ns(2_000_000_000)
+
+
+_FIRST = """
+import torch
+from q4_quantized_linear_gb300 import binding as q4
+heads, kv_heads, d, page, n, rows = 8, 2, 128, 32, 5000, 300
+g = torch.Generator(device="cuda").manual_seed(5)
+ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+K, V, Q = (torch.randn(rows, h * d, generator=g, device="cuda").to(torch.bfloat16) for h in (kv_heads, kv_heads, heads))
+pages = torch.zeros((10, q4.q4_kv_page_size(page, kv_heads, d, q4.Q4_TYPE_I8)), dtype=torch.uint8, device="cuda")
+cache = (pages, 10, page, kv_heads, d, q4.Q4_TYPE_I8, torch.arange(10, dtype=torch.int32, device="cuda"), 10)
+batch = (ints(rows), ints(0, rows), 1)
+need = q4.q4_attention_workspace_size(rows, 1, heads, kv_heads, d)
+ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+O, k, v = torch.zeros_like(Q), torch.zeros_like(K), torch.zeros_like(V)
+logits = torch.randn(4, n, generator=g, device="cuda")
+P, tokens, kept = torch.zeros(4, n, device="cuda"), torch.zeros((1, 4), dtype=torch.int32, device="cuda"), ints(0)
+accept, sample, drafted = torch.full((1, 3), 0.5, device="cuda"), torch.full((1,), 0.5, device="cuda"), ints(1, 2, 3).reshape(1, 3)
+
+
+def step():
+    q4.q4_kv_write(*cache, *batch, K, kv_heads * d, V, kv_heads * d, q4.Q4_TYPE_BF16, rows)
+    q4.q4_attention(O, heads * d, Q, heads * d, q4.Q4_TYPE_BF16, heads, d ** -0.5, 0, *cache, *batch, rows, 0, ws, need)
+    q4.q4_kv_read(k, kv_heads * d, v, kv_heads * d, q4.Q4_TYPE_BF16, *cache, None, ints_0, 1, rows)
+    q4.q4_token_probs(P, n, logits, n, q4.Q4_TYPE_F32, None, 4, n)
+    q4.q4_draft_verify(tokens, 4, kept, P, n, None, 0, drafted, 3, None, accept, 3, sample, 1, 3, n)
+
+
+ints_0 = batch[1]
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    step()
+out = (O, k, v, P, tokens, kept)
+graph.replay()
+torch.cuda.synchronize()
+first = [x.clone() for x in out]
+for x in out:
+    x.zero_()
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(first, out)) and bool(first[0].any()) and bool(first[3].any())
+assert q4.q4_last_device_status(clear=True) == 0
+print("same")
+"""
+
+
+def test_first_call_is_captured(q4lib):
+    """A process whose first calls are captured gives what the plain calls give."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", _FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "same" in done.stdout, done.stderr[-2000:]
