@@ -23,6 +23,11 @@
 // a row's four lanes have seen is brought together only then.
 //   A page's rows past the sequence's end are never copied: what their place in
 // the ring holds is zeros or an earlier tile's, finite as all values of the cache.
+//   Measured, 32 heads on 8 of 128: 16 x 5 tokens over up to 4096, bf16 44 us (203 MB,
+// 4.6 TB/s); 16 x 1 over up to 8192, int8 44 with its write (153 MB; the chains from
+// codes to products, 54 % of the issue slots); one token over 1000, fp32 12 with its
+// write (three launches that wait for one another); 540 over 8100, fp32 over fp16 366
+// and over int8 590 (products: four for the two of 16-bit types).
 #pragma once
 
 #include <type_traits>
