@@ -496,7 +496,9 @@ Q4MM_API size_t q4_attention_workspace_size(int64_t rows, int64_t n_seq, int64_t
 /* Attention of the new tokens over the cache, which holds their own keys and
  * values already (q4_kv_write of the same batch). Query head h uses cached head
  * h / (heads / kv_heads); the token at place x sees the places y <= x, and with
- * window > 0 only y > x - window:
+ * window > 0 only y > x - window (what lies before all of a sequence's windows need
+ * not be there: its table entries are not read, its places need never have been
+ * written):
  *     O[r][h] = sum_y p_y V_y / sum_y p_y,   p_y = exp(scale * <Q[r][h], K_y>)
  * A row that sees nothing (a len below the number of new tokens) gives zeros.
  *   Q, O: device, heads of d values next to each other, one type: F32, F16 or BF16

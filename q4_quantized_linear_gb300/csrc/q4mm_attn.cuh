@@ -198,11 +198,22 @@ __device__ __forceinline__ void put_meta(const AttnArgs &a, const Walk &w)
     a.meta[2 * blockIdx.x + 1] = make_int4(w.q.start, 0, 0, 0);
 }
 
-// Page i of a sequence that needs `pages` (0 past them). One that the cache does not
-// have is recorded, and one that it has is read in its place.
-__device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *table, int i, int pages)
+// The first token that some row of the item's block sees. What lies before it is not
+// there: its table entries are not looked at (a server may have given the pages back),
+// its places may never have been written, and a tile that holds some of them has no
+// values there (0, for a term of 0 times NaN is NaN).
+__device__ __forceinline__ int first_seen(const AttnArgs &a, const Walk &w)
 {
-    const int page = i < pages ? table[i] : 0;
+    int lo, x;
+    row_range(a, w.q, w.b * a.block, lo, x);
+    return lo;
+}
+// Page i of a sequence of which an item needs first .. upto - 1 (-1: not one of them).
+// One that the cache does not have is recorded, and one that it has is read in its place.
+__device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *table, int i, int first, int upto)
+{
+    if (i < first || i >= upto) return -1;
+    const int page = table[i];
     if (page >= 0 && page < a.c.n_pages) return page;
     record_status(a.status, kErrCheck);
     return min(max(page, 0), a.c.n_pages - 1);

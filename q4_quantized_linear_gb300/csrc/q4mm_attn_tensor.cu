@@ -103,12 +103,12 @@ struct Turn {
 // scales a row and tile from shared memory, which the products' operands keep busy,
 // took the softmax 7000 clocks of a tile's 2048 (540 tokens over 8100: 205 us).
 struct Bounds {
-    int from = 0, upto = 0;
+    int begin = 0, from = 0, upto = 0;   // (begin: first_seen())
     __device__ __forceinline__ Bounds() {}
     __device__ __forceinline__ Bounds(const AttnArgs &a, const Walk &w)
     {
         int x;
-        row_range(a, w.q, w.b * a.block, x, upto);
+        row_range(a, w.q, w.b * a.block, begin, upto);
         row_range(a, w.q, min((w.b + 1) * a.block, w.q.rows) - 1, from, x);
     }
     __device__ __forceinline__ bool exact(const AttnArgs &a, int t0) const { return a.type != Q4_TYPE_BF16 || t0 + kTile > upto || t0 < from; }
@@ -649,14 +649,15 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             for (; ok && w.valid(); w.next(a)) {
                 const int32_t *table = a.c.table + w.s * a.c.ldt;
                 const int64_t head = static_cast<int64_t>(w.h) * a.c.head_bytes;
-                const int end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> a.c.log_page;
+                const int begin = first_seen(a, w), end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> a.c.log_page;
                 int held = -32, page = 0;                              // lane l holds page held + l of the sequence
                 for (int t = w.from; ok && t < w.upto; ++t, ++issued) {
-                    const int t0 = (w.first + t) * kTile, tokens = min(max(end - t0, 0), kTile);
-                    const int p0 = t0 >> a.c.log_page, np = tokens > 0 ? ((t0 + tokens - 1) >> a.c.log_page) - p0 + 1 : 0;
+                    // tokens lo .. lo + tokens - 1 of the tile are there
+                    const int t0 = (w.first + t) * kTile, lo = max(t0, begin), tokens = max(min(end, t0 + kTile) - lo, 0);
+                    const int p0 = lo >> a.c.log_page, np = tokens > 0 ? ((lo + tokens - 1) >> a.c.log_page) - p0 + 1 : 0;
                     if (np > 0 && p0 + np > held + 32) {
                         held = p0;
-                        page = page_of(a, table, held + lane, pages);
+                        page = page_of(a, table, held + lane, p0, pages);
                     }
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {                   // keys, then values
@@ -672,6 +673,13 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         }
                         ok = __all_sync(0xFFFFFFFFu, go) != 0;
                         if (!ok) break;
+                        if (kv == 1 && lo > t0) {
+                            // no values before the block's first token
+                            for (int x = lane; x < (lo - t0) * CH * 8; x += 32)
+                                sts128(dst + x / ((lo - t0) * 8) * kAtomRows + x % ((lo - t0) * 8) * 16, make_uint4(0u, 0u, 0u, 0u));
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
                         if (lane == 0) {
                             if (kv == 0) {
                                 uint32_t flags = (both() ? kTwo : 0u) | (t == w.from ? kFirst : 0u);
@@ -690,9 +698,9 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                             const int x = x0 + lane, j = x / CH, y = x % CH;
                             const int pg = __shfl_sync(0xFFFFFFFFu, page, min(p0 + j - held, 31));
                             if (x < pieces) {
-                                const int in = max(t0 - ((p0 + j) << a.c.log_page), 0);
+                                const int in = max(lo - ((p0 + j) << a.c.log_page), 0);
                                 const int at = ((p0 + j) << a.c.log_page) + in - t0;
-                                const int n = min(in_page - in, tokens - at);
+                                const int n = min(in_page - in, lo - t0 + tokens - at);
                                 bulk_g2s(dst + y * kAtomRows + at * 128,
                                          a.c.pages + pg * a.c.page_bytes + head + ((kv * CH + y) * in_page + in) * 128,
                                          static_cast<uint32_t>(n * 128), full);
@@ -735,37 +743,37 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             // where the fetched tile's keys are (nullptr: not held) and their scales
             const uint8_t *src[4];
             const float4 *scale_src;
-            int scale_tokens;
+            int scale_there;                                           // bits of its four tokens that are there
             const auto aim = [&] {
                 if (!w.valid()) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) src[i] = nullptr;
-                    scale_src = nullptr, scale_tokens = 0;
+                    scale_src = nullptr, scale_there = 0;
                     return;
                 }
                 const int end = min(w.hi, w.q.len), t0 = (w.first + at) * kTile, tokens = min(max(end - t0, 0), kTile);
                 const int32_t *table = a.c.table + w.s * a.c.ldt;
                 const int p0 = t0 >> log_page, pages = (end + in_page - 1) >> log_page;
                 if (fresh) {
+                    bounds = Bounds(a, w);
                     held = p0;
-                    page = page_of(a, table, held + lane, pages);
-                    ahead = page_of(a, table, held + 32 + lane, pages);
+                    page = page_of(a, table, held + lane, bounds.begin >> log_page, pages);
+                    ahead = page_of(a, table, held + 32 + lane, bounds.begin >> log_page, pages);
                 } else if (p0 >= held + 32) {                          // (a tile's pages never straddle: 32 is a multiple of their number)
                     held += 32;
                     page = ahead;
-                    ahead = page_of(a, table, held + 32 + lane, pages);
+                    ahead = page_of(a, table, held + 32 + lane, bounds.begin >> log_page, pages);
                 }
                 const uint8_t *head = a.c.pages + static_cast<int64_t>(w.h) * a.c.head_bytes;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int tok = i * 32 + me / 4, x = t0 + tok;
                     const int pg = __shfl_sync(0xFFFFFFFFu, page, (x >> log_page) - held);
-                    src[i] = tok < tokens ? head + pg * a.c.page_bytes + (x & (in_page - 1)) * 64 + 16 * unit : nullptr;
+                    src[i] = tok < tokens && x >= bounds.begin ? head + pg * a.c.page_bytes + (x & (in_page - 1)) * 64 + 16 * unit : nullptr;
                 }
                 const int x = t0 + 4 * lane, pg = __shfl_sync(0xFFFFFFFFu, page, (x >> log_page) - held);
-                scale_tokens = tokens - 4 * lane;
-                scale_src = scale_tokens > 0 ? reinterpret_cast<const float4 *>(head + pg * a.c.page_bytes + 2 * to_values + (x & (in_page - 1)) * 4) : nullptr;
-                if (fresh) bounds = Bounds(a, w);
+                scale_there = (15 >> (4 - min(max(tokens - 4 * lane, 0), 4))) & (15 << min(max(bounds.begin - x, 0), 4));
+                scale_src = scale_there != 0 ? reinterpret_cast<const float4 *>(head + pg * a.c.page_bytes + 2 * to_values + (x & (in_page - 1)) * 4) : nullptr;
                 exact = bounds.exact(a, t0);
                 mark = (both() ? kTwo : 0u) | (fresh ? kFirst : 0u);
                 fresh = false;
@@ -782,9 +790,10 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             };
             const auto load_scales = [&](int kv) {
                 float4 s = scale_src ? __ldcg(scale_src + kv * (in_page / 4)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (scale_tokens < 4) s.w = 0.0f;
-                if (scale_tokens < 3) s.z = 0.0f;
-                if (scale_tokens < 2) s.y = 0.0f;
+                if (!(scale_there & 1)) s.x = 0.0f;
+                if (!(scale_there & 2)) s.y = 0.0f;
+                if (!(scale_there & 4)) s.z = 0.0f;
+                if (!(scale_there & 8)) s.w = 0.0f;
                 return s;
             };
             aim();

@@ -174,10 +174,10 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
         for (; ok && w.valid(); w.next(a)) {
             const int32_t *table = a.c.table + w.s * a.c.ldt;
             const uint8_t *head = a.c.pages + static_cast<int64_t>(w.h) * a.c.head_bytes;
-            const int end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> log_page;
+            const int end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> log_page, first_page = first_seen(a, w) >> log_page;
             // lane l holds page held + l of the sequence, and the one 32 further on
             int held = ((w.first + w.from) * kWarpTile) >> log_page;
-            int page = page_of(a, table, held + lane, pages), ahead = page_of(a, table, held + 32 + lane, pages);
+            int page = page_of(a, table, held + lane, first_page, pages), ahead = page_of(a, table, held + 32 + lane, first_page, pages);
             for (int t = w.from; t < w.upto; ++t) {
                 const int t0 = (w.first + t) * kWarpTile, tokens = min(max(end - t0, 0), kWarpTile);
                 const int p0 = t0 >> log_page;
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
                 if (p0 >= held + 32) {                      // (a tile's pages never straddle: 32 is a multiple of their number)
                     page = ahead;
                     held += 32;
-                    ahead = page_of(a, table, held + 32 + lane, pages);
+                    ahead = page_of(a, table, held + 32 + lane, first_page, pages);
                 }
                 if (*reinterpret_cast<volatile int *>(abort)) { ok = false; break; }
                 if (issued >= a.stages && !tile_wait(&empty[stage], phase ^ 1u, a.wait_ns)) {
@@ -198,22 +198,28 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
                 if (!ok) break;
                 uint8_t *dst = ring + stage * stage_bytes;
                 const int rest_scales = KIND == kI8 ? (rest + 3) & ~3 : 0;
-                if (lane == 0) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(whole * block_bytes + rest * 2 * chunks * RB + 8 * rest_scales));
-                __syncwarp();
                 const int y = lane - 8;                     // lanes 8 and on: a piece each of the page that is not whole
                 const int pg = __shfl_sync(0xFFFFFFFFu, page, min(p0 - held + min(lane, whole), 31));
                 const uint8_t *src = head + pg * a.c.page_bytes;
-                if (lane < whole) {
-                    bulk_g2s(dst + lane * block_bytes, src, static_cast<uint32_t>(block_bytes), &full[stage]);
-                } else if (y >= 0 && y < per_page && rest > 0) {
+                int bytes = 0;                              // (a page behind the window: none)
+                if (pg >= 0 && lane < whole) {
+                    bytes = block_bytes;
+                    dst += lane * block_bytes;
+                } else if (pg >= 0 && y >= 0 && y < per_page && rest > 0) {
                     const int in = in_page <= kWarpTile ? 0 : t0 & (in_page - 1);
                     dst += whole * block_bytes;
-                    if (y < 2 * chunks)
-                        bulk_g2s(dst + y * chunk_bytes, src + (y * in_page + in) * RB, static_cast<uint32_t>(rest * RB), &full[stage]);
-                    else
-                        bulk_g2s(dst + scales_at + (y - 2 * chunks) * (together * 4), src + 2 * chunks * in_page * RB + ((y - 2 * chunks) * in_page + in) * 4,
-                                 static_cast<uint32_t>(rest_scales * 4), &full[stage]);
+                    if (y < 2 * chunks) {
+                        bytes = rest * RB;
+                        dst += y * chunk_bytes, src += (y * in_page + in) * RB;
+                    } else {
+                        bytes = rest_scales * 4;
+                        dst += scales_at + (y - 2 * chunks) * (together * 4), src += 2 * chunks * in_page * RB + ((y - 2 * chunks) * in_page + in) * 4;
+                    }
                 }
+                const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(bytes));
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], all);
+                __syncwarp();
+                if (bytes > 0) bulk_g2s(dst, src, static_cast<uint32_t>(bytes), &full[stage]);
                 ++issued;
                 if (++stage == a.stages) stage = 0, phase ^= 1u;
             }
@@ -348,14 +354,14 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
             for (int ks = 0; ks < DP / 16; ++ks) load_q(0, ks, qr[ks]);
         }
         const float rf0 = row_factor[wm * 16 + g], rf1 = row_factor[wm * 16 + g + 8];
-        int lo0, hi0, lo1, hi1, full_from, full_upto;
+        int lo0, hi0, lo1, hi1, begin, full_from, full_upto;
         const int end = min(w.hi, w.q.len);
         {
             const int r0 = min(w.b * S::kBlock + wm * 16 + g, w.q.rows - 1), r1 = min(w.b * S::kBlock + wm * 16 + g + 8, w.q.rows - 1);
             row_range(a, w.q, r0, lo0, hi0);
             row_range(a, w.q, r1, lo1, hi1);
             int x;
-            row_range(a, w.q, w.b * S::kBlock, x, full_upto);                                  // the first row's end
+            row_range(a, w.q, w.b * S::kBlock, begin, full_upto);                              // the first row's start and end
             row_range(a, w.q, min((w.b + 1) * S::kBlock, w.q.rows) - 1, full_from, x);         // the last row's start
         }
         float o[OT][4] = {};
@@ -445,11 +451,25 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
                         if (!sees0) s[nt][i] = neg_inf();
                         if (!sees1) s[nt][2 + i] = neg_inf();
                         if constexpr (KIND == kI8) {
-                            if (x >= end) sv[nt][i] = 0.0f;     // a token that was not copied has no scale
+                            if (x < begin || x >= end) sv[nt][i] = 0.0f;   // a token that is not there has no scale
                             if (sees0) v0max = fmaxf(v0max, sv[nt][i]);
                             if (sees1) v1max = fmaxf(v1max, sv[nt][i]);
                         }
                     }
+                }
+                if (KIND != kI8 && t0 < begin) {
+                    // no values before the block's first token (each warp that reads them
+                    // clears them: the others write the same)
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) {
+#pragma unroll 1
+                        for (int y = lane >> 3; y < min(begin - t0 - 16 * i, 16); y += 4) {
+                            for (int ch = 0; ch < chunks; ++ch)
+                                sts128(ring + stage * stage_bytes + v_at + ch * chunk_bytes + off[i] + y * RB + 16 * (lane & 7), make_uint4(0u, 0u, 0u, 0u));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
                 }
             } else if constexpr (KIND == kI8) {
 #pragma unroll
