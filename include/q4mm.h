@@ -453,8 +453,10 @@ Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, 
  *   (a shared beginning); a call that writes a place twice leaves either.
  * A sequence holds at most ldt * page_tokens tokens (and 2^30); a longer len counts
  * as that. A page that a call needs and that is not 0 .. n_pages - 1 is recorded
- * as Q4_ERR_DEVICE_CHECK (q4_last_device_status) and nothing is accessed past the
- * cache; what such a token gives is unspecified.
+ * as Q4_ERR_DEVICE_CHECK (q4_last_device_status) and nothing is read or written in
+ * its place; what the rows that see such a token get is unspecified, the others are
+ * what they are without it. Places of a sequence that its rows see and that were never
+ * written give that sequence's rows anything; other sequences are not touched by it.
  *
  * pages: n_pages blobs of q4_kv_page_size bytes, 16-byte aligned, in the layout
  * that the kernels read: for each head K, then V, each as [64 dims][token][64

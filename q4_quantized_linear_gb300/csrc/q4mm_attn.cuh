@@ -209,14 +209,15 @@ __device__ __forceinline__ int first_seen(const AttnArgs &a, const Walk &w)
     return lo;
 }
 // Page i of a sequence of which an item needs first .. upto - 1 (-1: not one of them).
-// One that the cache does not have is recorded, and one that it has is read in its place.
+// One that the cache does not have is recorded: -2, nothing is read in its place, and
+// its values are 0, so that rows that do not see its tokens are what they are without it.
 __device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *table, int i, int first, int upto)
 {
     if (i < first || i >= upto) return -1;
     const int page = table[i];
     if (page >= 0 && page < a.c.n_pages) return page;
     record_status(a.status, kErrCheck);
-    return min(max(page, 0), a.c.n_pages - 1);
+    return -2;
 }
 
 // ----------------------------------------------------------- arithmetic --

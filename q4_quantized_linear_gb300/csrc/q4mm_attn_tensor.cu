@@ -28,8 +28,9 @@
 // split: what the ninth to sixteenth warp gain, spills lose).
 //   K and V lie in the pages as the tensor cores read them, 64 dims a row of 128
 // bytes, swizzled: K as a K-major operand, V (dims contiguous) as an N-major one.
-//   A page's rows past the sequence's end are never copied: what their place holds
-// is zeros or an earlier tile's values, finite as all values of the cache.
+//   Places before a block's first visible token and past its last are never copied: what
+// is in their place may be another sequence's, of a page that was never written at
+// that, so their values are set to 0 beside the copies of a tile that has some.
 #include <algorithm>
 #include <type_traits>
 
@@ -185,9 +186,6 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
     pdl_launch_dependents();
     Walk w;
     w.begin(a, reinterpret_cast<long long *>(qs));
-    if (!CODES)
-        for (int x = tid; x < S::kV * S::kTileBytes / 16; x += S::kThreads) sts128(vs + 16 * x, make_uint4(0u, 0u, 0u, 0u));
-    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -673,13 +671,29 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         }
                         ok = __all_sync(0xFFFFFFFFu, go) != 0;
                         if (!ok) break;
-                        if (kv == 1 && lo > t0) {
-                            // no values before the block's first token
-                            for (int x = lane; x < (lo - t0) * CH * 8; x += 32)
-                                sts128(dst + x / ((lo - t0) * 8) * kAtomRows + x % ((lo - t0) * 8) * 16, make_uint4(0u, 0u, 0u, 0u));
-                            fence_proxy_async_smem();
-                            __syncwarp();
+                        // a lane copies 64 dims of a page's tokens: n from row `at` of the tile on
+                        static_assert(kTile / 16 * CH <= 32, "a lane a piece");
+                        const int j = lane / CH, y = lane % CH, pg = __shfl_sync(0xFFFFFFFFu, page, min(p0 + j - held, 31));
+                        const int in = max(lo - ((p0 + j) << a.c.log_page), 0), at = ((p0 + j) << a.c.log_page) + in - t0;
+                        const int n = j < np ? min(in_page - in, lo - t0 + tokens - at) : 0;
+                        if (kv == 1) {
+                            // no values where no token is, and none of a page that the cache does not have
+                            const auto clear = [&](int from, int upto, int chunk) {
+                                for (int i = 8 * from + lane; i < 8 * upto; i += 32) sts128(dst + chunk * kAtomRows + 16 * i, make_uint4(0u, 0u, 0u, 0u));
+                            };
+                            unsigned bad = __ballot_sync(0xFFFFFFFFu, n > 0 && pg < 0);
+                            if (tokens < kTile || bad != 0) {
+                                for (int i = 0; i < CH; ++i) clear(0, lo - t0, i), clear(lo - t0 + tokens, kTile, i);
+                                for (; bad != 0; bad &= bad - 1) {
+                                    const int l = __ffs(bad) - 1, from = __shfl_sync(0xFFFFFFFFu, at, l);
+                                    clear(from, from + __shfl_sync(0xFFFFFFFFu, n, l), l % CH);
+                                }
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                            }
                         }
+                        const int bytes = pg >= 0 ? n * 128 : 0;
+                        const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(bytes));
                         if (lane == 0) {
                             if (kv == 0) {
                                 uint32_t flags = (both() ? kTwo : 0u) | (t == w.from ? kFirst : 0u);
@@ -690,22 +704,12 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                                 }
                                 bars->flags[tn.slot] = flags;
                             }
-                            mbar_arrive_expect_tx(full, static_cast<uint32_t>(tokens * CH * 128));
+                            mbar_arrive_expect_tx(full, all);
                         }
                         __syncwarp();
-                        const int pieces = np * CH;
-                        for (int x0 = 0; x0 < pieces; x0 += 32) {
-                            const int x = x0 + lane, j = x / CH, y = x % CH;
-                            const int pg = __shfl_sync(0xFFFFFFFFu, page, min(p0 + j - held, 31));
-                            if (x < pieces) {
-                                const int in = max(lo - ((p0 + j) << a.c.log_page), 0);
-                                const int at = ((p0 + j) << a.c.log_page) + in - t0;
-                                const int n = min(in_page - in, lo - t0 + tokens - at);
-                                bulk_g2s(dst + y * kAtomRows + at * 128,
-                                         a.c.pages + pg * a.c.page_bytes + head + ((kv * CH + y) * in_page + in) * 128,
-                                         static_cast<uint32_t>(n * 128), full);
-                            }
-                        }
+                        if (bytes > 0)
+                            bulk_g2s(dst + y * kAtomRows + at * 128, a.c.pages + pg * a.c.page_bytes + head + ((kv * CH + y) * in_page + in) * 128,
+                                     static_cast<uint32_t>(bytes), full);
                         landing_k = kv == 0 ? issued + 1 : landing_k;
                         landing_v = kv == 1 ? issued + 1 : landing_v;
                         tn.step(kDepth[kv]);
@@ -769,10 +773,11 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                 for (int i = 0; i < 4; ++i) {
                     const int tok = i * 32 + me / 4, x = t0 + tok;
                     const int pg = __shfl_sync(0xFFFFFFFFu, page, (x >> log_page) - held);
-                    src[i] = tok < tokens && x >= bounds.begin ? head + pg * a.c.page_bytes + (x & (in_page - 1)) * 64 + 16 * unit : nullptr;
+                    src[i] = tok < tokens && x >= bounds.begin && pg >= 0 ? head + pg * a.c.page_bytes + (x & (in_page - 1)) * 64 + 16 * unit : nullptr;
                 }
                 const int x = t0 + 4 * lane, pg = __shfl_sync(0xFFFFFFFFu, page, (x >> log_page) - held);
                 scale_there = (15 >> (4 - min(max(tokens - 4 * lane, 0), 4))) & (15 << min(max(bounds.begin - x, 0), 4));
+                if (pg < 0) scale_there = 0;                           // a page that the cache does not have
                 scale_src = scale_there != 0 ? reinterpret_cast<const float4 *>(head + pg * a.c.page_bytes + 2 * to_values + (x & (in_page - 1)) * 4) : nullptr;
                 exact = bounds.exact(a, t0);
                 mark = (both() ? kTwo : 0u) | (fresh ? kFirst : 0u);

@@ -21,8 +21,9 @@
 // sum to fp32, so the sums over a tile start at zero and are added in fp32.
 //   A running maximum is raised only where a row's scores pass it by 2^8, and what
 // a row's four lanes have seen is brought together only then.
-//   A page's rows past the sequence's end are never copied: what their place in
-// the ring holds is zeros or an earlier tile's, finite as all values of the cache.
+//   Places before a block's first visible token and past its last are never looked at
+// as values: what is in their place in the ring may be another sequence's, of a page
+// that was never written at that, so the warps that multiply by it clear it first.
 //   Measured, 32 heads on 8 of 128: 16 x 5 tokens over up to 4096, bf16 44 us (203 MB,
 // 4.6 TB/s); 16 x 1 over up to 8192, int8 44 with its write (153 MB; the chains from
 // codes to products, 54 % of the issue slots); one token over 1000, fp32 12 with its
@@ -152,9 +153,6 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
         *abort = 0;
         fence_barrier_init();
     }
-    if (KIND != kI8)
-        for (int x = tid; x < a.stages * stage_bytes / 16; x += kAttnThreads) sts128(ring + 16 * x, make_uint4(0u, 0u, 0u, 0u));
-    fence_proxy_async_smem();
     pdl_wait();
     pdl_launch_dependents();
     Walk w;
@@ -215,6 +213,13 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
                         bytes = rest_scales * 4;
                         dst += scales_at + (y - 2 * chunks) * (together * 4), src += 2 * chunks * in_page * RB + ((y - 2 * chunks) * in_page + in) * 4;
                     }
+                }
+                // a page that the cache does not have: no values and no scales
+                for (unsigned bad = __ballot_sync(0xFFFFFFFFu, pg == -2 && (lane < whole || (y == 0 && rest > 0))); bad != 0; bad &= bad - 1) {
+                    const int at = min(__ffs(bad) - 1, whole) * block_bytes + v_at;
+                    for (int x = lane; x < (block_bytes - v_at) / 16; x += 32) sts128(ring + stage * stage_bytes + at + 16 * x, make_uint4(0u, 0u, 0u, 0u));
+                    fence_proxy_async_smem();
+                    __syncwarp();
                 }
                 const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(bytes));
                 if (lane == 0) mbar_arrive_expect_tx(&full[stage], all);
@@ -457,13 +462,15 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
                         }
                     }
                 }
-                if (KIND != kI8 && t0 < begin) {
-                    // no values before the block's first token (each warp that reads them
-                    // clears them: the others write the same)
+                if (KIND != kI8 && (t0 < begin || t0 + S::kTokens > end)) {
+                    // no values before the block's first token and past its last (each warp that
+                    // reads them clears them: the others write the same)
 #pragma unroll
                     for (int i = 0; i < NG; ++i) {
 #pragma unroll 1
-                        for (int y = lane >> 3; y < min(begin - t0 - 16 * i, 16); y += 4) {
+                        for (int y = lane >> 3; y < 16; y += 4) {
+                            const int x = t0 + 16 * i + y;
+                            if (x >= begin && x < end) continue;
                             for (int ch = 0; ch < chunks; ++ch)
                                 sts128(ring + stage * stage_bytes + v_at + ch * chunk_bytes + off[i] + y * RB + 16 * (lane & 7), make_uint4(0u, 0u, 0u, 0u));
                         }
