@@ -451,8 +451,9 @@ Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, 
  *   order of its tokens; token t is in page table[s][t / page_tokens]. Entries
  *   that no token of a call needs are not read. One page may stand in several rows
  *   (a shared beginning); a call that writes a place twice leaves either.
- * A sequence holds at most ldt * page_tokens tokens (and 2^30); a longer len counts
- * as that. A page that a call needs and that is not 0 .. n_pages - 1 is recorded
+ * The table holds ldt * page_tokens tokens of a sequence (and 2^30 at most). With a
+ * longer len the new tokens' places are those that the len says; the ones past the
+ * table are recorded by the write and the read, and no query sees a token there. A page that a call needs and that is not 0 .. n_pages - 1 is recorded
  * as Q4_ERR_DEVICE_CHECK (q4_last_device_status) and nothing is read or written in
  * its place; what the rows that see such a token get is unspecified, the others are
  * what they are without it. Places of a sequence that its rows see and that were never

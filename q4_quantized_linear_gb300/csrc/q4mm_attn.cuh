@@ -20,7 +20,7 @@
 namespace q4 {
 
 struct Seq {
-    int n, len, start, rows, blocks;   // new tokens, tokens held, first row, query rows, blocks of them
+    int n, len, start, rows, blocks;   // new tokens, tokens with them, first row, query rows, blocks of them
 };
 
 __device__ __forceinline__ Seq seq_at(const AttnArgs &a, int s)
@@ -29,18 +29,20 @@ __device__ __forceinline__ Seq seq_at(const AttnArgs &a, int s)
     Seq q;
     q.n = max(hi - lo, 0);
     q.start = lo;
-    q.len = min(max(a.lens[s], 0), a.c.capacity);
+    q.len = max(a.lens[s], 0);
     q.rows = q.n * a.group;
     if (q.rows <= a.rows_above || q.rows > a.rows_upto) q.rows = 0;
     q.blocks = (q.rows + a.block - 1) / a.block;
     return q;
 }
-// Tokens lo .. hi - 1 that query row r sees.
+// Tokens lo .. hi - 1 that query row r sees. Its place is where the write puts its
+// keys, past the table's end too; tokens there are not in the cache.
 __device__ __forceinline__ void row_range(const AttnArgs &a, const Seq &q, int r, int &lo, int &hi)
 {
     const int pos = q.len - q.n + r / a.group;
-    hi = max(pos + 1, 0);
-    lo = a.window > 0 ? max(hi - a.window, 0) : 0;
+    const int upto = max(pos + 1, 0);
+    hi = min(upto, a.c.capacity);
+    lo = a.window > 0 ? min(max(upto - a.window, 0), hi) : 0;
 }
 // Tiles of block b: the first, and how many (one at least, so that rows that see
 // nothing are written too); `hi`: tokens past it are seen by none of its rows.

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             row_range(a, w.q, min(my_row, w.q.rows - 1), lo, hi);
             row_range(a, w.q, min(first_row, w.q.rows - 1), other, full_upto);
             row_range(a, w.q, min(first_row + 31, w.q.rows - 1), full_from, other);
-            const int end = min(w.hi, w.q.len);
+            const int end = w.hi;
             hi = min(hi, end);
             float m = neg_inf(), l = 0.0f;
             int E = -118;                                              // of the sums' unit, over codes
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             for (; ok && w.valid(); w.next(a)) {
                 const int32_t *table = a.c.table + w.s * a.c.ldt;
                 const int64_t head = static_cast<int64_t>(w.h) * a.c.head_bytes;
-                const int begin = first_seen(a, w), end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> a.c.log_page;
+                const int begin = first_seen(a, w), end = w.hi, pages = (end + in_page - 1) >> a.c.log_page;
                 int held = -32, page = 0;                              // lane l holds page held + l of the sequence
                 for (int t = w.from; ok && t < w.upto; ++t, ++issued) {
                     // tokens lo .. lo + tokens - 1 of the tile are there
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                     scale_src = nullptr, scale_there = 0;
                     return;
                 }
-                const int end = min(w.hi, w.q.len), t0 = (w.first + at) * kTile, tokens = min(max(end - t0, 0), kTile);
+                const int end = w.hi, t0 = (w.first + at) * kTile, tokens = min(max(end - t0, 0), kTile);
                 const int32_t *table = a.c.table + w.s * a.c.ldt;
                 const int p0 = t0 >> log_page, pages = (end + in_page - 1) >> log_page;
                 if (fresh) {

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
         for (; ok && w.valid(); w.next(a)) {
             const int32_t *table = a.c.table + w.s * a.c.ldt;
             const uint8_t *head = a.c.pages + static_cast<int64_t>(w.h) * a.c.head_bytes;
-            const int end = min(w.hi, w.q.len), pages = (end + in_page - 1) >> log_page, first_page = first_seen(a, w) >> log_page;
+            const int end = w.hi, pages = (end + in_page - 1) >> log_page, first_page = first_seen(a, w) >> log_page;
             // lane l holds page held + l of the sequence, and the one 32 further on
             int held = ((w.first + w.from) * kWarpTile) >> log_page;
             int page = page_of(a, table, held + lane, first_page, pages), ahead = page_of(a, table, held + 32 + lane, first_page, pages);
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
         }
         const float rf0 = row_factor[wm * 16 + g], rf1 = row_factor[wm * 16 + g + 8];
         int lo0, hi0, lo1, hi1, begin, full_from, full_upto;
-        const int end = min(w.hi, w.q.len);
+        const int end = w.hi;
         {
             const int r0 = min(w.b * S::kBlock + wm * 16 + g, w.q.rows - 1), r1 = min(w.b * S::kBlock + wm * 16 + g + 8, w.q.rows - 1);
             row_range(a, w.q, r0, lo0, hi0);

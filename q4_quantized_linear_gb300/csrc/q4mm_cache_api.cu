@@ -183,7 +183,7 @@ Q4MM_API int q4_attention(void *O, int64_t ldo, const void *Q, int64_t ldq, int 
     a.type = type, a.vec = al.bytes() == 16;
     a.group = static_cast<int>(heads / kv_heads);
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.window = window < a.c.capacity ? static_cast<int>(window) : 0;
+    a.window = window < 0x7FFFFFFF ? static_cast<int>(window) : 0;   // (a len is below 2^31)
     a.lens = lens, a.starts = starts;
     a.n_seq = static_cast<int>(n_seq), a.rows = static_cast<int>(rows);
     a.meta = static_cast<int4 *>(workspace);
