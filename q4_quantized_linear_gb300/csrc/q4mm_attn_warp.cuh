@@ -198,33 +198,35 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
                 const int rest_scales = KIND == kI8 ? (rest + 3) & ~3 : 0;
                 const int y = lane - 8;                     // lanes 8 and on: a piece each of the page that is not whole
                 const int pg = __shfl_sync(0xFFFFFFFFu, page, min(p0 - held + min(lane, whole), 31));
+                const bool mine = lane < whole || (y >= 0 && y < per_page && rest > 0);   // the lane has something to copy
+                const bool there = mine && pg >= 0;
+                uint32_t bytes = static_cast<uint32_t>(whole * block_bytes + rest * 2 * chunks * RB + 8 * rest_scales);
+                if (__any_sync(0xFFFFFFFFu, there != mine)) {
+                    // pages behind the window are left out; one that the cache does not have has no
+                    // values and no scales
+                    for (unsigned bad = __ballot_sync(0xFFFFFFFFu, mine && pg == -2 && y <= 0); bad != 0; bad &= bad - 1) {
+                        const int at = min(__ffs(bad) - 1, whole) * block_bytes + v_at;
+                        for (int x = lane; x < (block_bytes - v_at) / 16; x += 32) sts128(dst + at + 16 * x, make_uint4(0u, 0u, 0u, 0u));
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    const int own = !there ? 0 : lane < whole ? block_bytes : y < 2 * chunks ? rest * RB : rest_scales * 4;
+                    bytes = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(own));
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+                __syncwarp();
                 const uint8_t *src = head + pg * a.c.page_bytes;
-                int bytes = 0;                              // (a page behind the window: none)
-                if (pg >= 0 && lane < whole) {
-                    bytes = block_bytes;
-                    dst += lane * block_bytes;
-                } else if (pg >= 0 && y >= 0 && y < per_page && rest > 0) {
+                if (there && lane < whole) {
+                    bulk_g2s(dst + lane * block_bytes, src, static_cast<uint32_t>(block_bytes), &full[stage]);
+                } else if (there) {
                     const int in = in_page <= kWarpTile ? 0 : t0 & (in_page - 1);
                     dst += whole * block_bytes;
-                    if (y < 2 * chunks) {
-                        bytes = rest * RB;
-                        dst += y * chunk_bytes, src += (y * in_page + in) * RB;
-                    } else {
-                        bytes = rest_scales * 4;
-                        dst += scales_at + (y - 2 * chunks) * (together * 4), src += 2 * chunks * in_page * RB + ((y - 2 * chunks) * in_page + in) * 4;
-                    }
+                    if (y < 2 * chunks)
+                        bulk_g2s(dst + y * chunk_bytes, src + (y * in_page + in) * RB, static_cast<uint32_t>(rest * RB), &full[stage]);
+                    else
+                        bulk_g2s(dst + scales_at + (y - 2 * chunks) * (together * 4), src + 2 * chunks * in_page * RB + ((y - 2 * chunks) * in_page + in) * 4,
+                                 static_cast<uint32_t>(rest_scales * 4), &full[stage]);
                 }
-                // a page that the cache does not have: no values and no scales
-                for (unsigned bad = __ballot_sync(0xFFFFFFFFu, pg == -2 && (lane < whole || (y == 0 && rest > 0))); bad != 0; bad &= bad - 1) {
-                    const int at = min(__ffs(bad) - 1, whole) * block_bytes + v_at;
-                    for (int x = lane; x < (block_bytes - v_at) / 16; x += 32) sts128(ring + stage * stage_bytes + at + 16 * x, make_uint4(0u, 0u, 0u, 0u));
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(bytes));
-                if (lane == 0) mbar_arrive_expect_tx(&full[stage], all);
-                __syncwarp();
-                if (bytes > 0) bulk_g2s(dst, src, static_cast<uint32_t>(bytes), &full[stage]);
                 ++issued;
                 if (++stage == a.stages) stage = 0, phase ^= 1u;
             }
@@ -359,14 +361,13 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
             for (int ks = 0; ks < DP / 16; ++ks) load_q(0, ks, qr[ks]);
         }
         const float rf0 = row_factor[wm * 16 + g], rf1 = row_factor[wm * 16 + g + 8];
-        int lo0, hi0, lo1, hi1, begin, full_from, full_upto;
-        const int end = w.hi;
+        int lo0, hi0, lo1, hi1, full_from, full_upto;
         {
             const int r0 = min(w.b * S::kBlock + wm * 16 + g, w.q.rows - 1), r1 = min(w.b * S::kBlock + wm * 16 + g + 8, w.q.rows - 1);
             row_range(a, w.q, r0, lo0, hi0);
             row_range(a, w.q, r1, lo1, hi1);
             int x;
-            row_range(a, w.q, w.b * S::kBlock, begin, full_upto);                              // the first row's start and end
+            row_range(a, w.q, w.b * S::kBlock, x, full_upto);                                  // the first row's end
             row_range(a, w.q, min((w.b + 1) * S::kBlock, w.q.rows) - 1, full_from, x);         // the last row's start
         }
         float o[OT][4] = {};
@@ -452,16 +453,17 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int x = t0 + nt * 8 + 2 * c + i;
-                        const bool sees0 = x >= lo0 && x < hi0 && x < end, sees1 = x >= lo1 && x < hi1 && x < end;
+                        const bool sees0 = x >= lo0 && x < hi0, sees1 = x >= lo1 && x < hi1;
                         if (!sees0) s[nt][i] = neg_inf();
                         if (!sees1) s[nt][2 + i] = neg_inf();
                         if constexpr (KIND == kI8) {
-                            if (x < begin || x >= end) sv[nt][i] = 0.0f;   // a token that is not there has no scale
+                            if (!sees0 && !sees1) sv[nt][i] = 0.0f;   // (it may not be there)
                             if (sees0) v0max = fmaxf(v0max, sv[nt][i]);
                             if (sees1) v1max = fmaxf(v1max, sv[nt][i]);
                         }
                     }
                 }
+                const int begin = KIND != kI8 ? first_seen(a, w) : t0, end = w.hi;
                 if (KIND != kI8 && (t0 < begin || t0 + S::kTokens > end)) {
                     // no values before the block's first token and past its last (each warp that
                     // reads them clears them: the others write the same)
