@@ -379,8 +379,11 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         }
                     }
                 }
-                // terms in the sums' unit: of a tile whose values carry their scales 2^shift times p
-                const int shift = CODES && !exact ? max(__float_as_int(tail.z) - E, -120) : 0;
+                // terms in the sums' unit: of a tile whose values carry their scales 2^shift times p.
+                // Below 2^-40 they are 0 in fp16 (terms are below 2^15, its smallest step is 2^-24), so a
+                // smaller shift changes no product; but the denominator adds them up before that
+                // rounding, and fp32 still holds them down to 2^-93 of the largest.
+                const int shift = CODES && !exact ? max(__float_as_int(tail.z) - E, -40) : 0;
                 const float u = (m == neg_inf() ? 0.0f : m - kLift) - static_cast<float>(shift);
                 const F2 rf2 = f2(rft, rft), u2 = f2(-u, -u);
                 [[maybe_unused]] const float down = CODES ? pow2(-E) : 1.0f;
