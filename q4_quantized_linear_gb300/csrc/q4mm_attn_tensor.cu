@@ -275,13 +275,14 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->q_full[half]);
             const int my_row = first_row + lane;
-            const float rf = CODES ? row_factor[half * kHalf + (warp & 3) * 32 + lane] : a.scale_log2;
+            float rf = CODES ? row_factor[half * kHalf + (warp & 3) * 32 + lane] : a.scale_log2;
             int lo, hi, full_from, full_upto, other;
             row_range(a, w.q, min(my_row, w.q.rows - 1), lo, hi);
             row_range(a, w.q, min(first_row, w.q.rows - 1), other, full_upto);
             row_range(a, w.q, min(first_row + 31, w.q.rows - 1), full_from, other);
-            const int end = w.hi;
-            hi = min(hi, end);
+            // A column that a row does not see has a score of -infinity, and is multiplied by the row's
+            // factor: not by 0, and where the row sees nothing not by that of a query that is not finite.
+            if (CODES && (rf == 0.0f || lo >= hi)) rf = 1.401298464324817e-45f;
             float m = neg_inf(), l = 0.0f;
             int E = -118;                                              // of the sums' unit, over codes
             const Bounds bounds(a, w);
