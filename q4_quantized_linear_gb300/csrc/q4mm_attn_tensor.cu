@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(TensorShape<KIND, DP>::kThreads, 1) attn_tenso
                         for (int i = 0; i < 4; ++i) raw[p][i] = 0u;
                         if (row < w.q.rows && 8 * x < a.c.d) {
                             const int i = row / a.group, head = w.h * a.group + row - i * a.group;
-                            load_raw<decltype(vec)::value>(a.Q, (static_cast<int64_t>(w.q.start) + i) * a.ldq + head * a.c.d + 8 * x, raw[p]);
+                            load_raw<decltype(vec)::value>(a.Q, (static_cast<int64_t>(w.q.start) + i) * a.ldq + static_cast<int64_t>(head) * a.c.d + 8 * x, raw[p]);
                         }
                     }
                 };

@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kAttnThreads, WarpShape<KIND, TERMS, WM, DP>::
                         for (int i = 0; i < Raw::kWords; ++i) raw[p].w[i] = 0u;
                         if (row < w.q.rows && 8 * x < a.c.d) {
                             const int i = row / a.group, head = w.h * a.group + row - i * a.group;
-                            const int64_t at = (static_cast<int64_t>(w.q.start) + i) * a.ldq + head * a.c.d + 8 * x;
+                            const int64_t at = (static_cast<int64_t>(w.q.start) + i) * a.ldq + static_cast<int64_t>(head) * a.c.d + 8 * x;
                             load_raw<decltype(whole_vectors)::value>(a.Q, at, raw[p].w);
                         }
                     }
