@@ -528,7 +528,8 @@ Q4MM_API int q4_attention(void *O, int64_t ldo, const void *Q, int64_t ldq, int 
  * in fp32. T: device fp32 [rows], NULL for ones; T = 0 gives 1 for the row's
  * largest logit (the lowest of equal ones; NaN counts for nothing) and 0
  * elsewhere. A logit of -inf has probability 0, a row of them zeros; a NaN or
- * +inf makes a row NaN (T > 0). T < 0 gives NaN.
+ * +inf makes a row NaN (T > 0). T < 0 or NaN gives NaN; 0 < T < 2^-126 counts as
+ * 2^-126, T = +inf as the largest finite number.
  *   P: device fp32, row r at P + r * ldp; logits: type F32, F16 or BF16, apart from P.
  *   1 <= n <= 2^24. 16-byte aligned rows of both are accessed 16 bytes at a time. */
 Q4MM_API int q4_token_probs(float *P, int64_t ldp, const void *logits, int64_t ldl, int type, const float *temperature,

@@ -137,7 +137,9 @@ template <typename T> __global__ void __launch_bounds__(kProbsMaxThreads) probs_
     };
     const float temperature = a.temperature ? a.temperature[row] : 1.0f;
     const bool greedy = temperature == 0.0f;
-    const float f = temperature > 0.0f ? __fdiv_rn(1.4426950408889634f, temperature) : __int_as_float(0x7FC00000);
+    // (0 < f < infinity: a difference of 0 stays 0 and one of -infinity what it is)
+    const float f = temperature > 0.0f ? __fdiv_rn(1.4426950408889634f, fminf(fmaxf(temperature, 1.17549435e-38f), 3.40282347e38f))
+                                       : __int_as_float(0x7FC00000);
     float m = -inf, s = 0.0f;
     over(false, [&](int64_t w0, int n) {
         for (int w = tid; w < n; w += step) {
