@@ -549,8 +549,8 @@ Q4MM_API int q4_token_probs(float *P, int64_t ldp, const void *logits, int64_t l
  *   tokens[s * ldt + j], j <= max_draft: the kept tokens, the drawn one, then -1.
  * accept and sample are uniform in [0, 1). The product is exact, and the draw by
  * whole numbers of steps of 2^-60: exact for probabilities from 2^-36 on, so that
- * tokens do not depend on the order of a sum. A probability counts as 0 if it is
- * negative or NaN, as 1 above; a row's sum must stay below 8. A drafted token
+ * tokens do not depend on the order of a sum. A probability counts, here and
+ * where a token is kept, as 0 if it is negative or NaN, as 1 above; a row's sum must stay below 8. A drafted token
  * outside 0 .. n - 1 is not kept. 1 <= n <= 2^20, max_draft <= 1024. */
 Q4MM_API int q4_draft_verify(int32_t *tokens, int64_t ldt, int32_t *kept, const float *P, int64_t ldp, const float *Q,
                              int64_t ldq, const int32_t *drafted, int64_t ldd, const int32_t *counts, const float *accept,

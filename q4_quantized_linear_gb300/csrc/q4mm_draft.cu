@@ -259,6 +259,8 @@ template <typename T> cudaError_t launch_probs(ProbsArgs a, int sm_count, cudaSt
 
 // ---------------------------------------------------------- verification --
 
+__device__ __forceinline__ float probability(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }   // (NaN: 0)
+
 // The draw is by whole numbers: probabilities in steps of 2^-60 (exact from 2^-36
 // on), their sums exact whatever the order, and the place of u times the sum is
 // found without a rounding; so the same numbers always give the same token, on any
@@ -273,7 +275,7 @@ struct Steps {
     __device__ __forceinline__ void add(float p, float q)
     {
         constexpr float kA = 3.0f, kB = 3.0f * 1.1920928955078125e-7f, kC = 1.5f * 7.275957614183426e-12f;   // 1.5 2^1, 2^-22, 2^-37
-        p = fminf(fmaxf(p, 0.0f), 1.0f), q = fminf(fmaxf(q, 0.0f), 1.0f);   // (NaN: 0)
+        p = probability(p), q = probability(q);
         const float pa = p + kA, qa = q + kA, p1 = p - (pa - kA), q1 = q - (qa - kA);
         const float pb = p1 + kB, qb = q1 + kB, p2 = p1 - (pb - kB), q2 = q1 - (qb - kB);
         const float pc = p2 + kC, qc = q2 + kC;
@@ -384,8 +386,8 @@ template <int V> __global__ void __launch_bounds__(kVerifyThreads) verify_kernel
                 const float u = a.accept[seq * a.lda + i];
                 const int64_t x = a.drafted[seq * a.ldd + i];
                 if (x >= 0 && x < a.n) {
-                    const double px = a.P[(seq * (a.max_draft + 1) + i) * a.ldp + x];
-                    const double qx = a.Q ? static_cast<double>(a.Q[(seq * a.max_draft + i) * a.ldq + x]) : 1.0;
+                    const double px = probability(a.P[(seq * (a.max_draft + 1) + i) * a.ldp + x]);
+                    const double qx = a.Q ? static_cast<double>(probability(a.Q[(seq * a.max_draft + i) * a.ldq + x])) : 1.0;
                     stays = static_cast<double>(u) * qx < px;   // the product is exact
                 }
             }
