@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -30,6 +31,10 @@ SOURCES = ["q4mm_api.cu", "q4mm_pack.cu", "q4mm_decode.cu", "q4mm_gemv.cu", "q4m
 DEPS = ["q4mm_device.cuh", "q4mm_internal.h", "q4mm_rows.cuh", "q4mm_rows.h", "q4mm_norm.h", "q4mm_norm.cuh", "q4mm_norm_stream.cuh", "q4mm_moe.h",
         "q4mm_w8a8.h", "q4mm_cache.h", "q4mm_attn.cuh", "q4mm_attn_warp.cuh"]
 
+# Kernels whose warpgroups share out the registers of the launch (setmaxnreg), and the
+# registers a thread that the shares add up to: with fewer a share is waited for forever.
+SHARED_REGISTERS = {"q4mm_attn_tensor.cu": ("attn_tensor_kernelILi2E", 128)}
+
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]
@@ -49,16 +54,28 @@ def _stale(target: str, inputs: list[str]) -> bool:
     return any(os.path.getmtime(i) > t for i in inputs)
 
 
+def check_registers(src: str, log: str) -> None:
+    """Raises if ptxas's report (-v) does not give every kernel of SHARED_REGISTERS its count."""
+    if src not in SHARED_REGISTERS:
+        return
+    kernel, count = SHARED_REGISTERS[src]
+    found = re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", log, flags=re.DOTALL)
+    used = {name: int(n) for name, n in found if kernel in name}
+    if not used or any(n != count for n in used.values()):
+        raise RuntimeError(f"{src}: the shares of {kernel} add up to {count} registers a thread, ptxas gave {sorted(used.values())}")
+
+
 def _compile(src: str, verbose_ptxas: bool, outdir: str = BUILD, extra: tuple = ()) -> str:
     obj = os.path.join(outdir, os.path.splitext(src)[0] + ".o")
     inputs = [os.path.join(CSRC, src), HEADER] + [os.path.join(CSRC, d) for d in DEPS] + [__file__]
     if not _stale(obj, inputs):
         return obj
-    cmd = [nvcc()] + ARCH + NVCC_FLAGS + list(extra) + (["-Xptxas", "-v"] if verbose_ptxas else []) + \
+    cmd = [nvcc()] + ARCH + NVCC_FLAGS + list(extra) + (["-Xptxas", "-v"] if verbose_ptxas or src in SHARED_REGISTERS else []) + \
         ["-c", os.path.join(CSRC, src), "-o", obj + ".tmp"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+    check_registers(src, r.stderr)
     if verbose_ptxas and r.stderr:
         sys.stderr.write(r.stderr)
     os.replace(obj + ".tmp", obj)

@@ -32,6 +32,7 @@
 // is in their place may be another sequence's, of a page that was never written at
 // that, so their values are set to 0 beside the copies of a tile that has some.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "q4mm_attn.cuh"
@@ -51,7 +52,7 @@ template <int KIND, int DP> struct TensorShape {
     // warpgroups share the registers out.
     static constexpr int kThreads = kCodes ? 512 : 320;
     static constexpr int kConvertWarp0 = 8, kMmaWarp = kCodes ? 12 : 8, kCopyWarp = 9;
-    static constexpr int kLaunchRegs = 128, kSoftmaxRegs = 144, kConvertRegs = 128, kMmaRegs = 96;   // codes
+    static constexpr int kLaunchRegs = 128, kSoftmaxRegs = 144, kConvertRegs = 128, kMmaRegs = 96;   // codes (kLaunchRegs: build.py checks it)
     static constexpr int kTileBytes = kChunks * static_cast<int>(kAtomRows);
     // 16-bit: rings of K and of V tiles. Codes: one ring of fp16 tiles, K and V in turn.
     static constexpr int kK = kCodes || DP == 64 ? 4 : 2, kV = kCodes ? 0 : DP == 64 ? 4 : 3;
@@ -904,14 +905,19 @@ template <int KIND, int DP> cudaError_t launch(const AttnArgs &args, int sm_coun
     cudaError_t e = set_max_smem(f, TensorShape<KIND, DP>::kSmem);
     if (e != cudaSuccess) return e;
     if constexpr (TensorShape<KIND, DP>::kCodes) {
-        // the warpgroups' registers have to add up to what the launch has
-        static const bool enough = [f] {
-            using S = TensorShape<KIND, DP>;
+        // The warpgroups' registers have to add up to what the launch has: a share that is not
+        // there is waited for without end. The build refuses another count; looked at until it
+        // is known, so that a query that fails once is asked again.
+        using S = TensorShape<KIND, DP>;
+        static_assert(4 * S::kLaunchRegs >= 2 * S::kSoftmaxRegs + S::kConvertRegs + S::kMmaRegs, "the warpgroups' shares");
+        static std::atomic<bool> enough{false};
+        if (!enough.load(std::memory_order_relaxed)) {
             cudaFuncAttributes fa{};
-            return cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs == S::kLaunchRegs &&
-                   4 * S::kLaunchRegs >= 2 * S::kSoftmaxRegs + S::kConvertRegs + S::kMmaRegs;
-        }();
-        if (!enough) return cudaErrorLaunchOutOfResources;
+            e = cudaFuncGetAttributes(&fa, f);
+            if (e != cudaSuccess) return e;
+            if (fa.numRegs != S::kLaunchRegs) return cudaErrorLaunchOutOfResources;
+            enough.store(true, std::memory_order_relaxed);
+        }
     }
     *ctas = std::min(kTensorMaxCtas, sm_count);
     void *p[] = {&a};
