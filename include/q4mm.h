@@ -506,7 +506,7 @@ Q4MM_API size_t q4_attention_workspace_size(int64_t rows, int64_t n_seq, int64_t
  * A row that sees nothing (a len below the number of new tokens) gives zeros.
  *   Q, O: device, heads of d values next to each other, one type: F32, F16 or BF16
  *   over codes, F32 or F16 over an F16 cache, BF16 over a BF16 one. O may be Q.
- *   scale > 0; heads a multiple of kv_heads; rows * heads <= 2^30.
+ *   0 < scale < 2.3e38; heads a multiple of kv_heads; rows * heads <= 2^30.
  *   max_new: at least the most new tokens of a sequence (0: rows); it chooses
  *   the kernel, results hold whatever it is.
  *   workspace: q4_attention_workspace_size bytes; calls that can run at the same

@@ -14,6 +14,7 @@ constexpr int64_t kMaxRows = int64_t(1) << 30;     // rows x heads
 constexpr int64_t kMaxPageTokens = 1024;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;   // of a sequence
 constexpr int64_t kMaxVocab = int64_t(1) << 24;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr size_t kMetaBytes = 2 * sizeof(int4) * kAttnMaxCtas;
 
 cudaStream_t as_stream(q4mm_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -159,7 +160,7 @@ Q4MM_API int q4_attention(void *O, int64_t ldo, const void *Q, int64_t ldq, int 
                           size_t workspace_bytes, q4mm_stream_t stream)
 {
     if (!is_float_type(type) || !valid_page(page_tokens, kv_heads, d, ctype) || heads < 1 || heads % kv_heads != 0 ||
-        !valid_batch(n_seq, rows, heads) || window < 0 || max_new < 0 || !(scale > 0.0f) || !std::isfinite(scale))
+        !valid_batch(n_seq, rows, heads) || window < 0 || max_new < 0 || !(scale > 0.0f) || !std::isfinite(scale * kLog2e))
         return Q4_ERR_INVALID_ARG;
     // the tensor cores multiply numbers of one type
     if ((ctype == Q4_TYPE_BF16 && type != Q4_TYPE_BF16) || (ctype == Q4_TYPE_F16 && type == Q4_TYPE_BF16)) return Q4_ERR_INVALID_ARG;
@@ -182,7 +183,7 @@ Q4MM_API int q4_attention(void *O, int64_t ldo, const void *Q, int64_t ldq, int 
     a.ldo = ldo, a.ldq = ldq;
     a.type = type, a.vec = al.bytes() == 16;
     a.group = static_cast<int>(heads / kv_heads);
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale * kLog2e;   // (scores in powers of two)
     a.window = window < 0x7FFFFFFF ? static_cast<int>(window) : 0;   // (a len is below 2^31)
     a.lens = lens, a.starts = starts;
     a.n_seq = static_cast<int>(n_seq), a.rows = static_cast<int>(rows);
