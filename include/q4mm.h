@@ -450,7 +450,8 @@ Q4MM_API int q4_moe_combine_backward(void *dYs, int64_t lddys, float *dweights, 
  *   table: device int32, row s at table + s * ldt: the pages of sequence s in the
  *   order of its tokens; token t is in page table[s][t / page_tokens]. Entries
  *   that no token of a call needs are not read. One page may stand in several rows
- *   (a shared beginning); a call that writes a place twice leaves either.
+ *   (a shared beginning). What a place holds that one call writes twice is unspecified:
+ *   its keys, values and scales may be of different rows.
  * The table holds ldt * page_tokens tokens of a sequence (and 2^30 at most). With a
  * longer len the new tokens' places are those that the len says; the ones past the
  * table are recorded by the write and the read, and no query sees a token there. A page that a call needs and that is not 0 .. n_pages - 1 is recorded

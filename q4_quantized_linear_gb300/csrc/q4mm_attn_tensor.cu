@@ -19,9 +19,10 @@
 // what the waits between them add. A test of a barrier that is already there answers
 // after some 190 while products read shared memory, and the queue of products holds
 // about three of 64: a loop takes 3300. 2048 new tokens over 16384, 32 heads on 8 of
-// 128: 412 us, 1250 TFLOP/s (65 % of the measured bf16 rate); over codes the converting
-// warps' 3000 a tile of K or V bound it (540 over 8100: 153 us); short items (windowed
-// prompts of 2000, 540 wide: 67 us) their start and end, 8000 to 10000 an item. Tried and
+// 128: 418 us, 1230 TFLOP/s (64 % of the measured bf16 rate); over codes the converting
+// warps' 3000 a tile of K or V bound it (540 over 8100: 153 us; 140 to 148 bytes a thread
+// are spilled); short items (prompts of up to 2000, a window of 1024, 64 dims: 63 us) their
+// start and end, 8000 to 10000 an item. Tried and
 // slower: two issuing warps (the halves fall into step), 16 softmax warps with half a
 // row each, scores held in registers between the maximum and the terms (spills), eight
 // converting warps, four for keys and four for values (150 to 188 us by the registers'

@@ -25,10 +25,12 @@
 // as values: what is in their place in the ring may be another sequence's, of a page
 // that was never written at that, so the warps that multiply by it clear it first.
 //   Measured, 32 heads on 8 of 128: 16 x 5 tokens over up to 4096, bf16 44 us (203 MB,
-// 4.6 TB/s); 16 x 1 over up to 8192, int8 44 with its write (153 MB; the chains from
-// codes to products, 54 % of the issue slots); one token over 1000, fp32 12 with its
-// write (three launches that wait for one another); 540 over 8100, fp32 over fp16 366
-// and over int8 590 (products: four for the two of 16-bit types).
+// 4.6 TB/s); 16 x 1 over up to 8192, int8 45 with its write (153 MB; the chains from
+// codes to products, 55 % of the issue slots), without it 42, fp32 over int8 54; one token
+// over 1000, fp32 15 with its write (three launches that wait for one another; 12 with
+// inputs in L2); 540 over 8100, fp32 over fp16 363 and over int8 577 (products: four for
+// the two of 16-bit types). At 128 dims the blocks of 64 rows spill: 260 bytes a thread for
+// 16-bit types, 428 over codes, 484 and 692 for fp32; a block of 16 over codes 32.
 #pragma once
 
 #include <type_traits>

@@ -103,7 +103,8 @@ int kv_rows(bool write, const void *K, int64_t ldk, const void *V, int64_t ldv, 
 }
 
 // Whether the tcgen05 kernel has a part in a call with up to so many query rows of
-// a sequence and head: its tensor memory holds the sums of heads of up to 128 dims.
+// a sequence and head: with its two halves tensor memory holds the sums of heads of up to
+// 128 dims.
 bool tensor_takes(int64_t rows, int chunks) { return rows > kWarpRows && chunks <= 2; }
 
 int block_of(int64_t rows)
@@ -196,8 +197,12 @@ Q4MM_API int q4_attention(void *O, int64_t ldo, const void *Q, int64_t ldq, int 
     cudaStream_t s = as_stream(stream);
     return guarded([&] {
         if (type != Q4_TYPE_F32 && tensor_takes(most, a.c.chunks)) {
-            // sequences with many new tokens; all of them where those are the rule (the second
-            // pair of launches took 8 of 84 us of four prompts that had no use for it)
+            // sequences with many new tokens; all of them where those are the rule by the size of
+            // the buffers. Without this the second pair of launches took 8 of 84 us of four prompts
+            // that had no use for it. What it costs where a batch has both (32 heads on 8 of 128,
+            // single tokens over 8192; the two parts in calls of their own): 4 prompts of 2000 and 4
+            // tokens, bf16 cache, 240 us (211 + 32), int8 543 (472 + 27); 8 prompts of 540 and 24
+            // tokens 282 (79 + 125) and 682 (173 + 84).
             const bool alone = rows * a.group >= n_seq * 8 * kWarpRows || n_seq == 1;
             AttnArgs many = a;
             many.rows_above = alone ? 0 : kWarpRows;

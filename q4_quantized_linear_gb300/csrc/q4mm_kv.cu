@@ -121,11 +121,13 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float factor)
     return w;
 }
 
-// Heads' rows that a thread has in flight, and CTAs an SM at most. 4 prompts of up to 2048
-// fp32 into int8 take 33 us (135 MB, 4.1 TB/s), 3 x up to 8000 int8 into bf16 21.5 (97 MB,
-// 4.5 TB/s), bf16 into bf16 22.6 (128 MB, 5.7 TB/s). Within a microsecond of that: two and
-// four rows, 8 and 64 CTAs, the next row's loads before a row is stored, a CTA's rows
-// along a head instead of a token; slower: 32-byte loads, 16 codes a lane (29).
+// Heads' rows that a thread has in flight, and CTAs an SM at most. The write alone, 6554
+// tokens of 8 heads of 128: fp32 into int8 16.1 us (67 MB, 4.2 TB/s), into fp16 15.9 (5.1), bf16
+// into bf16 15.9 (3.4), into int8 16.2 (2.5): by the rows, not by the bytes. The read alone, 3
+// sequences of up to 8000: int8 into bf16 21.9 (97 MB, 4.4 TB/s), bf16 into bf16 23.6 (128 MB,
+// 5.4); the write's tokens int8 into fp32 21.1 (67 MB, 3.2). Both together within a
+// microsecond: two and four rows, 8 and 64 CTAs, the next row's loads before a row is
+// stored, a CTA's rows along a head instead of a token; slower: 32-byte loads, 16 codes a lane.
 constexpr int kWriteAhead = 1, kReadAhead = 2, kBlocksPerSM = 16;
 
 // C: the cache's element type (int8_t: codes).
